@@ -601,11 +601,222 @@ int dopt_step_clipped_noalloc(const dopt_layout *layout, const dopt_adam_cfg *cf
                               float *exp_avg_sq, void *const *param_replicas, uint32_t flags,
                               float *main_grad, float *norm_out, cudaStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Operators of the layers whose grads the step consumes: tokens sorted by
+ * expert and back, and activations kept in 8 bits for the backward pass.
+ * The pages have no counterpart (the tutorial's §8.1 describes activation
+ * checkpoints, not this format).  All are asynchronous on `stream`, check
+ * their arguments on the host before any launch, allocate nothing, and are
+ * launched as programmatic dependents as the step kernels are: they touch no
+ * memory before the kernel before them on the stream has completed.  Results
+ * do not depend on the order in which blocks run.
+ *
+ * Rows: a "row stride" is in elements, at least the row length; pointers
+ * need only be aligned to their elements (the widest access of 16, 8, 4 or 2
+ * bytes that pointers, row strides and row lengths allow is used, so 16-byte
+ * aligned rows are the fast ones).  Outputs must not overlap inputs unless
+ * stated.
+ * ------------------------------------------------------------------------ */
+
+#define DOPT_MAX_EXPERTS 1024
+#define DOPT_MAX_TOPK 64
+#define DOPT_MAX_GROUPS 256
+#define DOPT_MAX_COLS 4194304
+
+/*
+ * Bytes of workspace that dopt_route_sort needs for these sizes (0 up to
+ * 4096 slots).  Host only.  Errors: DOPT_E_ARG.
+ */
+int dopt_route_workspace(int64_t tokens, int32_t k, int32_t n_experts, int64_t *bytes);
+
+/*
+ * Sort a router's choices by expert.  A slot is one (token, choice) pair, in
+ * the order token * k + choice; slots whose id is outside [0, n_experts)
+ * are dropped (another rank's expert, a token over capacity).  The kept
+ * slots, ordered by expert and by slot inside an expert, are the rows.
+ *   expert_ids  device [tokens][k], 4- or 8-byte signed integers (id_bytes);
+ *               an id may come twice in a token
+ *   slot_row    device int32 [tokens][k], written: the slot's row, -1 if
+ *               dropped
+ *   row_token   device int32 [tokens * k], written: the row's token, -1 past
+ *               the last row
+ *   offsets     device int32 [n_experts + 1], written: the first row of each
+ *               expert, then the number of rows
+ *   workspace   device, dopt_route_workspace bytes, 4-byte aligned; calls
+ *               that share one must not overlap on the GPU
+ * 1 <= k <= DOPT_MAX_TOPK, 1 <= n_experts <= DOPT_MAX_EXPERTS, tokens * k <
+ * 2^31.  tokens = 0 writes offsets (zeros).  Errors: DOPT_E_ARG,
+ * DOPT_E_ALIGN, DOPT_E_CUDA.
+ */
+int dopt_route_sort(const void *expert_ids, int32_t id_bytes, int64_t tokens, int32_t k,
+                    int32_t n_experts, int32_t *slot_row, int32_t *row_token, int32_t *offsets,
+                    void *workspace, int64_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Copy each token's row of x to the rows of its slots: rows[slot_row[t][j]] =
+ * x[t], bit for bit.  It is also the gradient of an unweighted combine.
+ *   x         device [tokens][cols], row stride ld
+ *   slot_row  device int32 [tokens][k]; entries outside [0, n_rows) are
+ *             skipped
+ *   rows      device [n_rows][cols], contiguous; rows that no slot names are
+ *             not written
+ * cols <= DOPT_MAX_COLS, n_rows < 2^31.  Errors: DOPT_E_ARG, DOPT_E_ALIGN,
+ * DOPT_E_CUDA.
+ */
+int dopt_route_dispatch(const void *x, dopt_dtype dtype, int64_t tokens, int64_t cols, int64_t ld,
+                        const int32_t *slot_row, int32_t k, void *rows, int64_t n_rows,
+                        cudaStream_t stream);
+
+/*
+ * The way back: out[t] = sum over j, in order, of weights[t][j] *
+ * rows[slot_row[t][j]], in fp32 and rounded once.  Entries of slot_row outside
+ * [0, n_rows) are left out whatever their weight; a token without rows gets
+ * zeros.  weights NULL: every weight is 1, which is the gradient of
+ * dopt_route_dispatch.
+ *   rows     device [n_rows][cols], contiguous
+ *   weights  device fp32 [tokens][k] or NULL
+ *   out      device [tokens][cols], row stride ld, of the rows' type
+ * Limits and errors as dopt_route_dispatch.
+ */
+int dopt_route_combine(const void *rows, dopt_dtype dtype, int64_t n_rows, const int32_t *slot_row,
+                       const float *weights, int64_t tokens, int32_t k, int64_t cols, void *out,
+                       int64_t ld, cudaStream_t stream);
+
+/*
+ * The gradients of dopt_route_combine with weights, from the gradient d_out
+ * of its output, in one pass over the rows:
+ *     d_rows[r]       = weights[t][j] * d_out[t]      (r = slot_row[t][j])
+ *     d_weights[t][j] = sum over columns of d_out[t] * rows[r]   (fp32)
+ * Dropped slots get d_weights 0; rows that no slot names are not written.
+ *   d_out      device [tokens][cols], row stride ld
+ *   rows       device [n_rows][cols], contiguous, as given to the combine
+ *   d_rows     device [n_rows][cols], contiguous
+ *   d_weights  device fp32 [tokens][k]
+ * Limits and errors as dopt_route_dispatch.
+ */
+int dopt_route_combine_grad(const void *d_out, int64_t ld, const void *rows, dopt_dtype dtype,
+                            int64_t n_rows, const int32_t *slot_row, const float *weights,
+                            int64_t tokens, int32_t k, int64_t cols, void *d_rows,
+                            float *d_weights, cudaStream_t stream);
+
+/*
+ * An activation kept in 8 bits ("checkpoint"): one caller-owned device
+ * buffer, 16-byte aligned, of dopt_ckpt_bytes(rows, cols) bytes:
+ *     int8  codes [rows][pitch]      pitch = cols rounded up to DOPT_CKPT_PITCH
+ *     uint8 exps  [rows][pitch / 32]
+ * Each row's columns form blocks of DOPT_CKPT_BLOCK = 32 (the last one may be
+ * short) that share a power-of-two step: value = code * 2^(exp - 127), codes
+ * in -127..127.  With top the largest magnitude of the block, the step is
+ * 2^(floor(log2 top) - 6), no less than 2^-126 (2^-24 when fp16 values are
+ * saved), and a code is value / step rounded to nearest even and held to
+ * +-127: off by at most half a step, or by less than one where the value lies
+ * beyond 127.5 steps.  exp = 255 marks a block that held an Inf or a NaN; all
+ * of it reads back as NaN (so a poisoned activation reaches the grads, where
+ * DOPT_STEP_SKIP_NONFINITE sees it).  Codes past the last column are 0.
+ * The step is a power of two so that a value has 7 significant bits: bf16
+ * (and fp16, if fp16 values were saved) holds it exactly, and the matrix
+ * products of the backward pass read it without a second rounding.
+ */
+#define DOPT_CKPT_BLOCK 32
+#define DOPT_CKPT_PITCH 128
+
+/* Size of a checkpoint of rows x cols values: rows * pitch * 33 / 32 bytes.
+ * rows < 2^31, 1 <= cols <= DOPT_MAX_COLS.  Host only.  Errors: DOPT_E_ARG. */
+int dopt_ckpt_bytes(int64_t rows, int64_t cols, int64_t *bytes);
+
+/* Keep x (device [rows][cols], row stride ld) in the checkpoint.  Writes all
+ * of the buffer.  Errors: DOPT_E_ARG, DOPT_E_ALIGN, DOPT_E_CUDA. */
+int dopt_ckpt_save(const void *x, dopt_dtype dtype, int64_t rows, int64_t cols, int64_t ld,
+                   void *ckpt, cudaStream_t stream);
+
+/*
+ * Read a checkpoint back, rounded once to the output type (exact for bf16 and
+ * fp32, and for fp16 if fp16 values were saved).
+ *   row_index  device int32 [n_out] or NULL: output row i is checkpoint row
+ *              row_index[i] (zeros where it is outside [0, rows)); NULL: all
+ *              rows in order (n_out = rows).  With dopt_route_sort's
+ *              row_token this reads the tokens sorted by expert.
+ *   out        device [n_out][cols], row stride ld
+ * Errors: DOPT_E_ARG, DOPT_E_ALIGN, DOPT_E_CUDA.
+ */
+int dopt_ckpt_load(const void *ckpt, int64_t rows, int64_t cols, const int32_t *row_index,
+                   int64_t n_out, void *out, dopt_dtype dtype, int64_t ld, cudaStream_t stream);
+
+/* Activation functions: silu(h) = h sigmoid(h); gelu in its tanh form; swiglu
+ * of h = [g, u] (two halves of the columns) = silu(g) * u. */
+typedef enum { DOPT_ACT_SILU = 0, DOPT_ACT_GELU = 1, DOPT_ACT_SWIGLU = 2 } dopt_act;
+
+/*
+ * The backward pass of an activation function from its kept input h:
+ * d_in = d_out * act'(h), computed in fp32 from the kept values and rounded
+ * once.
+ *   ckpt   checkpoint of h, [rows][cols] (cols even for swiglu)
+ *   d_out  device [rows][width], row stride ld; width = cols, or cols / 2 for
+ *          swiglu
+ *   d_in   device [rows][cols], row stride ld_in, of d_out's type; for silu
+ *          and gelu it may be d_out itself (the same row stride)
+ * Errors: DOPT_E_ARG, DOPT_E_ALIGN, DOPT_E_CUDA.
+ */
+int dopt_ckpt_act_grad(const void *ckpt, int64_t rows, int64_t cols, dopt_act act,
+                       const void *d_out, int64_t ld, dopt_dtype dtype, void *d_in, int64_t ld_in,
+                       cudaStream_t stream);
+
+/* dopt_ckpt_wgrad flag: add to the grads in the buffer (another microbatch of
+ * the same step) instead of writing them. */
+#define DOPT_WGRAD_ACCUMULATE 1u
+
+/*
+ * Weight gradients of y = x W^T from the kept input, written where a flat
+ * grad replica holds them.  For each group g of rows (an expert; one group of
+ * all rows for a dense layer), o < outs, c < cols:
+ *     grad[grad_offsets[g] + o * cols + c]  (+)=
+ *         sum over rows r in [offsets[g], offsets[g + 1]) of
+ *             dy[r][o] * x[row_token[r]][c]
+ * with the kept values x, products exact, sums in fp32, and one rounding to
+ * the grad type (after adding the old grad, with DOPT_WGRAD_ACCUMULATE).  A
+ * group without rows gets zeros (is left alone with DOPT_WGRAD_ACCUMULATE).
+ * Rows of dy outside every group are not read as values.
+ *   ckpt          checkpoint of x, [x_rows][cols], saved from ckpt_dtype
+ *   row_token     device int32 [dy_rows] or NULL (row r of dy goes with row r
+ *                 of x; dy_rows <= x_rows then): a row outside [0, x_rows)
+ *                 counts as zeros.  dopt_route_sort's row_token lets the
+ *                 tokens be kept once, unsorted.
+ *   dy            device [dy_rows][outs], row stride dy_ld; bf16, or fp16 with
+ *                 a checkpoint saved from fp16 (both factors have one type)
+ *   offsets       device int32 [n_groups + 1] or NULL (n_groups = 1, all
+ *                 rows), as dopt_route_sort writes them; values are held to
+ *                 [0, dy_rows]
+ *   grad_offsets  HOST int64 [n_groups], copied by the call: the params'
+ *                 starts in the buffer (dopt_layout_param_offsets); the
+ *                 groups' grads must not overlap
+ *   grad          device, grad_numel elements of grad_dtype, e.g. one grad
+ *                 replica of dopt_step
+ *   workspace     device, 16-byte aligned, workspace_bytes long, or NULL:
+ *                 with room for it, few or short outputs split the rows over
+ *                 more blocks and join their fp32 sums in a fixed order.
+ *                 dopt_ckpt_wgrad_workspace says how much is of use; the
+ *                 result depends on the bytes given by rounding only.  Calls
+ *                 that share one must not overlap on the GPU.
+ * Errors: DOPT_E_ARG, DOPT_E_ALIGN, DOPT_E_CUDA.
+ */
+int dopt_ckpt_wgrad(const void *ckpt, dopt_dtype ckpt_dtype, int64_t x_rows, int64_t cols,
+                    const int32_t *row_token, const void *dy, dopt_dtype dy_dtype,
+                    int64_t dy_rows, int64_t outs, int64_t dy_ld, const int32_t *offsets,
+                    int32_t n_groups, const int64_t *grad_offsets, void *grad,
+                    dopt_dtype grad_dtype, int64_t grad_numel, uint32_t flags, void *workspace,
+                    int64_t workspace_bytes, cudaStream_t stream);
+
+/* Bytes of workspace that a dopt_ckpt_wgrad of these sizes can make use of
+ * (0 where it would not split).  Host only.  Errors: DOPT_E_ARG. */
+int dopt_ckpt_wgrad_workspace(int64_t dy_rows, int64_t outs, int64_t cols, int32_t n_groups,
+                              int64_t *bytes);
+
 /* Device-side checks (library infrastructure for testing; the pages have
  * no counterpart): a test build of the library, compiled with
  * DOPT_DEVICE_CHECKS defined; built by build(checked=True) as
- * libdopt_checked.so).  In that build every kernel checks, before each
- * vector or element access, that the index lies inside the buffers (all of
+ * libdopt_checked.so).  In that build every kernel of the flat buffer (the
+ * step, all-reduce, gather and norm kernels) checks, before each vector or
+ * element access, that the index lies inside the buffers (all of
  * a launch's buffers are padded_numel long) and that a vector starts on an
  * 8-element boundary; a failed check sets its DOPT_CHECK_* bit, records the
  * first bad element index and skips the access instead of making it.

@@ -57,3 +57,43 @@ from .binding import (  # noqa: F401
     step_from_host,
     version,
 )
+
+# The layer operators' binding imports torch, so it is loaded on first use.
+_LAYER_OPS = (
+    "DOPT_ACT_GELU",
+    "DOPT_ACT_SILU",
+    "DOPT_ACT_SWIGLU",
+    "DOPT_CKPT_BLOCK",
+    "DOPT_CKPT_PITCH",
+    "DOPT_MAX_COLS",
+    "DOPT_MAX_EXPERTS",
+    "DOPT_MAX_GROUPS",
+    "DOPT_MAX_TOPK",
+    "DOPT_WGRAD_ACCUMULATE",
+    "Checkpoint",
+    "checkpoint",
+    "ckpt_bytes",
+    "dopt_ckpt_act_grad",
+    "dopt_ckpt_load",
+    "dopt_ckpt_save",
+    "dopt_ckpt_wgrad",
+    "dopt_route_combine",
+    "dopt_route_combine_grad",
+    "dopt_route_dispatch",
+    "dopt_route_sort",
+    "route_workspace",
+    "wgrad_workspace",
+)
+
+
+def __getattr__(name):
+    if name in _LAYER_OPS:
+        from . import layer_ops
+
+        value = globals()[name] = getattr(layer_ops, name)
+        return value
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
+
+def __dir__():
+    return sorted(set(globals()) | set(_LAYER_OPS))

@@ -143,6 +143,23 @@ def _declare(lib):
     lib.dopt_stage_wait_test.argtypes = [ctypes.c_uint32]
     lib.dopt_device_checks.restype = ctypes.c_int
     lib.dopt_device_checks.argtypes = [ctypes.c_int, P(ctypes.c_uint32), P(ctypes.c_int64)]
+    i32, i64 = ctypes.c_int32, ctypes.c_int64
+    for name, types in (
+            ("dopt_route_workspace", [i64, i32, i32, P(i64)]),
+            ("dopt_route_sort", [vp, i32, i64, i32, i32, vp, vp, vp, vp, i64, vp]),
+            ("dopt_route_dispatch", [vp, ctypes.c_int, i64, i64, i64, vp, i32, vp, i64, vp]),
+            ("dopt_route_combine", [vp, ctypes.c_int, i64, vp, vp, i64, i32, i64, vp, i64, vp]),
+            ("dopt_route_combine_grad", [vp, i64, vp, ctypes.c_int, i64, vp, vp, i64, i32, i64, vp,
+                                         vp, vp]),
+            ("dopt_ckpt_bytes", [i64, i64, P(i64)]),
+            ("dopt_ckpt_save", [vp, ctypes.c_int, i64, i64, i64, vp, vp]),
+            ("dopt_ckpt_load", [vp, i64, i64, vp, i64, vp, ctypes.c_int, i64, vp]),
+            ("dopt_ckpt_act_grad", [vp, i64, i64, ctypes.c_int, vp, i64, ctypes.c_int, vp, i64, vp]),
+            ("dopt_ckpt_wgrad", [vp, ctypes.c_int, i64, i64, vp, vp, ctypes.c_int, i64, i64, i64, vp,
+                                 i32, P(i64), vp, ctypes.c_int, i64, ctypes.c_uint32, vp, i64, vp]),
+            ("dopt_ckpt_wgrad_workspace", [i64, i64, i64, i32, P(i64)])):
+        getattr(lib, name).restype = ctypes.c_int
+        getattr(lib, name).argtypes = types
     lib.dopt_last_error.restype = ctypes.c_char_p
     lib.dopt_last_error.argtypes = []
     lib.dopt_version.restype = ctypes.c_char_p

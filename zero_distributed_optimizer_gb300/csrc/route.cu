@@ -1,0 +1,555 @@
+// Tokens sorted by expert and back: the stable counting sort of a router's
+// choices (dopt_route_sort), the copy of each token's row to its experts'
+// places (dopt_route_dispatch), the weighted sum of the experts' rows
+// (dopt_route_combine) and its gradients (dopt_route_combine_grad).  dopt.h
+// states their contracts.
+#include "op_common.cuh"
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// Sort.  Slots in order; bin e < E is expert e, bin E the dropped slots.  A
+// slot's row is the number of slots in lower bins plus the number of earlier
+// slots of its own bin: counts per tile of 4096 slots, then, inside a tile,
+// counts per warp, so that every prefix is a sum of integers and the order
+// inside a bin is the slots' order (stable, the same at every call).  Up to
+// one tile of slots takes one launch of one CTA; more take a launch that
+// counts the tiles and one that places them.
+// ---------------------------------------------------------------------------
+
+constexpr int kSortThreads = 1024;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kSortRounds = 4;  // slots a thread takes
+constexpr int64_t kSortTile = int64_t(kSortThreads) * kSortRounds;
+
+struct SortArgs {
+    const void *ids;
+    int32_t *slot_row, *row_token, *offsets;
+    int32_t *counts;  // [tiles][bins]
+    int32_t slots, k, experts, tiles;
+    int32_t wide;  // 64-bit ids
+};
+
+__device__ __forceinline__ int bin_of(const SortArgs &a, int64_t slot) {
+    const int64_t id = a.wide ? static_cast<const int64_t *>(a.ids)[slot]
+                              : int64_t(static_cast<const int32_t *>(a.ids)[slot]);
+    return id >= 0 && id < a.experts ? int(id) : a.experts;
+}
+
+__global__ void __launch_bounds__(kSortThreads) dopt_route_count_kernel(const SortArgs a) {
+    extern __shared__ int32_t hist[];
+    const int bins = a.experts + 1;
+    let_dependents_start();
+    for (int b = threadIdx.x; b < bins; b += kSortThreads) hist[b] = 0;
+    wait_for_grids_before();
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kSortRounds; ++r) {
+        const int64_t s = blockIdx.x * kSortTile + r * kSortThreads + threadIdx.x;
+        if (s < a.slots) atomicAdd(&hist[bin_of(a, s)], 1);
+    }
+    __syncthreads();
+    for (int b = threadIdx.x; b < bins; b += kSortThreads)
+        a.counts[int64_t(blockIdx.x) * bins + b] = hist[b];
+}
+
+// Shared memory: base[bins], then per-warp counts [32][bins] of 16 bits (a
+// tile has 4096 slots).
+__global__ void __launch_bounds__(kSortThreads) dopt_route_place_kernel(const SortArgs a) {
+    extern __shared__ int32_t smem[];
+    __shared__ int32_t warp_sum[kSortWarps];
+    const int bins = a.experts + 1;
+    int32_t *total = smem, *base = smem + bins;
+    uint16_t *cnt = reinterpret_cast<uint16_t *>(smem + 2 * bins);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    let_dependents_start();
+    for (int b = threadIdx.x; b < bins; b += kSortThreads) total[b] = base[b] = 0;
+    for (int i = threadIdx.x; i < kSortWarps * bins; i += kSortThreads) cnt[i] = 0;
+    wait_for_grids_before();
+    __syncthreads();
+
+    // this warp's 128 slots, 32 at a time: each slot's rank among the warp's slots of its bin
+    int bin[kSortRounds], rank[kSortRounds];
+    const int64_t s0 = blockIdx.x * kSortTile + int64_t(warp) * 32 * kSortRounds + lane;
+#pragma unroll
+    for (int r = 0; r < kSortRounds; ++r) bin[r] = s0 + 32 * r < a.slots ? bin_of(a, s0 + 32 * r) : -1;
+#pragma unroll
+    for (int r = 0; r < kSortRounds; ++r) {
+        const unsigned peers = __match_any_sync(kFull, bin[r]);
+        const int before = __popc(peers & ((1u << lane) - 1u));
+        if (bin[r] >= 0) rank[r] = cnt[warp * bins + bin[r]] + before;
+        __syncwarp();
+        if (bin[r] >= 0 && before == 0) cnt[warp * bins + bin[r]] += uint16_t(__popc(peers));
+        __syncwarp();
+    }
+    if (a.tiles > 1) {  // slots of each bin in all tiles, and in the tiles before this one
+        const int n = a.tiles * bins, mine = int(blockIdx.x) * bins;
+        for (int i = threadIdx.x; i < n; i += kSortThreads) {
+            const int32_t c = a.counts[i];
+            if (c) {
+                atomicAdd(&total[i % bins], c);
+                if (i < mine) atomicAdd(&base[i % bins], c);
+            }
+        }
+    }
+    __syncthreads();
+    // the warps' counts become the slots of the bin in the warps before
+    for (int b = threadIdx.x; b < bins; b += kSortThreads) {
+        int run = 0;
+        for (int w = 0; w < kSortWarps; ++w) {
+            const int c = cnt[w * bins + b];
+            cnt[w * bins + b] = uint16_t(run);
+            run += c;
+        }
+        if (a.tiles == 1) total[b] = run;
+    }
+    __syncthreads();
+    // base += slots in lower bins (an exclusive scan of total over the bins)
+    int carry = 0;
+    for (int b0 = 0; b0 < bins; b0 += kSortThreads) {
+        const int b = b0 + int(threadIdx.x);
+        const int v = b < bins ? total[b] : 0;
+        int incl = v;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(kFull, incl, d);
+            if (lane >= d) incl += o;
+        }
+        if (lane == 31) warp_sum[warp] = incl;
+        __syncthreads();
+        if (warp == 0) {
+            int x = warp_sum[lane];
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int o = __shfl_up_sync(kFull, x, d);
+                if (lane >= d) x += o;
+            }
+            warp_sum[lane] = x;
+        }
+        __syncthreads();
+        const int excl = carry + incl - v + (warp ? warp_sum[warp - 1] : 0);
+        if (b < bins) {
+            base[b] += excl;
+            if (blockIdx.x == 0) a.offsets[b] = excl;
+        }
+        carry += warp_sum[kSortWarps - 1];
+        __syncthreads();
+    }
+#pragma unroll
+    for (int r = 0; r < kSortRounds; ++r) {
+        if (bin[r] < 0) continue;
+        const int row = base[bin[r]] + cnt[warp * bins + bin[r]] + rank[r];
+        const int64_t s = s0 + 32 * r;
+        const bool kept = bin[r] < a.experts;
+        a.slot_row[s] = kept ? row : -1;
+        a.row_token[row] = kept ? int32_t(s / a.k) : -1;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Rows.  Every kernel moves rows in accesses of VB bytes, the widest (16, 8,
+// 4 or 2) that the pointers, the row strides and the row length allow.
+// ---------------------------------------------------------------------------
+
+constexpr int kRowThreads = 256;
+constexpr int kRowWarps = kRowThreads / 32;
+
+struct RowArgs {
+    const void *x;           // dispatch: tokens; combine: sorted rows; gradient: d_out
+    const void *rows;        // gradient: sorted rows
+    void *out;               // dispatch: sorted rows; combine: tokens; gradient: d_rows
+    const int32_t *slot_row;
+    const float *weights;
+    float *d_weights;
+    int64_t tokens, n_rows;
+    int64_t ld;              // row stride of the token-ordered array, in accesses
+    int32_t vecs;            // accesses a row
+    int32_t k;
+};
+
+// A warp takes 32 * U accesses of one token's row: read once, written to the
+// row of each of the token's k slots.
+template <int VB, int U>
+__global__ void __launch_bounds__(kRowThreads) dopt_route_dispatch_kernel(const RowArgs a) {
+    using V = typename Raw<VB>::type;
+    const int lane = threadIdx.x & 31;
+    const int64_t t = int64_t(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
+    let_dependents_start();
+    wait_for_grids_before();
+    if (t >= a.tokens) return;
+    const int c0 = int(blockIdx.y) * 32 * U + lane;
+    const V *src = static_cast<const V *>(a.x) + t * a.ld;
+    V v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (c0 + 32 * u < a.vecs) v[u] = src[c0 + 32 * u];
+    for (int j0 = 0; j0 < a.k; j0 += 32) {
+        const int mine = j0 + lane < a.k ? a.slot_row[t * a.k + j0 + lane] : -1;
+        const int n = min(32, a.k - j0);
+        for (int j = 0; j < n; ++j) {
+            const int r = __shfl_sync(kFull, mine, j);
+            if (r < 0 || r >= a.n_rows) continue;
+            V *dst = static_cast<V *>(a.out) + int64_t(r) * a.vecs;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (c0 + 32 * u < a.vecs) dst[c0 + 32 * u] = v[u];
+        }
+    }
+}
+
+// A warp takes 32 * U accesses of one token's row: the sum over the token's
+// slots, in order, of weight * row, in fp32, rounded once.  Dropped slots
+// are left out (a weight of NaN there does not matter).
+template <typename T, int VB, int U>
+__global__ void __launch_bounds__(kRowThreads) dopt_route_combine_kernel(const RowArgs a) {
+    using V = typename Raw<VB>::type;
+    constexpr int N = VB / int(sizeof(T));
+    constexpr int kAhead = 4;  // slots whose rows are in flight at once
+    const int lane = threadIdx.x & 31;
+    const int64_t t = int64_t(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
+    let_dependents_start();
+    wait_for_grids_before();
+    if (t >= a.tokens) return;
+    const int c0 = int(blockIdx.y) * 32 * U + lane;
+    const V *rows = static_cast<const V *>(a.x);
+    float acc[U][N] = {};
+    for (int j0 = 0; j0 < a.k; j0 += 32) {
+        int row = -1;
+        float weight = 1.0f;
+        if (j0 + lane < a.k) {
+            row = a.slot_row[t * a.k + j0 + lane];
+            if (a.weights) weight = a.weights[t * a.k + j0 + lane];
+        }
+        const int n = min(32, a.k - j0);
+        for (int j = 0; j < n; j += kAhead) {
+            V v[kAhead][U];
+            int r[kAhead];
+            float w[kAhead];
+#pragma unroll
+            for (int q = 0; q < kAhead; ++q) {
+                r[q] = __shfl_sync(kFull, row, (j + q) & 31);
+                w[q] = __shfl_sync(kFull, weight, (j + q) & 31);
+                if (j + q >= n || r[q] >= a.n_rows) r[q] = -1;
+                if (r[q] < 0) continue;
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (c0 + 32 * u < a.vecs) v[q][u] = rows[int64_t(r[q]) * a.vecs + c0 + 32 * u];
+            }
+#pragma unroll
+            for (int q = 0; q < kAhead; ++q) {
+                if (r[q] < 0) continue;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (c0 + 32 * u >= a.vecs) continue;
+                    float f[N];
+                    unpack<T, VB>(v[q][u], f);
+#pragma unroll
+                    for (int i = 0; i < N; ++i) acc[u][i] = fmaf(w[q], f[i], acc[u][i]);
+                }
+            }
+        }
+    }
+    V *dst = static_cast<V *>(a.out) + t * a.ld;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (c0 + 32 * u < a.vecs) dst[c0 + 32 * u] = pack<T, VB>(acc[u]);
+}
+
+// A warp takes one slot: d_row = weight * d_out in one pass that also sums
+// <d_out, row>.  A CTA's 8 warps take consecutive slots, so the reads of
+// d_out by a token's k slots mostly hit in L1.
+template <typename T, int VB, int U>
+__global__ void __launch_bounds__(kRowThreads) dopt_route_combine_grad_kernel(const RowArgs a) {
+    using V = typename Raw<VB>::type;
+    constexpr int N = VB / int(sizeof(T));
+    const int lane = threadIdx.x & 31;
+    const int64_t s = int64_t(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
+    let_dependents_start();
+    wait_for_grids_before();
+    if (s >= a.tokens * a.k) return;
+    const int r = a.slot_row[s];
+    if (r < 0 || r >= a.n_rows) {
+        if (lane == 0) a.d_weights[s] = 0.0f;
+        return;
+    }
+    const float w = a.weights[s];
+    const V *d = static_cast<const V *>(a.x) + s / a.k * a.ld;
+    const V *y = static_cast<const V *>(a.rows) + int64_t(r) * a.vecs;
+    V *out = static_cast<V *>(a.out) + int64_t(r) * a.vecs;
+    float dot = 0.0f;
+    for (int c0 = lane; c0 < a.vecs; c0 += 32 * U) {
+        V dv[U], yv[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (c0 + 32 * u < a.vecs) {
+                yv[u] = y[c0 + 32 * u];
+                dv[u] = d[c0 + 32 * u];
+            }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (c0 + 32 * u >= a.vecs) continue;
+            float df[N], yf[N];
+            unpack<T, VB>(dv[u], df);
+            unpack<T, VB>(yv[u], yf);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                dot = fmaf(df[i], yf[i], dot);
+                df[i] = w * df[i];
+            }
+            out[c0 + 32 * u] = pack<T, VB>(df);
+        }
+    }
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) dot += __shfl_xor_sync(kFull, dot, m);
+    if (lane == 0) a.d_weights[s] = dot;
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+
+int64_t sort_workspace(int64_t slots, int32_t experts) {
+    const int64_t tiles = (slots + kSortTile - 1) / kSortTile;
+    return tiles > 1 ? tiles * (experts + 1) * int64_t(sizeof(int32_t)) : 0;
+}
+
+int check_slots(const char *who, int64_t tokens, int32_t k) {
+    if (tokens < 0 || k < 1 || k > DOPT_MAX_TOPK || tokens > INT32_MAX / k)
+        return dopt::fail(DOPT_E_ARG, "%s: tokens %lld, k %d (k in 1..%d, tokens * k below 2^31)",
+                          who, static_cast<long long>(tokens), k, DOPT_MAX_TOPK);
+    return DOPT_OK;
+}
+
+int check_rows(const char *who, dopt_dtype dtype, int64_t n_rows, int64_t cols, int64_t ld) {
+    if (!valid_dtype(dtype)) return dopt::fail(DOPT_E_ARG, "%s: unknown dtype %d", who, int(dtype));
+    if (n_rows < 0 || n_rows > INT32_MAX)
+        return dopt::fail(DOPT_E_ARG, "%s: n_rows out of range", who);
+    if (cols < 1 || cols > DOPT_MAX_COLS || ld < cols)
+        return dopt::fail(DOPT_E_ARG, "%s: cols %lld, row stride %lld (cols in 1..%d, stride >= cols)",
+                          who, static_cast<long long>(cols), static_cast<long long>(ld), DOPT_MAX_COLS);
+    return DOPT_OK;
+}
+
+int check_pointer(const char *who, const char *name, const void *p, size_t align) {
+    if (!p) return dopt::fail(DOPT_E_ARG, "%s: %s is NULL", who, name);
+    if (!aligned_to(p, align))
+        return dopt::fail(DOPT_E_ALIGN, "%s: %s is not aligned to its elements", who, name);
+    return DOPT_OK;
+}
+
+template <int VB, int U>
+int launch_dispatch(const char *who, const RowArgs &a, cudaStream_t stream) {
+    const dim3 grid(unsigned((a.tokens + kRowWarps - 1) / kRowWarps),
+                    unsigned((a.vecs + 32 * U - 1) / (32 * U)));
+    return launch_op(who, dopt_route_dispatch_kernel<VB, U>, grid, dim3(kRowThreads), 0, stream, a);
+}
+
+template <typename T, int VB, int U>
+int launch_combine(const char *who, const RowArgs &a, cudaStream_t stream) {
+    const dim3 grid(unsigned((a.tokens + kRowWarps - 1) / kRowWarps),
+                    unsigned((a.vecs + 32 * U - 1) / (32 * U)));
+    return launch_op(who, dopt_route_combine_kernel<T, VB, U>, grid, dim3(kRowThreads), 0, stream, a);
+}
+
+template <typename T>
+int pick_combine(const char *who, const RowArgs &a, int vb, cudaStream_t stream) {
+    if (vb == 16) return launch_combine<T, 16, 2>(who, a, stream);
+    if (vb == 8) return launch_combine<T, 8, 4>(who, a, stream);
+    if (vb == 4) return launch_combine<T, 4, 4>(who, a, stream);
+    if constexpr (sizeof(T) == 2) return launch_combine<T, 2, 4>(who, a, stream);
+    return DOPT_E_ALIGN;  // not reached: fp32 rows are 4-byte aligned
+}
+
+template <typename T, int VB, int U>
+int launch_combine_grad(const char *who, const RowArgs &a, cudaStream_t stream) {
+    const dim3 grid(unsigned((a.tokens * a.k + kRowWarps - 1) / kRowWarps));
+    return launch_op(who, dopt_route_combine_grad_kernel<T, VB, U>, grid, dim3(kRowThreads), 0,
+                     stream, a);
+}
+
+template <typename T>
+int pick_combine_grad(const char *who, const RowArgs &a, int vb, cudaStream_t stream) {
+    if (vb == 16) return launch_combine_grad<T, 16, 4>(who, a, stream);
+    if (vb == 8) return launch_combine_grad<T, 8, 4>(who, a, stream);
+    if (vb == 4) return launch_combine_grad<T, 4, 8>(who, a, stream);
+    if constexpr (sizeof(T) == 2) return launch_combine_grad<T, 2, 8>(who, a, stream);
+    return DOPT_E_ALIGN;  // not reached: fp32 rows are 4-byte aligned
+}
+
+}  // namespace
+
+extern "C" int dopt_route_workspace(int64_t tokens, int32_t k, int32_t n_experts, int64_t *bytes) {
+    dopt::clear_error();
+    const char *who = "dopt_route_workspace";
+    if (!bytes) return dopt::fail(DOPT_E_ARG, "%s: bytes is NULL", who);
+    int rc = check_slots(who, tokens, k);
+    if (rc != DOPT_OK) return rc;
+    if (n_experts < 1 || n_experts > DOPT_MAX_EXPERTS)
+        return dopt::fail(DOPT_E_ARG, "%s: n_experts %d (1..%d)", who, n_experts, DOPT_MAX_EXPERTS);
+    *bytes = sort_workspace(tokens * k, n_experts);
+    return DOPT_OK;
+}
+
+extern "C" int dopt_route_sort(const void *expert_ids, int32_t id_bytes, int64_t tokens, int32_t k,
+                               int32_t n_experts, int32_t *slot_row, int32_t *row_token,
+                               int32_t *offsets, void *workspace, int64_t workspace_bytes,
+                               cudaStream_t stream) {
+    using dopt::fail;
+    dopt::clear_error();
+    const char *who = "dopt_route_sort";
+    OpRange range(who);
+    if (id_bytes != 4 && id_bytes != 8)
+        return fail(DOPT_E_ARG, "%s: id_bytes %d is not 4 or 8", who, id_bytes);
+    int rc = check_slots(who, tokens, k);
+    if (rc != DOPT_OK) return rc;
+    if (n_experts < 1 || n_experts > DOPT_MAX_EXPERTS)
+        return fail(DOPT_E_ARG, "%s: n_experts %d (1..%d)", who, n_experts, DOPT_MAX_EXPERTS);
+    if ((rc = check_pointer(who, "offsets", offsets, 4)) != DOPT_OK) return rc;
+    if (tokens > 0) {
+        if ((rc = check_pointer(who, "expert_ids", expert_ids, size_t(id_bytes))) != DOPT_OK) return rc;
+        if ((rc = check_pointer(who, "slot_row", slot_row, 4)) != DOPT_OK) return rc;
+        if ((rc = check_pointer(who, "row_token", row_token, 4)) != DOPT_OK) return rc;
+    }
+    const int64_t need = sort_workspace(tokens * k, n_experts);
+    if (need > 0) {
+        if ((rc = check_pointer(who, "workspace", workspace, 4)) != DOPT_OK) return rc;
+        if (workspace_bytes < need)
+            return fail(DOPT_E_ARG, "%s: workspace of %lld bytes, %lld needed", who,
+                        static_cast<long long>(workspace_bytes), static_cast<long long>(need));
+    }
+    SortArgs a{};
+    a.ids = expert_ids;
+    a.slot_row = slot_row;
+    a.row_token = row_token;
+    a.offsets = offsets;
+    a.counts = static_cast<int32_t *>(workspace);
+    a.slots = int32_t(tokens * k);
+    a.k = k;
+    a.experts = n_experts;
+    a.tiles = int32_t(std::max<int64_t>(1, (a.slots + kSortTile - 1) / kSortTile));
+    a.wide = id_bytes == 8;
+    const size_t bins = size_t(n_experts) + 1;
+    if (a.tiles > 1) {
+        rc = launch_op(who, dopt_route_count_kernel, dim3(unsigned(a.tiles)), dim3(kSortThreads),
+                       bins * sizeof(int32_t), stream, a);
+        if (rc != DOPT_OK) return rc;
+    }
+    const size_t smem = 2 * bins * sizeof(int32_t) + kSortWarps * bins * sizeof(uint16_t);
+    if (smem > 48 * 1024) {
+        cudaError_t e = cudaFuncSetAttribute(dopt_route_place_kernel,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+        if (e != cudaSuccess) {
+            cudaGetLastError();
+            return fail(DOPT_E_CUDA, "%s: shared-memory limit: %s", who, cudaGetErrorString(e));
+        }
+    }
+    return launch_op(who, dopt_route_place_kernel, dim3(unsigned(a.tiles)), dim3(kSortThreads), smem,
+                     stream, a);
+}
+
+extern "C" int dopt_route_dispatch(const void *x, dopt_dtype dtype, int64_t tokens, int64_t cols,
+                                   int64_t ld, const int32_t *slot_row, int32_t k, void *rows,
+                                   int64_t n_rows, cudaStream_t stream) {
+    dopt::clear_error();
+    const char *who = "dopt_route_dispatch";
+    OpRange range(who);
+    int rc = check_slots(who, tokens, k);
+    if (rc == DOPT_OK) rc = check_rows(who, dtype, n_rows, cols, ld);
+    if (rc != DOPT_OK || tokens == 0 || n_rows == 0) return rc;
+    const size_t b = elem_bytes(dtype);
+    if ((rc = check_pointer(who, "x", x, b)) != DOPT_OK) return rc;
+    if ((rc = check_pointer(who, "slot_row", slot_row, 4)) != DOPT_OK) return rc;
+    if ((rc = check_pointer(who, "rows", rows, b)) != DOPT_OK) return rc;
+    const int vb = access_bytes(address_bits(x) | address_bits(rows) | uint64_t(ld) * b |
+                                uint64_t(cols) * b);
+    RowArgs a{};
+    a.x = x;
+    a.out = rows;
+    a.slot_row = slot_row;
+    a.tokens = tokens;
+    a.n_rows = n_rows;
+    a.ld = ld * int64_t(b) / vb;
+    a.vecs = int32_t(cols * int64_t(b) / vb);
+    a.k = k;
+    switch (vb) {
+        case 16: return launch_dispatch<16, 2>(who, a, stream);
+        case 8: return launch_dispatch<8, 4>(who, a, stream);
+        case 4: return launch_dispatch<4, 8>(who, a, stream);
+        default: return launch_dispatch<2, 8>(who, a, stream);
+    }
+}
+
+extern "C" int dopt_route_combine(const void *rows, dopt_dtype dtype, int64_t n_rows,
+                                  const int32_t *slot_row, const float *weights, int64_t tokens,
+                                  int32_t k, int64_t cols, void *out, int64_t ld,
+                                  cudaStream_t stream) {
+    dopt::clear_error();
+    const char *who = "dopt_route_combine";
+    OpRange range(who);
+    int rc = check_slots(who, tokens, k);
+    if (rc == DOPT_OK) rc = check_rows(who, dtype, n_rows, cols, ld);
+    if (rc != DOPT_OK || tokens == 0) return rc;
+    const size_t b = elem_bytes(dtype);
+    if (n_rows > 0 && (rc = check_pointer(who, "rows", rows, b)) != DOPT_OK) return rc;
+    if ((rc = check_pointer(who, "slot_row", slot_row, 4)) != DOPT_OK) return rc;
+    if (weights && (rc = check_pointer(who, "weights", weights, 4)) != DOPT_OK) return rc;
+    if ((rc = check_pointer(who, "out", out, b)) != DOPT_OK) return rc;
+    const int vb = access_bytes(address_bits(rows) | address_bits(out) | uint64_t(ld) * b |
+                                uint64_t(cols) * b);
+    RowArgs a{};
+    a.x = rows;
+    a.out = out;
+    a.slot_row = slot_row;
+    a.weights = weights;
+    a.tokens = tokens;
+    a.n_rows = n_rows;
+    a.ld = ld * int64_t(b) / vb;
+    a.vecs = int32_t(cols * int64_t(b) / vb);
+    a.k = k;
+    switch (dtype) {
+        case DOPT_BF16: return pick_combine<__nv_bfloat16>(who, a, vb, stream);
+        case DOPT_FP16: return pick_combine<__half>(who, a, vb, stream);
+        default: return pick_combine<float>(who, a, vb, stream);
+    }
+}
+
+extern "C" int dopt_route_combine_grad(const void *d_out, int64_t ld, const void *rows,
+                                       dopt_dtype dtype, int64_t n_rows, const int32_t *slot_row,
+                                       const float *weights, int64_t tokens, int32_t k,
+                                       int64_t cols, void *d_rows, float *d_weights,
+                                       cudaStream_t stream) {
+    dopt::clear_error();
+    const char *who = "dopt_route_combine_grad";
+    OpRange range(who);
+    int rc = check_slots(who, tokens, k);
+    if (rc == DOPT_OK) rc = check_rows(who, dtype, n_rows, cols, ld);
+    if (rc != DOPT_OK || tokens == 0) return rc;
+    const size_t b = elem_bytes(dtype);
+    if ((rc = check_pointer(who, "d_out", d_out, b)) != DOPT_OK) return rc;
+    if (n_rows > 0) {
+        if ((rc = check_pointer(who, "rows", rows, b)) != DOPT_OK) return rc;
+        if ((rc = check_pointer(who, "d_rows", d_rows, b)) != DOPT_OK) return rc;
+    }
+    if ((rc = check_pointer(who, "slot_row", slot_row, 4)) != DOPT_OK) return rc;
+    if ((rc = check_pointer(who, "weights", weights, 4)) != DOPT_OK) return rc;
+    if ((rc = check_pointer(who, "d_weights", d_weights, 4)) != DOPT_OK) return rc;
+    const int vb = access_bytes(address_bits(d_out) | address_bits(rows) | address_bits(d_rows) |
+                                uint64_t(ld) * b | uint64_t(cols) * b);
+    RowArgs a{};
+    a.x = d_out;
+    a.rows = rows;
+    a.out = d_rows;
+    a.slot_row = slot_row;
+    a.weights = weights;
+    a.d_weights = d_weights;
+    a.tokens = tokens;
+    a.n_rows = n_rows;
+    a.ld = ld * int64_t(b) / vb;
+    a.vecs = int32_t(cols * int64_t(b) / vb);
+    a.k = k;
+    switch (dtype) {
+        case DOPT_BF16: return pick_combine_grad<__nv_bfloat16>(who, a, vb, stream);
+        case DOPT_FP16: return pick_combine_grad<__half>(who, a, vb, stream);
+        default: return pick_combine_grad<float>(who, a, vb, stream);
+    }
+}
