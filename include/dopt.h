@@ -797,6 +797,10 @@ int dopt_ckpt_act_grad(const void *ckpt, int64_t rows, int64_t cols, dopt_act ac
  *                 dopt_ckpt_wgrad_workspace says how much is of use; the
  *                 result depends on the bytes given by rounding only.  Calls
  *                 that share one must not overlap on the GPU.
+ * The first call on a device looks up its number of SMs and the driver's
+ * tensor-map encoder; make it before any stream capture.  A wait inside the
+ * kernel that does not end within 2 s (a copy that never completes) leaves its
+ * tile unwritten and is counted (dopt_wgrad_timeouts) instead of hanging.
  * Errors: DOPT_E_ARG, DOPT_E_ALIGN, DOPT_E_CUDA.
  */
 int dopt_ckpt_wgrad(const void *ckpt, dopt_dtype ckpt_dtype, int64_t x_rows, int64_t cols,
@@ -810,6 +814,11 @@ int dopt_ckpt_wgrad(const void *ckpt, dopt_dtype ckpt_dtype, int64_t x_rows, int
  * (0 where it would not split).  Host only.  Errors: DOPT_E_ARG. */
 int dopt_ckpt_wgrad_workspace(int64_t dy_rows, int64_t outs, int64_t cols, int32_t n_groups,
                               int64_t *bytes);
+
+/* Count of dopt_ckpt_wgrad blocks on the current device whose waits ran out
+ * (0 unless a copy or product failed to complete); with reset != 0 the count
+ * is then cleared.  Synchronous.  Errors: DOPT_E_ARG (NULL count), DOPT_E_CUDA. */
+int dopt_wgrad_timeouts(int reset, uint32_t *count);
 
 /* Device-side checks (library infrastructure for testing; the pages have
  * no counterpart): a test build of the library, compiled with

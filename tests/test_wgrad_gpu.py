@@ -198,3 +198,7 @@ def test_repeats_and_another_stream():
         grads.append(grad)
     torch.cuda.synchronize()
     assert all(torch.equal(grads[0], x) for x in grads[1:])
+
+
+def test_no_wait_ran_out():
+    assert dopt.wgrad_timeouts() == 0

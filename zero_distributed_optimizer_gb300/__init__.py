@@ -82,6 +82,7 @@ _LAYER_OPS = (
     "dopt_route_dispatch",
     "dopt_route_sort",
     "route_workspace",
+    "wgrad_timeouts",
     "wgrad_workspace",
 )
 

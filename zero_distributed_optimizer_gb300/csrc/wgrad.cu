@@ -1,90 +1,592 @@
 // The weight gradients of a linear layer, or of a layer's experts, from the
 // 8-bit checkpoint of its input, written into the flat grad buffer
 // (dopt_ckpt_wgrad; dopt.h states the contract).
+#include <cuda.h>
+
+#include <mutex>
+#include <type_traits>
+
 #include "op_common.cuh"
 
 namespace {
 
+// A pair of CTAs (a cluster of two, on two SMs) computes a tile of 256
+// columns c by up to 256 outputs o of one group's gradient with
+// tcgen05.mma.cta_group::2: M = c, N = o, K = the group's rows in steps of
+// 64.  Each CTA keeps 128 of the c (operand A) and half of the o (operand B)
+// in shared memory, both as they lie in memory, rows of K with M or N
+// contiguous, in slabs of 64 columns x 64 rows with the 128-byte swizzle.
+//
+//   dy  bf16 / fp16, by TMA (a ring of 4 steps); by plain loads in a group's
+//       last step, whose rows past the group must read as zeros whatever the
+//       next group holds there, and where rows are not 16-byte aligned
+//   x   8 warps load 16 codes a thread four steps ahead, widen them (exactly)
+//       and store them swizzled (a ring of 3 steps)
+//
+// The sums are fp32 in tensor memory (128 lanes x 256 columns a CTA: half of
+// it, so two CTAs share an SM and one's stores run under the other's
+// products).  With lanes along c the stores of a warp are contiguous.
+constexpr int kTileC = 256;          // of a pair
+constexpr int kTileO = 256;
+constexpr int kK = 64;               // rows a step
+constexpr int kDyRing = 4;
+constexpr int kXRing = 3;
+constexpr int kSlab = kK * 128;      // 64 columns x 64 rows of 16 bits
+constexpr int kStage = 2 * kSlab;    // a CTA's 128 columns
+constexpr int kWorkers = 256;        // threads that widen and store
+constexpr int kWgradThreads = kWorkers + 64;
+constexpr int kTmemCols = 256;
+constexpr int kAhead = 4;            // steps whose codes are in flight
+constexpr int kMaxSplit = 16;
+constexpr int64_t kSlotBytes = int64_t(kTileC) * kTileO * 4;
+
+struct WgradBarriers {
+    unsigned long long dy_full[kDyRing], dy_empty[kDyRing], x_full[kXRing], x_empty[kXRing], done;
+    uint32_t tmem;
+    int32_t failed;
+};
+constexpr size_t kWgradSmem = (kDyRing + kXRing) * size_t(kStage) + sizeof(WgradBarriers);
+static_assert(kWgradSmem <= 115712, "two CTAs share an SM's 228 KB");
+
 struct WgradArgs {
+    CUtensorMap dy_map;        // with `tma`
     const uint8_t *codes, *scales;
     const int32_t *row_token;  // or NULL: row r reads checkpoint row r
     const void *dy;
     const int32_t *offsets;    // or NULL: one group of all rows
     void *grad;
+    float *partial;            // fp32 sums of the split tiles, [slot][o][c]
     int64_t x_rows, cols, pitch;
     int64_t dy_rows, outs, dy_ld;
+    int32_t tiles_c, tiles_o;
+    int32_t whole;             // tiles before the split ones
+    int32_t split;             // parts of a split tile
     int32_t accumulate;
+    int32_t tma, vec;          // dy by TMA; dy's rows are 16-byte aligned
+    int32_t grad_dtype;
     int64_t grad_offset[DOPT_MAX_GROUPS];
 };
 
-constexpr int kTile = 64;
-constexpr int kStep = 16;
+// Waits that ran past their limit (a copy or product that never completed);
+// the pair then left its tile alone.
+__device__ unsigned int g_wgrad_timeouts;
+constexpr unsigned long long kWaitNs = 2000000000ull;  // 2 s
 
-// A CTA takes 64 x 64 values of one group's gradient and goes through the
-// group's rows 16 at a time.
-template <typename T, typename G>
-__global__ void __launch_bounds__(256) dopt_ckpt_wgrad_kernel(const __grid_constant__ WgradArgs a) {
-    __shared__ float ys[kStep][kTile], xs[kStep][kTile];
-    let_dependents_start();
-    wait_for_grids_before();
-    const int g = blockIdx.z;
-    const int64_t o0 = int64_t(blockIdx.y) * kTile, c0 = int64_t(blockIdx.x) * kTile;
-    int64_t lo = 0, hi = a.dy_rows;
-    if (a.offsets) {
-        lo = min(max(int64_t(a.offsets[g]), int64_t(0)), a.dy_rows);
-        hi = min(max(int64_t(a.offsets[g + 1]), lo), a.dy_rows);
-    }
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    float acc[4][4] = {};
-    for (int64_t r0 = lo; r0 < hi; r0 += kStep) {
-        for (int i = threadIdx.x; i < kStep * kTile; i += 256) {
-            const int q = i / kTile, e = i % kTile;
-            const int64_t r = r0 + q;
-            float y = 0.0f, x = 0.0f;
-            if (r < hi) {
-                if (o0 + e < a.outs) y = to_f32(static_cast<const T *>(a.dy)[r * a.dy_ld + o0 + e]);
-                const int64_t t = a.row_token ? a.row_token[r] : r;
-                if (t >= 0 && t < a.x_rows && c0 + e < a.cols) {
-                    const int64_t at = t * a.pitch + c0 + e;
-                    x = float(int8_t(a.codes[at])) * ckpt_step(a.scales[at / kBlock]);
-                }
-            }
-            ys[q][e] = y;
-            xs[q][e] = x;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int q = 0; q < kStep; ++q)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(ys[q][ty * 4 + i], xs[q][tx + 16 * j], acc[i][j]);
-        __syncthreads();
-    }
-    G *grad = static_cast<G *>(a.grad) + a.grad_offset[g];
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int64_t o = o0 + ty * 4 + i, c = c0 + tx + 16 * j;
-            if (o >= a.outs || c >= a.cols) continue;
-            G *p = grad + o * a.cols + c;
-            *p = from_f32<G>(a.accumulate ? to_f32(*p) + acc[i][j] : acc[i][j]);
-        }
+__device__ __forceinline__ uint32_t smem_of(const void *p) {
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
-template <typename T, typename G>
-int launch_wgrad(const char *who, const WgradArgs &a, int n_groups, cudaStream_t stream) {
-    const dim3 grid(unsigned((a.cols + kTile - 1) / kTile), unsigned((a.outs + kTile - 1) / kTile),
-                    unsigned(n_groups));
-    return launch_op(who, dopt_ckpt_wgrad_kernel<T, G>, grid, dim3(256), 0, stream, a);
+// Wait for a phase of a barrier that threads of the cluster arrive on; false
+// once any wait of this CTA has run out of time.
+__device__ __forceinline__ bool wait_phase(WgradBarriers &b, unsigned long long &bar, uint32_t parity) {
+    const uint32_t at = smem_of(&bar);
+    unsigned long long t0 = 0;
+    for (;;) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(at), "r"(parity)
+            : "memory");
+        if (done) return true;
+        if (*static_cast<volatile int32_t *>(&b.failed)) return false;
+        unsigned long long now;
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+        if (t0 == 0) t0 = now;
+        if (now - t0 > kWaitNs) {
+            if (atomicExch(&b.failed, 1) == 0) atomicAdd(&g_wgrad_timeouts, 1u);
+            return false;
+        }
+    }
+}
+
+// Wait for the last use of each slot of a ring.
+__device__ __forceinline__ void drain(WgradBarriers &b, unsigned long long *empty, int ring, int steps) {
+    for (int s = 0; s < ring && s < steps; ++s)
+        if (!wait_phase(b, empty[s], uint32_t((steps - 1 - s) / ring) & 1)) return;
+}
+
+__device__ __forceinline__ uint32_t leader_address(uint32_t own) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(own));
+    return r;
+}
+__device__ __forceinline__ void arrive_remote(uint32_t cluster_address) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_address)
+                 : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Descriptor of an operand slab pair: 128-byte swizzle, 1024 bytes from 8
+// rows to the next 8, one slab from 64 columns to the next 64.
+__device__ __forceinline__ uint64_t slab_descriptor(uint32_t address) {
+    return (uint64_t(address & 0x3ffff) >> 4) | (uint64_t(kSlab >> 4) << 16) | (uint64_t(1024 >> 4) << 32) |
+           (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+
+// The 16-byte chunk q (of 16) of row k in a stage, swizzled.
+__device__ __forceinline__ uint32_t stage_chunk(int k, int q) {
+    return uint32_t((q >> 3) * kSlab + k * 128 + (((q & 7) ^ (k & 7)) << 4));
+}
+
+// 16 codes to 16 values of 16 bits, exactly: code * 2^k has 7 significant
+// bits.  bf16: with m a code's low 7 bits and s its sign bit, 128 + m and
+// 128 (1 + s) are bf16 whose bits are those of the code and 0x4300, and the
+// code is their difference.  fp16: 1024 + (code + 128) likewise, less 1152.
+__device__ __forceinline__ void widen(__nv_bfloat16, const uint4 &w, uint32_t byte, uint4 (&out)[2]) {
+    const uint32_t step = byte == kNanByte ? 0x7fff7fffu : byte * 0x00800080u;
+    const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+    uint32_t o[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t pair = __byte_perm(in[i / 2], 0, i & 1 ? 0x4342 : 0x4140);
+        const uint32_t m = (pair & 0x007f007fu) | 0x43004300u, s = (pair & 0x00800080u) | 0x43004300u;
+        const __nv_bfloat162 q = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&m),
+                                         *reinterpret_cast<const __nv_bfloat162 *>(&s));
+        const __nv_bfloat162 v = __hmul2(q, *reinterpret_cast<const __nv_bfloat162 *>(&step));
+        o[i] = *reinterpret_cast<const uint32_t *>(&v);
+    }
+    out[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    out[1] = make_uint4(o[4], o[5], o[6], o[7]);
+}
+__device__ __forceinline__ void widen(__half, const uint4 &w, uint32_t byte, uint4 (&out)[2]) {
+    const __half2 step = __float2half2_rn(ckpt_step(byte));
+    const uint32_t in[4] = {w.x ^ 0x80808080u, w.y ^ 0x80808080u, w.z ^ 0x80808080u, w.w ^ 0x80808080u};
+    uint32_t o[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t pair = __byte_perm(in[i / 2], 0x64646464u, i & 1 ? 0x4342 : 0x4140);
+        const __half2 q = __hsub2(*reinterpret_cast<const __half2 *>(&pair), __float2half2_rn(1152.0f));
+        const __half2 v = __hmul2(q, step);
+        o[i] = *reinterpret_cast<const uint32_t *>(&v);
+    }
+    out[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    out[1] = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+// The part of the work that one pair does.
+struct WgradItem {
+    int64_t lo, hi;    // rows
+    int64_t c0, o0;    // of the pair's tile
+    int32_t group, slot;  // slot < 0: the whole sum, written to the grads
+    int32_t n;         // outputs of the product (a multiple of 32)
+};
+
+__device__ __forceinline__ WgradItem item_of(const WgradArgs &a, int item) {
+    WgradItem it;
+    int tile = item, part = 0, parts = 1;
+    it.slot = -1;
+    if (item >= a.whole) {
+        parts = a.split;
+        tile = a.whole + (item - a.whole) / parts;
+        part = (item - a.whole) % parts;
+        if (parts > 1) it.slot = item - a.whole;
+    }
+    const int per_group = a.tiles_c * a.tiles_o;
+    it.group = tile / per_group;
+    tile %= per_group;
+    it.c0 = int64_t(tile % a.tiles_c) * kTileC;
+    it.o0 = int64_t(tile / a.tiles_c) * kTileO;
+    it.n = int(min(int64_t(kTileO), (a.outs - it.o0 + 31) / 32 * 32));
+    it.lo = 0;
+    it.hi = a.dy_rows;
+    if (a.offsets) {
+        it.lo = min(max(int64_t(a.offsets[it.group]), int64_t(0)), a.dy_rows);
+        it.hi = min(max(int64_t(a.offsets[it.group + 1]), it.lo), a.dy_rows);
+    }
+    if (parts > 1) {
+        const int64_t steps = (it.hi - it.lo + kK - 1) / kK;
+        const int64_t end = it.hi;
+        it.hi = min(end, it.lo + steps * (part + 1) / parts * kK);
+        it.lo = min(end, it.lo + steps * part / parts * kK);
+    }
+    return it;
+}
+
+// A CTA's half of 64 rows of dy by plain loads, zeros past the rows and
+// columns there are.
+template <typename T>
+__device__ __forceinline__ void stage_dy(const WgradArgs &a, int64_t r0, int64_t hi, int64_t o0, int n_half,
+                                         unsigned char *stage) {
+    const T *dy = static_cast<const T *>(a.dy);
+    const int chunks = (n_half + 7) / 8;
+    for (int i = threadIdx.x; i < kK * 16; i += kWorkers) {
+        const int k = i >> 4, q = i & 15;
+        if (q >= chunks) continue;
+        const int64_t r = r0 + k, o = o0 + q * 8;
+        uint4 raw = make_uint4(0, 0, 0, 0);
+        if (r < hi && o < a.outs) {
+            const T *p = dy + r * a.dy_ld + o;
+            if (a.vec && o + 8 <= a.outs) {
+                raw = *reinterpret_cast<const uint4 *>(p);
+            } else {
+                uint16_t e[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    e[j] = o + j < a.outs ? reinterpret_cast<const uint16_t *>(p)[j] : uint16_t(0);
+                memcpy(&raw, e, sizeof raw);
+            }
+        }
+        *reinterpret_cast<uint4 *>(stage + stage_chunk(k, q)) = raw;
+    }
+}
+
+// 32 lanes x 16 columns of a CTA's sums to the grads; `any` false: zeros.
+template <typename G>
+__device__ __forceinline__ void store_sums(const WgradArgs &a, const WgradItem &it, int64_t c, int64_t o,
+                                           const float (&f)[16]) {
+    if (c >= a.cols) return;
+    G *p = static_cast<G *>(a.grad) + a.grad_offset[it.group] + o * a.cols + c;
+    if (a.accumulate) {
+        G old[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            if (o + j < a.outs) old[j] = p[j * a.cols];
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            if (o + j < a.outs) p[j * a.cols] = from_f32<G>(to_f32(old[j]) + f[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            if (o + j < a.outs) p[j * a.cols] = from_f32<G>(f[j]);
+    }
 }
 
 template <typename T>
-int pick_wgrad(const char *who, const WgradArgs &a, int n_groups, dopt_dtype grad_dtype,
-               cudaStream_t stream) {
-    switch (grad_dtype) {
-        case DOPT_BF16: return launch_wgrad<T, __nv_bfloat16>(who, a, n_groups, stream);
-        case DOPT_FP16: return launch_wgrad<T, __half>(who, a, n_groups, stream);
-        default: return launch_wgrad<T, float>(who, a, n_groups, stream);
+__global__ void __launch_bounds__(kWgradThreads, 2) __cluster_dims__(2, 1, 1)
+    dopt_ckpt_wgrad_kernel(const __grid_constant__ WgradArgs a) {
+    extern __shared__ __align__(1024) unsigned char smem[];
+    unsigned char *dy_ring = smem, *x_ring = smem + kDyRing * kStage;
+    WgradBarriers &b = *reinterpret_cast<WgradBarriers *>(smem + (kDyRing + kXRing) * kStage);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t rank;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+
+    let_dependents_start();
+    if (threadIdx.x == 0) {
+        auto init = [](unsigned long long &bar, int count) {
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_of(&bar)), "r"(count) : "memory");
+        };
+        for (int i = 0; i < kDyRing; ++i) init(b.dy_full[i], 1), init(b.dy_empty[i], 1);
+        for (int i = 0; i < kXRing; ++i) init(b.x_full[i], 2 * kWorkers / 32), init(b.x_empty[i], 1);
+        init(b.done, 1);
+        b.failed = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kWorkers / 32 + 1) {  // all of the pair's CTAs allocate; freed before they end
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_of(&b.tmem)),
+                     "n"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    }
+    wait_for_grids_before();
+    __syncthreads();
+    cluster_sync();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    const uint32_t tmem = b.tmem;
+
+    const WgradItem it = item_of(a, int(blockIdx.x >> 1));
+    const int rows = int(it.hi - it.lo);
+    const int steps = (rows + kK - 1) / kK;
+    const int tma_steps = a.tma ? rows / kK : 0;
+    const int n_half = it.n / 2;
+    const int64_t my_o = it.o0 + int64_t(rank) * n_half;
+    const int64_t my_c = it.c0 + int64_t(rank) * (kTileC / 2);
+
+    if (warp == kWorkers / 32) {
+        if (lane == 0) {  // dy, by TMA into both CTAs, counted on the leader's barriers
+            const int boxes = (n_half + 63) / 64;
+            for (int i = 0; i < tma_steps; ++i) {
+                const int s = i % kDyRing;
+                if (i >= kDyRing && !wait_phase(b, b.dy_empty[s], uint32_t(i / kDyRing - 1) & 1)) break;
+                const uint32_t full = smem_of(&b.dy_full[s]);
+                if (rank == 0)
+                    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full),
+                                 "r"(2 * boxes * kSlab)
+                                 : "memory");
+                for (int x = 0; x < boxes; ++x)
+                    asm volatile(
+                        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+                        " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_of(dy_ring + s * kStage + x * kSlab)),
+                        "l"(&a.dy_map), "r"(int(my_o) + 64 * x), "r"(int(it.lo) + i * kK),
+                        "r"(leader_address(full))
+                        : "memory");
+            }
+            // every arrival on this CTA's barriers has happened before it ends
+            drain(b, b.dy_empty, kDyRing, steps);
+            drain(b, b.x_empty, kXRing, steps);
+        }
+    } else if (warp == kWorkers / 32 + 1) {
+        if (lane == 0 && rank == 0 && steps > 0) {  // the pair's products
+            constexpr uint32_t kFormat = std::is_same<T, __nv_bfloat16>::value ? 1 : 0;
+            const uint32_t idesc = (1u << 4) | (kFormat << 7) | (kFormat << 10) | (1u << 15) | (1u << 16) |
+                                   (uint32_t(it.n >> 3) << 17) | (uint32_t(kTileC >> 4) << 24);
+            bool ok = true;
+            for (int i = 0; i < steps && ok; ++i) {
+                const int sd = i % kDyRing, sx = i % kXRing;
+                ok = wait_phase(b, b.x_full[sx], uint32_t(i / kXRing) & 1);
+                if (ok && i < tma_steps) ok = wait_phase(b, b.dy_full[sd], uint32_t(i / kDyRing) & 1);
+                if (!ok) break;
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                const int subs = (min(kK, rows - i * kK) + 15) / 16;
+                for (int k = 0; k < subs; ++k) {
+                    const uint64_t da = slab_descriptor(smem_of(x_ring + sx * kStage) + k * 2048);
+                    const uint64_t db = slab_descriptor(smem_of(dy_ring + sd * kStage) + k * 2048);
+                    asm volatile(
+                        "{\n\t.reg .pred p;\n\t"
+                        "setp.ne.u32 p, %4, 0;\n\t"
+                        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem),
+                        "l"(da), "l"(db), "r"(idesc), "r"(uint32_t(i > 0 || k > 0))
+                        : "memory");
+                }
+                auto commit = [](unsigned long long &bar) {  // to both CTAs' barriers
+                    asm volatile(
+                        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+                        " [%0], %1;" ::"r"(smem_of(&bar)),
+                        "h"(uint16_t(3))
+                        : "memory");
+                };
+                commit(b.x_empty[sx]);
+                commit(b.dy_empty[sd]);
+                if (i == steps - 1) commit(b.done);
+            }
+        }
+    } else {
+        // x: thread t takes rows t / 8 and 32 + t / 8 of a step and 16 of its CTA's columns
+        const int j = threadIdx.x & 7, k0 = threadIdx.x >> 3;
+        const int64_t c = my_c + 16 * j;
+        const bool column = c < a.pitch;
+        // a warp's 8 rows of 4 steps: lane l holds the row of step l / 8, row
+        // (l & 3) + 4 * warp + 32 * ((l >> 2) & 1)
+        auto tokens = [&](int first) -> int {
+            const int64_t r = it.lo + int64_t(first + (lane >> 3)) * kK + (lane & 3) + 4 * warp + ((lane >> 2) & 1) * 32;
+            if (r >= it.hi) return -1;
+            const int t = a.row_token ? a.row_token[r] : int(r);
+            return t >= 0 && t < a.x_rows ? t : -1;
+        };
+        uint4 code[kAhead][2];
+        uint32_t exps[kAhead];
+        auto fetch = [&](int slot, int group_tokens) {  // the codes of step `slot` of a group of four
+            exps[slot] = 0x0101;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int64_t t = __shfl_sync(kFull, group_tokens, slot * 8 + h * 4 + (lane >> 3));
+                code[slot][h] = make_uint4(0, 0, 0, 0);
+                if (t >= 0 && column) {
+                    code[slot][h] = __ldg(reinterpret_cast<const uint4 *>(a.codes + t * a.pitch + c));
+                    const uint32_t e = __ldg(a.scales + (t * a.pitch + c) / kBlock);
+                    exps[slot] = h == 0 ? (exps[slot] & 0xff00u) | e : (exps[slot] & 0x00ffu) | (e << 8);
+                }
+            }
+        };
+        int now = tokens(0), next = tokens(kAhead);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) fetch(u, now);
+        bool ok = true;
+        const uint32_t full0 = leader_address(smem_of(&b.x_full[0]));
+        for (int i0 = 0; i0 < steps && ok; i0 += kAhead) {
+            now = next;
+            next = tokens(i0 + 2 * kAhead);
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int i = i0 + u;
+                if (i >= steps || !ok) break;
+                const int s = i % kXRing;
+                uint4 v[2][2];
+                widen(T(), code[u][0], exps[u] & 0xff, v[0]);
+                widen(T(), code[u][1], exps[u] >> 8, v[1]);
+                fetch(u, now);
+                if (i >= kXRing) ok = wait_phase(b, b.x_empty[s], uint32_t(i / kXRing - 1) & 1);
+                if (i >= tma_steps && i >= kDyRing && ok)
+                    ok = wait_phase(b, b.dy_empty[i % kDyRing], uint32_t(i / kDyRing - 1) & 1);
+                ok = __all_sync(kFull, ok);
+                if (!ok) break;
+                unsigned char *stage = x_ring + s * kStage;
+                // lanes of the upper slab store their second half first, so that
+                // 8 lanes' chunks fall into 8 different banks' groups
+                const int swap = j >> 2;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    *reinterpret_cast<uint4 *>(stage + stage_chunk(k0 + 32 * h, 2 * j + swap)) = swap ? v[h][1] : v[h][0];
+                    *reinterpret_cast<uint4 *>(stage + stage_chunk(k0 + 32 * h, 2 * j + 1 - swap)) = swap ? v[h][0] : v[h][1];
+                }
+                if (i >= tma_steps)
+                    stage_dy<T>(a, it.lo + int64_t(i) * kK, it.hi, my_o, n_half, dy_ring + (i % kDyRing) * kStage);
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) arrive_remote(full0 + uint32_t(s) * 8);
+            }
+        }
+        // the sums: warp w reads the 32 lanes that are its own (w % 4) and half of the columns
+        if (steps > 0) {
+            ok = ok && wait_phase(b, b.done, 0);
+            ok = __all_sync(kFull, ok);
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        }
+        if (ok) {
+            const int quad = warp & 3;
+            const int m = int(rank) * (kTileC / 2) + quad * 32 + lane;
+            const int cols = it.n / 2;
+            for (int o = (warp >> 2) * cols; o < ((warp >> 2) + 1) * cols; o += 16) {
+                float f[16] = {};
+                if (steps > 0) {
+                    uint32_t r[16];
+                    asm volatile(
+                        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+                        "%12, %13, %14, %15}, [%16];"
+                        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+                          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+                          "=r"(r[14]), "=r"(r[15])
+                        : "r"(tmem + (uint32_t(quad * 32) << 16) + uint32_t(o)));
+                    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) f[q] = __uint_as_float(r[q]);
+                }
+                if (it.slot >= 0) {
+                    float *p = a.partial + it.slot * (kSlotBytes / 4) + int64_t(o) * kTileC + m;
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) p[q * kTileC] = f[q];
+                } else if (a.grad_dtype == DOPT_FP32) {
+                    store_sums<float>(a, it, it.c0 + m, it.o0 + o, f);
+                } else if (a.grad_dtype == DOPT_BF16) {
+                    store_sums<__nv_bfloat16>(a, it, it.c0 + m, it.o0 + o, f);
+                } else {
+                    store_sums<__half>(a, it, it.c0 + m, it.o0 + o, f);
+                }
+            }
+        }
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    }
+    __syncthreads();
+    if (b.failed && threadIdx.x == 0) {  // copies still in flight get as long again
+        unsigned long long t0, now;
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+        do {
+            asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+        } while (now - t0 < kWaitNs);
+    }
+    __syncwarp();
+    cluster_sync();  // the peer's barriers and operands stay until both are done
+    if (warp == kWorkers / 32 + 1) {
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTmemCols));
+    }
+}
+
+// The split tiles' parts, added in the order of the rows and written.
+// blockIdx.x: tile, blockIdx.y: 16 of its outputs; a thread: one column.
+template <typename G>
+__global__ void __launch_bounds__(kTileC) dopt_ckpt_wgrad_join_kernel(const __grid_constant__ WgradArgs a) {
+    let_dependents_start();
+    wait_for_grids_before();
+    const WgradItem it = item_of(a, a.whole + int(blockIdx.x) * a.split);
+    const int o = int(blockIdx.y) * 16;
+    if (o >= it.n) return;
+    float f[16] = {};
+    for (int s = 0; s < a.split; ++s) {
+        const float *p = a.partial + (it.slot + s) * (kSlotBytes / 4) + int64_t(o) * kTileC + threadIdx.x;
+        float v[16];
+#pragma unroll
+        for (int q = 0; q < 16; ++q) v[q] = __ldcs(p + q * kTileC);
+#pragma unroll
+        for (int q = 0; q < 16; ++q) f[q] += v[q];
+    }
+    store_sums<G>(a, it, it.c0 + threadIdx.x, it.o0 + o, f);
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+
+// How the tiles go over `pairs` pairs of SMs.  Whole waves of tiles are done
+// tile by tile; the last, partial wave's tiles are split along the rows into
+// the number of parts whose estimated time is least, in steps of 64 rows: a
+// wave of parts is steps / parts, the join's launch takes about as long as 11
+// steps and a part's trip through memory 0.2.
+struct Split {
+    int64_t whole, tail;
+    int parts;
+};
+Split plan_split(int64_t tiles, int64_t steps, int64_t pairs, int64_t workspace_bytes) {
+    Split best{tiles, 0, 1};
+    const int64_t tail = tiles % pairs;
+    if (tail == 0) return best;
+    double least = double(steps);
+    for (int s = 2; s <= kMaxSplit && steps / s >= 4; ++s) {
+        if (tail * s * kSlotBytes > workspace_bytes) break;
+        const double t = double((tail * s + pairs - 1) / pairs) * double(steps) / s + 11.0 + 0.2 * double(tail * s);
+        if (t < least) {
+            least = t;
+            best = Split{tiles - tail, tail, s};
+        }
+    }
+    return best;
+}
+
+int64_t tiles_of(int64_t outs, int64_t cols, int n_groups) {
+    return (outs + kTileO - 1) / kTileO * ((cols + kTileC - 1) / kTileC) * n_groups;
+}
+int64_t steps_of(int64_t dy_rows, int n_groups) { return (dy_rows / n_groups + kK - 1) / kK; }
+
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+std::mutex g_wgrad_mutex;
+EncodeTiled g_encode = nullptr;
+int g_pairs[64] = {};  // pairs of SMs of a device, once its kernels are set up
+
+// The tensor-map encoder, the kernels' shared-memory limit and the device's
+// number of SM pairs, looked up once per device.
+int set_up(const char *who, EncodeTiled *encode, int *pairs) {
+    using dopt::fail;
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e == cudaSuccess && (device < 0 || device >= 64)) return fail(DOPT_E_ARG, "%s: device %d", who, device);
+    std::lock_guard<std::mutex> lock(g_wgrad_mutex);
+    if (e == cudaSuccess && !g_encode) {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult found{};
+        e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found);
+        if (e == cudaSuccess && (found != cudaDriverEntryPointSuccess || !f))
+            return fail(DOPT_E_CUDA, "%s: the driver has no tensor maps", who);
+        if (e == cudaSuccess) g_encode = reinterpret_cast<EncodeTiled>(f);
+    }
+    if (e == cudaSuccess && g_pairs[device] == 0) {
+        int sms = 0;
+        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(dopt_ckpt_wgrad_kernel<__nv_bfloat16>,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, int(kWgradSmem));
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(dopt_ckpt_wgrad_kernel<__half>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     int(kWgradSmem));
+        if (e == cudaSuccess) g_pairs[device] = std::max(1, sms / 2);
+    }
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return fail(DOPT_E_CUDA, "%s: set-up: %s", who, cudaGetErrorString(e));
+    }
+    *encode = g_encode;
+    *pairs = g_pairs[device];
+    return DOPT_OK;
+}
+
+template <typename T>
+int launch_wgrad(const char *who, const WgradArgs &a, int64_t items, int64_t tail, cudaStream_t stream) {
+    int rc = launch_op(who, dopt_ckpt_wgrad_kernel<T>, dim3(unsigned(2 * items)), dim3(kWgradThreads), kWgradSmem,
+                       stream, a);
+    if (rc != DOPT_OK || a.split == 1) return rc;
+    const dim3 grid(unsigned(tail), kTileO / 16);
+    switch (a.grad_dtype) {
+        case DOPT_BF16: return launch_op(who, dopt_ckpt_wgrad_join_kernel<__nv_bfloat16>, grid, dim3(kTileC), 0, stream, a);
+        case DOPT_FP16: return launch_op(who, dopt_ckpt_wgrad_join_kernel<__half>, grid, dim3(kTileC), 0, stream, a);
+        default: return launch_op(who, dopt_ckpt_wgrad_join_kernel<float>, grid, dim3(kTileC), 0, stream, a);
     }
 }
 
@@ -166,8 +668,35 @@ extern "C" int dopt_ckpt_wgrad(const void *ckpt, dopt_dtype ckpt_dtype, int64_t 
     a.outs = outs;
     a.dy_ld = dy_ld;
     a.accumulate = (flags & DOPT_WGRAD_ACCUMULATE) != 0;
-    if (dy_dtype == DOPT_BF16) return pick_wgrad<__nv_bfloat16>(who, a, n_groups, grad_dtype, stream);
-    return pick_wgrad<__half>(who, a, n_groups, grad_dtype, stream);
+    a.vec = aligned_to(dy, 16) && dy_ld * 2 % 16 == 0;
+    a.grad_dtype = grad_dtype;
+    EncodeTiled encode = nullptr;
+    int pairs = 0;
+    int rc = set_up(who, &encode, &pairs);
+    if (rc != DOPT_OK) return rc;
+    if (a.vec && dy_rows > 0) {  // 16-byte aligned rows go by TMA
+        const cuuint64_t dims[2] = {cuuint64_t(outs), cuuint64_t(dy_rows)};
+        const cuuint64_t strides[1] = {cuuint64_t(dy_ld) * 2};
+        const cuuint32_t box[2] = {64, kK}, unit[2] = {1, 1};
+        const CUresult r = encode(&a.dy_map,
+                                  dy_dtype == DOPT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                        : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                                  2, const_cast<void *>(dy), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+        a.tma = r == CUDA_SUCCESS;  // a stride past the map's limit: plain loads
+    }
+    const int64_t tiles = tiles_of(outs, cols, n_groups);
+    const Split split = plan_split(tiles, steps_of(dy_rows, n_groups), pairs, workspace_bytes);
+    const int64_t items = split.whole + split.tail * split.parts;
+    if (items > INT32_MAX / 2) return fail(DOPT_E_ARG, "%s: %lld tiles", who, static_cast<long long>(tiles));
+    a.tiles_c = int32_t((cols + kTileC - 1) / kTileC);
+    a.tiles_o = int32_t((outs + kTileO - 1) / kTileO);
+    a.whole = int32_t(split.whole);
+    a.split = split.parts;
+    a.partial = static_cast<float *>(workspace);
+    if (dy_dtype == DOPT_BF16) return launch_wgrad<__nv_bfloat16>(who, a, items, split.tail, stream);
+    return launch_wgrad<__half>(who, a, items, split.tail, stream);
 }
 
 extern "C" int dopt_ckpt_wgrad_workspace(int64_t dy_rows, int64_t outs, int64_t cols,
@@ -180,6 +709,26 @@ extern "C" int dopt_ckpt_wgrad_workspace(int64_t dy_rows, int64_t outs, int64_t 
         return dopt::fail(DOPT_E_ARG, "%s: %lld rows, %lld x %lld, %d groups", who,
                           static_cast<long long>(dy_rows), static_cast<long long>(outs),
                           static_cast<long long>(cols), n_groups);
-    *bytes = 0;
+    // for a device of 76 pairs of SMs; a call takes what it is given
+    const Split split = plan_split(tiles_of(outs, cols, n_groups), steps_of(dy_rows, n_groups), 76, INT64_MAX);
+    *bytes = split.parts > 1 ? split.tail * split.parts * kSlotBytes : 0;
+    return DOPT_OK;
+}
+
+extern "C" int dopt_wgrad_timeouts(int reset, uint32_t *count) {
+    using dopt::fail;
+    dopt::clear_error();
+    if (!count) return fail(DOPT_E_ARG, "dopt_wgrad_timeouts: NULL output");
+    unsigned int c = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&c, g_wgrad_timeouts, sizeof c);
+    if (e == cudaSuccess && reset) {
+        const unsigned int zero = 0;
+        e = cudaMemcpyToSymbol(g_wgrad_timeouts, &zero, sizeof zero);
+    }
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return fail(DOPT_E_CUDA, "dopt_wgrad_timeouts: %s", cudaGetErrorString(e));
+    }
+    *count = c;
     return DOPT_OK;
 }

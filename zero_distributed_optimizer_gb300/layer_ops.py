@@ -299,3 +299,11 @@ def dopt_ckpt_wgrad(ckpt: Checkpoint, dy, grad, grad_offsets, offsets=None, row_
           rp, dp, _dtype_code(dy.dtype, "dy"), dy_rows, outs, ld, op, n_groups, starts, gp,
           _dtype_code(grad.dtype, "grad"), numel, DOPT_WGRAD_ACCUMULATE if accumulate else 0, wp, wn,
           stream)
+
+
+def wgrad_timeouts(reset: bool = False) -> int:
+    """Blocks of :func:`dopt_ckpt_wgrad` on the current device whose waits ran
+    out of time (0 unless a copy or product failed to complete); reset clears it."""
+    c = ctypes.c_uint32(0)
+    _check(lib().dopt_wgrad_timeouts(1 if reset else 0, ctypes.byref(c)))
+    return c.value
