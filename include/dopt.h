@@ -710,8 +710,8 @@ int dopt_route_combine_grad(const void *d_out, int64_t ld, const void *rows, dop
  * 2^(floor(log2 top) - 6), no less than 2^-126 (2^-24 when fp16 values are
  * saved), and a code is value / step rounded to nearest even and held to
  * +-127: off by at most half a step, or by less than one where the value lies
- * beyond 127.5 steps.  exp = 255 marks a block that held an Inf or a NaN; all
- * of it reads back as NaN (so a poisoned activation reaches the grads, where
+ * beyond 127.5 steps.  exp = 255 (with codes 0) marks a block that held an
+ * Inf or a NaN; all of it reads back as NaN (so a poisoned activation reaches the grads, where
  * DOPT_STEP_SKIP_NONFINITE sees it).  Codes past the last column are 0.
  * The step is a power of two so that a value has 7 significant bits: bf16
  * (and fp16, if fp16 values were saved) holds it exactly, and the matrix

@@ -20,8 +20,13 @@ namespace {
 //   dy  bf16 / fp16, by TMA (a ring of 4 steps); by plain loads in a group's
 //       last step, whose rows past the group must read as zeros whatever the
 //       next group holds there, and where rows are not 16-byte aligned
-//   x   8 warps load 16 codes a thread four steps ahead, widen them (exactly)
-//       and store them swizzled (a ring of 3 steps)
+//   x   one warp copies a step's 64 rows of 128 codes to shared memory
+//       (16-byte asynchronous copies, from wherever the row's token is) with
+//       their exponent bytes, 3 steps ahead; 8 warps widen them (exactly) and store them
+//       swizzled (a ring of 2 steps).  These warps keep no load of their own
+//       in flight: the fence before a product would wait for it (codes loaded
+//       ahead into registers ran at 581 TFLOP/s, a third of the warps'
+//       time in that fence).  A row that counts as zeros has exponent bytes 0.
 //
 // The sums are fp32 in tensor memory (128 lanes x 256 columns a CTA: half of
 // it, so two CTAs share an SM and one's stores run under the other's
@@ -29,23 +34,27 @@ namespace {
 constexpr int kTileC = 256;          // of a pair
 constexpr int kTileO = 256;
 constexpr int kK = 64;               // rows a step
-constexpr int kDyRing = 4;
-constexpr int kXRing = 3;
+constexpr int kDyRing = 3;
+constexpr int kXRing = 2;
+constexpr int kRawRing = 3;
 constexpr int kSlab = kK * 128;      // 64 columns x 64 rows of 16 bits
 constexpr int kStage = 2 * kSlab;    // a CTA's 128 columns
 constexpr int kWorkers = 256;        // threads that widen and store
-constexpr int kWgradThreads = kWorkers + 64;
+constexpr int kWgradThreads = kWorkers + 96;
+constexpr int kDyWarp = kWorkers / 32, kMmaWarp = kDyWarp + 1, kRawWarp = kDyWarp + 2;
 constexpr int kTmemCols = 256;
-constexpr int kAhead = 4;            // steps whose codes are in flight
+constexpr int kRawCodes = kK * 128;  // a CTA's codes of a step, then 4 exponent bytes a row
+constexpr int kRaw = kRawCodes + kK * 4;
 constexpr int kMaxSplit = 16;
 constexpr int64_t kSlotBytes = int64_t(kTileC) * kTileO * 4;
 
 struct WgradBarriers {
-    unsigned long long dy_full[kDyRing], dy_empty[kDyRing], x_full[kXRing], x_empty[kXRing], done;
+    unsigned long long dy_full[kDyRing], dy_empty[kDyRing], x_full[kXRing], x_empty[kXRing];
+    unsigned long long raw_full[kRawRing], raw_empty[kRawRing], done;
     uint32_t tmem;
     int32_t failed;
 };
-constexpr size_t kWgradSmem = (kDyRing + kXRing) * size_t(kStage) + sizeof(WgradBarriers);
+constexpr size_t kWgradSmem = (kDyRing + kXRing) * size_t(kStage) + kRawRing * size_t(kRaw) + sizeof(WgradBarriers);
 static_assert(kWgradSmem <= 115712, "two CTAs share an SM's 228 KB");
 
 struct WgradArgs {
@@ -114,11 +123,18 @@ __device__ __forceinline__ uint32_t leader_address(uint32_t own) {
     return r;
 }
 __device__ __forceinline__ void arrive_remote(uint32_t cluster_address) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_address)
-                 : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_address) : "memory");
 }
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// An asynchronous copy of N bytes to shared memory; zeros unless `there`
+// (then nothing is read).
+template <int N>
+__device__ __forceinline__ void copy_async(uint32_t to, const void *from, bool there) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(to), "l"(from), "n"(N), "r"(there ? N : 0)
+                 : "memory");
 }
 
 // Descriptor of an operand slab pair: 128-byte swizzle, 1024 bytes from 8
@@ -133,39 +149,37 @@ __device__ __forceinline__ uint32_t stage_chunk(int k, int q) {
     return uint32_t((q >> 3) * kSlab + k * 128 + (((q & 7) ^ (k & 7)) << 4));
 }
 
-// 16 codes to 16 values of 16 bits, exactly: code * 2^k has 7 significant
+// 8 codes to 8 values of 16 bits, exactly: code * 2^k has 7 significant
 // bits.  bf16: with m a code's low 7 bits and s its sign bit, 128 + m and
 // 128 (1 + s) are bf16 whose bits are those of the code and 0x4300, and the
 // code is their difference.  fp16: 1024 + (code + 128) likewise, less 1152.
-__device__ __forceinline__ void widen(__nv_bfloat16, const uint4 &w, uint32_t byte, uint4 (&out)[2]) {
-    const uint32_t step = byte == kNanByte ? 0x7fff7fffu : byte * 0x00800080u;
-    const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-    uint32_t o[8];
+// (Codes of a block with exponent 255 are 0: times infinity, NaN.)
+__device__ __forceinline__ uint4 widen(__nv_bfloat16, const uint2 &w, uint32_t byte) {
+    const uint32_t step = byte * 0x00800080u;
+    uint32_t o[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t pair = __byte_perm(in[i / 2], 0, i & 1 ? 0x4342 : 0x4140);
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t pair = __byte_perm(i < 2 ? w.x : w.y, 0, i & 1 ? 0x4342 : 0x4140);
         const uint32_t m = (pair & 0x007f007fu) | 0x43004300u, s = (pair & 0x00800080u) | 0x43004300u;
         const __nv_bfloat162 q = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&m),
                                          *reinterpret_cast<const __nv_bfloat162 *>(&s));
         const __nv_bfloat162 v = __hmul2(q, *reinterpret_cast<const __nv_bfloat162 *>(&step));
         o[i] = *reinterpret_cast<const uint32_t *>(&v);
     }
-    out[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    out[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    return make_uint4(o[0], o[1], o[2], o[3]);
 }
-__device__ __forceinline__ void widen(__half, const uint4 &w, uint32_t byte, uint4 (&out)[2]) {
-    const __half2 step = __float2half2_rn(ckpt_step(byte));
-    const uint32_t in[4] = {w.x ^ 0x80808080u, w.y ^ 0x80808080u, w.z ^ 0x80808080u, w.w ^ 0x80808080u};
-    uint32_t o[8];
+__device__ __forceinline__ uint4 widen(__half, const uint2 &w, uint32_t byte) {
+    const __half2 step = __float2half2_rn(__uint_as_float(byte << 23));
+    const uint2 u = make_uint2(w.x ^ 0x80808080u, w.y ^ 0x80808080u);
+    uint32_t o[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t pair = __byte_perm(in[i / 2], 0x64646464u, i & 1 ? 0x4342 : 0x4140);
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t pair = __byte_perm(i < 2 ? u.x : u.y, 0x64646464u, i & 1 ? 0x4342 : 0x4140);
         const __half2 q = __hsub2(*reinterpret_cast<const __half2 *>(&pair), __float2half2_rn(1152.0f));
         const __half2 v = __hmul2(q, step);
         o[i] = *reinterpret_cast<const uint32_t *>(&v);
     }
-    out[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    out[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 // The part of the work that one pair does.
@@ -260,8 +274,8 @@ template <typename T>
 __global__ void __launch_bounds__(kWgradThreads, 2) __cluster_dims__(2, 1, 1)
     dopt_ckpt_wgrad_kernel(const __grid_constant__ WgradArgs a) {
     extern __shared__ __align__(1024) unsigned char smem[];
-    unsigned char *dy_ring = smem, *x_ring = smem + kDyRing * kStage;
-    WgradBarriers &b = *reinterpret_cast<WgradBarriers *>(smem + (kDyRing + kXRing) * kStage);
+    unsigned char *dy_ring = smem, *x_ring = smem + kDyRing * kStage, *raw_ring = x_ring + kXRing * kStage;
+    WgradBarriers &b = *reinterpret_cast<WgradBarriers *>(raw_ring + kRawRing * kRaw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint32_t rank;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
@@ -273,11 +287,12 @@ __global__ void __launch_bounds__(kWgradThreads, 2) __cluster_dims__(2, 1, 1)
         };
         for (int i = 0; i < kDyRing; ++i) init(b.dy_full[i], 1), init(b.dy_empty[i], 1);
         for (int i = 0; i < kXRing; ++i) init(b.x_full[i], 2 * kWorkers / 32), init(b.x_empty[i], 1);
+        for (int i = 0; i < kRawRing; ++i) init(b.raw_full[i], 32), init(b.raw_empty[i], kWorkers / 32);
         init(b.done, 1);
         b.failed = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == kWorkers / 32 + 1) {  // all of the pair's CTAs allocate; freed before they end
+    if (warp == kMmaWarp) {  // all of the pair's CTAs allocate; freed before they end
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_of(&b.tmem)),
                      "n"(kTmemCols)
                      : "memory");
@@ -298,7 +313,7 @@ __global__ void __launch_bounds__(kWgradThreads, 2) __cluster_dims__(2, 1, 1)
     const int64_t my_o = it.o0 + int64_t(rank) * n_half;
     const int64_t my_c = it.c0 + int64_t(rank) * (kTileC / 2);
 
-    if (warp == kWorkers / 32) {
+    if (warp == kDyWarp) {
         if (lane == 0) {  // dy, by TMA into both CTAs, counted on the leader's barriers
             const int boxes = (n_half + 63) / 64;
             for (int i = 0; i < tma_steps; ++i) {
@@ -321,7 +336,7 @@ __global__ void __launch_bounds__(kWgradThreads, 2) __cluster_dims__(2, 1, 1)
             drain(b, b.dy_empty, kDyRing, steps);
             drain(b, b.x_empty, kXRing, steps);
         }
-    } else if (warp == kWorkers / 32 + 1) {
+    } else if (warp == kMmaWarp) {
         if (lane == 0 && rank == 0 && steps > 0) {  // the pair's products
             constexpr uint32_t kFormat = std::is_same<T, __nv_bfloat16>::value ? 1 : 0;
             const uint32_t idesc = (1u << 4) | (kFormat << 7) | (kFormat << 10) | (1u << 15) | (1u << 16) |
@@ -356,70 +371,68 @@ __global__ void __launch_bounds__(kWgradThreads, 2) __cluster_dims__(2, 1, 1)
                 if (i == steps - 1) commit(b.done);
             }
         }
-    } else {
-        // x: thread t takes rows t / 8 and 32 + t / 8 of a step and 16 of its CTA's columns
-        const int j = threadIdx.x & 7, k0 = threadIdx.x >> 3;
-        const int64_t c = my_c + 16 * j;
-        const bool column = c < a.pitch;
-        // a warp's 8 rows of 4 steps: lane l holds the row of step l / 8, row
-        // (l & 3) + 4 * warp + 32 * ((l >> 2) & 1)
-        auto tokens = [&](int first) -> int {
-            const int64_t r = it.lo + int64_t(first + (lane >> 3)) * kK + (lane & 3) + 4 * warp + ((lane >> 2) & 1) * 32;
-            if (r >= it.hi) return -1;
+    } else if (warp == kRawWarp) {
+        // codes and exponent bytes: lane l takes rows l and l + 32 of a step
+        const bool column = my_c < a.pitch;
+        auto token = [&](int i, int h) -> int {
+            const int64_t r = it.lo + int64_t(i) * kK + 32 * h + lane;
+            if (r >= it.hi || !column) return -1;
             const int t = a.row_token ? a.row_token[r] : int(r);
             return t >= 0 && t < a.x_rows ? t : -1;
         };
-        uint4 code[kAhead][2];
-        uint32_t exps[kAhead];
-        auto fetch = [&](int slot, int group_tokens) {  // the codes of step `slot` of a group of four
-            exps[slot] = 0x0101;
+        int next[2] = {token(0, 0), token(0, 1)};
+        for (int i = 0; i < steps; ++i) {
+            const int s = i % kRawRing;
+            const int t[2] = {next[0], next[1]};
+            next[0] = token(i + 1, 0);
+            next[1] = token(i + 1, 1);
+            const bool ok = i < kRawRing || wait_phase(b, b.raw_empty[s], uint32_t(i / kRawRing - 1) & 1);
+            if (!__all_sync(kFull, ok)) break;
+            const uint32_t full = smem_of(&b.raw_full[s]), raw = smem_of(raw_ring + s * kRaw);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int64_t t = __shfl_sync(kFull, group_tokens, slot * 8 + h * 4 + (lane >> 3));
-                code[slot][h] = make_uint4(0, 0, 0, 0);
-                if (t >= 0 && column) {
-                    code[slot][h] = __ldg(reinterpret_cast<const uint4 *>(a.codes + t * a.pitch + c));
-                    const uint32_t e = __ldg(a.scales + (t * a.pitch + c) / kBlock);
-                    exps[slot] = h == 0 ? (exps[slot] & 0xff00u) | e : (exps[slot] & 0x00ffu) | (e << 8);
+#pragma unroll
+                for (int n = 0; n < 8; ++n) {  // 4 rows at a time, 8 lanes a row
+                    const int from = __shfl_sync(kFull, t[h], 4 * n + (lane >> 3));
+                    copy_async<16>(raw + uint32_t(32 * h + 4 * n) * 128 + lane * 16,
+                                   a.codes + int64_t(max(from, 0)) * a.pitch + my_c + (lane & 7) * 16, from >= 0);
                 }
+                copy_async<4>(raw + kRawCodes + uint32_t(lane + 32 * h) * 4,
+                              a.scales + (int64_t(max(t[h], 0)) * a.pitch + my_c) / kBlock, t[h] >= 0);
             }
-        };
-        int now = tokens(0), next = tokens(kAhead);
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) fetch(u, now);
-        bool ok = true;
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full) : "memory");
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    } else {
+        // x: a warp takes two rows at a time, a thread 8 columns: chunk q of
+        // rows 2 warp + lane / 16 + 16 h
+        const int q = lane & 15, k0 = 2 * warp + (lane >> 4);
         const uint32_t full0 = leader_address(smem_of(&b.x_full[0]));
-        for (int i0 = 0; i0 < steps && ok; i0 += kAhead) {
-            now = next;
-            next = tokens(i0 + 2 * kAhead);
+        bool ok = true;
+        for (int i = 0; i < steps; ++i) {
+            const int s = i % kXRing, sr = i % kRawRing;
+            if (i >= kXRing) ok = wait_phase(b, b.x_empty[s], uint32_t(i / kXRing - 1) & 1);
+            if (ok) ok = wait_phase(b, b.raw_full[sr], uint32_t(i / kRawRing) & 1);
+            if (i >= tma_steps && i >= kDyRing && ok)
+                ok = wait_phase(b, b.dy_empty[i % kDyRing], uint32_t(i / kDyRing - 1) & 1);
+            ok = __all_sync(kFull, ok);
+            if (!ok) break;
+            const unsigned char *raw = raw_ring + sr * kRaw;
+            unsigned char *stage = x_ring + s * kStage;
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                const int i = i0 + u;
-                if (i >= steps || !ok) break;
-                const int s = i % kXRing;
-                uint4 v[2][2];
-                widen(T(), code[u][0], exps[u] & 0xff, v[0]);
-                widen(T(), code[u][1], exps[u] >> 8, v[1]);
-                fetch(u, now);
-                if (i >= kXRing) ok = wait_phase(b, b.x_empty[s], uint32_t(i / kXRing - 1) & 1);
-                if (i >= tma_steps && i >= kDyRing && ok)
-                    ok = wait_phase(b, b.dy_empty[i % kDyRing], uint32_t(i / kDyRing - 1) & 1);
-                ok = __all_sync(kFull, ok);
-                if (!ok) break;
-                unsigned char *stage = x_ring + s * kStage;
-                // lanes of the upper slab store their second half first, so that
-                // 8 lanes' chunks fall into 8 different banks' groups
-                const int swap = j >> 2;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    *reinterpret_cast<uint4 *>(stage + stage_chunk(k0 + 32 * h, 2 * j + swap)) = swap ? v[h][1] : v[h][0];
-                    *reinterpret_cast<uint4 *>(stage + stage_chunk(k0 + 32 * h, 2 * j + 1 - swap)) = swap ? v[h][0] : v[h][1];
-                }
-                if (i >= tma_steps)
-                    stage_dy<T>(a, it.lo + int64_t(i) * kK, it.hi, my_o, n_half, dy_ring + (i % kDyRing) * kStage);
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) arrive_remote(full0 + uint32_t(s) * 8);
+            for (int h = 0; h < 4; ++h) {
+                const int k = k0 + 16 * h;
+                const uint2 codes = *reinterpret_cast<const uint2 *>(raw + k * 128 + q * 8);
+                *reinterpret_cast<uint4 *>(stage + stage_chunk(k, q)) =
+                    widen(T(), codes, raw[kRawCodes + k * 4 + (q >> 2)]);
+            }
+            if (i >= tma_steps)
+                stage_dy<T>(a, it.lo + int64_t(i) * kK, it.hi, my_o, n_half, dy_ring + (i % kDyRing) * kStage);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+                asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_of(&b.raw_empty[sr])) : "memory");
+                arrive_remote(full0 + uint32_t(s) * 8);
             }
         }
         // the sums: warp w reads the 32 lanes that are its own (w % 4) and half of the columns
@@ -472,7 +485,7 @@ __global__ void __launch_bounds__(kWgradThreads, 2) __cluster_dims__(2, 1, 1)
     }
     __syncwarp();
     cluster_sync();  // the peer's barriers and operands stay until both are done
-    if (warp == kWorkers / 32 + 1) {
+    if (warp == kMmaWarp) {
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTmemCols));
     }
