@@ -377,30 +377,42 @@ __global__ void __launch_bounds__(kWgradThreads, 2) __cluster_dims__(2, 1, 1)
         auto token = [&](int i, int h) -> int {
             const int64_t r = it.lo + int64_t(i) * kK + 32 * h + lane;
             if (r >= it.hi || !column) return -1;
-            const int t = a.row_token ? a.row_token[r] : int(r);
-            return t >= 0 && t < a.x_rows ? t : -1;
+            return a.row_token ? a.row_token[r] : int(r);
         };
-        int next[2] = {token(0, 0), token(0, 1)};
-        for (int i = 0; i < steps; ++i) {
-            const int s = i % kRawRing;
-            const int t[2] = {next[0], next[1]};
-            next[0] = token(i + 1, 0);
-            next[1] = token(i + 1, 1);
-            const bool ok = i < kRawRing || wait_phase(b, b.raw_empty[s], uint32_t(i / kRawRing - 1) & 1);
-            if (!__all_sync(kFull, ok)) break;
-            const uint32_t full = smem_of(&b.raw_full[s]), raw = smem_of(raw_ring + s * kRaw);
+        // the rows' tokens, loaded for four steps at a time and four steps
+        // ahead (looked at only when they are used, so that nothing waits)
+        int now[4][2], next[4][2];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+        for (int u = 0; u < 8; ++u) now[u >> 1][u & 1] = token(u >> 1, u & 1);
+        bool ok = true;
+        for (int i0 = 0; i0 < steps && ok; i0 += 4) {
 #pragma unroll
-                for (int n = 0; n < 8; ++n) {  // 4 rows at a time, 8 lanes a row
-                    const int from = __shfl_sync(kFull, t[h], 4 * n + (lane >> 3));
-                    copy_async<16>(raw + uint32_t(32 * h + 4 * n) * 128 + lane * 16,
-                                   a.codes + int64_t(max(from, 0)) * a.pitch + my_c + (lane & 7) * 16, from >= 0);
+            for (int u = 0; u < 8; ++u) next[u >> 1][u & 1] = token(i0 + 4 + (u >> 1), u & 1);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int i = i0 + u;
+                if (i >= steps) break;
+                const int s = i % kRawRing;
+                if (i >= kRawRing) ok = wait_phase(b, b.raw_empty[s], uint32_t(i / kRawRing - 1) & 1);
+                ok = __all_sync(kFull, ok);
+                if (!ok) break;
+                const uint32_t full = smem_of(&b.raw_full[s]), raw = smem_of(raw_ring + s * kRaw);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int t = now[u][h] < a.x_rows ? now[u][h] : -1;
+#pragma unroll
+                    for (int n = 0; n < 8; ++n) {  // 4 rows at a time, 8 lanes a row
+                        const int from = __shfl_sync(kFull, t, 4 * n + (lane >> 3));
+                        copy_async<16>(raw + uint32_t(32 * h + 4 * n) * 128 + lane * 16,
+                                       a.codes + int64_t(max(from, 0)) * a.pitch + my_c + (lane & 7) * 16, from >= 0);
+                    }
+                    copy_async<4>(raw + kRawCodes + uint32_t(lane + 32 * h) * 4,
+                                  a.scales + (int64_t(max(t, 0)) * a.pitch + my_c) / kBlock, t >= 0);
                 }
-                copy_async<4>(raw + kRawCodes + uint32_t(lane + 32 * h) * 4,
-                              a.scales + (int64_t(max(t[h], 0)) * a.pitch + my_c) / kBlock, t[h] >= 0);
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full) : "memory");
             }
-            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full) : "memory");
+#pragma unroll
+            for (int u = 0; u < 8; ++u) now[u >> 1][u & 1] = next[u >> 1][u & 1];
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
@@ -411,21 +423,24 @@ __global__ void __launch_bounds__(kWgradThreads, 2) __cluster_dims__(2, 1, 1)
         bool ok = true;
         for (int i = 0; i < steps; ++i) {
             const int s = i % kXRing, sr = i % kRawRing;
+            ok = wait_phase(b, b.raw_full[sr], uint32_t(i / kRawRing) & 1);
+            if (!__all_sync(kFull, ok)) break;
+            const unsigned char *raw = raw_ring + sr * kRaw;
+            uint4 v[4];
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                const int k = k0 + 16 * h;
+                v[h] = widen(T(), *reinterpret_cast<const uint2 *>(raw + k * 128 + q * 8),
+                             raw[kRawCodes + k * 4 + (q >> 2)]);
+            }
             if (i >= kXRing) ok = wait_phase(b, b.x_empty[s], uint32_t(i / kXRing - 1) & 1);
-            if (ok) ok = wait_phase(b, b.raw_full[sr], uint32_t(i / kRawRing) & 1);
             if (i >= tma_steps && i >= kDyRing && ok)
                 ok = wait_phase(b, b.dy_empty[i % kDyRing], uint32_t(i / kDyRing - 1) & 1);
             ok = __all_sync(kFull, ok);
             if (!ok) break;
-            const unsigned char *raw = raw_ring + sr * kRaw;
             unsigned char *stage = x_ring + s * kStage;
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                const int k = k0 + 16 * h;
-                const uint2 codes = *reinterpret_cast<const uint2 *>(raw + k * 128 + q * 8);
-                *reinterpret_cast<uint4 *>(stage + stage_chunk(k, q)) =
-                    widen(T(), codes, raw[kRawCodes + k * 4 + (q >> 2)]);
-            }
+            for (int h = 0; h < 4; ++h) *reinterpret_cast<uint4 *>(stage + stage_chunk(k0 + 16 * h, q)) = v[h];
             if (i >= tma_steps)
                 stage_dy<T>(a, it.lo + int64_t(i) * kK, it.hi, my_o, n_half, dy_ring + (i % kDyRing) * kStage);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
