@@ -20,7 +20,7 @@ namespace {
 //   dy  bf16 / fp16, by TMA (a ring of 4 steps); by plain loads in a group's
 //       last step, whose rows past the group must read as zeros whatever the
 //       next group holds there, and where rows are not 16-byte aligned
-//   x   one warp copies a step's 64 rows of 128 codes to shared memory
+//   x   two warps copy a step's 64 rows of 128 codes to shared memory
 //       (16-byte asynchronous copies, from wherever the row's token is) with
 //       their exponent bytes, 3 steps ahead; 8 warps widen them (exactly) and store them
 //       swizzled (a ring of 2 steps).  These warps keep no load of their own
@@ -40,8 +40,9 @@ constexpr int kRawRing = 3;
 constexpr int kSlab = kK * 128;      // 64 columns x 64 rows of 16 bits
 constexpr int kStage = 2 * kSlab;    // a CTA's 128 columns
 constexpr int kWorkers = 256;        // threads that widen and store
-constexpr int kWgradThreads = kWorkers + 96;
-constexpr int kDyWarp = kWorkers / 32, kMmaWarp = kDyWarp + 1, kRawWarp = kDyWarp + 2;
+constexpr int kWgradThreads = kWorkers + 128;
+constexpr int kMmaWarp = kWorkers / 32, kDyWarp = kMmaWarp + 1, kRawWarp = kMmaWarp + 2;  // and the next
+constexpr int kGroup = kWorkers / kXRing;  // threads that fill one stage of the x ring
 constexpr int kTmemCols = 256;
 constexpr int kRawCodes = kK * 128;  // a CTA's codes of a step, then 4 exponent bytes a row
 constexpr int kRaw = kRawCodes + kK * 4;
@@ -94,10 +95,10 @@ __device__ __forceinline__ bool wait_phase(WgradBarriers &b, unsigned long long 
         uint32_t done;
         asm volatile(
             "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
             "selp.u32 %0, 1, 0, p;\n\t}"
             : "=r"(done)
-            : "r"(at), "r"(parity)
+            : "r"(at), "r"(parity), "r"(1000000u)  // sleeps up to 1 ms a try
             : "memory");
         if (done) return true;
         if (*static_cast<volatile int32_t *>(&b.failed)) return false;
@@ -149,6 +150,11 @@ __device__ __forceinline__ uint32_t stage_chunk(int k, int q) {
     return uint32_t((q >> 3) * kSlab + k * 128 + (((q & 7) ^ (k & 7)) << 4));
 }
 
+// Rows of operand A are columns c in the order 0 2 1 3, 4 6 5 7, ...: the
+// bytes 0 and 2 of a word of codes, and 1 and 3, are then its pairs, without
+// a permutation of bytes.
+__device__ __forceinline__ int column_of(int m) { return (m & ~3) | ((m & 1) << 1) | ((m >> 1) & 1); }
+
 // 8 codes to 8 values of 16 bits, exactly: code * 2^k has 7 significant
 // bits.  bf16: with m a code's low 7 bits and s its sign bit, 128 + m and
 // 128 (1 + s) are bf16 whose bits are those of the code and 0x4300, and the
@@ -159,7 +165,7 @@ __device__ __forceinline__ uint4 widen(__nv_bfloat16, const uint2 &w, uint32_t b
     uint32_t o[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t pair = __byte_perm(i < 2 ? w.x : w.y, 0, i & 1 ? 0x4342 : 0x4140);
+        const uint32_t pair = (i < 2 ? w.x : w.y) >> (i & 1 ? 8 : 0);
         const uint32_t m = (pair & 0x007f007fu) | 0x43004300u, s = (pair & 0x00800080u) | 0x43004300u;
         const __nv_bfloat162 q = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&m),
                                          *reinterpret_cast<const __nv_bfloat162 *>(&s));
@@ -170,11 +176,10 @@ __device__ __forceinline__ uint4 widen(__nv_bfloat16, const uint2 &w, uint32_t b
 }
 __device__ __forceinline__ uint4 widen(__half, const uint2 &w, uint32_t byte) {
     const __half2 step = __float2half2_rn(__uint_as_float(byte << 23));
-    const uint2 u = make_uint2(w.x ^ 0x80808080u, w.y ^ 0x80808080u);
     uint32_t o[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t pair = __byte_perm(i < 2 ? u.x : u.y, 0x64646464u, i & 1 ? 0x4342 : 0x4140);
+        const uint32_t pair = (((i < 2 ? w.x : w.y) >> (i & 1 ? 8 : 0)) & 0x00ff00ffu) ^ 0x64806480u;
         const __half2 q = __hsub2(*reinterpret_cast<const __half2 *>(&pair), __float2half2_rn(1152.0f));
         const __half2 v = __hmul2(q, step);
         o[i] = *reinterpret_cast<const uint32_t *>(&v);
@@ -228,7 +233,7 @@ __device__ __forceinline__ void stage_dy(const WgradArgs &a, int64_t r0, int64_t
                                          unsigned char *stage) {
     const T *dy = static_cast<const T *>(a.dy);
     const int chunks = (n_half + 7) / 8;
-    for (int i = threadIdx.x; i < kK * 16; i += kWorkers) {
+    for (int i = threadIdx.x % kGroup; i < kK * 16; i += kGroup) {
         const int k = i >> 4, q = i & 15;
         if (q >= chunks) continue;
         const int64_t r = r0 + k, o = o0 + q * 8;
@@ -286,8 +291,8 @@ __global__ void __launch_bounds__(kWgradThreads, 2) __cluster_dims__(2, 1, 1)
             asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_of(&bar)), "r"(count) : "memory");
         };
         for (int i = 0; i < kDyRing; ++i) init(b.dy_full[i], 1), init(b.dy_empty[i], 1);
-        for (int i = 0; i < kXRing; ++i) init(b.x_full[i], 2 * kWorkers / 32), init(b.x_empty[i], 1);
-        for (int i = 0; i < kRawRing; ++i) init(b.raw_full[i], 32), init(b.raw_empty[i], kWorkers / 32);
+        for (int i = 0; i < kXRing; ++i) init(b.x_full[i], 2 * kGroup / 32), init(b.x_empty[i], 1);
+        for (int i = 0; i < kRawRing; ++i) init(b.raw_full[i], 64), init(b.raw_empty[i], kGroup / 32);
         init(b.done, 1);
         b.failed = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -313,30 +318,7 @@ __global__ void __launch_bounds__(kWgradThreads, 2) __cluster_dims__(2, 1, 1)
     const int64_t my_o = it.o0 + int64_t(rank) * n_half;
     const int64_t my_c = it.c0 + int64_t(rank) * (kTileC / 2);
 
-    if (warp == kDyWarp) {
-        if (lane == 0) {  // dy, by TMA into both CTAs, counted on the leader's barriers
-            const int boxes = (n_half + 63) / 64;
-            for (int i = 0; i < tma_steps; ++i) {
-                const int s = i % kDyRing;
-                if (i >= kDyRing && !wait_phase(b, b.dy_empty[s], uint32_t(i / kDyRing - 1) & 1)) break;
-                const uint32_t full = smem_of(&b.dy_full[s]);
-                if (rank == 0)
-                    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full),
-                                 "r"(2 * boxes * kSlab)
-                                 : "memory");
-                for (int x = 0; x < boxes; ++x)
-                    asm volatile(
-                        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-                        " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_of(dy_ring + s * kStage + x * kSlab)),
-                        "l"(&a.dy_map), "r"(int(my_o) + 64 * x), "r"(int(it.lo) + i * kK),
-                        "r"(leader_address(full))
-                        : "memory");
-            }
-            // every arrival on this CTA's barriers has happened before it ends
-            drain(b, b.dy_empty, kDyRing, steps);
-            drain(b, b.x_empty, kXRing, steps);
-        }
-    } else if (warp == kMmaWarp) {
+    if (warp == kMmaWarp) {
         if (lane == 0 && rank == 0 && steps > 0) {  // the pair's products
             constexpr uint32_t kFormat = std::is_same<T, __nv_bfloat16>::value ? 1 : 0;
             const uint32_t idesc = (1u << 4) | (kFormat << 7) | (kFormat << 10) | (1u << 15) | (1u << 16) |
@@ -371,23 +353,49 @@ __global__ void __launch_bounds__(kWgradThreads, 2) __cluster_dims__(2, 1, 1)
                 if (i == steps - 1) commit(b.done);
             }
         }
-    } else if (warp == kRawWarp) {
-        // codes and exponent bytes: lane l takes rows l and l + 32 of a step
-        const bool column = my_c < a.pitch;
-        auto token = [&](int i, int h) -> int {
-            const int64_t r = it.lo + int64_t(i) * kK + 32 * h + lane;
-            if (r >= it.hi || !column) return -1;
+    } else if (warp == kDyWarp) {
+        if (lane == 0) {  // dy, by TMA into both CTAs, counted on the leader's barriers
+            const int boxes = (n_half + 63) / 64;
+            for (int i = 0; i < tma_steps; ++i) {
+                const int s = i % kDyRing;
+                if (i >= kDyRing && !wait_phase(b, b.dy_empty[s], uint32_t(i / kDyRing - 1) & 1)) break;
+                const uint32_t full = smem_of(&b.dy_full[s]);
+                if (rank == 0)
+                    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full),
+                                 "r"(2 * boxes * kSlab)
+                                 : "memory");
+                for (int x = 0; x < boxes; ++x)
+                    asm volatile(
+                        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+                        " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_of(dy_ring + s * kStage + x * kSlab)),
+                        "l"(&a.dy_map), "r"(int(my_o) + 64 * x), "r"(int(it.lo) + i * kK), "r"(leader_address(full))
+                        : "memory");
+            }
+            // every arrival on this CTA's barriers has happened before it ends
+            drain(b, b.dy_empty, kDyRing, steps);
+            drain(b, b.x_empty, kXRing, steps);
+        }
+    } else if (warp >= kRawWarp) {
+        // x: two warps, 32 rows of a step each; lane l has the l-th row's
+        // token, loaded for four steps at a time and four steps ahead (looked
+        // at only when it is used, so that nothing waits)
+        const int row0 = 32 * (warp - kRawWarp);
+        const bool any = my_c < a.pitch && a.x_rows > 0;
+        const unsigned char *codes = a.codes + my_c + (lane & 7) * 16;
+        const unsigned char *scales = a.scales + my_c / kBlock;
+        const uint32_t pitch = uint32_t(a.pitch);
+        auto token = [&](int i) -> int {
+            const int64_t r = it.lo + int64_t(i) * kK + row0 + lane;
+            if (r >= it.hi) return -1;
             return a.row_token ? a.row_token[r] : int(r);
         };
-        // the rows' tokens, loaded for four steps at a time and four steps
-        // ahead (looked at only when they are used, so that nothing waits)
-        int now[4][2], next[4][2];
+        int now[4], next[4];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) now[u >> 1][u & 1] = token(u >> 1, u & 1);
+        for (int u = 0; u < 4; ++u) now[u] = token(u);
         bool ok = true;
         for (int i0 = 0; i0 < steps && ok; i0 += 4) {
 #pragma unroll
-            for (int u = 0; u < 8; ++u) next[u >> 1][u & 1] = token(i0 + 4 + (u >> 1), u & 1);
+            for (int u = 0; u < 4; ++u) next[u] = token(i0 + 4 + u);
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 const int i = i0 + u;
@@ -396,58 +404,72 @@ __global__ void __launch_bounds__(kWgradThreads, 2) __cluster_dims__(2, 1, 1)
                 if (i >= kRawRing) ok = wait_phase(b, b.raw_empty[s], uint32_t(i / kRawRing - 1) & 1);
                 ok = __all_sync(kFull, ok);
                 if (!ok) break;
-                const uint32_t full = smem_of(&b.raw_full[s]), raw = smem_of(raw_ring + s * kRaw);
+                const bool there = any && now[u] >= 0 && now[u] < a.x_rows;
+                const uint32_t t = there ? uint32_t(now[u]) : 0u;
+                // a row that counts as zeros has whatever codes, and exponent bytes 0
+                unsigned char *raw = raw_ring + s * kRaw + row0 * 128, *exps = raw_ring + s * kRaw + kRawCodes + (row0 + lane) * 4;
+                if (any) {
+                    const uint32_t to = smem_of(raw) + lane * 16;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int t = now[u][h] < a.x_rows ? now[u][h] : -1;
-#pragma unroll
-                    for (int n = 0; n < 8; ++n) {  // 4 rows at a time, 8 lanes a row
-                        const int from = __shfl_sync(kFull, t, 4 * n + (lane >> 3));
-                        copy_async<16>(raw + uint32_t(32 * h + 4 * n) * 128 + lane * 16,
-                                       a.codes + int64_t(max(from, 0)) * a.pitch + my_c + (lane & 7) * 16, from >= 0);
-                    }
-                    copy_async<4>(raw + kRawCodes + uint32_t(lane + 32 * h) * 4,
-                                  a.scales + (int64_t(max(t, 0)) * a.pitch + my_c) / kBlock, t >= 0);
+                    for (int n = 0; n < 8; ++n)  // 4 rows at a time, 8 lanes a row
+                        copy_async<16>(to + n * 512, codes + uint64_t(__shfl_sync(kFull, t, 4 * n + (lane >> 3))) * pitch,
+                                       true);
+                    copy_async<4>(smem_of(exps), scales + uint64_t(t) * (pitch / kBlock), there);
+                } else {
+                    *reinterpret_cast<uint32_t *>(exps) = 0;
                 }
-                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full) : "memory");
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_of(&b.raw_full[s]))
+                             : "memory");
             }
 #pragma unroll
-            for (int u = 0; u < 8; ++u) now[u >> 1][u & 1] = next[u >> 1][u & 1];
+            for (int u = 0; u < 4; ++u) now[u] = next[u];
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
-        // x: a warp takes two rows at a time, a thread 8 columns: chunk q of
-        // rows 2 warp + lane / 16 + 16 h
-        const int q = lane & 15, k0 = 2 * warp + (lane >> 4);
-        const uint32_t full0 = leader_address(smem_of(&b.x_full[0]));
+        // x: half of these warps fill the even steps' stage of the ring, half
+        // the odd steps', so that one half's waits, stores and fence run under
+        // the other's conversions.  A warp takes two rows at a time, a thread
+        // 8 columns: chunk q of rows 2 w + lane / 16 + 8 h.
+        const int half = warp / (kGroup / 32), w = warp % (kGroup / 32);
+        const int q = lane & 15, k0 = 2 * w + (lane >> 4);
+        const uint32_t full = leader_address(smem_of(&b.x_full[half]));
+        // 8 rows on: 1024 bytes on, and the swizzle is the same
+        unsigned char *stage = x_ring + half * kStage + stage_chunk(k0, q);
+        const unsigned char *my_raw = raw_ring + k0 * 128 + q * 8;
+        const unsigned char *my_exp = raw_ring + kRawCodes + k0 * 4 + (q >> 2);
         bool ok = true;
-        for (int i = 0; i < steps; ++i) {
-            const int s = i % kXRing, sr = i % kRawRing;
-            ok = wait_phase(b, b.raw_full[sr], uint32_t(i / kRawRing) & 1);
-            if (!__all_sync(kFull, ok)) break;
-            const unsigned char *raw = raw_ring + sr * kRaw;
+        uint32_t phase = 1;  // of the stage (a new barrier passes a wait for phase 1)
+        for (int i = half; i < steps; i += kXRing, phase ^= 1) {
+            const int sr = i % kRawRing;
+            // the other half is done with this slot: only then is the parity of
+            // its phase this step's (a ring of 3 alternates between the halves)
+            ok = i < kRawRing || wait_phase(b, b.raw_empty[sr], uint32_t(i / kRawRing - 1) & 1);
+            ok = ok && wait_phase(b, b.raw_full[sr], uint32_t(i / kRawRing) & 1);
+            const unsigned char *raw = my_raw + sr * kRaw, *exp = my_exp + sr * kRaw;
             uint4 v[4];
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                const int k = k0 + 16 * h;
-                v[h] = widen(T(), *reinterpret_cast<const uint2 *>(raw + k * 128 + q * 8),
-                             raw[kRawCodes + k * 4 + (q >> 2)]);
-            }
-            if (i >= kXRing) ok = wait_phase(b, b.x_empty[s], uint32_t(i / kXRing - 1) & 1);
+            for (int h = 0; h < 4; ++h)
+                v[h] = widen(T(), *reinterpret_cast<const uint2 *>(raw + h * 1024), exp[h * 32]);
+            ok = wait_phase(b, b.x_empty[half], phase) && ok;
             if (i >= tma_steps && i >= kDyRing && ok)
                 ok = wait_phase(b, b.dy_empty[i % kDyRing], uint32_t(i / kDyRing - 1) & 1);
-            ok = __all_sync(kFull, ok);
-            if (!ok) break;
-            unsigned char *stage = x_ring + s * kStage;
+            if (!__all_sync(kFull, ok)) {
+                ok = false;
+                break;
+            }
 #pragma unroll
-            for (int h = 0; h < 4; ++h) *reinterpret_cast<uint4 *>(stage + stage_chunk(k0 + 16 * h, q)) = v[h];
+            for (int h = 0; h < 4; ++h) *reinterpret_cast<uint4 *>(stage + h * 1024) = v[h];
+#pragma unroll
+            for (int h = 4; h < 8; ++h)
+                *reinterpret_cast<uint4 *>(stage + h * 1024) =
+                    widen(T(), *reinterpret_cast<const uint2 *>(raw + h * 1024), exp[h * 32]);
             if (i >= tma_steps)
                 stage_dy<T>(a, it.lo + int64_t(i) * kK, it.hi, my_o, n_half, dy_ring + (i % kDyRing) * kStage);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) {
                 asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_of(&b.raw_empty[sr])) : "memory");
-                arrive_remote(full0 + uint32_t(s) * 8);
+                arrive_remote(full);
             }
         }
         // the sums: warp w reads the 32 lanes that are its own (w % 4) and half of the columns
@@ -480,11 +502,11 @@ __global__ void __launch_bounds__(kWgradThreads, 2) __cluster_dims__(2, 1, 1)
 #pragma unroll
                     for (int q = 0; q < 16; ++q) p[q * kTileC] = f[q];
                 } else if (a.grad_dtype == DOPT_FP32) {
-                    store_sums<float>(a, it, it.c0 + m, it.o0 + o, f);
+                    store_sums<float>(a, it, it.c0 + column_of(m), it.o0 + o, f);
                 } else if (a.grad_dtype == DOPT_BF16) {
-                    store_sums<__nv_bfloat16>(a, it, it.c0 + m, it.o0 + o, f);
+                    store_sums<__nv_bfloat16>(a, it, it.c0 + column_of(m), it.o0 + o, f);
                 } else {
-                    store_sums<__half>(a, it, it.c0 + m, it.o0 + o, f);
+                    store_sums<__half>(a, it, it.c0 + column_of(m), it.o0 + o, f);
                 }
             }
         }
@@ -524,7 +546,7 @@ __global__ void __launch_bounds__(kTileC) dopt_ckpt_wgrad_join_kernel(const __gr
 #pragma unroll
         for (int q = 0; q < 16; ++q) f[q] += v[q];
     }
-    store_sums<G>(a, it, it.c0 + threadIdx.x, it.o0 + o, f);
+    store_sums<G>(a, it, it.c0 + column_of(threadIdx.x), it.o0 + o, f);
 }
 
 // ---------------------------------------------------------------------------
