@@ -10,53 +10,55 @@
 
 namespace {
 
-// A pair of CTAs (a cluster of two, on two SMs) computes a tile of 256
-// columns c by up to 256 outputs o of one group's gradient with
+// A pair of CTAs (a cluster of two, one CTA an SM) goes through tiles of 256
+// columns c by NB * 256 outputs o of one group's gradient, with
 // tcgen05.mma.cta_group::2: M = c, N = o, K = the group's rows in steps of
 // 64.  Each CTA keeps 128 of the c (operand A) and half of the o (operand B)
 // in shared memory, both as they lie in memory, rows of K with M or N
 // contiguous, in slabs of 64 columns x 64 rows with the 128-byte swizzle.
 //
-//   dy  bf16 / fp16, by TMA (a ring of 4 steps); by plain loads in a group's
-//       last step, whose rows past the group must read as zeros whatever the
-//       next group holds there, and where rows are not 16-byte aligned
-//   x   two warps copy a step's 64 rows of 128 codes to shared memory
-//       (16-byte asynchronous copies, from wherever the row's token is) with
-//       their exponent bytes, 3 steps ahead; 8 warps widen them (exactly) and store them
-//       swizzled (a ring of 2 steps).  These warps keep no load of their own
-//       in flight: the fence before a product would wait for it (codes loaded
-//       ahead into registers ran at 581 TFLOP/s, a third of the warps'
-//       time in that fence).  A row that counts as zeros has exponent bytes 0.
+//   dy  bf16 / fp16, by TMA (a ring of 8 blocks of 256 o); by plain loads in a
+//       group's last step, whose rows past the group must read as zeros
+//       whatever the next group holds there, and where rows are not 16-byte
+//       aligned
+//   x   16 warps load 8 codes a thread and row into registers, widen them to
+//       16 bits (exactly) and store them swizzled (a ring of 4 steps).  Four
+//       warps take a step, so that one step's waits, stores and fence run
+//       under another's conversions; a warp loads its next step's codes after
+//       the fence that ends a step and finds them there four steps later.  A
+//       row that counts as zeros has exponent bytes 0.
 //
-// The sums are fp32 in tensor memory (128 lanes x 256 columns a CTA: half of
-// it, so two CTAs share an SM and one's stores run under the other's
-// products).  With lanes along c the stores of a warp are contiguous.
+// The sums are fp32 in tensor memory, 128 lanes x 512 columns a CTA: NB = 1
+// uses it for two tiles in turn, four warps storing one while the other is
+// summed; NB = 2 for one tile of twice the outputs, so that codes are widened
+// once for two products, and its stores are waited for.  With lanes along c
+// the stores of a warp are contiguous.
 constexpr int kTileC = 256;          // of a pair
-constexpr int kTileO = 256;
+constexpr int kTileO = 256;          // of a product; a tile has NB of them
 constexpr int kK = 64;               // rows a step
-constexpr int kDyRing = 3;
-constexpr int kXRing = 2;
-constexpr int kRawRing = 3;
+constexpr int kDyRing = 8;
+constexpr int kXRing = 4;
 constexpr int kSlab = kK * 128;      // 64 columns x 64 rows of 16 bits
 constexpr int kStage = 2 * kSlab;    // a CTA's 128 columns
-constexpr int kWorkers = 256;        // threads that widen and store
-constexpr int kWgradThreads = kWorkers + 128;
-constexpr int kMmaWarp = kWorkers / 32, kDyWarp = kMmaWarp + 1, kRawWarp = kMmaWarp + 2;  // and the next
-constexpr int kGroup = kWorkers / kXRing;  // threads that fill one stage of the x ring
-constexpr int kTmemCols = 256;
-constexpr int kRawCodes = kK * 128;  // a CTA's codes of a step, then 4 exponent bytes a row
-constexpr int kRaw = kRawCodes + kK * 4;
+constexpr int kGroups = 4;           // of warps that widen codes
+constexpr int kGroup = 128;          // threads of one
+constexpr int kWorkers = kGroups * kGroup;
+constexpr int kStoreWarp = kWorkers / 32, kMmaWarp = kStoreWarp + 4, kDyWarp = kMmaWarp + 1;
+constexpr int kWgradThreads = 32 * (kDyWarp + 1);
+constexpr int kTmemCols = 512;
 constexpr int kMaxSplit = 16;
-constexpr int64_t kSlotBytes = int64_t(kTileC) * kTileO * 4;
+static_assert(kStoreWarp % 4 == 0, "a warp reads the tensor-memory lanes of its place in four");
 
 struct WgradBarriers {
     unsigned long long dy_full[kDyRing], dy_empty[kDyRing], x_full[kXRing], x_empty[kXRing];
-    unsigned long long raw_full[kRawRing], raw_empty[kRawRing], done;
+    unsigned long long sum_full[2], sum_empty[2];
     uint32_t tmem;
     int32_t failed;
 };
-constexpr size_t kWgradSmem = (kDyRing + kXRing) * size_t(kStage) + kRawRing * size_t(kRaw) + sizeof(WgradBarriers);
-static_assert(kWgradSmem <= 115712, "two CTAs share an SM's 228 KB");
+constexpr size_t kWgradSmem = (kDyRing + kXRing) * size_t(kStage) + sizeof(WgradBarriers);
+static_assert(kWgradSmem <= 232448, "a CTA's 227 KB");
+
+__host__ __device__ constexpr int64_t slot_floats(int nb) { return int64_t(kTileC) * kTileO * nb; }
 
 struct WgradArgs {
     CUtensorMap dy_map;        // with `tma`
@@ -69,6 +71,7 @@ struct WgradArgs {
     int64_t x_rows, cols, pitch;
     int64_t dy_rows, outs, dy_ld;
     int32_t tiles_c, tiles_o;
+    int32_t items;             // tiles and parts of tiles
     int32_t whole;             // tiles before the split ones
     int32_t split;             // parts of a split tile
     int32_t accumulate;
@@ -95,7 +98,7 @@ __device__ __forceinline__ bool wait_phase(WgradBarriers &b, unsigned long long 
         uint32_t done;
         asm volatile(
             "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
             "selp.u32 %0, 1, 0, p;\n\t}"
             : "=r"(done)
             : "r"(at), "r"(parity), "r"(1000000u)  // sleeps up to 1 ms a try
@@ -112,10 +115,21 @@ __device__ __forceinline__ bool wait_phase(WgradBarriers &b, unsigned long long 
     }
 }
 
-// Wait for the last use of each slot of a ring.
-__device__ __forceinline__ void drain(WgradBarriers &b, unsigned long long *empty, int ring, int steps) {
-    for (int s = 0; s < ring && s < steps; ++s)
-        if (!wait_phase(b, empty[s], uint32_t((steps - 1 - s) / ring) & 1)) return;
+// Wait for the last of `uses` uses of each slot of a ring.
+__device__ __forceinline__ void drain(WgradBarriers &b, unsigned long long *empty, int ring, int uses) {
+    for (int s = 0; s < ring && s < uses; ++s)
+        if (!wait_phase(b, empty[s], uint32_t((uses - 1 - s) / ring) & 1)) return;
+}
+
+// A value that is the same in all lanes, and known to be.
+template <typename V>
+__device__ __forceinline__ V uniform(V v) {
+    return __shfl_sync(kFull, v, 0);
+}
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 __device__ __forceinline__ uint32_t leader_address(uint32_t own) {
@@ -128,14 +142,6 @@ __device__ __forceinline__ void arrive_remote(uint32_t cluster_address) {
 }
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// An asynchronous copy of N bytes to shared memory; zeros unless `there`
-// (then nothing is read).
-template <int N>
-__device__ __forceinline__ void copy_async(uint32_t to, const void *from, bool there) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(to), "l"(from), "n"(N), "r"(there ? N : 0)
-                 : "memory");
 }
 
 // Descriptor of an operand slab pair: 128-byte swizzle, 1024 bytes from 8
@@ -187,14 +193,16 @@ __device__ __forceinline__ uint4 widen(__half, const uint2 &w, uint32_t byte) {
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// The part of the work that one pair does.
+// A tile, or a part of one.
 struct WgradItem {
-    int64_t lo, hi;    // rows
-    int64_t c0, o0;    // of the pair's tile
+    int64_t lo, hi;       // rows
+    int64_t c0, o0;
     int32_t group, slot;  // slot < 0: the whole sum, written to the grads
-    int32_t n;         // outputs of the product (a multiple of 32)
+    int32_t steps, full;  // of 64 rows, and those that are full
+    int32_t blocks;       // products of up to 256 outputs
 };
 
+template <int NB>
 __device__ __forceinline__ WgradItem item_of(const WgradArgs &a, int item) {
     WgradItem it;
     int tile = item, part = 0, parts = 1;
@@ -209,8 +217,8 @@ __device__ __forceinline__ WgradItem item_of(const WgradArgs &a, int item) {
     it.group = tile / per_group;
     tile %= per_group;
     it.c0 = int64_t(tile % a.tiles_c) * kTileC;
-    it.o0 = int64_t(tile / a.tiles_c) * kTileO;
-    it.n = int(min(int64_t(kTileO), (a.outs - it.o0 + 31) / 32 * 32));
+    it.o0 = int64_t(tile / a.tiles_c) * (kTileO * NB);
+    it.blocks = a.outs - it.o0 > kTileO ? NB : 1;
     it.lo = 0;
     it.hi = a.dy_rows;
     if (a.offsets) {
@@ -223,7 +231,14 @@ __device__ __forceinline__ WgradItem item_of(const WgradArgs &a, int item) {
         it.hi = min(end, it.lo + steps * (part + 1) / parts * kK);
         it.lo = min(end, it.lo + steps * part / parts * kK);
     }
+    it.steps = int(it.hi - it.lo + kK - 1) / kK;
+    it.full = int(it.hi - it.lo) / kK;
     return it;
+}
+
+// Outputs of a tile's product nb: a multiple of 32.
+__device__ __forceinline__ int block_outs(const WgradArgs &a, const WgradItem &it, int nb) {
+    return int(min(int64_t(kTileO), (a.outs - it.o0 - nb * kTileO + 31) / 32 * 32));
 }
 
 // A CTA's half of 64 rows of dy by plain loads, zeros past the rows and
@@ -254,7 +269,7 @@ __device__ __forceinline__ void stage_dy(const WgradArgs &a, int64_t r0, int64_t
     }
 }
 
-// 32 lanes x 16 columns of a CTA's sums to the grads; `any` false: zeros.
+// 16 outputs' sums of one column to the grads.
 template <typename G>
 __device__ __forceinline__ void store_sums(const WgradArgs &a, const WgradItem &it, int64_t c, int64_t o,
                                            const float (&f)[16]) {
@@ -275,15 +290,16 @@ __device__ __forceinline__ void store_sums(const WgradArgs &a, const WgradItem &
     }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kWgradThreads, 2) __cluster_dims__(2, 1, 1)
+template <typename T, int NB>
+__global__ void __launch_bounds__(kWgradThreads, 1) __cluster_dims__(2, 1, 1)
     dopt_ckpt_wgrad_kernel(const __grid_constant__ WgradArgs a) {
     extern __shared__ __align__(1024) unsigned char smem[];
-    unsigned char *dy_ring = smem, *x_ring = smem + kDyRing * kStage, *raw_ring = x_ring + kXRing * kStage;
-    WgradBarriers &b = *reinterpret_cast<WgradBarriers *>(raw_ring + kRawRing * kRaw);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    unsigned char *dy_ring = smem, *x_ring = smem + kDyRing * kStage;
+    WgradBarriers &b = *reinterpret_cast<WgradBarriers *>(x_ring + kXRing * kStage);
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     uint32_t rank;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    const int first = int(blockIdx.x >> 1), stride = int(gridDim.x >> 1);
 
     let_dependents_start();
     if (threadIdx.x == 0) {
@@ -292,12 +308,11 @@ __global__ void __launch_bounds__(kWgradThreads, 2) __cluster_dims__(2, 1, 1)
         };
         for (int i = 0; i < kDyRing; ++i) init(b.dy_full[i], 1), init(b.dy_empty[i], 1);
         for (int i = 0; i < kXRing; ++i) init(b.x_full[i], 2 * kGroup / 32), init(b.x_empty[i], 1);
-        for (int i = 0; i < kRawRing; ++i) init(b.raw_full[i], 64), init(b.raw_empty[i], kGroup / 32);
-        init(b.done, 1);
+        for (int i = 0; i < 2; ++i) init(b.sum_full[i], 1), init(b.sum_empty[i], 2 * 4);
         b.failed = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == kMmaWarp) {  // all of the pair's CTAs allocate; freed before they end
+    if (warp == kMmaWarp) {  // both of the pair's CTAs allocate; freed before they end
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_of(&b.tmem)),
                      "n"(kTmemCols)
                      : "memory");
@@ -310,181 +325,141 @@ __global__ void __launch_bounds__(kWgradThreads, 2) __cluster_dims__(2, 1, 1)
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tmem = b.tmem;
 
-    const WgradItem it = item_of(a, int(blockIdx.x >> 1));
-    const int rows = int(it.hi - it.lo);
-    const int steps = (rows + kK - 1) / kK;
-    const int tma_steps = a.tma ? rows / kK : 0;
-    const int n_half = it.n / 2;
-    const int64_t my_o = it.o0 + int64_t(rank) * n_half;
-    const int64_t my_c = it.c0 + int64_t(rank) * (kTileC / 2);
-
-    if (warp == kMmaWarp) {
-        if (lane == 0 && rank == 0 && steps > 0) {  // the pair's products
+    // Every role walks the same items.  n counts steps, u blocks of dy and t
+    // tiles that have rows: a ring's slot and phase follow from them.
+    if (warp == kDyWarp) {
+        // dy, by TMA into both CTAs, counted on the leader's barriers
+        int n = 0, u = 0;
+        bool ok = true;
+        for (int item = first; item < a.items && ok; item += stride) {
+            const WgradItem it = item_of<NB>(a, item);
+            const int steps = uniform(it.steps), full_steps = a.tma ? uniform(it.full) : 0;
+            const int blocks = it.blocks;  // (of the item's number alone)
+            const int outs[2] = {block_outs(a, it, 0), blocks > 1 ? block_outs(a, it, 1) : 0};
+            int row = uniform(int(it.lo));
+            for (int i = 0; i < steps && ok; ++i, ++n, row += kK) {
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+                    if (nb >= blocks) break;
+                    const int s = u % kDyRing;
+                    if (u >= kDyRing) ok = __all_sync(kFull, wait_phase(b, b.dy_empty[s], uint32_t(u / kDyRing - 1) & 1));
+                    if (!ok) break;
+                    if (elect_one()) {
+                        const uint32_t full = smem_of(&b.dy_full[s]);
+                        // the steps that are not full are stored by the widening warps
+                        const int boxes = i < full_steps ? (outs[nb] / 2 + 63) / 64 : 0;
+                        if (rank == 0)
+                            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full),
+                                         "r"(2 * boxes * kSlab)
+                                         : "memory");
+                        for (int x = 0; x < boxes; ++x)
+                            asm volatile(
+                                "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::"
+                                "bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_of(dy_ring + s * kStage + x * kSlab)),
+                                "l"(&a.dy_map), "r"(int(it.o0) + nb * kTileO + int(rank) * (outs[nb] / 2) + 64 * x),
+                                "r"(row), "r"(leader_address(full))
+                                : "memory");
+                    }
+                    __syncwarp();
+                    ++u;
+                }
+            }
+        }
+        // every arrival on this CTA's barriers has happened before it ends
+        if (ok) drain(b, b.dy_empty, kDyRing, u), drain(b, b.x_empty, kXRing, n);
+    } else if (warp == kMmaWarp) {
+        // The pair's products.  The whole warp walks the steps and one lane
+        // issues: operands that are the same in all lanes go to a product
+        // without the loop that a lane of its own would need (the products of
+        // a step then took 1180 cycles to issue and 512 to compute).
+        if (rank == 0) {
             constexpr uint32_t kFormat = std::is_same<T, __nv_bfloat16>::value ? 1 : 0;
-            const uint32_t idesc = (1u << 4) | (kFormat << 7) | (kFormat << 10) | (1u << 15) | (1u << 16) |
-                                   (uint32_t(it.n >> 3) << 17) | (uint32_t(kTileC >> 4) << 24);
+            constexpr uint32_t kInstruction = (1u << 4) | (kFormat << 7) | (kFormat << 10) | (1u << 15) | (1u << 16) |
+                                              (uint32_t(kTileC >> 4) << 24);
+            auto commit = [](unsigned long long &bar) {  // to both CTAs' barriers, once the products are done
+                asm volatile(
+                    "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+                    " [%0], %1;" ::"r"(smem_of(&bar)),
+                    "h"(uint16_t(3))
+                    : "memory");
+            };
+            auto product = [](uint32_t sums, uint64_t da, uint64_t db, uint32_t idesc, bool add) {
+                asm volatile(
+                    "{\n\t.reg .pred p;\n\t"
+                    "setp.ne.u32 p, %4, 0;\n\t"
+                    "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(sums),
+                    "l"(da), "l"(db), "r"(idesc), "r"(uint32_t(add))
+                    : "memory");
+            };
+            const uint32_t base = uniform(tmem);
+            const uint64_t x0 = slab_descriptor(smem_of(x_ring)), dy0 = slab_descriptor(smem_of(dy_ring));
+            int n = 0, u = 0, t = 0;
             bool ok = true;
-            for (int i = 0; i < steps && ok; ++i) {
-                const int sd = i % kDyRing, sx = i % kXRing;
-                ok = wait_phase(b, b.x_full[sx], uint32_t(i / kXRing) & 1);
-                if (ok && i < tma_steps) ok = wait_phase(b, b.dy_full[sd], uint32_t(i / kDyRing) & 1);
-                if (!ok) break;
+            for (int item = first; item < a.items && ok; item += stride) {
+                const WgradItem it = item_of<NB>(a, item);
+                const int steps = uniform(it.steps), full_steps = uniform(it.full);
+                const int rest = (uniform(int(it.hi - it.lo)) - full_steps * kK + 15) / 16;  // products of the last step
+                if (steps == 0) continue;
+                const int blocks = it.blocks;
+                const uint32_t idesc[2] = {kInstruction | (uint32_t(block_outs(a, it, 0) >> 3) << 17),
+                                           kInstruction | (uint32_t(blocks > 1 ? block_outs(a, it, 1) >> 3 : 0) << 17)};
+                const int buffer = NB == 1 ? t & 1 : 0, use = NB == 1 ? t >> 1 : t;
+                const uint32_t sums = base + uint32_t(buffer * kTileO);
+                if (use > 0) ok = __all_sync(kFull, wait_phase(b, b.sum_empty[buffer], uint32_t(use - 1) & 1));
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                const int subs = (min(kK, rows - i * kK) + 15) / 16;
-                for (int k = 0; k < subs; ++k) {
-                    const uint64_t da = slab_descriptor(smem_of(x_ring + sx * kStage) + k * 2048);
-                    const uint64_t db = slab_descriptor(smem_of(dy_ring + sd * kStage) + k * 2048);
-                    asm volatile(
-                        "{\n\t.reg .pred p;\n\t"
-                        "setp.ne.u32 p, %4, 0;\n\t"
-                        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem),
-                        "l"(da), "l"(db), "r"(idesc), "r"(uint32_t(i > 0 || k > 0))
-                        : "memory");
+                for (int i = 0; i < steps && ok; ++i, ++n) {
+                    const int sx = n % kXRing;
+                    ok = __all_sync(kFull, wait_phase(b, b.x_full[sx], uint32_t(n / kXRing) & 1));
+                    const uint64_t da = x0 + uint64_t(sx * (kStage >> 4));
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) {
+                        if (nb >= blocks || !ok) break;
+                        const int sd = u % kDyRing;
+                        ok = __all_sync(kFull, wait_phase(b, b.dy_full[sd], uint32_t(u / kDyRing) & 1));
+                        if (!ok) break;
+                        ++u;
+                        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                        const uint64_t db = dy0 + uint64_t(sd * (kStage >> 4));
+                        if (elect_one()) {  // 16 rows on: 2048 bytes on
+                            if (i < full_steps) {
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    product(sums + uint32_t(nb * kTileO), da + uint64_t(k * 128), db + uint64_t(k * 128),
+                                            idesc[nb], i > 0 || k > 0);
+                            } else {
+                                for (int k = 0; k < rest; ++k)
+                                    product(sums + uint32_t(nb * kTileO), da + uint64_t(k * 128), db + uint64_t(k * 128),
+                                            idesc[nb], i > 0 || k > 0);
+                            }
+                            commit(b.dy_empty[sd]);
+                            if (nb == blocks - 1) commit(b.x_empty[sx]);
+                            if (nb == blocks - 1 && i == steps - 1) commit(b.sum_full[buffer]);
+                        }
+                        __syncwarp();
+                    }
                 }
-                auto commit = [](unsigned long long &bar) {  // to both CTAs' barriers
-                    asm volatile(
-                        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-                        " [%0], %1;" ::"r"(smem_of(&bar)),
-                        "h"(uint16_t(3))
-                        : "memory");
-                };
-                commit(b.x_empty[sx]);
-                commit(b.dy_empty[sd]);
-                if (i == steps - 1) commit(b.done);
+                ++t;
             }
         }
-    } else if (warp == kDyWarp) {
-        if (lane == 0) {  // dy, by TMA into both CTAs, counted on the leader's barriers
-            const int boxes = (n_half + 63) / 64;
-            for (int i = 0; i < tma_steps; ++i) {
-                const int s = i % kDyRing;
-                if (i >= kDyRing && !wait_phase(b, b.dy_empty[s], uint32_t(i / kDyRing - 1) & 1)) break;
-                const uint32_t full = smem_of(&b.dy_full[s]);
-                if (rank == 0)
-                    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full),
-                                 "r"(2 * boxes * kSlab)
-                                 : "memory");
-                for (int x = 0; x < boxes; ++x)
-                    asm volatile(
-                        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-                        " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_of(dy_ring + s * kStage + x * kSlab)),
-                        "l"(&a.dy_map), "r"(int(my_o) + 64 * x), "r"(int(it.lo) + i * kK), "r"(leader_address(full))
-                        : "memory");
-            }
-            // every arrival on this CTA's barriers has happened before it ends
-            drain(b, b.dy_empty, kDyRing, steps);
-            drain(b, b.x_empty, kXRing, steps);
-        }
-    } else if (warp >= kRawWarp) {
-        // x: two warps, 32 rows of a step each; lane l has the l-th row's
-        // token, loaded for four steps at a time and four steps ahead (looked
-        // at only when it is used, so that nothing waits)
-        const int row0 = 32 * (warp - kRawWarp);
-        const bool any = my_c < a.pitch && a.x_rows > 0;
-        const unsigned char *codes = a.codes + my_c + (lane & 7) * 16;
-        const unsigned char *scales = a.scales + my_c / kBlock;
-        const uint32_t pitch = uint32_t(a.pitch);
-        auto token = [&](int i) -> int {
-            const int64_t r = it.lo + int64_t(i) * kK + row0 + lane;
-            if (r >= it.hi) return -1;
-            return a.row_token ? a.row_token[r] : int(r);
-        };
-        int now[4], next[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) now[u] = token(u);
+    } else if (warp >= kStoreWarp) {
+        // the sums to the grads: warp w reads the 32 lanes that are its own
+        const int m = int(rank) * (kTileC / 2) + (warp & 3) * 32 + lane;
+        const uint32_t lanes = tmem + (uint32_t((warp & 3) * 32) << 16);
+        int t = 0;
         bool ok = true;
-        for (int i0 = 0; i0 < steps && ok; i0 += 4) {
-#pragma unroll
-            for (int u = 0; u < 4; ++u) next[u] = token(i0 + 4 + u);
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int i = i0 + u;
-                if (i >= steps) break;
-                const int s = i % kRawRing;
-                if (i >= kRawRing) ok = wait_phase(b, b.raw_empty[s], uint32_t(i / kRawRing - 1) & 1);
-                ok = __all_sync(kFull, ok);
-                if (!ok) break;
-                const bool there = any && now[u] >= 0 && now[u] < a.x_rows;
-                const uint32_t t = there ? uint32_t(now[u]) : 0u;
-                // a row that counts as zeros has whatever codes, and exponent bytes 0
-                unsigned char *raw = raw_ring + s * kRaw + row0 * 128, *exps = raw_ring + s * kRaw + kRawCodes + (row0 + lane) * 4;
-                if (any) {
-                    const uint32_t to = smem_of(raw) + lane * 16;
-#pragma unroll
-                    for (int n = 0; n < 8; ++n)  // 4 rows at a time, 8 lanes a row
-                        copy_async<16>(to + n * 512, codes + uint64_t(__shfl_sync(kFull, t, 4 * n + (lane >> 3))) * pitch,
-                                       true);
-                    copy_async<4>(smem_of(exps), scales + uint64_t(t) * (pitch / kBlock), there);
-                } else {
-                    *reinterpret_cast<uint32_t *>(exps) = 0;
-                }
-                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_of(&b.raw_full[s]))
-                             : "memory");
+        for (int item = first; item < a.items && ok; item += stride) {
+            const WgradItem it = item_of<NB>(a, item);
+            const int buffer = NB == 1 ? t & 1 : 0, use = NB == 1 ? t >> 1 : t;
+            if (it.steps > 0) {
+                ok = wait_phase(b, b.sum_full[buffer], uint32_t(use) & 1);
+                if (!__all_sync(kFull, ok)) break;
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             }
-#pragma unroll
-            for (int u = 0; u < 4; ++u) now[u] = next[u];
-        }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-    } else {
-        // x: half of these warps fill the even steps' stage of the ring, half
-        // the odd steps', so that one half's waits, stores and fence run under
-        // the other's conversions.  A warp takes two rows at a time, a thread
-        // 8 columns: chunk q of rows 2 w + lane / 16 + 8 h.
-        const int half = warp / (kGroup / 32), w = warp % (kGroup / 32);
-        const int q = lane & 15, k0 = 2 * w + (lane >> 4);
-        const uint32_t full = leader_address(smem_of(&b.x_full[half]));
-        // 8 rows on: 1024 bytes on, and the swizzle is the same
-        unsigned char *stage = x_ring + half * kStage + stage_chunk(k0, q);
-        const unsigned char *my_raw = raw_ring + k0 * 128 + q * 8;
-        const unsigned char *my_exp = raw_ring + kRawCodes + k0 * 4 + (q >> 2);
-        bool ok = true;
-        uint32_t phase = 1;  // of the stage (a new barrier passes a wait for phase 1)
-        for (int i = half; i < steps; i += kXRing, phase ^= 1) {
-            const int sr = i % kRawRing;
-            // the other half is done with this slot: only then is the parity of
-            // its phase this step's (a ring of 3 alternates between the halves)
-            ok = i < kRawRing || wait_phase(b, b.raw_empty[sr], uint32_t(i / kRawRing - 1) & 1);
-            ok = ok && wait_phase(b, b.raw_full[sr], uint32_t(i / kRawRing) & 1);
-            const unsigned char *raw = my_raw + sr * kRaw, *exp = my_exp + sr * kRaw;
-            uint4 v[4];
-#pragma unroll
-            for (int h = 0; h < 4; ++h)
-                v[h] = widen(T(), *reinterpret_cast<const uint2 *>(raw + h * 1024), exp[h * 32]);
-            ok = wait_phase(b, b.x_empty[half], phase) && ok;
-            if (i >= tma_steps && i >= kDyRing && ok)
-                ok = wait_phase(b, b.dy_empty[i % kDyRing], uint32_t(i / kDyRing - 1) & 1);
-            if (!__all_sync(kFull, ok)) {
-                ok = false;
-                break;
-            }
-#pragma unroll
-            for (int h = 0; h < 4; ++h) *reinterpret_cast<uint4 *>(stage + h * 1024) = v[h];
-#pragma unroll
-            for (int h = 4; h < 8; ++h)
-                *reinterpret_cast<uint4 *>(stage + h * 1024) =
-                    widen(T(), *reinterpret_cast<const uint2 *>(raw + h * 1024), exp[h * 32]);
-            if (i >= tma_steps)
-                stage_dy<T>(a, it.lo + int64_t(i) * kK, it.hi, my_o, n_half, dy_ring + (i % kDyRing) * kStage);
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) {
-                asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_of(&b.raw_empty[sr])) : "memory");
-                arrive_remote(full);
-            }
-        }
-        // the sums: warp w reads the 32 lanes that are its own (w % 4) and half of the columns
-        if (steps > 0) {
-            ok = ok && wait_phase(b, b.done, 0);
-            ok = __all_sync(kFull, ok);
-            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        }
-        if (ok) {
-            const int quad = warp & 3;
-            const int m = int(rank) * (kTileC / 2) + quad * 32 + lane;
-            const int cols = it.n / 2;
-            for (int o = (warp >> 2) * cols; o < ((warp >> 2) + 1) * cols; o += 16) {
+            const int64_t c = it.c0 + column_of(m);
+            const int outs = (it.blocks - 1) * kTileO + block_outs(a, it, it.blocks - 1);
+            for (int o = 0; o < outs; o += 16) {
                 float f[16] = {};
-                if (steps > 0) {
+                if (it.steps > 0) {
                     uint32_t r[16];
                     asm volatile(
                         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
@@ -492,25 +467,118 @@ __global__ void __launch_bounds__(kWgradThreads, 2) __cluster_dims__(2, 1, 1)
                         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
                           "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
                           "=r"(r[14]), "=r"(r[15])
-                        : "r"(tmem + (uint32_t(quad * 32) << 16) + uint32_t(o)));
+                        : "r"(lanes + uint32_t(buffer * kTileO + o)));
                     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
                     for (int q = 0; q < 16; ++q) f[q] = __uint_as_float(r[q]);
                 }
                 if (it.slot >= 0) {
-                    float *p = a.partial + it.slot * (kSlotBytes / 4) + int64_t(o) * kTileC + m;
+                    float *p = a.partial + it.slot * slot_floats(NB) + int64_t(o) * kTileC + m;
 #pragma unroll
                     for (int q = 0; q < 16; ++q) p[q * kTileC] = f[q];
                 } else if (a.grad_dtype == DOPT_FP32) {
-                    store_sums<float>(a, it, it.c0 + column_of(m), it.o0 + o, f);
+                    store_sums<float>(a, it, c, it.o0 + o, f);
                 } else if (a.grad_dtype == DOPT_BF16) {
-                    store_sums<__nv_bfloat16>(a, it, it.c0 + column_of(m), it.o0 + o, f);
+                    store_sums<__nv_bfloat16>(a, it, c, it.o0 + o, f);
                 } else {
-                    store_sums<__half>(a, it, it.c0 + column_of(m), it.o0 + o, f);
+                    store_sums<__half>(a, it, c, it.o0 + o, f);
                 }
             }
+            if (it.steps > 0) {
+                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) arrive_remote(leader_address(smem_of(&b.sum_empty[buffer])));
+                ++t;
+            }
         }
-        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    } else {
+        // x: group g takes steps g, g + 4, ... of all the pair's steps; a warp 16
+        // rows of a step, two at a time, a thread 8 columns: chunk q of rows
+        // 2 w + lane / 16 + 8 h
+        const int w = warp & 3, q = lane & 15;
+        struct {
+            WgradItem it;
+            int item, i, n, u;  // the item, the step in it; the step and block of dy of all
+        } at;
+        at.item = first;
+        at.i = at.n = at.u = 0;
+        // on by so many steps, over items; false past the last
+        auto advance = [&](int by) -> bool {
+            at.i += by;
+            at.n += by;
+            at.u += by * at.it.blocks;
+            while (at.i >= at.it.steps) {
+                at.u -= (at.i - at.it.steps) * at.it.blocks;
+                at.i -= at.it.steps;
+                at.item += stride;
+                if (at.item >= a.items) return false;
+                at.it = item_of<NB>(a, at.item);
+                at.u += at.i * at.it.blocks;
+            }
+            return true;
+        };
+        uint2 code[8];
+        uint32_t exp[8];
+        int tokens = -1;
+        // the token of row 2 w + (l & 1) + 8 (l / 2) of the step, in lane l
+        auto load_tokens = [&]() {
+            const int64_t r = at.it.lo + int64_t(at.i) * kK + 2 * w + (lane & 1) + 4 * (lane & 14);
+            tokens = -1;
+            if (r < at.it.hi && lane < 16) tokens = a.row_token ? a.row_token[r] : int(r);
+        };
+        auto load_codes = [&]() {
+            const int64_t c = at.it.c0 + int64_t(rank) * (kTileC / 2);
+            const bool any = c < a.pitch && a.x_rows > 0;
+            const unsigned char *codes = a.codes + c + q * 8, *scales = a.scales + c / kBlock + (q >> 2);
+            const uint32_t pitch = uint32_t(a.pitch);
+#pragma unroll
+            for (int h = 0; h < 8; ++h) {
+                const int t = __shfl_sync(kFull, tokens, 2 * h + (lane >> 4));
+                code[h] = make_uint2(0, 0);
+                exp[h] = 0;  // counts as zeros
+                if (any && t >= 0 && t < a.x_rows) {
+                    code[h] = __ldg(reinterpret_cast<const uint2 *>(codes + uint64_t(uint32_t(t)) * pitch));
+                    exp[h] = __ldg(scales + uint64_t(uint32_t(t)) * (pitch / kBlock));
+                }
+            }
+        };
+        at.it = item_of<NB>(a, min(first, a.items - 1));
+        bool more = first < a.items && advance(warp >> 2);
+        if (more) load_tokens(), load_codes();
+        // 8 rows on: 1024 bytes on, and the swizzle is the same
+        unsigned char *my_stage = x_ring + stage_chunk(2 * w + (lane >> 4), q);
+        bool ok = true;
+        while (more) {
+            const int s = at.n % kXRing;
+            unsigned char *stage = my_stage + s * kStage;
+            uint4 v[4];
+#pragma unroll
+            for (int h = 0; h < 4; ++h) v[h] = widen(T(), code[h], exp[h]);
+            if (at.n >= kXRing) ok = wait_phase(b, b.x_empty[s], uint32_t(at.n / kXRing - 1) & 1);
+            if (!__all_sync(kFull, ok)) break;
+#pragma unroll
+            for (int h = 0; h < 4; ++h) *reinterpret_cast<uint4 *>(stage + h * 1024) = v[h];
+#pragma unroll
+            for (int h = 4; h < 8; ++h)
+                *reinterpret_cast<uint4 *>(stage + h * 1024) = widen(T(), code[h], exp[h]);
+            if (!a.tma || at.i >= at.it.full) {
+                // the step's dy too: its slots' last products are done, since
+                // those of the step that x_empty was waited for are
+                for (int nb = 0; nb < at.it.blocks; ++nb) {
+                    const int u = at.u + nb, n_half = block_outs(a, at.it, nb) / 2;
+                    if (u >= kDyRing) ok = wait_phase(b, b.dy_empty[u % kDyRing], uint32_t(u / kDyRing - 1) & 1) && ok;
+                    stage_dy<T>(a, at.it.lo + int64_t(at.i) * kK, at.it.hi,
+                                at.it.o0 + nb * kTileO + int64_t(rank) * n_half, n_half,
+                                dy_ring + (u % kDyRing) * kStage);
+                }
+                if (!__all_sync(kFull, ok)) break;
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) arrive_remote(leader_address(smem_of(&b.x_full[s])));
+            more = advance(kGroups);
+            if (more) load_tokens(), load_codes();
+        }
     }
     __syncthreads();
     if (b.failed && threadIdx.x == 0) {  // copies still in flight get as long again
@@ -530,16 +598,16 @@ __global__ void __launch_bounds__(kWgradThreads, 2) __cluster_dims__(2, 1, 1)
 
 // The split tiles' parts, added in the order of the rows and written.
 // blockIdx.x: tile, blockIdx.y: 16 of its outputs; a thread: one column.
-template <typename G>
+template <typename G, int NB>
 __global__ void __launch_bounds__(kTileC) dopt_ckpt_wgrad_join_kernel(const __grid_constant__ WgradArgs a) {
     let_dependents_start();
     wait_for_grids_before();
-    const WgradItem it = item_of(a, a.whole + int(blockIdx.x) * a.split);
+    const WgradItem it = item_of<NB>(a, a.whole + int(blockIdx.x) * a.split);
     const int o = int(blockIdx.y) * 16;
-    if (o >= it.n) return;
+    if (it.o0 + o >= a.outs) return;
     float f[16] = {};
     for (int s = 0; s < a.split; ++s) {
-        const float *p = a.partial + (it.slot + s) * (kSlotBytes / 4) + int64_t(o) * kTileC + threadIdx.x;
+        const float *p = a.partial + (it.slot + s) * slot_floats(NB) + int64_t(o) * kTileC + threadIdx.x;
         float v[16];
 #pragma unroll
         for (int q = 0; q < 16; ++q) v[q] = __ldcs(p + q * kTileC);
@@ -553,35 +621,40 @@ __global__ void __launch_bounds__(kTileC) dopt_ckpt_wgrad_join_kernel(const __gr
 // Host side
 // ---------------------------------------------------------------------------
 
-// How the tiles go over `pairs` pairs of SMs.  Whole waves of tiles are done
-// tile by tile; the last, partial wave's tiles are split along the rows into
-// the number of parts whose estimated time is least, in steps of 64 rows: a
-// wave of parts is steps / parts, the join's launch takes about as long as 11
-// steps and a part's trip through memory 0.2.
-struct Split {
+// How the work goes over `pairs` pairs of SMs: tiles of nb * 256 outputs,
+// whole waves of them tile by tile and the last, partial wave's tiles split
+// along the rows into parts.  Chosen for the least estimated time, in units
+// of one product of 64 rows: a step of nb products takes as long as 1.25 or
+// 2.1 of them (the codes are widened under one or under two products), the
+// stores of a tile 10 a block, waited for with nb = 2 and after the last
+// tile, the join's launch 12 and a part's trip through memory 0.2 a block.
+struct Plan {
+    int nb, parts;
     int64_t whole, tail;
-    int parts;
 };
-Split plan_split(int64_t tiles, int64_t steps, int64_t pairs, int64_t workspace_bytes) {
-    Split best{tiles, 0, 1};
-    const int64_t tail = tiles % pairs;
-    if (tail == 0) return best;
-    double least = double(steps);
-    for (int s = 2; s <= kMaxSplit && steps / s >= 4; ++s) {
-        if (tail * s * kSlotBytes > workspace_bytes) break;
-        const double t = double((tail * s + pairs - 1) / pairs) * double(steps) / s + 11.0 + 0.2 * double(tail * s);
-        if (t < least) {
-            least = t;
-            best = Split{tiles - tail, tail, s};
+Plan plan_wgrad(int64_t outs, int64_t cols, int n_groups, int64_t dy_rows, int64_t pairs, int64_t workspace_bytes) {
+    const double steps = double(dy_rows / n_groups + kK - 1) / kK;
+    Plan best{};
+    double least = -1;
+    for (int nb = 1; nb <= 2; ++nb) {
+        const int64_t tiles = (outs + kTileO * nb - 1) / (kTileO * nb) * ((cols + kTileC - 1) / kTileC) * n_groups;
+        const int64_t tail = tiles % pairs;
+        const double step = nb == 1 ? 1.25 : 2.1, stores = 10.0 * nb;
+        const double each = steps * step + (nb == 2 ? stores : 0.0);
+        const double waves = double(tiles / pairs) * each + (nb == 1 ? stores : 0.0);
+        for (int parts = 1; parts <= kMaxSplit; ++parts) {
+            if (parts > 1 && (tail == 0 || steps / parts < 4 || tail * parts * slot_floats(nb) * 4 > workspace_bytes))
+                break;
+            double t = waves + double((tail * parts + pairs - 1) / pairs) * (each - steps * step + steps * step / parts);
+            if (parts > 1) t += 12.0 + 0.2 * nb * double(tail * parts);
+            if (least < 0 || t < least) {
+                least = t;
+                best = parts > 1 ? Plan{nb, parts, tiles - tail, tail} : Plan{nb, 1, tiles, 0};
+            }
         }
     }
     return best;
 }
-
-int64_t tiles_of(int64_t outs, int64_t cols, int n_groups) {
-    return (outs + kTileO - 1) / kTileO * ((cols + kTileC - 1) / kTileC) * n_groups;
-}
-int64_t steps_of(int64_t dy_rows, int n_groups) { return (dy_rows / n_groups + kK - 1) / kK; }
 
 using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
@@ -590,6 +663,10 @@ using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t,
 std::mutex g_wgrad_mutex;
 EncodeTiled g_encode = nullptr;
 int g_pairs[64] = {};  // pairs of SMs of a device, once its kernels are set up
+
+cudaError_t allow_smem(void (*kernel)(WgradArgs)) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kWgradSmem));
+}
 
 // The tensor-map encoder, the kernels' shared-memory limit and the device's
 // number of SM pairs, looked up once per device.
@@ -611,11 +688,10 @@ int set_up(const char *who, EncodeTiled *encode, int *pairs) {
         int sms = 0;
         e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device);
         if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(dopt_ckpt_wgrad_kernel<__nv_bfloat16>,
-                                     cudaFuncAttributeMaxDynamicSharedMemorySize, int(kWgradSmem));
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(dopt_ckpt_wgrad_kernel<__half>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     int(kWgradSmem));
+            e = allow_smem(dopt_ckpt_wgrad_kernel<__nv_bfloat16, 1>);
+        if (e == cudaSuccess) e = allow_smem(dopt_ckpt_wgrad_kernel<__nv_bfloat16, 2>);
+        if (e == cudaSuccess) e = allow_smem(dopt_ckpt_wgrad_kernel<__half, 1>);
+        if (e == cudaSuccess) e = allow_smem(dopt_ckpt_wgrad_kernel<__half, 2>);
         if (e == cudaSuccess) g_pairs[device] = std::max(1, sms / 2);
     }
     if (e != cudaSuccess) {
@@ -627,16 +703,18 @@ int set_up(const char *who, EncodeTiled *encode, int *pairs) {
     return DOPT_OK;
 }
 
-template <typename T>
-int launch_wgrad(const char *who, const WgradArgs &a, int64_t items, int64_t tail, cudaStream_t stream) {
-    int rc = launch_op(who, dopt_ckpt_wgrad_kernel<T>, dim3(unsigned(2 * items)), dim3(kWgradThreads), kWgradSmem,
-                       stream, a);
+template <typename T, int NB>
+int launch_wgrad(const char *who, const WgradArgs &a, int64_t pairs, int64_t tail, cudaStream_t stream) {
+    int rc = launch_op(who, dopt_ckpt_wgrad_kernel<T, NB>, dim3(unsigned(2 * std::min<int64_t>(a.items, pairs))),
+                       dim3(kWgradThreads), kWgradSmem, stream, a);
     if (rc != DOPT_OK || a.split == 1) return rc;
-    const dim3 grid(unsigned(tail), kTileO / 16);
+    const dim3 grid(unsigned(tail), kTileO * NB / 16);
     switch (a.grad_dtype) {
-        case DOPT_BF16: return launch_op(who, dopt_ckpt_wgrad_join_kernel<__nv_bfloat16>, grid, dim3(kTileC), 0, stream, a);
-        case DOPT_FP16: return launch_op(who, dopt_ckpt_wgrad_join_kernel<__half>, grid, dim3(kTileC), 0, stream, a);
-        default: return launch_op(who, dopt_ckpt_wgrad_join_kernel<float>, grid, dim3(kTileC), 0, stream, a);
+        case DOPT_BF16:
+            return launch_op(who, dopt_ckpt_wgrad_join_kernel<__nv_bfloat16, NB>, grid, dim3(kTileC), 0, stream, a);
+        case DOPT_FP16:
+            return launch_op(who, dopt_ckpt_wgrad_join_kernel<__half, NB>, grid, dim3(kTileC), 0, stream, a);
+        default: return launch_op(who, dopt_ckpt_wgrad_join_kernel<float, NB>, grid, dim3(kTileC), 0, stream, a);
     }
 }
 
@@ -736,17 +814,20 @@ extern "C" int dopt_ckpt_wgrad(const void *ckpt, dopt_dtype ckpt_dtype, int64_t 
                                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
         a.tma = r == CUDA_SUCCESS;  // a stride past the map's limit: plain loads
     }
-    const int64_t tiles = tiles_of(outs, cols, n_groups);
-    const Split split = plan_split(tiles, steps_of(dy_rows, n_groups), pairs, workspace_bytes);
-    const int64_t items = split.whole + split.tail * split.parts;
-    if (items > INT32_MAX / 2) return fail(DOPT_E_ARG, "%s: %lld tiles", who, static_cast<long long>(tiles));
+    const Plan plan = plan_wgrad(outs, cols, n_groups, dy_rows, pairs, workspace_bytes);
+    const int64_t items = plan.whole + plan.tail * plan.parts;
+    if (items > INT32_MAX / 2) return fail(DOPT_E_ARG, "%s: %lld tiles", who, static_cast<long long>(items));
     a.tiles_c = int32_t((cols + kTileC - 1) / kTileC);
-    a.tiles_o = int32_t((outs + kTileO - 1) / kTileO);
-    a.whole = int32_t(split.whole);
-    a.split = split.parts;
+    a.tiles_o = int32_t((outs + kTileO * plan.nb - 1) / (kTileO * plan.nb));
+    a.items = int32_t(items);
+    a.whole = int32_t(plan.whole);
+    a.split = plan.parts;
     a.partial = static_cast<float *>(workspace);
-    if (dy_dtype == DOPT_BF16) return launch_wgrad<__nv_bfloat16>(who, a, items, split.tail, stream);
-    return launch_wgrad<__half>(who, a, items, split.tail, stream);
+    if (dy_dtype == DOPT_BF16)
+        return plan.nb == 1 ? launch_wgrad<__nv_bfloat16, 1>(who, a, pairs, plan.tail, stream)
+                            : launch_wgrad<__nv_bfloat16, 2>(who, a, pairs, plan.tail, stream);
+    return plan.nb == 1 ? launch_wgrad<__half, 1>(who, a, pairs, plan.tail, stream)
+                        : launch_wgrad<__half, 2>(who, a, pairs, plan.tail, stream);
 }
 
 extern "C" int dopt_ckpt_wgrad_workspace(int64_t dy_rows, int64_t outs, int64_t cols,
@@ -760,8 +841,8 @@ extern "C" int dopt_ckpt_wgrad_workspace(int64_t dy_rows, int64_t outs, int64_t 
                           static_cast<long long>(dy_rows), static_cast<long long>(outs),
                           static_cast<long long>(cols), n_groups);
     // for a device of 76 pairs of SMs; a call takes what it is given
-    const Split split = plan_split(tiles_of(outs, cols, n_groups), steps_of(dy_rows, n_groups), 76, INT64_MAX);
-    *bytes = split.parts > 1 ? split.tail * split.parts * kSlotBytes : 0;
+    const Plan plan = plan_wgrad(outs, cols, n_groups, dy_rows, 76, INT64_MAX);
+    *bytes = plan.tail * plan.parts * slot_floats(plan.nb) * int64_t(sizeof(float));
     return DOPT_OK;
 }
 
