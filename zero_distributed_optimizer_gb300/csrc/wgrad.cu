@@ -269,24 +269,67 @@ __device__ __forceinline__ void stage_dy(const WgradArgs &a, int64_t r0, int64_t
     }
 }
 
-// 16 outputs' sums of one column to the grads.
+// 16 outputs' sums of one column to the grads; `all`: the 16 are all outputs.
 template <typename G>
 __device__ __forceinline__ void store_sums(const WgradArgs &a, const WgradItem &it, int64_t c, int64_t o,
-                                           const float (&f)[16]) {
+                                           const float (&f)[16], bool all) {
     if (c >= a.cols) return;
     G *p = static_cast<G *>(a.grad) + a.grad_offset[it.group] + o * a.cols + c;
+    const int n = all ? 16 : int(min(int64_t(16), a.outs - o));
     if (a.accumulate) {
         G old[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j)
-            if (o + j < a.outs) old[j] = p[j * a.cols];
+            if (j < n) old[j] = p[j * a.cols];
 #pragma unroll
         for (int j = 0; j < 16; ++j)
-            if (o + j < a.outs) p[j * a.cols] = from_f32<G>(to_f32(old[j]) + f[j]);
+            if (j < n) p[j * a.cols] = from_f32<G>(to_f32(old[j]) + f[j]);
+    } else if (all) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j, p += a.cols) *p = from_f32<G>(f[j]);
     } else {
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-            if (o + j < a.outs) p[j * a.cols] = from_f32<G>(f[j]);
+        for (int j = 0; j < 16; ++j, p += a.cols)
+            if (j < n) *p = from_f32<G>(f[j]);
+    }
+}
+
+// 32 lanes x 16 columns of tensor memory, in flight until wait_sums.
+__device__ __forceinline__ void load_sums(uint32_t at, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(at));
+}
+__device__ __forceinline__ void wait_sums(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+}
+
+// A tile's sums of a warp's 32 columns, at `sums` in tensor memory, to the grads.
+template <typename G>
+__device__ __forceinline__ void store_tile(const WgradArgs &a, const WgradItem &it, int64_t c, int outs, uint32_t sums) {
+    for (int o = 0; o < outs; o += 32) {  // (outs is a multiple of 32)
+        uint32_t r[2][16] = {};
+        if (it.steps > 0) {
+            load_sums(sums + uint32_t(o), r[0]);
+            load_sums(sums + uint32_t(o + 16), r[1]);
+            wait_sums(r[0]);
+            wait_sums(r[1]);
+        }
+        const bool all = it.o0 + o + 32 <= a.outs;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float f[16];
+#pragma unroll
+            for (int q = 0; q < 16; ++q) f[q] = __uint_as_float(r[h][q]);
+            store_sums<G>(a, it, c, it.o0 + o + 16 * h, f, all);
+        }
     }
 }
 
@@ -457,32 +500,21 @@ __global__ void __launch_bounds__(kWgradThreads, 1) __cluster_dims__(2, 1, 1)
             }
             const int64_t c = it.c0 + column_of(m);
             const int outs = (it.blocks - 1) * kTileO + block_outs(a, it, it.blocks - 1);
-            for (int o = 0; o < outs; o += 16) {
-                float f[16] = {};
-                if (it.steps > 0) {
-                    uint32_t r[16];
-                    asm volatile(
-                        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-                        "%12, %13, %14, %15}, [%16];"
-                        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-                          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-                          "=r"(r[14]), "=r"(r[15])
-                        : "r"(lanes + uint32_t(buffer * kTileO + o)));
-                    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+            const uint32_t sums = lanes + uint32_t(buffer * kTileO);
+            if (it.slot >= 0) {
+                float *p = a.partial + it.slot * slot_floats(NB) + m;
+                for (int o = 0; o < outs; o += 16) {
+                    uint32_t r[16] = {};
+                    if (it.steps > 0) load_sums(sums + uint32_t(o), r), wait_sums(r);
 #pragma unroll
-                    for (int q = 0; q < 16; ++q) f[q] = __uint_as_float(r[q]);
+                    for (int q = 0; q < 16; ++q, p += kTileC) *p = __uint_as_float(r[q]);
                 }
-                if (it.slot >= 0) {
-                    float *p = a.partial + it.slot * slot_floats(NB) + int64_t(o) * kTileC + m;
-#pragma unroll
-                    for (int q = 0; q < 16; ++q) p[q * kTileC] = f[q];
-                } else if (a.grad_dtype == DOPT_FP32) {
-                    store_sums<float>(a, it, c, it.o0 + o, f);
-                } else if (a.grad_dtype == DOPT_BF16) {
-                    store_sums<__nv_bfloat16>(a, it, c, it.o0 + o, f);
-                } else {
-                    store_sums<__half>(a, it, c, it.o0 + o, f);
-                }
+            } else if (a.grad_dtype == DOPT_FP32) {
+                store_tile<float>(a, it, c, outs, sums);
+            } else if (a.grad_dtype == DOPT_BF16) {
+                store_tile<__nv_bfloat16>(a, it, c, outs, sums);
+            } else {
+                store_tile<__half>(a, it, c, outs, sums);
             }
             if (it.steps > 0) {
                 asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -614,7 +646,7 @@ __global__ void __launch_bounds__(kTileC) dopt_ckpt_wgrad_join_kernel(const __gr
 #pragma unroll
         for (int q = 0; q < 16; ++q) f[q] += v[q];
     }
-    store_sums<G>(a, it, it.c0 + column_of(threadIdx.x), it.o0 + o, f);
+    store_sums<G>(a, it, it.c0 + column_of(threadIdx.x), it.o0 + o, f, false);
 }
 
 // ---------------------------------------------------------------------------
