@@ -55,7 +55,14 @@ struct WgradBarriers {
     uint32_t tmem;
     int32_t failed;
 };
-constexpr size_t kWgradSmem = (kDyRing + kXRing) * size_t(kStage) + sizeof(WgradBarriers);
+// The groups' first rows and, with several groups, the groups from the one
+// with the most rows down.
+struct WgradGroups {
+    int32_t first[DOPT_MAX_GROUPS + 1];
+    int32_t order[DOPT_MAX_GROUPS];
+};
+constexpr size_t kWgradSmem =
+    (kDyRing + kXRing) * size_t(kStage) + sizeof(WgradBarriers) + sizeof(WgradGroups);
 static_assert(kWgradSmem <= 232448, "a CTA's 227 KB");
 
 __host__ __device__ constexpr int64_t slot_floats(int nb) { return int64_t(kTileC) * kTileO * nb; }
@@ -68,8 +75,8 @@ struct WgradArgs {
     const int32_t *offsets;    // or NULL: one group of all rows
     void *grad;
     float *partial;            // fp32 sums of the split tiles, [slot][o][c]
-    int64_t x_rows, cols, pitch;
-    int64_t dy_rows, outs, dy_ld;
+    int64_t cols, pitch, dy_ld;
+    int32_t x_rows, dy_rows, outs, groups;
     int32_t tiles_c, tiles_o;
     int32_t items;             // tiles and parts of tiles
     int32_t whole;             // tiles before the split ones
@@ -195,15 +202,25 @@ __device__ __forceinline__ uint4 widen(__half, const uint2 &w, uint32_t byte) {
 
 // A tile, or a part of one.
 struct WgradItem {
-    int64_t lo, hi;       // rows
-    int64_t c0, o0;
+    int32_t lo, rows;     // rows of dy
+    int32_t c0, o0;
     int32_t group, slot;  // slot < 0: the whole sum, written to the grads
     int32_t steps, full;  // of 64 rows, and those that are full
     int32_t blocks;       // products of up to 256 outputs
 };
 
+// The item that pair p of `pairs` takes in round k: the rounds' order turns
+// back and forth, which, with the groups in order of falling length, gives
+// the pairs nearly equal shares (1.07 times the mean for 64 experts of 30 to
+// 3000 rows, where rounds in one order gave 1.33).  Negative: none is left.
+__device__ __forceinline__ int item_number(const WgradArgs &a, int k) {
+    const int pairs = int(gridDim.x >> 1), p = int(blockIdx.x >> 1);
+    const int item = k * pairs + (k & 1 ? pairs - 1 - p : p);
+    return item < a.items ? item : -1;
+}
+
 template <int NB>
-__device__ __forceinline__ WgradItem item_of(const WgradArgs &a, int item) {
+__device__ __forceinline__ WgradItem item_of(const WgradArgs &a, const WgradGroups &g, int item) {
     WgradItem it;
     int tile = item, part = 0, parts = 1;
     it.slot = -1;
@@ -214,47 +231,59 @@ __device__ __forceinline__ WgradItem item_of(const WgradArgs &a, int item) {
         if (parts > 1) it.slot = item - a.whole;
     }
     const int per_group = a.tiles_c * a.tiles_o;
-    it.group = tile / per_group;
+    it.group = g.order[tile / per_group];
     tile %= per_group;
-    it.c0 = int64_t(tile % a.tiles_c) * kTileC;
-    it.o0 = int64_t(tile / a.tiles_c) * (kTileO * NB);
+    it.c0 = tile % a.tiles_c * kTileC;
+    it.o0 = tile / a.tiles_c * (kTileO * NB);
     it.blocks = a.outs - it.o0 > kTileO ? NB : 1;
-    it.lo = 0;
-    it.hi = a.dy_rows;
-    if (a.offsets) {
-        it.lo = min(max(int64_t(a.offsets[it.group]), int64_t(0)), a.dy_rows);
-        it.hi = min(max(int64_t(a.offsets[it.group + 1]), it.lo), a.dy_rows);
-    }
+    it.lo = g.first[it.group];
+    it.rows = max(0, g.first[it.group + 1] - it.lo);
     if (parts > 1) {
-        const int64_t steps = (it.hi - it.lo + kK - 1) / kK;
-        const int64_t end = it.hi;
-        it.hi = min(end, it.lo + steps * (part + 1) / parts * kK);
-        it.lo = min(end, it.lo + steps * part / parts * kK);
+        const int steps = (it.rows + kK - 1) / kK;
+        const int from = int(int64_t(steps) * part / parts * kK), to = int(int64_t(steps) * (part + 1) / parts * kK);
+        it.lo += from;
+        it.rows = min(it.rows, to) - from;
     }
-    it.steps = int(it.hi - it.lo + kK - 1) / kK;
-    it.full = int(it.hi - it.lo) / kK;
+    it.steps = (it.rows + kK - 1) / kK;
+    it.full = it.rows / kK;
     return it;
+}
+
+// The groups' tables, by all threads of the CTA.
+__device__ __forceinline__ void fill_groups(const WgradArgs &a, WgradGroups &g) {
+    for (int e = threadIdx.x; e <= a.groups; e += blockDim.x)
+        g.first[e] = a.offsets ? min(max(a.offsets[e], 0), a.dy_rows) : e * a.dy_rows;
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.groups; e += blockDim.x) {
+        const int rows = g.first[e + 1] - g.first[e];
+        int rank = 0;
+        for (int o = 0; o < a.groups; ++o) {
+            const int other = g.first[o + 1] - g.first[o];
+            rank += other > rows || (other == rows && o < e);
+        }
+        g.order[rank] = e;
+    }
 }
 
 // Outputs of a tile's product nb: a multiple of 32.
 __device__ __forceinline__ int block_outs(const WgradArgs &a, const WgradItem &it, int nb) {
-    return int(min(int64_t(kTileO), (a.outs - it.o0 - nb * kTileO + 31) / 32 * 32));
+    return min(kTileO, (a.outs - it.o0 - nb * kTileO + 31) / 32 * 32);
 }
 
 // A CTA's half of 64 rows of dy by plain loads, zeros past the rows and
 // columns there are.
 template <typename T>
-__device__ __forceinline__ void stage_dy(const WgradArgs &a, int64_t r0, int64_t hi, int64_t o0, int n_half,
+__device__ __forceinline__ void stage_dy(const WgradArgs &a, int r0, int rows, int o0, int n_half,
                                          unsigned char *stage) {
     const T *dy = static_cast<const T *>(a.dy);
     const int chunks = (n_half + 7) / 8;
     for (int i = threadIdx.x % kGroup; i < kK * 16; i += kGroup) {
         const int k = i >> 4, q = i & 15;
         if (q >= chunks) continue;
-        const int64_t r = r0 + k, o = o0 + q * 8;
+        const int o = o0 + q * 8;
         uint4 raw = make_uint4(0, 0, 0, 0);
-        if (r < hi && o < a.outs) {
-            const T *p = dy + r * a.dy_ld + o;
+        if (k < rows && o < a.outs) {
+            const T *p = dy + (r0 + k) * a.dy_ld + o;
             if (a.vec && o + 8 <= a.outs) {
                 raw = *reinterpret_cast<const uint4 *>(p);
             } else {
@@ -271,11 +300,11 @@ __device__ __forceinline__ void stage_dy(const WgradArgs &a, int64_t r0, int64_t
 
 // 16 outputs' sums of one column to the grads; `all`: the 16 are all outputs.
 template <typename G>
-__device__ __forceinline__ void store_sums(const WgradArgs &a, const WgradItem &it, int64_t c, int64_t o,
+__device__ __forceinline__ void store_sums(const WgradArgs &a, const WgradItem &it, int c, int o,
                                            const float (&f)[16], bool all) {
     if (c >= a.cols) return;
     G *p = static_cast<G *>(a.grad) + a.grad_offset[it.group] + o * a.cols + c;
-    const int n = all ? 16 : int(min(int64_t(16), a.outs - o));
+    const int n = all ? 16 : min(16, a.outs - o);
     if (a.accumulate) {
         G old[16];
 #pragma unroll
@@ -313,7 +342,7 @@ __device__ __forceinline__ void wait_sums(uint32_t (&r)[16]) {
 
 // A tile's sums of a warp's 32 columns, at `sums` in tensor memory, to the grads.
 template <typename G>
-__device__ __forceinline__ void store_tile(const WgradArgs &a, const WgradItem &it, int64_t c, int outs, uint32_t sums) {
+__device__ __forceinline__ void store_tile(const WgradArgs &a, const WgradItem &it, int c, int outs, uint32_t sums) {
     for (int o = 0; o < outs; o += 32) {  // (outs is a multiple of 32)
         uint32_t r[2][16] = {};
         if (it.steps > 0) {
@@ -339,10 +368,10 @@ __global__ void __launch_bounds__(kWgradThreads, 1) __cluster_dims__(2, 1, 1)
     extern __shared__ __align__(1024) unsigned char smem[];
     unsigned char *dy_ring = smem, *x_ring = smem + kDyRing * kStage;
     WgradBarriers &b = *reinterpret_cast<WgradBarriers *>(x_ring + kXRing * kStage);
+    WgradGroups &groups = *reinterpret_cast<WgradGroups *>(&b + 1);
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     uint32_t rank;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-    const int first = int(blockIdx.x >> 1), stride = int(gridDim.x >> 1);
 
     let_dependents_start();
     if (threadIdx.x == 0) {
@@ -363,6 +392,7 @@ __global__ void __launch_bounds__(kWgradThreads, 1) __cluster_dims__(2, 1, 1)
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     }
     wait_for_grids_before();
+    fill_groups(a, groups);
     __syncthreads();
     cluster_sync();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -374,12 +404,12 @@ __global__ void __launch_bounds__(kWgradThreads, 1) __cluster_dims__(2, 1, 1)
         // dy, by TMA into both CTAs, counted on the leader's barriers
         int n = 0, u = 0;
         bool ok = true;
-        for (int item = first; item < a.items && ok; item += stride) {
-            const WgradItem it = item_of<NB>(a, item);
+        for (int k = 0, item; ok && (item = item_number(a, k)) >= 0; ++k) {
+            const WgradItem it = item_of<NB>(a, groups, item);
             const int steps = uniform(it.steps), full_steps = a.tma ? uniform(it.full) : 0;
             const int blocks = it.blocks;  // (of the item's number alone)
             const int outs[2] = {block_outs(a, it, 0), blocks > 1 ? block_outs(a, it, 1) : 0};
-            int row = uniform(int(it.lo));
+            int row = uniform(it.lo);
             for (int i = 0; i < steps && ok; ++i, ++n, row += kK) {
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb) {
@@ -399,7 +429,7 @@ __global__ void __launch_bounds__(kWgradThreads, 1) __cluster_dims__(2, 1, 1)
                             asm volatile(
                                 "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::"
                                 "bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_of(dy_ring + s * kStage + x * kSlab)),
-                                "l"(&a.dy_map), "r"(int(it.o0) + nb * kTileO + int(rank) * (outs[nb] / 2) + 64 * x),
+                                "l"(&a.dy_map), "r"(it.o0 + nb * kTileO + int(rank) * (outs[nb] / 2) + 64 * x),
                                 "r"(row), "r"(leader_address(full))
                                 : "memory");
                     }
@@ -438,10 +468,10 @@ __global__ void __launch_bounds__(kWgradThreads, 1) __cluster_dims__(2, 1, 1)
             const uint64_t x0 = slab_descriptor(smem_of(x_ring)), dy0 = slab_descriptor(smem_of(dy_ring));
             int n = 0, u = 0, t = 0;
             bool ok = true;
-            for (int item = first; item < a.items && ok; item += stride) {
-                const WgradItem it = item_of<NB>(a, item);
+            for (int round = 0, item; ok && (item = item_number(a, round)) >= 0; ++round) {
+                const WgradItem it = item_of<NB>(a, groups, item);
                 const int steps = uniform(it.steps), full_steps = uniform(it.full);
-                const int rest = (uniform(int(it.hi - it.lo)) - full_steps * kK + 15) / 16;  // products of the last step
+                const int rest = (uniform(it.rows) - full_steps * kK + 15) / 16;  // products of the last step
                 if (steps == 0) continue;
                 const int blocks = it.blocks;
                 const uint32_t idesc[2] = {kInstruction | (uint32_t(block_outs(a, it, 0) >> 3) << 17),
@@ -490,15 +520,15 @@ __global__ void __launch_bounds__(kWgradThreads, 1) __cluster_dims__(2, 1, 1)
         const uint32_t lanes = tmem + (uint32_t((warp & 3) * 32) << 16);
         int t = 0;
         bool ok = true;
-        for (int item = first; item < a.items && ok; item += stride) {
-            const WgradItem it = item_of<NB>(a, item);
+        for (int k = 0, item; ok && (item = item_number(a, k)) >= 0; ++k) {
+            const WgradItem it = item_of<NB>(a, groups, item);
             const int buffer = NB == 1 ? t & 1 : 0, use = NB == 1 ? t >> 1 : t;
             if (it.steps > 0) {
                 ok = wait_phase(b, b.sum_full[buffer], uint32_t(use) & 1);
                 if (!__all_sync(kFull, ok)) break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             }
-            const int64_t c = it.c0 + column_of(m);
+            const int c = it.c0 + column_of(m);
             const int outs = (it.blocks - 1) * kTileO + block_outs(a, it, it.blocks - 1);
             const uint32_t sums = lanes + uint32_t(buffer * kTileO);
             if (it.slot >= 0) {
@@ -530,10 +560,9 @@ __global__ void __launch_bounds__(kWgradThreads, 1) __cluster_dims__(2, 1, 1)
         const int w = warp & 3, q = lane & 15;
         struct {
             WgradItem it;
-            int item, i, n, u;  // the item, the step in it; the step and block of dy of all
+            int k, i, n, u;  // the round, the step in its item; the step and block of dy of all
         } at;
-        at.item = first;
-        at.i = at.n = at.u = 0;
+        at.k = at.i = at.n = at.u = 0;
         // on by so many steps, over items; false past the last
         auto advance = [&](int by) -> bool {
             at.i += by;
@@ -542,40 +571,44 @@ __global__ void __launch_bounds__(kWgradThreads, 1) __cluster_dims__(2, 1, 1)
             while (at.i >= at.it.steps) {
                 at.u -= (at.i - at.it.steps) * at.it.blocks;
                 at.i -= at.it.steps;
-                at.item += stride;
-                if (at.item >= a.items) return false;
-                at.it = item_of<NB>(a, at.item);
+                const int item = item_number(a, ++at.k);
+                if (item < 0) return false;
+                at.it = item_of<NB>(a, groups, item);
                 at.u += at.i * at.it.blocks;
             }
             return true;
         };
         uint2 code[8];
         uint32_t exp[8];
-        int tokens = -1;
+        constexpr int kNone = INT32_MIN;  // the token of a row that counts as zeros
+        int tokens = kNone;
         // the token of row 2 w + (l & 1) + 8 (l / 2) of the step, in lane l
         auto load_tokens = [&]() {
-            const int64_t r = at.it.lo + int64_t(at.i) * kK + 2 * w + (lane & 1) + 4 * (lane & 14);
-            tokens = -1;
-            if (r < at.it.hi && lane < 16) tokens = a.row_token ? a.row_token[r] : int(r);
+            const int r = at.i * kK + 2 * w + (lane & 1) + 4 * (lane & 14);
+            tokens = kNone;
+            if (r < at.it.rows && lane < 16) tokens = a.row_token ? a.row_token[at.it.lo + r] : at.it.lo + r;
         };
+        const uint32_t pitch = uint32_t(a.pitch);
         auto load_codes = [&]() {
-            const int64_t c = at.it.c0 + int64_t(rank) * (kTileC / 2);
-            const bool any = c < a.pitch && a.x_rows > 0;
-            const unsigned char *codes = a.codes + c + q * 8, *scales = a.scales + c / kBlock + (q >> 2);
-            const uint32_t pitch = uint32_t(a.pitch);
+            const int c = at.it.c0 + int(rank) * (kTileC / 2);
+            if (c >= a.pitch || a.x_rows <= 0) {  // no such columns, or no rows: zeros
 #pragma unroll
-            for (int h = 0; h < 8; ++h) {
-                const int t = __shfl_sync(kFull, tokens, 2 * h + (lane >> 4));
-                code[h] = make_uint2(0, 0);
-                exp[h] = 0;  // counts as zeros
-                if (any && t >= 0 && t < a.x_rows) {
-                    code[h] = __ldg(reinterpret_cast<const uint2 *>(codes + uint64_t(uint32_t(t)) * pitch));
-                    exp[h] = __ldg(scales + uint64_t(uint32_t(t)) * (pitch / kBlock));
-                }
+                for (int h = 0; h < 8; ++h) code[h] = make_uint2(0, 0), exp[h] = 0;
+                return;
+            }
+            const unsigned char *codes = a.codes + (c + q * 8), *scales = a.scales + (c / kBlock + (q >> 2));
+            const int mine = uint32_t(tokens) < uint32_t(a.x_rows) ? tokens : kNone;
+#pragma unroll
+            for (int h = 0; h < 8; ++h) {  // (a row that counts as zeros reads row 0 and exponent 0)
+                const int t = __shfl_sync(kFull, mine, 2 * h + (lane >> 4));
+                const uint32_t row = uint32_t(t) & 0x7fffffffu;
+                code[h] = __ldg(reinterpret_cast<const uint2 *>(codes + uint64_t(row) * pitch));
+                exp[h] = __ldg(scales + uint64_t(row) * (pitch / kBlock));
+                if (t < 0) exp[h] = 0;
             }
         };
-        at.it = item_of<NB>(a, min(first, a.items - 1));
-        bool more = first < a.items && advance(warp >> 2);
+        at.it = item_of<NB>(a, groups, item_number(a, 0));
+        bool more = advance(warp >> 2);
         if (more) load_tokens(), load_codes();
         // 8 rows on: 1024 bytes on, and the swizzle is the same
         unsigned char *my_stage = x_ring + stage_chunk(2 * w + (lane >> 4), q);
@@ -599,8 +632,8 @@ __global__ void __launch_bounds__(kWgradThreads, 1) __cluster_dims__(2, 1, 1)
                 for (int nb = 0; nb < at.it.blocks; ++nb) {
                     const int u = at.u + nb, n_half = block_outs(a, at.it, nb) / 2;
                     if (u >= kDyRing) ok = wait_phase(b, b.dy_empty[u % kDyRing], uint32_t(u / kDyRing - 1) & 1) && ok;
-                    stage_dy<T>(a, at.it.lo + int64_t(at.i) * kK, at.it.hi,
-                                at.it.o0 + nb * kTileO + int64_t(rank) * n_half, n_half,
+                    stage_dy<T>(a, at.it.lo + at.i * kK, at.it.rows - at.i * kK,
+                                at.it.o0 + nb * kTileO + int(rank) * n_half, n_half,
                                 dy_ring + (u % kDyRing) * kStage);
                 }
                 if (!__all_sync(kFull, ok)) break;
@@ -634,7 +667,10 @@ template <typename G, int NB>
 __global__ void __launch_bounds__(kTileC) dopt_ckpt_wgrad_join_kernel(const __grid_constant__ WgradArgs a) {
     let_dependents_start();
     wait_for_grids_before();
-    const WgradItem it = item_of<NB>(a, a.whole + int(blockIdx.x) * a.split);
+    __shared__ WgradGroups groups;
+    fill_groups(a, groups);
+    __syncthreads();
+    const WgradItem it = item_of<NB>(a, groups, a.whole + int(blockIdx.x) * a.split);
     const int o = int(blockIdx.y) * 16;
     if (it.o0 + o >= a.outs) return;
     float f[16] = {};
@@ -675,7 +711,8 @@ Plan plan_wgrad(int64_t outs, int64_t cols, int n_groups, int64_t dy_rows, int64
         const double each = steps * step + (nb == 2 ? stores : 0.0);
         const double waves = double(tiles / pairs) * each + (nb == 1 ? stores : 0.0);
         for (int parts = 1; parts <= kMaxSplit; ++parts) {
-            if (parts > 1 && (tail == 0 || steps / parts < 4 || tail * parts * slot_floats(nb) * 4 > workspace_bytes))
+            // (groups go from long to short: the tail's tiles are the shortest)
+            if (parts > 1 && (tail == 0 || (n_groups > 1 && tiles > pairs) || steps / parts < 4 || tail * parts * slot_floats(nb) * 4 > workspace_bytes))
                 break;
             double t = waves + double((tail * parts + pairs - 1) / pairs) * (each - steps * step + steps * step / parts);
             if (parts > 1) t += 12.0 + 0.2 * nb * double(tail * parts);
@@ -822,10 +859,11 @@ extern "C" int dopt_ckpt_wgrad(const void *ckpt, dopt_dtype ckpt_dtype, int64_t 
     a.dy = dy;
     a.offsets = offsets;
     a.grad = grad;
-    a.x_rows = x_rows;
+    a.x_rows = int32_t(x_rows);
     a.cols = cols;
-    a.dy_rows = dy_rows;
-    a.outs = outs;
+    a.dy_rows = int32_t(dy_rows);
+    a.outs = int32_t(outs);
+    a.groups = n_groups;
     a.dy_ld = dy_ld;
     a.accumulate = (flags & DOPT_WGRAD_ACCUMULATE) != 0;
     a.vec = aligned_to(dy, 16) && dy_ld * 2 % 16 == 0;
