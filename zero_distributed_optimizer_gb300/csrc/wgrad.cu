@@ -98,28 +98,36 @@ __device__ __forceinline__ uint32_t smem_of(const void *p) {
 
 // Wait for a phase of a barrier that threads of the cluster arrive on; false
 // once any wait of this CTA has run out of time.
-__device__ __forceinline__ bool wait_phase(WgradBarriers &b, unsigned long long &bar, uint32_t parity) {
-    const uint32_t at = smem_of(&bar);
-    unsigned long long t0 = 0;
+__device__ __forceinline__ bool try_phase(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+__device__ __noinline__ bool wait_long(WgradBarriers &b, uint32_t bar, uint32_t parity) {
+    unsigned long long t0, now;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
     for (;;) {
-        uint32_t done;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(done)
-            : "r"(at), "r"(parity), "r"(1000000u)  // sleeps up to 1 ms a try
-            : "memory");
-        if (done) return true;
+        for (int i = 0; i < 64; ++i)
+            if (try_phase(bar, parity)) return true;
         if (*static_cast<volatile int32_t *>(&b.failed)) return false;
-        unsigned long long now;
         asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
-        if (t0 == 0) t0 = now;
         if (now - t0 > kWaitNs) {
             if (atomicExch(&b.failed, 1) == 0) atomicAdd(&g_wgrad_timeouts, 1u);
             return false;
         }
     }
+}
+__device__ __forceinline__ bool wait_phase(WgradBarriers &b, unsigned long long &bar, uint32_t parity) {
+    const uint32_t at = smem_of(&bar);
+    for (int i = 0; i < 16; ++i)
+        if (try_phase(at, parity)) return true;
+    return wait_long(b, at, parity);
 }
 
 // Wait for the last of `uses` uses of each slot of a ring.
@@ -180,10 +188,9 @@ __device__ __forceinline__ uint4 widen(__nv_bfloat16, const uint2 &w, uint32_t b
     for (int i = 0; i < 4; ++i) {
         const uint32_t pair = (i < 2 ? w.x : w.y) >> (i & 1 ? 8 : 0);
         const uint32_t m = (pair & 0x007f007fu) | 0x43004300u, s = (pair & 0x00800080u) | 0x43004300u;
-        const __nv_bfloat162 q = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&m),
-                                         *reinterpret_cast<const __nv_bfloat162 *>(&s));
-        const __nv_bfloat162 v = __hmul2(q, *reinterpret_cast<const __nv_bfloat162 *>(&step));
-        o[i] = *reinterpret_cast<const uint32_t *>(&v);
+        uint32_t code;
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(code) : "r"(s), "r"(0xbf80bf80u), "r"(m));      // m - s
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(o[i]) : "r"(code), "r"(step), "r"(0x80008000u));  // times step
     }
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
