@@ -305,6 +305,16 @@ __device__ __forceinline__ void stage_dy(const WgradArgs &a, int r0, int rows, i
     }
 }
 
+// The 128 bytes of the first block of those rows that are this thread's, on
+// their way to L2 before stage_dy reads them.
+template <typename T>
+__device__ __forceinline__ void prefetch_dy(const WgradArgs &a, const WgradItem &it, int i, uint32_t rank) {
+    const int t = threadIdx.x % kGroup, k = i * kK + (t >> 1);
+    const int o = it.o0 + int(rank) * (block_outs(a, it, 0) / 2) + (t & 1) * 64;
+    if (k < it.rows && o < a.outs)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const T *>(a.dy) + (it.lo + k) * a.dy_ld + o));
+}
+
 // 16 outputs' sums of one column to the grads; `all`: the 16 are all outputs.
 template <typename G>
 __device__ __forceinline__ void store_sums(const WgradArgs &a, const WgradItem &it, int c, int o,
@@ -649,7 +659,11 @@ __global__ void __launch_bounds__(kWgradThreads, 1) __cluster_dims__(2, 1, 1)
             __syncwarp();
             if (lane == 0) arrive_remote(leader_address(smem_of(&b.x_full[s])));
             more = advance(kGroups);
-            if (more) load_tokens(), load_codes();
+            if (more) {
+                load_tokens();
+                if (!a.tma || at.i >= at.it.full) prefetch_dy<T>(a, at.it, at.i, rank);
+                load_codes();
+            }
         }
     }
     __syncthreads();
