@@ -2,15 +2,24 @@
 // (dopt_ckpt_load) and an activation function's backward pass from its kept
 // input (dopt_ckpt_act_grad).  dopt.h states the format.
 //
-// Every kernel gives a thread 16 columns of a row: half a block of 32, one
-// 16-byte load or store of codes, two (four for fp32) of values.  A thread
-// block covers bx threads' columns of `by` rows and strides over the rows,
-// so no index is divided.
+// Saving and reading back give a thread 32 bytes of a row's values (16 columns
+// of 16 bits, 8 of fp32), the activation gradients 8 columns: few enough
+// registers that the threads of an SM keep enough loads in flight for
+// memory's rate, enough columns that indexes cost little.  A thread block
+// covers bx threads' columns of 256 / bx rows and strides over
+// the rows, so no index is divided.
+//
+// Codes are always aligned (a row's pitch is a multiple of 128).  Rows of
+// values that are not 16-byte aligned are read and written in the aligned
+// 16-byte pieces around them all the same: the bx threads of a row hold
+// neighbouring pieces, take the part that is missing from their neighbour
+// and shift; only pieces that reach over the ends of the row (reading) or of
+// the threads' stretch of it (writing) go element by element.  (One element
+// at a time, 16384 x 5631 bf16 took 585 us to keep and read back.)
 #include "op_common.cuh"
 
 namespace {
 
-constexpr int kCols = 16;  // columns a thread takes
 constexpr int kCkptThreads = 256;
 
 struct CkptArgs {
@@ -19,160 +28,300 @@ struct CkptArgs {
     uint8_t *codes;       // [rows][pitch], the exponent bytes after them
     uint8_t *scales;      // [rows][pitch / 32]
     const int32_t *index; // load: row of each output row, or NULL
-    int64_t rows;         // rows of the checkpoint
-    int64_t n_out;        // rows the launch goes through
-    int64_t cols, pitch;
     int64_t ld, ld_out;
-    int64_t half;         // gated: columns of the output (cols / 2)
+    int32_t rows;         // rows of the checkpoint
+    int32_t n_out;        // rows the launch goes through
+    int32_t cols, pitch;
+    int32_t half;         // gated: columns of the output (cols / 2)
     int32_t min_exp;      // least exponent byte
     int32_t vec;          // rows are 16-byte aligned
 };
 
-// 16 values of a row from column c on; columns at or past `cols` are 0.
+// ---------------------------------------------------------------------------
+// 8 values of a row.  All threads of a warp call these together; `lane` is
+// the thread's place among the bx of its row, `here` whether the row exists.
+// ---------------------------------------------------------------------------
+
+// (hi, lo) a 16-byte piece and its successor, shifted down by `bytes` (0..15):
+// the 4 words from that byte on.
+__device__ __forceinline__ uint4 shift_down(const uint4 &lo, const uint4 &hi, uint32_t bytes) {
+    uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    if (bytes & 8) {
+#pragma unroll
+        for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+    }
+    if (bytes & 4) {
+#pragma unroll
+        for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+    }
+    const uint32_t bits = (bytes & 3) * 8;
+    return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
+                      __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
+}
+__device__ __forceinline__ uint4 shuffle_down(const uint4 &v, int width) {
+    return make_uint4(__shfl_down_sync(kFull, v.x, 1, width), __shfl_down_sync(kFull, v.y, 1, width),
+                      __shfl_down_sync(kFull, v.z, 1, width), __shfl_down_sync(kFull, v.w, 1, width));
+}
+__device__ __forceinline__ uint4 shuffle_up(const uint4 &v, int width) {
+    return make_uint4(__shfl_up_sync(kFull, v.x, 1, width), __shfl_up_sync(kFull, v.y, 1, width),
+                      __shfl_up_sync(kFull, v.z, 1, width), __shfl_up_sync(kFull, v.w, 1, width));
+}
+
+// The 16 bytes at elements [e, e + 16 / sizeof(T)) of a row of `cols`; those
+// before or past the row are not read (0).
 template <typename T>
-__device__ __forceinline__ void load_vals(const T *row, int64_t c, int64_t cols, bool vec,
-                                          float (&f)[kCols]) {
+__device__ __forceinline__ uint4 load_piece(const T *row, int e, int cols) {
     constexpr int N = 16 / int(sizeof(T));
-    if (vec && c + kCols <= cols) {
-        uint4 raw[kCols / N];
+    if (e >= 0 && e + N <= cols) return __ldcs(reinterpret_cast<const uint4 *>(row + e));
+    using E = typename Raw<int(sizeof(T))>::type;
+    E v[N];
 #pragma unroll
-        for (int i = 0; i < kCols / N; ++i) raw[i] = reinterpret_cast<const uint4 *>(row + c)[i];
+    for (int i = 0; i < N; ++i) v[i] = e + i >= 0 && e + i < cols ? reinterpret_cast<const E *>(row)[e + i] : E(0);
+    uint4 raw;
+    memcpy(&raw, v, sizeof raw);
+    return raw;
+}
+// The same to elements [e, ...) of which those in [from, to) are written.
+template <typename T>
+__device__ __forceinline__ void store_piece(T *row, int e, int from, int to, const uint4 &raw) {
+    constexpr int N = 16 / int(sizeof(T));
+    if (e >= from && e + N <= to) {
+        __stcs(reinterpret_cast<uint4 *>(row + e), raw);
+        return;
+    }
+    using E = typename Raw<int(sizeof(T))>::type;
+    E v[N];
+    memcpy(v, &raw, sizeof raw);
 #pragma unroll
-        for (int i = 0; i < kCols / N; ++i) {
-            float g[N];
+    for (int i = 0; i < N; ++i)
+        if (e + i >= from && e + i < to) reinterpret_cast<E *>(row)[e + i] = v[i];
+}
+
+template <typename T, int COLS>
+struct Values {
+    static constexpr int kPer = 16 / int(sizeof(T));  // elements a piece
+    static constexpr int kPieces = COLS / kPer;
+    uint4 raw[kPieces];
+
+    // Values from column c on; those at or past `cols` (0 where there is no row) are 0.
+    __device__ __forceinline__ void load(const T *row, int c, int cols, bool vec, int lane, int bx) {
+        if (vec) {
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) raw[i] = load_piece(row, c + i * kPer, cols);
+        } else {
+            const uint32_t off = uint32_t(reinterpret_cast<uintptr_t>(row + c) & 15);
+            const int e = c - int(off / sizeof(T));
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) raw[i] = load_piece(row, e + i * kPer, cols);
+            uint4 next = shuffle_down(raw[0], bx);
+            if (lane == bx - 1) next = load_piece(row, e + COLS, cols);
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) raw[i] = shift_down(raw[i], i + 1 < kPieces ? raw[i + 1] : next, off);
+        }
+    }
+
+    __device__ __forceinline__ void get(float (&f)[COLS]) const {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            float g[kPer];
             unpack<T, 16>(raw[i], g);
 #pragma unroll
-            for (int q = 0; q < N; ++q) f[i * N + q] = g[q];
+            for (int q = 0; q < kPer; ++q) f[i * kPer + q] = g[q];
         }
+    }
+    __device__ __forceinline__ void set(const float (&f)[COLS]) {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            float g[kPer];
+#pragma unroll
+            for (int q = 0; q < kPer; ++q) g[q] = f[i * kPer + q];
+            raw[i] = pack<T, 16>(g);
+        }
+    }
+
+    // Values to column c on, those before `cols`.
+    __device__ __forceinline__ void store(T *row, int c, int cols, bool vec, int lane, int bx) const {
+        if (vec) {
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) store_piece(row, c + i * kPer, c, cols, raw[i]);
+        } else {
+            const int from = c - lane * COLS, to = min(cols, from + bx * COLS);  // what the row's threads hold
+            const uint32_t off = uint32_t(reinterpret_cast<uintptr_t>(row + c) & 15);
+            const int e = c - int(off / sizeof(T));
+            const uint4 before = shuffle_up(raw[kPieces - 1], bx);
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i)
+                store_piece(row, e + i * kPer, from, to,
+                            off ? shift_down(i ? raw[i - 1] : before, raw[i], 16 - off) : raw[i]);
+            if (lane == bx - 1 && off)  // the rest of the last thread's values
+                store_piece(row, e + COLS, from, to,
+                            shift_down(raw[kPieces - 1], make_uint4(0, 0, 0, 0), 16 - off));
+        }
+    }
+};
+
+// ---------------------------------------------------------------------------
+// Codes
+// ---------------------------------------------------------------------------
+
+// 4 codes as fp32: the byte of code + 128 in the low bits of 2^23, less
+// 2^23 + 128.
+__device__ __forceinline__ void code_values(uint32_t w, float *f) {
+    w ^= 0x80808080u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440u + i)) - 8388736.0f;
+}
+
+__device__ __forceinline__ uint64_t kept_at(const CkptArgs &a, uint32_t r, int c) {
+    return uint64_t(r) * uint32_t(a.pitch) + uint32_t(c);
+}
+
+// The COLS (8 or 16) kept values from column c (a multiple of COLS) of row r on.
+template <int COLS>
+__device__ __forceinline__ void load_kept(const CkptArgs &a, uint32_t r, int c, float (&f)[COLS]) {
+    const uint64_t at = kept_at(a, r, c);
+    uint32_t w[COLS / 4];
+    if constexpr (COLS == 16) {
+        const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(a.codes + at));
+        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
     } else {
-#pragma unroll
-        for (int i = 0; i < kCols; ++i) f[i] = c + i < cols ? to_f32(row[c + i]) : 0.0f;
+        const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(a.codes + at));
+        w[0] = v.x, w[1] = v.y;
     }
+    const float step = ckpt_step(a.scales[at / kBlock]);
+#pragma unroll
+    for (int i = 0; i < COLS / 4; ++i) code_values(w[i], f + 4 * i);
+#pragma unroll
+    for (int i = 0; i < COLS; ++i) f[i] *= step;
 }
 
-template <typename T>
-__device__ __forceinline__ void store_vals(T *row, int64_t c, int64_t cols, bool vec,
-                                           const float (&f)[kCols]) {
-    constexpr int N = 16 / int(sizeof(T));
-    if (vec && c + kCols <= cols) {
+// The 8 kept values from any column on (the gated half of an odd width):
+// codes from the aligned 8 bytes around them, exponents of up to two blocks.
+// Nothing past the row's pitch is read.
+__device__ __forceinline__ void load_kept_any(const CkptArgs &a, uint32_t r, int c, float (&f)[8]) {
+    const uint64_t at = kept_at(a, r, c & ~7);
+    const uint32_t bytes = c & 7;
+    const uint2 lo = __ldcs(reinterpret_cast<const uint2 *>(a.codes + at));
+    uint2 hi = make_uint2(0, 0);
+    if (bytes && (c & ~7) + 8 < a.pitch) hi = __ldcs(reinterpret_cast<const uint2 *>(a.codes + at + 8));
+    const uint4 w = shift_down(make_uint4(lo.x, lo.y, hi.x, hi.y), make_uint4(0, 0, 0, 0), bytes);
+    const uint64_t block = kept_at(a, r, c) / kBlock;
+    const float first = ckpt_step(a.scales[block]);
+    const int in_first = kBlock - (c & (kBlock - 1));
+    const float second = in_first < 8 && c + in_first < a.pitch ? ckpt_step(a.scales[block + 1]) : first;
+    code_values(w.x, f);
+    code_values(w.y, f + 4);
 #pragma unroll
-        for (int i = 0; i < kCols / N; ++i) {
-            float g[N];
-#pragma unroll
-            for (int q = 0; q < N; ++q) g[q] = f[i * N + q];
-            reinterpret_cast<uint4 *>(row + c)[i] = pack<T, 16>(g);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < kCols; ++i)
-            if (c + i < cols) row[c + i] = from_f32<T>(f[i]);
-    }
+    for (int i = 0; i < 8; ++i) f[i] *= i < in_first ? first : second;
 }
 
-// The 16 kept values from column c (a multiple of 16) of row r on.
-__device__ __forceinline__ void load_kept(const CkptArgs &a, int64_t r, int64_t c, float (&f)[kCols]) {
-    const uint4 raw = *reinterpret_cast<const uint4 *>(a.codes + r * a.pitch + c);
-    const float step = ckpt_step(a.scales[(r * a.pitch + c) / kBlock]);
-    int8_t q[kCols];
-    memcpy(q, &raw, sizeof q);
-#pragma unroll
-    for (int i = 0; i < kCols; ++i) f[i] = float(q[i]) * step;
-}
-
-// The kept values from any column on, one at a time.
-__device__ __forceinline__ void load_kept_any(const CkptArgs &a, int64_t r, int64_t c, int64_t end,
-                                              float (&f)[kCols]) {
-#pragma unroll
-    for (int i = 0; i < kCols; ++i) {
-        f[i] = 0.0f;
-        if (c + i < end) {
-            const int64_t at = r * a.pitch + c + i;
-            f[i] = float(int8_t(a.codes[at])) * ckpt_step(a.scales[at / kBlock]);
-        }
-    }
-}
-
-// A block of 32 columns is two neighbouring threads.  The step is the power
-// of two 2^k with the largest magnitude in [64, 128) steps (k no less than
-// the type's least); codes are round-to-nearest-even of value / step,
+// A block of 32 columns is 32 / COLS neighbouring threads.  The step is the
+// power of two 2^k with the largest magnitude in [64, 128) steps (k no less
+// than the type's least); codes are round-to-nearest-even of value / step,
 // clamped to 127.  Multiplying by a power of two is exact, so a code is one
-// rounding of the value; and code * step has at most 7 significant bits, so
-// the products of the backward pass read it in 16 bits without a second
-// rounding.  The comparison of magnitudes as integers puts Inf and NaN above
-// every finite value.
+// rounding of the value (done by adding 1.5 * 2^23, whose last bit weighs 1);
+// and code * step has at most 7 significant bits, so the products of the
+// backward pass read it in 16 bits without a second rounding.  The comparison
+// of magnitudes as integers puts Inf and NaN above every finite value.
 template <typename T>
-__global__ void __launch_bounds__(kCkptThreads) dopt_ckpt_save_kernel(const CkptArgs a) {
+__global__ void __launch_bounds__(kCkptThreads) dopt_ckpt_save_kernel(const __grid_constant__ CkptArgs a) {
+    constexpr int COLS = 32 / int(sizeof(T));
     let_dependents_start();
     wait_for_grids_before();
-    const int64_t c = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) * kCols;
-    if (c >= a.pitch) return;  // both threads of a block: the pitch is a multiple of 32
-    // a block's two lanes of the warp (bx is 8, 16 or 32: a warp may hold several rows)
-    const unsigned pair = 3u << ((threadIdx.y * blockDim.x + threadIdx.x) & 30);
-    for (int64_t r = int64_t(blockIdx.y) * blockDim.y + threadIdx.y; r < a.rows;
-         r += int64_t(gridDim.y) * blockDim.y) {
-        float f[kCols];
-        load_vals(static_cast<const T *>(a.x) + r * a.ld, c, a.cols, a.vec, f);
+    const int bx = blockDim.x, lane = threadIdx.x;
+    const int c = (blockIdx.x * bx + lane) * COLS;
+    for (uint32_t r0 = blockIdx.y * blockDim.y; r0 < uint32_t(a.rows); r0 += gridDim.y * blockDim.y) {
+        const uint32_t r = r0 + threadIdx.y;
+        const bool here = r < uint32_t(a.rows);
+        Values<T, COLS> x;
+        x.load(static_cast<const T *>(a.x) + (here ? int64_t(r) * a.ld : 0), c, here ? a.cols : 0, a.vec, lane, bx);
+        float f[COLS];
+        x.get(f);
         uint32_t top = 0;
 #pragma unroll
-        for (int i = 0; i < kCols; ++i) top = max(top, __float_as_uint(f[i]) & 0x7fffffffu);
-        top = max(top, __shfl_xor_sync(pair, top, 1));
+        for (int i = 0; i < COLS; ++i) top = max(top, __float_as_uint(f[i]) & 0x7fffffffu);
+        top = max(top, __shfl_xor_sync(kFull, top, 1));
+        if constexpr (COLS == 8) top = max(top, __shfl_xor_sync(kFull, top, 2));
         const bool finite = top < 0x7f800000u;
         const int byte = max(int(top >> 23) - 6, a.min_exp);
         const float inv = __uint_as_float(uint32_t(254 - byte) << 23);
-        uint8_t q[kCols];
+        uint32_t q[COLS], w[COLS / 4];
 #pragma unroll
-        for (int i = 0; i < kCols; ++i) {
-            const float v = fminf(fmaxf(f[i] * inv, -127.0f), 127.0f);
-            q[i] = finite ? uint8_t(int8_t(__float2int_rn(v))) : 0;
+        for (int i = 0; i < COLS; ++i)
+            q[i] = __float_as_uint(fminf(fmaxf(f[i] * inv, -127.0f), 127.0f) + 12582912.0f);
+#pragma unroll
+        for (int i = 0; i < COLS / 4; ++i) {
+            w[i] = __byte_perm(__byte_perm(q[4 * i], q[4 * i + 1], 0x0040),
+                               __byte_perm(q[4 * i + 2], q[4 * i + 3], 0x0040), 0x5410);
+            if (!finite) w[i] = 0;
         }
-        uint4 raw;
-        memcpy(&raw, q, sizeof raw);
-        *reinterpret_cast<uint4 *>(a.codes + r * a.pitch + c) = raw;
-        if ((threadIdx.x & 1) == 0)
-            a.scales[(r * a.pitch + c) / kBlock] = uint8_t(finite ? byte : kNanByte);
+        if (here && c < a.pitch) {
+            const uint64_t at = kept_at(a, r, c);
+            if constexpr (COLS == 16)
+                *reinterpret_cast<uint4 *>(a.codes + at) = make_uint4(w[0], w[1], w[2], w[3]);
+            else
+                *reinterpret_cast<uint2 *>(a.codes + at) = make_uint2(w[0], w[1]);
+            if (c % kBlock == 0) a.scales[at / kBlock] = uint8_t(finite ? byte : kNanByte);
+        }
     }
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kCkptThreads) dopt_ckpt_load_kernel(const CkptArgs a) {
+__global__ void __launch_bounds__(kCkptThreads) dopt_ckpt_load_kernel(const __grid_constant__ CkptArgs a) {
+    constexpr int COLS = 32 / int(sizeof(T));
     let_dependents_start();
     wait_for_grids_before();
-    const int64_t c = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) * kCols;
-    if (c >= a.cols) return;
-    for (int64_t o = int64_t(blockIdx.y) * blockDim.y + threadIdx.y; o < a.n_out;
-         o += int64_t(gridDim.y) * blockDim.y) {
-        const int64_t r = a.index ? a.index[o] : o;
-        float f[kCols] = {};
-        if (r >= 0 && r < a.rows) load_kept(a, r, c, f);
-        store_vals(static_cast<T *>(a.out) + o * a.ld_out, c, a.cols, a.vec, f);
+    const int bx = blockDim.x, lane = threadIdx.x;
+    const int c = (blockIdx.x * bx + lane) * COLS;
+    for (uint32_t r0 = blockIdx.y * blockDim.y; r0 < uint32_t(a.n_out); r0 += gridDim.y * blockDim.y) {
+        const uint32_t o = r0 + threadIdx.y;
+        const bool here = o < uint32_t(a.n_out);
+        float f[COLS] = {};
+        if (here && c < a.cols) {
+            const uint32_t r = a.index ? uint32_t(a.index[o]) : o;
+            if (r < uint32_t(a.rows)) load_kept<COLS>(a, r, c, f);
+        }
+        Values<T, COLS> y;
+        y.set(f);
+        y.store(static_cast<T *>(a.out) + (here ? int64_t(o) * a.ld_out : 0), c, here ? a.cols : 0, a.vec, lane, bx);
     }
 }
 
-// 1 / (1 + e^-x) and 1 - that, each with small relative error for |x| <= 87
-// (further out e^-x leaves fp32's normal range).  Results that are rounded
-// to 16 bits take the hardware's exponential and division (at most 2 +
-// 1.173 |x| units in the last place of fp32, below 2^-16 over that range),
-// fp32 ones the library's.
+// ---------------------------------------------------------------------------
+// Activation functions
+// ---------------------------------------------------------------------------
+
+// s = 1 / (1 + e^-x) and 1 - s = e^-x s, each with small relative error for
+// x >= -87 (below, e^-x leaves fp32's normal range).  Results that are rounded
+// to 16 bits take the hardware's exponential and reciprocal (the exponential
+// is off by at most 2 + 1.173 |x| units in the last place), fp32 ones the
+// library's.
 template <typename T>
-__device__ __forceinline__ void sigmoid(float x, float &s, float &one_minus) {
+__device__ __forceinline__ void sigmoid(float x, float &s, float &rest) {
     const float e = sizeof(T) == 4 ? expf(-x) : __expf(-x);
     s = sizeof(T) == 4 ? 1.0f / (1.0f + e) : __fdividef(1.0f, 1.0f + e);
-    one_minus = e * s;
+    rest = e * s;
 }
-__device__ __forceinline__ float clamp_nan(float x, float b) {  // NaN stays NaN
-    return x < -b ? -b : x > b ? b : x;
+__device__ __forceinline__ float at_least(float x, float b) {  // NaN stays NaN
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(b));
+    return y;
+}
+__device__ __forceinline__ float at_most(float x, float b) {
+    float y;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(b));
+    return y;
 }
 
 // silu'(h) = s (1 + h (1 - s)) and silu(h) = h s, s = sigmoid(h).  Below -87
-// both are 0 to within 2e-36; above 87 they are 1 and h (and h (1 - s) must
-// not become Inf * 0).
+// both are within 2e-36 of what they are there, 0 in effect.
 template <typename T>
 __device__ __forceinline__ float silu_slope(float h, float &silu) {
-    const float x = clamp_nan(h, 87.0f);
-    float s, m;
-    sigmoid<T>(x, s, m);
-    silu = h < -87.0f ? 0.0f : h * s;
-    return h < -87.0f ? 0.0f : s * fmaf(x, m, 1.0f);
+    const float x = at_least(h, -87.0f);
+    float s, rest;
+    sigmoid<T>(x, s, rest);
+    silu = x * s;
+    return s * fmaf(x, rest, 1.0f);
 }
 
 // GELU in its tanh form is h p with p = (1 + tanh u) / 2 = sigmoid(2u),
@@ -181,48 +330,56 @@ __device__ __forceinline__ float silu_slope(float h, float &silu) {
 template <typename T>
 __device__ __forceinline__ float gelu_slope(float h) {
     constexpr float kC = 0.79788456080286536f, kA = 0.044715f;
-    const float x = clamp_nan(h, 9.9f);
+    const float x = at_most(at_least(h, -9.9f), 9.9f);
     const float x2 = x * x;
-    float p, m;
-    sigmoid<T>(2.0f * kC * x * fmaf(kA, x2, 1.0f), p, m);
-    return h < -9.9f ? 0.0f : fmaf(2.0f * kC * x * fmaf(3.0f * kA, x2, 1.0f), p * m, p);
+    float p, rest;
+    sigmoid<T>(2.0f * kC * x * fmaf(kA, x2, 1.0f), p, rest);
+    return fmaf(2.0f * kC * x * fmaf(3.0f * kA, x2, 1.0f), p * rest, p);
 }
 
 template <typename T, int ACT>
-__global__ void __launch_bounds__(kCkptThreads) dopt_ckpt_act_grad_kernel(const CkptArgs a) {
+__global__ void __launch_bounds__(kCkptThreads) dopt_ckpt_act_grad_kernel(const __grid_constant__ CkptArgs a) {
+    constexpr int COLS = 8;
     let_dependents_start();
     wait_for_grids_before();
-    const int64_t c = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) * kCols;
-    const int64_t width = ACT == DOPT_ACT_SWIGLU ? a.half : a.cols;
-    if (c >= width) return;
-    for (int64_t r = int64_t(blockIdx.y) * blockDim.y + threadIdx.y; r < a.rows;
-         r += int64_t(gridDim.y) * blockDim.y) {
-        float d[kCols], h[kCols];
-        load_vals(static_cast<const T *>(a.x) + r * a.ld, c, width, a.vec, d);
-        load_kept(a, r, c, h);
-        T *out = static_cast<T *>(a.out) + r * a.ld_out;
-        if constexpr (ACT == DOPT_ACT_SWIGLU) {
-            float u[kCols];
-            if (width % kBlock == 0)
-                load_kept(a, r, width + c, u);
-            else
-                load_kept_any(a, r, width + c, a.cols, u);
+    const int bx = blockDim.x, lane = threadIdx.x;
+    const int c = (blockIdx.x * bx + lane) * COLS;
+    const int width = ACT == DOPT_ACT_SWIGLU ? a.half : a.cols;
+    for (uint32_t r0 = blockIdx.y * blockDim.y; r0 < uint32_t(a.rows); r0 += gridDim.y * blockDim.y) {
+        const uint32_t r = r0 + threadIdx.y;
+        const bool here = r < uint32_t(a.rows);
+        Values<T, COLS> x;
+        x.load(static_cast<const T *>(a.x) + (here ? int64_t(r) * a.ld : 0), c, here ? width : 0, a.vec, lane, bx);
+        float h[COLS] = {}, u[COLS] = {};
+        if (here && c < width) {
+            load_kept<COLS>(a, r, c, h);
+            if constexpr (ACT == DOPT_ACT_SWIGLU) {
+                if (width % kBlock == 0)
+                    load_kept<COLS>(a, r, width + c, u);
+                else
+                    load_kept_any(a, r, width + c, u);
+            }
+        }
+        float d[COLS];
+        x.get(d);
+        T *out = static_cast<T *>(a.out) + (here ? int64_t(r) * a.ld_out : 0);
 #pragma unroll
-            for (int i = 0; i < kCols; ++i) {
-                float silu;
+        for (int i = 0; i < COLS; ++i) {
+            float silu;
+            if constexpr (ACT == DOPT_ACT_SWIGLU) {
                 const float slope = silu_slope<T>(h[i], silu);
                 h[i] = d[i] * u[i] * slope;
                 u[i] = d[i] * silu;
+            } else {
+                h[i] = d[i] * (ACT == DOPT_ACT_SILU ? silu_slope<T>(h[i], silu) : gelu_slope<T>(h[i]));
             }
-            store_vals(out, c, width, a.vec, h);
-            store_vals(out + width, c, width, a.vec, u);
-        } else {
-#pragma unroll
-            for (int i = 0; i < kCols; ++i) {
-                float silu;
-                d[i] *= ACT == DOPT_ACT_SILU ? silu_slope<T>(h[i], silu) : gelu_slope<T>(h[i]);
-            }
-            store_vals(out, c, width, a.vec, d);
+        }
+        Values<T, COLS> y;
+        y.set(h);
+        y.store(out, c, here ? width : 0, a.vec, lane, bx);
+        if constexpr (ACT == DOPT_ACT_SWIGLU) {
+            y.set(u);
+            y.store(out + width, c, here ? width : 0, a.vec, lane, bx);
         }
     }
 }
@@ -260,19 +417,20 @@ bool vec_rows(const void *p, dopt_dtype dtype, int64_t ld) {
 
 CkptArgs ckpt_args(const void *ckpt, int64_t rows, int64_t cols) {
     CkptArgs a{};
-    a.rows = rows;
-    a.cols = cols;
-    a.pitch = ckpt_pitch(cols);
+    a.rows = int32_t(rows);
+    a.cols = int32_t(cols);
+    a.pitch = int32_t(ckpt_pitch(cols));
     a.codes = static_cast<uint8_t *>(const_cast<void *>(ckpt));
     a.scales = a.codes + rows * a.pitch;
     return a;
 }
 
-// Blocks of bx threads along the columns and 256 / bx rows.
+// Blocks of bx threads along the columns, `each` columns a thread, and
+// 256 / bx rows.
 template <typename Kernel>
-int launch_rows(const char *who, Kernel kernel, const CkptArgs &a, int64_t cols, int64_t rows,
+int launch_rows(const char *who, Kernel kernel, const CkptArgs &a, int64_t cols, int each, int64_t rows,
                 cudaStream_t stream) {
-    const int64_t groups = (cols + kCols - 1) / kCols;
+    const int64_t groups = (cols + each - 1) / each;
     const int bx = groups > 16 ? 32 : groups > 8 ? 16 : 8;
     const int by = kCkptThreads / bx;
     const dim3 grid(unsigned((groups + bx - 1) / bx),
@@ -284,11 +442,11 @@ template <typename T>
 int launch_act(const char *who, dopt_act act, const CkptArgs &a, int64_t width, cudaStream_t stream) {
     switch (act) {
         case DOPT_ACT_SILU:
-            return launch_rows(who, dopt_ckpt_act_grad_kernel<T, DOPT_ACT_SILU>, a, width, a.rows, stream);
+            return launch_rows(who, dopt_ckpt_act_grad_kernel<T, DOPT_ACT_SILU>, a, width, 8, a.rows, stream);
         case DOPT_ACT_GELU:
-            return launch_rows(who, dopt_ckpt_act_grad_kernel<T, DOPT_ACT_GELU>, a, width, a.rows, stream);
+            return launch_rows(who, dopt_ckpt_act_grad_kernel<T, DOPT_ACT_GELU>, a, width, 8, a.rows, stream);
         default:
-            return launch_rows(who, dopt_ckpt_act_grad_kernel<T, DOPT_ACT_SWIGLU>, a, width, a.rows, stream);
+            return launch_rows(who, dopt_ckpt_act_grad_kernel<T, DOPT_ACT_SWIGLU>, a, width, 8, a.rows, stream);
     }
 }
 
@@ -321,9 +479,9 @@ extern "C" int dopt_ckpt_save(const void *x, dopt_dtype dtype, int64_t rows, int
     a.vec = vec_rows(x, dtype, ld);
     a.min_exp = dtype == DOPT_FP16 ? 127 - 24 : 1;
     switch (dtype) {
-        case DOPT_BF16: return launch_rows(who, dopt_ckpt_save_kernel<__nv_bfloat16>, a, a.pitch, rows, stream);
-        case DOPT_FP16: return launch_rows(who, dopt_ckpt_save_kernel<__half>, a, a.pitch, rows, stream);
-        default: return launch_rows(who, dopt_ckpt_save_kernel<float>, a, a.pitch, rows, stream);
+        case DOPT_BF16: return launch_rows(who, dopt_ckpt_save_kernel<__nv_bfloat16>, a, a.pitch, 16, rows, stream);
+        case DOPT_FP16: return launch_rows(who, dopt_ckpt_save_kernel<__half>, a, a.pitch, 16, rows, stream);
+        default: return launch_rows(who, dopt_ckpt_save_kernel<float>, a, a.pitch, 8, rows, stream);
     }
 }
 
@@ -347,12 +505,12 @@ extern "C" int dopt_ckpt_load(const void *ckpt, int64_t rows, int64_t cols, cons
     a.out = out;
     a.ld_out = ld;
     a.index = row_index;
-    a.n_out = n_out;
+    a.n_out = int32_t(n_out);
     a.vec = vec_rows(out, dtype, ld);
     switch (dtype) {
-        case DOPT_BF16: return launch_rows(who, dopt_ckpt_load_kernel<__nv_bfloat16>, a, cols, n_out, stream);
-        case DOPT_FP16: return launch_rows(who, dopt_ckpt_load_kernel<__half>, a, cols, n_out, stream);
-        default: return launch_rows(who, dopt_ckpt_load_kernel<float>, a, cols, n_out, stream);
+        case DOPT_BF16: return launch_rows(who, dopt_ckpt_load_kernel<__nv_bfloat16>, a, cols, 16, n_out, stream);
+        case DOPT_FP16: return launch_rows(who, dopt_ckpt_load_kernel<__half>, a, cols, 16, n_out, stream);
+        default: return launch_rows(who, dopt_ckpt_load_kernel<float>, a, cols, 8, n_out, stream);
     }
 }
 
@@ -378,7 +536,7 @@ extern "C" int dopt_ckpt_act_grad(const void *ckpt, int64_t rows, int64_t cols, 
     a.out = d_in;
     a.ld = ld;
     a.ld_out = ld_in;
-    a.half = width;
+    a.half = int32_t(width);
     a.vec = vec_rows(d_out, dtype, ld) && vec_rows(d_in, dtype, ld_in) &&
             (act != DOPT_ACT_SWIGLU || width * int64_t(elem_bytes(dtype)) % 16 == 0);
     switch (dtype) {

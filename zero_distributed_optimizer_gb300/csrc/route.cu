@@ -84,24 +84,32 @@ __global__ void __launch_bounds__(kSortThreads) dopt_route_place_kernel(const So
     }
     if (a.tiles > 1) {  // slots of each bin in all tiles, and in the tiles before this one
         const int n = a.tiles * bins, mine = int(blockIdx.x) * bins;
-        for (int i = threadIdx.x; i < n; i += kSortThreads) {
-            const int32_t c = a.counts[i];
-            if (c) {
-                atomicAdd(&total[i % bins], c);
-                if (i < mine) atomicAdd(&base[i % bins], c);
+        for (int i0 = threadIdx.x; i0 < n; i0 += 4 * kSortThreads) {
+            int32_t c[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) c[j] = i0 + j * kSortThreads < n ? a.counts[i0 + j * kSortThreads] : 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int i = i0 + j * kSortThreads;
+                if (c[j]) {
+                    atomicAdd(&total[i % bins], c[j]);
+                    if (i < mine) atomicAdd(&base[i % bins], c[j]);
+                }
             }
         }
     }
     __syncthreads();
     // the warps' counts become the slots of the bin in the warps before
-    for (int b = threadIdx.x; b < bins; b += kSortThreads) {
-        int run = 0;
-        for (int w = 0; w < kSortWarps; ++w) {
-            const int c = cnt[w * bins + b];
-            cnt[w * bins + b] = uint16_t(run);
-            run += c;
+    for (int b = warp; b < bins; b += kSortWarps) {  // lane l: warp l's count
+        const int c = cnt[lane * bins + b];
+        int incl = c;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(kFull, incl, d);
+            if (lane >= d) incl += o;
         }
-        if (a.tiles == 1) total[b] = run;
+        cnt[lane * bins + b] = uint16_t(incl - c);
+        if (a.tiles == 1 && lane == 31) total[b] = incl;
     }
     __syncthreads();
     // base += slots in lower bins (an exclusive scan of total over the bins)
@@ -197,111 +205,149 @@ __global__ void __launch_bounds__(kRowThreads) dopt_route_dispatch_kernel(const 
     }
 }
 
-// A warp takes 32 * U accesses of one token's row: the sum over the token's
-// slots, in order, of weight * row, in fp32, rounded once.  Dropped slots
-// are left out (a weight of NaN there does not matter).
-template <typename T, int VB, int U>
-__global__ void __launch_bounds__(kRowThreads) dopt_route_combine_kernel(const RowArgs a) {
+// A warp takes 32 * U accesses of a token's row, of one token after another:
+// the sum over the token's slots, in order, of weight * row, in fp32, rounded
+// once.  Dropped slots are left out (a weight of NaN there does not matter).
+// The rows of A slots are in flight at once, and the next token's slots and
+// weights are loaded under them.
+template <typename T, int VB, int U, int A>
+__global__ void __launch_bounds__(kRowThreads) dopt_route_combine_kernel(const __grid_constant__ RowArgs a) {
     using V = typename Raw<VB>::type;
     constexpr int N = VB / int(sizeof(T));
-    constexpr int kAhead = 4;  // slots whose rows are in flight at once
     const int lane = threadIdx.x & 31;
-    const int64_t t = int64_t(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
+    const int64_t stride = int64_t(gridDim.x) * kRowWarps;
+    int64_t t = int64_t(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
     let_dependents_start();
     wait_for_grids_before();
-    if (t >= a.tokens) return;
     const int c0 = int(blockIdx.y) * 32 * U + lane;
     const V *rows = static_cast<const V *>(a.x);
-    float acc[U][N] = {};
-    for (int j0 = 0; j0 < a.k; j0 += 32) {
-        int row = -1;
-        float weight = 1.0f;
-        if (j0 + lane < a.k) {
-            row = a.slot_row[t * a.k + j0 + lane];
-            if (a.weights) weight = a.weights[t * a.k + j0 + lane];
+    int next_row = -1;
+    float next_weight = 1.0f;
+    auto slots_of = [&](int64_t token, int j0) {
+        next_row = -1;
+        if (token < a.tokens && j0 + lane < a.k) {
+            next_row = a.slot_row[token * a.k + j0 + lane];
+            if (a.weights) next_weight = a.weights[token * a.k + j0 + lane];
         }
-        const int n = min(32, a.k - j0);
-        for (int j = 0; j < n; j += kAhead) {
-            V v[kAhead][U];
-            int r[kAhead];
-            float w[kAhead];
+    };
+    slots_of(t, 0);
+    for (; t < a.tokens; t += stride) {
+        float acc[U][N] = {};
+        for (int j0 = 0; j0 < a.k; j0 += 32) {
+            int row = next_row;
+            const float weight = next_weight;
+            if (row >= a.n_rows) row = -1;
+            if (j0 + 32 < a.k) slots_of(t, j0 + 32);
+            else slots_of(t + stride, 0);
+            const int n = min(32, a.k - j0);
+            for (int j = 0; j < n; j += A) {
+                V v[A][U];
+                int r[A];
 #pragma unroll
-            for (int q = 0; q < kAhead; ++q) {
-                r[q] = __shfl_sync(kFull, row, (j + q) & 31);
-                w[q] = __shfl_sync(kFull, weight, (j + q) & 31);
-                if (j + q >= n || r[q] >= a.n_rows) r[q] = -1;
-                if (r[q] < 0) continue;
+                for (int q = 0; q < A; ++q) {
+                    r[q] = j + q < n ? __shfl_sync(kFull, row, j + q) : -1;
+                    if (r[q] < 0) continue;
+                    const V *p = rows + int64_t(r[q]) * a.vecs + c0;
 #pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (c0 + 32 * u < a.vecs) v[q][u] = rows[int64_t(r[q]) * a.vecs + c0 + 32 * u];
-            }
+                    for (int u = 0; u < U; ++u)
+                        if (c0 + 32 * u < a.vecs) v[q][u] = p[32 * u];
+                }
 #pragma unroll
-            for (int q = 0; q < kAhead; ++q) {
-                if (r[q] < 0) continue;
+                for (int q = 0; q < A; ++q) {
+                    if (r[q] < 0) continue;
+                    const float w = __shfl_sync(kFull, weight, j + q);
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    if (c0 + 32 * u >= a.vecs) continue;
-                    float f[N];
-                    unpack<T, VB>(v[q][u], f);
+                    for (int u = 0; u < U; ++u) {
+                        float f[N];
+                        unpack<T, VB>(v[q][u], f);
 #pragma unroll
-                    for (int i = 0; i < N; ++i) acc[u][i] = fmaf(w[q], f[i], acc[u][i]);
+                        for (int i = 0; i < N; ++i) acc[u][i] = fmaf(w, f[i], acc[u][i]);
+                    }
                 }
             }
         }
-    }
-    V *dst = static_cast<V *>(a.out) + t * a.ld;
+        V *dst = static_cast<V *>(a.out) + t * a.ld + c0;
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-        if (c0 + 32 * u < a.vecs) dst[c0 + 32 * u] = pack<T, VB>(acc[u]);
+        for (int u = 0; u < U; ++u)
+            if (c0 + 32 * u < a.vecs) __stcs(dst + 32 * u, pack<T, VB>(acc[u]));
+    }
 }
 
-// A warp takes one slot: d_row = weight * d_out in one pass that also sums
-// <d_out, row>.  A CTA's 8 warps take consecutive slots, so the reads of
-// d_out by a token's k slots mostly hit in L1.
+// A warp takes two neighbouring slots, of one pair after another: d_row =
+// weight * d_out in one pass that also sums <d_out, row>.  Both slots' loads
+// are in flight at once, and the next pair's rows and weights are looked up
+// under them; d_out, read by all of a token's slots, mostly hits in L1.
 template <typename T, int VB, int U>
-__global__ void __launch_bounds__(kRowThreads) dopt_route_combine_grad_kernel(const RowArgs a) {
+__global__ void __launch_bounds__(kRowThreads) dopt_route_combine_grad_kernel(const __grid_constant__ RowArgs a) {
     using V = typename Raw<VB>::type;
     constexpr int N = VB / int(sizeof(T));
     const int lane = threadIdx.x & 31;
-    const int64_t s = int64_t(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
+    const int64_t slots = a.tokens * a.k, stride = int64_t(gridDim.x) * kRowWarps * 2;
+    int64_t s = (int64_t(blockIdx.x) * kRowWarps + (threadIdx.x >> 5)) * 2;
     let_dependents_start();
     wait_for_grids_before();
-    if (s >= a.tokens * a.k) return;
-    const int r = a.slot_row[s];
-    if (r < 0 || r >= a.n_rows) {
-        if (lane == 0) a.d_weights[s] = 0.0f;
-        return;
-    }
-    const float w = a.weights[s];
-    const V *d = static_cast<const V *>(a.x) + s / a.k * a.ld;
-    const V *y = static_cast<const V *>(a.rows) + int64_t(r) * a.vecs;
-    V *out = static_cast<V *>(a.out) + int64_t(r) * a.vecs;
-    float dot = 0.0f;
-    for (int c0 = lane; c0 < a.vecs; c0 += 32 * U) {
-        V dv[U], yv[U];
+    int next_row[2];
+    float next_weight[2];
+    auto look_up = [&](int64_t first) {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (c0 + 32 * u < a.vecs) {
-                yv[u] = y[c0 + 32 * u];
-                dv[u] = d[c0 + 32 * u];
+        for (int g = 0; g < 2; ++g) {
+            next_row[g] = first + g < slots ? a.slot_row[first + g] : -1;
+            next_weight[g] = first + g < slots ? a.weights[first + g] : 0.0f;
+        }
+    };
+    look_up(s);
+    for (; s < slots; s += stride) {
+        int row[2];
+        float w[2], dot[2] = {};
+        const V *d[2], *y[2];
+        V *out[2];
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            row[g] = next_row[g] < a.n_rows ? next_row[g] : -1;
+            w[g] = next_weight[g];
+            // (slots are below 2^31)
+            d[g] = static_cast<const V *>(a.x) + int64_t(uint32_t(s + g) / uint32_t(a.k)) * a.ld;
+            y[g] = static_cast<const V *>(a.rows) + int64_t(max(row[g], 0)) * a.vecs;
+            out[g] = static_cast<V *>(a.out) + int64_t(max(row[g], 0)) * a.vecs;
+        }
+        look_up(s + stride);
+        for (int c0 = lane; c0 < a.vecs; c0 += 32 * U) {
+            V dv[2][U], yv[2][U];
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                if (row[g] < 0) continue;
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (c0 + 32 * u < a.vecs) {
+                        yv[g][u] = __ldcs(y[g] + c0 + 32 * u);
+                        dv[g][u] = d[g][c0 + 32 * u];
+                    }
             }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (c0 + 32 * u >= a.vecs) continue;
-            float df[N], yf[N];
-            unpack<T, VB>(dv[u], df);
-            unpack<T, VB>(yv[u], yf);
+            for (int g = 0; g < 2; ++g) {
+                if (row[g] < 0) continue;
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                dot = fmaf(df[i], yf[i], dot);
-                df[i] = w * df[i];
+                for (int u = 0; u < U; ++u) {
+                    if (c0 + 32 * u >= a.vecs) continue;
+                    float df[N], yf[N];
+                    unpack<T, VB>(dv[g][u], df);
+                    unpack<T, VB>(yv[g][u], yf);
+#pragma unroll
+                    for (int i = 0; i < N; ++i) {
+                        dot[g] = fmaf(df[i], yf[i], dot[g]);
+                        df[i] = w[g] * df[i];
+                    }
+                    __stcs(out[g] + c0 + 32 * u, pack<T, VB>(df));
+                }
             }
-            out[c0 + 32 * u] = pack<T, VB>(df);
+        }
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+#pragma unroll
+            for (int m = 16; m > 0; m >>= 1) dot[g] += __shfl_xor_sync(kFull, dot[g], m);
+            if (lane == 0 && s + g < slots) a.d_weights[s + g] = dot[g];  // 0 for a dropped slot
         }
     }
-#pragma unroll
-    for (int m = 16; m > 0; m >>= 1) dot += __shfl_xor_sync(kFull, dot, m);
-    if (lane == 0) a.d_weights[s] = dot;
 }
 
 // ---------------------------------------------------------------------------
@@ -344,35 +390,44 @@ int launch_dispatch(const char *who, const RowArgs &a, cudaStream_t stream) {
     return launch_op(who, dopt_route_dispatch_kernel<VB, U>, grid, dim3(kRowThreads), 0, stream, a);
 }
 
-template <typename T, int VB, int U>
+// Blocks for `blocks` blocks' work: no more than 16 rounds of 6 an SM's worth
+// (each then takes several tokens in turn).
+unsigned row_blocks(int64_t blocks) { return unsigned(std::min<int64_t>(blocks, 152 * 6)); }
+
+template <typename T, int VB, int U, int A>
 int launch_combine(const char *who, const RowArgs &a, cudaStream_t stream) {
-    const dim3 grid(unsigned((a.tokens + kRowWarps - 1) / kRowWarps),
-                    unsigned((a.vecs + 32 * U - 1) / (32 * U)));
-    return launch_op(who, dopt_route_combine_kernel<T, VB, U>, grid, dim3(kRowThreads), 0, stream, a);
+    const dim3 grid(row_blocks((a.tokens + kRowWarps - 1) / kRowWarps), unsigned((a.vecs + 32 * U - 1) / (32 * U)));
+    return launch_op(who, dopt_route_combine_kernel<T, VB, U, A>, grid, dim3(kRowThreads), 0, stream, a);
+}
+
+// Slots in flight: 2 for up to 2 a token, 4 otherwise.
+template <typename T, int VB, int U>
+int pick_ahead(const char *who, const RowArgs &a, cudaStream_t stream) {
+    return a.k <= 2 ? launch_combine<T, VB, U, 2>(who, a, stream) : launch_combine<T, VB, U, 4>(who, a, stream);
 }
 
 template <typename T>
 int pick_combine(const char *who, const RowArgs &a, int vb, cudaStream_t stream) {
-    if (vb == 16) return launch_combine<T, 16, 2>(who, a, stream);
-    if (vb == 8) return launch_combine<T, 8, 4>(who, a, stream);
-    if (vb == 4) return launch_combine<T, 4, 4>(who, a, stream);
-    if constexpr (sizeof(T) == 2) return launch_combine<T, 2, 4>(who, a, stream);
+    if (vb == 16) return pick_ahead<T, 16, 2>(who, a, stream);
+    if (vb == 8) return pick_ahead<T, 8, 4>(who, a, stream);
+    if (vb == 4) return pick_ahead<T, 4, 4>(who, a, stream);
+    if constexpr (sizeof(T) == 2) return pick_ahead<T, 2, 4>(who, a, stream);
     return DOPT_E_ALIGN;  // not reached: fp32 rows are 4-byte aligned
 }
 
 template <typename T, int VB, int U>
 int launch_combine_grad(const char *who, const RowArgs &a, cudaStream_t stream) {
-    const dim3 grid(unsigned((a.tokens * a.k + kRowWarps - 1) / kRowWarps));
+    const dim3 grid(row_blocks((a.tokens * a.k + 2 * kRowWarps - 1) / (2 * kRowWarps)));
     return launch_op(who, dopt_route_combine_grad_kernel<T, VB, U>, grid, dim3(kRowThreads), 0,
                      stream, a);
 }
 
 template <typename T>
 int pick_combine_grad(const char *who, const RowArgs &a, int vb, cudaStream_t stream) {
-    if (vb == 16) return launch_combine_grad<T, 16, 4>(who, a, stream);
-    if (vb == 8) return launch_combine_grad<T, 8, 4>(who, a, stream);
-    if (vb == 4) return launch_combine_grad<T, 4, 8>(who, a, stream);
-    if constexpr (sizeof(T) == 2) return launch_combine_grad<T, 2, 8>(who, a, stream);
+    if (vb == 16) return launch_combine_grad<T, 16, 2>(who, a, stream);
+    if (vb == 8) return launch_combine_grad<T, 8, 2>(who, a, stream);
+    if (vb == 4) return launch_combine_grad<T, 4, 4>(who, a, stream);
+    if constexpr (sizeof(T) == 2) return launch_combine_grad<T, 2, 4>(who, a, stream);
     return DOPT_E_ALIGN;  // not reached: fp32 rows are 4-byte aligned
 }
 
