@@ -612,10 +612,9 @@ int dopt_step_clipped_noalloc(const dopt_layout *layout, const dopt_adam_cfg *cf
  * do not depend on the order in which blocks run.
  *
  * Rows: a "row stride" is in elements, at least the row length; pointers
- * need only be aligned to their elements (the widest access of 16, 8, 4 or 2
- * bytes that pointers, row strides and row lengths allow is used, so 16-byte
- * aligned rows are the fast ones).  Outputs must not overlap inputs unless
- * stated.
+ * need only be aligned to their elements (16-byte aligned rows are the fast
+ * ones).  Outputs must not
+ * overlap inputs unless stated.
  * ------------------------------------------------------------------------ */
 
 #define DOPT_MAX_EXPERTS 1024

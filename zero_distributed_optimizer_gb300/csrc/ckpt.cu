@@ -9,14 +9,10 @@
 // covers bx threads' columns of 256 / bx rows and strides over
 // the rows, so no index is divided.
 //
-// Codes are always aligned (a row's pitch is a multiple of 128).  Rows of
-// values that are not 16-byte aligned are read and written in the aligned
-// 16-byte pieces around them all the same: the bx threads of a row hold
-// neighbouring pieces, take the part that is missing from their neighbour
-// and shift; only pieces that reach over the ends of the row (reading) or of
-// the threads' stretch of it (writing) go element by element.  (One element
-// at a time, 16384 x 5631 bf16 took 585 us to keep and read back.)
-#include "op_common.cuh"
+// Codes are always aligned (a row's pitch is a multiple of 128); rows of
+// values that are not go in aligned pieces all the same (rows.cuh): 16384 x
+// 5631 bf16, kept and read back, took 585 us one element at a time.
+#include "rows.cuh"
 
 namespace {
 
@@ -38,64 +34,9 @@ struct CkptArgs {
 };
 
 // ---------------------------------------------------------------------------
-// 8 values of a row.  All threads of a warp call these together; `lane` is
-// the thread's place among the bx of its row, `here` whether the row exists.
+// COLS values of a row.  All threads of a warp call these together; `lane` is
+// the thread's place among the bx of its row.
 // ---------------------------------------------------------------------------
-
-// (hi, lo) a 16-byte piece and its successor, shifted down by `bytes` (0..15):
-// the 4 words from that byte on.
-__device__ __forceinline__ uint4 shift_down(const uint4 &lo, const uint4 &hi, uint32_t bytes) {
-    uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-    if (bytes & 8) {
-#pragma unroll
-        for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
-    }
-    if (bytes & 4) {
-#pragma unroll
-        for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
-    }
-    const uint32_t bits = (bytes & 3) * 8;
-    return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
-                      __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
-}
-__device__ __forceinline__ uint4 shuffle_down(const uint4 &v, int width) {
-    return make_uint4(__shfl_down_sync(kFull, v.x, 1, width), __shfl_down_sync(kFull, v.y, 1, width),
-                      __shfl_down_sync(kFull, v.z, 1, width), __shfl_down_sync(kFull, v.w, 1, width));
-}
-__device__ __forceinline__ uint4 shuffle_up(const uint4 &v, int width) {
-    return make_uint4(__shfl_up_sync(kFull, v.x, 1, width), __shfl_up_sync(kFull, v.y, 1, width),
-                      __shfl_up_sync(kFull, v.z, 1, width), __shfl_up_sync(kFull, v.w, 1, width));
-}
-
-// The 16 bytes at elements [e, e + 16 / sizeof(T)) of a row of `cols`; those
-// before or past the row are not read (0).
-template <typename T>
-__device__ __forceinline__ uint4 load_piece(const T *row, int e, int cols) {
-    constexpr int N = 16 / int(sizeof(T));
-    if (e >= 0 && e + N <= cols) return __ldcs(reinterpret_cast<const uint4 *>(row + e));
-    using E = typename Raw<int(sizeof(T))>::type;
-    E v[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = e + i >= 0 && e + i < cols ? reinterpret_cast<const E *>(row)[e + i] : E(0);
-    uint4 raw;
-    memcpy(&raw, v, sizeof raw);
-    return raw;
-}
-// The same to elements [e, ...) of which those in [from, to) are written.
-template <typename T>
-__device__ __forceinline__ void store_piece(T *row, int e, int from, int to, const uint4 &raw) {
-    constexpr int N = 16 / int(sizeof(T));
-    if (e >= from && e + N <= to) {
-        __stcs(reinterpret_cast<uint4 *>(row + e), raw);
-        return;
-    }
-    using E = typename Raw<int(sizeof(T))>::type;
-    E v[N];
-    memcpy(v, &raw, sizeof raw);
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        if (e + i >= from && e + i < to) reinterpret_cast<E *>(row)[e + i] = v[i];
-}
 
 template <typename T, int COLS>
 struct Values {
@@ -293,13 +234,19 @@ __global__ void __launch_bounds__(kCkptThreads) dopt_ckpt_load_kernel(const __gr
 
 // s = 1 / (1 + e^-x) and 1 - s = e^-x s, each with small relative error for
 // x >= -87 (below, e^-x leaves fp32's normal range).  Results that are rounded
-// to 16 bits take the hardware's exponential and reciprocal (the exponential
-// is off by at most 2 + 1.173 |x| units in the last place), fp32 ones the
-// library's.
+// to 16 bits take the hardware's powers of two and reciprocal, each off by at
+// most 2^-22 of its result, the power also by the rounding of -x / ln 2 (in
+// all below (2 + 1.2 |x|) 2^-23); fp32 ones take the library's functions.
 template <typename T>
 __device__ __forceinline__ void sigmoid(float x, float &s, float &rest) {
-    const float e = sizeof(T) == 4 ? expf(-x) : __expf(-x);
-    s = sizeof(T) == 4 ? 1.0f / (1.0f + e) : __fdividef(1.0f, 1.0f + e);
+    float e;
+    if constexpr (sizeof(T) == 4) {
+        e = expf(-x);
+        s = 1.0f / (1.0f + e);
+    } else {
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.44269504f));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + e));
+    }
     rest = e * s;
 }
 __device__ __forceinline__ float at_least(float x, float b) {  // NaN stays NaN

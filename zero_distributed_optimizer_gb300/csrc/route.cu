@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(kRowThreads) dopt_route_combine_kernel(const _
                     const V *p = rows + int64_t(r[q]) * a.vecs + c0;
 #pragma unroll
                     for (int u = 0; u < U; ++u)
-                        if (c0 + 32 * u < a.vecs) v[q][u] = p[32 * u];
+                        if (c0 + 32 * u < a.vecs) v[q][u] = __ldcs(p + 32 * u);
                 }
 #pragma unroll
                 for (int q = 0; q < A; ++q) {
@@ -273,36 +273,36 @@ __global__ void __launch_bounds__(kRowThreads) dopt_route_combine_kernel(const _
     }
 }
 
-// A warp takes two neighbouring slots, of one pair after another: d_row =
-// weight * d_out in one pass that also sums <d_out, row>.  Both slots' loads
-// are in flight at once, and the next pair's rows and weights are looked up
+// A warp takes G neighbouring slots, and G others after them: d_row =
+// weight * d_out in one pass that also sums <d_out, row>.  The G slots' loads
+// are in flight at once, and the next ones' rows and weights are looked up
 // under them; d_out, read by all of a token's slots, mostly hits in L1.
-template <typename T, int VB, int U>
+template <typename T, int VB, int U, int G>
 __global__ void __launch_bounds__(kRowThreads) dopt_route_combine_grad_kernel(const __grid_constant__ RowArgs a) {
     using V = typename Raw<VB>::type;
     constexpr int N = VB / int(sizeof(T));
     const int lane = threadIdx.x & 31;
-    const int64_t slots = a.tokens * a.k, stride = int64_t(gridDim.x) * kRowWarps * 2;
-    int64_t s = (int64_t(blockIdx.x) * kRowWarps + (threadIdx.x >> 5)) * 2;
+    const int64_t slots = a.tokens * a.k, stride = int64_t(gridDim.x) * kRowWarps * G;
+    int64_t s = (int64_t(blockIdx.x) * kRowWarps + (threadIdx.x >> 5)) * G;
     let_dependents_start();
     wait_for_grids_before();
-    int next_row[2];
-    float next_weight[2];
+    int next_row[G];
+    float next_weight[G];
     auto look_up = [&](int64_t first) {
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
+        for (int g = 0; g < G; ++g) {
             next_row[g] = first + g < slots ? a.slot_row[first + g] : -1;
             next_weight[g] = first + g < slots ? a.weights[first + g] : 0.0f;
         }
     };
     look_up(s);
     for (; s < slots; s += stride) {
-        int row[2];
-        float w[2], dot[2] = {};
-        const V *d[2], *y[2];
-        V *out[2];
+        int row[G];
+        float w[G], dot[G] = {};
+        const V *d[G], *y[G];
+        V *out[G];
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
+        for (int g = 0; g < G; ++g) {
             row[g] = next_row[g] < a.n_rows ? next_row[g] : -1;
             w[g] = next_weight[g];
             // (slots are below 2^31)
@@ -312,9 +312,9 @@ __global__ void __launch_bounds__(kRowThreads) dopt_route_combine_grad_kernel(co
         }
         look_up(s + stride);
         for (int c0 = lane; c0 < a.vecs; c0 += 32 * U) {
-            V dv[2][U], yv[2][U];
+            V dv[G][U], yv[G][U];
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
+            for (int g = 0; g < G; ++g) {
                 if (row[g] < 0) continue;
 #pragma unroll
                 for (int u = 0; u < U; ++u)
@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(kRowThreads) dopt_route_combine_grad_kernel(co
                     }
             }
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
+            for (int g = 0; g < G; ++g) {
                 if (row[g] < 0) continue;
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(kRowThreads) dopt_route_combine_grad_kernel(co
             }
         }
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
+        for (int g = 0; g < G; ++g) {
 #pragma unroll
             for (int m = 16; m > 0; m >>= 1) dot[g] += __shfl_xor_sync(kFull, dot[g], m);
             if (lane == 0 && s + g < slots) a.d_weights[s + g] = dot[g];  // 0 for a dropped slot
@@ -390,8 +390,8 @@ int launch_dispatch(const char *who, const RowArgs &a, cudaStream_t stream) {
     return launch_op(who, dopt_route_dispatch_kernel<VB, U>, grid, dim3(kRowThreads), 0, stream, a);
 }
 
-// Blocks for `blocks` blocks' work: no more than 16 rounds of 6 an SM's worth
-// (each then takes several tokens in turn).
+// Blocks for `blocks` blocks' work: at most 6 an SM's worth, each taking
+// several tokens in turn.
 unsigned row_blocks(int64_t blocks) { return unsigned(std::min<int64_t>(blocks, 152 * 6)); }
 
 template <typename T, int VB, int U, int A>
@@ -415,19 +415,18 @@ int pick_combine(const char *who, const RowArgs &a, int vb, cudaStream_t stream)
     return DOPT_E_ALIGN;  // not reached: fp32 rows are 4-byte aligned
 }
 
-template <typename T, int VB, int U>
+template <typename T, int VB, int U, int G>
 int launch_combine_grad(const char *who, const RowArgs &a, cudaStream_t stream) {
-    const dim3 grid(row_blocks((a.tokens * a.k + 2 * kRowWarps - 1) / (2 * kRowWarps)));
-    return launch_op(who, dopt_route_combine_grad_kernel<T, VB, U>, grid, dim3(kRowThreads), 0,
-                     stream, a);
+    const dim3 grid(row_blocks((a.tokens * a.k + G * kRowWarps - 1) / (G * kRowWarps)));
+    return launch_op(who, dopt_route_combine_grad_kernel<T, VB, U, G>, grid, dim3(kRowThreads), 0, stream, a);
 }
 
 template <typename T>
 int pick_combine_grad(const char *who, const RowArgs &a, int vb, cudaStream_t stream) {
-    if (vb == 16) return launch_combine_grad<T, 16, 2>(who, a, stream);
-    if (vb == 8) return launch_combine_grad<T, 8, 2>(who, a, stream);
-    if (vb == 4) return launch_combine_grad<T, 4, 4>(who, a, stream);
-    if constexpr (sizeof(T) == 2) return launch_combine_grad<T, 2, 4>(who, a, stream);
+    if (vb == 16) return launch_combine_grad<T, 16, 2, 2>(who, a, stream);
+    if (vb == 8) return launch_combine_grad<T, 8, 4, 1>(who, a, stream);
+    if (vb == 4) return launch_combine_grad<T, 4, 8, 1>(who, a, stream);
+    if constexpr (sizeof(T) == 2) return launch_combine_grad<T, 2, 8, 1>(who, a, stream);
     return DOPT_E_ALIGN;  // not reached: fp32 rows are 4-byte aligned
 }
 

@@ -1,0 +1,66 @@
+#pragma once
+// 16-byte accesses to rows of any alignment.  Rows that are not 16-byte
+// aligned are read and written in the aligned pieces around them: the threads
+// of a row hold neighbouring pieces, take the part that is missing from their
+// neighbour and shift.  Only pieces that reach over the ends of the row
+// (reading) or of the threads' stretch of it (writing) go element by element.
+#include "op_common.cuh"
+
+namespace {
+
+// A 16-byte piece and its successor, shifted down by `bytes` (0..15): the 4
+// words from that byte on.
+__device__ __forceinline__ uint4 shift_down(const uint4 &lo, const uint4 &hi, uint32_t bytes) {
+    uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    if (bytes & 8) {
+#pragma unroll
+        for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+    }
+    if (bytes & 4) {
+#pragma unroll
+        for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+    }
+    const uint32_t bits = (bytes & 3) * 8;
+    return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
+                      __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
+}
+__device__ __forceinline__ uint4 shuffle_down(const uint4 &v, int width) {
+    return make_uint4(__shfl_down_sync(kFull, v.x, 1, width), __shfl_down_sync(kFull, v.y, 1, width),
+                      __shfl_down_sync(kFull, v.z, 1, width), __shfl_down_sync(kFull, v.w, 1, width));
+}
+__device__ __forceinline__ uint4 shuffle_up(const uint4 &v, int width) {
+    return make_uint4(__shfl_up_sync(kFull, v.x, 1, width), __shfl_up_sync(kFull, v.y, 1, width),
+                      __shfl_up_sync(kFull, v.z, 1, width), __shfl_up_sync(kFull, v.w, 1, width));
+}
+
+// The 16 bytes at elements [e, e + 16 / sizeof(T)) of a row of `cols`; those
+// before or past the row are not read (0).
+template <typename T>
+__device__ __forceinline__ uint4 load_piece(const T *row, int e, int cols) {
+    constexpr int N = 16 / int(sizeof(T));
+    if (e >= 0 && e + N <= cols) return __ldcs(reinterpret_cast<const uint4 *>(row + e));
+    using E = typename Raw<int(sizeof(T))>::type;
+    E v[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = e + i >= 0 && e + i < cols ? reinterpret_cast<const E *>(row)[e + i] : E(0);
+    uint4 raw;
+    memcpy(&raw, v, sizeof raw);
+    return raw;
+}
+// The same to elements [e, ...) of which those in [from, to) are written.
+template <typename T>
+__device__ __forceinline__ void store_piece(T *row, int e, int from, int to, const uint4 &raw) {
+    constexpr int N = 16 / int(sizeof(T));
+    if (e >= from && e + N <= to) {
+        __stcs(reinterpret_cast<uint4 *>(row + e), raw);
+        return;
+    }
+    using E = typename Raw<int(sizeof(T))>::type;
+    E v[N];
+    memcpy(v, &raw, sizeof raw);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (e + i >= from && e + i < to) reinterpret_cast<E *>(row)[e + i] = v[i];
+}
+
+}  // namespace

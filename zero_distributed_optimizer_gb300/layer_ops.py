@@ -28,6 +28,9 @@ DOPT_ACT_GELU = 1
 DOPT_ACT_SWIGLU = 2
 DOPT_WGRAD_ACCUMULATE = 1
 
+# torch's query of a device's current stream, without building a Stream object
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
 _CODES = {torch.bfloat16: DOPT_BF16, torch.float32: DOPT_FP32, torch.float16: DOPT_FP16}
 _ACTS = {"silu": DOPT_ACT_SILU, "gelu": DOPT_ACT_GELU, "swiglu": DOPT_ACT_SWIGLU}
 
@@ -72,12 +75,17 @@ def _rows(t, name: str, dtype, shape, index: int):
     return t.data_ptr(), s0 if shape[0] > 1 else shape[1]
 
 
-def _call(index: int, function, *args):
-    if index == torch.cuda.current_device():
-        _check(function(*args[:-1], _stream_handle(args[-1])))
-    else:
+def _call(index: int, stream, function, *args):
+    """function(*args, stream handle) with the tensors' device current."""
+    if index != torch.cuda.current_device():
         with _on(torch.device("cuda", index)):
-            _check(function(*args[:-1], _stream_handle(args[-1])))
+            return _check(function(*args, _stream_handle(stream)))
+    if stream is None and _raw_stream is not None:
+        rc = function(*args, _raw_stream(index))
+    else:
+        rc = function(*args, _stream_handle(stream))
+    if rc:
+        _check(rc)
 
 
 # ---------------------------------------------------------------------------
@@ -112,11 +120,11 @@ def dopt_route_sort(expert_ids, n_experts: int, slot_row, row_token, offsets, wo
     if workspace.get_device() != index or workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
         raise _bad(f"workspace must be a contiguous uint8 tensor on cuda:{index}")
     i32 = torch.int32
-    _call(index, lib().dopt_route_sort, expert_ids.data_ptr(), 8 if wide else 4, tokens, k,
+    _call(index, stream, lib().dopt_route_sort, expert_ids.data_ptr(), 8 if wide else 4, tokens, k,
           n_experts, _dense(slot_row, "slot_row", i32, (tokens, k), index),
           _dense(row_token, "row_token", i32, (tokens * k,), index),
           _dense(offsets, "offsets", i32, (n_experts + 1,), index),
-          workspace.data_ptr(), workspace.numel(), stream)
+          workspace.data_ptr(), workspace.numel())
 
 
 def _check_slot_row(slot_row, index: int):
@@ -138,8 +146,8 @@ def dopt_route_dispatch(x, slot_row, rows, stream=None) -> None:
         raise _bad("rows must be [n_rows, cols]")
     n_rows, cols = rows.shape
     xp, ld = _rows(x, "x", rows.dtype, (tokens, cols), index)
-    _call(index, lib().dopt_route_dispatch, xp, _dtype_code(x.dtype, "x"), tokens, cols, ld, sr, k,
-          _dense(rows, "rows", x.dtype, (n_rows, cols), index), n_rows, stream)
+    _call(index, stream, lib().dopt_route_dispatch, xp, _dtype_code(x.dtype, "x"), tokens, cols, ld, sr, k,
+          _dense(rows, "rows", x.dtype, (n_rows, cols), index), n_rows)
 
 
 def dopt_route_combine(rows, slot_row, weights, out, stream=None) -> None:
@@ -156,8 +164,8 @@ def dopt_route_combine(rows, slot_row, weights, out, stream=None) -> None:
     n_rows, cols = rows.shape
     op, ld = _rows(out, "out", rows.dtype, (tokens, cols), index)
     wp = None if weights is None else _dense(weights, "weights", torch.float32, (tokens, k), index)
-    _call(index, lib().dopt_route_combine, _dense(rows, "rows", rows.dtype, (n_rows, cols), index),
-          _dtype_code(rows.dtype, "rows"), n_rows, sr, wp, tokens, k, cols, op, ld, stream)
+    _call(index, stream, lib().dopt_route_combine, _dense(rows, "rows", rows.dtype, (n_rows, cols), index),
+          _dtype_code(rows.dtype, "rows"), n_rows, sr, wp, tokens, k, cols, op, ld)
 
 
 def dopt_route_combine_grad(d_out, rows, slot_row, weights, d_rows, d_weights, stream=None) -> None:
@@ -171,10 +179,10 @@ def dopt_route_combine_grad(d_out, rows, slot_row, weights, d_rows, d_weights, s
     n_rows, cols = rows.shape
     dt, f32 = rows.dtype, torch.float32
     dp, ld = _rows(d_out, "d_out", dt, (tokens, cols), index)
-    _call(index, lib().dopt_route_combine_grad, dp, ld, _dense(rows, "rows", dt, (n_rows, cols), index),
+    _call(index, stream, lib().dopt_route_combine_grad, dp, ld, _dense(rows, "rows", dt, (n_rows, cols), index),
           _dtype_code(dt, "rows"), n_rows, sr, _dense(weights, "weights", f32, (tokens, k), index),
           tokens, k, cols, _dense(d_rows, "d_rows", dt, (n_rows, cols), index),
-          _dense(d_weights, "d_weights", f32, (tokens, k), index), stream)
+          _dense(d_weights, "d_weights", f32, (tokens, k), index))
 
 
 # ---------------------------------------------------------------------------
@@ -222,8 +230,7 @@ def dopt_ckpt_save(x, ckpt: Checkpoint, stream=None) -> None:
     """Keep x ([rows, cols], contiguous rows, of the checkpoint's type) in `ckpt`."""
     cp, index = _check_ckpt(ckpt)
     xp, ld = _rows(x, "x", ckpt.dtype, (ckpt.rows, ckpt.cols), index)
-    _call(index, lib().dopt_ckpt_save, xp, _dtype_code(x.dtype, "x"), ckpt.rows, ckpt.cols, ld, cp,
-          stream)
+    _call(index, stream, lib().dopt_ckpt_save, xp, _dtype_code(x.dtype, "x"), ckpt.rows, ckpt.cols, ld, cp)
 
 
 def dopt_ckpt_load(ckpt: Checkpoint, out, row_index=None, stream=None) -> None:
@@ -237,8 +244,8 @@ def dopt_ckpt_load(ckpt: Checkpoint, out, row_index=None, stream=None) -> None:
         n = row_index.numel()
         ip = _dense(row_index, "row_index", torch.int32, (n,), index)
     op, ld = _rows(out, "out", out.dtype, (n, ckpt.cols), index)
-    _call(index, lib().dopt_ckpt_load, cp, ckpt.rows, ckpt.cols, ip, n, op,
-          _dtype_code(out.dtype, "out"), ld, stream)
+    _call(index, stream, lib().dopt_ckpt_load, cp, ckpt.rows, ckpt.cols, ip, n, op,
+          _dtype_code(out.dtype, "out"), ld)
 
 
 def dopt_ckpt_act_grad(ckpt: Checkpoint, act: str, d_out, d_in, stream=None) -> None:
@@ -252,8 +259,8 @@ def dopt_ckpt_act_grad(ckpt: Checkpoint, act: str, d_out, d_in, stream=None) -> 
     width = ckpt.cols // 2 if code == DOPT_ACT_SWIGLU else ckpt.cols
     dp, ld = _rows(d_out, "d_out", d_out.dtype, (ckpt.rows, width), index)
     ip, ld_in = _rows(d_in, "d_in", d_out.dtype, (ckpt.rows, ckpt.cols), index)
-    _call(index, lib().dopt_ckpt_act_grad, cp, ckpt.rows, ckpt.cols, code, dp, ld,
-          _dtype_code(d_out.dtype, "d_out"), ip, ld_in, stream)
+    _call(index, stream, lib().dopt_ckpt_act_grad, cp, ckpt.rows, ckpt.cols, code, dp, ld,
+          _dtype_code(d_out.dtype, "d_out"), ip, ld_in)
 
 
 def wgrad_workspace(dy_rows: int, outs: int, cols: int, n_groups: int = 1, device=None):
@@ -295,10 +302,9 @@ def dopt_ckpt_wgrad(ckpt: Checkpoint, dy, grad, grad_offsets, offsets=None, row_
             raise _bad(f"workspace must be a contiguous uint8 tensor on cuda:{index}")
         wp, wn = workspace.data_ptr(), workspace.numel()
     starts = (ctypes.c_int64 * max(n_groups, 1))(*grad_offsets)
-    _call(index, lib().dopt_ckpt_wgrad, cp, _dtype_code(ckpt.dtype, "checkpoint"), ckpt.rows, ckpt.cols,
+    _call(index, stream, lib().dopt_ckpt_wgrad, cp, _dtype_code(ckpt.dtype, "checkpoint"), ckpt.rows, ckpt.cols,
           rp, dp, _dtype_code(dy.dtype, "dy"), dy_rows, outs, ld, op, n_groups, starts, gp,
-          _dtype_code(grad.dtype, "grad"), numel, DOPT_WGRAD_ACCUMULATE if accumulate else 0, wp, wn,
-          stream)
+          _dtype_code(grad.dtype, "grad"), numel, DOPT_WGRAD_ACCUMULATE if accumulate else 0, wp, wn)
 
 
 def wgrad_timeouts(reset: bool = False) -> int:
