@@ -613,8 +613,7 @@ int dopt_step_clipped_noalloc(const dopt_layout *layout, const dopt_adam_cfg *cf
  *
  * Rows: a "row stride" is in elements, at least the row length; pointers
  * need only be aligned to their elements (16-byte aligned rows are the fast
- * ones).  Outputs must not
- * overlap inputs unless stated.
+ * ones).  Outputs must not overlap inputs unless stated.
  * ------------------------------------------------------------------------ */
 
 #define DOPT_MAX_EXPERTS 1024
@@ -792,7 +791,9 @@ int dopt_ckpt_act_grad(const void *ckpt, int64_t rows, int64_t cols, dopt_act ac
  *                 replica of dopt_step
  *   workspace     device, 16-byte aligned, workspace_bytes long, or NULL:
  *                 with room for it, few or short outputs split the rows over
- *                 more blocks and join their fp32 sums in a fixed order.
+ *                 more blocks and join their fp32 sums in a fixed order, and
+ *                 dy whose rows are not 16-byte aligned is first copied into
+ *                 rows that are (without, it is read element by element).
  *                 dopt_ckpt_wgrad_workspace says how much is of use; the
  *                 result depends on the bytes given by rounding only.  Calls
  *                 that share one must not overlap on the GPU.
@@ -809,8 +810,8 @@ int dopt_ckpt_wgrad(const void *ckpt, dopt_dtype ckpt_dtype, int64_t x_rows, int
                     dopt_dtype grad_dtype, int64_t grad_numel, uint32_t flags, void *workspace,
                     int64_t workspace_bytes, cudaStream_t stream);
 
-/* Bytes of workspace that a dopt_ckpt_wgrad of these sizes can make use of
- * (0 where it would not split).  Host only.  Errors: DOPT_E_ARG. */
+/* Bytes of workspace that a dopt_ckpt_wgrad of these sizes and contiguous dy
+ * can make use of (0: none).  Host only.  Errors: DOPT_E_ARG. */
 int dopt_ckpt_wgrad_workspace(int64_t dy_rows, int64_t outs, int64_t cols, int32_t n_groups,
                               int64_t *bytes);
 

@@ -63,4 +63,72 @@ __device__ __forceinline__ void store_piece(T *row, int e, int from, int to, con
         if (e + i >= from && e + i < to) reinterpret_cast<E *>(row)[e + i] = v[i];
 }
 
+// ---------------------------------------------------------------------------
+// COLS values of a row.  All threads of a warp call these together; `lane` is
+// the thread's place among the bx of its row.
+// ---------------------------------------------------------------------------
+
+template <typename T, int COLS>
+struct Values {
+    static constexpr int kPer = 16 / int(sizeof(T));  // elements a piece
+    static constexpr int kPieces = COLS / kPer;
+    uint4 raw[kPieces];
+
+    // Values from column c on; those at or past `cols` (0 where there is no row) are 0.
+    __device__ __forceinline__ void load(const T *row, int c, int cols, bool vec, int lane, int bx) {
+        if (vec) {
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) raw[i] = load_piece(row, c + i * kPer, cols);
+        } else {
+            const uint32_t off = uint32_t(reinterpret_cast<uintptr_t>(row + c) & 15);
+            const int e = c - int(off / sizeof(T));
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) raw[i] = load_piece(row, e + i * kPer, cols);
+            uint4 next = shuffle_down(raw[0], bx);
+            if (lane == bx - 1) next = load_piece(row, e + COLS, cols);
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) raw[i] = shift_down(raw[i], i + 1 < kPieces ? raw[i + 1] : next, off);
+        }
+    }
+
+    __device__ __forceinline__ void get(float (&f)[COLS]) const {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            float g[kPer];
+            unpack<T, 16>(raw[i], g);
+#pragma unroll
+            for (int q = 0; q < kPer; ++q) f[i * kPer + q] = g[q];
+        }
+    }
+    __device__ __forceinline__ void set(const float (&f)[COLS]) {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            float g[kPer];
+#pragma unroll
+            for (int q = 0; q < kPer; ++q) g[q] = f[i * kPer + q];
+            raw[i] = pack<T, 16>(g);
+        }
+    }
+
+    // Values to column c on, those before `cols`.
+    __device__ __forceinline__ void store(T *row, int c, int cols, bool vec, int lane, int bx) const {
+        if (vec) {
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) store_piece(row, c + i * kPer, c, cols, raw[i]);
+        } else {
+            const int from = c - lane * COLS, to = min(cols, from + bx * COLS);  // what the row's threads hold
+            const uint32_t off = uint32_t(reinterpret_cast<uintptr_t>(row + c) & 15);
+            const int e = c - int(off / sizeof(T));
+            const uint4 before = shuffle_up(raw[kPieces - 1], bx);
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i)
+                store_piece(row, e + i * kPer, from, to,
+                            off ? shift_down(i ? raw[i - 1] : before, raw[i], 16 - off) : raw[i]);
+            if (lane == bx - 1 && off)  // the rest of the last thread's values
+                store_piece(row, e + COLS, from, to,
+                            shift_down(raw[kPieces - 1], make_uint4(0, 0, 0, 0), 16 - off));
+        }
+    }
+};
+
 }  // namespace

@@ -6,7 +6,7 @@
 #include <mutex>
 #include <type_traits>
 
-#include "op_common.cuh"
+#include "rows.cuh"
 
 namespace {
 
@@ -706,6 +706,24 @@ __global__ void __launch_bounds__(kTileC) dopt_ckpt_wgrad_join_kernel(const __gr
     store_sums<G>(a, it, it.c0 + column_of(threadIdx.x), it.o0 + o, f, false);
 }
 
+// dy with rows that are not 16-byte aligned, into rows that are (`ld`, a
+// multiple of 8, zeros past the outputs): one pass, which 16384 x 5631 rows
+// repay seven times over.
+template <typename T>
+__global__ void __launch_bounds__(256) dopt_ckpt_wgrad_align_kernel(const T *dy, int64_t dy_ld, int rows, int outs,
+                                                                   T *copy, int64_t ld) {
+    let_dependents_start();
+    wait_for_grids_before();
+    const int lane = threadIdx.x, c = (blockIdx.x * 32 + lane) * 8;
+    for (uint32_t r0 = blockIdx.y * 8; r0 < uint32_t(rows); r0 += gridDim.y * 8) {
+        const uint32_t r = r0 + threadIdx.y;
+        const bool here = r < uint32_t(rows);
+        Values<T, 8> v;
+        v.load(dy + (here ? int64_t(r) * dy_ld : 0), c, here ? outs : 0, false, lane, 32);
+        if (here && c < ld) *reinterpret_cast<uint4 *>(copy + int64_t(r) * ld + c) = v.raw[0];
+    }
+}
+
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
@@ -791,6 +809,18 @@ int set_up(const char *who, EncodeTiled *encode, int *pairs) {
     *encode = g_encode;
     *pairs = g_pairs[device];
     return DOPT_OK;
+}
+
+// Row length, in elements, and bytes of the aligned copy of dy.
+int64_t copy_ld(int64_t outs) { return (outs + 7) / 8 * 8; }
+int64_t copy_bytes(int64_t dy_rows, int64_t outs) { return (dy_rows * copy_ld(outs) * 2 + 15) / 16 * 16; }
+
+template <typename T>
+int align_dy(const char *who, const void *dy, int64_t dy_ld, int64_t dy_rows, int64_t outs, void *copy,
+             cudaStream_t stream) {
+    const dim3 grid(unsigned((copy_ld(outs) + 255) / 256), unsigned(std::min<int64_t>((dy_rows + 7) / 8, 65535)));
+    return launch_op(who, dopt_ckpt_wgrad_align_kernel<T>, grid, dim3(32, 8), 0, stream, static_cast<const T *>(dy),
+                     dy_ld, int(dy_rows), int(outs), static_cast<T *>(copy), copy_ld(outs));
 }
 
 template <typename T, int NB>
@@ -888,11 +918,23 @@ extern "C" int dopt_ckpt_wgrad(const void *ckpt, dopt_dtype ckpt_dtype, int64_t 
     a.dy_ld = dy_ld;
     a.accumulate = (flags & DOPT_WGRAD_ACCUMULATE) != 0;
     a.vec = aligned_to(dy, 16) && dy_ld * 2 % 16 == 0;
+    const int64_t copied = copy_bytes(dy_rows, outs);
+    const bool copy = !a.vec && dy_rows > 0 && workspace_bytes >= copied;
     a.grad_dtype = grad_dtype;
     EncodeTiled encode = nullptr;
     int pairs = 0;
     int rc = set_up(who, &encode, &pairs);
     if (rc != DOPT_OK) return rc;
+    if (copy) {
+        rc = dy_dtype == DOPT_BF16 ? align_dy<__nv_bfloat16>(who, dy, dy_ld, dy_rows, outs, workspace, stream)
+                                   : align_dy<__half>(who, dy, dy_ld, dy_rows, outs, workspace, stream);
+        if (rc != DOPT_OK) return rc;
+        dy = a.dy = workspace;
+        dy_ld = a.dy_ld = copy_ld(outs);
+        a.vec = 1;
+        workspace = static_cast<char *>(workspace) + copied;
+        workspace_bytes -= copied;
+    }
     if (a.vec && dy_rows > 0) {  // 16-byte aligned rows go by TMA
         const cuuint64_t dims[2] = {cuuint64_t(outs), cuuint64_t(dy_rows)};
         const cuuint64_t strides[1] = {cuuint64_t(dy_ld) * 2};
@@ -933,7 +975,8 @@ extern "C" int dopt_ckpt_wgrad_workspace(int64_t dy_rows, int64_t outs, int64_t 
                           static_cast<long long>(cols), n_groups);
     // for a device of 76 pairs of SMs; a call takes what it is given
     const Plan plan = plan_wgrad(outs, cols, n_groups, dy_rows, 76, INT64_MAX);
-    *bytes = plan.tail * plan.parts * slot_floats(plan.nb) * int64_t(sizeof(float));
+    *bytes = plan.tail * plan.parts * slot_floats(plan.nb) * int64_t(sizeof(float)) +
+             (outs % 8 != 0 ? copy_bytes(dy_rows, outs) : 0);
     return DOPT_OK;
 }
 
