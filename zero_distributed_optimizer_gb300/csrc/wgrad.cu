@@ -21,7 +21,7 @@ namespace {
 //       group's last step, whose rows past the group must read as zeros
 //       whatever the next group holds there, and where rows are not 16-byte
 //       aligned
-//   x   16 warps load 8 codes a thread and row into registers, widen them to
+//   x   16 warps load 16 codes a thread and row into registers, widen them to
 //       16 bits (exactly) and store them swizzled (a ring of 4 steps).  Four
 //       warps take a step, so that one step's waits, stores and fence run
 //       under another's conversions; a warp loads its next step's codes after
@@ -572,9 +572,11 @@ __global__ void __launch_bounds__(kWgradThreads, 1) __cluster_dims__(2, 1, 1)
         }
     } else {
         // x: group g takes steps g, g + 4, ... of all the pair's steps; a warp 16
-        // rows of a step, two at a time, a thread 8 columns: chunk q of rows
-        // 2 w + lane / 16 + 8 h
-        const int w = warp & 3, q = lane & 15;
+        // rows of a step, a thread 16 columns of four of them: rows 4 w + r +
+        // 16 h, columns c16 on.  Eight lanes' chunks, of two neighbouring rows
+        // in one slab, fall into different banks.
+        const int w = warp & 3, r = ((lane >> 2) & 1) + 2 * (lane >> 4);
+        const int c16 = 64 * ((lane >> 3) & 1) + 16 * (lane & 3);
         struct {
             WgradItem it;
             int k, i, n, u;  // the round, the step in its item; the step and block of dy of all
@@ -595,54 +597,70 @@ __global__ void __launch_bounds__(kWgradThreads, 1) __cluster_dims__(2, 1, 1)
             }
             return true;
         };
-        uint2 code[8];
-        uint32_t exp[8];
-        constexpr int kNone = INT32_MIN;  // the token of a row that counts as zeros
-        int tokens = kNone;
-        // the token of row 2 w + (l & 1) + 8 (l / 2) of the step, in lane l
+        uint4 code[4];
+        uint32_t exp[4];
+        int tokens = -1;
+        uint32_t absent = 0;  // bit r + 4 h: that row counts as zeros
+        // the token of row 4 w + (l & 3) + 16 (l / 4) of the step, in lane l
         auto load_tokens = [&]() {
-            const int r = at.i * kK + 2 * w + (lane & 1) + 4 * (lane & 14);
-            tokens = kNone;
-            if (r < at.it.rows && lane < 16) tokens = a.row_token ? a.row_token[at.it.lo + r] : at.it.lo + r;
+            const int k = at.i * kK + 4 * w + (lane & 3) + 4 * (lane & 12);
+            tokens = -1;
+            if (k < at.it.rows && lane < 16) tokens = a.row_token ? a.row_token[at.it.lo + k] : at.it.lo + k;
         };
         const uint32_t pitch = uint32_t(a.pitch);
         auto load_codes = [&]() {
             const int c = at.it.c0 + int(rank) * (kTileC / 2);
             if (c >= a.pitch || a.x_rows <= 0) {  // no such columns, or no rows: zeros
 #pragma unroll
-                for (int h = 0; h < 8; ++h) code[h] = make_uint2(0, 0), exp[h] = 0;
+                for (int h = 0; h < 4; ++h) code[h] = make_uint4(0, 0, 0, 0);
+                absent = 0xffff;
                 return;
             }
-            const unsigned char *codes = a.codes + (c + q * 8), *scales = a.scales + (c / kBlock + (q >> 2));
-            const int mine = uint32_t(tokens) < uint32_t(a.x_rows) ? tokens : kNone;
+            const unsigned char *codes = a.codes + (c + c16), *scales = a.scales + (c + c16) / kBlock;
+            const bool there = uint32_t(tokens) < uint32_t(a.x_rows);
+            absent = __ballot_sync(kFull, !there);
+            const uint32_t mine = there ? uint32_t(tokens) : 0;  // (an absent row reads row 0)
 #pragma unroll
-            for (int h = 0; h < 8; ++h) {  // (a row that counts as zeros reads row 0 and exponent 0)
-                const int t = __shfl_sync(kFull, mine, 2 * h + (lane >> 4));
-                const uint32_t row = uint32_t(t) & 0x7fffffffu;
-                code[h] = __ldg(reinterpret_cast<const uint2 *>(codes + uint64_t(row) * pitch));
-                exp[h] = __ldg(scales + uint64_t(row) * (pitch / kBlock));
-                if (t < 0) exp[h] = 0;
+            for (int h = 0; h < 4; ++h) {
+                const uint64_t row = __shfl_sync(kFull, mine, r + 4 * h);
+                code[h] = __ldg(reinterpret_cast<const uint4 *>(codes + row * pitch));
+                exp[h] = __ldg(scales + row * (pitch / kBlock));
             }
         };
         at.it = item_of<NB>(a, groups, item_number(a, 0));
         bool more = advance(warp >> 2);
         if (more) load_tokens(), load_codes();
-        // 8 rows on: 1024 bytes on, and the swizzle is the same
-        unsigned char *my_stage = x_ring + stage_chunk(2 * w + (lane >> 4), q);
+        // 16 rows on: 2048 bytes on, and the swizzle is the same
+        const uint32_t chunk0 = stage_chunk(4 * w + r, c16 / 8), chunk1 = stage_chunk(4 * w + r, c16 / 8 + 1);
         bool ok = true;
         while (more) {
             const int s = at.n % kXRing;
-            unsigned char *stage = my_stage + s * kStage;
+            unsigned char *stage = x_ring + s * kStage;
+            if (absent & 0xffff) {
+#pragma unroll
+                for (int h = 0; h < 4; ++h)
+                    if (absent >> (r + 4 * h) & 1) exp[h] = 0;
+            }
             uint4 v[4];
 #pragma unroll
-            for (int h = 0; h < 4; ++h) v[h] = widen(T(), code[h], exp[h]);
+            for (int h = 0; h < 2; ++h) {
+                v[2 * h] = widen(T(), make_uint2(code[h].x, code[h].y), exp[h]);
+                v[2 * h + 1] = widen(T(), make_uint2(code[h].z, code[h].w), exp[h]);
+            }
             if (at.n >= kXRing) ok = wait_phase(b, b.x_empty[s], uint32_t(at.n / kXRing - 1) & 1);
             if (!__all_sync(kFull, ok)) break;
 #pragma unroll
-            for (int h = 0; h < 4; ++h) *reinterpret_cast<uint4 *>(stage + h * 1024) = v[h];
+            for (int h = 0; h < 2; ++h) {
+                *reinterpret_cast<uint4 *>(stage + chunk0 + h * 2048) = v[2 * h];
+                *reinterpret_cast<uint4 *>(stage + chunk1 + h * 2048) = v[2 * h + 1];
+            }
 #pragma unroll
-            for (int h = 4; h < 8; ++h)
-                *reinterpret_cast<uint4 *>(stage + h * 1024) = widen(T(), code[h], exp[h]);
+            for (int h = 2; h < 4; ++h) {
+                *reinterpret_cast<uint4 *>(stage + chunk0 + h * 2048) =
+                    widen(T(), make_uint2(code[h].x, code[h].y), exp[h]);
+                *reinterpret_cast<uint4 *>(stage + chunk1 + h * 2048) =
+                    widen(T(), make_uint2(code[h].z, code[h].w), exp[h]);
+            }
             if (!a.tma || at.i >= at.it.full) {
                 // the step's dy too: its slots' last products are done, since
                 // those of the step that x_empty was waited for are
