@@ -109,12 +109,17 @@ __device__ __forceinline__ bool try_phase(uint32_t bar, uint32_t parity) {
         : "memory");
     return done != 0;
 }
+// (Warps that poll take issue slots from those that work: where a wait is
+// long and its end not urgent, they sleep between two tries.)
+template <int SLEEP_NS>
 __device__ __noinline__ bool wait_long(WgradBarriers &b, uint32_t bar, uint32_t parity) {
     unsigned long long t0, now;
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
     for (;;) {
-        for (int i = 0; i < 64; ++i)
+        for (int i = 0; i < 64; ++i) {
             if (try_phase(bar, parity)) return true;
+            if (SLEEP_NS > 0) __nanosleep(SLEEP_NS);
+        }
         if (*static_cast<volatile int32_t *>(&b.failed)) return false;
         asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
         if (now - t0 > kWaitNs) {
@@ -123,11 +128,12 @@ __device__ __noinline__ bool wait_long(WgradBarriers &b, uint32_t bar, uint32_t 
         }
     }
 }
+template <int SLEEP_NS = 0>
 __device__ __forceinline__ bool wait_phase(WgradBarriers &b, unsigned long long &bar, uint32_t parity) {
     const uint32_t at = smem_of(&bar);
-    for (int i = 0; i < 16; ++i)
+    for (int i = 0; i < (SLEEP_NS > 0 ? 1 : 16); ++i)
         if (try_phase(at, parity)) return true;
-    return wait_long(b, at, parity);
+    return wait_long<SLEEP_NS>(b, at, parity);
 }
 
 // Wait for the last of `uses` uses of each slot of a ring.
@@ -172,8 +178,7 @@ __device__ __forceinline__ uint32_t stage_chunk(int k, int q) {
 }
 
 // Rows of operand A are columns c in the order 0 2 1 3, 4 6 5 7, ...: the
-// bytes 0 and 2 of a word of codes, and 1 and 3, are then its pairs, without
-// a permutation of bytes.
+// bytes 0 and 2 of a word of codes, and 1 and 3, are then its pairs.
 __device__ __forceinline__ int column_of(int m) { return (m & ~3) | ((m & 1) << 1) | ((m >> 1) & 1); }
 
 // 8 codes to 8 values of 16 bits, exactly: code * 2^k has 7 significant
@@ -186,8 +191,8 @@ __device__ __forceinline__ uint4 widen(__nv_bfloat16, const uint2 &w, uint32_t b
     uint32_t o[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t pair = (i < 2 ? w.x : w.y) >> (i & 1 ? 8 : 0);
-        const uint32_t m = (pair & 0x007f007fu) | 0x43004300u, s = (pair & 0x00800080u) | 0x43004300u;
+        const uint32_t pair = __byte_perm(i < 2 ? w.x : w.y, 0x43434343u, i & 1 ? 0x4341 : 0x4240);
+        const uint32_t m = pair & 0xff7fff7fu, s = pair & 0xff80ff80u;
         uint32_t code;
         asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(code) : "r"(s), "r"(0xbf80bf80u), "r"(m));      // m - s
         asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(o[i]) : "r"(code), "r"(step), "r"(0x80008000u));  // times step
@@ -196,10 +201,11 @@ __device__ __forceinline__ uint4 widen(__nv_bfloat16, const uint2 &w, uint32_t b
 }
 __device__ __forceinline__ uint4 widen(__half, const uint2 &w, uint32_t byte) {
     const __half2 step = __float2half2_rn(__uint_as_float(byte << 23));
+    const uint2 u = make_uint2(w.x ^ 0x80808080u, w.y ^ 0x80808080u);
     uint32_t o[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t pair = (((i < 2 ? w.x : w.y) >> (i & 1 ? 8 : 0)) & 0x00ff00ffu) ^ 0x64806480u;
+        const uint32_t pair = __byte_perm(i < 2 ? u.x : u.y, 0x64646464u, i & 1 ? 0x4341 : 0x4240);
         const __half2 q = __hsub2(*reinterpret_cast<const __half2 *>(&pair), __float2half2_rn(1152.0f));
         const __half2 v = __hmul2(q, step);
         o[i] = *reinterpret_cast<const uint32_t *>(&v);
@@ -432,7 +438,7 @@ __global__ void __launch_bounds__(kWgradThreads, 1) __cluster_dims__(2, 1, 1)
                 for (int nb = 0; nb < NB; ++nb) {
                     if (nb >= blocks) break;
                     const int s = u % kDyRing;
-                    if (u >= kDyRing) ok = __all_sync(kFull, wait_phase(b, b.dy_empty[s], uint32_t(u / kDyRing - 1) & 1));
+                    if (u >= kDyRing) ok = __all_sync(kFull, wait_phase<64>(b, b.dy_empty[s], uint32_t(u / kDyRing - 1) & 1));
                     if (!ok) break;
                     if (elect_one()) {
                         const uint32_t full = smem_of(&b.dy_full[s]);
@@ -541,7 +547,7 @@ __global__ void __launch_bounds__(kWgradThreads, 1) __cluster_dims__(2, 1, 1)
             const WgradItem it = item_of<NB>(a, groups, item);
             const int buffer = NB == 1 ? t & 1 : 0, use = NB == 1 ? t >> 1 : t;
             if (it.steps > 0) {
-                ok = wait_phase(b, b.sum_full[buffer], uint32_t(use) & 1);
+                ok = wait_phase<200>(b, b.sum_full[buffer], uint32_t(use) & 1);
                 if (!__all_sync(kFull, ok)) break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             }
@@ -647,7 +653,7 @@ __global__ void __launch_bounds__(kWgradThreads, 1) __cluster_dims__(2, 1, 1)
                 v[2 * h] = widen(T(), make_uint2(code[h].x, code[h].y), exp[h]);
                 v[2 * h + 1] = widen(T(), make_uint2(code[h].z, code[h].w), exp[h]);
             }
-            if (at.n >= kXRing) ok = wait_phase(b, b.x_empty[s], uint32_t(at.n / kXRing - 1) & 1);
+            if (at.n >= kXRing) ok = wait_phase<32>(b, b.x_empty[s], uint32_t(at.n / kXRing - 1) & 1);
             if (!__all_sync(kFull, ok)) break;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
