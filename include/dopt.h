@@ -623,7 +623,7 @@ int dopt_step_clipped_noalloc(const dopt_layout *layout, const dopt_adam_cfg *cf
 
 /*
  * Bytes of workspace that dopt_route_sort needs for these sizes (0 up to
- * 4096 slots).  Host only.  Errors: DOPT_E_ARG.
+ * 32768 slots).  Host only.  Errors: DOPT_E_ARG.
  */
 int dopt_route_workspace(int64_t tokens, int32_t k, int32_t n_experts, int64_t *bytes);
 

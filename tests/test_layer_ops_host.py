@@ -33,8 +33,8 @@ def test_sizes(lib):
         with pytest.raises(dopt.DoptError):
             dopt.ckpt_bytes(rows, cols)
     n = ctypes.c_int64(-1)
-    assert lib.dopt_route_workspace(4096, 1, 8, ctypes.byref(n)) == 0 and n.value == 0
-    assert lib.dopt_route_workspace(4097, 1, 8, ctypes.byref(n)) == 0 and n.value > 0
+    assert lib.dopt_route_workspace(4096, 8, 8, ctypes.byref(n)) == 0 and n.value == 0
+    assert lib.dopt_route_workspace(4097, 8, 8, ctypes.byref(n)) == 0 and n.value > 0
     _refused(lib, lib.dopt_route_workspace(1, 0, 8, ctypes.byref(n)), B.DOPT_E_ARG, "dopt_route_workspace")
     _refused(lib, lib.dopt_route_workspace(1, 1, 0, ctypes.byref(n)), B.DOPT_E_ARG, "n_experts")
     _refused(lib, lib.dopt_ckpt_wgrad_workspace(-1, 1, 1, 1, ctypes.byref(n)), B.DOPT_E_ARG, "wgrad_workspace")
@@ -50,7 +50,7 @@ def test_sizes(lib):
     (dict(offsets=0), B.DOPT_E_ARG, "offsets"), (dict(ws=0), B.DOPT_E_ARG, "workspace"),
     (dict(ws_bytes=8), B.DOPT_E_ARG, "workspace of 8 bytes")])
 def test_sort_refusals(lib, change, code, text):
-    a = dict(ids=P, id_bytes=8, tokens=5000, k=2, experts=8, slot_row=P, row_token=P, offsets=P, ws=P,
+    a = dict(ids=P, id_bytes=8, tokens=600000, k=2, experts=8, slot_row=P, row_token=P, offsets=P, ws=P,
              ws_bytes=1 << 20)
     a.update(change)
     _refused(lib, lib.dopt_route_sort(*a.values(), None), code, text)

@@ -44,6 +44,25 @@ def test_sort(tokens, k, experts, wide, kind):
         assert np.array_equal(a.cpu().numpy(), b)
 
 
+@pytest.mark.parametrize("tokens,k,experts", [
+    (4096, 8, 1024), (16384, 2, 300), (16385, 2, 300), (524288, 2, 64), (400000, 3, 1024), (262145, 4, 7),
+    (700000, 2, 5), (1300000, 3, 900)])
+def test_sort_many_slots(tokens, k, experts):
+    """One block of the sort, its cluster, and tiles in two launches, against a stable sort."""
+    g = torch.Generator(device=DEV).manual_seed(tokens)
+    ids = torch.randint(-1, experts + 1, (tokens, k), generator=g, device=DEV)
+    slot_row, row_token, offsets = _sort(ids, experts)
+    flat = ids.reshape(-1)
+    key = torch.where((flat >= 0) & (flat < experts), flat, experts)
+    key, order = torch.sort(key, stable=True)
+    n = int((key < experts).sum())
+    assert torch.equal(row_token[:n], (order[:n] // k).int()) and torch.all(row_token[n:] == -1)
+    want = torch.full((tokens * k,), -1, dtype=torch.int32, device=DEV)
+    want[order[:n]] = torch.arange(n, dtype=torch.int32, device=DEV)
+    assert torch.equal(slot_row.view(-1), want)
+    assert torch.equal(offsets, torch.searchsorted(key, torch.arange(experts + 1, device=DEV)).int())
+
+
 def _rows(n, cols, dtype, layout, g):
     """A [n, cols] tensor: contiguous, with a longer row stride, or starting
     one element into its storage."""

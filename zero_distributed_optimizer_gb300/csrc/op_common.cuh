@@ -123,24 +123,33 @@ inline uint64_t address_bits(const void *p) { return reinterpret_cast<uintptr_t>
 // the kernels launched this way execute griddepcontrol.wait before their
 // first access to memory.
 template <typename... KArgs, typename... Args>
-int launch_op(const char *who, void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
-              cudaStream_t stream, const Args &...args) {
+int launch_cluster(const char *who, void (*kernel)(KArgs...), dim3 grid, unsigned cluster, dim3 block, size_t smem,
+                   cudaStream_t stream, const Args &...args) {
     cudaLaunchConfig_t lc = {};
     lc.gridDim = grid;
     lc.blockDim = block;
     lc.dynamicSmemBytes = smem;
     lc.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     lc.attrs = attr;
-    lc.numAttrs = 1;
+    lc.numAttrs = cluster > 0 ? 2 : 1;
     cudaError_t e = cudaLaunchKernelEx(&lc, kernel, KArgs(args)...);
     if (e != cudaSuccess) {
         cudaGetLastError();
         return dopt::fail(DOPT_E_CUDA, "%s: launch: %s", who, cudaGetErrorString(e));
     }
     return DOPT_OK;
+}
+// (cluster 0: as the kernel was compiled)
+template <typename... KArgs, typename... Args>
+int launch_op(const char *who, void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+              const Args &...args) {
+    return launch_cluster(who, kernel, grid, 0, block, smem, stream, args...);
 }
 
 __device__ __forceinline__ void wait_for_grids_before() {

@@ -10,24 +10,39 @@ namespace {
 // ---------------------------------------------------------------------------
 // Sort.  Slots in order; bin e < E is expert e, bin E the dropped slots.  A
 // slot's row is the number of slots in lower bins plus the number of earlier
-// slots of its own bin: counts per tile of 4096 slots, then, inside a tile,
-// counts per warp, so that every prefix is a sum of integers and the order
-// inside a bin is the slots' order (stable, the same at every call).  Up to
-// one tile of slots takes one launch of one CTA; more take a launch that
-// counts the tiles and one that places them.
+// slots of its own bin, so the order inside a bin is the slots' order (stable,
+// the same at every call).  Every prefix is a sum of integers.
+//
+// Up to 2^15 slots: one launch of one cluster of 8 blocks (one block up to
+// 4096 slots).  Blocks, and warps in a block, take consecutive stretches; a
+// warp counts its slots by bin, 32 at a time, the counts become first rows by
+// a scan over the warps, over the blocks (through the cluster's shared
+// memory) and over the bins, and the warp goes through its slots again.
+// More slots: a launch that counts stretches of 4096 slots (of more above
+// 304 * 4096, so that there are at most 304 of them) and one that places
+// them, each block adding up the stretches before it.  2^18 slots of 64 experts:
+// 41 us in the cluster (its 8 SMs store to a sector a slot), 4.8 + 10.1 us in
+// the two launches; sorting 2^15 slots of 64 experts and copying their 2048
+// bf16 columns takes 40.4 us with the cluster, 42.5 us with the two.
+// (Putting a tile's rows in order in shared memory before they are stored
+// changed nothing: 10.1 us.)
 // ---------------------------------------------------------------------------
 
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortRounds = 4;  // slots a thread takes
+constexpr int kSortRounds = 4;  // slots a thread takes at a time
 constexpr int64_t kSortTile = int64_t(kSortThreads) * kSortRounds;
+constexpr int kSortCluster = 8;
+constexpr int64_t kClusterSlots = int64_t(1) << 15;
+constexpr int64_t kSortMaxTiles = 304;
 
 struct SortArgs {
     const void *ids;
     int32_t *slot_row, *row_token, *offsets;
     int32_t *counts;  // [tiles][bins]
     int32_t slots, k, experts, tiles;
-    int32_t wide;  // 64-bit ids
+    int32_t rounds;  // of 4096 slots, a tile
+    int32_t wide;    // 64-bit ids
 };
 
 __device__ __forceinline__ int bin_of(const SortArgs &a, int64_t slot) {
@@ -36,121 +51,221 @@ __device__ __forceinline__ int bin_of(const SortArgs &a, int64_t slot) {
     return id >= 0 && id < a.experts ? int(id) : a.experts;
 }
 
-__global__ void __launch_bounds__(kSortThreads) dopt_route_count_kernel(const SortArgs a) {
+// This lane's slot among its warp's 32: how many slots of its bin came before
+// it; count[] moves on.  The lanes of a bin are those that agree in every one
+// of its `bits` bits, a ballot each (a match instruction costs an SM some 60
+// cycles a warp: with it a cluster sorted 262144 slots in 62 us).
+__device__ __forceinline__ int rank_in_warp(int bin, int bits, int lane, int32_t *count) {
+    unsigned peers = __ballot_sync(kFull, bin >= 0);
+    for (int b = 0; b < bits; ++b) {
+        const bool set = bin >> b & 1;
+        const unsigned with = __ballot_sync(kFull, set);
+        peers &= set ? with : ~with;
+    }
+    const int before = __popc(peers & ((1u << lane) - 1u));
+    const int at = bin >= 0 ? count[bin] + before : 0;
+    __syncwarp();
+    if (bin >= 0 && before == 0) count[bin] = at + __popc(peers);
+    __syncwarp();
+    return at;
+}
+
+__device__ __forceinline__ int inclusive_scan(int v, int lane) {
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(kFull, v, d);
+        if (lane >= d) v += o;
+    }
+    return v;
+}
+
+// base[b] += the sum of total[0..b); written to `offsets` too unless NULL.
+// By all threads of the block.
+__device__ __forceinline__ void scan_bins(const int32_t *total, int32_t *base, int bins, int32_t *offsets,
+                                          int32_t (&warp_sum)[kSortWarps]) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int carry = 0;
+    for (int b0 = 0; b0 < bins; b0 += kSortThreads) {
+        const int b = b0 + int(threadIdx.x);
+        const int v = b < bins ? total[b] : 0;
+        const int incl = inclusive_scan(v, lane);
+        if (lane == 31) warp_sum[warp] = incl;
+        __syncthreads();
+        if (warp == 0) warp_sum[lane] = inclusive_scan(warp_sum[lane], lane);
+        __syncthreads();
+        const int excl = carry + incl - v + (warp ? warp_sum[warp - 1] : 0);
+        if (b < bins) {
+            base[b] += excl;
+            if (offsets) offsets[b] = excl;
+        }
+        carry += warp_sum[kSortWarps - 1];
+        __syncthreads();
+    }
+}
+
+// Shared memory: total[bins], base[bins], then counts [32 warps][bins].
+__global__ void __launch_bounds__(kSortThreads) dopt_route_sort_kernel(const __grid_constant__ SortArgs a) {
+    extern __shared__ int32_t smem[];
+    __shared__ int32_t warp_sum[kSortWarps];
+    const int bins = a.experts + 1;
+    int32_t *total = smem, *base = smem + bins, *count = smem + 2 * bins;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, bits = 32 - __clz(a.experts);
+    const int blocks = int(gridDim.x), block = int(blockIdx.x);  // the grid is the cluster
+    let_dependents_start();
+    for (int i = threadIdx.x; i < kSortWarps * bins; i += kSortThreads) count[i] = 0;
+    wait_for_grids_before();
+    __syncthreads();
+
+    // this warp's slots: whole rounds of 32 * kSortRounds
+    constexpr int kRound = 32 * kSortRounds;
+    const int64_t rounds = (a.slots + int64_t(kRound) * kSortWarps * blocks - 1) / (int64_t(kRound) * kSortWarps * blocks);
+    const int64_t first = (int64_t(block) * kSortWarps + warp) * rounds * kRound;
+    int32_t *mine = count + warp * bins;
+    auto load = [&](int64_t round, int (&bin)[kSortRounds]) {
+#pragma unroll
+        for (int q = 0; q < kSortRounds; ++q) {
+            const int64_t s = first + round * kRound + q * 32 + lane;
+            bin[q] = round < rounds && s < a.slots ? bin_of(a, s) : -1;
+        }
+    };
+    int bin[kSortRounds], next[kSortRounds];
+    load(0, next);
+    for (int64_t r = 0; r < rounds; ++r) {
+#pragma unroll
+        for (int q = 0; q < kSortRounds; ++q) bin[q] = next[q];
+        load(r + 1, next);
+#pragma unroll
+        for (int q = 0; q < kSortRounds; ++q)
+            if (bin[q] >= 0) atomicAdd(&mine[bin[q]], 1);
+    }
+    load(0, next);  // for the second time through, under the scans
+    __syncthreads();
+    for (int b = warp; b < bins; b += kSortWarps) {  // lane l: warp l's count
+        const int c = count[lane * bins + b], incl = inclusive_scan(c, lane);
+        count[lane * bins + b] = incl - c;
+        if (lane == 31) total[b] = incl;
+    }
+    __syncthreads();
+    if (blocks > 1) {
+        asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+        for (int b = threadIdx.x; b < bins; b += kSortThreads) {
+            const uint32_t own = static_cast<uint32_t>(__cvta_generic_to_shared(&total[b]));
+            int before = 0, all = 0;
+            for (int o = 0; o < blocks; ++o) {
+                uint32_t at;
+                int32_t v;
+                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(own), "r"(o));
+                asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+                if (o < block) before += v;
+                all += v;
+            }
+            base[b] = before;
+            smem[(2 + kSortWarps) * bins + b] = all;
+        }
+        // the others' totals have been read before any of them goes
+        asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+        total = smem + (2 + kSortWarps) * bins;
+    } else {
+        for (int b = threadIdx.x; b < bins; b += kSortThreads) base[b] = 0;
+    }
+    __syncthreads();
+    scan_bins(total, base, bins, block == 0 ? a.offsets : nullptr, warp_sum);
+    for (int64_t r = 0; r < rounds; ++r) {
+#pragma unroll
+        for (int q = 0; q < kSortRounds; ++q) bin[q] = next[q];
+        load(r + 1, next);
+#pragma unroll
+        for (int q = 0; q < kSortRounds; ++q) {
+            const int row = rank_in_warp(bin[q], bits, lane, mine);
+            if (bin[q] < 0) continue;
+            const int64_t s = first + r * kRound + q * 32 + lane;
+            const bool kept = bin[q] < a.experts;
+            a.slot_row[s] = kept ? base[bin[q]] + row : -1;
+            a.row_token[base[bin[q]] + row] = kept ? int32_t(s / a.k) : -1;
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kSortThreads) dopt_route_count_kernel(const __grid_constant__ SortArgs a) {
     extern __shared__ int32_t hist[];
     const int bins = a.experts + 1;
     let_dependents_start();
     for (int b = threadIdx.x; b < bins; b += kSortThreads) hist[b] = 0;
     wait_for_grids_before();
     __syncthreads();
+    for (int round = 0; round < a.rounds; ++round) {
+        const int64_t s0 = (int64_t(blockIdx.x) * a.rounds + round) * kSortTile + threadIdx.x;
 #pragma unroll
-    for (int r = 0; r < kSortRounds; ++r) {
-        const int64_t s = blockIdx.x * kSortTile + r * kSortThreads + threadIdx.x;
-        if (s < a.slots) atomicAdd(&hist[bin_of(a, s)], 1);
+        for (int r = 0; r < kSortRounds; ++r)
+            if (s0 + r * kSortThreads < a.slots) atomicAdd(&hist[bin_of(a, s0 + r * kSortThreads)], 1);
     }
     __syncthreads();
     for (int b = threadIdx.x; b < bins; b += kSortThreads)
         a.counts[int64_t(blockIdx.x) * bins + b] = hist[b];
 }
 
-// Shared memory: base[bins], then per-warp counts [32][bins] of 16 bits (a
-// tile has 4096 slots).
-__global__ void __launch_bounds__(kSortThreads) dopt_route_place_kernel(const SortArgs a) {
+// Shared memory as above.
+__global__ void __launch_bounds__(kSortThreads) dopt_route_place_kernel(const __grid_constant__ SortArgs a) {
     extern __shared__ int32_t smem[];
     __shared__ int32_t warp_sum[kSortWarps];
     const int bins = a.experts + 1;
-    int32_t *total = smem, *base = smem + bins;
-    uint16_t *cnt = reinterpret_cast<uint16_t *>(smem + 2 * bins);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int32_t *total = smem, *base = smem + bins, *count = smem + 2 * bins;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, bits = 32 - __clz(a.experts);
     let_dependents_start();
     for (int b = threadIdx.x; b < bins; b += kSortThreads) total[b] = base[b] = 0;
-    for (int i = threadIdx.x; i < kSortWarps * bins; i += kSortThreads) cnt[i] = 0;
+    for (int i = threadIdx.x; i < kSortWarps * bins; i += kSortThreads) count[i] = 0;
     wait_for_grids_before();
     __syncthreads();
-
-    // this warp's 128 slots, 32 at a time: each slot's rank among the warp's slots of its bin
     int bin[kSortRounds], rank[kSortRounds];
-    const int64_t s0 = blockIdx.x * kSortTile + int64_t(warp) * 32 * kSortRounds + lane;
+    auto take = [&](int64_t s0) {
 #pragma unroll
-    for (int r = 0; r < kSortRounds; ++r) bin[r] = s0 + 32 * r < a.slots ? bin_of(a, s0 + 32 * r) : -1;
+        for (int r = 0; r < kSortRounds; ++r) bin[r] = s0 + 32 * r < a.slots ? bin_of(a, s0 + 32 * r) : -1;
 #pragma unroll
-    for (int r = 0; r < kSortRounds; ++r) {
-        const unsigned peers = __match_any_sync(kFull, bin[r]);
-        const int before = __popc(peers & ((1u << lane) - 1u));
-        if (bin[r] >= 0) rank[r] = cnt[warp * bins + bin[r]] + before;
-        __syncwarp();
-        if (bin[r] >= 0 && before == 0) cnt[warp * bins + bin[r]] += uint16_t(__popc(peers));
-        __syncwarp();
-    }
-    if (a.tiles > 1) {  // slots of each bin in all tiles, and in the tiles before this one
-        const int n = a.tiles * bins, mine = int(blockIdx.x) * bins;
-        for (int i0 = threadIdx.x; i0 < n; i0 += 4 * kSortThreads) {
-            int32_t c[4];
+        for (int r = 0; r < kSortRounds; ++r) rank[r] = rank_in_warp(bin[r], bits, lane, count + warp * bins);
+    };
+    int64_t s0 = int64_t(blockIdx.x) * a.rounds * kSortTile + int64_t(warp) * 32 * kSortRounds + lane;
+    take(s0);
+    // slots of each bin in all tiles, and in the tiles before this one
+    const int n = a.tiles * bins, mine = int(blockIdx.x) * bins;
+    for (int i0 = threadIdx.x; i0 < n; i0 += 4 * kSortThreads) {
+        int32_t c[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) c[j] = i0 + j * kSortThreads < n ? a.counts[i0 + j * kSortThreads] : 0;
+        for (int j = 0; j < 4; ++j) c[j] = i0 + j * kSortThreads < n ? a.counts[i0 + j * kSortThreads] : 0;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int i = i0 + j * kSortThreads;
-                if (c[j]) {
-                    atomicAdd(&total[i % bins], c[j]);
-                    if (i < mine) atomicAdd(&base[i % bins], c[j]);
-                }
+        for (int j = 0; j < 4; ++j) {
+            const int i = i0 + j * kSortThreads;
+            if (c[j]) {
+                atomicAdd(&total[i % bins], c[j]);
+                if (i < mine) atomicAdd(&base[i % bins], c[j]);
             }
         }
     }
     __syncthreads();
-    // the warps' counts become the slots of the bin in the warps before
-    for (int b = warp; b < bins; b += kSortWarps) {  // lane l: warp l's count
-        const int c = cnt[lane * bins + b];
-        int incl = c;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int o = __shfl_up_sync(kFull, incl, d);
-            if (lane >= d) incl += o;
-        }
-        cnt[lane * bins + b] = uint16_t(incl - c);
-        if (a.tiles == 1 && lane == 31) total[b] = incl;
-    }
-    __syncthreads();
-    // base += slots in lower bins (an exclusive scan of total over the bins)
-    int carry = 0;
-    for (int b0 = 0; b0 < bins; b0 += kSortThreads) {
-        const int b = b0 + int(threadIdx.x);
-        const int v = b < bins ? total[b] : 0;
-        int incl = v;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int o = __shfl_up_sync(kFull, incl, d);
-            if (lane >= d) incl += o;
-        }
-        if (lane == 31) warp_sum[warp] = incl;
-        __syncthreads();
-        if (warp == 0) {
-            int x = warp_sum[lane];
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int o = __shfl_up_sync(kFull, x, d);
-                if (lane >= d) x += o;
-            }
-            warp_sum[lane] = x;
+    scan_bins(total, base, bins, blockIdx.x == 0 ? a.offsets : nullptr, warp_sum);
+    for (int round = 0;; ++round) {
+        for (int b = warp; b < bins; b += kSortWarps) {  // lane l: warp l's count
+            const int c = count[lane * bins + b], incl = inclusive_scan(c, lane);
+            count[lane * bins + b] = incl - c;
+            if (lane == 31) total[b] = incl;
         }
         __syncthreads();
-        const int excl = carry + incl - v + (warp ? warp_sum[warp - 1] : 0);
-        if (b < bins) {
-            base[b] += excl;
-            if (blockIdx.x == 0) a.offsets[b] = excl;
-        }
-        carry += warp_sum[kSortWarps - 1];
-        __syncthreads();
-    }
 #pragma unroll
-    for (int r = 0; r < kSortRounds; ++r) {
-        if (bin[r] < 0) continue;
-        const int row = base[bin[r]] + cnt[warp * bins + bin[r]] + rank[r];
-        const int64_t s = s0 + 32 * r;
-        const bool kept = bin[r] < a.experts;
-        a.slot_row[s] = kept ? row : -1;
-        a.row_token[row] = kept ? int32_t(s / a.k) : -1;
+        for (int r = 0; r < kSortRounds; ++r) {
+            if (bin[r] < 0) continue;
+            const int64_t s = s0 + 32 * r;
+            const int row = base[bin[r]] + count[warp * bins + bin[r]] + rank[r];
+            const bool kept = bin[r] < a.experts;
+            a.slot_row[s] = kept ? row : -1;
+            a.row_token[row] = kept ? int32_t(s / a.k) : -1;
+        }
+        if (round + 1 == a.rounds) return;
+        __syncthreads();
+        for (int b = threadIdx.x; b < bins; b += kSortThreads) base[b] += total[b];
+        for (int i = threadIdx.x; i < kSortWarps * bins; i += kSortThreads) count[i] = 0;
+        __syncthreads();
+        s0 += kSortTile;
+        take(s0);
+        __syncthreads();
     }
 }
 
@@ -354,9 +469,29 @@ __global__ void __launch_bounds__(kRowThreads) dopt_route_combine_grad_kernel(co
 // Host side
 // ---------------------------------------------------------------------------
 
+// Rounds of 4096 slots a stretch.
+int64_t sort_rounds(int64_t slots) { return (slots + kSortTile * kSortMaxTiles - 1) / (kSortTile * kSortMaxTiles); }
+
+int64_t sort_tiles(int64_t slots) {
+    const int64_t tile = kSortTile * sort_rounds(slots);
+    return (slots + tile - 1) / tile;
+}
+
 int64_t sort_workspace(int64_t slots, int32_t experts) {
-    const int64_t tiles = (slots + kSortTile - 1) / kSortTile;
-    return tiles > 1 ? tiles * (experts + 1) * int64_t(sizeof(int32_t)) : 0;
+    return slots > kClusterSlots ? sort_tiles(slots) * (experts + 1) * int64_t(sizeof(int32_t)) : 0;
+}
+
+// The sorting kernels' shared memory; its limit is raised where it is past
+// the default.
+int sort_smem(const char *who, void (*kernel)(SortArgs), size_t bins, size_t *bytes) {
+    *bytes = (3 + kSortWarps) * bins * sizeof(int32_t);
+    if (*bytes <= 48 * 1024) return DOPT_OK;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(*bytes));
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return dopt::fail(DOPT_E_CUDA, "%s: shared-memory limit: %s", who, cudaGetErrorString(e));
+    }
+    return DOPT_OK;
 }
 
 int check_slots(const char *who, int64_t tokens, int32_t k) {
@@ -480,25 +615,21 @@ extern "C" int dopt_route_sort(const void *expert_ids, int32_t id_bytes, int64_t
     a.slots = int32_t(tokens * k);
     a.k = k;
     a.experts = n_experts;
-    a.tiles = int32_t(std::max<int64_t>(1, (a.slots + kSortTile - 1) / kSortTile));
     a.wide = id_bytes == 8;
     const size_t bins = size_t(n_experts) + 1;
-    if (a.tiles > 1) {
-        rc = launch_op(who, dopt_route_count_kernel, dim3(unsigned(a.tiles)), dim3(kSortThreads),
-                       bins * sizeof(int32_t), stream, a);
-        if (rc != DOPT_OK) return rc;
+    size_t smem = 0;
+    if (need == 0) {
+        if ((rc = sort_smem(who, dopt_route_sort_kernel, bins, &smem)) != DOPT_OK) return rc;
+        const unsigned blocks = a.slots <= kSortTile ? 1 : kSortCluster;
+        return launch_cluster(who, dopt_route_sort_kernel, dim3(blocks), blocks, dim3(kSortThreads), smem, stream, a);
     }
-    const size_t smem = 2 * bins * sizeof(int32_t) + kSortWarps * bins * sizeof(uint16_t);
-    if (smem > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(dopt_route_place_kernel,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-        if (e != cudaSuccess) {
-            cudaGetLastError();
-            return fail(DOPT_E_CUDA, "%s: shared-memory limit: %s", who, cudaGetErrorString(e));
-        }
-    }
-    return launch_op(who, dopt_route_place_kernel, dim3(unsigned(a.tiles)), dim3(kSortThreads), smem,
-                     stream, a);
+    a.rounds = int32_t(sort_rounds(a.slots));
+    a.tiles = int32_t(sort_tiles(a.slots));
+    rc = launch_op(who, dopt_route_count_kernel, dim3(unsigned(a.tiles)), dim3(kSortThreads), bins * sizeof(int32_t),
+                   stream, a);
+    if (rc != DOPT_OK) return rc;
+    if ((rc = sort_smem(who, dopt_route_place_kernel, bins, &smem)) != DOPT_OK) return rc;
+    return launch_op(who, dopt_route_place_kernel, dim3(unsigned(a.tiles)), dim3(kSortThreads), smem, stream, a);
 }
 
 extern "C" int dopt_route_dispatch(const void *x, dopt_dtype dtype, int64_t tokens, int64_t cols,
