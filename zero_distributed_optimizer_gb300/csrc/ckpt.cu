@@ -37,12 +37,22 @@ struct CkptArgs {
 // Codes
 // ---------------------------------------------------------------------------
 
-// 4 codes as fp32: the byte of code + 128 in the low bits of 2^23, less
-// 2^23 + 128.
-__device__ __forceinline__ void code_values(uint32_t w, float *f) {
+// 4 codes times a step (of exponent byte `byte`) as fp32: with the byte of
+// code + 128 in the low bits of 2^23, that number less 2^23 + 128.  Both
+// products with the step are exact, so one fused operation gives the value,
+// unless 2^23 steps leave fp32's range.
+__device__ __forceinline__ void code_values(uint32_t w, uint32_t byte, float *f) {
+    const float step = ckpt_step(byte);
     w ^= 0x80808080u;
+    if (byte < 230 || byte == kNanByte) {
+        const float less = step * -8388736.0f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440u + i)) - 8388736.0f;
+        for (int i = 0; i < 4; ++i) f[i] = fmaf(__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440u + i)), step, less);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            f[i] = (__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440u + i)) - 8388736.0f) * step;
+    }
 }
 
 __device__ __forceinline__ uint64_t kept_at(const CkptArgs &a, uint32_t r, int c) {
@@ -61,11 +71,9 @@ __device__ __forceinline__ void load_kept(const CkptArgs &a, uint32_t r, int c, 
         const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(a.codes + at));
         w[0] = v.x, w[1] = v.y;
     }
-    const float step = ckpt_step(a.scales[at / kBlock]);
+    const uint32_t byte = a.scales[at / kBlock];
 #pragma unroll
-    for (int i = 0; i < COLS / 4; ++i) code_values(w[i], f + 4 * i);
-#pragma unroll
-    for (int i = 0; i < COLS; ++i) f[i] *= step;
+    for (int i = 0; i < COLS / 4; ++i) code_values(w[i], byte, f + 4 * i);
 }
 
 // The 8 kept values from any column on (the gated half of an odd width):
@@ -79,13 +87,19 @@ __device__ __forceinline__ void load_kept_any(const CkptArgs &a, uint32_t r, int
     if (bytes && (c & ~7) + 8 < a.pitch) hi = __ldcs(reinterpret_cast<const uint2 *>(a.codes + at + 8));
     const uint4 w = shift_down(make_uint4(lo.x, lo.y, hi.x, hi.y), make_uint4(0, 0, 0, 0), bytes);
     const uint64_t block = kept_at(a, r, c) / kBlock;
-    const float first = ckpt_step(a.scales[block]);
+    const uint32_t first = a.scales[block];
     const int in_first = kBlock - (c & (kBlock - 1));
-    const float second = in_first < 8 && c + in_first < a.pitch ? ckpt_step(a.scales[block + 1]) : first;
-    code_values(w.x, f);
-    code_values(w.y, f + 4);
+    code_values(w.x, first, f);
+    code_values(w.y, first, f + 4);
+    if (in_first < 8 && c + in_first < a.pitch) {
+        float g[8];
+        const uint32_t second = a.scales[block + 1];
+        code_values(w.x, second, g);
+        code_values(w.y, second, g + 4);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] *= i < in_first ? first : second;
+        for (int i = 0; i < 8; ++i)
+            if (i >= in_first) f[i] = g[i];
+    }
 }
 
 // A block of 32 columns is 32 / COLS neighbouring threads.  The step is the
