@@ -2,16 +2,22 @@
 // (dopt_ckpt_load) and an activation function's backward pass from its kept
 // input (dopt_ckpt_act_grad).  dopt.h states the format.
 //
-// Saving and reading back give a thread 32 bytes of a row's values (16 columns
-// of 16 bits, 8 of fp32), the activation gradients 8 columns: few enough
-// registers that the threads of an SM keep enough loads in flight for
-// memory's rate, enough columns that indexes cost little.  A thread block
-// covers bx threads' columns of 256 / bx rows and strides over
-// the rows, so no index is divided.
+// All three are bound by memory.  Saving and reading back give a thread 32
+// bytes of a row's values (16 columns of 16 bits, 8 of fp32), the activation
+// gradients 8 columns: few enough registers that the threads of an SM keep
+// enough loads in flight for memory's rate, enough columns that indexes cost
+// little.  A thread block covers bx threads' columns of 256 / bx rows, so no
+// index is divided, and goes on to the next rows where that pays
+// (launch_rows); the next rows' loads are then in flight under the
+// arithmetic.  16384 x 5632 bf16, kept and read back: 86 us (6.5 TB/s); the
+// gated gradient of 16384 x 2 * 5632: 122 us (6.1 TB/s), of which its
+// instructions are some 60 us.
 //
-// Codes are always aligned (a row's pitch is a multiple of 128); rows of
-// values that are not go in aligned pieces all the same (rows.cuh): 16384 x
-// 5631 bf16, kept and read back, took 585 us one element at a time.
+// Codes are always aligned (a row's pitch is a multiple of 128).  Rows of
+// whole, aligned groups have kernels without the checks for any others (94 us
+// with them).  Rows that are not go in aligned pieces all the same
+// (rows.cuh): 16384 x 5631 bf16, kept and read back, 121 us (585 us one
+// element at a time).
 #include "rows.cuh"
 
 namespace {
@@ -31,7 +37,33 @@ struct CkptArgs {
     int32_t half;         // gated: columns of the output (cols / 2)
     int32_t min_exp;      // least exponent byte
     int32_t vec;          // rows are 16-byte aligned
+    int32_t turns;        // times a block takes its number of rows
 };
+
+// ---------------------------------------------------------------------------
+// Two fp32 numbers and operations on both, one instruction each
+// ---------------------------------------------------------------------------
+
+struct F2 {
+    uint64_t v;
+    __device__ __forceinline__ F2(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
+    __device__ __forceinline__ F2(float a) : F2(a, a) {}
+    __device__ __forceinline__ void get(float &a, float &b) const {
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+    }
+};
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+    asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(a.v) : "l"(b.v));
+    return a;
+}
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(a.v) : "l"(b.v));
+    return a;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(a.v) : "l"(b.v), "l"(c.v));
+    return a;
+}
 
 // ---------------------------------------------------------------------------
 // Codes
@@ -45,9 +77,11 @@ __device__ __forceinline__ void code_values(uint32_t w, uint32_t byte, float *f)
     const float step = ckpt_step(byte);
     w ^= 0x80808080u;
     if (byte < 230 || byte == kNanByte) {
-        const float less = step * -8388736.0f;
+        const F2 less = step * -8388736.0f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) f[i] = fmaf(__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440u + i)), step, less);
+        for (int i = 0; i < 4; i += 2)
+            fma2(F2(__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440u + i)),
+                    __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7441u + i))), step, less).get(f[i], f[i + 1]);
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -59,22 +93,31 @@ __device__ __forceinline__ uint64_t kept_at(const CkptArgs &a, uint32_t r, int c
     return uint64_t(r) * uint32_t(a.pitch) + uint32_t(c);
 }
 
-// The COLS (8 or 16) kept values from column c (a multiple of COLS) of row r on.
+// The COLS (8 or 16) kept values from column c (a multiple of COLS) of row r
+// on; 0 where the checkpoint has no such row.
 template <int COLS>
-__device__ __forceinline__ void load_kept(const CkptArgs &a, uint32_t r, int c, float (&f)[COLS]) {
-    const uint64_t at = kept_at(a, r, c);
-    uint32_t w[COLS / 4];
-    if constexpr (COLS == 16) {
-        const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(a.codes + at));
-        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-    } else {
-        const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(a.codes + at));
-        w[0] = v.x, w[1] = v.y;
-    }
-    const uint32_t byte = a.scales[at / kBlock];
+struct Kept {
+    uint32_t w[COLS / 4], byte;
+    __device__ __forceinline__ void load(const CkptArgs &a, uint32_t r, int c) {
 #pragma unroll
-    for (int i = 0; i < COLS / 4; ++i) code_values(w[i], byte, f + 4 * i);
-}
+        for (int i = 0; i < COLS / 4; ++i) w[i] = 0;
+        byte = 1;
+        if (r >= uint32_t(a.rows)) return;
+        const uint64_t at = kept_at(a, r, c);
+        if constexpr (COLS == 16) {
+            const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(a.codes + at));
+            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+        } else {
+            const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(a.codes + at));
+            w[0] = v.x, w[1] = v.y;
+        }
+        byte = a.scales[at / kBlock];
+    }
+    __device__ __forceinline__ void get(float (&f)[COLS]) const {
+#pragma unroll
+        for (int i = 0; i < COLS / 4; ++i) code_values(w[i], byte, f + 4 * i);
+    }
+};
 
 // The 8 kept values from any column on (the gated half of an odd width):
 // codes from the aligned 8 bytes around them, exponents of up to two blocks.
@@ -110,20 +153,33 @@ __device__ __forceinline__ void load_kept_any(const CkptArgs &a, uint32_t r, int
 // and code * step has at most 7 significant bits, so the products of the
 // backward pass read it in 16 bits without a second rounding.  The comparison
 // of magnitudes as integers puts Inf and NaN above every finite value.
-template <typename T>
+// WHOLE: rows of whole, aligned groups of COLS columns.  The next row's loads
+// are in flight under a row's arithmetic.
+template <typename T, bool WHOLE>
 __global__ void __launch_bounds__(kCkptThreads) dopt_ckpt_save_kernel(const __grid_constant__ CkptArgs a) {
     constexpr int COLS = 32 / int(sizeof(T));
     let_dependents_start();
     wait_for_grids_before();
     const int bx = blockDim.x, lane = threadIdx.x;
     const int c = (blockIdx.x * bx + lane) * COLS;
-    for (uint32_t r0 = blockIdx.y * blockDim.y; r0 < uint32_t(a.rows); r0 += gridDim.y * blockDim.y) {
+    const uint32_t step = blockDim.y, first = blockIdx.y * step * a.turns;
+    const uint32_t end = min(first + step * a.turns, uint32_t(a.rows));
+    Values<T, COLS> x;
+    auto load = [&](uint32_t r) {
+        const bool here = r < uint32_t(a.rows);
+        const T *row = static_cast<const T *>(a.x) + (here ? int64_t(r) * a.ld : 0);
+        if constexpr (WHOLE)
+            x.load_whole(row, c, here && c < a.cols);
+        else
+            x.load(row, c, here ? a.cols : 0, a.vec, lane, bx);
+    };
+    load(first + threadIdx.y);
+    for (uint32_t r0 = first; r0 < end; r0 += step) {
         const uint32_t r = r0 + threadIdx.y;
         const bool here = r < uint32_t(a.rows);
-        Values<T, COLS> x;
-        x.load(static_cast<const T *>(a.x) + (here ? int64_t(r) * a.ld : 0), c, here ? a.cols : 0, a.vec, lane, bx);
         float f[COLS];
         x.get(f);
+        if (r0 + step < end) load(r + step);
         uint32_t top = 0;
 #pragma unroll
         for (int i = 0; i < COLS; ++i) top = max(top, __float_as_uint(f[i]) & 0x7fffffffu);
@@ -153,24 +209,34 @@ __global__ void __launch_bounds__(kCkptThreads) dopt_ckpt_save_kernel(const __gr
     }
 }
 
-template <typename T>
+template <typename T, bool WHOLE>
 __global__ void __launch_bounds__(kCkptThreads) dopt_ckpt_load_kernel(const __grid_constant__ CkptArgs a) {
     constexpr int COLS = 32 / int(sizeof(T));
     let_dependents_start();
     wait_for_grids_before();
     const int bx = blockDim.x, lane = threadIdx.x;
     const int c = (blockIdx.x * bx + lane) * COLS;
-    for (uint32_t r0 = blockIdx.y * blockDim.y; r0 < uint32_t(a.n_out); r0 += gridDim.y * blockDim.y) {
+    const uint32_t step = blockDim.y, first = blockIdx.y * step * a.turns;
+    const uint32_t n = min(first + step * a.turns, uint32_t(a.n_out));
+    // the checkpoint's row of output row o
+    auto row_of = [&](uint32_t o) { return o >= n || c >= a.cols ? ~0u : a.index ? uint32_t(a.index[o]) : o; };
+    Kept<COLS> kept;
+    kept.load(a, row_of(first + threadIdx.y), c);
+    uint32_t next = row_of(first + threadIdx.y + step);
+    for (uint32_t r0 = first; r0 < n; r0 += step) {
         const uint32_t o = r0 + threadIdx.y;
-        const bool here = o < uint32_t(a.n_out);
-        float f[COLS] = {};
-        if (here && c < a.cols) {
-            const uint32_t r = a.index ? uint32_t(a.index[o]) : o;
-            if (r < uint32_t(a.rows)) load_kept<COLS>(a, r, c, f);
-        }
+        float f[COLS];
+        kept.get(f);
+        kept.load(a, next, c);
+        next = row_of(o + 2 * step);
         Values<T, COLS> y;
         y.set(f);
-        y.store(static_cast<T *>(a.out) + (here ? int64_t(o) * a.ld_out : 0), c, here ? a.cols : 0, a.vec, lane, bx);
+        const bool here = o < n;
+        T *row = static_cast<T *>(a.out) + (here ? int64_t(o) * a.ld_out : 0);
+        if constexpr (WHOLE)
+            y.store_whole(row, c, here && c < a.cols);
+        else
+            y.store(row, c, here ? a.cols : 0, a.vec, lane, bx);
     }
 }
 
@@ -184,16 +250,22 @@ __global__ void __launch_bounds__(kCkptThreads) dopt_ckpt_load_kernel(const __gr
 // most 2^-22 of its result, the power also by the rounding of -x / ln 2 (in
 // all below (2 + 1.2 |x|) 2^-23); fp32 ones take the library's functions.
 template <typename T>
-__device__ __forceinline__ void sigmoid(float x, float &s, float &rest) {
-    float e;
+__device__ __forceinline__ void sigmoid(F2 x, F2 &s, F2 &rest) {
+    float x0, x1, e0, e1, d0, d1;
     if constexpr (sizeof(T) == 4) {
-        e = expf(-x);
-        s = 1.0f / (1.0f + e);
+        x.get(x0, x1);
+        e0 = expf(-x0), e1 = expf(-x1);
+        s = F2(1.0f / (1.0f + e0), 1.0f / (1.0f + e1));
     } else {
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.44269504f));
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + e));
+        (x * -1.44269504f).get(x0, x1);
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(x0));
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(x1));
+        (F2(e0, e1) + 1.0f).get(d0, d1);
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(d0) : "f"(d0));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(d1) : "f"(d1));
+        s = F2(d0, d1);
     }
-    rest = e * s;
+    rest = F2(e0, e1) * s;
 }
 __device__ __forceinline__ float at_least(float x, float b) {  // NaN stays NaN
     float y;
@@ -209,27 +281,85 @@ __device__ __forceinline__ float at_most(float x, float b) {
 // silu'(h) = s (1 + h (1 - s)) and silu(h) = h s, s = sigmoid(h).  Below -87
 // both are within 2e-36 of what they are there, 0 in effect.
 template <typename T>
-__device__ __forceinline__ float silu_slope(float h, float &silu) {
-    const float x = at_least(h, -87.0f);
-    float s, rest;
+__device__ __forceinline__ F2 silu_slope(float h0, float h1, F2 &silu) {
+    const F2 x(at_least(h0, -87.0f), at_least(h1, -87.0f));
+    F2 s = 0.0f, rest = 0.0f;
     sigmoid<T>(x, s, rest);
     silu = x * s;
-    return s * fmaf(x, rest, 1.0f);
+    return s * fma2(x, rest, 1.0f);
 }
 
 // GELU in its tanh form is h p with p = (1 + tanh u) / 2 = sigmoid(2u),
 // u = c (h + a h^3); its slope p + h 2 p (1 - p) c (1 + 3 a h^2).  Beyond
 // |h| = 9.9 (2u = 85) it is 0 or 1 to within 1e-34.
 template <typename T>
-__device__ __forceinline__ float gelu_slope(float h) {
+__device__ __forceinline__ F2 gelu_slope(float h0, float h1) {
     constexpr float kC = 0.79788456080286536f, kA = 0.044715f;
-    const float x = at_most(at_least(h, -9.9f), 9.9f);
-    const float x2 = x * x;
-    float p, rest;
-    sigmoid<T>(2.0f * kC * x * fmaf(kA, x2, 1.0f), p, rest);
-    return fmaf(2.0f * kC * x * fmaf(3.0f * kA, x2, 1.0f), p * rest, p);
+    const F2 x(at_most(at_least(h0, -9.9f), 9.9f), at_most(at_least(h1, -9.9f), 9.9f));
+    const F2 x2 = x * x, cx = x * (2.0f * kC);
+    F2 p = 0.0f, rest = 0.0f;
+    sigmoid<T>(cx * fma2(kA, x2, 1.0f), p, rest);
+    return fma2(cx * fma2(3.0f * kA, x2, 1.0f), p * rest, p);
 }
 
+template <typename T, int ACT>
+__device__ __forceinline__ void act_grad(const float (&d)[8], float (&h)[8], float (&u)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        const F2 dd(d[i], d[i + 1]);
+        F2 silu = 0.0f;
+        if constexpr (ACT == DOPT_ACT_SWIGLU) {
+            const F2 slope = silu_slope<T>(h[i], h[i + 1], silu);
+            (dd * F2(u[i], u[i + 1]) * slope).get(h[i], h[i + 1]);
+            (dd * silu).get(u[i], u[i + 1]);
+        } else if constexpr (ACT == DOPT_ACT_SILU) {
+            (dd * silu_slope<T>(h[i], h[i + 1], silu)).get(h[i], h[i + 1]);
+        } else {
+            (dd * gelu_slope<T>(h[i], h[i + 1])).get(h[i], h[i + 1]);
+        }
+    }
+}
+
+// Rows of whole, aligned groups of 8 columns: the next row's loads are in
+// flight under a row's arithmetic.
+template <typename T, int ACT>
+__global__ void __launch_bounds__(kCkptThreads) dopt_ckpt_act_grad_whole_kernel(const __grid_constant__ CkptArgs a) {
+    constexpr bool kGated = ACT == DOPT_ACT_SWIGLU;
+    const int width = kGated ? a.half : a.cols;
+    const int c = int(blockIdx.x * blockDim.x + threadIdx.x) * 8;
+    const uint32_t step = blockDim.y, first = blockIdx.y * step * a.turns;
+    const uint32_t end = min(first + step * a.turns, uint32_t(a.rows));
+    uint32_t r = first + threadIdx.y;
+    let_dependents_start();
+    wait_for_grids_before();
+    if (c >= width || r >= end) return;
+    Values<T, 8> x;
+    Kept<8> kept_h, kept_u;
+    auto load = [&](uint32_t row) {
+        x.load_whole(static_cast<const T *>(a.x) + int64_t(row) * a.ld, c, true);
+        kept_h.load(a, row, c);
+        if constexpr (kGated) kept_u.load(a, row, width + c);
+    };
+    load(r);
+    for (; r < end; r += step) {
+        float d[8], h[8], u[8];
+        x.get(d);
+        kept_h.get(h);
+        if constexpr (kGated) kept_u.get(u);
+        if (r + step < end) load(r + step);
+        act_grad<T, ACT>(d, h, u);
+        T *out = static_cast<T *>(a.out) + int64_t(r) * a.ld_out;
+        Values<T, 8> y;
+        y.set(h);
+        y.store_whole(out, c, true);
+        if constexpr (kGated) {
+            y.set(u);
+            y.store_whole(out, width + c, true);
+        }
+    }
+}
+
+// Rows of any width and alignment.
 template <typename T, int ACT>
 __global__ void __launch_bounds__(kCkptThreads) dopt_ckpt_act_grad_kernel(const __grid_constant__ CkptArgs a) {
     constexpr int COLS = 8;
@@ -238,35 +368,24 @@ __global__ void __launch_bounds__(kCkptThreads) dopt_ckpt_act_grad_kernel(const 
     const int bx = blockDim.x, lane = threadIdx.x;
     const int c = (blockIdx.x * bx + lane) * COLS;
     const int width = ACT == DOPT_ACT_SWIGLU ? a.half : a.cols;
-    for (uint32_t r0 = blockIdx.y * blockDim.y; r0 < uint32_t(a.rows); r0 += gridDim.y * blockDim.y) {
+    const uint32_t step = blockDim.y, first = blockIdx.y * step * a.turns;
+    const uint32_t end = min(first + step * a.turns, uint32_t(a.rows));
+    for (uint32_t r0 = first; r0 < end; r0 += step) {
         const uint32_t r = r0 + threadIdx.y;
         const bool here = r < uint32_t(a.rows);
         Values<T, COLS> x;
         x.load(static_cast<const T *>(a.x) + (here ? int64_t(r) * a.ld : 0), c, here ? width : 0, a.vec, lane, bx);
         float h[COLS] = {}, u[COLS] = {};
         if (here && c < width) {
-            load_kept<COLS>(a, r, c, h);
-            if constexpr (ACT == DOPT_ACT_SWIGLU) {
-                if (width % kBlock == 0)
-                    load_kept<COLS>(a, r, width + c, u);
-                else
-                    load_kept_any(a, r, width + c, u);
-            }
+            Kept<COLS> kept;
+            kept.load(a, r, c);
+            kept.get(h);
+            if constexpr (ACT == DOPT_ACT_SWIGLU) load_kept_any(a, r, width + c, u);
         }
         float d[COLS];
         x.get(d);
         T *out = static_cast<T *>(a.out) + (here ? int64_t(r) * a.ld_out : 0);
-#pragma unroll
-        for (int i = 0; i < COLS; ++i) {
-            float silu;
-            if constexpr (ACT == DOPT_ACT_SWIGLU) {
-                const float slope = silu_slope<T>(h[i], silu);
-                h[i] = d[i] * u[i] * slope;
-                u[i] = d[i] * silu;
-            } else {
-                h[i] = d[i] * (ACT == DOPT_ACT_SILU ? silu_slope<T>(h[i], silu) : gelu_slope<T>(h[i]));
-            }
-        }
+        act_grad<T, ACT>(d, h, u);
         Values<T, COLS> y;
         y.set(h);
         y.store(out, c, here ? width : 0, a.vec, lane, bx);
@@ -319,27 +438,54 @@ CkptArgs ckpt_args(const void *ckpt, int64_t rows, int64_t cols) {
 }
 
 // Blocks of bx threads along the columns, `each` columns a thread, and
-// 256 / bx rows.
+// 256 / bx rows at a time, for up to `turns` times, where that leaves 5 blocks
+// an SM.  Whole rows are saved and read back in one turn (16384 x 5632 bf16:
+// 86 us; 87 in two turns, 92 in four); there is arithmetic to hide the next
+// loads under in the others: the gated gradient takes 135, 125, 122.5 and 124
+// us in 1, 2, 4 and 8 turns, 16384 x 5631 saved and read back 136, 126, 121
+// and 123.
 template <typename Kernel>
-int launch_rows(const char *who, Kernel kernel, const CkptArgs &a, int64_t cols, int each, int64_t rows,
+int launch_rows(const char *who, Kernel kernel, CkptArgs a, int64_t cols, int each, int64_t rows, int turns,
                 cudaStream_t stream) {
     const int64_t groups = (cols + each - 1) / each;
     const int bx = groups > 16 ? 32 : groups > 8 ? 16 : 8;
     const int by = kCkptThreads / bx;
-    const dim3 grid(unsigned((groups + bx - 1) / bx),
-                    unsigned(std::min<int64_t>((rows + by - 1) / by, 65535)));
+    const int64_t across = (groups + bx - 1) / bx, down = (rows + by - 1) / by;
+    a.turns = int(std::max<int64_t>(1, std::min<int64_t>(turns, across * down / (152 * 5))));
+    while ((down + a.turns - 1) / a.turns > 65535) a.turns *= 2;  // the grid's limit
+    const dim3 grid(unsigned(across), unsigned((down + a.turns - 1) / a.turns));
     return launch_op(who, kernel, grid, dim3(bx, by), 0, stream, a);
+}
+
+template <typename T>
+int launch_save(const char *who, const CkptArgs &a, cudaStream_t stream) {
+    constexpr int kEach = 32 / int(sizeof(T));
+    return a.vec && a.cols % kEach == 0
+               ? launch_rows(who, dopt_ckpt_save_kernel<T, true>, a, a.pitch, kEach, a.rows, 1, stream)
+               : launch_rows(who, dopt_ckpt_save_kernel<T, false>, a, a.pitch, kEach, a.rows, 4, stream);
+}
+
+template <typename T>
+int launch_load(const char *who, const CkptArgs &a, cudaStream_t stream) {
+    constexpr int kEach = 32 / int(sizeof(T));
+    return a.vec && a.cols % kEach == 0
+               ? launch_rows(who, dopt_ckpt_load_kernel<T, true>, a, a.cols, kEach, a.n_out, 1, stream)
+               : launch_rows(who, dopt_ckpt_load_kernel<T, false>, a, a.cols, kEach, a.n_out, 4, stream);
+}
+
+template <typename T, int ACT>
+int launch_act_as(const char *who, const CkptArgs &a, int64_t width, cudaStream_t stream) {
+    return a.vec && width % 8 == 0
+               ? launch_rows(who, dopt_ckpt_act_grad_whole_kernel<T, ACT>, a, width, 8, a.rows, 4, stream)
+               : launch_rows(who, dopt_ckpt_act_grad_kernel<T, ACT>, a, width, 8, a.rows, 4, stream);
 }
 
 template <typename T>
 int launch_act(const char *who, dopt_act act, const CkptArgs &a, int64_t width, cudaStream_t stream) {
     switch (act) {
-        case DOPT_ACT_SILU:
-            return launch_rows(who, dopt_ckpt_act_grad_kernel<T, DOPT_ACT_SILU>, a, width, 8, a.rows, stream);
-        case DOPT_ACT_GELU:
-            return launch_rows(who, dopt_ckpt_act_grad_kernel<T, DOPT_ACT_GELU>, a, width, 8, a.rows, stream);
-        default:
-            return launch_rows(who, dopt_ckpt_act_grad_kernel<T, DOPT_ACT_SWIGLU>, a, width, 8, a.rows, stream);
+        case DOPT_ACT_SILU: return launch_act_as<T, DOPT_ACT_SILU>(who, a, width, stream);
+        case DOPT_ACT_GELU: return launch_act_as<T, DOPT_ACT_GELU>(who, a, width, stream);
+        default: return launch_act_as<T, DOPT_ACT_SWIGLU>(who, a, width, stream);
     }
 }
 
@@ -372,9 +518,9 @@ extern "C" int dopt_ckpt_save(const void *x, dopt_dtype dtype, int64_t rows, int
     a.vec = vec_rows(x, dtype, ld);
     a.min_exp = dtype == DOPT_FP16 ? 127 - 24 : 1;
     switch (dtype) {
-        case DOPT_BF16: return launch_rows(who, dopt_ckpt_save_kernel<__nv_bfloat16>, a, a.pitch, 16, rows, stream);
-        case DOPT_FP16: return launch_rows(who, dopt_ckpt_save_kernel<__half>, a, a.pitch, 16, rows, stream);
-        default: return launch_rows(who, dopt_ckpt_save_kernel<float>, a, a.pitch, 8, rows, stream);
+        case DOPT_BF16: return launch_save<__nv_bfloat16>(who, a, stream);
+        case DOPT_FP16: return launch_save<__half>(who, a, stream);
+        default: return launch_save<float>(who, a, stream);
     }
 }
 
@@ -401,9 +547,9 @@ extern "C" int dopt_ckpt_load(const void *ckpt, int64_t rows, int64_t cols, cons
     a.n_out = int32_t(n_out);
     a.vec = vec_rows(out, dtype, ld);
     switch (dtype) {
-        case DOPT_BF16: return launch_rows(who, dopt_ckpt_load_kernel<__nv_bfloat16>, a, cols, 16, n_out, stream);
-        case DOPT_FP16: return launch_rows(who, dopt_ckpt_load_kernel<__half>, a, cols, 16, n_out, stream);
-        default: return launch_rows(who, dopt_ckpt_load_kernel<float>, a, cols, 8, n_out, stream);
+        case DOPT_BF16: return launch_load<__nv_bfloat16>(who, a, stream);
+        case DOPT_FP16: return launch_load<__half>(who, a, stream);
+        default: return launch_load<float>(who, a, stream);
     }
 }
 

@@ -91,6 +91,18 @@ struct Values {
         }
     }
 
+    // The same where c and the row are aligned and all COLS values are there (or none: `some` false).
+    __device__ __forceinline__ void load_whole(const T *row, int c, bool some) {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)
+            raw[i] = some ? __ldcs(reinterpret_cast<const uint4 *>(row + c) + i) : make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void store_whole(T *row, int c, bool some) const {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)
+            if (some) __stcs(reinterpret_cast<uint4 *>(row + c) + i, raw[i]);
+    }
+
     __device__ __forceinline__ void get(float (&f)[COLS]) const {
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
