@@ -17,10 +17,11 @@ namespace {
 // in shared memory, both as they lie in memory, rows of K with M or N
 // contiguous, in slabs of 64 columns x 64 rows with the 128-byte swizzle.
 //
-//   dy  bf16 / fp16, by TMA (a ring of 8 blocks of 256 o); by plain loads in a
-//       group's last step, whose rows past the group must read as zeros
-//       whatever the next group holds there, and where rows are not 16-byte
-//       aligned
+//   dy  bf16 / fp16, by TMA (a ring of 8 blocks of 256 o); by the warps that
+//       widen codes in a group's last step, whose rows past the group must read
+//       as zeros whatever the next group holds there (copies of 16 bytes, in
+//       flight under the conversions), and where rows are not 16-byte aligned
+//       (plain loads)
 //   x   16 warps load 16 codes a thread and row into registers, widen them to
 //       16 bits (exactly) and store them swizzled (a ring of 4 steps).  Four
 //       warps take a step, so that one step's waits, stores and fence run
@@ -283,8 +284,9 @@ __device__ __forceinline__ int block_outs(const WgradArgs &a, const WgradItem &i
     return min(kTileO, (a.outs - it.o0 - nb * kTileO + 31) / 32 * 32);
 }
 
-// A CTA's half of 64 rows of dy by plain loads, zeros past the rows and
-// columns there are.
+// A CTA's half of 64 rows of dy, zeros past the rows and columns there are, by
+// a group's threads: aligned rows by asynchronous copies of 16 bytes, all in
+// flight until copies_done, others by plain loads.
 template <typename T>
 __device__ __forceinline__ void stage_dy(const WgradArgs &a, int r0, int rows, int o0, int n_half,
                                          unsigned char *stage) {
@@ -293,50 +295,56 @@ __device__ __forceinline__ void stage_dy(const WgradArgs &a, int r0, int rows, i
     for (int i = threadIdx.x % kGroup; i < kK * 16; i += kGroup) {
         const int k = i >> 4, q = i & 15;
         if (q >= chunks) continue;
-        const int o = o0 + q * 8;
-        uint4 raw = make_uint4(0, 0, 0, 0);
-        if (k < rows && o < a.outs) {
-            const T *p = dy + (r0 + k) * a.dy_ld + o;
-            if (a.vec && o + 8 <= a.outs) {
-                raw = *reinterpret_cast<const uint4 *>(p);
-            } else {
-                uint16_t e[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    e[j] = o + j < a.outs ? reinterpret_cast<const uint16_t *>(p)[j] : uint16_t(0);
-                memcpy(&raw, e, sizeof raw);
-            }
+        const int o = o0 + q * 8, n = k < rows ? min(8, max(0, a.outs - o)) : 0;
+        const T *p = n > 0 ? dy + (r0 + k) * a.dy_ld + o : dy;
+        if (a.vec) {
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_of(stage + stage_chunk(k, q))),
+                         "l"(p), "r"(2 * n)
+                         : "memory");
+            continue;
         }
+        uint16_t e[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) e[j] = j < n ? reinterpret_cast<const uint16_t *>(p)[j] : uint16_t(0);
+        uint4 raw;
+        memcpy(&raw, e, sizeof raw);
         *reinterpret_cast<uint4 *>(stage + stage_chunk(k, q)) = raw;
     }
 }
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// The 128 bytes of the first block of those rows that are this thread's, on
-// their way to L2 before stage_dy reads them.
-template <typename T>
-__device__ __forceinline__ void prefetch_dy(const WgradArgs &a, const WgradItem &it, int i, uint32_t rank) {
-    const int t = threadIdx.x % kGroup, k = i * kK + (t >> 1);
-    const int o = it.o0 + int(rank) * (block_outs(a, it, 0) / 2) + (t & 1) * 64;
-    if (k < it.rows && o < a.outs)
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const T *>(a.dy) + (it.lo + k) * a.dy_ld + o));
+// The dy of step i of the item of round k, block u of all on, into slots
+// whose last products are done.
+template <typename T, int NB>
+__device__ __forceinline__ bool stage_step(const WgradArgs &a, const WgradGroups &g, WgradBarriers &b,
+                                        unsigned char *dy_ring, int k, int i, int u, uint32_t rank) {
+    const WgradItem it = item_of<NB>(a, g, item_number(a, k));
+    bool ok = true;
+    for (int nb = 0; nb < it.blocks; ++nb, ++u) {
+        const int n_half = block_outs(a, it, nb) / 2;
+        if (u >= kDyRing) ok = wait_phase(b, b.dy_empty[u % kDyRing], uint32_t(u / kDyRing - 1) & 1);
+        if (!__all_sync(kFull, ok)) return false;
+        stage_dy<T>(a, it.lo + i * kK, it.rows - i * kK, it.o0 + nb * kTileO + int(rank) * n_half, n_half,
+                    dy_ring + (u % kDyRing) * kStage);
+    }
+    return true;
 }
 
-// 16 outputs' sums of one column to the grads; `all`: the 16 are all outputs.
+// 16 outputs' sums of one column, of which `n` are outputs, to the grads from p on.
 template <typename G>
-__device__ __forceinline__ void store_sums(const WgradArgs &a, const WgradItem &it, int c, int o,
-                                           const float (&f)[16], bool all) {
-    if (c >= a.cols) return;
-    G *p = static_cast<G *>(a.grad) + a.grad_offset[it.group] + o * a.cols + c;
-    const int n = all ? 16 : min(16, a.outs - o);
+__device__ __forceinline__ void store_sums(const WgradArgs &a, G *p, int n, const float (&f)[16]) {
     if (a.accumulate) {
-        G old[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-            if (j < n) old[j] = p[j * a.cols];
+        for (int j0 = 0; j0 < 16; j0 += 4) {
+            G old[4];
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-            if (j < n) p[j * a.cols] = from_f32<G>(to_f32(old[j]) + f[j]);
-    } else if (all) {
+            for (int j = 0; j < 4; ++j)
+                if (j0 + j < n) old[j] = p[j * a.cols];
+#pragma unroll
+            for (int j = 0; j < 4; ++j, p += a.cols)
+                if (j0 + j < n) *p = from_f32<G>(to_f32(old[j]) + f[j0 + j]);
+        }
+    } else if (n >= 16) {
 #pragma unroll
         for (int j = 0; j < 16; ++j, p += a.cols) *p = from_f32<G>(f[j]);
     } else {
@@ -344,6 +352,12 @@ __device__ __forceinline__ void store_sums(const WgradArgs &a, const WgradItem &
         for (int j = 0; j < 16; ++j, p += a.cols)
             if (j < n) *p = from_f32<G>(f[j]);
     }
+}
+
+// The grad of column c and the tile's first output.
+template <typename G>
+__device__ __forceinline__ G *grad_at(const WgradArgs &a, const WgradItem &it, int c) {
+    return static_cast<G *>(a.grad) + a.grad_offset[it.group] + it.o0 * a.cols + c;
 }
 
 // 32 lanes x 16 columns of tensor memory, in flight until wait_sums.
@@ -366,6 +380,8 @@ __device__ __forceinline__ void wait_sums(uint32_t (&r)[16]) {
 // A tile's sums of a warp's 32 columns, at `sums` in tensor memory, to the grads.
 template <typename G>
 __device__ __forceinline__ void store_tile(const WgradArgs &a, const WgradItem &it, int c, int outs, uint32_t sums) {
+    G *p = grad_at<G>(a, it, c);
+    const int there = c < a.cols ? a.outs - it.o0 : 0;
     for (int o = 0; o < outs; o += 32) {  // (outs is a multiple of 32)
         uint32_t r[2][16] = {};
         if (it.steps > 0) {
@@ -374,13 +390,12 @@ __device__ __forceinline__ void store_tile(const WgradArgs &a, const WgradItem &
             wait_sums(r[0]);
             wait_sums(r[1]);
         }
-        const bool all = it.o0 + o + 32 <= a.outs;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < 2; ++h, p += 16 * a.cols) {
             float f[16];
 #pragma unroll
             for (int q = 0; q < 16; ++q) f[q] = __uint_as_float(r[h][q]);
-            store_sums<G>(a, it, c, it.o0 + o + 16 * h, f, all);
+            store_sums(a, p, there - o - 16 * h, f);
         }
     }
 }
@@ -584,25 +599,32 @@ __global__ void __launch_bounds__(kWgradThreads, 1) __cluster_dims__(2, 1, 1)
         const int w = warp & 3, r = ((lane >> 2) & 1) + 2 * (lane >> 4);
         const int c16 = 64 * ((lane >> 3) & 1) + 16 * (lane & 3);
         struct {
-            WgradItem it;
             int k, i, n, u;  // the round, the step in its item; the step and block of dy of all
+            int lo, rows, c, blocks;
         } at;
         at.k = at.i = at.n = at.u = 0;
+        auto enter = [&](int item) {
+            const WgradItem it = item_of<NB>(a, groups, item);
+            at.lo = it.lo, at.rows = it.rows, at.blocks = NB == 1 ? 1 : it.blocks;
+            at.c = it.c0 + int(rank) * (kTileC / 2);
+        };
         // on by so many steps, over items; false past the last
         auto advance = [&](int by) -> bool {
             at.i += by;
             at.n += by;
-            at.u += by * at.it.blocks;
-            while (at.i >= at.it.steps) {
-                at.u -= (at.i - at.it.steps) * at.it.blocks;
-                at.i -= at.it.steps;
+            at.u += by * at.blocks;
+            for (int steps; at.i >= (steps = (at.rows + kK - 1) / kK);) {
+                at.u -= (at.i - steps) * at.blocks;
+                at.i -= steps;
                 const int item = item_number(a, ++at.k);
                 if (item < 0) return false;
-                at.it = item_of<NB>(a, groups, item);
-                at.u += at.i * at.it.blocks;
+                enter(item);
+                at.u += at.i * at.blocks;
             }
             return true;
         };
+        // whether the step's dy comes from here
+        auto own = [&]() { return !a.tma || at.i >= at.rows / kK; };
         uint4 code[4];
         uint32_t exp[4];
         int tokens = -1;
@@ -611,11 +633,11 @@ __global__ void __launch_bounds__(kWgradThreads, 1) __cluster_dims__(2, 1, 1)
         auto load_tokens = [&]() {
             const int k = at.i * kK + 4 * w + (lane & 3) + 4 * (lane & 12);
             tokens = -1;
-            if (k < at.it.rows && lane < 16) tokens = a.row_token ? a.row_token[at.it.lo + k] : at.it.lo + k;
+            if (k < at.rows && lane < 16) tokens = a.row_token ? a.row_token[at.lo + k] : at.lo + k;
         };
         const uint32_t pitch = uint32_t(a.pitch);
         auto load_codes = [&]() {
-            const int c = at.it.c0 + int(rank) * (kTileC / 2);
+            const int c = at.c;
             if (c >= a.pitch || a.x_rows <= 0) {  // no such columns, or no rows: zeros
 #pragma unroll
                 for (int h = 0; h < 4; ++h) code[h] = make_uint4(0, 0, 0, 0);
@@ -633,15 +655,17 @@ __global__ void __launch_bounds__(kWgradThreads, 1) __cluster_dims__(2, 1, 1)
                 exp[h] = __ldg(scales + row * (pitch / kBlock));
             }
         };
-        at.it = item_of<NB>(a, groups, item_number(a, 0));
+        enter(item_number(a, 0));
         bool more = advance(warp >> 2);
         if (more) load_tokens(), load_codes();
         // 16 rows on: 2048 bytes on, and the swizzle is the same
         const uint32_t chunk0 = stage_chunk(4 * w + r, c16 / 8), chunk1 = stage_chunk(4 * w + r, c16 / 8 + 1);
         bool ok = true;
         while (more) {
-            const int s = at.n % kXRing;
+            const int n = at.n, s = n % kXRing;
             unsigned char *stage = x_ring + s * kStage;
+            const bool own_dy = own();
+            if (own_dy) ok = stage_step<T, NB>(a, groups, b, dy_ring, at.k, at.i, at.u, rank);
             if (absent & 0xffff) {
 #pragma unroll
                 for (int h = 0; h < 4; ++h)
@@ -653,7 +677,7 @@ __global__ void __launch_bounds__(kWgradThreads, 1) __cluster_dims__(2, 1, 1)
                 v[2 * h] = widen(T(), make_uint2(code[h].x, code[h].y), exp[h]);
                 v[2 * h + 1] = widen(T(), make_uint2(code[h].z, code[h].w), exp[h]);
             }
-            if (at.n >= kXRing) ok = wait_phase<32>(b, b.x_empty[s], uint32_t(at.n / kXRing - 1) & 1);
+            if (n >= kXRing) ok = wait_phase<32>(b, b.x_empty[s], uint32_t(n / kXRing - 1) & 1) && ok;
             if (!__all_sync(kFull, ok)) break;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -667,25 +691,13 @@ __global__ void __launch_bounds__(kWgradThreads, 1) __cluster_dims__(2, 1, 1)
                 *reinterpret_cast<uint4 *>(stage + chunk1 + h * 2048) =
                     widen(T(), make_uint2(code[h].z, code[h].w), exp[h]);
             }
-            if (!a.tma || at.i >= at.it.full) {
-                // the step's dy too: its slots' last products are done, since
-                // those of the step that x_empty was waited for are
-                for (int nb = 0; nb < at.it.blocks; ++nb) {
-                    const int u = at.u + nb, n_half = block_outs(a, at.it, nb) / 2;
-                    if (u >= kDyRing) ok = wait_phase(b, b.dy_empty[u % kDyRing], uint32_t(u / kDyRing - 1) & 1) && ok;
-                    stage_dy<T>(a, at.it.lo + at.i * kK, at.it.rows - at.i * kK,
-                                at.it.o0 + nb * kTileO + int(rank) * n_half, n_half,
-                                dy_ring + (u % kDyRing) * kStage);
-                }
-                if (!__all_sync(kFull, ok)) break;
-            }
+            if (own_dy) copies_done();
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) arrive_remote(leader_address(smem_of(&b.x_full[s])));
             more = advance(kGroups);
             if (more) {
                 load_tokens();
-                if (!a.tma || at.i >= at.it.full) prefetch_dy<T>(a, at.it, at.i, rank);
                 load_codes();
             }
         }
@@ -727,7 +739,8 @@ __global__ void __launch_bounds__(kTileC) dopt_ckpt_wgrad_join_kernel(const __gr
 #pragma unroll
         for (int q = 0; q < 16; ++q) f[q] += v[q];
     }
-    store_sums<G>(a, it, it.c0 + column_of(threadIdx.x), it.o0 + o, f, false);
+    const int c = it.c0 + column_of(threadIdx.x);
+    if (c < a.cols) store_sums(a, grad_at<G>(a, it, c) + o * a.cols, a.outs - it.o0 - o, f);
 }
 
 // dy with rows that are not 16-byte aligned, into rows that are (`ld`, a
