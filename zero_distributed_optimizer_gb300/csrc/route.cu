@@ -18,20 +18,21 @@ namespace {
 // warp counts its slots by bin, 32 at a time, the counts become first rows by
 // a scan over the warps, over the blocks (through the cluster's shared
 // memory) and over the bins, and the warp goes through its slots again.
-// More slots: a launch that counts stretches of 4096 slots (of more above
-// 304 * 4096, so that there are at most 304 of them) and one that places
-// them, each block adding up the stretches before it.  2^18 slots of 64 experts:
-// 41 us in the cluster (its 8 SMs store to a sector a slot), 4.8 + 10.1 us in
-// the two launches; sorting 2^15 slots of 64 experts and copying their 2048
-// bf16 columns takes 40.4 us with the cluster, 42.5 us with the two.
-// (Putting a tile's rows in order in shared memory before they are stored
-// changed nothing: 10.1 us.)
+// More slots: a launch that counts stretches of 2048 slots (of more above
+// 304 * 2048, so that there are at most 304 of them) and one that places
+// them, each block adding up the stretches before it.  Sorting 2^18 slots of
+// 64 experts and copying their 512 bf16 columns takes 86 us with the cluster
+// (41 us for the sort: its 8 SMs store to a sector a slot) and 56 us with the
+// two launches (58 and 63 us with stretches of 4096 and 1024); 2^15 slots and
+// 2048 columns 40.4 us with the cluster and 42.5 us with the two.  (Putting a
+// stretch's rows in order before they are stored changed nothing.)
 // ---------------------------------------------------------------------------
 
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortRounds = 4;  // slots a thread takes at a time
-constexpr int64_t kSortTile = int64_t(kSortThreads) * kSortRounds;
+constexpr int kSortRounds = 4;  // slots a thread takes at a time, in the cluster
+constexpr int kTileRounds = 2;  // in the two launches
+constexpr int64_t kSortTile = int64_t(kSortThreads) * kTileRounds;
 constexpr int kSortCluster = 8;
 constexpr int64_t kClusterSlots = int64_t(1) << 15;
 constexpr int64_t kSortMaxTiles = 304;
@@ -41,7 +42,7 @@ struct SortArgs {
     int32_t *slot_row, *row_token, *offsets;
     int32_t *counts;  // [tiles][bins]
     int32_t slots, k, experts, tiles;
-    int32_t rounds;  // of 4096 slots, a tile
+    int32_t rounds;  // of 2048 slots, a tile
     int32_t wide;    // 64-bit ids
 };
 
@@ -196,7 +197,7 @@ __global__ void __launch_bounds__(kSortThreads) dopt_route_count_kernel(const __
     for (int round = 0; round < a.rounds; ++round) {
         const int64_t s0 = (int64_t(blockIdx.x) * a.rounds + round) * kSortTile + threadIdx.x;
 #pragma unroll
-        for (int r = 0; r < kSortRounds; ++r)
+        for (int r = 0; r < kTileRounds; ++r)
             if (s0 + r * kSortThreads < a.slots) atomicAdd(&hist[bin_of(a, s0 + r * kSortThreads)], 1);
     }
     __syncthreads();
@@ -216,14 +217,14 @@ __global__ void __launch_bounds__(kSortThreads) dopt_route_place_kernel(const __
     for (int i = threadIdx.x; i < kSortWarps * bins; i += kSortThreads) count[i] = 0;
     wait_for_grids_before();
     __syncthreads();
-    int bin[kSortRounds], rank[kSortRounds];
+    int bin[kTileRounds], rank[kTileRounds];
     auto take = [&](int64_t s0) {
 #pragma unroll
-        for (int r = 0; r < kSortRounds; ++r) bin[r] = s0 + 32 * r < a.slots ? bin_of(a, s0 + 32 * r) : -1;
+        for (int r = 0; r < kTileRounds; ++r) bin[r] = s0 + 32 * r < a.slots ? bin_of(a, s0 + 32 * r) : -1;
 #pragma unroll
-        for (int r = 0; r < kSortRounds; ++r) rank[r] = rank_in_warp(bin[r], bits, lane, count + warp * bins);
+        for (int r = 0; r < kTileRounds; ++r) rank[r] = rank_in_warp(bin[r], bits, lane, count + warp * bins);
     };
-    int64_t s0 = int64_t(blockIdx.x) * a.rounds * kSortTile + int64_t(warp) * 32 * kSortRounds + lane;
+    int64_t s0 = int64_t(blockIdx.x) * a.rounds * kSortTile + int64_t(warp) * 32 * kTileRounds + lane;
     take(s0);
     // slots of each bin in all tiles, and in the tiles before this one
     const int n = a.tiles * bins, mine = int(blockIdx.x) * bins;
@@ -250,7 +251,7 @@ __global__ void __launch_bounds__(kSortThreads) dopt_route_place_kernel(const __
         }
         __syncthreads();
 #pragma unroll
-        for (int r = 0; r < kSortRounds; ++r) {
+        for (int r = 0; r < kTileRounds; ++r) {
             if (bin[r] < 0) continue;
             const int64_t s = s0 + 32 * r;
             const int row = base[bin[r]] + count[warp * bins + bin[r]] + rank[r];
@@ -469,7 +470,7 @@ __global__ void __launch_bounds__(kRowThreads) dopt_route_combine_grad_kernel(co
 // Host side
 // ---------------------------------------------------------------------------
 
-// Rounds of 4096 slots a stretch.
+// Rounds of 2048 slots a stretch.
 int64_t sort_rounds(int64_t slots) { return (slots + kSortTile * kSortMaxTiles - 1) / (kSortTile * kSortMaxTiles); }
 
 int64_t sort_tiles(int64_t slots) {
@@ -620,7 +621,7 @@ extern "C" int dopt_route_sort(const void *expert_ids, int32_t id_bytes, int64_t
     size_t smem = 0;
     if (need == 0) {
         if ((rc = sort_smem(who, dopt_route_sort_kernel, bins, &smem)) != DOPT_OK) return rc;
-        const unsigned blocks = a.slots <= kSortTile ? 1 : kSortCluster;
+        const unsigned blocks = a.slots <= kSortThreads * kSortRounds ? 1 : kSortCluster;
         return launch_cluster(who, dopt_route_sort_kernel, dim3(blocks), blocks, dim3(kSortThreads), smem, stream, a);
     }
     a.rounds = int32_t(sort_rounds(a.slots));
