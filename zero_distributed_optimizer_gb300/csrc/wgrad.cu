@@ -768,10 +768,14 @@ __global__ void __launch_bounds__(256) dopt_ckpt_wgrad_align_kernel(const T *dy,
 // How the work goes over `pairs` pairs of SMs: tiles of nb * 256 outputs,
 // whole waves of them tile by tile and the last, partial wave's tiles split
 // along the rows into parts.  Chosen for the least estimated time, in units
-// of one product of 64 rows: a step of nb products takes as long as 1.25 or
-// 2.1 of them (the codes are widened under one or under two products), the
-// stores of a tile 10 a block, waited for with nb = 2 and after the last
-// tile, the join's launch 12 and a part's trip through memory 0.2 a block.
+// of one product of 64 rows (0.295 us): a step takes 1.25 with nb = 1 (codes
+// are widened for one product) and 2.0 with nb = 2, a tile's stores 10 a block
+// (with nb = 1 they run under the next tile's products but slow them), the
+// join's launch 12 and a part's trip through memory 0.2 a block.  In us, with
+// nb = 1 and 2: 16384 rows x 5632 columns x 2048 outputs 224 and 199, 2048 x
+// 5632 x 2048 41.4 and 46.3, 4096 x 768 x 768 18.8 and 22.8, 8 experts of 4096
+// rows x 1024 x 4096 191 and 165, 64 of 1024 x 512 x 1408 94.4 and 93.1, 128 of
+// 1024 x 2048 x 768 348 and 353.
 struct Plan {
     int nb, parts;
     int64_t whole, tail;
@@ -783,9 +787,8 @@ Plan plan_wgrad(int64_t outs, int64_t cols, int n_groups, int64_t dy_rows, int64
     for (int nb = 1; nb <= 2; ++nb) {
         const int64_t tiles = (outs + kTileO * nb - 1) / (kTileO * nb) * ((cols + kTileC - 1) / kTileC) * n_groups;
         const int64_t tail = tiles % pairs;
-        const double step = nb == 1 ? 1.25 : 2.1, stores = 10.0 * nb;
-        const double each = steps * step + (nb == 2 ? stores : 0.0);
-        const double waves = double(tiles / pairs) * each + (nb == 1 ? stores : 0.0);
+        const double step = nb == 1 ? 1.25 : 2.0, each = steps * step + 10.0 * nb;
+        const double waves = double(tiles / pairs) * each;
         for (int parts = 1; parts <= kMaxSplit; ++parts) {
             // (groups go from long to short: the tail's tiles are the shortest)
             if (parts > 1 && (tail == 0 || (n_groups > 1 && tiles > pairs) || steps / parts < 4 || tail * parts * slot_floats(nb) * 4 > workspace_bytes))
