@@ -292,7 +292,9 @@ struct RowArgs {
 };
 
 // A warp takes 32 * U accesses of one token's row: read once, written to the
-// row of each of the token's k slots.
+// row of each of the token's k slots.  Bound by memory, mostly writing: 32768
+// tokens x 512 bf16 to 8 slots take 45 us (6.7 TB/s); of 511 columns, by 2-byte
+// accesses, 87 us.
 template <int VB, int U>
 __global__ void __launch_bounds__(kRowThreads) dopt_route_dispatch_kernel(const RowArgs a) {
     using V = typename Raw<VB>::type;
@@ -325,7 +327,9 @@ __global__ void __launch_bounds__(kRowThreads) dopt_route_dispatch_kernel(const 
 // the sum over the token's slots, in order, of weight * row, in fp32, rounded
 // once.  Dropped slots are left out (a weight of NaN there does not matter).
 // The rows of A slots are in flight at once, and the next token's slots and
-// weights are loaded under them.
+// weights are loaded under them.  Bound by memory: 32768 tokens x 512 bf16
+// from 8 slots take 47 us (6.4 TB/s); 61 us with the rows kept in L1, which
+// none is read from twice.
 template <typename T, int VB, int U, int A>
 __global__ void __launch_bounds__(kRowThreads) dopt_route_combine_kernel(const __grid_constant__ RowArgs a) {
     using V = typename Raw<VB>::type;
@@ -392,7 +396,9 @@ __global__ void __launch_bounds__(kRowThreads) dopt_route_combine_kernel(const _
 // A warp takes G neighbouring slots, and G others after them: d_row =
 // weight * d_out in one pass that also sums <d_out, row>.  The G slots' loads
 // are in flight at once, and the next ones' rows and weights are looked up
-// under them; d_out, read by all of a token's slots, mostly hits in L1.
+// under them; d_out, read by all of a token's slots, mostly hits in L1.  Bound
+// by memory, half of it writing: 95 us (6.1 TB/s) for 32768 tokens x 512 bf16
+// and 8 slots; 144 us with one slot a warp.
 template <typename T, int VB, int U, int G>
 __global__ void __launch_bounds__(kRowThreads) dopt_route_combine_grad_kernel(const __grid_constant__ RowArgs a) {
     using V = typename Raw<VB>::type;

@@ -34,6 +34,13 @@ namespace {
 // summed; NB = 2 for one tile of twice the outputs, so that codes are widened
 // once for two products, and its stores are waited for.  With lanes along c
 // the stores of a warp are contiguous.
+//
+// Long sums are bound by the tensor cores: 16384 rows x 5632 columns x 2048
+// outputs, bf16, take 198 us (1.90 PFLOP/s; 225 us, 1.68, where the card's
+// power limits it).  Many short groups are bound by the steps' latency (codes
+// of a step's rows arrive, are widened and fenced, 4 steps at a time) and by
+// the stores, together: 64 experts of about 1024 rows x 512 columns x 1408
+// outputs, fp32 grads, take 92 us (1.02 PFLOP/s, 4.0 TB/s).
 constexpr int kTileC = 256;          // of a pair
 constexpr int kTileO = 256;          // of a product; a tile has NB of them
 constexpr int kK = 64;               // rows a step
