@@ -144,6 +144,28 @@ def test_act_grad(rows, width, layout, act, dtype):
         assert torch.equal(d, d_in)
 
 
+@pytest.mark.parametrize("rows,cols,dtype", [
+    (1701, 4101, torch.bfloat16), (1701, 2051, torch.float32), (1531, 4112, torch.float16)], ids=str)
+def test_blocks_of_several_rows_in_turn(rows, cols, dtype):
+    """Enough rows for a thread block to take several groups of them, the last
+    ones short of a whole group: every row, kept, read back (by index too, from
+    the last row on) and through the activation gradients."""
+    half = dtype == torch.float16
+    x = _values(rows, cols, dtype, "normal", 3).clamp(-9, 9)
+    c, out = _save(x), torch.zeros_like(x)
+    kept = R.kept_values(R.f64(x), half)
+    dopt.dopt_ckpt_load(c, out)
+    assert np.array_equal(R.f64(out), kept)
+    index = torch.arange(rows - 1, -1, -1, dtype=torch.int32, device=DEV)
+    dopt.dopt_ckpt_load(c, out, row_index=index)
+    assert np.array_equal(R.f64(out), kept[::-1])
+    for act in ("gelu",) if cols % 2 else ("gelu", "swiglu"):
+        d = _values(rows, cols // 2 if act == "swiglu" else cols, dtype, "normal", 4)
+        dopt.dopt_ckpt_act_grad(c, act, d, out)
+        want, bound = R.act_grad(act, kept, R.f64(d))
+        R.close(out, want, bound, dtype, act)
+
+
 @pytest.mark.parametrize("act", ["silu", "gelu", "swiglu"])
 def test_act_grad_against_differences(act):
     """Central differences of the function itself at the kept values, in 64
