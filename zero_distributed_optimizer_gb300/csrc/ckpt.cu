@@ -16,7 +16,7 @@
 // Codes are always aligned (a row's pitch is a multiple of 128).  Rows of
 // whole, aligned groups have kernels without the checks for any others (94 us
 // with them).  Rows that are not go in aligned pieces all the same
-// (rows.cuh): 16384 x 5631 bf16, kept and read back, 121 us (585 us one
+// (rows.cuh): 16384 x 5631 bf16, kept and read back, 113 us (585 us one
 // element at a time).
 #include "rows.cuh"
 
@@ -122,28 +122,35 @@ struct Kept {
 // The 8 kept values from any column on (the gated half of an odd width):
 // codes from the aligned 8 bytes around them, exponents of up to two blocks.
 // Nothing past the row's pitch is read.
-__device__ __forceinline__ void load_kept_any(const CkptArgs &a, uint32_t r, int c, float (&f)[8]) {
-    const uint64_t at = kept_at(a, r, c & ~7);
-    const uint32_t bytes = c & 7;
-    const uint2 lo = __ldcs(reinterpret_cast<const uint2 *>(a.codes + at));
-    uint2 hi = make_uint2(0, 0);
-    if (bytes && (c & ~7) + 8 < a.pitch) hi = __ldcs(reinterpret_cast<const uint2 *>(a.codes + at + 8));
-    const uint4 w = shift_down(make_uint4(lo.x, lo.y, hi.x, hi.y), make_uint4(0, 0, 0, 0), bytes);
-    const uint64_t block = kept_at(a, r, c) / kBlock;
-    const uint32_t first = a.scales[block];
-    const int in_first = kBlock - (c & (kBlock - 1));
-    code_values(w.x, first, f);
-    code_values(w.y, first, f + 4);
-    if (in_first < 8 && c + in_first < a.pitch) {
-        float g[8];
-        const uint32_t second = a.scales[block + 1];
-        code_values(w.x, second, g);
-        code_values(w.y, second, g + 4);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i >= in_first) f[i] = g[i];
+struct KeptAny {
+    uint2 lo, hi;
+    uint32_t first, second, bytes, in_first;
+    __device__ __forceinline__ void load(const CkptArgs &a, uint32_t r, int c, bool some) {
+        bytes = c & 7;
+        in_first = kBlock - (c & (kBlock - 1));
+        lo = hi = make_uint2(0, 0);
+        first = second = 1;
+        if (!some) return;
+        const uint64_t at = kept_at(a, r, c & ~7), block = kept_at(a, r, c) / kBlock;
+        lo = __ldcs(reinterpret_cast<const uint2 *>(a.codes + at));
+        if (bytes && (c & ~7) + 8 < a.pitch) hi = __ldcs(reinterpret_cast<const uint2 *>(a.codes + at + 8));
+        first = a.scales[block];
+        if (in_first < 8 && c + int(in_first) < a.pitch) second = a.scales[block + 1];
     }
-}
+    __device__ __forceinline__ void get(float (&f)[8]) const {
+        const uint4 w = shift_down(make_uint4(lo.x, lo.y, hi.x, hi.y), make_uint4(0, 0, 0, 0), bytes);
+        code_values(w.x, first, f);
+        code_values(w.y, first, f + 4);
+        if (in_first < 8) {
+            float g[8];
+            code_values(w.x, second, g);
+            code_values(w.y, second, g + 4);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i >= int(in_first)) f[i] = g[i];
+        }
+    }
+};
 
 // A block of 32 columns is 32 / COLS neighbouring threads.  The step is the
 // power of two 2^k with the largest magnitude in [64, 128) steps (k no less
@@ -165,19 +172,21 @@ __global__ void __launch_bounds__(kCkptThreads) dopt_ckpt_save_kernel(const __gr
     const uint32_t step = blockDim.y, first = blockIdx.y * step * a.turns;
     const uint32_t end = min(first + step * a.turns, uint32_t(a.rows));
     Values<T, COLS> x;
+    typename Values<T, COLS>::Ahead ahead;
     auto load = [&](uint32_t r) {
         const bool here = r < uint32_t(a.rows);
         const T *row = static_cast<const T *>(a.x) + (here ? int64_t(r) * a.ld : 0);
         if constexpr (WHOLE)
             x.load_whole(row, c, here && c < a.cols);
         else
-            x.load(row, c, here ? a.cols : 0, a.vec, lane, bx);
+            x.fetch(ahead, row, c, here ? a.cols : 0, a.vec, lane, bx);
     };
     load(first + threadIdx.y);
     for (uint32_t r0 = first; r0 < end; r0 += step) {
         const uint32_t r = r0 + threadIdx.y;
         const bool here = r < uint32_t(a.rows);
         float f[COLS];
+        if constexpr (!WHOLE) x.take(ahead, a.vec, lane, bx);
         x.get(f);
         if (r0 + step < end) load(r + step);
         uint32_t top = 0;
@@ -370,20 +379,26 @@ __global__ void __launch_bounds__(kCkptThreads) dopt_ckpt_act_grad_kernel(const 
     const int width = ACT == DOPT_ACT_SWIGLU ? a.half : a.cols;
     const uint32_t step = blockDim.y, first = blockIdx.y * step * a.turns;
     const uint32_t end = min(first + step * a.turns, uint32_t(a.rows));
+    Values<T, COLS> x;
+    typename Values<T, COLS>::Ahead ahead;
+    Kept<COLS> kept_h;
+    KeptAny kept_u;
+    auto load = [&](uint32_t r) {
+        const bool here = r < uint32_t(a.rows), some = here && c < width;
+        x.fetch(ahead, static_cast<const T *>(a.x) + (here ? int64_t(r) * a.ld : 0), c, here ? width : 0, a.vec, lane, bx);
+        kept_h.load(a, some ? r : ~0u, c);
+        if constexpr (ACT == DOPT_ACT_SWIGLU) kept_u.load(a, r, width + c, some);
+    };
+    load(first + threadIdx.y);
     for (uint32_t r0 = first; r0 < end; r0 += step) {
         const uint32_t r = r0 + threadIdx.y;
         const bool here = r < uint32_t(a.rows);
-        Values<T, COLS> x;
-        x.load(static_cast<const T *>(a.x) + (here ? int64_t(r) * a.ld : 0), c, here ? width : 0, a.vec, lane, bx);
-        float h[COLS] = {}, u[COLS] = {};
-        if (here && c < width) {
-            Kept<COLS> kept;
-            kept.load(a, r, c);
-            kept.get(h);
-            if constexpr (ACT == DOPT_ACT_SWIGLU) load_kept_any(a, r, width + c, u);
-        }
-        float d[COLS];
+        float d[COLS], h[COLS], u[COLS];
+        x.take(ahead, a.vec, lane, bx);
         x.get(d);
+        kept_h.get(h);
+        if constexpr (ACT == DOPT_ACT_SWIGLU) kept_u.get(u);
+        if (r0 + step < end) load(r + step);
         T *out = static_cast<T *>(a.out) + (here ? int64_t(r) * a.ld_out : 0);
         act_grad<T, ACT>(d, h, u);
         Values<T, COLS> y;
@@ -442,8 +457,8 @@ CkptArgs ckpt_args(const void *ckpt, int64_t rows, int64_t cols) {
 // an SM.  Whole rows are saved and read back in one turn (16384 x 5632 bf16:
 // 86 us; 87 in two turns, 92 in four); there is arithmetic to hide the next
 // loads under in the others: the gated gradient takes 135, 125, 122.5 and 124
-// us in 1, 2, 4 and 8 turns, 16384 x 5631 saved and read back 136, 126, 121
-// and 123.
+// us in 1, 2, 4 and 8 turns, 16384 x 5631 saved and read back 130, 116, 113
+// and 116.
 template <typename Kernel>
 int launch_rows(const char *who, Kernel kernel, CkptArgs a, int64_t cols, int each, int64_t rows, int turns,
                 cudaStream_t stream) {

@@ -74,23 +74,38 @@ struct Values {
     static constexpr int kPieces = COLS / kPer;
     uint4 raw[kPieces];
 
+    // What is read for them, in flight until take(): the pieces around the
+    // values, and the one after them where no neighbour has it.
+    struct Ahead {
+        uint4 raw[kPieces], last;
+        uint32_t off;  // bytes from the first piece to the first value
+    };
+
     // Values from column c on; those at or past `cols` (0 where there is no row) are 0.
-    __device__ __forceinline__ void load(const T *row, int c, int cols, bool vec, int lane, int bx) {
+    static __device__ __forceinline__ void fetch(Ahead &a, const T *row, int c, int cols, bool vec, int lane, int bx) {
+        a.off = vec ? 0 : uint32_t(reinterpret_cast<uintptr_t>(row + c) & 15);
+        const int e = c - int(a.off / sizeof(T));
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) a.raw[i] = load_piece(row, e + i * kPer, cols);
+        a.last = make_uint4(0, 0, 0, 0);
+        if (!vec && lane == bx - 1) a.last = load_piece(row, e + COLS, cols);
+    }
+    __device__ __forceinline__ void take(const Ahead &a, bool vec, int lane, int bx) {
         if (vec) {
 #pragma unroll
-            for (int i = 0; i < kPieces; ++i) raw[i] = load_piece(row, c + i * kPer, cols);
+            for (int i = 0; i < kPieces; ++i) raw[i] = a.raw[i];
         } else {
-            const uint32_t off = uint32_t(reinterpret_cast<uintptr_t>(row + c) & 15);
-            const int e = c - int(off / sizeof(T));
+            uint4 next = shuffle_down(a.raw[0], bx);
+            if (lane == bx - 1) next = a.last;
 #pragma unroll
-            for (int i = 0; i < kPieces; ++i) raw[i] = load_piece(row, e + i * kPer, cols);
-            uint4 next = shuffle_down(raw[0], bx);
-            if (lane == bx - 1) next = load_piece(row, e + COLS, cols);
-#pragma unroll
-            for (int i = 0; i < kPieces; ++i) raw[i] = shift_down(raw[i], i + 1 < kPieces ? raw[i + 1] : next, off);
+            for (int i = 0; i < kPieces; ++i) raw[i] = shift_down(a.raw[i], i + 1 < kPieces ? a.raw[i + 1] : next, a.off);
         }
     }
-
+    __device__ __forceinline__ void load(const T *row, int c, int cols, bool vec, int lane, int bx) {
+        Ahead a;
+        fetch(a, row, c, cols, vec, lane, bx);
+        take(a, vec, lane, bx);
+    }
     // The same where c and the row are aligned and all COLS values are there (or none: `some` false).
     __device__ __forceinline__ void load_whole(const T *row, int c, bool some) {
 #pragma unroll
