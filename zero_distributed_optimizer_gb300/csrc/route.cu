@@ -293,8 +293,8 @@ struct RowArgs {
 
 // A warp takes 32 * U accesses of one token's row: read once, written to the
 // row of each of the token's k slots.  Bound by memory, mostly writing: 32768
-// tokens x 512 bf16 to 8 slots take 45 us (6.7 TB/s); of 511 columns, by 2-byte
-// accesses, 87 us.
+// tokens x 512 bf16 to 8 slots take 45 us (6.7 TB/s).  With the sort 56 us; 60
+// us for 510 columns (4-byte accesses), 101 us for 511 (2-byte ones).
 template <int VB, int U>
 __global__ void __launch_bounds__(kRowThreads) dopt_route_dispatch_kernel(const RowArgs a) {
     using V = typename Raw<VB>::type;
@@ -328,8 +328,8 @@ __global__ void __launch_bounds__(kRowThreads) dopt_route_dispatch_kernel(const 
 // once.  Dropped slots are left out (a weight of NaN there does not matter).
 // The rows of A slots are in flight at once, and the next token's slots and
 // weights are loaded under them.  Bound by memory: 32768 tokens x 512 bf16
-// from 8 slots take 47 us (6.4 TB/s); 61 us with the rows kept in L1, which
-// none is read from twice.
+// from 8 slots take 47 us (6.4 TB/s; 61 us with the rows kept in L1, though
+// none is read twice); 59 us for 510 columns, 82 us for 511.
 template <typename T, int VB, int U, int A>
 __global__ void __launch_bounds__(kRowThreads) dopt_route_combine_kernel(const __grid_constant__ RowArgs a) {
     using V = typename Raw<VB>::type;
@@ -397,8 +397,8 @@ __global__ void __launch_bounds__(kRowThreads) dopt_route_combine_kernel(const _
 // weight * d_out in one pass that also sums <d_out, row>.  The G slots' loads
 // are in flight at once, and the next ones' rows and weights are looked up
 // under them; d_out, read by all of a token's slots, mostly hits in L1.  Bound
-// by memory, half of it writing: 95 us (6.1 TB/s) for 32768 tokens x 512 bf16
-// and 8 slots; 144 us with one slot a warp.
+// by memory, half of it writing: 95 us (6.0 TB/s) for 32768 tokens x 512 bf16
+// and 8 slots; 115 us for 510 columns, 149 us for 511.
 template <typename T, int VB, int U, int G>
 __global__ void __launch_bounds__(kRowThreads) dopt_route_combine_grad_kernel(const __grid_constant__ RowArgs a) {
     using V = typename Raw<VB>::type;
@@ -533,7 +533,8 @@ int launch_dispatch(const char *who, const RowArgs &a, cudaStream_t stream) {
 }
 
 // Blocks for `blocks` blocks' work: at most 6 an SM's worth, each taking
-// several tokens in turn.
+// several tokens in turn (32768 tokens x 512 bf16, 8 slots, combine and its
+// gradient: 47 and 95 us; 4 an SM 55 and 119, 12 an SM 48 and 96).
 unsigned row_blocks(int64_t blocks) { return unsigned(std::min<int64_t>(blocks, 152 * 6)); }
 
 template <typename T, int VB, int U, int A>
@@ -542,7 +543,8 @@ int launch_combine(const char *who, const RowArgs &a, cudaStream_t stream) {
     return launch_op(who, dopt_route_combine_kernel<T, VB, U, A>, grid, dim3(kRowThreads), 0, stream, a);
 }
 
-// Slots in flight: 2 for up to 2 a token, 4 otherwise.
+// Slots in flight: 2 for up to 2 a token, 4 otherwise (47 us for 8 a token; 8
+// in flight 48.5).
 template <typename T, int VB, int U>
 int pick_ahead(const char *who, const RowArgs &a, cudaStream_t stream) {
     return a.k <= 2 ? launch_combine<T, VB, U, 2>(who, a, stream) : launch_combine<T, VB, U, 4>(who, a, stream);
@@ -563,6 +565,8 @@ int launch_combine_grad(const char *who, const RowArgs &a, cudaStream_t stream) 
     return launch_op(who, dopt_route_combine_grad_kernel<T, VB, U, G>, grid, dim3(kRowThreads), 0, stream, a);
 }
 
+// G = 2 slots a warp with 16-byte accesses, two of each row at a time: 95 us
+// where one slot takes 128 and four, one access each, 108.
 template <typename T>
 int pick_combine_grad(const char *who, const RowArgs &a, int vb, cudaStream_t stream) {
     if (vb == 16) return launch_combine_grad<T, 16, 2, 2>(who, a, stream);
