@@ -771,7 +771,12 @@ int dopt_ckpt_act_grad(const void *ckpt, int64_t rows, int64_t cols, dopt_act ac
  *         sum over rows r in [offsets[g], offsets[g + 1]) of
  *             dy[r][o] * x[row_token[r]][c]
  * with the kept values x, products exact, sums in fp32, and one rounding to
- * the grad type (after adding the old grad, with DOPT_WGRAD_ACCUMULATE).  A
+ * the grad type (after adding the old grad, with DOPT_WGRAD_ACCUMULATE).  The
+ * tensor cores' sums cut off low bits every 16 rows, so fp32 grads add sums of
+ * 1024 rows (512 with fp16 dy) up in fp32, rounding to nearest: off by about
+ * 4e-7 of the grads' size at any number of rows.  16-bit grads take up to
+ * 131072 rows (bf16) or 16384 (fp16) in one sum, which is then off by at most an
+ * eighth of their own rounding.  A
  * group without rows gets zeros (is left alone with DOPT_WGRAD_ACCUMULATE).
  * Rows of dy outside every group are not read as values.
  *   ckpt          checkpoint of x, [x_rows][cols], saved from ckpt_dtype

@@ -35,12 +35,22 @@ namespace {
 // once for two products, and its stores are waited for.  With lanes along c
 // the stores of a warp are contiguous.
 //
+// The tensor cores add 16 rows' products to a sum at a time and cut off what
+// its 24 bits do not hold, always toward zero: the error of one long sum grows
+// as its rows do (fp32 grads of 16384 rows were 1.1e-5 off with bf16 dy, 1.8e-5
+// with fp16, where fp32 additions that round are off by 2-7e-7).  So a sum takes
+// `chunk` steps; the four storing warps then add it to the tile's first sum,
+// rounding to nearest, and it starts anew.  Both are in tensor memory, with
+// NB = 1: the other buffer, once the tile before is stored.  sum_chunk has
+// the rows and why.  16384 rows x 5632 columns x 2048 outputs with fp32 grads
+// take 254 us so (195 in one sum of NB = 2).
+//
 // Long sums are bound by the tensor cores: 16384 rows x 5632 columns x 2048
 // outputs, bf16, take 198 us (1.90 PFLOP/s; 225 us, 1.68, where the card's
 // power limits it).  Many short groups are bound by the steps' latency (codes
 // of a step's rows arrive, are widened and fenced, 4 steps at a time) and by
 // the stores, together: 64 experts of about 1024 rows x 512 columns x 1408
-// outputs, fp32 grads, take 92 us (1.02 PFLOP/s, 4.0 TB/s).
+// outputs, fp32 grads, take 99 us (0.95 PFLOP/s, 3.8 TB/s; 93 in one sum).
 constexpr int kTileC = 256;          // of a pair
 constexpr int kTileO = 256;          // of a product; a tile has NB of them
 constexpr int kK = 64;               // rows a step
@@ -89,6 +99,7 @@ struct WgradArgs {
     int32_t items;             // tiles and parts of tiles
     int32_t whole;             // tiles before the split ones
     int32_t split;             // parts of a split tile
+    int32_t chunk;             // steps of a sum
     int32_t accumulate;
     int32_t tma, vec;          // dy by TMA; dy's rows are 16-byte aligned
     int32_t grad_dtype;
@@ -396,6 +407,31 @@ __device__ __forceinline__ void wait_sums(uint32_t (&r)[16]) {
                  : "memory");
 }
 
+// 16 columns back to tensor memory, in flight until tcgen05.wait::st.
+__device__ __forceinline__ void put_sums(uint32_t at, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16};" ::"r"(at),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+// A warp's 32 lanes of the sums at `from` added to those at `into`.
+__device__ __forceinline__ void add_tile(uint32_t into, uint32_t from, int outs) {
+    for (int o = 0; o < outs; o += 16) {  // (outs is a multiple of 32)
+        uint32_t r[16], more[16];
+        load_sums(into + uint32_t(o), r);
+        load_sums(from + uint32_t(o), more);
+        wait_sums(r);
+        wait_sums(more);
+#pragma unroll
+        for (int q = 0; q < 16; ++q) r[q] = __float_as_uint(__uint_as_float(r[q]) + __uint_as_float(more[q]));
+        put_sums(into + uint32_t(o), r);
+    }
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
 // A tile's sums of a warp's 32 columns, at `sums` in tensor memory, to the grads.
 template <typename G>
 __device__ __forceinline__ void store_tile(const WgradArgs &a, const WgradItem &it, int c, int outs, uint32_t sums) {
@@ -524,6 +560,7 @@ __global__ void __launch_bounds__(kWgradThreads, 1) __cluster_dims__(2, 1, 1)
             const uint32_t base = uniform(tmem);
             const uint64_t x0 = slab_descriptor(smem_of(x_ring)), dy0 = slab_descriptor(smem_of(dy_ring));
             int n = 0, u = 0, t = 0;
+            uint32_t used = 0, odd = 0;  // bit per buffer: used before, an odd number of times
             bool ok = true;
             for (int round = 0, item; ok && (item = item_number(a, round)) >= 0; ++round) {
                 const WgradItem it = item_of<NB>(a, groups, item);
@@ -533,12 +570,21 @@ __global__ void __launch_bounds__(kWgradThreads, 1) __cluster_dims__(2, 1, 1)
                 const int blocks = it.blocks;
                 const uint32_t idesc[2] = {kInstruction | (uint32_t(block_outs(a, it, 0) >> 3) << 17),
                                            kInstruction | (uint32_t(blocks > 1 ? block_outs(a, it, 1) >> 3 : 0) << 17)};
-                const int buffer = NB == 1 ? t & 1 : 0, use = NB == 1 ? t >> 1 : t;
-                const uint32_t sums = base + uint32_t(buffer * kTileO);
-                if (use > 0) ok = __all_sync(kFull, wait_phase(b, b.sum_empty[buffer], uint32_t(use - 1) & 1));
-                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                for (int i = 0; i < steps && ok; ++i, ++n) {
+                int buffer = NB == 1 ? t & 1 : 0, left = 0;  // steps left of the sum
+                uint32_t sums = base;
+                for (int i = 0; i < steps && ok; ++i, ++n, --left) {
                     const int sx = n % kXRing;
+                    const bool fresh = left == 0;
+                    if (fresh) {  // the tile's first sum, or the next one, in the other buffer
+                        if (NB == 1 && i > 0) buffer = ~t & 1;
+                        if (used >> buffer & 1)
+                            ok = __all_sync(kFull, wait_phase(b, b.sum_empty[buffer], ~(odd >> buffer) & 1));
+                        used |= 1u << buffer, odd ^= 1u << buffer;
+                        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                        sums = base + uint32_t(buffer * kTileO);
+                        left = min(a.chunk, steps - i);
+                        if (!ok) break;
+                    }
                     ok = __all_sync(kFull, wait_phase(b, b.x_full[sx], uint32_t(n / kXRing) & 1));
                     const uint64_t da = x0 + uint64_t(sx * (kStage >> 4));
 #pragma unroll
@@ -555,15 +601,15 @@ __global__ void __launch_bounds__(kWgradThreads, 1) __cluster_dims__(2, 1, 1)
 #pragma unroll
                                 for (int k = 0; k < 4; ++k)
                                     product(sums + uint32_t(nb * kTileO), da + uint64_t(k * 128), db + uint64_t(k * 128),
-                                            idesc[nb], i > 0 || k > 0);
+                                            idesc[nb], !fresh || k > 0);
                             } else {
                                 for (int k = 0; k < rest; ++k)
                                     product(sums + uint32_t(nb * kTileO), da + uint64_t(k * 128), db + uint64_t(k * 128),
-                                            idesc[nb], i > 0 || k > 0);
+                                            idesc[nb], !fresh || k > 0);
                             }
                             commit(b.dy_empty[sd]);
                             if (nb == blocks - 1) commit(b.x_empty[sx]);
-                            if (nb == blocks - 1 && i == steps - 1) commit(b.sum_full[buffer]);
+                            if (nb == blocks - 1 && left == 1) commit(b.sum_full[buffer]);
                         }
                         __syncwarp();
                     }
@@ -576,18 +622,31 @@ __global__ void __launch_bounds__(kWgradThreads, 1) __cluster_dims__(2, 1, 1)
         const int m = int(rank) * (kTileC / 2) + (warp & 3) * 32 + lane;
         const uint32_t lanes = tmem + (uint32_t((warp & 3) * 32) << 16);
         int t = 0;
+        uint32_t odd = 0;  // bit per buffer: used an odd number of times
         bool ok = true;
+        auto release = [&](int buffer) {
+            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) arrive_remote(leader_address(smem_of(&b.sum_empty[buffer])));
+        };
         for (int k = 0, item; ok && (item = item_number(a, k)) >= 0; ++k) {
             const WgradItem it = item_of<NB>(a, groups, item);
-            const int buffer = NB == 1 ? t & 1 : 0, use = NB == 1 ? t >> 1 : t;
-            if (it.steps > 0) {
-                ok = wait_phase<200>(b, b.sum_full[buffer], uint32_t(use) & 1);
-                if (!__all_sync(kFull, ok)) break;
-                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            }
             const int c = it.c0 + column_of(m);
             const int outs = (it.blocks - 1) * kTileO + block_outs(a, it, it.blocks - 1);
+            const int buffer = NB == 1 ? t & 1 : 0;
             const uint32_t sums = lanes + uint32_t(buffer * kTileO);
+            for (int i = 0; i < it.steps; i += a.chunk) {
+                const int from = NB == 1 && i > 0 ? buffer ^ 1 : buffer;
+                ok = __all_sync(kFull, wait_phase<200>(b, b.sum_full[from], odd >> from & 1));
+                if (!ok) break;
+                odd ^= 1u << from;
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                if (i > 0) {
+                    add_tile(sums, lanes + uint32_t(from * kTileO), outs);
+                    release(from);
+                }
+            }
+            if (!ok) break;
             if (it.slot >= 0) {
                 float *p = a.partial + it.slot * slot_floats(NB) + m;
                 for (int o = 0; o < outs; o += 16) {
@@ -604,9 +663,7 @@ __global__ void __launch_bounds__(kWgradThreads, 1) __cluster_dims__(2, 1, 1)
                 store_tile<__half>(a, it, c, outs, sums);
             }
             if (it.steps > 0) {
-                asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) arrive_remote(leader_address(smem_of(&b.sum_empty[buffer])));
+                release(buffer);
                 ++t;
             }
         }
@@ -794,24 +851,32 @@ __global__ void __launch_bounds__(256) dopt_ckpt_wgrad_align_kernel(const T *dy,
 // nb = 1 and 2: 16384 rows x 5632 columns x 2048 outputs 224 and 199, 2048 x
 // 5632 x 2048 41.4 and 46.3, 4096 x 768 x 768 18.8 and 22.8, 8 experts of 4096
 // rows x 1024 x 4096 191 and 165, 64 of 1024 x 512 x 1408 94.4 and 93.1, 128 of
-// 1024 x 2048 x 768 348 and 353.
+// 1024 x 2048 x 768 348 and 353 (all in one sum a tile).
+// A tile whose sum takes several chunks has nb = 1 (nb = 2 leaves no
+// tensor memory to start another sum in); adding one up stops the products for
+// 2.5.
 struct Plan {
     int nb, parts;
     int64_t whole, tail;
 };
-Plan plan_wgrad(int64_t outs, int64_t cols, int n_groups, int64_t dy_rows, int64_t pairs, int64_t workspace_bytes) {
+Plan plan_wgrad(int64_t outs, int64_t cols, int n_groups, int64_t dy_rows, int64_t chunk, int64_t pairs,
+                int64_t workspace_bytes) {
     const double steps = double(dy_rows / n_groups + kK - 1) / kK;
+    // (of several groups, one may have all the rows)
+    const int64_t longest = (dy_rows + kK - 1) / kK;
     Plan best{};
     double least = -1;
     for (int nb = 1; nb <= 2; ++nb) {
         const int64_t tiles = (outs + kTileO * nb - 1) / (kTileO * nb) * ((cols + kTileC - 1) / kTileC) * n_groups;
         const int64_t tail = tiles % pairs;
-        const double step = nb == 1 ? 1.25 : 2.0, each = steps * step + 10.0 * nb;
+        const double step = nb == 1 ? 1.25 + 2.5 / double(chunk) : 2.0, each = steps * step + 10.0 * nb;
         const double waves = double(tiles / pairs) * each;
         for (int parts = 1; parts <= kMaxSplit; ++parts) {
             // (groups go from long to short: the tail's tiles are the shortest)
             if (parts > 1 && (tail == 0 || (n_groups > 1 && tiles > pairs) || steps / parts < 4 || tail * parts * slot_floats(nb) * 4 > workspace_bytes))
                 break;
+            // (a tail's parts are shorter than the whole tiles that there are besides)
+            if (nb == 2 && longest > chunk * (n_groups > 1 || tiles > tail ? 1 : parts)) continue;
             double t = waves + double((tail * parts + pairs - 1) / pairs) * (each - steps * step + steps * step / parts);
             if (parts > 1) t += 12.0 + 0.2 * nb * double(tail * parts);
             if (least < 0 || t < least) {
@@ -821,6 +886,17 @@ Plan plan_wgrad(int64_t outs, int64_t cols, int n_groups, int64_t dy_rows, int64
         }
     }
     return best;
+}
+
+// Rows of one sum, in steps of 64.  fp32 grads: 1024 with bf16 dy and 512 with
+// fp16, whose products have more bits to lose; errors are then 3.2e-7 and
+// 4.2e-7 of the grads' size at any number of rows (random signs), and no more
+// than 64 * 2^-23 of the sum of magnitudes in a chunk.  16-bit grads take as
+// many rows as lose an eighth of their rounding: fp16 16384 (1.8e-5), bf16
+// 131072.
+int64_t sum_chunk(dopt_dtype dy, dopt_dtype grad) {
+    if (grad == DOPT_FP32) return dy == DOPT_BF16 ? 1024 / kK : 512 / kK;
+    return grad == DOPT_FP16 ? 16384 / kK : 131072 / kK;
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
@@ -1006,7 +1082,8 @@ extern "C" int dopt_ckpt_wgrad(const void *ckpt, dopt_dtype ckpt_dtype, int64_t 
                                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
         a.tma = r == CUDA_SUCCESS;  // a stride past the map's limit: plain loads
     }
-    const Plan plan = plan_wgrad(outs, cols, n_groups, dy_rows, pairs, workspace_bytes);
+    a.chunk = int32_t(sum_chunk(dy_dtype, grad_dtype));
+    const Plan plan = plan_wgrad(outs, cols, n_groups, dy_rows, a.chunk, pairs, workspace_bytes);
     const int64_t items = plan.whole + plan.tail * plan.parts;
     if (items > INT32_MAX / 2) return fail(DOPT_E_ARG, "%s: %lld tiles", who, static_cast<long long>(items));
     a.tiles_c = int32_t((cols + kTileC - 1) / kTileC);
@@ -1032,10 +1109,14 @@ extern "C" int dopt_ckpt_wgrad_workspace(int64_t dy_rows, int64_t outs, int64_t 
         return dopt::fail(DOPT_E_ARG, "%s: %lld rows, %lld x %lld, %d groups", who,
                           static_cast<long long>(dy_rows), static_cast<long long>(outs),
                           static_cast<long long>(cols), n_groups);
-    // for a device of 76 pairs of SMs; a call takes what it is given
-    const Plan plan = plan_wgrad(outs, cols, n_groups, dy_rows, 76, INT64_MAX);
-    *bytes = plan.tail * plan.parts * slot_floats(plan.nb) * int64_t(sizeof(float)) +
-             (outs % 8 != 0 ? copy_bytes(dy_rows, outs) : 0);
+    // for a device of 76 pairs of SMs and the types that take most; a call takes what it is given
+    int64_t most = 0;
+    for (dopt_dtype dy : {DOPT_BF16, DOPT_FP16})
+        for (dopt_dtype grad : {DOPT_BF16, DOPT_FP16, DOPT_FP32}) {
+            const Plan plan = plan_wgrad(outs, cols, n_groups, dy_rows, sum_chunk(dy, grad), 76, INT64_MAX);
+            most = std::max(most, plan.tail * plan.parts * slot_floats(plan.nb) * int64_t(sizeof(float)));
+        }
+    *bytes = most + (outs % 8 != 0 ? copy_bytes(dy_rows, outs) : 0);
     return DOPT_OK;
 }
 
