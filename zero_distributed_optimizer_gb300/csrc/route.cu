@@ -3,6 +3,8 @@
 // places (dopt_route_dispatch), the weighted sum of the experts' rows
 // (dopt_route_combine) and its gradients (dopt_route_combine_grad).  dopt.h
 // states their contracts.
+#include <mutex>
+
 #include "op_common.cuh"
 
 namespace {
@@ -488,12 +490,26 @@ int64_t sort_workspace(int64_t slots, int32_t experts) {
     return slots > kClusterSlots ? sort_tiles(slots) * (experts + 1) * int64_t(sizeof(int32_t)) : 0;
 }
 
-// The sorting kernels' shared memory; its limit is raised where it is past
-// the default.
-int sort_smem(const char *who, void (*kernel)(SortArgs), size_t bins, size_t *bytes) {
-    *bytes = (3 + kSortWarps) * bins * sizeof(int32_t);
-    if (*bytes <= 48 * 1024) return DOPT_OK;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(*bytes));
+// Bytes of the sorting kernels' shared memory.
+constexpr size_t sort_smem(size_t bins) { return (3 + kSortWarps) * bins * sizeof(int32_t); }
+
+std::mutex g_sort_mutex;
+bool g_sort_ready[64] = {};  // devices whose kernels are set up
+
+// Raises the sorting kernels' shared-memory limit, once a device and to what
+// the most experts need: the limit is the kernel's, for all threads and calls.
+int set_up_sort(const char *who) {
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e == cudaSuccess && (device < 0 || device >= 64)) return dopt::fail(DOPT_E_ARG, "%s: device %d", who, device);
+    std::lock_guard<std::mutex> lock(g_sort_mutex);
+    if (e == cudaSuccess && !g_sort_ready[device]) {
+        constexpr int kMost = int(sort_smem(DOPT_MAX_EXPERTS + 1));
+        e = cudaFuncSetAttribute(dopt_route_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(dopt_route_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+        g_sort_ready[device] = e == cudaSuccess;
+    }
     if (e != cudaSuccess) {
         cudaGetLastError();
         return dopt::fail(DOPT_E_CUDA, "%s: shared-memory limit: %s", who, cudaGetErrorString(e));
@@ -627,10 +643,9 @@ extern "C" int dopt_route_sort(const void *expert_ids, int32_t id_bytes, int64_t
     a.k = k;
     a.experts = n_experts;
     a.wide = id_bytes == 8;
-    const size_t bins = size_t(n_experts) + 1;
-    size_t smem = 0;
+    const size_t bins = size_t(n_experts) + 1, smem = sort_smem(bins);
+    if ((rc = set_up_sort(who)) != DOPT_OK) return rc;
     if (need == 0) {
-        if ((rc = sort_smem(who, dopt_route_sort_kernel, bins, &smem)) != DOPT_OK) return rc;
         const unsigned blocks = a.slots <= kSortThreads * kSortRounds ? 1 : kSortCluster;
         return launch_cluster(who, dopt_route_sort_kernel, dim3(blocks), blocks, dim3(kSortThreads), smem, stream, a);
     }
@@ -639,7 +654,6 @@ extern "C" int dopt_route_sort(const void *expert_ids, int32_t id_bytes, int64_t
     rc = launch_op(who, dopt_route_count_kernel, dim3(unsigned(a.tiles)), dim3(kSortThreads), bins * sizeof(int32_t),
                    stream, a);
     if (rc != DOPT_OK) return rc;
-    if ((rc = sort_smem(who, dopt_route_place_kernel, bins, &smem)) != DOPT_OK) return rc;
     return launch_op(who, dopt_route_place_kernel, dim3(unsigned(a.tiles)), dim3(kSortThreads), smem, stream, a);
 }
 
