@@ -622,8 +622,9 @@ int dopt_step_clipped_noalloc(const dopt_layout *layout, const dopt_adam_cfg *cf
 #define DOPT_MAX_COLS 4194304
 
 /*
- * Bytes of workspace that dopt_route_sort needs for these sizes (0 up to
- * 32768 slots).  Host only.  Errors: DOPT_E_ARG.
+ * Bytes of workspace that are enough for dopt_route_sort of these sizes and of
+ * any fewer tokens (0 up to 32768 slots; it never falls as slots or experts
+ * grow).  Host only.  Errors: DOPT_E_ARG.
  */
 int dopt_route_workspace(int64_t tokens, int32_t k, int32_t n_experts, int64_t *bytes);
 

@@ -71,3 +71,15 @@ def test_threads_with_different_numbers_of_experts():
         assert not isinstance(out[experts], Exception), out[experts]
         for a, b in zip(out[experts], R.sort(ids, experts)):
             assert np.array_equal(a.cpu().numpy(), b)
+
+
+@pytest.mark.parametrize("large,small", [(700000, 600000), (622593, 622592), (1245185, 1245184), (2000000, 40000)])
+def test_a_larger_batchs_workspace(large, small):
+    ws = dopt.route_workspace(large, 1, 5)
+    ids = torch.randint(0, 5, (small, 1), generator=torch.Generator(device=DEV).manual_seed(small), device=DEV)
+    slot_row, row_token = (torch.empty(s, dtype=torch.int32, device=DEV) for s in ((small, 1), (small,)))
+    offsets = torch.empty(6, dtype=torch.int32, device=DEV)
+    dopt.dopt_route_sort(ids, 5, slot_row, row_token, offsets, ws)
+    key, order = torch.sort(ids.reshape(-1), stable=True)
+    assert torch.equal(row_token, order.int())
+    assert torch.equal(offsets, torch.searchsorted(key, torch.arange(6, device=DEV)).int())

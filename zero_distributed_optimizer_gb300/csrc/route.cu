@@ -486,8 +486,17 @@ int64_t sort_tiles(int64_t slots) {
     return (slots + tile - 1) / tile;
 }
 
+// What a call uses.
 int64_t sort_workspace(int64_t slots, int32_t experts) {
     return slots > kClusterSlots ? sort_tiles(slots) * (experts + 1) * int64_t(sizeof(int32_t)) : 0;
+}
+
+// What any call of up to so many slots uses: with more than 304 stretches'
+// slots they get longer and, at first, fewer.
+int64_t sort_workspace_up_to(int64_t slots, int32_t experts) {
+    if (slots <= kClusterSlots) return 0;
+    const int64_t tiles = std::min<int64_t>(kSortMaxTiles, (slots + kSortTile - 1) / kSortTile);
+    return tiles * (experts + 1) * int64_t(sizeof(int32_t));
 }
 
 // Bytes of the sorting kernels' shared memory.
@@ -602,7 +611,7 @@ extern "C" int dopt_route_workspace(int64_t tokens, int32_t k, int32_t n_experts
     if (rc != DOPT_OK) return rc;
     if (n_experts < 1 || n_experts > DOPT_MAX_EXPERTS)
         return dopt::fail(DOPT_E_ARG, "%s: n_experts %d (1..%d)", who, n_experts, DOPT_MAX_EXPERTS);
-    *bytes = sort_workspace(tokens * k, n_experts);
+    *bytes = sort_workspace_up_to(tokens * k, n_experts);
     return DOPT_OK;
 }
 
