@@ -764,6 +764,9 @@ int dopt_ckpt_act_grad(const void *ckpt, int64_t rows, int64_t cols, dopt_act ac
  * the same step) instead of writing them. */
 #define DOPT_WGRAD_ACCUMULATE 1u
 
+/* The most rows of dy that dopt_ckpt_wgrad takes. */
+#define DOPT_WGRAD_MAX_ROWS 2147483584
+
 /*
  * Weight gradients of y = x W^T from the kept input, written where a flat
  * grad replica holds them.  For each group g of rows (an expert; one group of
@@ -786,7 +789,8 @@ int dopt_ckpt_act_grad(const void *ckpt, int64_t rows, int64_t cols, dopt_act ac
  *                 counts as zeros.  dopt_route_sort's row_token lets the
  *                 tokens be kept once, unsorted.
  *   dy            device [dy_rows][outs], row stride dy_ld; bf16, or fp16 with
- *                 a checkpoint saved from fp16 (both factors have one type)
+ *                 a checkpoint saved from fp16 (both factors have one type);
+ *                 dy_rows <= DOPT_WGRAD_MAX_ROWS
  *   offsets       device int32 [n_groups + 1] or NULL (n_groups = 1, all
  *                 rows), as dopt_route_sort writes them; values are held to
  *                 [0, dy_rows]

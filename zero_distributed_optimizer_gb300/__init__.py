@@ -70,6 +70,7 @@ _LAYER_OPS = (
     "DOPT_MAX_GROUPS",
     "DOPT_MAX_TOPK",
     "DOPT_WGRAD_ACCUMULATE",
+    "DOPT_WGRAD_MAX_ROWS",
     "Checkpoint",
     "checkpoint",
     "ckpt_bytes",

@@ -946,6 +946,10 @@ int set_up(const char *who, EncodeTiled *encode, int *pairs) {
     return DOPT_OK;
 }
 
+// Rows in whole steps stay below 2^31: the kernel counts them in 32 bits.
+constexpr int64_t kMostRows = int64_t(INT32_MAX) / kK * kK;
+static_assert(kMostRows == DOPT_WGRAD_MAX_ROWS, "the limit that dopt.h states");
+
 // Row length, in elements, and bytes of the aligned copy of dy.
 int64_t copy_ld(int64_t outs) { return (outs + 7) / 8 * 8; }
 int64_t copy_bytes(int64_t dy_rows, int64_t outs) { return (dy_rows * copy_ld(outs) * 2 + 15) / 16 * 16; }
@@ -999,7 +1003,7 @@ extern "C" int dopt_ckpt_wgrad(const void *ckpt, dopt_dtype ckpt_dtype, int64_t 
     const char *who = "dopt_ckpt_wgrad";
     OpRange range(who);
     if (x_rows < 0 || x_rows > INT32_MAX || cols < 1 || cols > DOPT_MAX_COLS || dy_rows < 0 ||
-        dy_rows > INT32_MAX || outs < 1 || outs > DOPT_MAX_COLS || dy_ld < outs)
+        dy_rows > kMostRows || outs < 1 || outs > DOPT_MAX_COLS || dy_ld < outs)
         return fail(DOPT_E_ARG, "%s: checkpoint %lld x %lld, dy %lld x %lld, row stride %lld", who,
                     static_cast<long long>(x_rows), static_cast<long long>(cols),
                     static_cast<long long>(dy_rows), static_cast<long long>(outs),
@@ -1104,7 +1108,7 @@ extern "C" int dopt_ckpt_wgrad_workspace(int64_t dy_rows, int64_t outs, int64_t 
     dopt::clear_error();
     const char *who = "dopt_ckpt_wgrad_workspace";
     if (!bytes) return dopt::fail(DOPT_E_ARG, "%s: bytes is NULL", who);
-    if (dy_rows < 0 || dy_rows > INT32_MAX || outs < 1 || outs > DOPT_MAX_COLS || cols < 1 ||
+    if (dy_rows < 0 || dy_rows > kMostRows || outs < 1 || outs > DOPT_MAX_COLS || cols < 1 ||
         cols > DOPT_MAX_COLS || n_groups < 1 || n_groups > DOPT_MAX_GROUPS)
         return dopt::fail(DOPT_E_ARG, "%s: %lld rows, %lld x %lld, %d groups", who,
                           static_cast<long long>(dy_rows), static_cast<long long>(outs),

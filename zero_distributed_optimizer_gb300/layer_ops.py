@@ -28,6 +28,7 @@ DOPT_ACT_SILU = 0
 DOPT_ACT_GELU = 1
 DOPT_ACT_SWIGLU = 2
 DOPT_WGRAD_ACCUMULATE = 1
+DOPT_WGRAD_MAX_ROWS = 2147483584
 
 # torch's query of a device's current stream, without building a Stream object
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
