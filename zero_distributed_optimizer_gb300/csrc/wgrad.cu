@@ -655,6 +655,8 @@ __global__ void __launch_bounds__(kWgradThreads, 1) __cluster_dims__(2, 1, 1)
 #pragma unroll
                     for (int q = 0; q < 16; ++q, p += kTileC) *p = __uint_as_float(r[q]);
                 }
+            } else if (a.accumulate && it.steps == 0) {
+                // nothing is added: the grads stay as they are
             } else if (a.grad_dtype == DOPT_FP32) {
                 store_tile<float>(a, it, c, outs, sums);
             } else if (a.grad_dtype == DOPT_BF16) {
@@ -805,7 +807,7 @@ __global__ void __launch_bounds__(kTileC) dopt_ckpt_wgrad_join_kernel(const __gr
     __syncthreads();
     const WgradItem it = item_of<NB>(a, groups, a.whole + int(blockIdx.x) * a.split);
     const int o = int(blockIdx.y) * 16;
-    if (it.o0 + o >= a.outs) return;
+    if (it.o0 + o >= a.outs || (a.accumulate && groups.first[it.group + 1] <= groups.first[it.group])) return;
     float f[16] = {};
     for (int s = 0; s < a.split; ++s) {
         const float *p = a.partial + (it.slot + s) * slot_floats(NB) + int64_t(o) * kTileC + threadIdx.x;
