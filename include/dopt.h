@@ -809,8 +809,11 @@ int dopt_ckpt_act_grad(const void *ckpt, int64_t rows, int64_t cols, dopt_act ac
  *                 that share one must not overlap on the GPU.
  * The first call on a device looks up its number of SMs and the driver's
  * tensor-map encoder; make it before any stream capture.  A wait inside the
- * kernel that does not end within 2 s (a copy that never completes) leaves its
- * tile unwritten and is counted (dopt_wgrad_timeouts) instead of hanging.
+ * kernel that does not end within 2 s (a copy that never completes) ends the
+ * work of its pair of blocks instead of hanging: it is counted
+ * (dopt_wgrad_timeouts), and all grads that the pair had still to write or add
+ * to (the rest of its tiles, or a tile that it had a part of) become NaN, so
+ * that DOPT_STEP_SKIP_NONFINITE sees them.
  * Errors: DOPT_E_ARG, DOPT_E_ALIGN, DOPT_E_CUDA.
  */
 int dopt_ckpt_wgrad(const void *ckpt, dopt_dtype ckpt_dtype, int64_t x_rows, int64_t cols,
@@ -829,6 +832,15 @@ int dopt_ckpt_wgrad_workspace(int64_t dy_rows, int64_t outs, int64_t cols, int32
  * (0 unless a copy or product failed to complete); with reset != 0 the count
  * is then cleared.  Synchronous.  Errors: DOPT_E_ARG (NULL count), DOPT_E_CUDA. */
 int dopt_wgrad_timeouts(int reset, uint32_t *count);
+
+/* Test build only (DOPT_DEVICE_CHECKS, libdopt_checked.so): in every
+ * dopt_ckpt_wgrad launched after this call on the current device, the first
+ * pair of blocks issues the products of its first `items` items only, so that
+ * waits of both its blocks run out (about 4 s, counted as 2) and they take the
+ * failure path described at dopt_ckpt_wgrad, without any fault; -1 restores
+ * normal work.  Synchronous.  Errors: DOPT_E_STATE in the product build,
+ * DOPT_E_ARG (items < -1), DOPT_E_CUDA. */
+int dopt_wgrad_wait_test(int32_t items);
 
 /* Device-side checks (library infrastructure for testing; the pages have
  * no counterpart): a test build of the library, compiled with

@@ -33,3 +33,12 @@ def test_the_most_rows_are_taken(lib):
     n = ctypes.c_int64(-1)
     assert dopt.DOPT_WGRAD_MAX_ROWS == 2 ** 31 - 64
     assert lib.dopt_ckpt_wgrad_workspace(2 ** 31 - 64, 8, 8, 1, ctypes.byref(n)) == 0
+
+
+def test_product_build_has_no_wait_test(lib):
+    if B.LIB_PATH.endswith("libdopt_checked.so"):
+        pytest.skip("this process runs the checked build")
+    for items in (-1, 0):
+        with pytest.raises(dopt.DoptError) as e:
+            dopt.wgrad_wait_test(items)
+        assert e.value.code == B.DOPT_E_STATE

@@ -84,6 +84,7 @@ _LAYER_OPS = (
     "dopt_route_sort",
     "route_workspace",
     "wgrad_timeouts",
+    "wgrad_wait_test",
     "wgrad_workspace",
 )
 

@@ -106,10 +106,24 @@ struct WgradArgs {
     int64_t grad_offset[DOPT_MAX_GROUPS];
 };
 
-// Waits that ran past their limit (a copy or product that never completed);
-// the pair then left its tile alone.
+// CTAs with a wait that ran past its limit (a copy or product that never
+// completed).  Such a pair ends its work; the grads that it has not written
+// become NaN, parts of split sums too, which carry it into theirs.
 __device__ unsigned int g_wgrad_timeouts;
 constexpr unsigned long long kWaitNs = 2000000000ull;  // 2 s
+constexpr uint32_t kNanBits = 0x7fffffffu;
+
+#ifdef DOPT_DEVICE_CHECKS
+// Test build only: the first pair issues the products of so many of its items
+// (-1: of all), so that the waits for the next one's run out
+// (dopt_wgrad_wait_test).
+__device__ int g_wgrad_items = -1;
+__device__ __forceinline__ bool products_withheld(int round) {
+    return blockIdx.x == 0 && g_wgrad_items >= 0 && round >= g_wgrad_items;
+}
+#else
+__device__ __forceinline__ bool products_withheld(int) { return false; }
+#endif
 
 __device__ __forceinline__ uint32_t smem_of(const void *p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -432,14 +446,18 @@ __device__ __forceinline__ void add_tile(uint32_t into, uint32_t from, int outs)
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// A tile's sums of a warp's 32 columns, at `sums` in tensor memory, to the grads.
+// A tile's sums of a warp's 32 columns, at `sums` in tensor memory, to the
+// grads; `fill` instead of them where there are none.
 template <typename G>
-__device__ __forceinline__ void store_tile(const WgradArgs &a, const WgradItem &it, int c, int outs, uint32_t sums) {
+__device__ __forceinline__ void store_tile(const WgradArgs &a, const WgradItem &it, int c, int outs, uint32_t sums,
+                                           bool there_are, uint32_t fill) {
     G *p = grad_at<G>(a, it, c);
     const int there = c < a.cols ? a.outs - it.o0 : 0;
     for (int o = 0; o < outs; o += 32) {  // (outs is a multiple of 32)
-        uint32_t r[2][16] = {};
-        if (it.steps > 0) {
+        uint32_t r[2][16];
+#pragma unroll
+        for (int q = 0; q < 16; ++q) r[0][q] = r[1][q] = fill;
+        if (there_are) {
             load_sums(sums + uint32_t(o), r[0]);
             load_sums(sums + uint32_t(o + 16), r[1]);
             wait_sums(r[0]);
@@ -563,6 +581,7 @@ __global__ void __launch_bounds__(kWgradThreads, 1) __cluster_dims__(2, 1, 1)
             uint32_t used = 0, odd = 0;  // bit per buffer: used before, an odd number of times
             bool ok = true;
             for (int round = 0, item; ok && (item = item_number(a, round)) >= 0; ++round) {
+                if (products_withheld(round)) break;
                 const WgradItem it = item_of<NB>(a, groups, item);
                 const int steps = uniform(it.steps), full_steps = uniform(it.full);
                 const int rest = (uniform(it.rows) - full_steps * kK + 15) / 16;  // products of the last step
@@ -629,13 +648,13 @@ __global__ void __launch_bounds__(kWgradThreads, 1) __cluster_dims__(2, 1, 1)
             __syncwarp();
             if (lane == 0) arrive_remote(leader_address(smem_of(&b.sum_empty[buffer])));
         };
-        for (int k = 0, item; ok && (item = item_number(a, k)) >= 0; ++k) {
+        for (int k = 0, item; (item = item_number(a, k)) >= 0; ++k) {
             const WgradItem it = item_of<NB>(a, groups, item);
             const int c = it.c0 + column_of(m);
             const int outs = (it.blocks - 1) * kTileO + block_outs(a, it, it.blocks - 1);
             const int buffer = NB == 1 ? t & 1 : 0;
             const uint32_t sums = lanes + uint32_t(buffer * kTileO);
-            for (int i = 0; i < it.steps; i += a.chunk) {
+            for (int i = 0; ok && i < it.steps; i += a.chunk) {
                 const int from = NB == 1 && i > 0 ? buffer ^ 1 : buffer;
                 ok = __all_sync(kFull, wait_phase<200>(b, b.sum_full[from], odd >> from & 1));
                 if (!ok) break;
@@ -646,25 +665,29 @@ __global__ void __launch_bounds__(kWgradThreads, 1) __cluster_dims__(2, 1, 1)
                     release(from);
                 }
             }
-            if (!ok) break;
+            // once a wait has run out, the items that have rows are lost
+            const bool there_are = ok && it.steps > 0;
+            const uint32_t fill = ok || it.steps == 0 ? 0 : kNanBits;
             if (it.slot >= 0) {
                 float *p = a.partial + it.slot * slot_floats(NB) + m;
                 for (int o = 0; o < outs; o += 16) {
-                    uint32_t r[16] = {};
-                    if (it.steps > 0) load_sums(sums + uint32_t(o), r), wait_sums(r);
+                    uint32_t r[16];
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) r[q] = fill;
+                    if (there_are) load_sums(sums + uint32_t(o), r), wait_sums(r);
 #pragma unroll
                     for (int q = 0; q < 16; ++q, p += kTileC) *p = __uint_as_float(r[q]);
                 }
             } else if (a.accumulate && it.steps == 0) {
                 // nothing is added: the grads stay as they are
             } else if (a.grad_dtype == DOPT_FP32) {
-                store_tile<float>(a, it, c, outs, sums);
+                store_tile<float>(a, it, c, outs, sums, there_are, fill);
             } else if (a.grad_dtype == DOPT_BF16) {
-                store_tile<__nv_bfloat16>(a, it, c, outs, sums);
+                store_tile<__nv_bfloat16>(a, it, c, outs, sums, there_are, fill);
             } else {
-                store_tile<__half>(a, it, c, outs, sums);
+                store_tile<__half>(a, it, c, outs, sums, there_are, fill);
             }
-            if (it.steps > 0) {
+            if (there_are) {
                 release(buffer);
                 ++t;
             }
@@ -1142,4 +1165,22 @@ extern "C" int dopt_wgrad_timeouts(int reset, uint32_t *count) {
     }
     *count = c;
     return DOPT_OK;
+}
+
+extern "C" int dopt_wgrad_wait_test(int32_t items) {
+    using dopt::fail;
+    dopt::clear_error();
+#ifdef DOPT_DEVICE_CHECKS
+    if (items < -1) return fail(DOPT_E_ARG, "dopt_wgrad_wait_test: %d items", items);
+    const int v = items;
+    const cudaError_t e = cudaMemcpyToSymbol(g_wgrad_items, &v, sizeof v);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return fail(DOPT_E_CUDA, "dopt_wgrad_wait_test: %s", cudaGetErrorString(e));
+    }
+    return DOPT_OK;
+#else
+    (void)items;
+    return fail(DOPT_E_STATE, "dopt_wgrad_wait_test: this library was built without DOPT_DEVICE_CHECKS");
+#endif
 }

@@ -317,7 +317,16 @@ def dopt_ckpt_wgrad(ckpt: Checkpoint, dy, grad, grad_offsets, offsets=None, row_
 
 def wgrad_timeouts(reset: bool = False) -> int:
     """Blocks of :func:`dopt_ckpt_wgrad` on the current device whose waits ran
-    out of time (0 unless a copy or product failed to complete); reset clears it."""
+    out of time (0 unless a copy or product failed to complete; the grads they
+    did not write are then NaN); reset clears it."""
     c = ctypes.c_uint32(0)
     _check(lib().dopt_wgrad_timeouts(1 if reset else 0, ctypes.byref(c)))
     return c.value
+
+
+def wgrad_wait_test(items: int) -> None:
+    """Test build only (dopt_wgrad_wait_test in dopt.h): the first pair of blocks
+    of later weight gradients stops after `items` of its items, so that its
+    waits run out; -1 restores normal work.  Raises DoptError with DOPT_E_STATE
+    in the product build."""
+    _check(lib().dopt_wgrad_wait_test(int(items)))

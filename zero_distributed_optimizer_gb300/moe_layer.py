@@ -41,7 +41,7 @@ class MoELayer:
         self.params = [self.master.bfloat16() for _ in range(D)]
         self.grads = [torch.zeros(N, dtype=torch.float32, device=device) for _ in range(D)]
         self.adam = B.AdamConfig(lr=lr, weight_decay=0.0, grad_scale=1.0 / D)
-        self.steps = 0
+        self.steps, self.timeouts = 0, ops.wgrad_timeouts()
         # what a pass needs, made once
         slots, bf16, i32 = tokens * k, torch.bfloat16, torch.int32
 
@@ -118,6 +118,8 @@ class MoELayer:
             diff = out.float() - target.float()
             losses.append(diff.square().mean())
             self.backward((diff * (2.0 / diff.numel())).to(x.dtype), saved, rank)
+        if ops.wgrad_timeouts() != self.timeouts:  # some grads are NaN
+            raise RuntimeError("a weight gradient's wait ran out of time: no step is taken")
         self.steps += 1
         B.dopt_step(self.layout, self.adam, self.steps, self.grads, self.master, self.exp_avg, self.exp_avg_sq,
                     self.params)
