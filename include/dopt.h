@@ -828,6 +828,15 @@ int dopt_ckpt_wgrad(const void *ckpt, dopt_dtype ckpt_dtype, int64_t x_rows, int
 int dopt_ckpt_wgrad_workspace(int64_t dy_rows, int64_t outs, int64_t cols, int32_t n_groups,
                               int64_t *bytes);
 
+/* How a dopt_ckpt_wgrad of these sizes and types divides its work on a device
+ * of 152 SMs, for tests that have to reach each form: plan[0], blocks of 256
+ * outputs in a tile (1 or 2); plan[1], whole tiles; plan[2], tiles whose rows
+ * are split; plan[3], into how many parts.  workspace_bytes: what is left for
+ * sums.  Host only.  Errors: DOPT_E_ARG. */
+int dopt_ckpt_wgrad_plan(int64_t dy_rows, int64_t outs, int64_t cols, int32_t n_groups,
+                         dopt_dtype dy_dtype, dopt_dtype grad_dtype, int64_t workspace_bytes,
+                         int64_t plan[4]);
+
 /* Count of dopt_ckpt_wgrad blocks on the current device whose waits ran out
  * (0 unless a copy or product failed to complete); with reset != 0 the count
  * is then cleared.  Synchronous.  Errors: DOPT_E_ARG (NULL count), DOPT_E_CUDA. */

@@ -83,6 +83,8 @@ _LAYER_OPS = (
     "dopt_route_dispatch",
     "dopt_route_sort",
     "route_workspace",
+    "WgradPlan",
+    "wgrad_plan",
     "wgrad_timeouts",
     "wgrad_wait_test",
     "wgrad_workspace",

@@ -158,6 +158,7 @@ def _declare(lib):
             ("dopt_ckpt_wgrad", [vp, ctypes.c_int, i64, i64, vp, vp, ctypes.c_int, i64, i64, i64, vp,
                                  i32, P(i64), vp, ctypes.c_int, i64, ctypes.c_uint32, vp, i64, vp]),
             ("dopt_ckpt_wgrad_workspace", [i64, i64, i64, i32, P(i64)]),
+            ("dopt_ckpt_wgrad_plan", [i64, i64, i64, i32, ctypes.c_int, ctypes.c_int, i64, P(i64)]),
             ("dopt_wgrad_timeouts", [ctypes.c_int, P(ctypes.c_uint32)]),
             ("dopt_wgrad_wait_test", [i32])):
         getattr(lib, name).restype = ctypes.c_int

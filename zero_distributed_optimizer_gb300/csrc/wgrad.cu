@@ -1149,6 +1149,27 @@ extern "C" int dopt_ckpt_wgrad_workspace(int64_t dy_rows, int64_t outs, int64_t 
     return DOPT_OK;
 }
 
+extern "C" int dopt_ckpt_wgrad_plan(int64_t dy_rows, int64_t outs, int64_t cols, int32_t n_groups,
+                                    dopt_dtype dy_dtype, dopt_dtype grad_dtype, int64_t workspace_bytes,
+                                    int64_t plan[4]) {
+    dopt::clear_error();
+    const char *who = "dopt_ckpt_wgrad_plan";
+    if (!plan) return dopt::fail(DOPT_E_ARG, "%s: plan is NULL", who);
+    if (dy_rows < 0 || dy_rows > kMostRows || outs < 1 || outs > DOPT_MAX_COLS || cols < 1 || cols > DOPT_MAX_COLS ||
+        n_groups < 1 || n_groups > DOPT_MAX_GROUPS || workspace_bytes < 0)
+        return dopt::fail(DOPT_E_ARG, "%s: %lld rows, %lld x %lld, %d groups, workspace of %lld bytes", who,
+                          static_cast<long long>(dy_rows), static_cast<long long>(outs), static_cast<long long>(cols),
+                          n_groups, static_cast<long long>(workspace_bytes));
+    if ((dy_dtype != DOPT_BF16 && dy_dtype != DOPT_FP16) || !valid_dtype(grad_dtype))
+        return dopt::fail(DOPT_E_ARG, "%s: dtypes %d, %d", who, int(dy_dtype), int(grad_dtype));
+    const Plan p = plan_wgrad(outs, cols, n_groups, dy_rows, sum_chunk(dy_dtype, grad_dtype), 76, workspace_bytes);
+    plan[0] = p.nb;
+    plan[1] = p.whole;
+    plan[2] = p.tail;
+    plan[3] = p.parts;
+    return DOPT_OK;
+}
+
 extern "C" int dopt_wgrad_timeouts(int reset, uint32_t *count) {
     using dopt::fail;
     dopt::clear_error();

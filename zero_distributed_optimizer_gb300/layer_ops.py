@@ -315,6 +315,24 @@ def dopt_ckpt_wgrad(ckpt: Checkpoint, dy, grad, grad_offsets, offsets=None, row_
           _dtype_code(grad.dtype, "grad"), numel, DOPT_WGRAD_ACCUMULATE if accumulate else 0, wp, wn)
 
 
+class WgradPlan(NamedTuple):
+    """How a weight gradient divides its work (dopt_ckpt_wgrad_plan in dopt.h)."""
+
+    blocks: int  # of 256 outputs, in a tile
+    whole: int   # tiles
+    split: int   # tiles whose rows are split
+    parts: int   # into so many
+
+
+def wgrad_plan(dy_rows: int, outs: int, cols: int, n_groups: int, dy_dtype, grad_dtype,
+               workspace_bytes: int) -> WgradPlan:
+    """The plan of such a :func:`dopt_ckpt_wgrad` on a device of 152 SMs."""
+    p = (ctypes.c_int64 * 4)()
+    _check(lib().dopt_ckpt_wgrad_plan(int(dy_rows), int(outs), int(cols), int(n_groups), _dtype_code(dy_dtype, "dy"),
+                                      _dtype_code(grad_dtype, "grad"), int(workspace_bytes), p))
+    return WgradPlan(*p)
+
+
 def wgrad_timeouts(reset: bool = False) -> int:
     """Blocks of :func:`dopt_ckpt_wgrad` on the current device whose waits ran
     out of time (0 unless a copy or product failed to complete; the grads they
