@@ -824,7 +824,9 @@ int dopt_ckpt_wgrad(const void *ckpt, dopt_dtype ckpt_dtype, int64_t x_rows, int
                     int64_t workspace_bytes, cudaStream_t stream);
 
 /* Bytes of workspace that a dopt_ckpt_wgrad of these sizes and contiguous dy
- * can make use of (0: none).  Host only.  Errors: DOPT_E_ARG. */
+ * can make use of, whatever its types (0: none).  A dy that is a view whose
+ * rows are not 16-byte aligned though outs is a multiple of 8 can use
+ * 2 * dy_rows * outs bytes more, for its copy.  Host only.  Errors: DOPT_E_ARG. */
 int dopt_ckpt_wgrad_workspace(int64_t dy_rows, int64_t outs, int64_t cols, int32_t n_groups,
                               int64_t *bytes);
 

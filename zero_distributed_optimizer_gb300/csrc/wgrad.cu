@@ -38,7 +38,7 @@ namespace {
 // The tensor cores add 16 rows' products to a sum at a time and cut off what
 // its 24 bits do not hold, always toward zero: the error of one long sum grows
 // as its rows do (fp32 grads of 16384 rows were 1.1e-5 off with bf16 dy, 1.8e-5
-// with fp16, where fp32 additions that round are off by 2-7e-7).  So a sum takes
+// with fp16, where fp32 additions that round are off by 2-4e-7).  So a sum takes
 // `chunk` steps; the four storing warps then add it to the tile's first sum,
 // rounding to nearest, and it starts anew.  Both are in tensor memory, with
 // NB = 1: the other buffer, once the tile before is stored.  sum_chunk has
@@ -46,11 +46,12 @@ namespace {
 // take 254 us so (195 in one sum of NB = 2).
 //
 // Long sums are bound by the tensor cores: 16384 rows x 5632 columns x 2048
-// outputs, bf16, take 198 us (1.90 PFLOP/s; 225 us, 1.68, where the card's
-// power limits it).  Many short groups are bound by the steps' latency (codes
+// outputs, bf16, take 200-204 us (1.89 PFLOP/s; 222-227 us, 1.68, where the
+// card's power limits it).  Many short groups are bound by the steps' latency (codes
 // of a step's rows arrive, are widened and fenced, 4 steps at a time) and by
 // the stores, together: 64 experts of about 1024 rows x 512 columns x 1408
-// outputs, fp32 grads, take 99 us (0.95 PFLOP/s, 3.8 TB/s; 93 in one sum).
+// outputs, fp32 grads, take 99-101 us (0.95 PFLOP/s, 3.8 TB/s; 93 in one sum).
+// Adding to old grads is bound by their loads, 4 in flight a thread: 449 us there.
 constexpr int kTileC = 256;          // of a pair
 constexpr int kTileO = 256;          // of a product; a tile has NB of them
 constexpr int kK = 64;               // rows a step

@@ -95,7 +95,8 @@ def _call(index: int, stream, function, *args):
 # ---------------------------------------------------------------------------
 
 def route_workspace(tokens: int, k: int, n_experts: int, device=None):
-    """A workspace for :func:`dopt_route_sort` of these sizes (a uint8 tensor)."""
+    """A workspace for :func:`dopt_route_sort` of these sizes and of any fewer
+    tokens (a uint8 tensor)."""
     n = ctypes.c_int64()
     _check(lib().dopt_route_workspace(int(tokens), int(k), int(n_experts), ctypes.byref(n)))
     return torch.empty(max(n.value, 16), dtype=torch.uint8,
@@ -272,7 +273,10 @@ def _starts(grad_offsets: tuple):
 
 
 def wgrad_workspace(dy_rows: int, outs: int, cols: int, n_groups: int = 1, device=None):
-    """A workspace for :func:`dopt_ckpt_wgrad` of these sizes (a uint8 tensor)."""
+    """A workspace for :func:`dopt_ckpt_wgrad` of these sizes and a contiguous dy
+    (a uint8 tensor).  A view of dy whose rows are not 16-byte aligned though
+    outs is a multiple of 8 is read element by element, three times slower,
+    unless the workspace has 2 * dy_rows * outs bytes more."""
     n = ctypes.c_int64()
     _check(lib().dopt_ckpt_wgrad_workspace(int(dy_rows), int(outs), int(cols), int(n_groups),
                                            ctypes.byref(n)))
