@@ -853,6 +853,145 @@ int dopt_wgrad_timeouts(int reset, uint32_t *count);
  * DOPT_E_ARG (items < -1), DOPT_E_CUDA. */
 int dopt_wgrad_wait_test(int32_t items);
 
+/* ------------------------------------------------------------------------
+ * Operators of a language model's two ends and of its residual stream: the
+ * token embedding and its gradient, the norms around a block, and the cross
+ * entropy of the output matrix's logits.  Conventions as for the layer
+ * operators above.  A param's gradient goes to its offset in a flat grad
+ * replica (the params' starts: dopt_layout_param_offsets), so that a table
+ * shared by both ends adds up in one place.
+ * ------------------------------------------------------------------------ */
+
+/* dopt_embed and dopt_embed_grad flag: add to what the output or the grads
+ * hold instead of writing them. */
+#define DOPT_EMBED_ACCUMULATE 1u
+
+/*
+ * out[t] = scale * table[ids[t]], in fp32 and rounded once (copied bit for bit
+ * with scale 1); zeros where ids[t] is outside [0, vocab) (padding, another
+ * rank's part of the vocabulary).  With DOPT_EMBED_ACCUMULATE it is added to
+ * out[t] before the rounding (positions on top of tokens), and an id outside
+ * leaves out[t] as it is.
+ *   table  device [vocab][cols], row stride ld_table
+ *   ids    device int32 or int64 (id_bytes 4 or 8) [tokens]
+ *   out    device [tokens][cols], row stride ld_out, of the table's type
+ * tokens < 2^31, 1 <= vocab < 2^31, 1 <= cols <= DOPT_MAX_COLS.  Errors:
+ * DOPT_E_ARG, DOPT_E_ALIGN, DOPT_E_CUDA.
+ */
+int dopt_embed(const void *table, dopt_dtype dtype, int64_t vocab, int64_t cols, int64_t ld_table,
+               const void *ids, int32_t id_bytes, int64_t tokens, float scale, void *out,
+               int64_t ld_out, uint32_t flags, cudaStream_t stream);
+
+/*
+ * The gradient of the table, written where a flat grad replica holds it: for
+ * every row v of it
+ *     grad[grad_offset + v * cols + c]  (+)=
+ *         scale * sum over t with ids[t] == v of d_out[t][c]
+ * in fp32, in an order that depends on ids alone, and rounded once.  A row
+ * that no id names gets zeros (is left alone with DOPT_EMBED_ACCUMULATE); ids
+ * outside [0, vocab) are left out, and their rows of d_out are not read.
+ *   d_out      device [tokens][cols], row stride ld
+ *   grad       device, grad_numel elements of grad_dtype
+ *   workspace  device, 16-byte aligned, dopt_embed_workspace bytes (the
+ *              sorted tokens, and sums of long runs); calls that share one
+ *              must not overlap on the GPU
+ * Limits as dopt_embed.  The first call on a device sets its kernels up; make
+ * it before any stream capture.  Errors: DOPT_E_ARG, DOPT_E_ALIGN, DOPT_E_CUDA.
+ */
+int dopt_embed_grad(const void *ids, int32_t id_bytes, int64_t tokens, const void *d_out,
+                    dopt_dtype dtype, int64_t cols, int64_t ld, int64_t vocab, float scale,
+                    void *grad, dopt_dtype grad_dtype, int64_t grad_numel, int64_t grad_offset,
+                    uint32_t flags, void *workspace, int64_t workspace_bytes, cudaStream_t stream);
+
+/* Bytes of workspace that are enough for dopt_embed_grad of these sizes and of
+ * any fewer tokens.  Host only.  Errors: DOPT_E_ARG. */
+int dopt_embed_workspace(int64_t tokens, int64_t vocab, int64_t cols, int64_t *bytes);
+
+/* Kinds of norm, of a row v: rms: v / sqrt(mean(v^2) + eps); layer: the same of
+ * v - mean(v).  Then times a weight and (layer) plus a bias, per column. */
+typedef enum { DOPT_NORM_RMS = 0, DOPT_NORM_LAYER = 1 } dopt_norm_kind;
+
+/* The most columns of a row. */
+#define DOPT_NORM_MAX_COLS 16384
+
+/* dopt_norm_grad flag: add to the params' grads in the buffer. */
+#define DOPT_NORM_ACCUMULATE 1u
+
+typedef struct {
+    int32_t kind; /* dopt_norm_kind, of both norms */
+    int32_t post; /* 1: the block's output is normed before it is added */
+    float eps;
+    float scale;  /* the residual scale: of the block's branch */
+} dopt_norm_cfg;
+
+/* Device pointers, each may be NULL; params [cols] of the rows' type. */
+typedef struct {
+    const void *weight, *bias;           /* of the next block's norm */
+    const void *post_weight, *post_bias; /* of the norm after the block */
+    const void *gate;                    /* per column of the branch */
+    const float *row_gate;               /* fp32 [rows], per row of the branch */
+} dopt_norm_params;
+
+/*
+ * What stands between two blocks, in one pass over the rows:
+ *     u = y, or norm(y) with post_weight and post_bias (cfg->post)
+ *     h = x + scale * row_gate[t] * gate[c] * u
+ *     n = norm(h) with weight and bias
+ * in fp32 throughout, n from the h before its rounding; each output is rounded
+ * once.  Without y (a model's first norm), h is x and n = norm(x).  Params
+ * that are NULL count as ones (bias as zeros).
+ *   x, y  device [rows][cols], row strides ld_x, ld_y; y may be NULL
+ *   h     device [rows][cols], written, or NULL; may be x with its row stride
+ *   n     device [rows][cols], written, or NULL
+ * rows < 2^31, 1 <= cols <= DOPT_NORM_MAX_COLS.  Errors: DOPT_E_ARG,
+ * DOPT_E_ALIGN, DOPT_E_CUDA.
+ */
+int dopt_norm(const dopt_norm_cfg *cfg, const dopt_norm_params *params, dopt_dtype dtype,
+              int64_t rows, int64_t cols, const void *x, int64_t ld_x, const void *y, int64_t ld_y,
+              void *h, int64_t ld_h, void *n, int64_t ld_n, cudaStream_t stream);
+
+/*
+ * The gradients of dopt_norm, in one pass over the rows and one over sums of
+ * columns, from h (as dopt_norm wrote it; x where there was no y), y, and the
+ * gradients d_n of n and d_h of h (what reaches h otherwise; either may be
+ * NULL, not both).  With hat(v) = the norm of v before weight and bias:
+ *     d_x         = d_h + the norm's gradient of d_n        (of x and h alike)
+ *     d_y         = scale * row_gate * gate * d_x, through the norm after the
+ *                   block if there is one
+ *     weight      sum over rows of d_n * hat(h)        bias       of d_n
+ *     post_weight sum of scale * row_gate * gate * d_x * hat(y)
+ *     post_bias   sum of scale * row_gate * gate * d_x
+ *     gate        sum of scale * row_gate * d_x * u
+ *     d_row_gate[t] = scale * sum over columns of gate * d_x * u
+ * The mean and the mean square of h and y are computed again.  fp32 sums, in
+ * an order that depends on the sizes alone; each result is rounded once (after
+ * adding the old grad, with DOPT_NORM_ACCUMULATE).
+ *   d_x, d_y      device [rows][cols], written, or NULL; d_x may be d_h with
+ *                 its row stride
+ *   d_row_gate    device fp32 [rows], written, or NULL
+ *   grad          device, grad_numel elements of grad_dtype
+ *   grad_offsets  HOST int64 [5], where the grads of weight, bias, post_weight,
+ *                 post_bias and gate go, -1 for none; or NULL for none at all.
+ *                 A NULL param has a gradient too; weight's and bias's need
+ *                 d_n, the others' y, post_*'s a norm after the block, biases'
+ *                 a layer norm
+ *   workspace     device, 16-byte aligned, dopt_norm_workspace bytes; calls
+ *                 that share one must not overlap on the GPU
+ * With rows = 0 the params' grads are zeros (are left alone with
+ * DOPT_NORM_ACCUMULATE).  Errors: DOPT_E_ARG, DOPT_E_ALIGN, DOPT_E_CUDA.
+ */
+int dopt_norm_grad(const dopt_norm_cfg *cfg, const dopt_norm_params *params, dopt_dtype dtype,
+                   int64_t rows, int64_t cols, const void *h, int64_t ld_h, const void *y,
+                   int64_t ld_y, const void *d_n, int64_t ld_d_n, const void *d_h, int64_t ld_d_h,
+                   void *d_x, int64_t ld_d_x, void *d_y, int64_t ld_d_y, float *d_row_gate,
+                   void *grad, dopt_dtype grad_dtype, int64_t grad_numel,
+                   const int64_t grad_offsets[5], uint32_t flags, void *workspace,
+                   int64_t workspace_bytes, cudaStream_t stream);
+
+/* Bytes of workspace for dopt_norm_grad of these sizes and of any fewer rows.
+ * Host only.  Errors: DOPT_E_ARG. */
+int dopt_norm_workspace(int64_t rows, int64_t cols, int64_t *bytes);
+
 /* Device-side checks (library infrastructure for testing; the pages have
  * no counterpart): a test build of the library, compiled with
  * DOPT_DEVICE_CHECKS defined; built by build(checked=True) as

@@ -90,15 +90,32 @@ _LAYER_OPS = (
     "wgrad_workspace",
 )
 
+# The same for the operators of a language model's ends and residual stream.
+_MODEL_OPS = (
+    "DOPT_EMBED_ACCUMULATE",
+    "DOPT_NORM_ACCUMULATE",
+    "DOPT_NORM_LAYER",
+    "DOPT_NORM_MAX_COLS",
+    "DOPT_NORM_RMS",
+    "dopt_embed",
+    "dopt_embed_grad",
+    "dopt_norm",
+    "dopt_norm_grad",
+    "embed_workspace",
+    "norm_workspace",
+)
+
 
 def __getattr__(name):
     if name in _LAYER_OPS:
-        from . import layer_ops
-
-        value = globals()[name] = getattr(layer_ops, name)
-        return value
-    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+        from . import layer_ops as module
+    elif name in _MODEL_OPS:
+        from . import model_ops as module
+    else:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    value = globals()[name] = getattr(module, name)
+    return value
 
 
 def __dir__():
-    return sorted(set(globals()) | set(_LAYER_OPS))
+    return sorted(set(globals()) | set(_LAYER_OPS) | set(_MODEL_OPS))

@@ -1,0 +1,558 @@
+// The token embedding (dopt_embed) and its gradient into the flat grad buffer
+// (dopt_embed_grad); dopt.h states the contracts.
+#include <mutex>
+
+#include "rows.cuh"
+
+namespace {
+
+constexpr int kEmbedThreads = 256;
+constexpr int kWarps = kEmbedThreads / 32;
+constexpr int kCols = 8;                 // columns a thread
+constexpr int kWarpCols = 32 * kCols;    // columns a warp
+constexpr int kSortThreads = 1024;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kMostRange = 1024;         // rows of the table that one sorting block owns
+constexpr int kChunk = 256;              // sorted tokens of a block that sums long runs
+constexpr int kShort = 32;               // tokens of a row that one warp sums
+static_assert(kChunk == kWarps * kShort, "a warp of the long runs' blocks takes 32 tokens");
+
+struct EmbedArgs {
+    const void *table;
+    const void *ids;
+    void *out;
+    int64_t ld_table, ld_out;
+    int64_t tokens, vocab;
+    int32_t cols, wide;  // wide: 64-bit ids
+    int32_t vec;         // the table's and the output's rows are 16-byte aligned
+    int32_t accumulate;
+    float scale;
+};
+
+template <typename I>
+__device__ __forceinline__ int64_t id_at(const void *ids, int64_t t) {
+    return int64_t(static_cast<const I *>(ids)[t]);
+}
+
+// out[t] = scale * table[id]: a warp takes 256 columns of four tokens, whose
+// ids and then rows are loaded together.
+template <typename T, typename I>
+__global__ void __launch_bounds__(kEmbedThreads) dopt_embed_kernel(const __grid_constant__ EmbedArgs a) {
+    let_dependents_start();
+    wait_for_grids_before();
+    constexpr int kTokens = 4;
+    const int lane = threadIdx.x & 31;
+    const int64_t t0 = (int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * kTokens;
+    const int c0 = int(blockIdx.y) * kWarpCols, c = c0 + lane * kCols;
+    int64_t id[kTokens];
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) id[i] = t0 + i < a.tokens ? id_at<I>(a.ids, t0 + i) : -1;
+    using V = Values<T, kCols>;
+    typename V::Ahead ahead[kTokens];
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) {
+        const bool there = uint64_t(id[i]) < uint64_t(a.vocab);
+        V::fetch(ahead[i], static_cast<const T *>(a.table) + (there ? id[i] * a.ld_table : 0), c, there ? a.cols : 0,
+                 a.vec, lane, 32);
+    }
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) {
+        if (t0 + i >= a.tokens) break;
+        if (a.accumulate && uint64_t(id[i]) >= uint64_t(a.vocab)) continue;  // nothing is added
+        V v;
+        v.take(ahead[i], a.vec, lane, 32);
+        T *row = static_cast<T *>(a.out) + (t0 + i) * a.ld_out;
+        if (a.scale != 1.0f || a.accumulate) {
+            float f[kCols], old[kCols] = {};
+            v.get(f);
+            if (a.accumulate) {
+                V o;
+                o.load(row, c, a.cols, a.vec, lane, 32);
+                o.get(old);
+            }
+#pragma unroll
+            for (int q = 0; q < kCols; ++q) f[q] = f[q] * a.scale + old[q];
+            v.set(f);
+        }
+        v.store(row, c, a.cols, a.vec, lane, 32);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Gradient
+// ---------------------------------------------------------------------------
+
+struct EmbedGradArgs {
+    const void *ids;
+    const void *d_out;
+    void *grad;             // of the table's first element
+    int32_t *first;         // [vocab + 1] the first sorted place of each row of the table
+    int32_t *token;         // [tokens] the tokens by row, in order within one
+    int32_t *row;           // [tokens] their rows
+    int2 *list;             // [tokens] (token, row in its range), by range
+    int32_t *arrived;       // [chunks * pieces] parts of the run that begins in a chunk
+    float *partial;         // [2 * chunks][part_ld] sums of runs that go on past a chunk
+    int64_t ld, tokens, vocab, part_ld;
+    int32_t cols, pieces;   // pieces: of 256 columns
+    int32_t range, chunks;
+    int32_t vec, vec_grad;  // d_out's, the grads' rows are 16-byte aligned
+    int32_t accumulate;
+    float scale;
+};
+
+// Exclusive sum over a block's warps of one number each; `total` of all.
+__device__ __forceinline__ uint32_t over_warps(uint32_t mine, uint32_t *buffer, uint32_t &total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    __syncthreads();
+    if (lane == 0) buffer[warp] = mine;
+    __syncthreads();
+    uint32_t v = buffer[lane], sum = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t u = __shfl_up_sync(kFull, sum, d);
+        if (lane >= d) sum += u;
+    }
+    total = __shfl_sync(kFull, sum, 31);
+    return __shfl_sync(kFull, sum - v, warp);
+}
+
+// The tokens sorted by id (stable).  A block owns `range` rows of the table.
+// It goes through all ids, so that it knows without any other block how many
+// lie below its own, lists those that are its own in order and sorts the
+// list: counts of each (warp, row), their prefixes, places.
+template <typename I>
+__global__ void __launch_bounds__(kSortThreads) dopt_embed_sort_kernel(const __grid_constant__ EmbedGradArgs a) {
+    extern __shared__ uint32_t count[];  // [warps][range]
+    __shared__ uint32_t buffer[32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t before = (1u << lane) - 1;
+    let_dependents_start();
+    wait_for_grids_before();
+    const int64_t lo = int64_t(blockIdx.x) * a.range;
+    const int rows = int(min(int64_t(a.range), a.vocab - lo));
+    for (int64_t i = int64_t(blockIdx.x) * kSortThreads + threadIdx.x; i < int64_t(a.chunks) * a.pieces;
+         i += int64_t(gridDim.x) * kSortThreads)
+        a.arrived[i] = 0;
+
+    constexpr int kAhead = 8;
+    const int64_t stretch = ((a.tokens + kSortWarps - 1) / kSortWarps + 31) / 32 * 32;
+    const int64_t from = warp * stretch, to = min(a.tokens, from + stretch);
+    uint32_t own = 0, below = 0;
+    for (int64_t i = from; i < to; i += 32 * kAhead) {
+        int64_t id[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) id[j] = i + 32 * j + lane < to ? id_at<I>(a.ids, i + 32 * j + lane) : -1;
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            own += uint64_t(id[j] - lo) < uint64_t(rows);
+            below += uint64_t(id[j]) < uint64_t(lo);
+        }
+    }
+    own = __reduce_add_sync(kFull, own);
+    below = __reduce_add_sync(kFull, below);
+    uint32_t total, base;
+    uint32_t place = over_warps(own, buffer, total);
+    over_warps(below, buffer, base);
+    if (total > 0) {  // (the same in all threads)
+        for (int64_t i = from; i < to; i += 32 * kAhead) {
+            int64_t id[kAhead];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) id[j] = i + 32 * j + lane < to ? id_at<I>(a.ids, i + 32 * j + lane) : -1;
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                const bool here = uint64_t(id[j] - lo) < uint64_t(rows);
+                const uint32_t all = __ballot_sync(kFull, here);
+                if (here)
+                    a.list[base + place + __popc(all & before)] = make_int2(int(i + 32 * j + lane), int(id[j] - lo));
+                place += __popc(all);
+            }
+        }
+    }
+    for (int i = threadIdx.x; i < kSortWarps * a.range; i += kSortThreads) count[i] = 0;
+    __syncthreads();
+    uint32_t *mine = count + warp * a.range;
+    const uint32_t share = ((total + kSortWarps - 1) / kSortWarps + 31) / 32 * 32;
+    const uint32_t begin = min(total, warp * share), end = min(total, begin + share);
+    for (uint32_t i = begin; i < end; i += 32) {
+        const int row = i + lane < end ? a.list[base + i + lane].y : -1;
+        const uint32_t peers = __match_any_sync(kFull, row);
+        if (row >= 0 && (peers & before) == 0) mine[row] += __popc(peers);
+        __syncwarp();
+    }
+    __syncthreads();
+    uint32_t of_row = 0;  // thread r: the tokens of row r
+    if (int(threadIdx.x) < rows && total > 0)
+        for (int w = 0; w < kSortWarps; ++w) {
+            uint32_t *p = count + w * a.range + threadIdx.x;
+            const uint32_t n = *p;
+            *p = of_row;
+            of_row += n;
+        }
+    uint32_t upto = of_row;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t u = __shfl_up_sync(kFull, upto, d);
+        if (lane >= d) upto += u;
+    }
+    uint32_t all;
+    const uint32_t start = base + over_warps(__shfl_sync(kFull, upto, 31), buffer, all) + upto - of_row;
+    if (int(threadIdx.x) < rows) {
+        a.first[lo + threadIdx.x] = int(start);
+        if (total > 0)
+            for (int w = 0; w < kSortWarps; ++w) count[w * a.range + threadIdx.x] += start;
+    }
+    if (blockIdx.x == gridDim.x - 1 && threadIdx.x == 0) a.first[a.vocab] = int(base + total);
+    __syncthreads();
+    for (uint32_t i = begin; i < end; i += 32) {
+        const int2 e = i + lane < end ? a.list[base + i + lane] : make_int2(0, -1);
+        const uint32_t peers = __match_any_sync(kFull, e.y);
+        const uint32_t at = e.y >= 0 ? mine[e.y] + __popc(peers & before) : 0;
+        __syncwarp();
+        if (e.y >= 0) {
+            a.token[at] = e.x;
+            a.row[at] = int(lo) + e.y;
+            if ((peers & before) == 0) mine[e.y] += __popc(peers);
+        }
+        __syncwarp();
+    }
+}
+
+// The sum of a warp's columns over n <= 32 sorted places from p on, in order.
+template <typename T>
+__device__ __forceinline__ void sum_tokens(const EmbedGradArgs &a, int p, int n, int c, int lane, float (&f)[kCols]) {
+    using V = Values<T, kCols>;
+    const int token = lane < n ? a.token[p + lane] : 0;
+#pragma unroll
+    for (int q = 0; q < kCols; ++q) f[q] = 0.0f;
+    constexpr int kAhead = sizeof(T) == 4 ? 4 : 8;
+    for (int i = 0; i < n; i += kAhead) {
+        typename V::Ahead ahead[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int64_t t = __shfl_sync(kFull, token, i + j < n ? i + j : 0);
+            V::fetch(ahead[j], static_cast<const T *>(a.d_out) + t * a.ld, c, i + j < n ? a.cols : 0, a.vec, lane, 32);
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            if (i + j >= n) break;
+            V v;
+            v.take(ahead[j], a.vec, lane, 32);
+            float g[kCols];
+            v.get(g);
+#pragma unroll
+            for (int q = 0; q < kCols; ++q) f[q] += g[q];
+        }
+    }
+}
+
+// scale * f to a row of the grads.
+template <typename G>
+__device__ __forceinline__ void put_row(const EmbedGradArgs &a, int64_t row, int c, int lane, float (&f)[kCols]) {
+    using V = Values<G, kCols>;
+    G *p = static_cast<G *>(a.grad) + row * a.cols;
+    float old[kCols] = {};
+    if (a.accumulate) {
+        V o;
+        o.load(p, c, a.cols, a.vec_grad, lane, 32);
+        o.get(old);
+    }
+#pragma unroll
+    for (int q = 0; q < kCols; ++q) f[q] = f[q] * a.scale + old[q];
+    V v;
+    v.set(f);
+    v.store(p, c, a.cols, a.vec_grad, lane, 32);
+}
+
+// The first chunks * pieces blocks take 256 sorted tokens and 256 columns
+// each, and of those the rows with more than 32 tokens.  A row whose tokens
+// reach past the chunk leaves a partial sum there; the block that brings the
+// last one adds them in order.  The other blocks' warps take all rows with up
+// to 32 tokens: the sums of one never wait for another.
+template <typename T, typename G>
+__global__ void __launch_bounds__(kEmbedThreads) dopt_embed_grad_kernel(const __grid_constant__ EmbedGradArgs a) {
+    let_dependents_start();
+    wait_for_grids_before();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float f[kCols];
+    const int64_t long_blocks = int64_t(a.chunks) * a.pieces;
+    if (blockIdx.x >= long_blocks) {
+        const int64_t tasks = a.vocab * a.pieces, step = (gridDim.x - long_blocks) * kWarps;
+        for (int64_t i = (blockIdx.x - long_blocks) * kWarps + warp; i < tasks; i += step) {
+            const int64_t row = i / a.pieces;
+            const int c = int(i % a.pieces) * kWarpCols + lane * kCols;
+            const int p = a.first[row], n = a.first[row + 1] - p;
+            if (n > kShort || (n == 0 && a.accumulate)) continue;
+            sum_tokens<T>(a, p, n, c, lane, f);
+            put_row<G>(a, row, c, lane, f);
+        }
+        return;
+    }
+    __shared__ int32_t starts[kChunk + 1];  // the places in the chunk where long rows' tokens begin, then their ends
+    __shared__ int32_t ends[kChunk];
+    __shared__ uint32_t heads[kWarps];
+    __shared__ float sums[kWarps][kWarpCols];
+    const int chunk = int(blockIdx.x / a.pieces), piece = int(blockIdx.x % a.pieces);
+    const int c = piece * kWarpCols + lane * kCols;
+    const int total = a.first[a.vocab];
+    const int base = chunk * kChunk, here = min(kChunk, total - base);
+    if (here <= 0) return;
+    {
+        const int i = threadIdx.x;
+        const int row = i < here ? a.row[base + i] : -1;
+        const int p = row >= 0 ? a.first[row] : 0, n = row >= 0 ? a.first[row + 1] - p : 0;
+        const bool head = n > kShort && (i == 0 || p == base + i);
+        const uint32_t all = __ballot_sync(kFull, head);
+        if (lane == 0) heads[warp] = all;
+        __syncthreads();
+        int k = __popc(all & ((1u << lane) - 1));
+        for (int w = 0; w < warp; ++w) k += __popc(heads[w]);
+        if (head) {
+            starts[k] = i;
+            ends[k] = min(here, p + n - base);
+        }
+    }
+    __syncthreads();
+    int runs = 0;
+    for (int w = 0; w < kWarps; ++w) runs += __popc(heads[w]);
+    for (int k = 0; k < runs; ++k) {
+        const int from = max(starts[k], warp * kShort), n = max(0, min(ends[k], (warp + 1) * kShort) - from);
+        sum_tokens<T>(a, base + from, n, c, lane, f);
+#pragma unroll
+        for (int q = 0; q < kCols; ++q) sums[warp][lane * kCols + q] = f[q];
+        __syncthreads();
+        if (warp == 0) {
+            for (int w = 1; w < kWarps; ++w)
+#pragma unroll
+                for (int q = 0; q < kCols; ++q) f[q] += sums[w][lane * kCols + q];
+            const int row = a.row[base + starts[k]];
+            const int p = a.first[row], e = a.first[row + 1];
+            const int first_chunk = p / kChunk, last_chunk = (e - 1) / kChunk;
+            bool done = first_chunk == last_chunk;
+            if (!done) {
+                // a chunk's slot 0: the row that began before it; slot 1: the one that goes on after it
+                auto slot = [&](int at) { return a.partial + (2 * int64_t(at) + (at == first_chunk)) * a.part_ld + c; };
+                float *mine = slot(chunk);
+#pragma unroll
+                for (int q = 0; q < kCols; ++q) mine[q] = f[q];
+                __threadfence();
+                __syncwarp();
+                int before = 0;
+                if (lane == 0) before = atomicAdd(a.arrived + int64_t(first_chunk) * a.pieces + piece, 1);
+                done = __shfl_sync(kFull, before, 0) == last_chunk - first_chunk;
+                if (done) {
+                    __threadfence();
+#pragma unroll
+                    for (int q = 0; q < kCols; ++q) f[q] = 0.0f;
+#pragma unroll 4
+                    for (int at = first_chunk; at <= last_chunk; ++at) {
+                        const float4 *s = reinterpret_cast<const float4 *>(slot(at));
+                        const float4 u = __ldcg(s), v = __ldcg(s + 1);
+                        f[0] += u.x, f[1] += u.y, f[2] += u.z, f[3] += u.w;
+                        f[4] += v.x, f[5] += v.y, f[6] += v.z, f[7] += v.w;
+                    }
+                }
+            }
+            if (done) put_row<G>(a, row, c, lane, f);
+        }
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+
+int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+
+// Places of the gradient's tables in its workspace.
+struct EmbedSpace {
+    int64_t first, token, row, list, arrived, partial, bytes, chunks, pieces, part_ld;
+    EmbedSpace(int64_t tokens, int64_t vocab, int64_t cols) {
+        chunks = (tokens + kChunk - 1) / kChunk;
+        pieces = (cols + kWarpCols - 1) / kWarpCols;
+        part_ld = pieces * kWarpCols;
+        first = 0;
+        token = first + round_up(4 * (vocab + 1), 16);
+        row = token + round_up(4 * tokens, 16);
+        list = row + round_up(4 * tokens, 16);
+        arrived = list + round_up(8 * tokens, 16);
+        partial = arrived + round_up(4 * chunks * pieces, 16);
+        bytes = partial + 8 * chunks * part_ld;
+    }
+};
+
+std::mutex g_embed_mutex;
+bool g_embed_ready[64] = {};  // devices whose sorting kernels are set up
+
+// Raises the sorting kernels' shared-memory limit, once a device.
+int set_up_sort(const char *who) {
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e == cudaSuccess && (device < 0 || device >= 64)) return dopt::fail(DOPT_E_ARG, "%s: device %d", who, device);
+    std::lock_guard<std::mutex> lock(g_embed_mutex);
+    if (e == cudaSuccess && !g_embed_ready[device]) {
+        constexpr int kMost = int(kSortWarps * kMostRange * sizeof(uint32_t));
+        e = cudaFuncSetAttribute(dopt_embed_sort_kernel<int32_t>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(dopt_embed_sort_kernel<int64_t>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+        g_embed_ready[device] = e == cudaSuccess;
+    }
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return dopt::fail(DOPT_E_CUDA, "%s: shared-memory limit: %s", who, cudaGetErrorString(e));
+    }
+    return DOPT_OK;
+}
+
+int check_ids(const char *who, const void *ids, int32_t id_bytes, int64_t tokens, int64_t vocab, int64_t cols) {
+    using dopt::fail;
+    if (id_bytes != 4 && id_bytes != 8) return fail(DOPT_E_ARG, "%s: id_bytes %d (4 or 8)", who, id_bytes);
+    if (tokens < 0 || tokens > INT32_MAX || vocab < 1 || vocab > INT32_MAX || cols < 1 || cols > DOPT_MAX_COLS)
+        return fail(DOPT_E_ARG, "%s: tokens %lld, vocab %lld, cols %lld", who, static_cast<long long>(tokens),
+                    static_cast<long long>(vocab), static_cast<long long>(cols));
+    if (tokens > 0 && !ids) return fail(DOPT_E_ARG, "%s: ids is NULL", who);
+    if (!aligned_to(ids, size_t(id_bytes))) return fail(DOPT_E_ALIGN, "%s: ids is not aligned to its elements", who);
+    return DOPT_OK;
+}
+
+template <typename T>
+int launch_embed(const char *who, const EmbedArgs &a, cudaStream_t stream) {
+    const dim3 grid(unsigned((a.tokens + 4 * kWarps - 1) / (4 * kWarps)), unsigned((a.cols + kWarpCols - 1) / kWarpCols));
+    return a.wide ? launch_op(who, dopt_embed_kernel<T, int64_t>, grid, dim3(kEmbedThreads), 0, stream, a)
+                  : launch_op(who, dopt_embed_kernel<T, int32_t>, grid, dim3(kEmbedThreads), 0, stream, a);
+}
+
+template <typename T, typename G>
+int launch_grad(const char *who, const EmbedGradArgs &a, cudaStream_t stream) {
+    const int64_t long_blocks = int64_t(a.chunks) * a.pieces;
+    const int64_t blocks = std::min<int64_t>((a.vocab * a.pieces + 2 * kWarps - 1) / (2 * kWarps), 1 << 20);
+    return launch_op(who, dopt_embed_grad_kernel<T, G>, dim3(unsigned(long_blocks + blocks)), dim3(kEmbedThreads), 0,
+                     stream, a);
+}
+template <typename T>
+int launch_grad(const char *who, dopt_dtype grad, const EmbedGradArgs &a, cudaStream_t stream) {
+    switch (grad) {
+        case DOPT_BF16: return launch_grad<T, __nv_bfloat16>(who, a, stream);
+        case DOPT_FP16: return launch_grad<T, __half>(who, a, stream);
+        default: return launch_grad<T, float>(who, a, stream);
+    }
+}
+
+}  // namespace
+
+extern "C" int dopt_embed(const void *table, dopt_dtype dtype, int64_t vocab, int64_t cols, int64_t ld_table,
+                          const void *ids, int32_t id_bytes, int64_t tokens, float scale, void *out, int64_t ld_out,
+                          uint32_t flags, cudaStream_t stream) {
+    using dopt::fail;
+    dopt::clear_error();
+    const char *who = "dopt_embed";
+    OpRange range(who);
+    int rc = check_ids(who, ids, id_bytes, tokens, vocab, cols);
+    if (rc != DOPT_OK) return rc;
+    if (!valid_dtype(dtype)) return fail(DOPT_E_ARG, "%s: unknown dtype %d", who, int(dtype));
+    if (ld_table < cols || ld_out < cols)
+        return fail(DOPT_E_ARG, "%s: row strides %lld, %lld for %lld columns", who, static_cast<long long>(ld_table),
+                    static_cast<long long>(ld_out), static_cast<long long>(cols));
+    if (flags & ~uint32_t(DOPT_EMBED_ACCUMULATE)) return fail(DOPT_E_ARG, "%s: unknown flags 0x%x", who, flags);
+    if (tokens > 0 && (!table || !out)) return fail(DOPT_E_ARG, "%s: NULL table or out", who);
+    const size_t b = elem_bytes(dtype);
+    if (!aligned_to(table, b) || !aligned_to(out, b))
+        return fail(DOPT_E_ALIGN, "%s: table or out is not aligned to its elements", who);
+    if (tokens == 0) return DOPT_OK;
+    EmbedArgs a{};
+    a.table = table;
+    a.ids = ids;
+    a.out = out;
+    a.ld_table = ld_table;
+    a.ld_out = ld_out;
+    a.tokens = tokens;
+    a.vocab = vocab;
+    a.cols = int32_t(cols);
+    a.wide = id_bytes == 8;
+    a.vec = (address_bits(table) | address_bits(out) | uint64_t(ld_table) * b | uint64_t(ld_out) * b) % 16 == 0;
+    a.accumulate = (flags & DOPT_EMBED_ACCUMULATE) != 0;
+    a.scale = scale;
+    switch (dtype) {
+        case DOPT_BF16: return launch_embed<__nv_bfloat16>(who, a, stream);
+        case DOPT_FP16: return launch_embed<__half>(who, a, stream);
+        default: return launch_embed<float>(who, a, stream);
+    }
+}
+
+extern "C" int dopt_embed_workspace(int64_t tokens, int64_t vocab, int64_t cols, int64_t *bytes) {
+    dopt::clear_error();
+    const char *who = "dopt_embed_workspace";
+    if (!bytes) return dopt::fail(DOPT_E_ARG, "%s: bytes is NULL", who);
+    if (tokens < 0 || tokens > INT32_MAX || vocab < 1 || vocab > INT32_MAX || cols < 1 || cols > DOPT_MAX_COLS)
+        return dopt::fail(DOPT_E_ARG, "%s: tokens %lld, vocab %lld, cols %lld", who, static_cast<long long>(tokens),
+                          static_cast<long long>(vocab), static_cast<long long>(cols));
+    *bytes = EmbedSpace(tokens, vocab, cols).bytes;
+    return DOPT_OK;
+}
+
+extern "C" int dopt_embed_grad(const void *ids, int32_t id_bytes, int64_t tokens, const void *d_out, dopt_dtype dtype,
+                               int64_t cols, int64_t ld, int64_t vocab, float scale, void *grad, dopt_dtype grad_dtype,
+                               int64_t grad_numel, int64_t grad_offset, uint32_t flags, void *workspace,
+                               int64_t workspace_bytes, cudaStream_t stream) {
+    using dopt::fail;
+    dopt::clear_error();
+    const char *who = "dopt_embed_grad";
+    OpRange range(who);
+    int rc = check_ids(who, ids, id_bytes, tokens, vocab, cols);
+    if (rc != DOPT_OK) return rc;
+    if (!valid_dtype(dtype) || !valid_dtype(grad_dtype)) return fail(DOPT_E_ARG, "%s: unknown dtype", who);
+    if (ld < cols)
+        return fail(DOPT_E_ARG, "%s: row stride %lld for %lld columns", who, static_cast<long long>(ld),
+                    static_cast<long long>(cols));
+    if (flags & ~uint32_t(DOPT_EMBED_ACCUMULATE)) return fail(DOPT_E_ARG, "%s: unknown flags 0x%x", who, flags);
+    if (!grad || (tokens > 0 && !d_out)) return fail(DOPT_E_ARG, "%s: NULL grad or d_out", who);
+    if (grad_offset < 0 || grad_offset > grad_numel - vocab * cols)
+        return fail(DOPT_E_ARG, "%s: %lld x %lld grads at %lld leave a buffer of %lld", who,
+                    static_cast<long long>(vocab), static_cast<long long>(cols), static_cast<long long>(grad_offset),
+                    static_cast<long long>(grad_numel));
+    const size_t b = elem_bytes(dtype), gb = elem_bytes(grad_dtype);
+    if (!aligned_to(d_out, b) || !aligned_to(grad, gb))
+        return fail(DOPT_E_ALIGN, "%s: d_out or grad is not aligned to its elements", who);
+    const EmbedSpace space(tokens, vocab, cols);
+    if (!workspace || workspace_bytes < space.bytes)
+        return fail(DOPT_E_ARG, "%s: workspace of %lld bytes, %lld are needed", who,
+                    static_cast<long long>(workspace ? workspace_bytes : 0), static_cast<long long>(space.bytes));
+    if (!aligned_to(workspace, 16)) return fail(DOPT_E_ALIGN, "%s: workspace is not 16-byte aligned", who);
+    char *ws = static_cast<char *>(workspace);
+    EmbedGradArgs a{};
+    a.ids = ids;
+    a.d_out = d_out;
+    a.grad = static_cast<char *>(grad) + grad_offset * int64_t(gb);
+    a.first = reinterpret_cast<int32_t *>(ws + space.first);
+    a.token = reinterpret_cast<int32_t *>(ws + space.token);
+    a.row = reinterpret_cast<int32_t *>(ws + space.row);
+    a.list = reinterpret_cast<int2 *>(ws + space.list);
+    a.arrived = reinterpret_cast<int32_t *>(ws + space.arrived);
+    a.partial = reinterpret_cast<float *>(ws + space.partial);
+    a.ld = ld;
+    a.tokens = tokens;
+    a.vocab = vocab;
+    a.part_ld = space.part_ld;
+    a.cols = int32_t(cols);
+    a.pieces = int32_t(space.pieces);
+    a.chunks = int32_t(space.chunks);
+    a.vec = (address_bits(d_out) | uint64_t(ld) * b) % 16 == 0;
+    a.vec_grad = (address_bits(a.grad) | uint64_t(cols) * gb) % 16 == 0;
+    a.accumulate = (flags & DOPT_EMBED_ACCUMULATE) != 0;
+    a.scale = scale;
+    a.range = int32_t(std::min<int64_t>(kMostRange, std::max<int64_t>(32, (vocab + 151) / 152)));
+    const size_t smem = size_t(kSortWarps) * a.range * sizeof(uint32_t);
+    const dim3 grid(unsigned((vocab + a.range - 1) / a.range));
+    if (int64_t(a.chunks) * a.pieces > INT32_MAX - (1 << 20))
+        return fail(DOPT_E_ARG, "%s: %lld tokens of %lld columns are too many for one call", who,
+                    static_cast<long long>(tokens), static_cast<long long>(cols));
+    if ((rc = set_up_sort(who)) != DOPT_OK) return rc;
+    auto sort = id_bytes == 8 ? dopt_embed_sort_kernel<int64_t> : dopt_embed_sort_kernel<int32_t>;
+    rc = launch_op(who, sort, grid, dim3(kSortThreads), smem, stream, a);
+    if (rc != DOPT_OK) return rc;
+    switch (dtype) {
+        case DOPT_BF16: return launch_grad<__nv_bfloat16>(who, grad_dtype, a, stream);
+        case DOPT_FP16: return launch_grad<__half>(who, grad_dtype, a, stream);
+        default: return launch_grad<float>(who, grad_dtype, a, stream);
+    }
+}

@@ -1,0 +1,192 @@
+"""Python binding of the operators of a language model's two ends and of its
+residual stream in include/dopt.h: the token embedding (``dopt_embed*``), the
+norms around a block (``dopt_norm*``) and the loss of the output matrix's logits
+(``dopt_head_loss*``).
+
+As in :mod:`.layer_ops`, every function checks what raw pointers cannot carry
+(device, dtype, shape, strides), passes pointers and sizes to libdopt.so, and is
+asynchronous on `stream` (default: torch's current stream).  Outputs and
+workspaces are the caller's; params' gradients go to offsets of a flat grad
+buffer.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from .binding import _check, dopt_norm_cfg, dopt_norm_params, lib
+from .layer_ops import _bad, _call, _cuda_index, _dense, _dtype_code, _rows
+
+DOPT_EMBED_ACCUMULATE = 1
+DOPT_NORM_RMS = 0
+DOPT_NORM_LAYER = 1
+DOPT_NORM_MAX_COLS = 16384
+DOPT_NORM_ACCUMULATE = 1
+
+_KINDS = {"rms": DOPT_NORM_RMS, "layer": DOPT_NORM_LAYER}
+_NORM_PARAMS = ("weight", "bias", "post_weight", "post_bias", "gate")
+
+
+def _bytes(n: int, device):
+    return torch.empty(max(n, 16), dtype=torch.uint8, device="cuda" if device is None else device)
+
+
+def _workspace(workspace, index: int):
+    """(address, bytes) of a workspace."""
+    if workspace is None:
+        return None, 0
+    if workspace.get_device() != index or workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
+        raise _bad(f"workspace must be a contiguous uint8 tensor on cuda:{index}")
+    return workspace.data_ptr(), workspace.numel()
+
+
+def _numbers(t, name: str, index: int):
+    """(address, bytes of an element, count) of contiguous one-dimensional int32 or int64 numbers."""
+    if t.dim() != 1 or not t.is_contiguous() or t.get_device() != index:
+        raise _bad(f"{name} must be a contiguous one-dimensional tensor on cuda:{index}, got "
+                   f"{tuple(t.shape)} on {t.device}")
+    wide = t.dtype is torch.int64
+    if not wide and t.dtype is not torch.int32:
+        raise _bad(f"{name} has dtype {t.dtype}, expected int32 or int64")
+    return t.data_ptr(), 8 if wide else 4, t.shape[0]
+
+
+def _flat(grad, index: int):
+    """(address, type code, elements) of a flat grad buffer."""
+    if grad.dim() != 1:
+        raise _bad("grad must be one-dimensional")
+    n = grad.numel()
+    return _dense(grad, "grad", grad.dtype, (n,), index), _dtype_code(grad.dtype, "grad"), n
+
+
+# ---------------------------------------------------------------------------
+# Token embedding
+# ---------------------------------------------------------------------------
+
+def dopt_embed(table, ids, out, scale: float = 1.0, accumulate: bool = False, stream=None) -> None:
+    """out[t] = scale * table[ids[t]]; zeros where ids[t] is outside the table.
+
+    table: [vocab, cols] with contiguous rows; ids: [tokens] int32 or int64;
+    out: [tokens, cols] with contiguous rows, of the table's type.  accumulate:
+    add to out instead (an id outside then leaves its row as it is).
+    """
+    index = _cuda_index(table, "table")
+    if table.dim() != 2:
+        raise _bad("table must be [vocab, cols]")
+    vocab, cols = table.shape
+    ip, wide, tokens = _numbers(ids, "ids", index)
+    tp, ld = _rows(table, "table", table.dtype, (vocab, cols), index)
+    op, ld_out = _rows(out, "out", table.dtype, (tokens, cols), index)
+    _call(index, stream, lib().dopt_embed, tp, _dtype_code(table.dtype, "table"), vocab, cols, ld, ip, wide, tokens,
+          scale, op, ld_out, DOPT_EMBED_ACCUMULATE if accumulate else 0)
+
+
+def embed_workspace(tokens: int, vocab: int, cols: int, device=None):
+    """A workspace for :func:`dopt_embed_grad` of these sizes and of any fewer
+    tokens (a uint8 tensor)."""
+    n = ctypes.c_int64()
+    _check(lib().dopt_embed_workspace(int(tokens), int(vocab), int(cols), ctypes.byref(n)))
+    return _bytes(n.value, device)
+
+
+def dopt_embed_grad(ids, d_out, grad, grad_offset: int, vocab: int, scale: float = 1.0, accumulate: bool = False,
+                    workspace=None, stream=None) -> None:
+    """The table's gradient, scale times the sum of d_out's rows of each id,
+    into grad[grad_offset:grad_offset + vocab * cols].
+
+    ids: [tokens] int32 or int64 (those outside [0, vocab) are left out);
+    d_out: [tokens, cols] with contiguous rows; grad: a 1-D contiguous bf16,
+    fp16 or fp32 tensor, e.g. a grad replica of :func:`dopt_step`.  accumulate:
+    add to the grads that are there.  workspace: from :func:`embed_workspace`.
+    """
+    index = _cuda_index(d_out, "d_out")
+    if d_out.dim() != 2:
+        raise _bad("d_out must be [tokens, cols]")
+    ip, wide, tokens = _numbers(ids, "ids", index)
+    cols = d_out.shape[1]
+    dp, ld = _rows(d_out, "d_out", d_out.dtype, (tokens, cols), index)
+    gp, code, numel = _flat(grad, index)
+    wp, wn = _workspace(workspace, index)
+    _call(index, stream, lib().dopt_embed_grad, ip, wide, tokens, dp, _dtype_code(d_out.dtype, "d_out"), cols, ld,
+          vocab, scale, gp, code, numel, grad_offset, DOPT_EMBED_ACCUMULATE if accumulate else 0, wp, wn)
+
+
+# ---------------------------------------------------------------------------
+# Norms around a block
+# ---------------------------------------------------------------------------
+
+def _norm_setting(kind, post, eps, scale, params, row_gate, dtype, rows, cols, index):
+    code = _KINDS.get(kind)
+    if code is None:
+        raise _bad(f"unknown norm {kind!r}: one of {', '.join(_KINDS)}")
+    at = [None if p is None else _dense(p, name, dtype, (cols,), index) for name, p in zip(_NORM_PARAMS, params)]
+    at.append(None if row_gate is None else _dense(row_gate, "row_gate", torch.float32, (rows,), index))
+    return dopt_norm_cfg(code, 1 if post else 0, eps, scale), dopt_norm_params(*at)
+
+
+def _matrix(t, name, dtype, shape, index):
+    return (None, shape[1]) if t is None else _rows(t, name, dtype, shape, index)
+
+
+def dopt_norm(kind: str, x, n, weight=None, bias=None, y=None, h=None, post: bool = False, post_weight=None,
+              post_bias=None, gate=None, row_gate=None, scale: float = 1.0, eps: float = 1e-5, stream=None) -> None:
+    """h = x + scale * row_gate * gate * u and n = norm(h), with u the block's
+    output y, or with `post` its norm.
+
+    kind: "rms" or "layer".  x, y, h, n: [rows, cols] with contiguous rows, of
+    one type; h or n may be None (not wanted), h may be x.  Without y: n =
+    norm(x).  weight, bias, post_weight, post_bias, gate: [cols] of that type,
+    row_gate: fp32 [rows]; None counts as ones (biases: zeros).
+    """
+    index = _cuda_index(x, "x")
+    if x.dim() != 2:
+        raise _bad("x must be [rows, cols]")
+    dt, shape = x.dtype, tuple(x.shape)
+    cfg, params = _norm_setting(kind, post, eps, scale, (weight, bias, post_weight, post_bias, gate), row_gate, dt,
+                                *shape, index)
+    _call(index, stream, lib().dopt_norm, ctypes.byref(cfg), ctypes.byref(params), _dtype_code(dt, "x"), *shape,
+          *_rows(x, "x", dt, shape, index), *_matrix(y, "y", dt, shape, index), *_matrix(h, "h", dt, shape, index),
+          *_matrix(n, "n", dt, shape, index))
+
+
+def norm_workspace(rows: int, cols: int, device=None):
+    """A workspace for :func:`dopt_norm_grad` of these sizes and of any fewer
+    rows (a uint8 tensor)."""
+    n = ctypes.c_int64()
+    _check(lib().dopt_norm_workspace(int(rows), int(cols), ctypes.byref(n)))
+    return _bytes(n.value, device)
+
+
+def dopt_norm_grad(kind: str, h, d_n, d_x, weight=None, y=None, d_y=None, d_h=None, post: bool = False,
+                   post_weight=None, post_bias=None, gate=None, row_gate=None, scale: float = 1.0, eps: float = 1e-5,
+                   d_row_gate=None, grad=None, grad_offsets=None, accumulate: bool = False, workspace=None,
+                   stream=None) -> None:
+    """The gradients of :func:`dopt_norm` from h (as it was written; x where
+    there was no y), y, and the gradients d_n of n and d_h of h (either may be
+    None).
+
+    d_x (may be d_h) and d_y: [rows, cols], or None; d_row_gate: fp32 [rows] or
+    None.  grad: a flat grad buffer; grad_offsets: where in it the gradients of
+    the params go, a dict of "weight", "bias", "post_weight", "post_bias" and
+    "gate" (those that are wanted).  accumulate: add to the grads that are
+    there.  workspace: from :func:`norm_workspace`.
+    """
+    index = _cuda_index(h, "h")
+    if h.dim() != 2:
+        raise _bad("h must be [rows, cols]")
+    dt, shape = h.dtype, tuple(h.shape)
+    offsets = dict(grad_offsets or {})
+    at = [offsets.pop(name, -1) for name in _NORM_PARAMS]
+    if offsets:
+        raise _bad(f"no such params: {', '.join(map(str, offsets))} (of {', '.join(_NORM_PARAMS)})")
+    cfg, params = _norm_setting(kind, post, eps, scale, (weight, None, post_weight, post_bias, gate), row_gate, dt,
+                                *shape, index)
+    gp, code, numel = (None, 0, 0) if grad is None else _flat(grad, index)
+    wp, wn = _workspace(workspace, index)
+    rp = None if d_row_gate is None else _dense(d_row_gate, "d_row_gate", torch.float32, (shape[0],), index)
+    _call(index, stream, lib().dopt_norm_grad, ctypes.byref(cfg), ctypes.byref(params), _dtype_code(dt, "h"), *shape,
+          *_rows(h, "h", dt, shape, index), *_matrix(y, "y", dt, shape, index), *_matrix(d_n, "d_n", dt, shape, index),
+          *_matrix(d_h, "d_h", dt, shape, index), *_matrix(d_x, "d_x", dt, shape, index),
+          *_matrix(d_y, "d_y", dt, shape, index), rp, gp, code, numel, (ctypes.c_int64 * 5)(*at),
+          DOPT_NORM_ACCUMULATE if accumulate else 0, wp, wn)
