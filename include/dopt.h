@@ -992,6 +992,109 @@ int dopt_norm_grad(const dopt_norm_cfg *cfg, const dopt_norm_params *params, dop
  * Host only.  Errors: DOPT_E_ARG. */
 int dopt_norm_workspace(int64_t rows, int64_t cols, int64_t *bytes);
 
+/* The most tokens and the largest vocabulary of a call. */
+#define DOPT_HEAD_MAX_ROWS 16777216
+#define DOPT_HEAD_MAX_VOCAB 16777216
+
+/* dopt_head_loss_grad flag: add to the output matrix's grads in the buffer. */
+#define DOPT_HEAD_ACCUMULATE 1u
+
+/*
+ * The cross entropy of a language model's output matrix, without the logits:
+ * with logit[t][v] = sum over c of x[t][c] * weight[v][c],
+ *     lse[t]  = log(sum over v of exp(logit[t][v]))
+ *     loss[t] = lse[t] - logit[t][targets[t]]
+ * and 0 where targets[t] is outside [0, vocab) (an ignored token; its lse is
+ * computed all the same).  The logits are fp32 sums of exact products on the
+ * tensor cores, and live in tensor memory alone; maxima and sums of
+ * exponentials are fp32.
+ *   x          device [rows][width], row stride ld_x, bf16 or fp16
+ *   weight     device [vocab][width], row stride ld_w, of the same type, e.g. a
+ *              param replica of dopt_step
+ *   targets    device int32 or int64 (target_bytes 4 or 8) [rows]
+ *   loss, lse  device fp32 [rows], written
+ *   workspace  device, 16-byte aligned, dopt_head_loss_workspace bytes; calls
+ *              that share one must not overlap on the GPU
+ * Matrices whose rows are not 16-byte aligned are first copied into rows that
+ * are.  rows <= DOPT_HEAD_MAX_ROWS, 1 <= vocab <= DOPT_HEAD_MAX_VOCAB, 1 <=
+ * width <= DOPT_MAX_COLS.  The first call on a device looks up what its kernels
+ * need; make it before any stream capture.  A wait inside a kernel that does
+ * not end within 2 s (a copy that never completes) ends the work of its pair of
+ * blocks instead of hanging: it is counted (dopt_head_timeouts), and what the
+ * pair had still to write becomes NaN, here and in dopt_head_loss_grad.
+ * Errors: DOPT_E_ARG, DOPT_E_ALIGN, DOPT_E_CUDA.
+ */
+int dopt_head_loss(const void *x, dopt_dtype dtype, int64_t rows, int64_t width, int64_t ld_x,
+                   const void *weight, int64_t vocab, int64_t ld_w, const void *targets,
+                   int32_t target_bytes, float *loss, float *lse, void *workspace,
+                   int64_t workspace_bytes, cudaStream_t stream);
+
+/* Bytes of workspace for dopt_head_loss of these sizes and of any fewer rows.
+ * aligned: the rows of x and weight are 16-byte aligned (0: they may not be,
+ * and are copied; a width that is not a multiple of 8 counts as 0).  Host only.
+ * Errors: DOPT_E_ARG. */
+int dopt_head_loss_workspace(int64_t rows, int64_t width, int64_t vocab, int32_t aligned,
+                             int64_t *bytes);
+
+/*
+ * The gradients of dopt_head_loss from its lse and the gradients d_loss and
+ * d_lse of its outputs (d_lse: a penalty on the logits' scale; NULL: zeros):
+ *     d[t][v]  = (d_loss[t] + d_lse[t]) * exp(logit[t][v] - lse[t])
+ *                - d_loss[t] * [v == targets[t]]
+ *     d_x[t]   = sum over v of d[t][v] * weight[v]
+ *     grad[grad_offset + v * width + c] (+)= sum over t of d[t][v] * x[t][c]
+ * where a target outside [0, vocab) makes d_loss[t] count as 0.  The vocabulary
+ * goes in pieces: the logits of one are computed again and their gradients d
+ * kept in the workspace for the two products.  d is rounded to x's type (with
+ * fp16, multiplied by a power of two that keeps the largest in range), which
+ * the 16-bit results round at least as much; for fp32 grads what that rounding
+ * leaves is multiplied too, so that d counts with twice the bits.  Sums are
+ * fp32 (of at most 1024 products, 512 with fp16, on the tensor cores for fp32
+ * grads), in an order that depends on the sizes alone, and each result is
+ * rounded once (after adding the old grad, with DOPT_HEAD_ACCUMULATE).
+ *   lse, d_loss, d_lse  device fp32 [rows]
+ *   d_x        device [rows][width], row stride ld_d_x, of x's type, written;
+ *              or NULL
+ *   grad       device, grad_numel elements of grad_dtype, e.g. a grad replica
+ *              of dopt_step; or NULL (a frozen output matrix)
+ *   workspace  device, 16-byte aligned: what dopt_head_loss_grad_workspace
+ *              says.  A call takes the fewest pieces that it has room for; the
+ *              results depend on their number by rounding only.  Calls that
+ *              share one must not overlap on the GPU.
+ * rows = 0 writes zeros to grad (leaves it alone with DOPT_HEAD_ACCUMULATE).
+ * Otherwise as dopt_head_loss.  Errors: DOPT_E_ARG, DOPT_E_ALIGN, DOPT_E_CUDA.
+ */
+int dopt_head_loss_grad(const void *x, dopt_dtype dtype, int64_t rows, int64_t width, int64_t ld_x,
+                        const void *weight, int64_t vocab, int64_t ld_w, const void *targets,
+                        int32_t target_bytes, const float *lse, const float *d_loss,
+                        const float *d_lse, void *d_x, int64_t ld_d_x, void *grad,
+                        dopt_dtype grad_dtype, int64_t grad_numel, int64_t grad_offset,
+                        uint32_t flags, void *workspace, int64_t workspace_bytes,
+                        cudaStream_t stream);
+
+/* Bytes of workspace for dopt_head_loss_grad of these sizes with the vocabulary
+ * in `pieces` pieces (1: the fastest; more take less), grads of grad_dtype
+ * (16-bit ones where there are none) and rows aligned or not, as for
+ * dopt_head_loss_workspace.  Host only.  Errors: DOPT_E_ARG. */
+int dopt_head_loss_grad_workspace(int64_t rows, int64_t width, int64_t vocab,
+                                  dopt_dtype grad_dtype, int64_t pieces, int32_t aligned,
+                                  int64_t *bytes);
+
+/* Count of blocks of dopt_head_loss and dopt_head_loss_grad on the current
+ * device whose waits ran out (0 unless a copy or product failed to complete);
+ * with reset != 0 the count is then cleared.  Synchronous.  Errors: DOPT_E_ARG
+ * (NULL count), DOPT_E_CUDA. */
+int dopt_head_timeouts(int reset, uint32_t *count);
+
+/* Test build only (DOPT_DEVICE_CHECKS, libdopt_checked.so): in every kernel of
+ * dopt_head_loss and dopt_head_loss_grad launched after this call on the
+ * current device, the first pair of blocks issues the products of its first
+ * `items` items only, so that its waits run out and it takes the failure path
+ * described at dopt_head_loss, without any fault; -1 restores normal work.
+ * Synchronous.  Errors: DOPT_E_STATE in the product build, DOPT_E_ARG (items <
+ * -1), DOPT_E_CUDA. */
+int dopt_head_wait_test(int32_t items);
+
 /* Device-side checks (library infrastructure for testing; the pages have
  * no counterpart): a test build of the library, compiled with
  * DOPT_DEVICE_CHECKS defined; built by build(checked=True) as

@@ -93,15 +93,24 @@ _LAYER_OPS = (
 # The same for the operators of a language model's ends and residual stream.
 _MODEL_OPS = (
     "DOPT_EMBED_ACCUMULATE",
+    "DOPT_HEAD_ACCUMULATE",
+    "DOPT_HEAD_MAX_ROWS",
+    "DOPT_HEAD_MAX_VOCAB",
     "DOPT_NORM_ACCUMULATE",
     "DOPT_NORM_LAYER",
     "DOPT_NORM_MAX_COLS",
     "DOPT_NORM_RMS",
     "dopt_embed",
     "dopt_embed_grad",
+    "dopt_head_loss",
+    "dopt_head_loss_grad",
     "dopt_norm",
     "dopt_norm_grad",
     "embed_workspace",
+    "head_loss_grad_workspace",
+    "head_loss_workspace",
+    "head_timeouts",
+    "head_wait_test",
     "norm_workspace",
 )
 

@@ -81,16 +81,6 @@ class dopt_adam_cfg(ctypes.Structure):
                 ("grad_scale", ctypes.c_float)]
 
 
-class dopt_norm_cfg(ctypes.Structure):
-    _fields_ = [("kind", ctypes.c_int32), ("post", ctypes.c_int32), ("eps", ctypes.c_float),
-                ("scale", ctypes.c_float)]
-
-
-class dopt_norm_params(ctypes.Structure):
-    _fields_ = [(name, ctypes.c_void_p) for name in
-                ("weight", "bias", "post_weight", "post_bias", "gate", "row_gate")]
-
-
 _lock = threading.Lock()
 _lib = None
 
@@ -176,11 +166,19 @@ def _declare(lib):
             ("dopt_embed_grad", [vp, i32, i64, vp, ctypes.c_int, i64, i64, i64, ctypes.c_float, vp,
                                  ctypes.c_int, i64, i64, ctypes.c_uint32, vp, i64, vp]),
             ("dopt_embed_workspace", [i64, i64, i64, P(i64)]),
-            ("dopt_norm", [P(dopt_norm_cfg), P(dopt_norm_params), ctypes.c_int, i64, i64, vp, i64, vp,
+            ("dopt_norm", [vp, vp, ctypes.c_int, i64, i64, vp, i64, vp,
                            i64, vp, i64, vp, i64, vp]),
-            ("dopt_norm_grad", [P(dopt_norm_cfg), P(dopt_norm_params), ctypes.c_int, i64, i64]
+            ("dopt_norm_grad", [vp, vp, ctypes.c_int, i64, i64]
              + [vp, i64] * 6 + [vp, vp, ctypes.c_int, i64, P(i64), ctypes.c_uint32, vp, i64, vp]),
-            ("dopt_norm_workspace", [i64, i64, P(i64)])):
+            ("dopt_norm_workspace", [i64, i64, P(i64)]),
+            ("dopt_head_loss_workspace", [i64, i64, i64, i32, P(i64)]),
+            ("dopt_head_loss", [vp, ctypes.c_int, i64, i64, i64, vp, i64, i64, vp, i32, vp, vp, vp, i64,
+                                vp]),
+            ("dopt_head_loss_grad_workspace", [i64, i64, i64, ctypes.c_int, i64, i32, P(i64)]),
+            ("dopt_head_loss_grad", [vp, ctypes.c_int, i64, i64, i64, vp, i64, i64, vp, i32, vp, vp, vp,
+                                     vp, i64, vp, ctypes.c_int, i64, i64, ctypes.c_uint32, vp, i64, vp]),
+            ("dopt_head_timeouts", [ctypes.c_int, P(ctypes.c_uint32)]),
+            ("dopt_head_wait_test", [i32])):
         getattr(lib, name).restype = ctypes.c_int
         getattr(lib, name).argtypes = types
     lib.dopt_last_error.restype = ctypes.c_char_p

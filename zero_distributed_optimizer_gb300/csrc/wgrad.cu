@@ -1,11 +1,10 @@
 // The weight gradients of a linear layer, or of a layer's experts, from the
 // 8-bit checkpoint of its input, written into the flat grad buffer
 // (dopt_ckpt_wgrad; dopt.h states the contract).
-#include <cuda.h>
-
 #include <mutex>
 #include <type_traits>
 
+#include "pairs.cuh"
 #include "rows.cuh"
 
 namespace {
@@ -126,10 +125,6 @@ __device__ __forceinline__ bool products_withheld(int round) {
 __device__ __forceinline__ bool products_withheld(int) { return false; }
 #endif
 
-__device__ __forceinline__ uint32_t smem_of(const void *p) {
-    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-
 // Wait for a phase of a barrier that threads of the cluster arrive on; false
 // once any wait of this CTA has run out of time.  Both CTAs of a pair arrive
 // on the leader's barriers and products of both read and write either one's
@@ -179,22 +174,6 @@ __device__ __forceinline__ void drain(WgradBarriers &b, unsigned long long *empt
         if (!wait_phase(b, empty[s], uint32_t((uses - 1 - s) / ring) & 1)) return;
 }
 
-// A value that is the same in all lanes, and known to be.
-template <typename V>
-__device__ __forceinline__ V uniform(V v) {
-    return __shfl_sync(kFull, v, 0);
-}
-__device__ __forceinline__ bool elect_one() {
-    uint32_t p;
-    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
-    return p != 0;
-}
-
-__device__ __forceinline__ uint32_t leader_address(uint32_t own) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(own));
-    return r;
-}
 // An arrival on the leader's barrier that releases, at the cluster's scope, what
 // this warp stored in shared memory before; that is all that its waiter reads
 // (sums leave tensor memory before tcgen05.fence::before_thread_sync).  A
@@ -206,9 +185,6 @@ __device__ __forceinline__ void arrive_remote(uint32_t cluster_address) {
         "fence.release.sync_restrict::shared::cta.cluster;\n\t"
         "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_address)
         : "memory");
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // Descriptor of an operand slab pair: 128-byte swizzle, 1024 bytes from 8
@@ -403,48 +379,6 @@ __device__ __forceinline__ void store_sums(const WgradArgs &a, G *p, int n, cons
 template <typename G>
 __device__ __forceinline__ G *grad_at(const WgradArgs &a, const WgradItem &it, int c) {
     return static_cast<G *>(a.grad) + a.grad_offset[it.group] + it.o0 * a.cols + c;
-}
-
-// 32 lanes x 16 columns of tensor memory, in flight until wait_sums.
-__device__ __forceinline__ void load_sums(uint32_t at, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(at));
-}
-__device__ __forceinline__ void wait_sums(uint32_t (&r)[16]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-                 :
-                 : "memory");
-}
-
-// 16 columns back to tensor memory, in flight until tcgen05.wait::st.
-__device__ __forceinline__ void put_sums(uint32_t at, const uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16};" ::"r"(at),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
-}
-
-// A warp's 32 lanes of the sums at `from` added to those at `into`.
-__device__ __forceinline__ void add_tile(uint32_t into, uint32_t from, int outs) {
-    for (int o = 0; o < outs; o += 16) {  // (outs is a multiple of 32)
-        uint32_t r[16], more[16];
-        load_sums(into + uint32_t(o), r);
-        load_sums(from + uint32_t(o), more);
-        wait_sums(r);
-        wait_sums(more);
-#pragma unroll
-        for (int q = 0; q < 16; ++q) r[q] = __float_as_uint(__uint_as_float(r[q]) + __uint_as_float(more[q]));
-        put_sums(into + uint32_t(o), r);
-    }
-    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
 // A tile's sums of a warp's 32 columns, at `sums` in tensor memory, to the
@@ -925,10 +859,6 @@ int64_t sum_chunk(dopt_dtype dy, dopt_dtype grad) {
     return grad == DOPT_FP16 ? 16384 / kK : 131072 / kK;
 }
 
-using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
 std::mutex g_wgrad_mutex;
 EncodeTiled g_encode = nullptr;
 int g_pairs[64] = {};  // pairs of SMs of a device, once its kernels are set up
@@ -946,12 +876,9 @@ int set_up(const char *who, EncodeTiled *encode, int *pairs) {
     if (e == cudaSuccess && (device < 0 || device >= 64)) return fail(DOPT_E_ARG, "%s: device %d", who, device);
     std::lock_guard<std::mutex> lock(g_wgrad_mutex);
     if (e == cudaSuccess && !g_encode) {
-        void *f = nullptr;
-        cudaDriverEntryPointQueryResult found{};
-        e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found);
-        if (e == cudaSuccess && (found != cudaDriverEntryPointSuccess || !f))
-            return fail(DOPT_E_CUDA, "%s: the driver has no tensor maps", who);
-        if (e == cudaSuccess) g_encode = reinterpret_cast<EncodeTiled>(f);
+        bool none = false;
+        e = find_encoder(&g_encode, &none);
+        if (none) return fail(DOPT_E_CUDA, "%s: the driver has no tensor maps", who);
     }
     if (e == cudaSuccess && g_pairs[device] == 0) {
         int sms = 0;

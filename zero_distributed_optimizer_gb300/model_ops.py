@@ -15,7 +15,7 @@ import ctypes
 
 import torch
 
-from .binding import _check, dopt_norm_cfg, dopt_norm_params, lib
+from .binding import _check, lib
 from .layer_ops import _bad, _call, _cuda_index, _dense, _dtype_code, _rows
 
 DOPT_EMBED_ACCUMULATE = 1
@@ -23,6 +23,9 @@ DOPT_NORM_RMS = 0
 DOPT_NORM_LAYER = 1
 DOPT_NORM_MAX_COLS = 16384
 DOPT_NORM_ACCUMULATE = 1
+DOPT_HEAD_MAX_ROWS = 16777216
+DOPT_HEAD_MAX_VOCAB = 16777216
+DOPT_HEAD_ACCUMULATE = 1
 
 _KINDS = {"rms": DOPT_NORM_RMS, "layer": DOPT_NORM_LAYER}
 _NORM_PARAMS = ("weight", "bias", "post_weight", "post_bias", "gate")
@@ -116,13 +119,23 @@ def dopt_embed_grad(ids, d_out, grad, grad_offset: int, vocab: int, scale: float
 # Norms around a block
 # ---------------------------------------------------------------------------
 
+class _NormCfg(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("post", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("scale", ctypes.c_float)]
+
+
+class _NormParams(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_void_p) for name in
+                ("weight", "bias", "post_weight", "post_bias", "gate", "row_gate")]
+
+
 def _norm_setting(kind, post, eps, scale, params, row_gate, dtype, rows, cols, index):
     code = _KINDS.get(kind)
     if code is None:
         raise _bad(f"unknown norm {kind!r}: one of {', '.join(_KINDS)}")
     at = [None if p is None else _dense(p, name, dtype, (cols,), index) for name, p in zip(_NORM_PARAMS, params)]
     at.append(None if row_gate is None else _dense(row_gate, "row_gate", torch.float32, (rows,), index))
-    return dopt_norm_cfg(code, 1 if post else 0, eps, scale), dopt_norm_params(*at)
+    return _NormCfg(code, 1 if post else 0, eps, scale), _NormParams(*at)
 
 
 def _matrix(t, name, dtype, shape, index):
@@ -190,3 +203,95 @@ def dopt_norm_grad(kind: str, h, d_n, d_x, weight=None, y=None, d_y=None, d_h=No
           *_matrix(d_h, "d_h", dt, shape, index), *_matrix(d_x, "d_x", dt, shape, index),
           *_matrix(d_y, "d_y", dt, shape, index), rp, gp, code, numel, (ctypes.c_int64 * 5)(*at),
           DOPT_NORM_ACCUMULATE if accumulate else 0, wp, wn)
+
+
+# ---------------------------------------------------------------------------
+# Loss of the output matrix's logits
+# ---------------------------------------------------------------------------
+
+def head_loss_workspace(rows: int, width: int, vocab: int, aligned: bool = True, device=None):
+    """A workspace for :func:`dopt_head_loss` of these sizes and of any fewer
+    rows (a uint8 tensor).  aligned: the rows of x and weight are 16-byte
+    aligned (a width that is not a multiple of 8 counts as False)."""
+    n = ctypes.c_int64()
+    _check(lib().dopt_head_loss_workspace(int(rows), int(width), int(vocab), 1 if aligned else 0, ctypes.byref(n)))
+    return _bytes(n.value, device)
+
+
+def head_loss_grad_workspace(rows: int, width: int, vocab: int, grad_dtype=torch.bfloat16, pieces: int = 1,
+                             aligned: bool = True, device=None):
+    """A workspace for :func:`dopt_head_loss_grad` with the vocabulary in
+    `pieces` pieces: 1 is the fastest, more take less memory (about 2 * rows *
+    vocab / pieces bytes, twice that for fp32 grads)."""
+    n = ctypes.c_int64()
+    _check(lib().dopt_head_loss_grad_workspace(int(rows), int(width), int(vocab), _dtype_code(grad_dtype, "grad"),
+                                               int(pieces), 1 if aligned else 0, ctypes.byref(n)))
+    return _bytes(n.value, device)
+
+
+def _head(x, weight, targets):
+    """(device index, the arguments that both directions begin with)."""
+    index = _cuda_index(x, "x")
+    if x.dim() != 2 or weight.dim() != 2:
+        raise _bad("x must be [rows, width] and weight [vocab, width]")
+    rows, width = x.shape
+    vocab = weight.shape[0]
+    xp, ld_x = _rows(x, "x", x.dtype, (rows, width), index)
+    wp, ld_w = _rows(weight, "weight", x.dtype, (vocab, width), index)
+    tp, wide, n = _numbers(targets, "targets", index)
+    if n != rows:
+        raise _bad(f"targets must have {rows} elements, got {n}")
+    return index, (xp, _dtype_code(x.dtype, "x"), rows, width, ld_x, wp, vocab, ld_w, tp, wide)
+
+
+def dopt_head_loss(x, weight, targets, loss, lse, workspace=None, stream=None) -> None:
+    """lse[t] = log(sum over v of exp(x[t] . weight[v])) and loss[t] = lse[t] -
+    x[t] . weight[targets[t]], 0 where the target is outside [0, vocab).
+
+    x: [rows, width], weight: [vocab, width], bf16 or fp16 with contiguous rows;
+    targets: int32 or int64 [rows]; loss, lse: fp32 [rows].  workspace: from
+    :func:`head_loss_workspace`.
+    """
+    index, args = _head(x, weight, targets)
+    rows, f32 = args[2], torch.float32
+    wp, wn = _workspace(workspace, index)
+    _call(index, stream, lib().dopt_head_loss, *args, _dense(loss, "loss", f32, (rows,), index),
+          _dense(lse, "lse", f32, (rows,), index), wp, wn)
+
+
+def dopt_head_loss_grad(x, weight, targets, lse, d_loss, d_x, grad, grad_offset: int = 0, d_lse=None,
+                        accumulate: bool = False, workspace=None, stream=None) -> None:
+    """The gradients of :func:`dopt_head_loss` from its lse and the gradients of
+    its outputs, d_loss and d_lse (fp32 [rows]; d_lse may be None).
+
+    d_x: [rows, width] of x's type with contiguous rows, or None; grad: a flat
+    grad buffer that takes the matrix's gradient at grad_offset, or None.
+    accumulate: add to the grads that are there.  workspace: from
+    :func:`head_loss_grad_workspace`.
+    """
+    index, args = _head(x, weight, targets)
+    rows, width, f32 = args[2], args[3], torch.float32
+    gp, code, numel = (None, 0, 0) if grad is None else _flat(grad, index)
+    wp, wn = _workspace(workspace, index)
+    _call(index, stream, lib().dopt_head_loss_grad, *args, _dense(lse, "lse", f32, (rows,), index),
+          _dense(d_loss, "d_loss", f32, (rows,), index),
+          None if d_lse is None else _dense(d_lse, "d_lse", f32, (rows,), index),
+          *_matrix(d_x, "d_x", x.dtype, (rows, width), index), gp, code, numel, grad_offset,
+          DOPT_HEAD_ACCUMULATE if accumulate else 0, wp, wn)
+
+
+def head_timeouts(reset: bool = False) -> int:
+    """Blocks of :func:`dopt_head_loss` and its gradient on the current device
+    whose waits ran out of time (0 unless a copy or product failed to complete;
+    what they did not write is then NaN); reset clears it."""
+    c = ctypes.c_uint32(0)
+    _check(lib().dopt_head_timeouts(1 if reset else 0, ctypes.byref(c)))
+    return c.value
+
+
+def head_wait_test(items: int) -> None:
+    """Test build only (dopt_head_wait_test in dopt.h): the first pair of blocks
+    of later launches stops after `items` of its items, so that its waits run
+    out; -1 restores normal work.  Raises DoptError with DOPT_E_STATE in the
+    product build."""
+    _check(lib().dopt_head_wait_test(int(items)))
