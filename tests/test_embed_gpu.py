@@ -110,7 +110,7 @@ def test_embed_grad(dtype, size, layout):
     g = torch.Generator(device=DEV).manual_seed(tokens + cols)
     ids = _ids(tokens, vocab, how, g, torch.int32 if layout == "strided" else torch.int64)
     d_out = _layout(torch.randn(tokens, cols, generator=g, device=DEV).to(dtype), layout)
-    d_out[(ids < 0) | (ids >= vocab)] = float("nan")  # never read
+    d_out[(ids < 0) | (ids >= vocab)] = float("nan")
     ws = dopt.embed_workspace(tokens, vocab, cols)
     ws.fill_(255)
     scale = 0.75

@@ -13,9 +13,9 @@ constexpr int kWarpCols = 32 * kCols;    // columns a warp
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMostRange = 1024;         // rows of the table that one sorting block owns
-constexpr int kChunk = 256;              // sorted tokens of a block that sums long runs
-constexpr int kShort = 32;               // tokens of a row that one warp sums
-static_assert(kChunk == kWarps * kShort, "a warp of the long runs' blocks takes 32 tokens");
+constexpr int kChunk = 256;              // sorted tokens of a summing block
+constexpr int kShort = 32;               // of which a warp takes
+static_assert(kChunk == kWarps * kShort, "a block's warps take a chunk");
 
 struct EmbedArgs {
     const void *table;
@@ -89,14 +89,15 @@ struct EmbedGradArgs {
     int32_t *first;         // [vocab + 1] the first sorted place of each row of the table
     int32_t *token;         // [tokens] the tokens by row, in order within one
     int32_t *row;           // [tokens] their rows
-    int2 *list;             // [tokens] (token, row in its range), by range
-    int32_t *arrived;       // [chunks * pieces] parts of the run that begins in a chunk
-    float *partial;         // [2 * chunks][part_ld] sums of runs that go on past a chunk
+    int2 *list;             // [tokens] (token, row in its range and more), by range
+    int32_t *arrived;       // [chunks * pieces] parts of the run that goes on after a chunk
+    float *partial;         // [2 * chunks][part_ld] sums of runs that reach over a chunk's ends
     int64_t ld, tokens, vocab, part_ld;
     int32_t cols, pieces;   // pieces: of 256 columns
-    int32_t range, chunks;
+    int32_t range, ranges, chunks;
     int32_t vec, vec_grad;  // d_out's, the grads' rows are 16-byte aligned
     int32_t accumulate;
+    int32_t grad_bytes;     // of an element
     float scale;
 };
 
@@ -116,10 +117,30 @@ __device__ __forceinline__ uint32_t over_warps(uint32_t mine, uint32_t *buffer, 
     return __shfl_sync(kFull, sum - v, warp);
 }
 
+// Zeros to all grads, by the blocks that sort nothing: 16 bytes a store, the
+// ends element by element.
+__device__ __forceinline__ void zero_grads(const EmbedGradArgs &a, int64_t block, int64_t blocks) {
+    char *p = static_cast<char *>(a.grad), *end = p + a.vocab * a.cols * a.grad_bytes;
+    char *from = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(p) + 15) & ~uintptr_t(15));
+    char *to = reinterpret_cast<char *>(reinterpret_cast<uintptr_t>(end) & ~uintptr_t(15));
+    if (from > to) from = to = end;  // (fewer than 16 bytes, between two boundaries)
+    const int64_t n = (to - from) / 16;
+    for (int64_t i = block * kSortThreads + threadIdx.x; i < n; i += blocks * kSortThreads)
+        reinterpret_cast<uint4 *>(from)[i] = make_uint4(0, 0, 0, 0);
+    if (block == 0) {  // whole elements of 2 bytes
+        for (char *q = p + 2 * threadIdx.x; q < from; q += 2 * kSortThreads) *reinterpret_cast<uint16_t *>(q) = 0;
+        for (char *q = to + 2 * threadIdx.x; q < end; q += 2 * kSortThreads) *reinterpret_cast<uint16_t *>(q) = 0;
+    }
+}
+
 // The tokens sorted by id (stable).  A block owns `range` rows of the table.
 // It goes through all ids, so that it knows without any other block how many
 // lie below its own, lists those that are its own in order and sorts the
-// list: counts of each (warp, row), their prefixes, places.
+// list: counts of each (warp, row), their prefixes, places.  A lane's rank
+// among its warp's tokens of one row comes from a ballot per bit of the row
+// and is kept with the token for the second pass.  The sort is bound by
+// latencies, so blocks that write the zeros of the rows without tokens run
+// beside it.
 template <typename I>
 __global__ void __launch_bounds__(kSortThreads) dopt_embed_sort_kernel(const __grid_constant__ EmbedGradArgs a) {
     extern __shared__ uint32_t count[];  // [warps][range]
@@ -128,15 +149,20 @@ __global__ void __launch_bounds__(kSortThreads) dopt_embed_sort_kernel(const __g
     const uint32_t before = (1u << lane) - 1;
     let_dependents_start();
     wait_for_grids_before();
+    if (int(blockIdx.x) >= a.ranges) {
+        zero_grads(a, blockIdx.x - a.ranges, gridDim.x - a.ranges);
+        return;
+    }
     const int64_t lo = int64_t(blockIdx.x) * a.range;
     const int rows = int(min(int64_t(a.range), a.vocab - lo));
     for (int64_t i = int64_t(blockIdx.x) * kSortThreads + threadIdx.x; i < int64_t(a.chunks) * a.pieces;
-         i += int64_t(gridDim.x) * kSortThreads)
+         i += int64_t(a.ranges) * kSortThreads)
         a.arrived[i] = 0;
+    for (int i = threadIdx.x; i < kSortWarps * a.range; i += kSortThreads) count[i] = 0;
 
     constexpr int kAhead = 8;
     const int64_t stretch = ((a.tokens + kSortWarps - 1) / kSortWarps + 31) / 32 * 32;
-    const int64_t from = warp * stretch, to = min(a.tokens, from + stretch);
+    const int64_t from = min(a.tokens, warp * stretch), to = min(a.tokens, from + stretch);
     uint32_t own = 0, below = 0;
     for (int64_t i = from; i < to; i += 32 * kAhead) {
         int64_t id[kAhead];
@@ -153,7 +179,7 @@ __global__ void __launch_bounds__(kSortThreads) dopt_embed_sort_kernel(const __g
     uint32_t total, base;
     uint32_t place = over_warps(own, buffer, total);
     over_warps(below, buffer, base);
-    if (total > 0) {  // (the same in all threads)
+    if (own > 0) {
         for (int64_t i = from; i < to; i += 32 * kAhead) {
             int64_t id[kAhead];
 #pragma unroll
@@ -168,15 +194,25 @@ __global__ void __launch_bounds__(kSortThreads) dopt_embed_sort_kernel(const __g
             }
         }
     }
-    for (int i = threadIdx.x; i < kSortWarps * a.range; i += kSortThreads) count[i] = 0;
     __syncthreads();
     uint32_t *mine = count + warp * a.range;
     const uint32_t share = ((total + kSortWarps - 1) / kSortWarps + 31) / 32 * 32;
     const uint32_t begin = min(total, warp * share), end = min(total, begin + share);
+    const int bits = 32 - __clz(a.range - 1);  // (range >= 32)
     for (uint32_t i = begin; i < end; i += 32) {
-        const int row = i + lane < end ? a.list[base + i + lane].y : -1;
-        const uint32_t peers = __match_any_sync(kFull, row);
-        if (row >= 0 && (peers & before) == 0) mine[row] += __popc(peers);
+        const bool there = i + lane < end;
+        const int row = there ? a.list[base + i + lane].y : 0;
+        uint32_t peers = __ballot_sync(kFull, there);
+        for (int k = 0; k < bits; ++k) {
+            const uint32_t ones = __ballot_sync(kFull, row >> k & 1);
+            peers &= row >> k & 1 ? ones : ~ones;
+        }
+        if (there) {
+            const int rank = __popc(peers & before);
+            if (rank == 0) mine[row] += __popc(peers);
+            // the row, the rank, and for the first of them how many they are
+            a.list[base + i + lane].y = row | rank << 16 | (rank == 0 ? __popc(peers) << 21 : 0);
+        }
         __syncwarp();
     }
     __syncthreads();
@@ -201,47 +237,20 @@ __global__ void __launch_bounds__(kSortThreads) dopt_embed_sort_kernel(const __g
         if (total > 0)
             for (int w = 0; w < kSortWarps; ++w) count[w * a.range + threadIdx.x] += start;
     }
-    if (blockIdx.x == gridDim.x - 1 && threadIdx.x == 0) a.first[a.vocab] = int(base + total);
+    if (int(blockIdx.x) == a.ranges - 1 && threadIdx.x == 0) a.first[a.vocab] = int(base + total);
     __syncthreads();
     for (uint32_t i = begin; i < end; i += 32) {
-        const int2 e = i + lane < end ? a.list[base + i + lane] : make_int2(0, -1);
-        const uint32_t peers = __match_any_sync(kFull, e.y);
-        const uint32_t at = e.y >= 0 ? mine[e.y] + __popc(peers & before) : 0;
+        const bool there = i + lane < end;
+        const int2 e = there ? a.list[base + i + lane] : make_int2(0, 0);
+        const int row = e.y & 0xffff;
+        const uint32_t at = there ? mine[row] + (e.y >> 16 & 31) : 0;
         __syncwarp();
-        if (e.y >= 0) {
+        if (there) {
             a.token[at] = e.x;
-            a.row[at] = int(lo) + e.y;
-            if ((peers & before) == 0) mine[e.y] += __popc(peers);
+            a.row[at] = int(lo) + row;
+            if (const uint32_t of_chunk = uint32_t(e.y) >> 21) mine[row] += of_chunk;  // by the first of a row
         }
         __syncwarp();
-    }
-}
-
-// The sum of a warp's columns over n <= 32 sorted places from p on, in order.
-template <typename T>
-__device__ __forceinline__ void sum_tokens(const EmbedGradArgs &a, int p, int n, int c, int lane, float (&f)[kCols]) {
-    using V = Values<T, kCols>;
-    const int token = lane < n ? a.token[p + lane] : 0;
-#pragma unroll
-    for (int q = 0; q < kCols; ++q) f[q] = 0.0f;
-    constexpr int kAhead = sizeof(T) == 4 ? 4 : 8;
-    for (int i = 0; i < n; i += kAhead) {
-        typename V::Ahead ahead[kAhead];
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-            const int64_t t = __shfl_sync(kFull, token, i + j < n ? i + j : 0);
-            V::fetch(ahead[j], static_cast<const T *>(a.d_out) + t * a.ld, c, i + j < n ? a.cols : 0, a.vec, lane, 32);
-        }
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-            if (i + j >= n) break;
-            V v;
-            v.take(ahead[j], a.vec, lane, 32);
-            float g[kCols];
-            v.get(g);
-#pragma unroll
-            for (int q = 0; q < kCols; ++q) f[q] += g[q];
-        }
     }
 }
 
@@ -263,98 +272,104 @@ __device__ __forceinline__ void put_row(const EmbedGradArgs &a, int64_t row, int
     v.store(p, c, a.cols, a.vec_grad, lane, 32);
 }
 
-// The first chunks * pieces blocks take 256 sorted tokens and 256 columns
-// each, and of those the rows with more than 32 tokens.  A row whose tokens
-// reach past the chunk leaves a partial sum there; the block that brings the
-// last one adds them in order.  The other blocks' warps take all rows with up
-// to 32 tokens: the sums of one never wait for another.
+// A block takes 256 sorted tokens and 256 columns, a warp 32 of the tokens,
+// whose rows of d_out are loaded ahead whatever rows of the table they go to.
+// A row whose tokens are all a warp's own is written by it.  Parts of a row
+// that reaches over warps meet in shared memory and are added in order by the
+// warp in which it begins; parts that reach over the chunk's ends are kept as
+// partial sums, and the block that brings a row's last one adds them in
+// order.
 template <typename T, typename G>
 __global__ void __launch_bounds__(kEmbedThreads) dopt_embed_grad_kernel(const __grid_constant__ EmbedGradArgs a) {
     let_dependents_start();
     wait_for_grids_before();
+    __shared__ float parts[kWarps][2][kWarpCols];  // of a warp's first row, if it began before; of its last, if it goes on
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    float f[kCols];
-    const int64_t long_blocks = int64_t(a.chunks) * a.pieces;
-    if (blockIdx.x >= long_blocks) {
-        const int64_t tasks = a.vocab * a.pieces, step = (gridDim.x - long_blocks) * kWarps;
-        for (int64_t i = (blockIdx.x - long_blocks) * kWarps + warp; i < tasks; i += step) {
-            const int64_t row = i / a.pieces;
-            const int c = int(i % a.pieces) * kWarpCols + lane * kCols;
-            const int p = a.first[row], n = a.first[row + 1] - p;
-            if (n > kShort || (n == 0 && a.accumulate)) continue;
-            sum_tokens<T>(a, p, n, c, lane, f);
-            put_row<G>(a, row, c, lane, f);
-        }
-        return;
-    }
-    __shared__ int32_t starts[kChunk + 1];  // the places in the chunk where long rows' tokens begin, then their ends
-    __shared__ int32_t ends[kChunk];
-    __shared__ uint32_t heads[kWarps];
-    __shared__ float sums[kWarps][kWarpCols];
     const int chunk = int(blockIdx.x / a.pieces), piece = int(blockIdx.x % a.pieces);
     const int c = piece * kWarpCols + lane * kCols;
     const int total = a.first[a.vocab];
-    const int base = chunk * kChunk, here = min(kChunk, total - base);
-    if (here <= 0) return;
-    {
-        const int i = threadIdx.x;
-        const int row = i < here ? a.row[base + i] : -1;
-        const int p = row >= 0 ? a.first[row] : 0, n = row >= 0 ? a.first[row + 1] - p : 0;
-        const bool head = n > kShort && (i == 0 || p == base + i);
-        const uint32_t all = __ballot_sync(kFull, head);
-        if (lane == 0) heads[warp] = all;
-        __syncthreads();
-        int k = __popc(all & ((1u << lane) - 1));
-        for (int w = 0; w < warp; ++w) k += __popc(heads[w]);
-        if (head) {
-            starts[k] = i;
-            ends[k] = min(here, p + n - base);
+    const int base = chunk * kChunk, p0 = base + warp * kShort, n = min(kShort, total - p0);
+    if (base >= total) return;
+    // lane i: the i-th of the warp's tokens
+    const int token = lane < n ? a.token[p0 + lane] : 0;
+    const int row = lane < n ? a.row[p0 + lane] : -1;
+    const int row_before = n > 0 && p0 > 0 ? a.row[p0 - 1] : -1, row_after = n == kShort && p0 + kShort < total ? a.row[p0 + kShort] : -1;
+    const int next = __shfl_down_sync(kFull, row, 1);
+    const uint32_t ends = __ballot_sync(kFull, lane < n && (lane == n - 1 || next != row));  // a row's last token here
+    const bool from_before = n > 0 && __shfl_sync(kFull, row, 0) == row_before;
+    const bool goes_on = n > 0 && row_after >= 0 && __shfl_sync(kFull, row, n > 0 ? n - 1 : 0) == row_after;
+    float f[kCols] = {};
+    using V = Values<T, kCols>;
+    constexpr int kAhead = sizeof(T) == 4 ? 4 : 8;
+    for (int i = 0; i < n; i += kAhead) {
+        typename V::Ahead ahead[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int64_t t = __shfl_sync(kFull, token, min(i + j, n - 1));
+            V::fetch(ahead[j], static_cast<const T *>(a.d_out) + t * a.ld, c, i + j < n ? a.cols : 0, a.vec, lane, 32);
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            if (i + j >= n) break;
+            V v;
+            v.take(ahead[j], a.vec, lane, 32);
+            float g[kCols];
+            v.get(g);
+#pragma unroll
+            for (int q = 0; q < kCols; ++q) f[q] += g[q];
+            if (!(ends >> (i + j) & 1)) continue;
+            const bool first = (ends & ((1u << (i + j)) - 1)) == 0;
+            if (first && from_before) {
+#pragma unroll
+                for (int q = 0; q < kCols; ++q) parts[warp][0][lane * kCols + q] = f[q];
+            } else if (i + j == n - 1 && goes_on) {
+#pragma unroll
+                for (int q = 0; q < kCols; ++q) parts[warp][1][lane * kCols + q] = f[q];
+            } else {
+                put_row<G>(a, __shfl_sync(kFull, row, i + j), c, lane, f);
+            }
+#pragma unroll
+            for (int q = 0; q < kCols; ++q) f[q] = 0.0f;
         }
     }
     __syncthreads();
-    int runs = 0;
-    for (int w = 0; w < kWarps; ++w) runs += __popc(heads[w]);
-    for (int k = 0; k < runs; ++k) {
-        const int from = max(starts[k], warp * kShort), n = max(0, min(ends[k], (warp + 1) * kShort) - from);
-        sum_tokens<T>(a, base + from, n, c, lane, f);
+    // The rows that reach over warps: each by the warp in which it begins, or by
+    // the first warp if that is in an earlier chunk.
+    for (int which = 0; which < 2; ++which) {
+        const bool through = from_before && __popc(ends) == 1;  // the warp's tokens are all of one row, of earlier warps
+        if (which == 0 ? !(warp == 0 && from_before) : !(goes_on && !through)) continue;
+        const int of = __shfl_sync(kFull, row, which == 0 ? 0 : n - 1);
+        const int lo = a.first[of], hi = a.first[of + 1];
+        const int last_warp = min(kWarps - 1, (hi - 1 - base) / kShort);
 #pragma unroll
-        for (int q = 0; q < kCols; ++q) sums[warp][lane * kCols + q] = f[q];
-        __syncthreads();
-        if (warp == 0) {
-            for (int w = 1; w < kWarps; ++w)
+        for (int q = 0; q < kCols; ++q) f[q] = parts[warp][which][lane * kCols + q];
+        for (int w = warp + 1; w <= last_warp; ++w)
 #pragma unroll
-                for (int q = 0; q < kCols; ++q) f[q] += sums[w][lane * kCols + q];
-            const int row = a.row[base + starts[k]];
-            const int p = a.first[row], e = a.first[row + 1];
-            const int first_chunk = p / kChunk, last_chunk = (e - 1) / kChunk;
-            bool done = first_chunk == last_chunk;
-            if (!done) {
-                // a chunk's slot 0: the row that began before it; slot 1: the one that goes on after it
-                auto slot = [&](int at) { return a.partial + (2 * int64_t(at) + (at == first_chunk)) * a.part_ld + c; };
-                float *mine = slot(chunk);
+            for (int q = 0; q < kCols; ++q) f[q] += parts[w][0][lane * kCols + q];
+        const int first_chunk = lo / kChunk, last_chunk = (hi - 1) / kChunk;
+        if (first_chunk != last_chunk) {
+            // a chunk's slot 0: the row that began before it; slot 1: the one that goes on after it
+            auto slot = [&](int at) { return a.partial + (2 * int64_t(at) + (at == first_chunk)) * a.part_ld + c; };
+            float4 *own = reinterpret_cast<float4 *>(slot(chunk));
+            own[0] = make_float4(f[0], f[1], f[2], f[3]);
+            own[1] = make_float4(f[4], f[5], f[6], f[7]);
+            __threadfence();
+            __syncwarp();
+            int before = 0;
+            if (lane == 0) before = atomicAdd(a.arrived + int64_t(first_chunk) * a.pieces + piece, 1);
+            if (__shfl_sync(kFull, before, 0) != last_chunk - first_chunk) continue;
+            __threadfence();
 #pragma unroll
-                for (int q = 0; q < kCols; ++q) mine[q] = f[q];
-                __threadfence();
-                __syncwarp();
-                int before = 0;
-                if (lane == 0) before = atomicAdd(a.arrived + int64_t(first_chunk) * a.pieces + piece, 1);
-                done = __shfl_sync(kFull, before, 0) == last_chunk - first_chunk;
-                if (done) {
-                    __threadfence();
-#pragma unroll
-                    for (int q = 0; q < kCols; ++q) f[q] = 0.0f;
+            for (int q = 0; q < kCols; ++q) f[q] = 0.0f;
 #pragma unroll 4
-                    for (int at = first_chunk; at <= last_chunk; ++at) {
-                        const float4 *s = reinterpret_cast<const float4 *>(slot(at));
-                        const float4 u = __ldcg(s), v = __ldcg(s + 1);
-                        f[0] += u.x, f[1] += u.y, f[2] += u.z, f[3] += u.w;
-                        f[4] += v.x, f[5] += v.y, f[6] += v.z, f[7] += v.w;
-                    }
-                }
+            for (int at = first_chunk; at <= last_chunk; ++at) {
+                const float4 *s = reinterpret_cast<const float4 *>(slot(at));
+                const float4 u = __ldcg(s), v = __ldcg(s + 1);
+                f[0] += u.x, f[1] += u.y, f[2] += u.z, f[3] += u.w;
+                f[4] += v.x, f[5] += v.y, f[6] += v.z, f[7] += v.w;
             }
-            if (done) put_row<G>(a, row, c, lane, f);
         }
-        __syncthreads();
+        put_row<G>(a, of, c, lane, f);
     }
 }
 
@@ -424,10 +439,8 @@ int launch_embed(const char *who, const EmbedArgs &a, cudaStream_t stream) {
 
 template <typename T, typename G>
 int launch_grad(const char *who, const EmbedGradArgs &a, cudaStream_t stream) {
-    const int64_t long_blocks = int64_t(a.chunks) * a.pieces;
-    const int64_t blocks = std::min<int64_t>((a.vocab * a.pieces + 2 * kWarps - 1) / (2 * kWarps), 1 << 20);
-    return launch_op(who, dopt_embed_grad_kernel<T, G>, dim3(unsigned(long_blocks + blocks)), dim3(kEmbedThreads), 0,
-                     stream, a);
+    return launch_op(who, dopt_embed_grad_kernel<T, G>, dim3(unsigned(a.chunks) * unsigned(a.pieces)), dim3(kEmbedThreads),
+                     0, stream, a);
 }
 template <typename T>
 int launch_grad(const char *who, dopt_dtype grad, const EmbedGradArgs &a, cudaStream_t stream) {
@@ -542,14 +555,17 @@ extern "C" int dopt_embed_grad(const void *ids, int32_t id_bytes, int64_t tokens
     a.scale = scale;
     a.range = int32_t(std::min<int64_t>(kMostRange, std::max<int64_t>(32, (vocab + 151) / 152)));
     const size_t smem = size_t(kSortWarps) * a.range * sizeof(uint32_t);
-    const dim3 grid(unsigned((vocab + a.range - 1) / a.range));
-    if (int64_t(a.chunks) * a.pieces > INT32_MAX - (1 << 20))
+    a.ranges = int32_t((vocab + a.range - 1) / a.range);
+    a.grad_bytes = int32_t(gb);
+    if (int64_t(a.chunks) * a.pieces > INT32_MAX)
         return fail(DOPT_E_ARG, "%s: %lld tokens of %lld columns are too many for one call", who,
                     static_cast<long long>(tokens), static_cast<long long>(cols));
     if ((rc = set_up_sort(who)) != DOPT_OK) return rc;
     auto sort = id_bytes == 8 ? dopt_embed_sort_kernel<int64_t> : dopt_embed_sort_kernel<int32_t>;
-    rc = launch_op(who, sort, grid, dim3(kSortThreads), smem, stream, a);
-    if (rc != DOPT_OK) return rc;
+    // (64 KB of zeros a block, up to two blocks an SM)
+    const int64_t zero_blocks = a.accumulate ? 0 : std::min<int64_t>(304, (vocab * cols * int64_t(gb) + 65535) / 65536);
+    rc = launch_op(who, sort, dim3(unsigned(a.ranges + zero_blocks)), dim3(kSortThreads), smem, stream, a);
+    if (rc != DOPT_OK || tokens == 0) return rc;
     switch (dtype) {
         case DOPT_BF16: return launch_grad<__nv_bfloat16>(who, grad_dtype, a, stream);
         case DOPT_FP16: return launch_grad<__half>(who, grad_dtype, a, stream);

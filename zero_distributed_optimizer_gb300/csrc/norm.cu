@@ -316,6 +316,321 @@ __global__ void __launch_bounds__(kMostRow) dopt_norm_grad_kernel(const __grid_c
         }
 }
 
+// ---------------------------------------------------------------------------
+// Rows and params that are 16-byte aligned, of a multiple of 8 columns
+// ---------------------------------------------------------------------------
+
+// 8 values of a thread.
+template <typename T>
+struct Eight {
+    static constexpr int kPieces = kCols * int(sizeof(T)) / 16;
+    uint4 raw[kPieces];
+    __device__ __forceinline__ void load(const T *p, bool there) {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)
+            raw[i] = there ? __ldcs(reinterpret_cast<const uint4 *>(p) + i) : make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void get(float (&f)[kCols]) const {
+        constexpr int kPer = 16 / int(sizeof(T));
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            float g[kPer];
+            unpack<T, 16>(raw[i], g);
+#pragma unroll
+            for (int q = 0; q < kPer; ++q) f[i * kPer + q] = g[q];
+        }
+    }
+    static __device__ __forceinline__ void put(T *p, const float (&f)[kCols], bool there) {
+        constexpr int kPer = 16 / int(sizeof(T));
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            float g[kPer];
+#pragma unroll
+            for (int q = 0; q < kPer; ++q) g[q] = f[i * kPer + q];
+            if (there) __stcs(reinterpret_cast<uint4 *>(p) + i, pack<T, 16>(g));
+        }
+    }
+};
+// 8 values of a param, which stays in L1 (nothing is kept of it from row to row).
+template <typename T>
+__device__ __forceinline__ void param_values(const void *param, int c, bool there, float none, float (&f)[kCols]) {
+#pragma unroll
+    for (int q = 0; q < kCols; ++q) f[q] = none;
+    if (param && there) {
+        Eight<T> v;
+#pragma unroll
+        for (int i = 0; i < Eight<T>::kPieces; ++i)
+            v.raw[i] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(param) + c) + i);
+        v.get(f);
+    }
+}
+
+// The next row's loads are in flight under a row's sums: they go to the
+// registers that this row's values came in.
+template <typename T, int NV, bool LAYER>
+__global__ void __launch_bounds__(NV == 1 ? 256 : kMostRow, NV == 1 ? 4 : 1)
+    dopt_norm_whole_kernel(const __grid_constant__ NormArgs a) {
+    __shared__ RowSums sums[8];
+    let_dependents_start();
+    wait_for_grids_before();
+    RowSums &s = sums[threadIdx.y];
+    int turn = 0;
+    const float per_col = 1.0f / float(a.cols);
+    int col[NV];
+    bool in[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) col[i] = RowValues<T, NV>::column(i), in[i] = col[i] < a.cols;
+    const int64_t step = int64_t(gridDim.x) * blockDim.y;
+    int64_t r = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
+    Eight<T> x[NV], y[NV];
+    float row_gate = 1.0f;
+    auto fetch = [&](int64_t row) {
+        const bool there = row < a.rows;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            x[i].load(static_cast<const T *>(a.x) + row * a.ld_x + col[i], there && in[i]);
+            y[i].load(static_cast<const T *>(a.y) + row * a.ld_y + col[i], there && in[i] && a.y);
+        }
+        if (a.row_gate && there) row_gate = a.row_gate[row];
+    };
+    fetch(r);
+    for (; r < a.rows; r += step) {
+        float h[NV][kCols], u[NV][kCols];
+        const float by = a.scale * row_gate;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) x[i].get(h[i]), y[i].get(u[i]);
+        fetch(r + step);
+        if (a.y) {
+            if (a.post) {
+                float mean = 0.0f;
+                if constexpr (LAYER) {
+                    float sum[1] = {0.0f};
+#pragma unroll
+                    for (int i = 0; i < NV; ++i)
+#pragma unroll
+                        for (int q = 0; q < kCols; ++q) sum[0] += u[i][q];
+                    row_sums(s, turn, sum);
+                    mean = sum[0] * per_col;
+                }
+                float square[1] = {0.0f};
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    if (!LAYER || in[i])
+#pragma unroll
+                        for (int q = 0; q < kCols; ++q) {
+                            if constexpr (LAYER) u[i][q] -= mean;
+                            square[0] = fmaf(u[i][q], u[i][q], square[0]);
+                        }
+                row_sums(s, turn, square);
+                const float factor = 1.0f / sqrtf(fmaf(square[0], per_col, a.eps));
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    float w[kCols];
+                    param_values<T>(a.post_weight, col[i], in[i], 1.0f, w);
+#pragma unroll
+                    for (int q = 0; q < kCols; ++q) u[i][q] *= factor * w[q];
+                    if (LAYER && a.post_bias) {
+                        param_values<T>(a.post_bias, col[i], in[i], 0.0f, w);
+#pragma unroll
+                        for (int q = 0; q < kCols; ++q) u[i][q] += w[q];
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                float g[kCols];
+                param_values<T>(a.gate, col[i], in[i], 1.0f, g);
+#pragma unroll
+                for (int q = 0; q < kCols; ++q) h[i][q] = fmaf(u[i][q], by * g[q], h[i][q]);
+                if (a.h) Eight<T>::put(static_cast<T *>(a.h) + r * a.ld_h + col[i], h[i], in[i]);
+            }
+        }
+        if (!a.n) continue;
+        float mean = 0.0f;
+        if constexpr (LAYER) {
+            float sum[1] = {0.0f};
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (in[i])
+#pragma unroll
+                    for (int q = 0; q < kCols; ++q) sum[0] += h[i][q];
+            row_sums(s, turn, sum);
+            mean = sum[0] * per_col;
+        }
+        float square[1] = {0.0f};
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (in[i])
+#pragma unroll
+                for (int q = 0; q < kCols; ++q) {
+                    if constexpr (LAYER) h[i][q] -= mean;
+                    square[0] = fmaf(h[i][q], h[i][q], square[0]);
+                }
+        row_sums(s, turn, square);
+        const float factor = 1.0f / sqrtf(fmaf(square[0], per_col, a.eps));
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float w[kCols];
+            param_values<T>(a.weight, col[i], in[i], 1.0f, w);
+#pragma unroll
+            for (int q = 0; q < kCols; ++q) h[i][q] *= factor * w[q];
+            if (LAYER && a.bias) {
+                param_values<T>(a.bias, col[i], in[i], 0.0f, w);
+#pragma unroll
+                for (int q = 0; q < kCols; ++q) h[i][q] += w[q];
+            }
+            Eight<T>::put(static_cast<T *>(a.n) + r * a.ld_n + col[i], h[i], in[i]);
+        }
+    }
+}
+
+// The gradients as dopt_norm_grad_kernel has them.  The sums of a row that do
+// not wait for one another go together: an RMS norm takes two rounds of them
+// (h's, y's and d_n's; then d_x's), a layer norm three.
+template <typename T, int NV, bool LAYER>
+__global__ void __launch_bounds__(NV == 1 ? 256 : kMostRow, NV == 1 ? (LAYER || sizeof(T) == 4 ? 2 : 3) : 1)
+    dopt_norm_grad_whole_kernel(const __grid_constant__ NormArgs a) {
+    constexpr int kSums = LAYER ? 4 : 2;
+    constexpr int kPost = LAYER ? 2 : 1;
+    __shared__ RowSums sums[8];
+    let_dependents_start();
+    wait_for_grids_before();
+    RowSums &s = sums[threadIdx.y];
+    int turn = 0;
+    const float per_col = 1.0f / float(a.cols);
+    int col[NV];
+    bool in[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) col[i] = RowValues<T, NV>::column(i), in[i] = col[i] < a.cols;
+    const int64_t step = int64_t(gridDim.x) * blockDim.y;
+    int64_t r = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
+    Eight<T> raw_h[NV], raw_y[NV], raw_dn[NV], raw_dh[NV];
+    float row_gate = 1.0f;
+    auto fetch = [&](int64_t row) {
+        const bool there = row < a.rows;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const bool here = there && in[i];
+            raw_h[i].load(static_cast<const T *>(a.x) + row * a.ld_x + col[i], here && a.d_n);
+            raw_dn[i].load(static_cast<const T *>(a.d_n) + row * a.ld_d_n + col[i], here && a.d_n);
+            raw_y[i].load(static_cast<const T *>(a.y) + row * a.ld_y + col[i], here && a.y);
+            raw_dh[i].load(static_cast<const T *>(a.d_h) + row * a.ld_d_h + col[i], here && a.d_h);
+        }
+        if (a.row_gate && there) row_gate = a.row_gate[row];
+    };
+    float acc[kSums][NV][kCols] = {};
+    fetch(r);
+    for (; r < a.rows; r += step) {
+        float h[NV][kCols], d[NV][kCols], u[NV][kCols], dx[NV][kCols];
+        const float by = a.scale * row_gate;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) raw_h[i].get(h[i]), raw_dn[i].get(d[i]), raw_y[i].get(u[i]), raw_dh[i].get(dx[i]);
+        fetch(r + step);
+        float h_mean = 0.0f, y_mean = 0.0f;
+        if constexpr (LAYER) {
+            float f[2] = {};
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int q = 0; q < kCols; ++q) f[0] += h[i][q], f[1] += u[i][q];
+            row_sums(s, turn, f);
+            h_mean = f[0] * per_col, y_mean = a.post ? f[1] * per_col : 0.0f;
+        }
+        float f[4] = {};  // of (h - mean)^2, (y - mean)^2, d_n w (h - mean), d_n w
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float w[kCols];
+            param_values<T>(a.weight, col[i], in[i], 1.0f, w);
+            if (in[i])
+#pragma unroll
+                for (int q = 0; q < kCols; ++q) {
+                    if constexpr (LAYER) h[i][q] -= h_mean, u[i][q] -= y_mean;
+                    const float g = d[i][q] * w[q];
+                    f[0] = fmaf(h[i][q], h[i][q], f[0]);
+                    f[1] = fmaf(u[i][q], u[i][q], f[1]);
+                    f[2] = fmaf(g, h[i][q], f[2]);
+                    if constexpr (LAYER) f[3] += g;
+                }
+        }
+        if constexpr (LAYER) {
+            row_sums(s, turn, f);
+        } else {
+            float three[3] = {f[0], f[1], f[2]};
+            row_sums(s, turn, three);
+            f[0] = three[0], f[1] = three[1], f[2] = three[2];
+        }
+        const float h_factor = a.d_n ? 1.0f / sqrtf(fmaf(f[0], per_col, a.eps)) : 0.0f;
+        const float y_factor = a.post ? 1.0f / sqrtf(fmaf(f[1], per_col, a.eps)) : 1.0f;
+        const float along = f[2] * h_factor * per_col, level = f[3] * per_col;
+        float dot[3] = {};
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float w[kCols];
+            param_values<T>(a.weight, col[i], in[i], 1.0f, w);
+#pragma unroll
+            for (int q = 0; q < kCols; ++q) {
+                h[i][q] *= h_factor;
+                acc[0][i][q] = fmaf(d[i][q], h[i][q], acc[0][i][q]);
+                if constexpr (LAYER) acc[1][i][q] += d[i][q];
+                float g = d[i][q] * w[q];
+                if constexpr (LAYER) g -= level;
+                dx[i][q] = fmaf(h_factor, fmaf(-h[i][q], along, g), dx[i][q]);
+            }
+            if (a.h) Eight<T>::put(static_cast<T *>(a.h) + r * a.ld_h + col[i], dx[i], in[i]);
+            if (!in[i])
+#pragma unroll
+                for (int q = 0; q < kCols; ++q) dx[i][q] = 0.0f;
+        }
+        if (!a.y) continue;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float w[kCols], g[kCols];
+            param_values<T>(a.post_weight, col[i], in[i], 1.0f, w);
+            param_values<T>(a.gate, col[i], in[i], 1.0f, g);
+            if (a.d_row_gate) {
+                float b[kCols];
+                param_values<T>(a.post_bias, col[i], in[i], 0.0f, b);
+#pragma unroll
+                for (int q = 0; q < kCols; ++q) dot[2] = fmaf(dx[i][q] * g[q], fmaf(u[i][q] * y_factor, w[q], b[q]), dot[2]);
+            }
+#pragma unroll
+            for (int q = 0; q < kCols; ++q) {
+                u[i][q] *= y_factor;
+                const float v = by * dx[i][q];
+                acc[kPost][i][q] = fmaf(v, u[i][q], acc[kPost][i][q]);
+                if constexpr (LAYER) acc[kPost + 1][i][q] += v;
+                dx[i][q] = v * (g[q] * w[q]);  // of hat(y)
+                dot[0] = fmaf(dx[i][q], u[i][q], dot[0]);
+                if constexpr (LAYER) dot[1] += dx[i][q];
+            }
+        }
+        if (a.post || a.d_row_gate) row_sums(s, turn, dot);
+        if (a.d_row_gate && threadIdx.x == 0) a.d_row_gate[r] = a.scale * dot[2];
+        if (!a.n) continue;
+        const float y_along = a.post ? dot[0] * per_col : 0.0f, y_level = LAYER && a.post ? dot[1] * per_col : 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+#pragma unroll
+            for (int q = 0; q < kCols; ++q) {
+                float v = dx[i][q];
+                if constexpr (LAYER) v -= y_level;
+                dx[i][q] = y_factor * fmaf(-u[i][q], y_along, v);
+            }
+            Eight<T>::put(static_cast<T *>(a.n) + r * a.ld_n + col[i], dx[i], in[i]);
+        }
+    }
+    const int64_t group = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
+#pragma unroll
+    for (int k = 0; k < kSums; ++k)
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (!in[i]) continue;
+            float4 *p = reinterpret_cast<float4 *>(a.partial + (group * kSums + k) * a.part_ld + col[i]);
+            p[0] = make_float4(acc[k][i][0], acc[k][i][1], acc[k][i][2], acc[k][i][3]);
+            p[1] = make_float4(acc[k][i][4], acc[k][i][5], acc[k][i][6], acc[k][i][7]);
+        }
+}
+
 struct ParamGradArgs {
     const float *partial;
     const void *post_weight, *post_bias, *gate;
@@ -381,21 +696,22 @@ struct NormShape {
 
 int64_t norm_part_ld(int64_t cols) { return (cols + kCols - 1) / kCols * kCols; }
 
+template <typename T, int NV, bool LAYER>
+int launch_norm(const char *who, const NormArgs &a, bool backward, int64_t blocks, dim3 block, cudaStream_t stream) {
+    const dim3 grid{unsigned(blocks)};
+    if (a.vec && a.vec_params && a.cols % kCols == 0)
+        return backward ? launch_op(who, dopt_norm_grad_whole_kernel<T, NV, LAYER>, grid, block, 0, stream, a)
+                        : launch_op(who, dopt_norm_whole_kernel<T, NV, LAYER>, grid, block, 0, stream, a);
+    return backward ? launch_op(who, dopt_norm_grad_kernel<T, NV, LAYER>, grid, block, 0, stream, a)
+                    : launch_op(who, dopt_norm_kernel<T, NV, LAYER>, grid, block, 0, stream, a);
+}
 template <typename T, bool LAYER>
 int launch_norm(const char *who, const NormArgs &a, bool backward, int64_t blocks, const NormShape &shape,
                 cudaStream_t stream) {
-    const dim3 grid{unsigned(blocks)};
-    if (backward) {
-        switch (shape.nv) {
-            case 1: return launch_op(who, dopt_norm_grad_kernel<T, 1, LAYER>, grid, shape.block, 0, stream, a);
-            case 2: return launch_op(who, dopt_norm_grad_kernel<T, 2, LAYER>, grid, shape.block, 0, stream, a);
-            default: return launch_op(who, dopt_norm_grad_kernel<T, 4, LAYER>, grid, shape.block, 0, stream, a);
-        }
-    }
     switch (shape.nv) {
-        case 1: return launch_op(who, dopt_norm_kernel<T, 1, LAYER>, grid, shape.block, 0, stream, a);
-        case 2: return launch_op(who, dopt_norm_kernel<T, 2, LAYER>, grid, shape.block, 0, stream, a);
-        default: return launch_op(who, dopt_norm_kernel<T, 4, LAYER>, grid, shape.block, 0, stream, a);
+        case 1: return launch_norm<T, 1, LAYER>(who, a, backward, blocks, shape.block, stream);
+        case 2: return launch_norm<T, 2, LAYER>(who, a, backward, blocks, shape.block, stream);
+        default: return launch_norm<T, 4, LAYER>(who, a, backward, blocks, shape.block, stream);
     }
 }
 int launch_norm(const char *who, dopt_dtype dtype, bool layer, const NormArgs &a, bool backward, int64_t blocks,
@@ -510,7 +826,7 @@ extern "C" int dopt_norm(const dopt_norm_cfg *cfg, const dopt_norm_params *param
     a.n = n, a.ld_n = ld_n;
     a.vec = bits % 16 == 0;
     const NormShape shape(cols);
-    const int64_t blocks = std::min<int64_t>((rows + shape.block.y - 1) / shape.block.y, 152 * 6);
+    const int64_t blocks = std::min<int64_t>((rows + shape.block.y - 1) / shape.block.y, 152 * 4);
     return launch_norm(who, dtype, cfg->kind == DOPT_NORM_LAYER, a, false, blocks, shape, stream);
 }
 
@@ -600,7 +916,7 @@ extern "C" int dopt_norm_grad(const dopt_norm_cfg *cfg, const dopt_norm_params *
         a.vec = bits % 16 == 0;
         const NormShape shape(cols);
         const int64_t blocks = std::min<int64_t>((rows + shape.block.y - 1) / shape.block.y,
-                                                 std::min<int64_t>(152 * 4, kParts / shape.block.y));
+                                                 std::min<int64_t>(152 * 3, kParts / shape.block.y));
         groups = blocks * shape.block.y;
         if ((rc = launch_norm(who, dtype, layer, a, true, blocks, shape, stream)) != DOPT_OK) return rc;
     }
