@@ -13,9 +13,8 @@ constexpr int kWarpCols = 32 * kCols;    // columns a warp
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMostRange = 1024;         // rows of the table that one sorting block owns
-constexpr int kChunk = 256;              // sorted tokens of a summing block
-constexpr int kShort = 32;               // of which a warp takes
-static_assert(kChunk == kWarps * kShort, "a block's warps take a chunk");
+constexpr int kMostShare = 32;           // sorted tokens that a warp sums
+constexpr int kRingBytes = 4096;         // of a warp's loads ahead
 
 struct EmbedArgs {
     const void *table;
@@ -78,6 +77,45 @@ __global__ void __launch_bounds__(kEmbedThreads) dopt_embed_kernel(const __grid_
     }
 }
 
+// The same where rows are 16-byte aligned, of a multiple of 8 columns.
+template <typename T, typename I>
+__global__ void __launch_bounds__(kEmbedThreads) dopt_embed_whole_kernel(const __grid_constant__ EmbedArgs a) {
+    let_dependents_start();
+    wait_for_grids_before();
+    constexpr int kTokens = 4, kPieces = kCols * int(sizeof(T)) / 16, kPer = 16 / int(sizeof(T));
+    const int64_t t0 = (int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * kTokens;
+    const int c = int(blockIdx.y) * kWarpCols + int(threadIdx.x & 31) * kCols;
+    if (c >= a.cols) return;
+    int64_t id[kTokens];
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) id[i] = t0 + i < a.tokens ? id_at<I>(a.ids, t0 + i) : -1;
+    uint4 v[kTokens][kPieces];
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) {
+        const bool there = uint64_t(id[i]) < uint64_t(a.vocab);
+        const uint4 *row = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.table) + id[i] * a.ld_table + c);
+#pragma unroll
+        for (int k = 0; k < kPieces; ++k) v[i][k] = there ? __ldg(row + k) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) {
+        if (t0 + i >= a.tokens || (a.accumulate && uint64_t(id[i]) >= uint64_t(a.vocab))) continue;
+        uint4 *row = reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + (t0 + i) * a.ld_out + c);
+#pragma unroll
+        for (int k = 0; k < kPieces; ++k) {
+            if (a.scale != 1.0f || a.accumulate) {
+                float f[kPer], old[kPer] = {};
+                unpack<T, 16>(v[i][k], f);
+                if (a.accumulate) unpack<T, 16>(row[k], old);
+#pragma unroll
+                for (int q = 0; q < kPer; ++q) f[q] = f[q] * a.scale + old[q];
+                v[i][k] = pack<T, 16>(f);
+            }
+            __stcs(row + k, v[i][k]);
+        }
+    }
+}
+
 // ---------------------------------------------------------------------------
 // Gradient
 // ---------------------------------------------------------------------------
@@ -94,7 +132,8 @@ struct EmbedGradArgs {
     float *partial;         // [2 * chunks][part_ld] sums of runs that reach over a chunk's ends
     int64_t ld, tokens, vocab, part_ld;
     int32_t cols, pieces;   // pieces: of 256 columns
-    int32_t range, ranges, chunks;
+    int32_t range, ranges;
+    int32_t share, chunks;  // sorted tokens of a summing warp; blocks of 8 of those
     int32_t vec, vec_grad;  // d_out's, the grads' rows are 16-byte aligned
     int32_t accumulate;
     int32_t grad_bytes;     // of an element
@@ -199,9 +238,11 @@ __global__ void __launch_bounds__(kSortThreads) dopt_embed_sort_kernel(const __g
     const uint32_t share = ((total + kSortWarps - 1) / kSortWarps + 31) / 32 * 32;
     const uint32_t begin = min(total, warp * share), end = min(total, begin + share);
     const int bits = 32 - __clz(a.range - 1);  // (range >= 32)
+    int2 next = begin + lane < end ? a.list[base + begin + lane] : make_int2(0, 0);
     for (uint32_t i = begin; i < end; i += 32) {
         const bool there = i + lane < end;
-        const int row = there ? a.list[base + i + lane].y : 0;
+        const int row = next.y;
+        if (i + 32 < end) next = i + 32 + lane < end ? a.list[base + i + 32 + lane] : make_int2(0, 0);
         uint32_t peers = __ballot_sync(kFull, there);
         for (int k = 0; k < bits; ++k) {
             const uint32_t ones = __ballot_sync(kFull, row >> k & 1);
@@ -239,9 +280,11 @@ __global__ void __launch_bounds__(kSortThreads) dopt_embed_sort_kernel(const __g
     }
     if (int(blockIdx.x) == a.ranges - 1 && threadIdx.x == 0) a.first[a.vocab] = int(base + total);
     __syncthreads();
+    next = begin + lane < end ? a.list[base + begin + lane] : make_int2(0, 0);
     for (uint32_t i = begin; i < end; i += 32) {
         const bool there = i + lane < end;
-        const int2 e = there ? a.list[base + i + lane] : make_int2(0, 0);
+        const int2 e = next;
+        if (i + 32 < end) next = i + 32 + lane < end ? a.list[base + i + 32 + lane] : make_int2(0, 0);
         const int row = e.y & 0xffff;
         const uint32_t at = there ? mine[row] + (e.y >> 16 & 31) : 0;
         __syncwarp();
@@ -255,81 +298,133 @@ __global__ void __launch_bounds__(kSortThreads) dopt_embed_sort_kernel(const __g
 }
 
 // scale * f to a row of the grads.
-template <typename G>
+template <typename G, bool WHOLE>
 __device__ __forceinline__ void put_row(const EmbedGradArgs &a, int64_t row, int c, int lane, float (&f)[kCols]) {
-    using V = Values<G, kCols>;
     G *p = static_cast<G *>(a.grad) + row * a.cols;
-    float old[kCols] = {};
-    if (a.accumulate) {
-        V o;
-        o.load(p, c, a.cols, a.vec_grad, lane, 32);
-        o.get(old);
-    }
+    if constexpr (WHOLE) {
+        constexpr int kPer = 16 / int(sizeof(G));
+        if (c < a.cols)
 #pragma unroll
-    for (int q = 0; q < kCols; ++q) f[q] = f[q] * a.scale + old[q];
-    V v;
-    v.set(f);
-    v.store(p, c, a.cols, a.vec_grad, lane, 32);
+            for (int k = 0; k < kCols / kPer; ++k) {
+                uint4 *at = reinterpret_cast<uint4 *>(p + c) + k;
+                float v[kPer], old[kPer] = {};
+                if (a.accumulate) unpack<G, 16>(*at, old);
+#pragma unroll
+                for (int q = 0; q < kPer; ++q) v[q] = f[k * kPer + q] * a.scale + old[q];
+                *at = pack<G, 16>(v);
+            }
+    } else {
+        using V = Values<G, kCols>;
+        float old[kCols] = {};
+        if (a.accumulate) {
+            V o;
+            o.load(p, c, a.cols, a.vec_grad, lane, 32);
+            o.get(old);
+        }
+#pragma unroll
+        for (int q = 0; q < kCols; ++q) f[q] = f[q] * a.scale + old[q];
+        V v;
+        v.set(f);
+        v.store(p, c, a.cols, a.vec_grad, lane, 32);
+    }
 }
 
-// A block takes 256 sorted tokens and 256 columns, a warp 32 of the tokens,
+// A block takes a chunk of sorted tokens and 256 columns, a warp an eighth of them,
 // whose rows of d_out are loaded ahead whatever rows of the table they go to.
 // A row whose tokens are all a warp's own is written by it.  Parts of a row
 // that reaches over warps meet in shared memory and are added in order by the
 // warp in which it begins; parts that reach over the chunk's ends are kept as
 // partial sums, and the block that brings a row's last one adds them in
 // order.
-template <typename T, typename G>
+template <typename T, typename G, bool WHOLE>
 __global__ void __launch_bounds__(kEmbedThreads) dopt_embed_grad_kernel(const __grid_constant__ EmbedGradArgs a) {
     let_dependents_start();
     wait_for_grids_before();
     __shared__ float parts[kWarps][2][kWarpCols];  // of a warp's first row, if it began before; of its last, if it goes on
+    __shared__ __align__(16) unsigned char rings[WHOLE ? kWarps : 1][WHOLE ? kRingBytes : 16];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int chunk = int(blockIdx.x / a.pieces), piece = int(blockIdx.x % a.pieces);
     const int c = piece * kWarpCols + lane * kCols;
-    const int total = a.first[a.vocab];
-    const int base = chunk * kChunk, p0 = base + warp * kShort, n = min(kShort, total - p0);
+    const int total = a.first[a.vocab], per_chunk = kWarps * a.share;
+    const int base = chunk * per_chunk, p0 = base + warp * a.share, n = min(a.share, total - p0);
     if (base >= total) return;
     // lane i: the i-th of the warp's tokens
     const int token = lane < n ? a.token[p0 + lane] : 0;
     const int row = lane < n ? a.row[p0 + lane] : -1;
-    const int row_before = n > 0 && p0 > 0 ? a.row[p0 - 1] : -1, row_after = n == kShort && p0 + kShort < total ? a.row[p0 + kShort] : -1;
+    const int row_before = n > 0 && p0 > 0 ? a.row[p0 - 1] : -1;
+    const int row_after = n == a.share && p0 + n < total ? a.row[p0 + n] : -1;
     const int next = __shfl_down_sync(kFull, row, 1);
     const uint32_t ends = __ballot_sync(kFull, lane < n && (lane == n - 1 || next != row));  // a row's last token here
     const bool from_before = n > 0 && __shfl_sync(kFull, row, 0) == row_before;
     const bool goes_on = n > 0 && row_after >= 0 && __shfl_sync(kFull, row, n > 0 ? n - 1 : 0) == row_after;
     float f[kCols] = {};
-    using V = Values<T, kCols>;
-    constexpr int kAhead = sizeof(T) == 4 ? 4 : 8;
-    for (int i = 0; i < n; i += kAhead) {
-        typename V::Ahead ahead[kAhead];
+    // token i's values are added; those of a row that ends there go where they belong
+    auto add = [&](int i, const float(&g)[kCols]) {
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-            const int64_t t = __shfl_sync(kFull, token, min(i + j, n - 1));
-            V::fetch(ahead[j], static_cast<const T *>(a.d_out) + t * a.ld, c, i + j < n ? a.cols : 0, a.vec, lane, 32);
+        for (int q = 0; q < kCols; ++q) f[q] += g[q];
+        if (!(ends >> i & 1)) return;
+        const bool head = (ends & ((1u << i) - 1)) == 0 && from_before, tail = i == n - 1 && goes_on;
+        if (head || tail) {
+#pragma unroll
+            for (int q = 0; q < kCols; ++q) parts[warp][head ? 0 : 1][lane * kCols + q] = f[q];
+        } else {
+            put_row<G, WHOLE>(a, __shfl_sync(kFull, row, i), c, lane, f);
         }
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-            if (i + j >= n) break;
-            V v;
-            v.take(ahead[j], a.vec, lane, 32);
-            float g[kCols];
-            v.get(g);
+        for (int q = 0; q < kCols; ++q) f[q] = 0.0f;
+    };
+    if constexpr (WHOLE) {
+        // rows of d_out on their way through shared memory, a thread's 8 columns its own
+        constexpr int kBytes = kCols * int(sizeof(T)), kAhead = kRingBytes / (32 * kBytes);
+        const uint32_t ring = uint32_t(__cvta_generic_to_shared(rings[warp] + lane * 16));
+        auto fetch = [&](int i) {
+            const int64_t t = __shfl_sync(kFull, token, i < n ? i : 0);
+            const char *from = reinterpret_cast<const char *>(static_cast<const T *>(a.d_out) + t * a.ld + c);
+            if (i < n && c < a.cols)
 #pragma unroll
-            for (int q = 0; q < kCols; ++q) f[q] += g[q];
-            if (!(ends >> (i + j) & 1)) continue;
-            const bool first = (ends & ((1u << (i + j)) - 1)) == 0;
-            if (first && from_before) {
+                for (int k = 0; k < kBytes / 16; ++k)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                     ring + uint32_t((i % kAhead) * 32 * kBytes + k * 512)),
+                                 "l"(from + 16 * k)
+                                 : "memory");
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        for (int i = 0; i < kAhead; ++i) fetch(i);
+        for (int i = 0; i < n; ++i) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+            float g[kCols] = {};
+            if (c < a.cols) {
+                constexpr int kPer = 16 / int(sizeof(T));
 #pragma unroll
-                for (int q = 0; q < kCols; ++q) parts[warp][0][lane * kCols + q] = f[q];
-            } else if (i + j == n - 1 && goes_on) {
+                for (int k = 0; k < kBytes / 16; ++k) {
+                    float part[kPer];
+                    unpack<T, 16>(*reinterpret_cast<const uint4 *>(rings[warp] + lane * 16 + (i % kAhead) * 32 * kBytes + k * 512), part);
 #pragma unroll
-                for (int q = 0; q < kCols; ++q) parts[warp][1][lane * kCols + q] = f[q];
-            } else {
-                put_row<G>(a, __shfl_sync(kFull, row, i + j), c, lane, f);
+                    for (int q = 0; q < kPer; ++q) g[k * kPer + q] = part[q];
+                }
+            }
+            fetch(i + kAhead);
+            add(i, g);
+        }
+    } else {
+        using V = Values<T, kCols>;
+        constexpr int kAhead = 4;
+        for (int i = 0; i < n; i += kAhead) {
+            typename V::Ahead ahead[kAhead];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                const int64_t t = __shfl_sync(kFull, token, min(i + j, n - 1));
+                V::fetch(ahead[j], static_cast<const T *>(a.d_out) + t * a.ld, c, i + j < n ? a.cols : 0, a.vec, lane, 32);
             }
 #pragma unroll
-            for (int q = 0; q < kCols; ++q) f[q] = 0.0f;
+            for (int j = 0; j < kAhead; ++j) {
+                if (i + j >= n) break;
+                V v;
+                v.take(ahead[j], a.vec, lane, 32);
+                float g[kCols];
+                v.get(g);
+                add(i + j, g);
+            }
         }
     }
     __syncthreads();
@@ -340,13 +435,13 @@ __global__ void __launch_bounds__(kEmbedThreads) dopt_embed_grad_kernel(const __
         if (which == 0 ? !(warp == 0 && from_before) : !(goes_on && !through)) continue;
         const int of = __shfl_sync(kFull, row, which == 0 ? 0 : n - 1);
         const int lo = a.first[of], hi = a.first[of + 1];
-        const int last_warp = min(kWarps - 1, (hi - 1 - base) / kShort);
+        const int last_warp = min(kWarps - 1, (hi - 1 - base) / a.share);
 #pragma unroll
         for (int q = 0; q < kCols; ++q) f[q] = parts[warp][which][lane * kCols + q];
         for (int w = warp + 1; w <= last_warp; ++w)
 #pragma unroll
             for (int q = 0; q < kCols; ++q) f[q] += parts[w][0][lane * kCols + q];
-        const int first_chunk = lo / kChunk, last_chunk = (hi - 1) / kChunk;
+        const int first_chunk = lo / per_chunk, last_chunk = (hi - 1) / per_chunk;
         if (first_chunk != last_chunk) {
             // a chunk's slot 0: the row that began before it; slot 1: the one that goes on after it
             auto slot = [&](int at) { return a.partial + (2 * int64_t(at) + (at == first_chunk)) * a.part_ld + c; };
@@ -369,7 +464,7 @@ __global__ void __launch_bounds__(kEmbedThreads) dopt_embed_grad_kernel(const __
                 f[4] += v.x, f[5] += v.y, f[6] += v.z, f[7] += v.w;
             }
         }
-        put_row<G>(a, of, c, lane, f);
+        put_row<G, WHOLE>(a, of, c, lane, f);
     }
 }
 
@@ -379,13 +474,24 @@ __global__ void __launch_bounds__(kEmbedThreads) dopt_embed_grad_kernel(const __
 
 int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
-// Places of the gradient's tables in its workspace.
+// Sorted tokens that a warp sums: 32, and fewer where 24 warps an SM would not
+// have so many.
+int32_t share_of(int64_t tokens, int64_t pieces) {
+    int32_t share = 2;
+    while (share < kMostShare && tokens * pieces > int64_t(share) * 152 * 24) share *= 2;
+    return share;
+}
+
+// Places of the gradient's tables in its workspace, with at most `share`
+// sorted tokens a warp.
 struct EmbedSpace {
     int64_t first, token, row, list, arrived, partial, bytes, chunks, pieces, part_ld;
+    int32_t share;
     EmbedSpace(int64_t tokens, int64_t vocab, int64_t cols) {
-        chunks = (tokens + kChunk - 1) / kChunk;
         pieces = (cols + kWarpCols - 1) / kWarpCols;
         part_ld = pieces * kWarpCols;
+        share = share_of(tokens, pieces);
+        chunks = (tokens + kWarps * share - 1) / (kWarps * share);
         first = 0;
         token = first + round_up(4 * (vocab + 1), 16);
         row = token + round_up(4 * tokens, 16);
@@ -395,6 +501,14 @@ struct EmbedSpace {
         bytes = partial + 8 * chunks * part_ld;
     }
 };
+// Bytes for so many tokens and for any fewer: there the chunks may be shorter
+// and so, up to the number that the shortest come to, more.
+int64_t most_space(int64_t tokens, int64_t vocab, int64_t cols) {
+    const EmbedSpace s(tokens, vocab, cols);
+    const int64_t most = std::max(s.chunks, std::min((tokens + 2 * kWarps - 1) / (2 * kWarps),
+                                                     (152 * 24 + s.pieces * kWarps - 1) / (s.pieces * kWarps) + 1));
+    return s.arrived + round_up(4 * most * s.pieces, 16) + 8 * most * s.part_ld;
+}
 
 std::mutex g_embed_mutex;
 bool g_embed_ready[64] = {};  // devices whose sorting kernels are set up
@@ -433,14 +547,19 @@ int check_ids(const char *who, const void *ids, int32_t id_bytes, int64_t tokens
 template <typename T>
 int launch_embed(const char *who, const EmbedArgs &a, cudaStream_t stream) {
     const dim3 grid(unsigned((a.tokens + 4 * kWarps - 1) / (4 * kWarps)), unsigned((a.cols + kWarpCols - 1) / kWarpCols));
+    if (a.vec && a.cols % kCols == 0)
+        return a.wide ? launch_op(who, dopt_embed_whole_kernel<T, int64_t>, grid, dim3(kEmbedThreads), 0, stream, a)
+                      : launch_op(who, dopt_embed_whole_kernel<T, int32_t>, grid, dim3(kEmbedThreads), 0, stream, a);
     return a.wide ? launch_op(who, dopt_embed_kernel<T, int64_t>, grid, dim3(kEmbedThreads), 0, stream, a)
                   : launch_op(who, dopt_embed_kernel<T, int32_t>, grid, dim3(kEmbedThreads), 0, stream, a);
 }
 
 template <typename T, typename G>
 int launch_grad(const char *who, const EmbedGradArgs &a, cudaStream_t stream) {
-    return launch_op(who, dopt_embed_grad_kernel<T, G>, dim3(unsigned(a.chunks) * unsigned(a.pieces)), dim3(kEmbedThreads),
-                     0, stream, a);
+    const dim3 grid(unsigned(a.chunks) * unsigned(a.pieces));
+    return a.vec && a.vec_grad && a.cols % kCols == 0
+               ? launch_op(who, dopt_embed_grad_kernel<T, G, true>, grid, dim3(kEmbedThreads), 0, stream, a)
+               : launch_op(who, dopt_embed_grad_kernel<T, G, false>, grid, dim3(kEmbedThreads), 0, stream, a);
 }
 template <typename T>
 int launch_grad(const char *who, dopt_dtype grad, const EmbedGradArgs &a, cudaStream_t stream) {
@@ -499,7 +618,7 @@ extern "C" int dopt_embed_workspace(int64_t tokens, int64_t vocab, int64_t cols,
     if (tokens < 0 || tokens > INT32_MAX || vocab < 1 || vocab > INT32_MAX || cols < 1 || cols > DOPT_MAX_COLS)
         return dopt::fail(DOPT_E_ARG, "%s: tokens %lld, vocab %lld, cols %lld", who, static_cast<long long>(tokens),
                           static_cast<long long>(vocab), static_cast<long long>(cols));
-    *bytes = EmbedSpace(tokens, vocab, cols).bytes;
+    *bytes = most_space(tokens, vocab, cols);
     return DOPT_OK;
 }
 
@@ -549,6 +668,7 @@ extern "C" int dopt_embed_grad(const void *ids, int32_t id_bytes, int64_t tokens
     a.cols = int32_t(cols);
     a.pieces = int32_t(space.pieces);
     a.chunks = int32_t(space.chunks);
+    a.share = space.share;
     a.vec = (address_bits(d_out) | uint64_t(ld) * b) % 16 == 0;
     a.vec_grad = (address_bits(a.grad) | uint64_t(cols) * gb) % 16 == 0;
     a.accumulate = (flags & DOPT_EMBED_ACCUMULATE) != 0;

@@ -320,6 +320,50 @@ __global__ void __launch_bounds__(kMostRow) dopt_norm_grad_kernel(const __grid_c
 // Rows and params that are 16-byte aligned, of a multiple of 8 columns
 // ---------------------------------------------------------------------------
 
+// f becomes the sums over the row's threads, with few shuffles: in a warp, the
+// values are first shared out over the lanes (a lane keeps the half of its
+// values that its number says, and adds the other lane's), then added; the
+// warps' sums, up to 8 a value and lane, are read by one load and added
+// likewise.
+struct LaneSums {
+    float v[2][kMostSums][kMostRow / 32];
+};
+template <int K>
+__device__ __forceinline__ void row_sums(LaneSums &s, int &turn, float (&f)[K]) {
+    static_assert(K == 1 || K == 2 || K == 4, "values are shared out by halves");
+    const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    float mine = f[0];
+    if constexpr (K == 4) {
+        const bool up = lane & 16;
+        float a = up ? f[2] : f[0], b = up ? f[3] : f[1];
+        a += __shfl_xor_sync(kFull, up ? f[0] : f[2], 16);
+        b += __shfl_xor_sync(kFull, up ? f[1] : f[3], 16);
+        mine = (lane & 8 ? b : a) + __shfl_xor_sync(kFull, lane & 8 ? a : b, 8);
+    } else if constexpr (K == 2) {
+        mine = (lane & 16 ? f[1] : f[0]) + __shfl_xor_sync(kFull, lane & 16 ? f[0] : f[1], 16);
+    }
+    // value k is now in the lanes from k * (32 / K) on
+#pragma unroll
+    for (int d = 16 / K; d > 0; d >>= 1) mine += __shfl_xor_sync(kFull, mine, d);
+    if (warps > 1) {
+        float(&v)[kMostSums][kMostRow / 32] = s.v[turn];
+        turn ^= 1;
+        if (lane % (32 / K) == 0) v[lane / (32 / K)][threadIdx.x >> 5] = mine;
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + threadIdx.y), "r"(blockDim.x) : "memory");
+        // lanes 8 k + w: value k of warps w and w + 8
+        const int k = lane >> 3, w = lane & 7;
+        mine = k < K && w < warps ? v[k][w] : 0.0f;
+        if (warps > 8 && k < K && w + 8 < warps) mine += v[k][w + 8];
+#pragma unroll
+        for (int d = 4; d > 0; d >>= 1) mine += __shfl_xor_sync(kFull, mine, d);
+#pragma unroll
+        for (int i = 0; i < K; ++i) f[i] = __shfl_sync(kFull, mine, 8 * i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < K; ++i) f[i] = __shfl_sync(kFull, mine, i * (32 / K));
+    }
+}
+
 // 8 values of a thread.
 template <typename T>
 struct Eight {
@@ -368,12 +412,12 @@ __device__ __forceinline__ void param_values(const void *param, int c, bool ther
 // The next row's loads are in flight under a row's sums: they go to the
 // registers that this row's values came in.
 template <typename T, int NV, bool LAYER>
-__global__ void __launch_bounds__(NV == 1 ? 256 : kMostRow, NV == 1 ? 4 : 1)
+__global__ void __launch_bounds__(NV == 4 ? kMostRow : 256, NV == 1 ? 4 : NV == 2 ? 2 : 1)
     dopt_norm_whole_kernel(const __grid_constant__ NormArgs a) {
-    __shared__ RowSums sums[8];
+    __shared__ LaneSums sums[8];
     let_dependents_start();
     wait_for_grids_before();
-    RowSums &s = sums[threadIdx.y];
+    LaneSums &s = sums[threadIdx.y];
     int turn = 0;
     const float per_col = 1.0f / float(a.cols);
     int col[NV];
@@ -384,13 +428,16 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : kMostRow, NV == 1 ? 4 : 1)
     int64_t r = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
     Eight<T> x[NV], y[NV];
     float row_gate = 1.0f;
+    const T *x_at = static_cast<const T *>(a.x) + r * a.ld_x, *y_at = static_cast<const T *>(a.y) + r * a.ld_y;
+    const bool with_y = a.y != nullptr;
     auto fetch = [&](int64_t row) {
         const bool there = row < a.rows;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            x[i].load(static_cast<const T *>(a.x) + row * a.ld_x + col[i], there && in[i]);
-            y[i].load(static_cast<const T *>(a.y) + row * a.ld_y + col[i], there && in[i] && a.y);
+            x[i].load(x_at + col[i], there && in[i]);
+            y[i].load(y_at + col[i], there && in[i] && with_y);
         }
+        x_at += step * a.ld_x, y_at += step * a.ld_y;
         if (a.row_gate && there) row_gate = a.row_gate[row];
     };
     fetch(r);
@@ -422,7 +469,7 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : kMostRow, NV == 1 ? 4 : 1)
                             square[0] = fmaf(u[i][q], u[i][q], square[0]);
                         }
                 row_sums(s, turn, square);
-                const float factor = 1.0f / sqrtf(fmaf(square[0], per_col, a.eps));
+                const float factor = rsqrtf(fmaf(square[0], per_col, a.eps));
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
                     float w[kCols];
@@ -467,7 +514,7 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : kMostRow, NV == 1 ? 4 : 1)
                     square[0] = fmaf(h[i][q], h[i][q], square[0]);
                 }
         row_sums(s, turn, square);
-        const float factor = 1.0f / sqrtf(fmaf(square[0], per_col, a.eps));
+        const float factor = rsqrtf(fmaf(square[0], per_col, a.eps));
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             float w[kCols];
@@ -488,14 +535,14 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : kMostRow, NV == 1 ? 4 : 1)
 // not wait for one another go together: an RMS norm takes two rounds of them
 // (h's, y's and d_n's; then d_x's), a layer norm three.
 template <typename T, int NV, bool LAYER>
-__global__ void __launch_bounds__(NV == 1 ? 256 : kMostRow, NV == 1 ? (LAYER || sizeof(T) == 4 ? 2 : 3) : 1)
+__global__ void __launch_bounds__(NV == 1 ? 256 : kMostRow, NV == 1 ? 2 : 1)
     dopt_norm_grad_whole_kernel(const __grid_constant__ NormArgs a) {
     constexpr int kSums = LAYER ? 4 : 2;
     constexpr int kPost = LAYER ? 2 : 1;
-    __shared__ RowSums sums[8];
+    __shared__ LaneSums sums[8];
     let_dependents_start();
     wait_for_grids_before();
-    RowSums &s = sums[threadIdx.y];
+    LaneSums &s = sums[threadIdx.y];
     int turn = 0;
     const float per_col = 1.0f / float(a.cols);
     int col[NV];
@@ -506,15 +553,16 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : kMostRow, NV == 1 ? (LAYER || 
     int64_t r = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
     Eight<T> raw_h[NV], raw_y[NV], raw_dn[NV], raw_dh[NV];
     float row_gate = 1.0f;
+    const bool with_n = a.d_n != nullptr, with_y = a.y != nullptr, with_h = a.d_h != nullptr;
     auto fetch = [&](int64_t row) {
         const bool there = row < a.rows;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const bool here = there && in[i];
-            raw_h[i].load(static_cast<const T *>(a.x) + row * a.ld_x + col[i], here && a.d_n);
-            raw_dn[i].load(static_cast<const T *>(a.d_n) + row * a.ld_d_n + col[i], here && a.d_n);
-            raw_y[i].load(static_cast<const T *>(a.y) + row * a.ld_y + col[i], here && a.y);
-            raw_dh[i].load(static_cast<const T *>(a.d_h) + row * a.ld_d_h + col[i], here && a.d_h);
+            raw_h[i].load(static_cast<const T *>(a.x) + row * a.ld_x + col[i], here && with_n);
+            raw_dn[i].load(static_cast<const T *>(a.d_n) + row * a.ld_d_n + col[i], here && with_n);
+            raw_y[i].load(static_cast<const T *>(a.y) + row * a.ld_y + col[i], here && with_y);
+            raw_dh[i].load(static_cast<const T *>(a.d_h) + row * a.ld_d_h + col[i], here && with_h);
         }
         if (a.row_gate && there) row_gate = a.row_gate[row];
     };
@@ -552,17 +600,11 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : kMostRow, NV == 1 ? (LAYER || 
                     if constexpr (LAYER) f[3] += g;
                 }
         }
-        if constexpr (LAYER) {
-            row_sums(s, turn, f);
-        } else {
-            float three[3] = {f[0], f[1], f[2]};
-            row_sums(s, turn, three);
-            f[0] = three[0], f[1] = three[1], f[2] = three[2];
-        }
-        const float h_factor = a.d_n ? 1.0f / sqrtf(fmaf(f[0], per_col, a.eps)) : 0.0f;
-        const float y_factor = a.post ? 1.0f / sqrtf(fmaf(f[1], per_col, a.eps)) : 1.0f;
+        row_sums(s, turn, f);
+        const float h_factor = a.d_n ? rsqrtf(fmaf(f[0], per_col, a.eps)) : 0.0f;
+        const float y_factor = a.post ? rsqrtf(fmaf(f[1], per_col, a.eps)) : 1.0f;
         const float along = f[2] * h_factor * per_col, level = f[3] * per_col;
-        float dot[3] = {};
+        float dot[4] = {};
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             float w[kCols];
@@ -604,7 +646,13 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : kMostRow, NV == 1 ? (LAYER || 
                 if constexpr (LAYER) dot[1] += dx[i][q];
             }
         }
-        if (a.post || a.d_row_gate) row_sums(s, turn, dot);
+        if (LAYER || a.d_row_gate) {
+            if (a.post || a.d_row_gate) row_sums(s, turn, dot);
+        } else if (a.post) {
+            float one[1] = {dot[0]};
+            row_sums(s, turn, one);
+            dot[0] = one[0];
+        }
         if (a.d_row_gate && threadIdx.x == 0) a.d_row_gate[r] = a.scale * dot[2];
         if (!a.n) continue;
         const float y_along = a.post ? dot[0] * per_col : 0.0f, y_level = LAYER && a.post ? dot[1] * per_col : 0.0f;
@@ -642,20 +690,29 @@ struct ParamGradArgs {
 
 // The groups' sums added, in an order of their numbers alone, and the params'
 // gradients made of them.  A block: 32 columns, by 32 warps.
-template <typename T, typename G>
+template <typename T, typename G, bool LAYER>
 __global__ void __launch_bounds__(1024) dopt_norm_param_kernel(const __grid_constant__ ParamGradArgs a) {
     __shared__ float part[32][4][33];
     let_dependents_start();
     wait_for_grids_before();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = int(blockIdx.x) * 32 + lane;
-    const int n_sums = a.layer ? 4 : 2;
+    constexpr int kSums = LAYER ? 4 : 2, kAhead = 16 / kSums;
     float f[4] = {};
     if (c < a.cols)
-#pragma unroll 4
-        for (int g = warp; g < a.groups; g += 32)
+        for (int g0 = warp; g0 < a.groups; g0 += 32 * kAhead) {
+            float v[kAhead][kSums];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (k < n_sums) f[k] += __ldcs(a.partial + (int64_t(g) * n_sums + k) * a.part_ld + c);
+            for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+                for (int k = 0; k < kSums; ++k) {
+                    const int g = g0 + 32 * j;
+                    v[j][k] = g < a.groups ? __ldcs(a.partial + (int64_t(g) * kSums + k) * a.part_ld + c) : 0.0f;
+                }
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+                for (int k = 0; k < kSums; ++k) f[k] += v[j][k];
+        }
 #pragma unroll
     for (int k = 0; k < 4; ++k) part[warp][k][lane] = f[k];
     __syncthreads();
@@ -665,11 +722,11 @@ __global__ void __launch_bounds__(1024) dopt_norm_param_kernel(const __grid_cons
         f[k] = 0.0f;
         for (int w = 0; w < 32; ++w) f[k] += part[w][k][lane];
     }
-    const float d_weight = f[0], d_bias = f[1], along = a.layer ? f[2] : f[1], level = f[3];
+    const float d_weight = f[0], d_bias = f[1], along = LAYER ? f[2] : f[1], level = f[3];
     auto value = [&](const void *p, float none) { return p ? to_f32(static_cast<const T *>(p)[c]) : none; };
     const float gate = value(a.gate, 1.0f);
     const float found[5] = {d_weight, d_bias, gate * along, gate * level,
-                            fmaf(value(a.post_weight, 1.0f), along, a.layer ? value(a.post_bias, 0.0f) * level : 0.0f)};
+                            fmaf(value(a.post_weight, 1.0f), along, LAYER ? value(a.post_bias, 0.0f) * level : 0.0f)};
 #pragma unroll
     for (int i = 0; i < 5; ++i) {
         if (a.at[i] < 0) continue;
@@ -682,13 +739,15 @@ __global__ void __launch_bounds__(1024) dopt_norm_param_kernel(const __grid_cons
 // Host side
 // ---------------------------------------------------------------------------
 
-// How rows are given to threads: NV groups of 8 columns a thread, so that a
-// row has up to 512 threads; short rows share a block.
+// How rows are given to threads: nv groups of 8 columns a thread; short rows
+// share a block.  A row's sums cost a thread the same whatever it holds, so the
+// forward pass, with few values to hold, takes two groups from 1024 columns on;
+// the gradients, which hold four times as many, take them from 2048 on.
 struct NormShape {
     int nv;
     dim3 block;
-    explicit NormShape(int64_t cols) {
-        nv = cols <= 2048 ? 1 : cols <= 8192 ? 2 : 4;
+    NormShape(int64_t cols, bool backward) {
+        nv = cols <= (backward ? 2048 : 1024) ? 1 : cols <= (backward ? 8192 : 4096) ? 2 : 4;
         const unsigned threads = unsigned((cols + 32 * kCols * nv - 1) / (32 * kCols * nv) * 32);
         block = dim3(threads, std::min(8u, std::max(1u, 256 / threads)));
     }
@@ -729,13 +788,18 @@ int launch_norm(const char *who, dopt_dtype dtype, bool layer, const NormArgs &a
     }
 }
 
+template <typename T, typename G>
+int launch_params(const char *who, const ParamGradArgs &a, cudaStream_t stream) {
+    const dim3 grid(unsigned((a.cols + 31) / 32));
+    return a.layer ? launch_op(who, dopt_norm_param_kernel<T, G, true>, grid, dim3(1024), 0, stream, a)
+                   : launch_op(who, dopt_norm_param_kernel<T, G, false>, grid, dim3(1024), 0, stream, a);
+}
 template <typename T>
 int launch_params(const char *who, dopt_dtype grad, const ParamGradArgs &a, cudaStream_t stream) {
-    const dim3 grid(unsigned((a.cols + 31) / 32));
     switch (grad) {
-        case DOPT_BF16: return launch_op(who, dopt_norm_param_kernel<T, __nv_bfloat16>, grid, dim3(1024), 0, stream, a);
-        case DOPT_FP16: return launch_op(who, dopt_norm_param_kernel<T, __half>, grid, dim3(1024), 0, stream, a);
-        default: return launch_op(who, dopt_norm_param_kernel<T, float>, grid, dim3(1024), 0, stream, a);
+        case DOPT_BF16: return launch_params<T, __nv_bfloat16>(who, a, stream);
+        case DOPT_FP16: return launch_params<T, __half>(who, a, stream);
+        default: return launch_params<T, float>(who, a, stream);
     }
 }
 
@@ -825,7 +889,7 @@ extern "C" int dopt_norm(const dopt_norm_cfg *cfg, const dopt_norm_params *param
     a.h = h, a.ld_h = ld_h;
     a.n = n, a.ld_n = ld_n;
     a.vec = bits % 16 == 0;
-    const NormShape shape(cols);
+    const NormShape shape(cols, false);
     const int64_t blocks = std::min<int64_t>((rows + shape.block.y - 1) / shape.block.y, 152 * 4);
     return launch_norm(who, dtype, cfg->kind == DOPT_NORM_LAYER, a, false, blocks, shape, stream);
 }
@@ -914,9 +978,9 @@ extern "C" int dopt_norm_grad(const dopt_norm_cfg *cfg, const dopt_norm_params *
         a.partial = static_cast<float *>(workspace);
         a.part_ld = norm_part_ld(cols);
         a.vec = bits % 16 == 0;
-        const NormShape shape(cols);
+        const NormShape shape(cols, true);
         const int64_t blocks = std::min<int64_t>((rows + shape.block.y - 1) / shape.block.y,
-                                                 std::min<int64_t>(152 * 3, kParts / shape.block.y));
+                                                 std::min<int64_t>(152 * 2, kParts / shape.block.y));
         groups = blocks * shape.block.y;
         if ((rc = launch_norm(who, dtype, layer, a, true, blocks, shape, stream)) != DOPT_OK) return rc;
     }
