@@ -29,7 +29,9 @@ constexpr int kMostSplit = 16, kMostSlots = 304;
 
 constexpr int kLogitWarps = 8;  // that go through logits
 constexpr int kLogitThreads = 32 * (kLogitWarps + 2);
-constexpr int kLossRing = 6, kGradRing = 5;
+// What a logit kernel keeps: nothing of the logits (the loss), or their
+// gradients in one or two parts of 16 bits, a buffer of 4 KB a part and warp.
+__host__ __device__ constexpr int logit_ring(int planes) { return planes == 2 ? 5 : 6; }
 constexpr int kOutBuffer = 32 * 128;  // 32 tokens x 64 logits of 16 bits
 constexpr int kStoreWarps = 4;
 constexpr int kProductThreads = 32 * (kStoreWarps + 2);
@@ -41,10 +43,11 @@ struct HeadBarriers {
     uint32_t tmem;
     int32_t failed;
 };
-constexpr size_t kLossSmem = kLossRing * size_t(kStage) + sizeof(HeadBarriers);
-constexpr size_t kGradSmem = kGradRing * size_t(kStage) + 2 * kLogitWarps * size_t(kOutBuffer) + sizeof(HeadBarriers);
+__host__ __device__ constexpr size_t logit_smem(int planes) {
+    return logit_ring(planes) * size_t(kStage) + planes * kLogitWarps * size_t(kOutBuffer) + sizeof(HeadBarriers);
+}
 constexpr size_t kProductSmem = kProductRing * size_t(kStage) + sizeof(HeadBarriers);
-static_assert(kLossSmem <= 232448 && kGradSmem <= 232448 && kProductSmem <= 232448, "a CTA's 227 KB");
+static_assert(logit_smem(1) <= 232448 && logit_smem(2) <= 232448 && kProductSmem <= 232448, "a CTA's 227 KB");
 
 // CTAs with a wait that ran past its limit (a copy or product that never
 // completed).  Such a pair ends its work; what it has not written becomes NaN.
@@ -143,6 +146,17 @@ __device__ __forceinline__ void load_box(uint32_t to, const CUtensorMap *map, in
         "l"(map), "r"(x), "r"(y), "r"(barrier)
         : "memory");
 }
+// Written once and read once or twice much later: the first to leave L2, where
+// the operands of the products stay (gradients of 16384 x 768 x 50257 2280 ->
+// 2222 us).
+__device__ __forceinline__ void store_box(const CUtensorMap *map, int x, int y, uint32_t from) {
+    asm volatile(
+        "{\n\t.reg .b64 policy;\n\t"
+        "createpolicy.fractional.L2::evict_first.b64 policy, 1.0;\n\t"
+        "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group.L2::cache_hint [%0, {%1, %2}], [%3], policy;\n\t}" ::"l"(map),
+        "r"(x), "r"(y), "r"(from)
+        : "memory");
+}
 __device__ __forceinline__ void expect_bytes(uint32_t barrier, int bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(barrier), "r"(bytes) : "memory");
 }
@@ -231,7 +245,7 @@ struct LogitArgs {
     int32_t rows, cols;         // tokens, columns of this launch
     int32_t steps, tiles_m, tiles_n, items;
     int32_t group;              // blocks of tokens that go through the vocabulary together
-    int32_t wide, planes;
+    int32_t wide;
 };
 
 struct Tile {
@@ -313,14 +327,16 @@ __device__ __forceinline__ float rest_of(float f) {
     return f - to_f32(from_f32<T>(f));
 }
 
-template <typename T, bool GRAD>
+// PLANES: 0, the loss; 1 or 2, the parts of the logits' gradients.
+template <typename T, int PLANES>
 __global__ void __launch_bounds__(kLogitThreads, 1) __cluster_dims__(2, 1, 1)
     dopt_head_logit_kernel(const __grid_constant__ LogitArgs a) {
     extern __shared__ __align__(1024) unsigned char smem[];
-    constexpr int kRing = GRAD ? kGradRing : kLossRing;
+    constexpr bool GRAD = PLANES > 0;
+    constexpr int kRing = logit_ring(PLANES);
     constexpr int kMmaWarp = kLogitWarps, kLoadWarp = kLogitWarps + 1;
     unsigned char *out_buffers = smem + kRing * kStage;
-    HeadBarriers &b = *reinterpret_cast<HeadBarriers *>(out_buffers + (GRAD ? 2 * kLogitWarps * kOutBuffer : 0));
+    HeadBarriers &b = *reinterpret_cast<HeadBarriers *>(out_buffers + PLANES * kLogitWarps * kOutBuffer);
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const int pairs = int(gridDim.x >> 1), pair = int(blockIdx.x >> 1);
@@ -378,7 +394,7 @@ __global__ void __launch_bounds__(kLogitThreads, 1) __cluster_dims__(2, 1, 1)
         // warp w: tokens 32 (w % 4) on, 128 columns from 128 (w / 4) on
         const int half = warp >> 2;
         const uint32_t lanes = tmem + (uint32_t((warp & 3) * 32) << 16) + uint32_t(half * 128);
-        unsigned char *out = out_buffers + warp * 2 * kOutBuffer;
+        unsigned char *out = out_buffers + warp * PLANES * kOutBuffer;
         int t = 0;
         bool ok = true;
         for (int item = pair; item < a.items; item += pairs, ++t) {
@@ -433,25 +449,21 @@ __global__ void __launch_bounds__(kLogitThreads, 1) __cluster_dims__(2, 1, 1)
                         for (int j = 0; j < 32; ++j)
                             if (at == j) l[j] -= by_target;
                     }
-                    for (int plane = 0; plane < a.planes; ++plane) {
-                        // slab k / 2 of plane p goes to the buffer of the same parity as 2 (k / 2) + p
-                        const int which = a.planes == 1 ? (k >> 1) & 1 : plane;
-                        unsigned char *to = out + which * kOutBuffer;
-                        if ((k & 1) == 0) {  // the copy that was last made from there has read it
-                            if (lane == 0) {
-                                if (a.planes == 1) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-                                else asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                            }
-                            __syncwarp();
-                        }
+                    if ((k & 1) == 0) {  // the copies last made from the buffers have read them
+                        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                        __syncwarp();
+                    }
+#pragma unroll
+                    for (int plane = 0; plane < PLANES; ++plane) {
+                        unsigned char *to = out + plane * kOutBuffer + lane * 128;
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             uint4 v;
                             v.x = pack2<T>(l[8 * q], l[8 * q + 1]), v.y = pack2<T>(l[8 * q + 2], l[8 * q + 3]);
                             v.z = pack2<T>(l[8 * q + 4], l[8 * q + 5]), v.w = pack2<T>(l[8 * q + 6], l[8 * q + 7]);
-                            *reinterpret_cast<uint4 *>(to + lane * 128 + ((((k & 1) * 4 + q) ^ (lane & 7)) << 4)) = v;
+                            *reinterpret_cast<uint4 *>(to + ((((k & 1) * 4 + q) ^ (lane & 7)) << 4)) = v;
                         }
-                        if (a.planes == 2 && plane == 0) {
+                        if (plane + 1 < PLANES) {
 #pragma unroll
                             for (int j = 0; j < 32; ++j) l[j] = rest_of<T>(l[j]);
                         }
@@ -461,18 +473,12 @@ __global__ void __launch_bounds__(kLogitThreads, 1) __cluster_dims__(2, 1, 1)
                         __syncwarp();
                         const int c = c0 + 32 * (k - 1);
                         if (lane == 0) {
-                            for (int plane = 0; plane < a.planes; ++plane) {
-                                const int which = a.planes == 1 ? (k >> 1) & 1 : plane;
-                                if (c < a.cols && row0 < a.rows)
-                                    asm volatile(
-                                        "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
-                                            &a.d_map[plane]),
-                                        "r"(c), "r"(row0), "r"(smem_of(out + which * kOutBuffer))
-                                        : "memory");
-                                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-                            }
+                            if (c < a.cols && row0 < a.rows)
+#pragma unroll
+                                for (int plane = 0; plane < PLANES; ++plane)
+                                    store_box(&a.d_map[plane], c, row0, smem_of(out + plane * kOutBuffer));
+                            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                         }
-                        __syncwarp();
                     }
                 }
             }
@@ -484,7 +490,7 @@ __global__ void __launch_bounds__(kLogitThreads, 1) __cluster_dims__(2, 1, 1)
 }
 
 // The parts of each row's sum joined: lse, and the loss.  A block: 32 rows, by
-// 8 warps' shares of the parts.
+// 32 warps' shares of the parts, eight parts at a time under one reference.
 struct JoinLossArgs {
     const float2 *partial;
     const float *at_target;
@@ -493,32 +499,49 @@ struct JoinLossArgs {
     int64_t vocab;
     int32_t parts, rows, wide;
 };
-__device__ __forceinline__ void join_sums(float &c, float &s, float c2, float s2) {
-    const float top = fmaxf(c, c2);
-    s = s * (c == top ? 1.0f : exp2f(c - top)) + s2 * (c2 == top ? 1.0f : exp2f(c2 - top));
+constexpr int kJoinWarps = 32;
+template <int N>
+__device__ __forceinline__ void join_sums(float &c, float &s, const float2 (&v)[N]) {
+    float top = c;
+#pragma unroll
+    for (int i = 0; i < N; ++i) top = fmaxf(top, v[i].x);
+    // (parts that are empty or whose reference is infinite: no difference of two infinities)
+    s = c == top ? s : s * exp2_of(c - top);
+#pragma unroll
+    for (int i = 0; i < N; ++i) s += v[i].x == top ? v[i].y : v[i].y * exp2_of(v[i].x - top);
     c = top;
 }
-__global__ void __launch_bounds__(256) dopt_head_join_kernel(const __grid_constant__ JoinLossArgs a) {
-    __shared__ float2 part[8][32];
+__global__ void __launch_bounds__(32 * kJoinWarps) dopt_head_join_kernel(const __grid_constant__ JoinLossArgs a) {
+    __shared__ float2 part[kJoinWarps][33];
     let_dependents_start();
     wait_for_grids_before();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = int(blockIdx.x) * 32 + lane;
+    const float2 none = make_float2(-INFINITY, 0.0f);
     float c = -INFINITY, s = 0.0f;
     if (row < a.rows)
-#pragma unroll 8
-        for (int p = warp; p < a.parts; p += 8) {
-            const float2 v = __ldcs(a.partial + int64_t(p) * a.rows + row);
-            join_sums(c, s, v.x, v.y);
+        for (int p = warp; p < a.parts; p += 8 * kJoinWarps) {
+            float2 v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] = p + i * kJoinWarps < a.parts ? __ldcs(a.partial + int64_t(p + i * kJoinWarps) * a.rows + row) : none;
+            join_sums(c, s, v);
         }
     part[warp][lane] = make_float2(c, s);
     __syncthreads();
-    if (warp > 0 || row >= a.rows) return;
-    for (int w = 1; w < 8; ++w) join_sums(c, s, part[w][lane].x, part[w][lane].y);
+    // warp w joins row w's: a lane a part, then halves
+    const int mine = int(blockIdx.x) * 32 + warp;
+    c = part[lane][warp].x, s = part[lane][warp].y;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        const float2 v[1] = {make_float2(__shfl_down_sync(kFull, c, d), __shfl_down_sync(kFull, s, d))};
+        join_sums(c, s, v);
+    }
+    if (lane > 0 || mine >= a.rows) return;
     const double lse = (double(c) + double(log2f(s))) * 0.69314718055994530942;
-    const int64_t target = a.wide ? static_cast<const int64_t *>(a.targets)[row]
-                                  : int64_t(static_cast<const int32_t *>(a.targets)[row]);
-    a.lse[row] = float(lse);
-    a.loss[row] = target >= 0 && target < a.vocab ? float(lse - double(a.at_target[row])) : 0.0f;
+    const int64_t target = a.wide ? static_cast<const int64_t *>(a.targets)[mine]
+                                  : int64_t(static_cast<const int32_t *>(a.targets)[mine]);
+    a.lse[mine] = float(lse);
+    a.loss[mine] = target >= 0 && target < a.vocab ? float(lse - double(a.at_target[mine])) : 0.0f;
 }
 
 // fp16 gradients of logits are multiplied by a power of two that brings the
@@ -804,8 +827,9 @@ cudaError_t allow_smem(K kernel, size_t bytes) {
 }
 template <typename T>
 cudaError_t allow_all() {
-    cudaError_t e = allow_smem(dopt_head_logit_kernel<T, false>, kLossSmem);
-    if (e == cudaSuccess) e = allow_smem(dopt_head_logit_kernel<T, true>, kGradSmem);
+    cudaError_t e = allow_smem(dopt_head_logit_kernel<T, 0>, logit_smem(0));
+    if (e == cudaSuccess) e = allow_smem(dopt_head_logit_kernel<T, 1>, logit_smem(1));
+    if (e == cudaSuccess) e = allow_smem(dopt_head_logit_kernel<T, 2>, logit_smem(2));
     if (e == cudaSuccess) e = allow_smem(dopt_head_product_kernel<T, false>, kProductSmem);
     if (e == cudaSuccess) e = allow_smem(dopt_head_product_kernel<T, true>, kProductSmem);
     return e;
@@ -1038,14 +1062,14 @@ int run_grad(const char *who, const GradCall &c, Operands o, const HeadSpace &sp
         a.first = v0;
         a.vocab = c.vocab;
         a.wide = c.target_bytes == 8;
-        a.planes = c.planes;
         rc = make_map(who, encode, &a.x_map, c.dtype, o.x, c.width, c.rows, o.ld_x, 64, 128);
         if (rc == DOPT_OK) rc = make_map(who, encode, &a.w_map, c.dtype, w, c.width, cols, o.ld_w, 64, 128);
         for (int p = 0; p < c.planes && rc == DOPT_OK; ++p)
             rc = make_map(who, encode, &a.d_map[p], c.dtype, rest + g.logits + p * plane, cols, c.rows, g.piece_ld, 64, 32);
         if (rc != DOPT_OK) return rc;
-        rc = launch_op(who, dopt_head_logit_kernel<T, true>, dim3(unsigned(2 * std::min<int64_t>(a.items, pairs))),
-                       dim3(kLogitThreads), kGradSmem, stream, a);
+        rc = launch_op(who, c.planes == 2 ? dopt_head_logit_kernel<T, 2> : dopt_head_logit_kernel<T, 1>,
+                       dim3(unsigned(2 * std::min<int64_t>(a.items, pairs))), dim3(kLogitThreads), logit_smem(c.planes),
+                       stream, a);
         if (rc != DOPT_OK) return rc;
         ProductArgs p{};
         p.partial = reinterpret_cast<float *>(rest + g.parts);
@@ -1153,11 +1177,11 @@ extern "C" int dopt_head_loss(const void *x, dopt_dtype dtype, int64_t rows, int
     a.partial = reinterpret_cast<float2 *>(rest + up_to(rows * 4, 256));
     const dim3 grid(unsigned(2 * std::min<int64_t>(a.items, pairs)));
     rc = dtype == DOPT_BF16
-             ? launch_op(who, dopt_head_logit_kernel<__nv_bfloat16, false>, grid, dim3(kLogitThreads), kLossSmem, stream, a)
-             : launch_op(who, dopt_head_logit_kernel<__half, false>, grid, dim3(kLogitThreads), kLossSmem, stream, a);
+             ? launch_op(who, dopt_head_logit_kernel<__nv_bfloat16, 0>, grid, dim3(kLogitThreads), logit_smem(0), stream, a)
+             : launch_op(who, dopt_head_logit_kernel<__half, 0>, grid, dim3(kLogitThreads), logit_smem(0), stream, a);
     if (rc != DOPT_OK) return rc;
     JoinLossArgs j{a.partial, a.at_target, targets, loss, lse, vocab, 2 * a.tiles_n, a.rows, a.wide};
-    return launch_op(who, dopt_head_join_kernel, dim3(unsigned((rows + 31) / 32)), dim3(256), 0, stream, j);
+    return launch_op(who, dopt_head_join_kernel, dim3(unsigned((rows + 31) / 32)), dim3(32 * kJoinWarps), 0, stream, j);
 }
 
 extern "C" int dopt_head_loss_grad_workspace(int64_t rows, int64_t width, int64_t vocab, dopt_dtype grad_dtype,
