@@ -245,6 +245,7 @@ struct LogitArgs {
     int32_t rows, cols;         // tokens, columns of this launch
     int32_t steps, tiles_m, tiles_n, items;
     int32_t group;              // blocks of tokens that go through the vocabulary together
+    int32_t x_ctas, step_bytes; // CTAs of a pair that have tokens; bytes of a pair's step
     int32_t wide;
 };
 
@@ -353,8 +354,9 @@ __global__ void __launch_bounds__(kLogitThreads, 1) __cluster_dims__(2, 1, 1)
                 if (!ok) break;
                 if (elect_one()) {
                     const uint32_t full = smem_of(&b.full[s]), to = smem_of(smem + s * kStage);
-                    if (rank == 0) expect_bytes(full, 2 * kStage);
-                    load_box(to, &a.x_map, i * kK, t.m0 + int(rank) * (kM / 2), leader_address(full));
+                    if (rank == 0) expect_bytes(full, a.step_bytes);
+                    if (int(rank) < a.x_ctas)
+                        load_box(to, &a.x_map, i * kK, t.m0 + int(rank) * (kM / 2), leader_address(full));
                     load_box(to + kOperand, &a.w_map, i * kK, t.n0 + int(rank) * (kN / 2), leader_address(full));
                 }
                 __syncwarp();
@@ -997,7 +999,15 @@ int make_operands(const char *who, Operands &o, const HeadSpace &space, char *ws
     return rc;
 }
 
+// Rows of x in a box: of few tokens, no more than there are.  The rest of the
+// operand is then whatever shared memory held, which reaches rows of the
+// logits alone that nothing reads; boxes of 128 rows for 24 tokens took 38 us
+// where these take 31 (24 x 2048 x 32000).
+uint32_t x_box_rows(int64_t rows) { return uint32_t(std::min<int64_t>(kM / 2, up_to(rows, 8))); }
+
 int fill_tiles(LogitArgs &a, int64_t rows, int64_t width, int64_t cols) {
+    a.x_ctas = rows > kM / 2 ? 2 : 1;
+    a.step_bytes = int32_t(a.x_ctas * x_box_rows(rows) * kK * 2 + 2 * kOperand);
     a.rows = int32_t(rows);
     a.cols = int32_t(cols);
     a.steps = int32_t((width + kK - 1) / kK);
@@ -1062,7 +1072,7 @@ int run_grad(const char *who, const GradCall &c, Operands o, const HeadSpace &sp
         a.first = v0;
         a.vocab = c.vocab;
         a.wide = c.target_bytes == 8;
-        rc = make_map(who, encode, &a.x_map, c.dtype, o.x, c.width, c.rows, o.ld_x, 64, 128);
+        rc = make_map(who, encode, &a.x_map, c.dtype, o.x, c.width, c.rows, o.ld_x, 64, x_box_rows(c.rows));
         if (rc == DOPT_OK) rc = make_map(who, encode, &a.w_map, c.dtype, w, c.width, cols, o.ld_w, 64, 128);
         for (int p = 0; p < c.planes && rc == DOPT_OK; ++p)
             rc = make_map(who, encode, &a.d_map[p], c.dtype, rest + g.logits + p * plane, cols, c.rows, g.piece_ld, 64, 32);
@@ -1167,7 +1177,7 @@ extern "C" int dopt_head_loss(const void *x, dopt_dtype dtype, int64_t rows, int
     Operands o{x, weight, ld_x, ld_w};
     rc = dtype == DOPT_BF16 ? make_operands<__nv_bfloat16>(who, o, space, ws, rows, width, vocab, stream)
                             : make_operands<__half>(who, o, space, ws, rows, width, vocab, stream);
-    if (rc == DOPT_OK) rc = make_map(who, encode, &a.x_map, dtype, o.x, width, rows, o.ld_x, 64, 128);
+    if (rc == DOPT_OK) rc = make_map(who, encode, &a.x_map, dtype, o.x, width, rows, o.ld_x, 64, x_box_rows(rows));
     if (rc == DOPT_OK) rc = make_map(who, encode, &a.w_map, dtype, o.w, width, vocab, o.ld_w, 64, 128);
     if (rc != DOPT_OK) return rc;
     a.targets = targets;
