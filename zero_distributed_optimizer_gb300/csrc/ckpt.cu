@@ -18,6 +18,7 @@
 // with them).  Rows that are not go in aligned pieces all the same
 // (rows.cuh): 16384 x 5631 bf16, kept and read back, 113 us (585 us one
 // element at a time).
+#include "f32x2.cuh"
 #include "rows.cuh"
 
 namespace {
@@ -39,31 +40,6 @@ struct CkptArgs {
     int32_t vec;          // rows are 16-byte aligned
     int32_t turns;        // times a block takes its number of rows
 };
-
-// ---------------------------------------------------------------------------
-// Two fp32 numbers and operations on both, one instruction each
-// ---------------------------------------------------------------------------
-
-struct F2 {
-    uint64_t v;
-    __device__ __forceinline__ F2(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
-    __device__ __forceinline__ F2(float a) : F2(a, a) {}
-    __device__ __forceinline__ void get(float &a, float &b) const {
-        asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-    }
-};
-__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
-    asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(a.v) : "l"(b.v));
-    return a;
-}
-__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
-    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(a.v) : "l"(b.v));
-    return a;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-    asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(a.v) : "l"(b.v), "l"(c.v));
-    return a;
-}
 
 // ---------------------------------------------------------------------------
 // Codes

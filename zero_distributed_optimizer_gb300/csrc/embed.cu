@@ -13,6 +13,8 @@ constexpr int kWarpCols = 32 * kCols;    // columns a warp
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMostRange = 1024;         // rows of the table that one sorting block owns
+constexpr int kListed = 128;             // of its own tokens that a sorting warp lists in shared memory
+constexpr int kLeastShift = 7;           // at least 128 sorting blocks
 constexpr int kMostShare = 32;           // sorted tokens that a warp sums
 constexpr int kRingBytes = 4096;         // of a warp's loads ahead
 
@@ -124,7 +126,7 @@ struct EmbedGradArgs {
     const void *ids;
     const void *d_out;
     void *grad;             // of the table's first element
-    int32_t *first;         // [vocab + 1] the first sorted place of each row of the table
+    int32_t *first;         // [ranges * range + 1] the first sorted place of each row of the table, by key
     int32_t *token;         // [tokens] the tokens by row, in order within one
     int32_t *row;           // [tokens] their rows
     int2 *list;             // [tokens] (token, row in its range and more), by range
@@ -132,13 +134,20 @@ struct EmbedGradArgs {
     float *partial;         // [2 * chunks][part_ld] sums of runs that reach over a chunk's ends
     int64_t ld, tokens, vocab, part_ld;
     int32_t cols, pieces;   // pieces: of 256 columns
-    int32_t range, ranges;
+    int32_t range, ranges, shift;  // ranges = 2^shift
     int32_t share, chunks;  // sorted tokens of a summing warp; blocks of 8 of those
     int32_t vec, vec_grad;  // d_out's, the grads' rows are 16-byte aligned
     int32_t accumulate;
     int32_t grad_bytes;     // of an element
     float scale;
 };
+
+// A row's place in the order of the sorted tokens: rows go to the sorting
+// blocks in turn, so that frequent ids next to each other (a tokenizer's most
+// frequent tokens often are) do not meet in one block.
+__device__ __forceinline__ int64_t key_of(const EmbedGradArgs &a, int row) {
+    return int64_t(row & (a.ranges - 1)) * a.range + (row >> a.shift);
+}
 
 // Exclusive sum over a block's warps of one number each; `total` of all.
 __device__ __forceinline__ uint32_t over_warps(uint32_t mine, uint32_t *buffer, uint32_t &total) {
@@ -172,9 +181,9 @@ __device__ __forceinline__ void zero_grads(const EmbedGradArgs &a, int64_t block
     }
 }
 
-// The tokens sorted by id (stable).  A block owns `range` rows of the table.
-// It goes through all ids, so that it knows without any other block how many
-// lie below its own, lists those that are its own in order and sorts the
+// The tokens sorted by the key of their row (stable).  A block owns `range`
+// rows of the table.  It goes through all ids, so that it knows without any
+// other block how many belong to those before it, lists those that are its own in order and sorts the
 // list: counts of each (warp, row), their prefixes, places.  A lane's rank
 // among its warp's tokens of one row comes from a ballot per bit of the row
 // and is kept with the token for the second pass.  The sort is bound by
@@ -182,7 +191,7 @@ __device__ __forceinline__ void zero_grads(const EmbedGradArgs &a, int64_t block
 // beside it.
 template <typename I>
 __global__ void __launch_bounds__(kSortThreads) dopt_embed_sort_kernel(const __grid_constant__ EmbedGradArgs a) {
-    extern __shared__ uint32_t count[];  // [warps][range]
+    extern __shared__ uint32_t count[];  // [warps][range], then the warps' lists
     __shared__ uint32_t buffer[32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t before = (1u << lane) - 1;
@@ -192,14 +201,14 @@ __global__ void __launch_bounds__(kSortThreads) dopt_embed_sort_kernel(const __g
         zero_grads(a, blockIdx.x - a.ranges, gridDim.x - a.ranges);
         return;
     }
-    const int64_t lo = int64_t(blockIdx.x) * a.range;
-    const int rows = int(min(int64_t(a.range), a.vocab - lo));
+    const int block = int(blockIdx.x), mask = a.ranges - 1;
     for (int64_t i = int64_t(blockIdx.x) * kSortThreads + threadIdx.x; i < int64_t(a.chunks) * a.pieces;
          i += int64_t(a.ranges) * kSortThreads)
         a.arrived[i] = 0;
     for (int i = threadIdx.x; i < kSortWarps * a.range; i += kSortThreads) count[i] = 0;
 
     constexpr int kAhead = 8;
+    int2 *const own_list = reinterpret_cast<int2 *>(count + kSortWarps * a.range + (a.range & 1) * kSortWarps) + warp * kListed;
     const int64_t stretch = ((a.tokens + kSortWarps - 1) / kSortWarps + 31) / 32 * 32;
     const int64_t from = min(a.tokens, warp * stretch), to = min(a.tokens, from + stretch);
     uint32_t own = 0, below = 0;
@@ -209,26 +218,32 @@ __global__ void __launch_bounds__(kSortThreads) dopt_embed_sort_kernel(const __g
         for (int j = 0; j < kAhead; ++j) id[j] = i + 32 * j + lane < to ? id_at<I>(a.ids, i + 32 * j + lane) : -1;
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
-            own += uint64_t(id[j] - lo) < uint64_t(rows);
-            below += uint64_t(id[j]) < uint64_t(lo);
+            const int of = uint64_t(id[j]) < uint64_t(a.vocab) ? int(id[j]) & mask : mask + 1;
+            below += of < block;
+            const uint32_t all = __ballot_sync(kFull, of == block);
+            const uint32_t at = own + __popc(all & before);
+            if (of == block && at < kListed) own_list[at] = make_int2(int(i + 32 * j + lane), int(id[j]) >> a.shift);
+            own += __popc(all);
         }
     }
-    own = __reduce_add_sync(kFull, own);
     below = __reduce_add_sync(kFull, below);
     uint32_t total, base;
     uint32_t place = over_warps(own, buffer, total);
     over_warps(below, buffer, base);
-    if (own > 0) {
+    // The warps' own lists where they hold all; otherwise one list in memory, of
+    // which each warp then takes the same share.
+    const bool in_memory = __syncthreads_or(own > kListed);
+    if (in_memory && own > 0) {
         for (int64_t i = from; i < to; i += 32 * kAhead) {
             int64_t id[kAhead];
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) id[j] = i + 32 * j + lane < to ? id_at<I>(a.ids, i + 32 * j + lane) : -1;
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) {
-                const bool here = uint64_t(id[j] - lo) < uint64_t(rows);
+                const bool here = uint64_t(id[j]) < uint64_t(a.vocab) && (int(id[j]) & mask) == block;
                 const uint32_t all = __ballot_sync(kFull, here);
                 if (here)
-                    a.list[base + place + __popc(all & before)] = make_int2(int(i + 32 * j + lane), int(id[j] - lo));
+                    a.list[base + place + __popc(all & before)] = make_int2(int(i + 32 * j + lane), int(id[j]) >> a.shift);
                 place += __popc(all);
             }
         }
@@ -236,13 +251,14 @@ __global__ void __launch_bounds__(kSortThreads) dopt_embed_sort_kernel(const __g
     __syncthreads();
     uint32_t *mine = count + warp * a.range;
     const uint32_t share = ((total + kSortWarps - 1) / kSortWarps + 31) / 32 * 32;
-    const uint32_t begin = min(total, warp * share), end = min(total, begin + share);
-    const int bits = 32 - __clz(a.range - 1);  // (range >= 32)
-    int2 next = begin + lane < end ? a.list[base + begin + lane] : make_int2(0, 0);
+    const uint32_t begin = in_memory ? min(total, warp * share) : 0, end = in_memory ? min(total, begin + share) : own;
+    int2 *const list = in_memory ? a.list + base : own_list;
+    const int bits = 32 - __clz(a.range - 1);
+    int2 next = begin + lane < end ? list[begin + lane] : make_int2(0, 0);
     for (uint32_t i = begin; i < end; i += 32) {
         const bool there = i + lane < end;
         const int row = next.y;
-        if (i + 32 < end) next = i + 32 + lane < end ? a.list[base + i + 32 + lane] : make_int2(0, 0);
+        if (i + 32 < end) next = i + 32 + lane < end ? list[i + 32 + lane] : make_int2(0, 0);
         uint32_t peers = __ballot_sync(kFull, there);
         for (int k = 0; k < bits; ++k) {
             const uint32_t ones = __ballot_sync(kFull, row >> k & 1);
@@ -252,13 +268,13 @@ __global__ void __launch_bounds__(kSortThreads) dopt_embed_sort_kernel(const __g
             const int rank = __popc(peers & before);
             if (rank == 0) mine[row] += __popc(peers);
             // the row, the rank, and for the first of them how many they are
-            a.list[base + i + lane].y = row | rank << 16 | (rank == 0 ? __popc(peers) << 21 : 0);
+            list[i + lane].y = row | rank << 16 | (rank == 0 ? __popc(peers) << 21 : 0);
         }
         __syncwarp();
     }
     __syncthreads();
     uint32_t of_row = 0;  // thread r: the tokens of row r
-    if (int(threadIdx.x) < rows && total > 0)
+    if (int(threadIdx.x) < a.range && total > 0)
         for (int w = 0; w < kSortWarps; ++w) {
             uint32_t *p = count + w * a.range + threadIdx.x;
             const uint32_t n = *p;
@@ -273,24 +289,24 @@ __global__ void __launch_bounds__(kSortThreads) dopt_embed_sort_kernel(const __g
     }
     uint32_t all;
     const uint32_t start = base + over_warps(__shfl_sync(kFull, upto, 31), buffer, all) + upto - of_row;
-    if (int(threadIdx.x) < rows) {
-        a.first[lo + threadIdx.x] = int(start);
+    if (int(threadIdx.x) < a.range) {
+        a.first[int64_t(block) * a.range + threadIdx.x] = int(start);
         if (total > 0)
             for (int w = 0; w < kSortWarps; ++w) count[w * a.range + threadIdx.x] += start;
     }
-    if (int(blockIdx.x) == a.ranges - 1 && threadIdx.x == 0) a.first[a.vocab] = int(base + total);
+    if (block == a.ranges - 1 && threadIdx.x == 0) a.first[int64_t(a.ranges) * a.range] = int(base + total);
     __syncthreads();
-    next = begin + lane < end ? a.list[base + begin + lane] : make_int2(0, 0);
+    next = begin + lane < end ? list[begin + lane] : make_int2(0, 0);
     for (uint32_t i = begin; i < end; i += 32) {
         const bool there = i + lane < end;
         const int2 e = next;
-        if (i + 32 < end) next = i + 32 + lane < end ? a.list[base + i + 32 + lane] : make_int2(0, 0);
+        if (i + 32 < end) next = i + 32 + lane < end ? list[i + 32 + lane] : make_int2(0, 0);
         const int row = e.y & 0xffff;
         const uint32_t at = there ? mine[row] + (e.y >> 16 & 31) : 0;
         __syncwarp();
         if (there) {
             a.token[at] = e.x;
-            a.row[at] = int(lo) + row;
+            a.row[at] = row << a.shift | block;
             if (const uint32_t of_chunk = uint32_t(e.y) >> 21) mine[row] += of_chunk;  // by the first of a row
         }
         __syncwarp();
@@ -329,12 +345,13 @@ __device__ __forceinline__ void put_row(const EmbedGradArgs &a, int64_t row, int
     }
 }
 
-// A block takes a chunk of sorted tokens and 256 columns, a warp an eighth of them,
-// whose rows of d_out are loaded ahead whatever rows of the table they go to.
-// A row whose tokens are all a warp's own is written by it.  Parts of a row
-// that reaches over warps meet in shared memory and are added in order by the
-// warp in which it begins; parts that reach over the chunk's ends are kept as
-// partial sums, and the block that brings a row's last one adds them in
+// A block takes a chunk of sorted tokens and 256 columns, a warp an eighth of
+// them, whose rows of d_out are loaded ahead whatever rows of the table they go
+// to.  A row of no more tokens than a share is summed and written by the warp in
+// whose share it begins, past the share's end too.  Longer ones are summed in parts: those
+// of a chunk's warps meet in shared memory and are added in order by the warp in
+// which the row begins (or the first); sums of a chunk's part are kept where the
+// row reaches over chunks, and the block that brings the last one adds them in
 // order.
 template <typename T, typename G, bool WHOLE>
 __global__ void __launch_bounds__(kEmbedThreads) dopt_embed_grad_kernel(const __grid_constant__ EmbedGradArgs a) {
@@ -345,30 +362,51 @@ __global__ void __launch_bounds__(kEmbedThreads) dopt_embed_grad_kernel(const __
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int chunk = int(blockIdx.x / a.pieces), piece = int(blockIdx.x % a.pieces);
     const int c = piece * kWarpCols + lane * kCols;
-    const int total = a.first[a.vocab], per_chunk = kWarps * a.share;
-    const int base = chunk * per_chunk, p0 = base + warp * a.share, n = min(a.share, total - p0);
+    const int per_chunk = kWarps * a.share;
+    const int base = chunk * per_chunk, p0 = base + warp * a.share;
+    // lane i: the warp's tokens i and 32 + i, with what may follow its share
+    // (loaded before it is known how many there are)
+    int token[2], row[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int64_t p = int64_t(p0) + 32 * k + lane;
+        token[k] = p < a.tokens ? a.token[p] : 0;
+        row[k] = p < a.tokens ? a.row[p] : -1;
+    }
+    int row_before = p0 > 0 && p0 < a.tokens ? a.row[p0 - 1] : -1;
+    const int total = a.first[int64_t(a.ranges) * a.range], n = min(a.share, total - p0);
     if (base >= total) return;
-    // lane i: the i-th of the warp's tokens
-    const int token = lane < n ? a.token[p0 + lane] : 0;
-    const int row = lane < n ? a.row[p0 + lane] : -1;
-    const int row_before = n > 0 && p0 > 0 ? a.row[p0 - 1] : -1;
-    const int row_after = n == a.share && p0 + n < total ? a.row[p0 + n] : -1;
-    const int next = __shfl_down_sync(kFull, row, 1);
-    const uint32_t ends = __ballot_sync(kFull, lane < n && (lane == n - 1 || next != row));  // a row's last token here
-    const bool from_before = n > 0 && __shfl_sync(kFull, row, 0) == row_before;
-    const bool goes_on = n > 0 && row_after >= 0 && __shfl_sync(kFull, row, n > 0 ? n - 1 : 0) == row_after;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        if (p0 + 32 * k + lane >= total) token[k] = 0, row[k] = -1;
+    if (n <= 0) row_before = -1;
+    auto row_at = [&](int i) { return __shfl_sync(kFull, i < 32 ? row[0] : row[1], i & 31); };
+    const int head_row = row_at(0), tail_row = row_at(max(n - 1, 0));
+    const bool from_before = n > 0 && head_row == row_before, goes_on = n == a.share && row_at(n) == tail_row && tail_row >= 0;
+    // the first and last rows' places, where they reach over the share's ends
+    int2 head = make_int2(0, 0), tail = make_int2(0, 0);
+    if (from_before) head = make_int2(a.first[key_of(a, head_row)], a.first[key_of(a, head_row) + 1]);
+    if (goes_on) tail = make_int2(a.first[key_of(a, tail_row)], a.first[key_of(a, tail_row) + 1]);
+    const bool head_part = head.y - head.x > a.share, tail_part = tail.y - tail.x > a.share;
+    const int from = from_before && !head_part ? min(n, head.y - p0) : 0;          // (an earlier warp's before that)
+    const int to = from < n && goes_on && !tail_part ? tail.y - p0 : max(n, 0);  // (less than a share past it)
+    // the tokens after which another row begins
+    const int after_lo = __shfl_down_sync(kFull, row[0], 1), after_hi = __shfl_down_sync(kFull, row[1], 1);
+    const int middle = __shfl_sync(kFull, row[1], 0);
+    const uint64_t ends = __ballot_sync(kFull, row[0] != (lane < 31 ? after_lo : middle)) |
+                          uint64_t(__ballot_sync(kFull, row[1] != after_hi)) << 32 | (to > 0 ? uint64_t(1) << (to - 1) : 0);
     float f[kCols] = {};
     // token i's values are added; those of a row that ends there go where they belong
     auto add = [&](int i, const float(&g)[kCols]) {
 #pragma unroll
         for (int q = 0; q < kCols; ++q) f[q] += g[q];
         if (!(ends >> i & 1)) return;
-        const bool head = (ends & ((1u << i) - 1)) == 0 && from_before, tail = i == n - 1 && goes_on;
-        if (head || tail) {
+        const bool of_head = head_part && (ends & ((uint64_t(1) << i) - 1)) == 0, of_tail = tail_part && i == n - 1;
+        if (of_head || of_tail) {
 #pragma unroll
-            for (int q = 0; q < kCols; ++q) parts[warp][head ? 0 : 1][lane * kCols + q] = f[q];
+            for (int q = 0; q < kCols; ++q) parts[warp][of_head ? 0 : 1][lane * kCols + q] = f[q];
         } else {
-            put_row<G, WHOLE>(a, __shfl_sync(kFull, row, i), c, lane, f);
+            put_row<G, WHOLE>(a, row_at(i), c, lane, f);
         }
 #pragma unroll
         for (int q = 0; q < kCols; ++q) f[q] = 0.0f;
@@ -378,19 +416,19 @@ __global__ void __launch_bounds__(kEmbedThreads) dopt_embed_grad_kernel(const __
         constexpr int kBytes = kCols * int(sizeof(T)), kAhead = kRingBytes / (32 * kBytes);
         const uint32_t ring = uint32_t(__cvta_generic_to_shared(rings[warp] + lane * 16));
         auto fetch = [&](int i) {
-            const int64_t t = __shfl_sync(kFull, token, i < n ? i : 0);
-            const char *from = reinterpret_cast<const char *>(static_cast<const T *>(a.d_out) + t * a.ld + c);
-            if (i < n && c < a.cols)
+            const int64_t t = __shfl_sync(kFull, i < 32 ? token[0] : token[1], i & 31);
+            const char *at = reinterpret_cast<const char *>(static_cast<const T *>(a.d_out) + t * a.ld + c);
+            if (i < to && c < a.cols)
 #pragma unroll
                 for (int k = 0; k < kBytes / 16; ++k)
                     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
                                      ring + uint32_t((i % kAhead) * 32 * kBytes + k * 512)),
-                                 "l"(from + 16 * k)
+                                 "l"(at + 16 * k)
                                  : "memory");
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
-        for (int i = 0; i < kAhead; ++i) fetch(i);
-        for (int i = 0; i < n; ++i) {
+        for (int i = from; i < from + kAhead; ++i) fetch(i);
+        for (int i = from; i < to; ++i) {
             asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
             float g[kCols] = {};
             if (c < a.cols) {
@@ -409,16 +447,17 @@ __global__ void __launch_bounds__(kEmbedThreads) dopt_embed_grad_kernel(const __
     } else {
         using V = Values<T, kCols>;
         constexpr int kAhead = 4;
-        for (int i = 0; i < n; i += kAhead) {
+        for (int i = from; i < to; i += kAhead) {
             typename V::Ahead ahead[kAhead];
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) {
-                const int64_t t = __shfl_sync(kFull, token, min(i + j, n - 1));
-                V::fetch(ahead[j], static_cast<const T *>(a.d_out) + t * a.ld, c, i + j < n ? a.cols : 0, a.vec, lane, 32);
+                const int64_t t = __shfl_sync(kFull, i + j < 32 ? token[0] : token[1], (i + j) & 31);
+                V::fetch(ahead[j], static_cast<const T *>(a.d_out) + (i + j < to ? t * a.ld : 0), c, i + j < to ? a.cols : 0,
+                         a.vec, lane, 32);
             }
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) {
-                if (i + j >= n) break;
+                if (i + j >= to) break;
                 V v;
                 v.take(ahead[j], a.vec, lane, 32);
                 float g[kCols];
@@ -428,13 +467,13 @@ __global__ void __launch_bounds__(kEmbedThreads) dopt_embed_grad_kernel(const __
         }
     }
     __syncthreads();
-    // The rows that reach over warps: each by the warp in which it begins, or by
-    // the first warp if that is in an earlier chunk.
+    // The rows in parts: each by the warp in which it begins, or by the first warp
+    // if that is in an earlier chunk.
     for (int which = 0; which < 2; ++which) {
-        const bool through = from_before && __popc(ends) == 1;  // the warp's tokens are all of one row, of earlier warps
-        if (which == 0 ? !(warp == 0 && from_before) : !(goes_on && !through)) continue;
-        const int of = __shfl_sync(kFull, row, which == 0 ? 0 : n - 1);
-        const int lo = a.first[of], hi = a.first[of + 1];
+        const bool through = head_part && head.x == tail.x;  // the share is all of one row, of earlier warps
+        if (which == 0 ? !(warp == 0 && head_part) : !(tail_part && !through)) continue;
+        const int of = which == 0 ? head_row : tail_row;
+        const int lo = which == 0 ? head.x : tail.x, hi = which == 0 ? head.y : tail.y;
         const int last_warp = min(kWarps - 1, (hi - 1 - base) / a.share);
 #pragma unroll
         for (int q = 0; q < kCols; ++q) f[q] = parts[warp][which][lane * kCols + q];
@@ -474,11 +513,11 @@ __global__ void __launch_bounds__(kEmbedThreads) dopt_embed_grad_kernel(const __
 
 int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
-// Sorted tokens that a warp sums: 32, and fewer where 24 warps an SM would not
+// Sorted tokens that a warp sums: 32, and fewer where 48 warps an SM would not
 // have so many.
 int32_t share_of(int64_t tokens, int64_t pieces) {
     int32_t share = 2;
-    while (share < kMostShare && tokens * pieces > int64_t(share) * 152 * 24) share *= 2;
+    while (share < kMostShare && tokens * pieces > int64_t(share) * 152 * 48) share *= 2;
     return share;
 }
 
@@ -486,14 +525,16 @@ int32_t share_of(int64_t tokens, int64_t pieces) {
 // sorted tokens a warp.
 struct EmbedSpace {
     int64_t first, token, row, list, arrived, partial, bytes, chunks, pieces, part_ld;
-    int32_t share;
+    int32_t share, shift, range;
     EmbedSpace(int64_t tokens, int64_t vocab, int64_t cols) {
         pieces = (cols + kWarpCols - 1) / kWarpCols;
         part_ld = pieces * kWarpCols;
         share = share_of(tokens, pieces);
         chunks = (tokens + kWarps * share - 1) / (kWarps * share);
+        for (shift = kLeastShift; (vocab + (int64_t(1) << shift) - 1) >> shift > kMostRange;) ++shift;
+        range = int32_t((vocab + (int64_t(1) << shift) - 1) >> shift);
         first = 0;
-        token = first + round_up(4 * (vocab + 1), 16);
+        token = first + round_up(4 * ((int64_t(range) << shift) + 1), 16);
         row = token + round_up(4 * tokens, 16);
         list = row + round_up(4 * tokens, 16);
         arrived = list + round_up(8 * tokens, 16);
@@ -506,8 +547,14 @@ struct EmbedSpace {
 int64_t most_space(int64_t tokens, int64_t vocab, int64_t cols) {
     const EmbedSpace s(tokens, vocab, cols);
     const int64_t most = std::max(s.chunks, std::min((tokens + 2 * kWarps - 1) / (2 * kWarps),
-                                                     (152 * 24 + s.pieces * kWarps - 1) / (s.pieces * kWarps) + 1));
+                                                     (152 * 48 + s.pieces * kWarps - 1) / (s.pieces * kWarps) + 1));
     return s.arrived + round_up(4 * most * s.pieces, 16) + 8 * most * s.part_ld;
+}
+
+// Bytes of the sorting kernels' shared memory: counts, and the warps' lists from
+// an 8-byte boundary on.
+constexpr size_t sort_smem(int range) {
+    return size_t(kSortWarps) * (range + (range & 1)) * sizeof(uint32_t) + size_t(kSortWarps) * kListed * sizeof(int2);
 }
 
 std::mutex g_embed_mutex;
@@ -520,7 +567,7 @@ int set_up_sort(const char *who) {
     if (e == cudaSuccess && (device < 0 || device >= 64)) return dopt::fail(DOPT_E_ARG, "%s: device %d", who, device);
     std::lock_guard<std::mutex> lock(g_embed_mutex);
     if (e == cudaSuccess && !g_embed_ready[device]) {
-        constexpr int kMost = int(kSortWarps * kMostRange * sizeof(uint32_t));
+        constexpr int kMost = int(sort_smem(kMostRange));
         e = cudaFuncSetAttribute(dopt_embed_sort_kernel<int32_t>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
         if (e == cudaSuccess)
             e = cudaFuncSetAttribute(dopt_embed_sort_kernel<int64_t>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
@@ -673,9 +720,10 @@ extern "C" int dopt_embed_grad(const void *ids, int32_t id_bytes, int64_t tokens
     a.vec_grad = (address_bits(a.grad) | uint64_t(cols) * gb) % 16 == 0;
     a.accumulate = (flags & DOPT_EMBED_ACCUMULATE) != 0;
     a.scale = scale;
-    a.range = int32_t(std::min<int64_t>(kMostRange, std::max<int64_t>(32, (vocab + 151) / 152)));
-    const size_t smem = size_t(kSortWarps) * a.range * sizeof(uint32_t);
-    a.ranges = int32_t((vocab + a.range - 1) / a.range);
+    a.range = space.range;
+    a.shift = space.shift;
+    a.ranges = 1 << space.shift;
+    const size_t smem = sort_smem(a.range);
     a.grad_bytes = int32_t(gb);
     if (int64_t(a.chunks) * a.pieces > INT32_MAX)
         return fail(DOPT_E_ARG, "%s: %lld tokens of %lld columns are too many for one call", who,
