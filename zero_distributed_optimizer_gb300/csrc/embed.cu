@@ -190,9 +190,10 @@ __device__ __forceinline__ void zero_grads(const EmbedGradArgs &a, int64_t block
 // latencies, so blocks that write the zeros of the rows without tokens run
 // beside it.
 template <typename I>
-__global__ void __launch_bounds__(kSortThreads) dopt_embed_sort_kernel(const __grid_constant__ EmbedGradArgs a) {
+__global__ void __launch_bounds__(kSortThreads, 2) dopt_embed_sort_kernel(const __grid_constant__ EmbedGradArgs a) {
     extern __shared__ uint32_t count[];  // [warps][range], then the warps' lists
     __shared__ uint32_t buffer[32];
+    __shared__ uint32_t first[kMostRange];  // the rows' first places
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t before = (1u << lane) - 1;
     let_dependents_start();
@@ -207,7 +208,7 @@ __global__ void __launch_bounds__(kSortThreads) dopt_embed_sort_kernel(const __g
         a.arrived[i] = 0;
     for (int i = threadIdx.x; i < kSortWarps * a.range; i += kSortThreads) count[i] = 0;
 
-    constexpr int kAhead = 8;
+    constexpr int kAhead = 4;
     int2 *const own_list = reinterpret_cast<int2 *>(count + kSortWarps * a.range + (a.range & 1) * kSortWarps) + warp * kListed;
     const int64_t stretch = ((a.tokens + kSortWarps - 1) / kSortWarps + 31) / 32 * 32;
     const int64_t from = min(a.tokens, warp * stretch), to = min(a.tokens, from + stretch);
@@ -275,11 +276,15 @@ __global__ void __launch_bounds__(kSortThreads) dopt_embed_sort_kernel(const __g
     __syncthreads();
     uint32_t of_row = 0;  // thread r: the tokens of row r
     if (int(threadIdx.x) < a.range && total > 0)
-        for (int w = 0; w < kSortWarps; ++w) {
-            uint32_t *p = count + w * a.range + threadIdx.x;
-            const uint32_t n = *p;
-            *p = of_row;
-            of_row += n;
+        for (int w = 0; w < kSortWarps; w += 8) {
+            uint32_t *p = count + w * a.range + threadIdx.x, n[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) n[k] = p[k * a.range];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                p[k * a.range] = of_row;
+                of_row += n[k];
+            }
         }
     uint32_t upto = of_row;
 #pragma unroll
@@ -291,8 +296,7 @@ __global__ void __launch_bounds__(kSortThreads) dopt_embed_sort_kernel(const __g
     const uint32_t start = base + over_warps(__shfl_sync(kFull, upto, 31), buffer, all) + upto - of_row;
     if (int(threadIdx.x) < a.range) {
         a.first[int64_t(block) * a.range + threadIdx.x] = int(start);
-        if (total > 0)
-            for (int w = 0; w < kSortWarps; ++w) count[w * a.range + threadIdx.x] += start;
+        first[threadIdx.x] = start;
     }
     if (block == a.ranges - 1 && threadIdx.x == 0) a.first[int64_t(a.ranges) * a.range] = int(base + total);
     __syncthreads();
@@ -302,7 +306,7 @@ __global__ void __launch_bounds__(kSortThreads) dopt_embed_sort_kernel(const __g
         const int2 e = next;
         if (i + 32 < end) next = i + 32 + lane < end ? list[i + 32 + lane] : make_int2(0, 0);
         const int row = e.y & 0xffff;
-        const uint32_t at = there ? mine[row] + (e.y >> 16 & 31) : 0;
+        const uint32_t at = there ? first[row] + mine[row] + (e.y >> 16 & 31) : 0;
         __syncwarp();
         if (there) {
             a.token[at] = e.x;
