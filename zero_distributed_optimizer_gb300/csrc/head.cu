@@ -33,7 +33,7 @@ constexpr int kLogitThreads = 32 * (kLogitWarps + 2);
 // gradients in one or two parts of 16 bits, a buffer of 4 KB a part and warp.
 __host__ __device__ constexpr int logit_ring(int planes) { return planes == 2 ? 5 : 6; }
 constexpr int kOutBuffer = 32 * 128;  // 32 tokens x 64 logits of 16 bits
-constexpr int kStoreWarps = 4;
+constexpr int kStoreWarps = 8;  // two to 32 lanes, half of the columns each
 constexpr int kProductThreads = 32 * (kStoreWarps + 2);
 constexpr int kProductRing = 6;
 
@@ -546,39 +546,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps) dopt_head_join_kernel(const _
     a.loss[mine] = target >= 0 && target < a.vocab ? float(lse - double(a.at_target[mine])) : 0.0f;
 }
 
-// fp16 gradients of logits are multiplied by a power of two that brings the
-// largest factor of a row to [2^13, 2^14): a mean's 1 / rows would leave them
-// below fp16's normal range.  factor[1] takes it back.
-struct FactorArgs {
-    const float *d_loss, *d_lse;
-    const void *targets;
-    float *factor;
-    int64_t vocab;
-    int32_t rows, wide;
-};
-__global__ void __launch_bounds__(1024) dopt_head_factor_kernel(const __grid_constant__ FactorArgs a) {
-    __shared__ float tops[32];
-    let_dependents_start();
-    wait_for_grids_before();
-    float top = 0.0f;
-    for (int r = threadIdx.x; r < a.rows; r += 1024) {
-        const int64_t t = a.wide ? static_cast<const int64_t *>(a.targets)[r]
-                                 : int64_t(static_cast<const int32_t *>(a.targets)[r]);
-        const float by_target = t >= 0 && t < a.vocab ? a.d_loss[r] : 0.0f;
-        top = fmaxf(top, fmaxf(fabsf(by_target), fabsf(by_target + (a.d_lse ? a.d_lse[r] : 0.0f))));
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
-    if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = top;
-    __syncthreads();
-    if (threadIdx.x > 0) return;
-    for (int w = 1; w < 32; ++w) top = fmaxf(top, tops[w]);
-    int up = 0;
-    if (top > 0.0f && top <= 3.402823466e38f) up = min(126, 13 - ilogbf(top));
-    a.factor[0] = ldexpf(1.0f, up);
-    a.factor[1] = ldexpf(1.0f, -up);
-}
-
 // ---------------------------------------------------------------------------
 // Products with the logits' gradients
 // ---------------------------------------------------------------------------
@@ -734,8 +701,8 @@ __global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
             }
         }
     } else {
-        const int m_in = int(rank) * (kM / 2) + (warp & 3) * 32 + lane;
-        const uint32_t lanes = tmem + (uint32_t((warp & 3) * 32) << 16);
+        const int m_in = int(rank) * (kM / 2) + (warp & 3) * 32 + lane, half = (warp >> 2) * (kN / 2);
+        const uint32_t lanes = tmem + (uint32_t((warp & 3) * 32) << 16) + uint32_t(half);
         int t = 0;
         uint32_t odd = 0;
         bool ok = true;
@@ -750,11 +717,12 @@ __global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
                 odd ^= 1u << from;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 if (i > 0) {
-                    add_tile(sums, lanes + uint32_t(from * kN), kN);
+                    add_tile(sums, lanes + uint32_t(from * kN), kN / 2);
                     release_sums(b, from, lane);
                 }
             }
-            for (int o = 0; o < kN; o += 16) {
+            for (int o = 0; o < kN / 2; o += 16) {
+                const int n = half + o;
                 uint32_t r[16];
                 float f[16];
 #pragma unroll
@@ -763,11 +731,11 @@ __global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
 #pragma unroll
                 for (int q = 0; q < 16; ++q) f[q] = __uint_as_float(r[q]);
                 if (it.slot >= 0) {
-                    float *p = a.partial + (int64_t(it.slot) * kN + o) * kM + m_in;
+                    float *p = a.partial + (int64_t(it.slot) * kN + n) * kM + m_in;
 #pragma unroll
                     for (int q = 0; q < 16; ++q) p[q * kM] = f[q];
-                } else if (it.n0 + o < a.outs) {
-                    store_any(a, m, it.n0 + o, f);
+                } else if (it.n0 + n < a.outs) {
+                    store_any(a, m, it.n0 + n, f);
                 }
             }
             if (ok) release_sums(b, buffer, lane);
@@ -796,21 +764,67 @@ __global__ void __launch_bounds__(kM) dopt_head_parts_kernel(const __grid_consta
     store_any(a, it.m0 + int(threadIdx.x), it.n0 + o, f);
 }
 
-// Rows that are not 16-byte aligned, into rows that are (`ld`, a multiple of
-// 8; zeros past the columns).
+// What comes before the products, in one launch.  Matrices whose rows are not
+// 16-byte aligned go into rows that are (`ld`, a multiple of 8; zeros past the
+// columns), 16 rows and 256 columns a block.  fp16 gradients of logits are
+// multiplied by a power of two that brings the largest factor of a row to
+// [2^13, 2^14): a mean's 1 / rows would leave them below fp16's normal range;
+// the first block finds it (factor[0]) and what takes it back (factor[1]).
+struct ReadyArgs {
+    const void *from[2];
+    void *to[2];
+    int64_t from_ld[2], rows[2];
+    int64_t blocks[2];  // of each matrix, after the factor's
+    int64_t ld;
+    int32_t cols, across;
+    const float *d_loss, *d_lse;
+    const void *targets;
+    float *factor;      // or NULL
+    int64_t vocab;
+    int32_t wide;
+    int32_t tokens;
+};
+constexpr int kReadyThreads = 512, kReadyRows = kReadyThreads / 32;
+__device__ __forceinline__ void find_factor(const ReadyArgs &a) {
+    __shared__ float tops[kReadyRows];
+    float top = 0.0f;
+    for (int r = threadIdx.x; r < a.tokens; r += kReadyThreads) {
+        const int64_t t = a.wide ? static_cast<const int64_t *>(a.targets)[r]
+                                 : int64_t(static_cast<const int32_t *>(a.targets)[r]);
+        const float by_target = t >= 0 && t < a.vocab ? a.d_loss[r] : 0.0f;
+        top = fmaxf(top, fmaxf(fabsf(by_target), fabsf(by_target + (a.d_lse ? a.d_lse[r] : 0.0f))));
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
+    if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = top;
+    __syncthreads();
+    if (threadIdx.x > 0) return;
+    for (int w = 1; w < kReadyRows; ++w) top = fmaxf(top, tops[w]);
+    int up = 0;
+    if (top > 0.0f && top <= 3.402823466e38f) up = min(126, 13 - ilogbf(top));
+    a.factor[0] = ldexpf(1.0f, up);
+    a.factor[1] = ldexpf(1.0f, -up);
+}
 template <typename T>
-__global__ void __launch_bounds__(256) dopt_head_align_kernel(const T *from, int64_t from_ld, int64_t rows, int cols,
-                                                              T *to, int64_t ld) {
+__global__ void __launch_bounds__(kReadyThreads) dopt_head_ready_kernel(const __grid_constant__ ReadyArgs a) {
     let_dependents_start();
     wait_for_grids_before();
-    const int lane = threadIdx.x, c = int(blockIdx.x * 32 + lane) * 8;
-    for (int64_t r0 = int64_t(blockIdx.y) * 8; r0 < rows; r0 += int64_t(gridDim.y) * 8) {
-        const int64_t r = r0 + threadIdx.y;
-        const bool here = r < rows;
-        Values<T, 8> v;
-        v.load(from + (here ? r * from_ld : 0), c, here ? cols : 0, false, lane, 32);
-        if (here && c < ld) *reinterpret_cast<uint4 *>(to + r * ld + c) = v.raw[0];
+    int64_t block = blockIdx.x;
+    if (a.factor) {
+        if (block == 0) {
+            find_factor(a);
+            return;
+        }
+        --block;
     }
+    const int which = block >= a.blocks[0];
+    if (which) block -= a.blocks[0];
+    const int lane = threadIdx.x & 31, c = int(block % a.across * 32 + lane) * 8;
+    const int64_t r = block / a.across * kReadyRows + (threadIdx.x >> 5);
+    if (r >= a.rows[which]) return;  // (a warp's rows are one)
+    Values<T, 8> v;
+    v.load(static_cast<const T *>(a.from[which]) + r * a.from_ld[which], c, a.cols, false, lane, 32);
+    if (c < a.ld) *reinterpret_cast<uint4 *>(static_cast<T *>(a.to[which]) + r * a.ld + c) = v.raw[0];
 }
 
 // ---------------------------------------------------------------------------
@@ -971,32 +985,27 @@ int check_head(const char *who, const void *x, dopt_dtype dtype, int64_t rows, i
 // (a tensor map's stride is below 2^40 bytes)
 bool by_tma(const void *p, int64_t ld) { return aligned_to(p, 16) && ld % 8 == 0 && ld < (int64_t(1) << 38); }
 
-template <typename T>
-int align_rows(const char *who, const void *from, int64_t from_ld, int64_t rows, int64_t cols, void *to, int64_t ld,
-               cudaStream_t stream) {
-    const dim3 grid(unsigned((ld + 255) / 256), unsigned(std::min<int64_t>((rows + 7) / 8, 16384)));
-    return launch_op(who, dopt_head_align_kernel<T>, grid, dim3(32, 8), 0, stream, static_cast<const T *>(from), from_ld,
-                     rows, int(cols), static_cast<T *>(to), ld);
-}
-
 // x and the output matrix as the kernels read them.
 struct Operands {
     const void *x, *w;
     int64_t ld_x, ld_w;
 };
 template <typename T>
-int make_operands(const char *who, Operands &o, const HeadSpace &space, char *ws, int64_t rows, int64_t width,
-                  int64_t vocab, cudaStream_t stream) {
-    int rc = DOPT_OK;
-    if (!by_tma(o.x, o.ld_x)) {
-        rc = align_rows<T>(who, o.x, o.ld_x, rows, width, ws + space.x_copy, space.copy_ld, stream);
-        o.x = ws + space.x_copy, o.ld_x = space.copy_ld;
-    }
-    if (rc == DOPT_OK && !by_tma(o.w, o.ld_w)) {
-        rc = align_rows<T>(who, o.w, o.ld_w, vocab, width, ws + space.w_copy, space.copy_ld, stream);
-        o.w = ws + space.w_copy, o.ld_w = space.copy_ld;
-    }
-    return rc;
+int make_ready(const char *who, Operands &o, const HeadSpace &space, char *ws, int64_t rows, int64_t width,
+               int64_t vocab, ReadyArgs a, cudaStream_t stream) {
+    const bool copy[2] = {!by_tma(o.x, o.ld_x), !by_tma(o.w, o.ld_w)};
+    if (!copy[0] && !copy[1] && !a.factor) return DOPT_OK;
+    a.ld = space.copy_ld;
+    a.cols = int32_t(width);
+    a.across = int32_t((a.ld + 255) / 256);
+    a.from[0] = o.x, a.from_ld[0] = o.ld_x, a.rows[0] = rows, a.to[0] = ws + space.x_copy;
+    a.from[1] = o.w, a.from_ld[1] = o.ld_w, a.rows[1] = vocab, a.to[1] = ws + space.w_copy;
+    for (int i = 0; i < 2; ++i) a.blocks[i] = copy[i] ? (a.rows[i] + kReadyRows - 1) / kReadyRows * a.across : 0;
+    if (copy[0]) o.x = a.to[0], o.ld_x = a.ld;
+    if (copy[1]) o.w = a.to[1], o.ld_w = a.ld;
+    const int64_t blocks = a.blocks[0] + a.blocks[1] + (a.factor ? 1 : 0);
+    if (blocks > INT32_MAX) return dopt::fail(DOPT_E_ARG, "%s: the matrices are too large to be copied", who);
+    return launch_op(who, dopt_head_ready_kernel<T>, dim3(unsigned(blocks)), dim3(kReadyThreads), 0, stream, a);
 }
 
 // Rows of x in a box: of few tokens, no more than there are.  The rest of the
@@ -1049,16 +1058,19 @@ struct GradCall {
 template <typename T>
 int run_grad(const char *who, const GradCall &c, Operands o, const HeadSpace &space, const GradSpace &g, char *ws,
              EncodeTiled encode, int pairs, cudaStream_t stream) {
-    int rc = make_operands<T>(who, o, space, ws, c.rows, c.width, c.vocab, stream);
-    if (rc != DOPT_OK) return rc;
     char *rest = ws + space.rest;
     float *factor = reinterpret_cast<float *>(rest + g.factor), *sums = reinterpret_cast<float *>(rest + g.sums);
     const int64_t plane = up_to(c.rows * g.piece_ld * 2, 256);
-    if (c.dtype == DOPT_FP16) {
-        FactorArgs f{c.d_loss, c.d_lse, c.targets, factor, c.vocab, int32_t(c.rows), c.target_bytes == 8};
-        rc = launch_op(who, dopt_head_factor_kernel, dim3(1), dim3(1024), 0, stream, f);
-        if (rc != DOPT_OK) return rc;
-    }
+    ReadyArgs ready{};
+    ready.d_loss = c.d_loss;
+    ready.d_lse = c.d_lse;
+    ready.targets = c.targets;
+    ready.factor = c.dtype == DOPT_FP16 ? factor : nullptr;
+    ready.vocab = c.vocab;
+    ready.wide = c.target_bytes == 8;
+    ready.tokens = int32_t(c.rows);
+    int rc = make_ready<T>(who, o, space, ws, c.rows, c.width, c.vocab, ready, stream);
+    if (rc != DOPT_OK) return rc;
     for (int64_t v0 = 0; v0 < c.vocab; v0 += g.piece) {
         const int64_t cols = std::min(g.piece, c.vocab - v0);
         const char *w = static_cast<const char *>(o.w) + v0 * o.ld_w * 2;
@@ -1175,8 +1187,8 @@ extern "C" int dopt_head_loss(const void *x, dopt_dtype dtype, int64_t rows, int
     if (!fill_tiles(a, rows, width, vocab)) return fail(DOPT_E_ARG, "%s: too many tiles", who);
     char *ws = static_cast<char *>(workspace), *rest = ws + space.rest;
     Operands o{x, weight, ld_x, ld_w};
-    rc = dtype == DOPT_BF16 ? make_operands<__nv_bfloat16>(who, o, space, ws, rows, width, vocab, stream)
-                            : make_operands<__half>(who, o, space, ws, rows, width, vocab, stream);
+    rc = dtype == DOPT_BF16 ? make_ready<__nv_bfloat16>(who, o, space, ws, rows, width, vocab, ReadyArgs{}, stream)
+                            : make_ready<__half>(who, o, space, ws, rows, width, vocab, ReadyArgs{}, stream);
     if (rc == DOPT_OK) rc = make_map(who, encode, &a.x_map, dtype, o.x, width, rows, o.ld_x, 64, x_box_rows(rows));
     if (rc == DOPT_OK) rc = make_map(who, encode, &a.w_map, dtype, o.w, width, vocab, o.ld_w, 64, 128);
     if (rc != DOPT_OK) return rc;

@@ -79,10 +79,10 @@ __global__ void __launch_bounds__(kMostRow) dopt_norm_kernel(const __grid_consta
 template <typename T, int NV, bool LAYER>
 __global__ void __launch_bounds__(NV == 4 ? kMostRow : 256, NV == 1 ? 4 : NV == 2 ? 2 : 1)
     dopt_norm_whole_kernel(const __grid_constant__ NormArgs a) {
-    __shared__ LaneSums sums[8];
+    __shared__ RowSums sums[8];
     let_dependents_start();
     wait_for_grids_before();
-    LaneSums &s = sums[threadIdx.y];
+    RowSums &s = sums[threadIdx.y];
     int turn = 0;
     const float per_col = 1.0f / float(a.cols);
     int col[NV];

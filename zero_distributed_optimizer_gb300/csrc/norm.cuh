@@ -31,31 +31,49 @@ struct NormArgs {
 // Sums over a row, by the threads (threadIdx.x) of its group (threadIdx.y)
 // ---------------------------------------------------------------------------
 
+// f becomes the sums over the row's threads with few shuffles: in a warp, the
+// values are first shared out over the lanes (a lane keeps the half of its
+// values that its number says, and adds the other lane's), then added; the
+// warps' sums, up to 8 a value and lane, are read by one load and added
+// likewise.  Two buffers in turn: a thread that writes one has passed the
+// barrier after the last reads of it.
 struct RowSums {
-    float v[2][kMostRow / 32][kMostSums];
+    float v[2][kMostSums][kMostRow / 32];
 };
-
-// f becomes the sums over the row's threads.  Two buffers in turn: a thread
-// that writes one has passed the barrier after the last reads of it.
 template <int K>
 __device__ __forceinline__ void row_sums(RowSums &s, int &turn, float (&f)[K]) {
+    static_assert(K == 1 || K == 2 || K == 4, "values are shared out by halves");
+    const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    float mine = f[0];
+    if constexpr (K == 4) {
+        const bool up = lane & 16;
+        float a = up ? f[2] : f[0], b = up ? f[3] : f[1];
+        a += __shfl_xor_sync(kFull, up ? f[0] : f[2], 16);
+        b += __shfl_xor_sync(kFull, up ? f[1] : f[3], 16);
+        mine = (lane & 8 ? b : a) + __shfl_xor_sync(kFull, lane & 8 ? a : b, 8);
+    } else if constexpr (K == 2) {
+        mine = (lane & 16 ? f[1] : f[0]) + __shfl_xor_sync(kFull, lane & 16 ? f[0] : f[1], 16);
+    }
+    // value k is now in the lanes from k * (32 / K) on
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1)
+    for (int d = 16 / K; d > 0; d >>= 1) mine += __shfl_xor_sync(kFull, mine, d);
+    if (warps > 1) {
+        float(&v)[kMostSums][kMostRow / 32] = s.v[turn];
+        turn ^= 1;
+        if (lane % (32 / K) == 0) v[lane / (32 / K)][threadIdx.x >> 5] = mine;
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + threadIdx.y), "r"(blockDim.x) : "memory");
+        // lanes 8 k + w: value k of warps w and w + 8
+        const int k = lane >> 3, w = lane & 7;
+        mine = k < K && w < warps ? v[k][w] : 0.0f;
+        if (warps > 8 && k < K && w + 8 < warps) mine += v[k][w + 8];
 #pragma unroll
-        for (int k = 0; k < K; ++k) f[k] += __shfl_xor_sync(kFull, f[k], d);
-    const int warps = blockDim.x >> 5;
-    if (warps == 1) return;
-    float(&v)[kMostRow / 32][kMostSums] = s.v[turn];
-    turn ^= 1;
-    if ((threadIdx.x & 31) == 0)
+        for (int d = 4; d > 0; d >>= 1) mine += __shfl_xor_sync(kFull, mine, d);
 #pragma unroll
-        for (int k = 0; k < K; ++k) v[threadIdx.x >> 5][k] = f[k];
-    asm volatile("bar.sync %0, %1;" ::"r"(1 + threadIdx.y), "r"(blockDim.x) : "memory");
+        for (int i = 0; i < K; ++i) f[i] = __shfl_sync(kFull, mine, 8 * i);
+    } else {
 #pragma unroll
-    for (int k = 0; k < K; ++k) f[k] = 0.0f;
-    for (int w = 0; w < warps; ++w)
-#pragma unroll
-        for (int k = 0; k < K; ++k) f[k] += v[w][k];
+        for (int i = 0; i < K; ++i) f[i] = __shfl_sync(kFull, mine, i * (32 / K));
+    }
 }
 
 // All threads of a row have read what they will (rows that are not aligned are
@@ -131,50 +149,6 @@ __device__ __forceinline__ void standard(RowSums &s, int &turn, const float (&f)
 // ---------------------------------------------------------------------------
 // Rows and params that are 16-byte aligned, of a multiple of 8 columns
 // ---------------------------------------------------------------------------
-
-// f becomes the sums over the row's threads, with few shuffles: in a warp, the
-// values are first shared out over the lanes (a lane keeps the half of its
-// values that its number says, and adds the other lane's), then added; the
-// warps' sums, up to 8 a value and lane, are read by one load and added
-// likewise.
-struct LaneSums {
-    float v[2][kMostSums][kMostRow / 32];
-};
-template <int K>
-__device__ __forceinline__ void row_sums(LaneSums &s, int &turn, float (&f)[K]) {
-    static_assert(K == 1 || K == 2 || K == 4, "values are shared out by halves");
-    const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-    float mine = f[0];
-    if constexpr (K == 4) {
-        const bool up = lane & 16;
-        float a = up ? f[2] : f[0], b = up ? f[3] : f[1];
-        a += __shfl_xor_sync(kFull, up ? f[0] : f[2], 16);
-        b += __shfl_xor_sync(kFull, up ? f[1] : f[3], 16);
-        mine = (lane & 8 ? b : a) + __shfl_xor_sync(kFull, lane & 8 ? a : b, 8);
-    } else if constexpr (K == 2) {
-        mine = (lane & 16 ? f[1] : f[0]) + __shfl_xor_sync(kFull, lane & 16 ? f[0] : f[1], 16);
-    }
-    // value k is now in the lanes from k * (32 / K) on
-#pragma unroll
-    for (int d = 16 / K; d > 0; d >>= 1) mine += __shfl_xor_sync(kFull, mine, d);
-    if (warps > 1) {
-        float(&v)[kMostSums][kMostRow / 32] = s.v[turn];
-        turn ^= 1;
-        if (lane % (32 / K) == 0) v[lane / (32 / K)][threadIdx.x >> 5] = mine;
-        asm volatile("bar.sync %0, %1;" ::"r"(1 + threadIdx.y), "r"(blockDim.x) : "memory");
-        // lanes 8 k + w: value k of warps w and w + 8
-        const int k = lane >> 3, w = lane & 7;
-        mine = k < K && w < warps ? v[k][w] : 0.0f;
-        if (warps > 8 && k < K && w + 8 < warps) mine += v[k][w + 8];
-#pragma unroll
-        for (int d = 4; d > 0; d >>= 1) mine += __shfl_xor_sync(kFull, mine, d);
-#pragma unroll
-        for (int i = 0; i < K; ++i) f[i] = __shfl_sync(kFull, mine, 8 * i);
-    } else {
-#pragma unroll
-        for (int i = 0; i < K; ++i) f[i] = __shfl_sync(kFull, mine, i * (32 / K));
-    }
-}
 
 // 8 values of a thread, as pairs.
 constexpr int kPairs = kCols / 2;

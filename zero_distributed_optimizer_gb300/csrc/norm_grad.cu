@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(kMostRow) dopt_norm_grad_kernel(const __grid_c
         const float by = a.row_gate ? a.scale * a.row_gate[r] : a.scale;
         float mean = 0.0f, factor = 1.0f;
         if (a.post) standard<NV, LAYER>(s, turn, u, a.cols, a.eps, mean, factor);
-        float dot[3] = {0.0f, 0.0f, 0.0f};
+        float dot[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = column(i);
@@ -137,10 +137,10 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : kMostRow, NV == 1 ? 2 : 1)
     dopt_norm_grad_whole_kernel(const __grid_constant__ NormArgs a) {
     constexpr int kSums = LAYER ? 4 : 2;
     constexpr int kPost = LAYER ? 2 : 1;
-    __shared__ LaneSums sums[8];
+    __shared__ RowSums sums[8];
     let_dependents_start();
     wait_for_grids_before();
-    LaneSums &s = sums[threadIdx.y];
+    RowSums &s = sums[threadIdx.y];
     int turn = 0;
     const float per_col = 1.0f / float(a.cols);
     int col[NV];

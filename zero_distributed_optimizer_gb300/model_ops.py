@@ -12,6 +12,7 @@ buffer.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -124,22 +125,41 @@ class _NormCfg(ctypes.Structure):
                 ("scale", ctypes.c_float)]
 
 
-class _NormParams(ctypes.Structure):
-    _fields_ = [(name, ctypes.c_void_p) for name in
-                ("weight", "bias", "post_weight", "post_bias", "gate", "row_gate")]
+_SixPointers = ctypes.c_void_p * 6  # dopt_norm_params
+_FiveOffsets = ctypes.c_int64 * 5
 
 
-def _norm_setting(kind, post, eps, scale, params, row_gate, dtype, rows, cols, index):
+@functools.lru_cache(maxsize=256)
+def _norm_cfg(kind, post, eps, scale):
+    """The configuration of these values (kept by value: the library only reads it)."""
     code = _KINDS.get(kind)
     if code is None:
         raise _bad(f"unknown norm {kind!r}: one of {', '.join(_KINDS)}")
-    at = [None if p is None else _dense(p, name, dtype, (cols,), index) for name, p in zip(_NORM_PARAMS, params)]
-    at.append(None if row_gate is None else _dense(row_gate, "row_gate", torch.float32, (rows,), index))
-    return _NormCfg(code, 1 if post else 0, eps, scale), _NormParams(*at)
+    return _NormCfg(code, post, eps, scale)
+
+
+@functools.lru_cache(maxsize=256)
+def _norm_offsets(offsets):
+    """The places of the params' gradients, -1 for none, from (name, place) pairs."""
+    at = dict(offsets)
+    found = [at.pop(name, -1) for name in _NORM_PARAMS]
+    if at:
+        raise _bad(f"no such params: {', '.join(map(str, at))} (of {', '.join(_NORM_PARAMS)})")
+    return _FiveOffsets(*found)
+
+
+def _norm_params(params, row_gate, dtype, shape, index):
+    cols = (shape[1],)
+    at = [None if p is None else _dense(p, name, dtype, cols, index) for name, p in zip(_NORM_PARAMS, params)]
+    return _SixPointers(*at, None if row_gate is None else _dense(row_gate, "row_gate", torch.float32, shape[:1], index))
 
 
 def _matrix(t, name, dtype, shape, index):
-    return (None, shape[1]) if t is None else _rows(t, name, dtype, shape, index)
+    if t is None:
+        return None, shape[1]
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == index:
+        return t.data_ptr(), shape[1]
+    return _rows(t, name, dtype, shape, index)
 
 
 def dopt_norm(kind: str, x, n, weight=None, bias=None, y=None, h=None, post: bool = False, post_weight=None,
@@ -155,12 +175,11 @@ def dopt_norm(kind: str, x, n, weight=None, bias=None, y=None, h=None, post: boo
     index = _cuda_index(x, "x")
     if x.dim() != 2:
         raise _bad("x must be [rows, cols]")
-    dt, shape = x.dtype, tuple(x.shape)
-    cfg, params = _norm_setting(kind, post, eps, scale, (weight, bias, post_weight, post_bias, gate), row_gate, dt,
-                                *shape, index)
-    _call(index, stream, lib().dopt_norm, ctypes.byref(cfg), ctypes.byref(params), _dtype_code(dt, "x"), *shape,
-          *_rows(x, "x", dt, shape, index), *_matrix(y, "y", dt, shape, index), *_matrix(h, "h", dt, shape, index),
-          *_matrix(n, "n", dt, shape, index))
+    dt, shape = x.dtype, x.shape
+    _call(index, stream, lib().dopt_norm, ctypes.byref(_norm_cfg(kind, 1 if post else 0, eps, scale)),
+          _norm_params((weight, bias, post_weight, post_bias, gate), row_gate, dt, shape, index), _dtype_code(dt, "x"),
+          *shape, *_matrix(x, "x", dt, shape, index), *_matrix(y, "y", dt, shape, index),
+          *_matrix(h, "h", dt, shape, index), *_matrix(n, "n", dt, shape, index))
 
 
 def norm_workspace(rows: int, cols: int, device=None):
@@ -188,20 +207,16 @@ def dopt_norm_grad(kind: str, h, d_n, d_x, weight=None, y=None, d_y=None, d_h=No
     index = _cuda_index(h, "h")
     if h.dim() != 2:
         raise _bad("h must be [rows, cols]")
-    dt, shape = h.dtype, tuple(h.shape)
-    offsets = dict(grad_offsets or {})
-    at = [offsets.pop(name, -1) for name in _NORM_PARAMS]
-    if offsets:
-        raise _bad(f"no such params: {', '.join(map(str, offsets))} (of {', '.join(_NORM_PARAMS)})")
-    cfg, params = _norm_setting(kind, post, eps, scale, (weight, None, post_weight, post_bias, gate), row_gate, dt,
-                                *shape, index)
+    dt, shape = h.dtype, h.shape
+    at = _norm_offsets(tuple(grad_offsets.items()) if grad_offsets else ())
     gp, code, numel = (None, 0, 0) if grad is None else _flat(grad, index)
     wp, wn = _workspace(workspace, index)
-    rp = None if d_row_gate is None else _dense(d_row_gate, "d_row_gate", torch.float32, (shape[0],), index)
-    _call(index, stream, lib().dopt_norm_grad, ctypes.byref(cfg), ctypes.byref(params), _dtype_code(dt, "h"), *shape,
-          *_rows(h, "h", dt, shape, index), *_matrix(y, "y", dt, shape, index), *_matrix(d_n, "d_n", dt, shape, index),
-          *_matrix(d_h, "d_h", dt, shape, index), *_matrix(d_x, "d_x", dt, shape, index),
-          *_matrix(d_y, "d_y", dt, shape, index), rp, gp, code, numel, (ctypes.c_int64 * 5)(*at),
+    rp = None if d_row_gate is None else _dense(d_row_gate, "d_row_gate", torch.float32, shape[:1], index)
+    _call(index, stream, lib().dopt_norm_grad, ctypes.byref(_norm_cfg(kind, 1 if post else 0, eps, scale)),
+          _norm_params((weight, None, post_weight, post_bias, gate), row_gate, dt, shape, index), _dtype_code(dt, "h"),
+          *shape, *_matrix(h, "h", dt, shape, index), *_matrix(y, "y", dt, shape, index),
+          *_matrix(d_n, "d_n", dt, shape, index), *_matrix(d_h, "d_h", dt, shape, index),
+          *_matrix(d_x, "d_x", dt, shape, index), *_matrix(d_y, "d_y", dt, shape, index), rp, gp, code, numel, at,
           DOPT_NORM_ACCUMULATE if accumulate else 0, wp, wn)
 
 
