@@ -1045,10 +1045,11 @@ int dopt_head_loss_workspace(int64_t rows, int64_t width, int64_t vocab, int32_t
  *     grad[grad_offset + v * width + c] (+)= sum over t of d[t][v] * x[t][c]
  * where a target outside [0, vocab) makes d_loss[t] count as 0.  The vocabulary
  * goes in pieces: the logits of one are computed again and their gradients d
- * kept in the workspace for the two products.  d is rounded to x's type (with
- * fp16, multiplied by a power of two that keeps the largest in range), which
- * the 16-bit results round at least as much; for fp32 grads what that rounding
- * leaves is multiplied too, so that d counts with twice the bits.  Sums are
+ * kept in the workspace for the two products.  d over the largest d_loss (so
+ * that equal weights are ones; with fp16 times 2^13, so that it stays in range)
+ * is rounded to x's type, about as much as the 16-bit results are; for fp32
+ * grads what that rounding leaves is multiplied too, so that d counts with twice
+ * the bits.  Sums are
  * fp32 (of at most 1024 products, 512 with fp16, on the tensor cores for fp32
  * grads), in an order that depends on the sizes alone, and each result is
  * rounded once (after adding the old grad, with DOPT_HEAD_ACCUMULATE).

@@ -238,7 +238,7 @@ struct LogitArgs {
     CUtensorMap d_map[2];       // gradients: their 16 bits, and what those leave (fp32 grads)
     const void *targets;
     const float *lse, *d_loss, *d_lse;
-    const float *factor;        // fp16 gradients: what they are multiplied by
+    const float *factor;        // gradients: what they are multiplied by
     float2 *partial;            // loss: [2 * tiles_n][rows] (reference, sum), powers of two
     float *at_target;           // loss: [rows] the target's logit
     int64_t first, vocab;       // this launch's first column of the vocabulary; all of them
@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(kLogitThreads, 1) __cluster_dims__(2, 1, 1)
                 by_target = whole >= 0 && whole < a.vocab ? a.d_loss[row] : 0.0f;
                 by_p = by_target + (a.d_lse ? a.d_lse[row] : 0.0f);
                 lse = a.lse[row];
-                if (std::is_same<T, __half>::value) by_p *= a.factor[0], by_target *= a.factor[0];
+                by_p *= a.factor[0], by_target *= a.factor[0];
             }
             if (ok) ok = wait_phase<100>(b, b.sum_full[buffer], uint32_t(t / 2) & 1);
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -766,10 +766,12 @@ __global__ void __launch_bounds__(kM) dopt_head_parts_kernel(const __grid_consta
 
 // What comes before the products, in one launch.  Matrices whose rows are not
 // 16-byte aligned go into rows that are (`ld`, a multiple of 8; zeros past the
-// columns), 16 rows and 256 columns a block.  fp16 gradients of logits are
-// multiplied by a power of two that brings the largest factor of a row to
-// [2^13, 2^14): a mean's 1 / rows would leave them below fp16's normal range;
-// the first block finds it (factor[0]) and what takes it back (factor[1]).
+// columns), 16 rows and 256 columns a block.  The first block finds the factor
+// of the logits' gradients (factor[0]) and what takes it back (factor[1]): one
+// over the largest d_loss, so that a mean's equal weights become ones and a
+// target's -(1 - p) is rounded by what p is, not by what 1 / rows happens to be
+// (the same way in every row: gradients were up to 2^-9 too large or small
+// throughout), and for fp16 times 2^13, to stay in its normal range.
 struct ReadyArgs {
     const void *from[2];
     void *to[2];
@@ -781,29 +783,48 @@ struct ReadyArgs {
     const void *targets;
     float *factor;      // or NULL
     int64_t vocab;
-    int32_t wide;
+    int32_t wide, half;
     int32_t tokens;
 };
 constexpr int kReadyThreads = 512, kReadyRows = kReadyThreads / 32;
 __device__ __forceinline__ void find_factor(const ReadyArgs &a) {
-    __shared__ float tops[kReadyRows];
-    float top = 0.0f;
-    for (int r = threadIdx.x; r < a.tokens; r += kReadyThreads) {
-        const int64_t t = a.wide ? static_cast<const int64_t *>(a.targets)[r]
-                                 : int64_t(static_cast<const int32_t *>(a.targets)[r]);
-        const float by_target = t >= 0 && t < a.vocab ? a.d_loss[r] : 0.0f;
-        top = fmaxf(top, fmaxf(fabsf(by_target), fabsf(by_target + (a.d_lse ? a.d_lse[r] : 0.0f))));
+    __shared__ float tops[2][kReadyRows];
+    constexpr int kAhead = 8;
+    float top = 0.0f, top_p = 0.0f;  // of d_loss, and of d_loss + d_lse
+    for (int r0 = threadIdx.x; r0 < a.tokens; r0 += kAhead * kReadyThreads) {
+        int64_t t[kAhead];
+        float loss[kAhead], lse[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int r = r0 + i * kReadyThreads;
+            const bool there = r < a.tokens;
+            t[i] = !there ? -1 : a.wide ? static_cast<const int64_t *>(a.targets)[r] : int64_t(static_cast<const int32_t *>(a.targets)[r]);
+            loss[i] = there ? a.d_loss[r] : 0.0f;
+            lse[i] = there && a.d_lse ? a.d_lse[r] : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const float by_target = t[i] >= 0 && t[i] < a.vocab ? loss[i] : 0.0f;
+            top = fmaxf(top, fabsf(by_target));
+            top_p = fmaxf(top_p, fabsf(by_target + lse[i]));
+        }
     }
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
-    if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = top;
+    for (int d = 16; d > 0; d >>= 1) {
+        top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
+        top_p = fmaxf(top_p, __shfl_xor_sync(kFull, top_p, d));
+    }
+    if ((threadIdx.x & 31) == 0) tops[0][threadIdx.x >> 5] = top, tops[1][threadIdx.x >> 5] = top_p;
     __syncthreads();
     if (threadIdx.x > 0) return;
-    for (int w = 1; w < kReadyRows; ++w) top = fmaxf(top, tops[w]);
-    int up = 0;
-    if (top > 0.0f && top <= 3.402823466e38f) up = min(126, 13 - ilogbf(top));
-    a.factor[0] = ldexpf(1.0f, up);
-    a.factor[1] = ldexpf(1.0f, -up);
+    for (int w = 1; w < kReadyRows; ++w) top = fmaxf(top, tops[0][w]), top_p = fmaxf(top_p, tops[1][w]);
+    // (a gradient is then at most 5 * 2^13; where d_lse is far larger, twice 2^13)
+    if (!(top_p <= 4.0f * top)) top = top_p;
+    const float most = a.half ? 8192.0f : 1.0f;
+    // (nothing to scale by: zeros, infinities, and what has no normal inverse)
+    const bool fine = top >= 1e-30f && top <= 1e30f;
+    a.factor[0] = fine ? most / top : 1.0f;
+    a.factor[1] = fine ? top / most : 1.0f;
 }
 template <typename T>
 __global__ void __launch_bounds__(kReadyThreads) dopt_head_ready_kernel(const __grid_constant__ ReadyArgs a) {
@@ -1065,7 +1086,8 @@ int run_grad(const char *who, const GradCall &c, Operands o, const HeadSpace &sp
     ready.d_loss = c.d_loss;
     ready.d_lse = c.d_lse;
     ready.targets = c.targets;
-    ready.factor = c.dtype == DOPT_FP16 ? factor : nullptr;
+    ready.factor = factor;
+    ready.half = c.dtype == DOPT_FP16;
     ready.vocab = c.vocab;
     ready.wide = c.target_bytes == 8;
     ready.tokens = int32_t(c.rows);
@@ -1106,7 +1128,7 @@ int run_grad(const char *who, const GradCall &c, Operands o, const HeadSpace &sp
             p.out = last ? c.d_x : sums;
             p.ld = last ? c.ld_d_x : c.width;
             p.add = v0 > 0 ? sums : nullptr;
-            p.back = last && c.dtype == DOPT_FP16 ? factor + 1 : nullptr;
+            p.back = last ? factor + 1 : nullptr;
             p.out_dtype = last ? c.dtype : DOPT_FP32;
             p.outs = int32_t(c.rows);
             p.steps = int32_t((cols + kK - 1) / kK);
@@ -1122,7 +1144,7 @@ int run_grad(const char *who, const GradCall &c, Operands o, const HeadSpace &sp
             p.out = c.grad + v0 * c.width * int64_t(elem_bytes(c.grad_dtype));
             p.ld = c.width;
             p.add = nullptr;
-            p.back = c.dtype == DOPT_FP16 ? factor + 1 : nullptr;
+            p.back = factor + 1;
             p.out_dtype = c.grad_dtype;
             p.outs = int32_t(cols);
             p.steps = int32_t((c.rows + kK - 1) / kK);
