@@ -243,7 +243,7 @@ struct LogitArgs {
     float *at_target;           // loss: [rows] the target's logit
     int64_t first, vocab;       // this launch's first column of the vocabulary; all of them
     int32_t rows, cols;         // tokens, columns of this launch
-    int32_t steps, tiles_m, tiles_n, items;
+    int32_t steps, chunk, tiles_m, tiles_n, items;  // chunk: steps of one sum
     int32_t group;              // blocks of tokens that go through the vocabulary together
     int32_t x_ctas, step_bytes; // CTAs of a pair that have tokens; bytes of a pair's step
     int32_t wide;
@@ -271,21 +271,6 @@ __device__ __forceinline__ float exp2_of(float x) {
     return y;
 }
 constexpr float kLog2e = 1.44269504088896340736f;
-
-// 32 lanes x 32 columns of sums.
-struct Sums32 {
-    uint32_t lo[16], hi[16];
-    __device__ __forceinline__ void load(uint32_t at) {
-        load_sums(at, lo);
-        load_sums(at + 16, hi);
-    }
-    __device__ __forceinline__ void get(float (&f)[32]) {
-        wait_sums(lo);
-        wait_sums(hi);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(lo[i]), f[16 + i] = __uint_as_float(hi[i]);
-    }
-};
 
 // A token's part of a tile: (c, s) with sum of exp(logit) = 2^c * s.
 struct Running {
@@ -370,23 +355,29 @@ __global__ void __launch_bounds__(kLogitThreads, 1) __cluster_dims__(2, 1, 1)
             const uint64_t first = k_descriptor(smem_of(smem));
             int n = 0, t = 0;
             bool ok = true;
-            for (int item = pair; ok && item < a.items; item += pairs, ++t) {
-                if (products_withheld(t)) break;
-                const int buffer = t & 1;
-                if (t >= 2) ok = wait_phase(b, b.sum_empty[buffer], uint32_t(t / 2 - 1) & 1);
-                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                const uint32_t sums = base + uint32_t(buffer * kN);
-                for (int i = 0; i < a.steps && ok; ++i, ++n) {
+            for (int item = pair, round = 0; ok && item < a.items; item += pairs, ++round) {
+                if (products_withheld(round)) break;
+                int left = 0, buffer = 0;  // steps left of the sum
+                for (int i = 0; i < a.steps && ok; ++i, ++n, --left) {
+                    const bool fresh = left == 0;
+                    if (fresh) {
+                        buffer = t & 1;
+                        if (t >= 2) ok = wait_phase(b, b.sum_empty[buffer], uint32_t(t / 2 - 1) & 1);
+                        ++t;
+                        left = min(a.chunk, a.steps - i);
+                        if (!ok) break;
+                    }
                     const int s = n % kRing;
                     ok = wait_phase(b, b.full[s], uint32_t(n / kRing) & 1);
                     if (!ok) break;
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                    const uint32_t sums = base + uint32_t(buffer * kN);
                     const uint64_t da = first + uint64_t(s * (kStage >> 4)), db = da + (kOperand >> 4);
                     if (elect_one()) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) product(sums, da + 2 * k, db + 2 * k, kIdesc, i > 0 || k > 0);
+                        for (int k = 0; k < 4; ++k) product(sums, da + 2 * k, db + 2 * k, kIdesc, !fresh || k > 0);
                         commit(b.empty[s]);
-                        if (i == a.steps - 1) commit(b.sum_full[buffer]);
+                        if (left == 1) commit(b.sum_full[buffer]);
                     }
                     __syncwarp();
                 }
@@ -399,9 +390,9 @@ __global__ void __launch_bounds__(kLogitThreads, 1) __cluster_dims__(2, 1, 1)
         unsigned char *out = out_buffers + warp * PLANES * kOutBuffer;
         int t = 0;
         bool ok = true;
-        for (int item = pair; item < a.items; item += pairs, ++t) {
+        for (int item = pair; item < a.items; item += pairs) {
             const Tile tile = tile_of(a, item);
-            const int buffer = t & 1, row0 = tile.m0 + int(rank) * (kM / 2) + (warp & 3) * 32, row = row0 + lane;
+            const int row0 = tile.m0 + int(rank) * (kM / 2) + (warp & 3) * 32, row = row0 + lane;
             const int c0 = tile.n0 + half * 128, there = a.cols - c0;
             const bool mine = row < a.rows;
             const int64_t target = mine ? target_of(a, row) : -1;
@@ -414,20 +405,34 @@ __global__ void __launch_bounds__(kLogitThreads, 1) __cluster_dims__(2, 1, 1)
                 lse = a.lse[row];
                 by_p *= a.factor[0], by_target *= a.factor[0];
             }
-            if (ok) ok = wait_phase<100>(b, b.sum_full[buffer], uint32_t(t / 2) & 1);
-            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            Sums32 next;
-            const uint32_t sums = lanes + uint32_t(buffer * kN);
-            if (ok) next.load(sums);
+            // the logits of 128 columns: their sums' parts, added as they come
+            float all[4][32];
+            for (int i = 0; i < a.steps; i += a.chunk, ++t) {
+                if (ok) ok = wait_phase<100>(b, b.sum_full[t & 1], uint32_t(t / 2) & 1);
+                if (!ok) break;
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                const uint32_t sums = lanes + uint32_t((t & 1) * kN);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t lo[16], hi[16];
+                    load_sums(sums + 32 * k, lo);
+                    load_sums(sums + 32 * k + 16, hi);
+                    wait_sums(lo);
+                    wait_sums(hi);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const float f = __uint_as_float(lo[j]), g = __uint_as_float(hi[j]);
+                        all[k][j] = i == 0 ? f : all[k][j] + f;
+                        all[k][16 + j] = i == 0 ? g : all[k][16 + j] + g;
+                    }
+                }
+                release_sums(b, t & 1, lane);
+            }
             Running running;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                float l[32];
-                if (ok) {
-                    next.get(l);
-                    if (k < 3) next.load(sums + 32 * (k + 1));
-                    else release_sums(b, buffer, lane);
-                } else {
+                float(&l)[32] = all[k];
+                if (!ok) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) l[j] = __uint_as_float(kNanBits);
                 }
@@ -942,8 +947,9 @@ Plan plan_product(int64_t tiles, int64_t steps, int64_t pairs) {
 }
 
 // Steps of one sum: the tensor cores cut off what 24 bits do not hold, always
-// toward zero, so that the error grows with the sum's length.  fp32 results add
-// sums of 1024 k (512 with fp16 factors) up in fp32, rounding to nearest;
+// toward zero, so that the error grows with the sum's length.  Logits and fp32
+// results add sums of 1024 k (512 with fp16 factors) up in fp32, rounding to
+// nearest (lse of width 4096 was 1.7e-6 off in one sum, torch's 6.7e-7);
 // 16-bit results lose less than an eighth of their own rounding in 131072
 // (bf16) or 16384 (fp16).
 int32_t sum_chunk(dopt_dtype factors, dopt_dtype out) {
@@ -1035,12 +1041,13 @@ int make_ready(const char *who, Operands &o, const HeadSpace &space, char *ws, i
 // where these take 31 (24 x 2048 x 32000).
 uint32_t x_box_rows(int64_t rows) { return uint32_t(std::min<int64_t>(kM / 2, up_to(rows, 8))); }
 
-int fill_tiles(LogitArgs &a, int64_t rows, int64_t width, int64_t cols) {
+int fill_tiles(LogitArgs &a, dopt_dtype dtype, int64_t rows, int64_t width, int64_t cols) {
     a.x_ctas = rows > kM / 2 ? 2 : 1;
     a.step_bytes = int32_t(a.x_ctas * x_box_rows(rows) * kK * 2 + 2 * kOperand);
     a.rows = int32_t(rows);
     a.cols = int32_t(cols);
     a.steps = int32_t((width + kK - 1) / kK);
+    a.chunk = sum_chunk(dtype, DOPT_FP32);
     a.tiles_m = int32_t((rows + kM - 1) / kM);
     a.tiles_n = int32_t((cols + kN - 1) / kN);
     // (blocks of tokens whose rows stay in L2 while the vocabulary goes by: 32 MB of them)
@@ -1097,7 +1104,7 @@ int run_grad(const char *who, const GradCall &c, Operands o, const HeadSpace &sp
         const int64_t cols = std::min(g.piece, c.vocab - v0);
         const char *w = static_cast<const char *>(o.w) + v0 * o.ld_w * 2;
         LogitArgs a{};
-        if (!fill_tiles(a, c.rows, c.width, cols)) return dopt::fail(DOPT_E_ARG, "%s: too many tiles", who);
+        if (!fill_tiles(a, c.dtype, c.rows, c.width, cols)) return dopt::fail(DOPT_E_ARG, "%s: too many tiles", who);
         a.targets = c.targets;
         a.lse = c.lse;
         a.d_loss = c.d_loss;
@@ -1206,7 +1213,7 @@ extern "C" int dopt_head_loss(const void *x, dopt_dtype dtype, int64_t rows, int
     int pairs = 0;
     if ((rc = set_up(who, &encode, &pairs)) != DOPT_OK) return rc;
     LogitArgs a{};
-    if (!fill_tiles(a, rows, width, vocab)) return fail(DOPT_E_ARG, "%s: too many tiles", who);
+    if (!fill_tiles(a, dtype, rows, width, vocab)) return fail(DOPT_E_ARG, "%s: too many tiles", who);
     char *ws = static_cast<char *>(workspace), *rest = ws + space.rest;
     Operands o{x, weight, ld_x, ld_w};
     rc = dtype == DOPT_BF16 ? make_ready<__nv_bfloat16>(who, o, space, ws, rows, width, vocab, ReadyArgs{}, stream)
