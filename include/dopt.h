@@ -866,6 +866,9 @@ int dopt_wgrad_wait_test(int32_t items);
  * hold instead of writing them. */
 #define DOPT_EMBED_ACCUMULATE 1u
 
+/* The most tokens of a call (places past the last one stay below 2^31). */
+#define DOPT_EMBED_MAX_TOKENS 2147418112
+
 /*
  * out[t] = scale * table[ids[t]], in fp32 and rounded once (copied bit for bit
  * with scale 1); zeros where ids[t] is outside [0, vocab) (padding, another
@@ -875,8 +878,8 @@ int dopt_wgrad_wait_test(int32_t items);
  *   table  device [vocab][cols], row stride ld_table
  *   ids    device int32 or int64 (id_bytes 4 or 8) [tokens]
  *   out    device [tokens][cols], row stride ld_out, of the table's type
- * tokens < 2^31, 1 <= vocab < 2^31, 1 <= cols <= DOPT_MAX_COLS.  Errors:
- * DOPT_E_ARG, DOPT_E_ALIGN, DOPT_E_CUDA.
+ * tokens <= DOPT_EMBED_MAX_TOKENS, 1 <= vocab < 2^31, 1 <= cols <=
+ * DOPT_MAX_COLS.  Errors: DOPT_E_ARG, DOPT_E_ALIGN, DOPT_E_CUDA.
  */
 int dopt_embed(const void *table, dopt_dtype dtype, int64_t vocab, int64_t cols, int64_t ld_table,
                const void *ids, int32_t id_bytes, int64_t tokens, float scale, void *out,

@@ -222,6 +222,30 @@ def test_long_sums(dtype):
     _check_grad(c, lse, dtype, d_x, grad, None)
 
 
+def test_every_target_ignored():
+    c = Case(100, 72, 300, torch.float16)
+    c.targets.fill_(-1)
+    loss, lse = c.loss()
+    assert not loss.any()
+    assert float((R.f64(lse) - R.head(c.x, c.w, c.targets)[1]).abs().max()) <= float(c.logit_error().max()) + 100 * F
+    d_x, grad = _grad(c, lse, torch.float32)
+    assert not d_x.any() and not grad[3:-5].any()
+    d_x, grad = _grad(c, lse, torch.float32, d_lse=c.d_lse)  # the penalty remains
+    _check_grad(c, lse, torch.float32, d_x, grad, c.d_lse)
+    d_x, grad = _grad(c, lse, torch.float32, d_lse=c.d_lse * 1e6)
+    c.d_lse = c.d_lse * 1e6
+    _check_grad(c, lse, torch.float32, d_x, grad, c.d_lse)
+
+
+def test_penalty_far_larger_than_the_loss():
+    """fp16: what the loss adds to a row's gradient is small beside the penalty, but stays in range."""
+    c = Case(150, 136, 400, torch.float16)
+    _, lse = c.loss()
+    c.d_lse = c.d_lse * 1e4
+    d_x, grad = _grad(c, lse, torch.float32, d_lse=c.d_lse)
+    _check_grad(c, lse, torch.float32, d_x, grad, c.d_lse)
+
+
 def test_no_rows():
     c = Case(0, 64, 300, torch.bfloat16)
     empty = torch.empty(0, device=DEV)

@@ -53,7 +53,7 @@ def test_workspaces_are_enough_for_fewer(lib):
 
 @pytest.mark.parametrize("call,args", [
     ("dopt_embed_workspace", (-1, 5, 8)), ("dopt_embed_workspace", (5, 0, 8)), ("dopt_embed_workspace", (5, 5, 0)),
-    ("dopt_embed_workspace", (2 ** 31, 5, 8)), ("dopt_norm_workspace", (5, 0)), ("dopt_norm_workspace", (5, 16385)),
+    ("dopt_embed_workspace", (2 ** 31 - 2 ** 16 + 1, 5, 8)), ("dopt_norm_workspace", (5, 0)), ("dopt_norm_workspace", (5, 16385)),
     ("dopt_norm_workspace", (-1, 5)), ("dopt_head_loss_workspace", (5, 8, 0, 1)),
     ("dopt_head_loss_workspace", (2 ** 24 + 1, 8, 5, 1)), ("dopt_head_loss_workspace", (5, 0, 5, 1)),
     ("dopt_head_loss_grad_workspace", (5, 8, 5, BF, 0, 1)), ("dopt_head_loss_grad_workspace", (5, 8, 5, 7, 1, 1)),
@@ -85,7 +85,7 @@ def test_embed_refusals(lib, change, code, text):
     (dict(numel=319), B.DOPT_E_ARG, "leave"), (dict(flags=4), B.DOPT_E_ARG, "flags"), (dict(ws=0), B.DOPT_E_ARG, "workspace"),
     (dict(ws_bytes=100), B.DOPT_E_ARG, "workspace of 100 bytes"), (dict(ws=P + 8), B.DOPT_E_ALIGN, "workspace"),
     (dict(grad=P + 2), B.DOPT_E_ALIGN, "grad"), (dict(d_out=P + 1), B.DOPT_E_ALIGN, "d_out"),
-    (dict(tokens=2 ** 31), B.DOPT_E_ARG, "tokens")], ids=str)
+    (dict(tokens=2 ** 31 - 2 ** 16 + 1), B.DOPT_E_ARG, "tokens")], ids=str)
 def test_embed_grad_refusals(lib, change, code, text):
     a = dict(ids=P, id_bytes=4, tokens=4, d_out=P, dtype=BF, cols=32, ld=32, vocab=10, scale=1.0, grad=P, grad_dtype=FP32,
              numel=500, offset=180, flags=0, ws=P, ws_bytes=1 << 20)

@@ -93,6 +93,7 @@ _LAYER_OPS = (
 # The same for the operators of a language model's ends and residual stream.
 _MODEL_OPS = (
     "DOPT_EMBED_ACCUMULATE",
+    "DOPT_EMBED_MAX_TOKENS",
     "DOPT_HEAD_ACCUMULATE",
     "DOPT_HEAD_MAX_ROWS",
     "DOPT_HEAD_MAX_VOCAB",

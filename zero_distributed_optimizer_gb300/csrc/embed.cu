@@ -587,7 +587,7 @@ int set_up_sort(const char *who) {
 int check_ids(const char *who, const void *ids, int32_t id_bytes, int64_t tokens, int64_t vocab, int64_t cols) {
     using dopt::fail;
     if (id_bytes != 4 && id_bytes != 8) return fail(DOPT_E_ARG, "%s: id_bytes %d (4 or 8)", who, id_bytes);
-    if (tokens < 0 || tokens > INT32_MAX || vocab < 1 || vocab > INT32_MAX || cols < 1 || cols > DOPT_MAX_COLS)
+    if (tokens < 0 || tokens > DOPT_EMBED_MAX_TOKENS || vocab < 1 || vocab > INT32_MAX || cols < 1 || cols > DOPT_MAX_COLS)
         return fail(DOPT_E_ARG, "%s: tokens %lld, vocab %lld, cols %lld", who, static_cast<long long>(tokens),
                     static_cast<long long>(vocab), static_cast<long long>(cols));
     if (tokens > 0 && !ids) return fail(DOPT_E_ARG, "%s: ids is NULL", who);
@@ -666,7 +666,7 @@ extern "C" int dopt_embed_workspace(int64_t tokens, int64_t vocab, int64_t cols,
     dopt::clear_error();
     const char *who = "dopt_embed_workspace";
     if (!bytes) return dopt::fail(DOPT_E_ARG, "%s: bytes is NULL", who);
-    if (tokens < 0 || tokens > INT32_MAX || vocab < 1 || vocab > INT32_MAX || cols < 1 || cols > DOPT_MAX_COLS)
+    if (tokens < 0 || tokens > DOPT_EMBED_MAX_TOKENS || vocab < 1 || vocab > INT32_MAX || cols < 1 || cols > DOPT_MAX_COLS)
         return dopt::fail(DOPT_E_ARG, "%s: tokens %lld, vocab %lld, cols %lld", who, static_cast<long long>(tokens),
                           static_cast<long long>(vocab), static_cast<long long>(cols));
     *bytes = most_space(tokens, vocab, cols);

@@ -14,16 +14,19 @@ struct F2 {
     }
 };
 __device__ __forceinline__ F2 operator*(F2 a, F2 b) {
-    asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(a.v) : "l"(b.v));
-    return a;
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
 }
 __device__ __forceinline__ F2 operator+(F2 a, F2 b) {
-    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(a.v) : "l"(b.v));
-    return a;
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
 }
 __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-    asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(a.v) : "l"(b.v), "l"(c.v));
-    return a;
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
 }
 
 }  // namespace

@@ -89,9 +89,11 @@ __global__ void __launch_bounds__(NV == 4 ? kMostRow : 256, NV == 1 ? 4 : NV == 
     bool in[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) col[i] = column(i), in[i] = col[i] < a.cols;
+    Eight<T> x[NV], y[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) x[i].zero(), y[i].zero();
     const int64_t step = int64_t(gridDim.x) * blockDim.y;
     int64_t r = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
-    Eight<T> x[NV], y[NV];
     float row_gate = 1.0f;
     const T *x_at = static_cast<const T *>(a.x) + r * a.ld_x, *y_at = static_cast<const T *>(a.y) + r * a.ld_y;
     const bool with_y = a.y != nullptr;

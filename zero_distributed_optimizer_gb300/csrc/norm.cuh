@@ -173,10 +173,15 @@ template <typename T>
 struct Eight {
     static constexpr int kPieces = kCols * int(sizeof(T)) / 16;
     uint4 raw[kPieces];
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) raw[i] = make_uint4(0, 0, 0, 0);
+    }
+    // (left as they are where they are not there)
     __device__ __forceinline__ void load(const T *p, bool there) {
 #pragma unroll
         for (int i = 0; i < kPieces; ++i)
-            raw[i] = there ? __ldcs(reinterpret_cast<const uint4 *>(p) + i) : make_uint4(0, 0, 0, 0);
+            if (there) raw[i] = __ldcs(reinterpret_cast<const uint4 *>(p) + i);
     }
     __device__ __forceinline__ void get(F2 (&f)[kPairs]) const {
         if constexpr (sizeof(T) == 2) {

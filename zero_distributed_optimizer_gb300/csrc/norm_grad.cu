@@ -150,18 +150,31 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : kMostRow, NV == 1 ? 2 : 1)
     const int64_t step = int64_t(gridDim.x) * blockDim.y;
     int64_t r = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
     Eight<T> raw_h[NV], raw_y[NV], raw_dn[NV], raw_dh[NV];
+    F2 branch[NV][kPairs] = {};  // gate * post_weight
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        raw_h[i].zero(), raw_y[i].zero(), raw_dn[i].zero(), raw_dh[i].zero();
+        F2 w[kPairs] = {}, g[kPairs] = {};
+        param_values<T>(a.post_weight, col[i], in[i], 1.0f, w);
+        param_values<T>(a.gate, col[i], in[i], 1.0f, g);
+#pragma unroll
+        for (int q = 0; q < kPairs; ++q) branch[i][q] = g[q] * w[q];
+    }
     float row_gate = 1.0f;
+    const T *h_at = static_cast<const T *>(a.x) + r * a.ld_x, *y_at = static_cast<const T *>(a.y) + r * a.ld_y;
+    const T *dn_at = static_cast<const T *>(a.d_n) + r * a.ld_d_n, *dh_at = static_cast<const T *>(a.d_h) + r * a.ld_d_h;
     const bool with_n = a.d_n != nullptr, with_y = a.y != nullptr, with_h = a.d_h != nullptr;
     auto fetch = [&](int64_t row) {
         const bool there = row < a.rows;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const bool here = there && in[i];
-            raw_h[i].load(static_cast<const T *>(a.x) + row * a.ld_x + col[i], here && with_n);
-            raw_dn[i].load(static_cast<const T *>(a.d_n) + row * a.ld_d_n + col[i], here && with_n);
-            raw_y[i].load(static_cast<const T *>(a.y) + row * a.ld_y + col[i], here && with_y);
-            raw_dh[i].load(static_cast<const T *>(a.d_h) + row * a.ld_d_h + col[i], here && with_h);
+            raw_h[i].load(h_at + col[i], here && with_n);
+            raw_dn[i].load(dn_at + col[i], here && with_n);
+            raw_y[i].load(y_at + col[i], here && with_y);
+            raw_dh[i].load(dh_at + col[i], here && with_h);
         }
+        h_at += step * a.ld_x, dn_at += step * a.ld_d_n, y_at += step * a.ld_y, dh_at += step * a.ld_d_h;
         if (a.row_gate && there) row_gate = a.row_gate[row];
     };
     F2 acc[kSums][NV][kPairs] = {};
@@ -229,15 +242,14 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : kMostRow, NV == 1 ? 2 : 1)
         F2 dot[3] = {F2(0.0f), F2(0.0f), F2(0.0f)};
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            F2 w[kPairs] = {}, g[kPairs] = {};
-            param_values<T>(a.post_weight, col[i], in[i], 1.0f, w);
-            param_values<T>(a.gate, col[i], in[i], 1.0f, g);
             if (!in[i]) continue;  // (a layer norm's level was taken off the values past the row too)
-            if (a.d_row_gate) {
-                F2 b[kPairs] = {};
+            if (a.d_row_gate) {  // u * gate = hat(y) * branch + post_bias * gate
+                F2 b[kPairs] = {}, g[kPairs] = {};
                 param_values<T>(LAYER ? a.post_bias : nullptr, col[i], in[i], 0.0f, b);
+                param_values<T>(a.gate, col[i], in[i], 1.0f, g);
 #pragma unroll
-                for (int q = 0; q < kPairs; ++q) dot[2] = fma2(dx[i][q] * g[q], fma2(u[i][q] * yf, w[q], b[q]), dot[2]);
+                for (int q = 0; q < kPairs; ++q)
+                    dot[2] = fma2(dx[i][q], fma2(u[i][q] * yf, branch[i][q], b[q] * g[q]), dot[2]);
             }
 #pragma unroll
             for (int q = 0; q < kPairs; ++q) {
@@ -245,7 +257,7 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : kMostRow, NV == 1 ? 2 : 1)
                 const F2 v = dx[i][q] * by2;
                 acc[kPost][i][q] = fma2(v, u[i][q], acc[kPost][i][q]);
                 if constexpr (LAYER) acc[kPost + 1][i][q] = acc[kPost + 1][i][q] + v;
-                dx[i][q] = v * (g[q] * w[q]);  // of hat(y)
+                dx[i][q] = v * branch[i][q];  // of hat(y)
                 dot[0] = fma2(dx[i][q], u[i][q], dot[0]);
                 if constexpr (LAYER) dot[1] = dot[1] + dx[i][q];
             }

@@ -20,6 +20,7 @@ from .binding import _check, lib
 from .layer_ops import _bad, _call, _cuda_index, _dense, _dtype_code, _rows
 
 DOPT_EMBED_ACCUMULATE = 1
+DOPT_EMBED_MAX_TOKENS = 2147418112
 DOPT_NORM_RMS = 0
 DOPT_NORM_LAYER = 1
 DOPT_NORM_MAX_COLS = 16384
