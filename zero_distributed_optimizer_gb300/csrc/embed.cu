@@ -317,6 +317,12 @@ __global__ void __launch_bounds__(kSortThreads, 2) dopt_embed_sort_kernel(const 
     }
 }
 
+__device__ __forceinline__ void add_part(float (&f)[kCols], const float4 *part) {
+    const float4 u = part[0], v = part[1];
+    f[0] += u.x, f[1] += u.y, f[2] += u.z, f[3] += u.w;
+    f[4] += v.x, f[5] += v.y, f[6] += v.z, f[7] += v.w;
+}
+
 // scale * f to a row of the grads.
 template <typename G, bool WHOLE>
 __device__ __forceinline__ void put_row(const EmbedGradArgs &a, int64_t row, int c, int lane, float (&f)[kCols]) {
@@ -327,10 +333,15 @@ __device__ __forceinline__ void put_row(const EmbedGradArgs &a, int64_t row, int
 #pragma unroll
             for (int k = 0; k < kCols / kPer; ++k) {
                 uint4 *at = reinterpret_cast<uint4 *>(p + c) + k;
-                float v[kPer], old[kPer] = {};
-                if (a.accumulate) unpack<G, 16>(*at, old);
+                float v[kPer];
 #pragma unroll
-                for (int q = 0; q < kPer; ++q) v[q] = f[k * kPer + q] * a.scale + old[q];
+                for (int q = 0; q < kPer; ++q) v[q] = f[k * kPer + q] * a.scale;
+                if (a.accumulate) {
+                    float old[kPer];
+                    unpack<G, 16>(*at, old);
+#pragma unroll
+                    for (int q = 0; q < kPer; ++q) v[q] += old[q];
+                }
                 *at = pack<G, 16>(v);
             }
     } else {
@@ -361,7 +372,7 @@ template <typename T, typename G, bool WHOLE>
 __global__ void __launch_bounds__(kEmbedThreads) dopt_embed_grad_kernel(const __grid_constant__ EmbedGradArgs a) {
     let_dependents_start();
     wait_for_grids_before();
-    __shared__ float parts[kWarps][2][kWarpCols];  // of a warp's first row, if it began before; of its last, if it goes on
+    __shared__ float4 parts[kWarps][2][kWarpCols / 4];  // of a warp's first row, if it began before; of its last, if it goes on
     __shared__ __align__(16) unsigned char rings[WHOLE ? kWarps : 1][WHOLE ? kRingBytes : 16];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int chunk = int(blockIdx.x / a.pieces), piece = int(blockIdx.x % a.pieces);
@@ -407,8 +418,8 @@ __global__ void __launch_bounds__(kEmbedThreads) dopt_embed_grad_kernel(const __
         if (!(ends >> i & 1)) return;
         const bool of_head = head_part && (ends & ((uint64_t(1) << i) - 1)) == 0, of_tail = tail_part && i == n - 1;
         if (of_head || of_tail) {
-#pragma unroll
-            for (int q = 0; q < kCols; ++q) parts[warp][of_head ? 0 : 1][lane * kCols + q] = f[q];
+            float4 *const part = parts[warp][of_head ? 0 : 1] + lane * 2;
+            part[0] = make_float4(f[0], f[1], f[2], f[3]), part[1] = make_float4(f[4], f[5], f[6], f[7]);
         } else {
             put_row<G, WHOLE>(a, row_at(i), c, lane, f);
         }
@@ -480,10 +491,9 @@ __global__ void __launch_bounds__(kEmbedThreads) dopt_embed_grad_kernel(const __
         const int lo = which == 0 ? head.x : tail.x, hi = which == 0 ? head.y : tail.y;
         const int last_warp = min(kWarps - 1, (hi - 1 - base) / a.share);
 #pragma unroll
-        for (int q = 0; q < kCols; ++q) f[q] = parts[warp][which][lane * kCols + q];
-        for (int w = warp + 1; w <= last_warp; ++w)
-#pragma unroll
-            for (int q = 0; q < kCols; ++q) f[q] += parts[w][0][lane * kCols + q];
+        for (int q = 0; q < kCols; ++q) f[q] = 0.0f;
+        add_part(f, parts[warp][which] + lane * 2);
+        for (int w = warp + 1; w <= last_warp; ++w) add_part(f, parts[w][0] + lane * 2);
         const int first_chunk = lo / per_chunk, last_chunk = (hi - 1) / per_chunk;
         if (first_chunk != last_chunk) {
             // a chunk's slot 0: the row that began before it; slot 1: the one that goes on after it
@@ -502,9 +512,8 @@ __global__ void __launch_bounds__(kEmbedThreads) dopt_embed_grad_kernel(const __
 #pragma unroll 4
             for (int at = first_chunk; at <= last_chunk; ++at) {
                 const float4 *s = reinterpret_cast<const float4 *>(slot(at));
-                const float4 u = __ldcg(s), v = __ldcg(s + 1);
-                f[0] += u.x, f[1] += u.y, f[2] += u.z, f[3] += u.w;
-                f[4] += v.x, f[5] += v.y, f[6] += v.z, f[7] += v.w;
+                const float4 part[2] = {__ldcg(s), __ldcg(s + 1)};
+                add_part(f, part);
             }
         }
         put_row<G, WHOLE>(a, of, c, lane, f);
