@@ -16,6 +16,7 @@ constexpr int kMostRange = 1024;         // rows of the table that one sorting b
 constexpr int kListed = 128;             // of its own tokens that a sorting warp lists in shared memory
 constexpr int kLeastShift = 7;           // at least 128 sorting blocks
 constexpr int kMostShare = 32;           // sorted tokens that a warp sums
+constexpr int kZeroRows = 4;             // rows of the table that a warp looks over for zeros
 constexpr int kRingBytes = 4096;         // of a warp's loads ahead
 
 struct EmbedArgs {
@@ -135,6 +136,7 @@ struct EmbedGradArgs {
     int64_t ld, tokens, vocab, part_ld;
     int32_t cols, pieces;   // pieces: of 256 columns
     int32_t range, ranges, shift;  // ranges = 2^shift
+    int64_t zeroed;                // rows that are zeroed beside the sort
     int32_t share, chunks;  // sorted tokens of a summing warp; blocks of 8 of those
     int32_t vec, vec_grad;  // d_out's, the grads' rows are 16-byte aligned
     int32_t accumulate;
@@ -165,20 +167,19 @@ __device__ __forceinline__ uint32_t over_warps(uint32_t mine, uint32_t *buffer, 
     return __shfl_sync(kFull, sum - v, warp);
 }
 
-// Zeros to all grads, by the blocks that sort nothing: 16 bytes a store, the
-// ends element by element.
-__device__ __forceinline__ void zero_grads(const EmbedGradArgs &a, int64_t block, int64_t blocks) {
-    char *p = static_cast<char *>(a.grad), *end = p + a.vocab * a.cols * a.grad_bytes;
+// Zeros to the bytes from p to `end` (whole elements of 2 bytes), by `threads`
+// threads, of which this is number i: 16 bytes a store, the ends 2 at a time.
+__device__ __forceinline__ void zero_bytes(char *p, char *end, int64_t i, int64_t threads) {
     char *from = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(p) + 15) & ~uintptr_t(15));
     char *to = reinterpret_cast<char *>(reinterpret_cast<uintptr_t>(end) & ~uintptr_t(15));
     if (from > to) from = to = end;  // (fewer than 16 bytes, between two boundaries)
     const int64_t n = (to - from) / 16;
-    for (int64_t i = block * kSortThreads + threadIdx.x; i < n; i += blocks * kSortThreads)
-        reinterpret_cast<uint4 *>(from)[i] = make_uint4(0, 0, 0, 0);
-    if (block == 0) {  // whole elements of 2 bytes
-        for (char *q = p + 2 * threadIdx.x; q < from; q += 2 * kSortThreads) *reinterpret_cast<uint16_t *>(q) = 0;
-        for (char *q = to + 2 * threadIdx.x; q < end; q += 2 * kSortThreads) *reinterpret_cast<uint16_t *>(q) = 0;
-    }
+    for (int64_t k = i; k < n; k += threads) reinterpret_cast<uint4 *>(from)[k] = make_uint4(0, 0, 0, 0);
+    for (char *q = p + 2 * i; q < from; q += 2 * threads) *reinterpret_cast<uint16_t *>(q) = 0;
+    for (char *q = to + 2 * i; q < end; q += 2 * threads) *reinterpret_cast<uint16_t *>(q) = 0;
+}
+__device__ __forceinline__ char *grad_row(const EmbedGradArgs &a, int64_t row) {
+    return static_cast<char *>(a.grad) + row * a.cols * a.grad_bytes;
 }
 
 // The tokens sorted by the key of their row (stable).  A block owns `range`
@@ -187,7 +188,7 @@ __device__ __forceinline__ void zero_grads(const EmbedGradArgs &a, int64_t block
 // list: counts of each (warp, row), their prefixes, places.  A lane's rank
 // among its warp's tokens of one row comes from a ballot per bit of the row
 // and is kept with the token for the second pass.  The sort is bound by
-// latencies, so blocks that write the zeros of the rows without tokens run
+// latencies, so blocks that write zeros to the first rows of the table run
 // beside it.
 template <typename I>
 __global__ void __launch_bounds__(kSortThreads, 2) dopt_embed_sort_kernel(const __grid_constant__ EmbedGradArgs a) {
@@ -199,7 +200,8 @@ __global__ void __launch_bounds__(kSortThreads, 2) dopt_embed_sort_kernel(const 
     let_dependents_start();
     wait_for_grids_before();
     if (int(blockIdx.x) >= a.ranges) {
-        zero_grads(a, blockIdx.x - a.ranges, gridDim.x - a.ranges);
+        zero_bytes(grad_row(a, 0), grad_row(a, a.zeroed), int64_t(blockIdx.x - a.ranges) * kSortThreads + threadIdx.x,
+                   int64_t(gridDim.x - a.ranges) * kSortThreads);
         return;
     }
     const int block = int(blockIdx.x), mask = a.ranges - 1;
@@ -375,6 +377,20 @@ __global__ void __launch_bounds__(kEmbedThreads) dopt_embed_grad_kernel(const __
     __shared__ float4 parts[kWarps][2][kWarpCols / 4];  // of a warp's first row, if it began before; of its last, if it goes on
     __shared__ __align__(16) unsigned char rings[WHOLE ? kWarps : 1][WHOLE ? kRingBytes : 16];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (blockIdx.x >= unsigned(a.chunks) * unsigned(a.pieces)) {
+        // zeros to the rows without tokens among those that the sort has left
+        const int64_t row0 = a.zeroed + (int64_t(blockIdx.x - unsigned(a.chunks) * unsigned(a.pieces)) * kWarps + warp) * kZeroRows;
+        bool empty = false;
+        if (lane < kZeroRows && row0 + lane < a.vocab) {
+            const int64_t key = key_of(a, int(row0 + lane));
+            empty = a.first[key] == a.first[key + 1];
+        }
+        for (uint32_t rest = __ballot_sync(kFull, empty); rest; rest &= rest - 1) {
+            const int64_t row = row0 + __ffs(rest) - 1;
+            zero_bytes(grad_row(a, row), grad_row(a, row + 1), lane, 32);
+        }
+        return;
+    }
     const int chunk = int(blockIdx.x / a.pieces), piece = int(blockIdx.x % a.pieces);
     const int c = piece * kWarpCols + lane * kCols;
     const int per_chunk = kWarps * a.share;
@@ -616,7 +632,8 @@ int launch_embed(const char *who, const EmbedArgs &a, cudaStream_t stream) {
 
 template <typename T, typename G>
 int launch_grad(const char *who, const EmbedGradArgs &a, cudaStream_t stream) {
-    const dim3 grid(unsigned(a.chunks) * unsigned(a.pieces));
+    const int64_t left = a.accumulate ? 0 : a.vocab - a.zeroed;
+    const dim3 grid(unsigned(a.chunks) * unsigned(a.pieces) + unsigned((left + kZeroRows * kWarps - 1) / (kZeroRows * kWarps)));
     return a.vec && a.vec_grad && a.cols % kCols == 0
                ? launch_op(who, dopt_embed_grad_kernel<T, G, true>, grid, dim3(kEmbedThreads), 0, stream, a)
                : launch_op(who, dopt_embed_grad_kernel<T, G, false>, grid, dim3(kEmbedThreads), 0, stream, a);
@@ -738,13 +755,17 @@ extern "C" int dopt_embed_grad(const void *ids, int32_t id_bytes, int64_t tokens
     a.ranges = 1 << space.shift;
     const size_t smem = sort_smem(a.range);
     a.grad_bytes = int32_t(gb);
-    if (int64_t(a.chunks) * a.pieces > INT32_MAX)
+    if (int64_t(a.chunks) * a.pieces + vocab / (kZeroRows * kWarps) + 1 > INT32_MAX)
         return fail(DOPT_E_ARG, "%s: %lld tokens of %lld columns are too many for one call", who,
                     static_cast<long long>(tokens), static_cast<long long>(cols));
     if ((rc = set_up_sort(who)) != DOPT_OK) return rc;
     auto sort = id_bytes == 8 ? dopt_embed_sort_kernel<int64_t> : dopt_embed_sort_kernel<int32_t>;
-    // (64 KB of zeros a block, up to two blocks an SM)
-    const int64_t zero_blocks = a.accumulate ? 0 : std::min<int64_t>(304, (vocab * cols * int64_t(gb) + 65535) / 65536);
+    // Zeros are written beside the sort (64 KB a block, up to two blocks an SM),
+    // which is bound by latencies, and a quarter of them after the sums' blocks,
+    // for the same reason (16384 x 768 into 50257 rows: all beside the sort 28.5
+    // us, three quarters 26.9, half 28.0).
+    a.zeroed = a.accumulate ? 0 : tokens > 0 ? vocab - vocab / 4 : vocab;
+    const int64_t zero_blocks = std::min<int64_t>(304, (a.zeroed * cols * int64_t(gb) + 65535) / 65536);
     rc = launch_op(who, sort, dim3(unsigned(a.ranges + zero_blocks)), dim3(kSortThreads), smem, stream, a);
     if (rc != DOPT_OK || tokens == 0) return rc;
     switch (dtype) {
