@@ -589,40 +589,64 @@ __device__ __forceinline__ Item item_of(const ProductArgs &a, int item) {
     return it;
 }
 
-// 16 sums of one column m, of which n are outputs, to the rows from p on.
-template <typename G>
-__device__ __forceinline__ void store_sums(const ProductArgs &a, G *p, const float *add, int n, const float (&f)[16]) {
-    float v[16];
+// 16 sums of one column, of which `there` are outputs, to the rows from p on;
+// `add`: the sums so far.
+template <typename G, bool ALL>
+__device__ __forceinline__ void store_sums(const ProductArgs &a, G *p, const float *add, int there, float back, float (&v)[16]) {
+    if (add) {
+        float more[16];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) v[j] = add && j < n ? f[j] + add[int64_t(j) * a.cols] : f[j];
-    if (a.back) {
-        const float back = *a.back;
+        for (int j = 0; j < 16; ++j)
+            if (ALL || j < there) more[j] = add[int64_t(j) * a.cols];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] *= back;
+        for (int j = 0; j < 16; ++j)
+            if (ALL || j < there) v[j] += more[j];
     }
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] *= back;
     if (a.accumulate) {
         G old[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j)
-            if (j < n) old[j] = p[j * a.ld];
+            if (ALL || j < there) old[j] = p[j * a.ld];
 #pragma unroll
         for (int j = 0; j < 16; ++j)
-            if (j < n) v[j] += to_f32(old[j]);
+            if (ALL || j < there) v[j] += to_f32(old[j]);
     }
 #pragma unroll
-    for (int j = 0; j < 16; ++j)
-        if (j < n) p[j * a.ld] = from_f32<G>(v[j]);
+    for (int j = 0; j < 16; ++j, p += a.ld)
+        if (ALL || j < there) *p = from_f32<G>(v[j]);
 }
 template <typename G>
-__device__ __forceinline__ void store_column(const ProductArgs &a, int m, int n, const float (&f)[16]) {
-    if (m < a.cols)
-        store_sums(a, static_cast<G *>(a.out) + n * a.ld + m, a.add ? a.add + int64_t(n) * a.cols + m : nullptr,
-                   a.outs - n, f);
+__device__ __forceinline__ void store_column(const ProductArgs &a, int m, int n, float back, float (&v)[16]) {
+    if (m >= a.cols || n >= a.outs) return;
+    G *p = static_cast<G *>(a.out) + n * a.ld + m;
+    const float *add = a.add ? a.add + int64_t(n) * a.cols + m : nullptr;
+    if (a.outs - n >= 16) store_sums<G, true>(a, p, add, 16, back, v);
+    else store_sums<G, false>(a, p, add, a.outs - n, back, v);
 }
-__device__ __forceinline__ void store_any(const ProductArgs &a, int m, int n, const float (&f)[16]) {
-    if (a.out_dtype == DOPT_FP32) store_column<float>(a, m, n, f);
-    else if (a.out_dtype == DOPT_BF16) store_column<__nv_bfloat16>(a, m, n, f);
-    else store_column<__half>(a, m, n, f);
+// A warp's half of a tile's columns, from column n on, at `sums` in tensor
+// memory, 32 at a time; NaN instead where there are none.
+template <typename G>
+__device__ __forceinline__ void store_tile(const ProductArgs &a, int m, int n, float back, uint32_t sums, bool there_are) {
+    for (int o = 0; o < kN / 2; o += 32) {
+        uint32_t r[2][16];
+#pragma unroll
+        for (int q = 0; q < 16; ++q) r[0][q] = r[1][q] = kNanBits;
+        if (there_are) {
+            load_sums(sums + uint32_t(o), r[0]);
+            load_sums(sums + uint32_t(o + 16), r[1]);
+            wait_sums(r[0]);
+            wait_sums(r[1]);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float v[16];
+#pragma unroll
+            for (int q = 0; q < 16; ++q) v[q] = __uint_as_float(r[h][q]);
+            store_column<G>(a, m, n + o + 16 * h, back, v);
+        }
+    }
 }
 
 // B_K: k is contiguous in the logits' gradients (d_x); otherwise n is (d_w).
@@ -708,6 +732,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
     } else {
         const int m_in = int(rank) * (kM / 2) + (warp & 3) * 32 + lane, half = (warp >> 2) * (kN / 2);
         const uint32_t lanes = tmem + (uint32_t((warp & 3) * 32) << 16) + uint32_t(half);
+        const float back = a.back ? *a.back : 1.0f;
         int t = 0;
         uint32_t odd = 0;
         bool ok = true;
@@ -726,22 +751,22 @@ __global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
                     release_sums(b, from, lane);
                 }
             }
-            for (int o = 0; o < kN / 2; o += 16) {
-                const int n = half + o;
-                uint32_t r[16];
-                float f[16];
+            if (it.slot >= 0) {
+                float *p = a.partial + (int64_t(it.slot) * kN + half) * kM + m_in;
+                for (int o = 0; o < kN / 2; o += 16) {
+                    uint32_t r[16];
 #pragma unroll
-                for (int q = 0; q < 16; ++q) r[q] = kNanBits;
-                if (ok) load_sums(sums + uint32_t(o), r), wait_sums(r);
+                    for (int q = 0; q < 16; ++q) r[q] = kNanBits;
+                    if (ok) load_sums(sums + uint32_t(o), r), wait_sums(r);
 #pragma unroll
-                for (int q = 0; q < 16; ++q) f[q] = __uint_as_float(r[q]);
-                if (it.slot >= 0) {
-                    float *p = a.partial + (int64_t(it.slot) * kN + n) * kM + m_in;
-#pragma unroll
-                    for (int q = 0; q < 16; ++q) p[q * kM] = f[q];
-                } else if (it.n0 + n < a.outs) {
-                    store_any(a, m, it.n0 + n, f);
+                    for (int q = 0; q < 16; ++q, p += kM) *p = __uint_as_float(r[q]);
                 }
+            } else if (a.out_dtype == DOPT_FP32) {
+                store_tile<float>(a, m, it.n0 + half, back, sums, ok);
+            } else if (a.out_dtype == DOPT_BF16) {
+                store_tile<__nv_bfloat16>(a, m, it.n0 + half, back, sums, ok);
+            } else {
+                store_tile<__half>(a, m, it.n0 + half, back, sums, ok);
             }
             if (ok) release_sums(b, buffer, lane);
         }
@@ -766,7 +791,11 @@ __global__ void __launch_bounds__(kM) dopt_head_parts_kernel(const __grid_consta
 #pragma unroll
         for (int q = 0; q < 16; ++q) f[q] += v[q];
     }
-    store_any(a, it.m0 + int(threadIdx.x), it.n0 + o, f);
+    const float back = a.back ? *a.back : 1.0f;
+    const int m = it.m0 + int(threadIdx.x);
+    if (a.out_dtype == DOPT_FP32) store_column<float>(a, m, it.n0 + o, back, f);
+    else if (a.out_dtype == DOPT_BF16) store_column<__nv_bfloat16>(a, m, it.n0 + o, back, f);
+    else store_column<__half>(a, m, it.n0 + o, back, f);
 }
 
 // What comes before the products, in one launch.  Matrices whose rows are not
