@@ -954,7 +954,7 @@ int make_map(const char *who, EncodeTiled encode, CUtensorMap *map, dopt_dtype d
 // How a product's tiles go over the pairs: whole waves tile by tile, the last
 // partial wave's tiles split along k.  Chosen for the least estimated time in
 // steps of 64 k: a tile's stores 4 (they run under the next tile's products),
-// the join's launch 12 and a part's trip through memory 0.2.
+// the join's launch 12 and a part's trip through memory 0.5.
 struct Plan {
     int64_t whole, tail;
     int parts;
@@ -966,7 +966,7 @@ Plan plan_product(int64_t tiles, int64_t steps, int64_t pairs) {
     double least = double(steps) + 4;
     for (int parts = 2; parts <= kMostSplit; ++parts) {
         if (steps / parts < 4 || tail * parts > kMostSlots) break;
-        const double t = double((tail * parts + pairs - 1) / pairs) * (double(steps) / parts + 4) + 12 + 0.2 * double(tail * parts);
+        const double t = double((tail * parts + pairs - 1) / pairs) * (double(steps) / parts + 4) + 12 + 0.5 * double(tail * parts);
         if (t < least) {
             least = t;
             best = Plan{tiles - tail, tail, parts};
