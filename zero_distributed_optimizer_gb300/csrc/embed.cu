@@ -1,5 +1,19 @@
 // The token embedding (dopt_embed) and its gradient into the flat grad buffer
 // (dopt_embed_grad); dopt.h states the contracts.
+//
+// The embedding is a copy, bound by memory: a warp takes 256 columns of four
+// tokens, so that four rows' loads are in flight together (16384 tokens of 768
+// bf16 columns: 7.5 us, 6.7 TB/s; rows that are not 16-byte aligned go in
+// shifted pieces, rows.cuh).
+//
+// The gradient sorts the tokens by row and sums each row's tokens in that order,
+// so that it does not depend on which block runs when, and every row of the
+// table is written once (or zeroed and then written).  Two launches: the sort,
+// a block a residue class of rows, bound by latencies (8.7 us for 16384 tokens
+// of 50257 rows), with zeros written beside it; and the sums, bound by the
+// latency of a few dependent loads and, for frequent rows, of joining parts.
+// 16384 tokens x 768 columns into 50257 rows, bf16: 27 us, of which the 77 MB of
+// grads alone take 10; 1001 tokens x 515 columns into 5003 rows, fp32: 13.5 us.
 #include <mutex>
 
 #include "rows.cuh"

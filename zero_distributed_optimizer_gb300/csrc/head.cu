@@ -20,6 +20,15 @@ namespace {
 //   d_x, d_w   M = the width, N = tokens or the vocabulary, K the other one.
 //              Lanes lie along the width, which is contiguous in both results,
 //              so a warp's stores are contiguous whatever the alignment.
+//
+// Long products are bound by the tensor cores (active 96-98 % of the cycles) and
+// then by the card's power: 16384 tokens x 768 x 50257, bf16, loss 618-647 us in
+// short runs (1.96-2.05 PFLOP/s), 708-725 under the power cap (1.75-1.79);
+// gradients 2070-2170 and 2390-2450 us (1.83 and 1.56-1.59 PFLOP/s).  The logits'
+// gradients are stored as they are made, 1.6 GB, which keeps the tensor cores at
+// 83 % there; in pieces that stay in L2 d_x's fp32 sums would move more.  Few
+// tokens are bound by reading the matrix: 24 x 2048 x 32000, loss 32 us (19 at
+// the copy rate), of which 7 are the two launches.
 constexpr int kM = 256, kN = 256, kK = 64;  // of a pair's tile, and of a step
 constexpr int kSlab = 64 * 128;             // 64 rows of 128 bytes
 constexpr int kOperand = 2 * kSlab;         // a CTA's share of one operand in a step
@@ -497,7 +506,9 @@ __global__ void __launch_bounds__(kLogitThreads, 1) __cluster_dims__(2, 1, 1)
 }
 
 // The parts of each row's sum joined: lse, and the loss.  A block: 32 rows, by
-// 32 warps' shares of the parts, eight parts at a time under one reference.
+// WARPS warps' shares of the parts (32 where there are few rows, 8 where there
+// is a block an SM: 16384 rows of 394 parts 21 us instead of 27), eight parts at
+// a time under one reference.
 struct JoinLossArgs {
     const float2 *partial;
     const float *at_target;
@@ -506,7 +517,6 @@ struct JoinLossArgs {
     int64_t vocab;
     int32_t parts, rows, wide;
 };
-constexpr int kJoinWarps = 32;
 template <int N>
 __device__ __forceinline__ void join_sums(float &c, float &s, const float2 (&v)[N]) {
     float top = c;
@@ -518,37 +528,42 @@ __device__ __forceinline__ void join_sums(float &c, float &s, const float2 (&v)[
     for (int i = 0; i < N; ++i) s += v[i].x == top ? v[i].y : v[i].y * exp2_of(v[i].x - top);
     c = top;
 }
-__global__ void __launch_bounds__(32 * kJoinWarps) dopt_head_join_kernel(const __grid_constant__ JoinLossArgs a) {
-    __shared__ float2 part[kJoinWarps][33];
+template <int WARPS>
+__global__ void __launch_bounds__(32 * WARPS) dopt_head_join_kernel(const __grid_constant__ JoinLossArgs a) {
+    __shared__ float2 part[WARPS][33];
     let_dependents_start();
     wait_for_grids_before();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = int(blockIdx.x) * 32 + lane;
     const float2 none = make_float2(-INFINITY, 0.0f);
     float c = -INFINITY, s = 0.0f;
     if (row < a.rows)
-        for (int p = warp; p < a.parts; p += 8 * kJoinWarps) {
+        for (int p = warp; p < a.parts; p += 8 * WARPS) {
             float2 v[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                v[i] = p + i * kJoinWarps < a.parts ? __ldcs(a.partial + int64_t(p + i * kJoinWarps) * a.rows + row) : none;
+                v[i] = p + i * WARPS < a.parts ? __ldcs(a.partial + int64_t(p + i * WARPS) * a.rows + row) : none;
             join_sums(c, s, v);
         }
     part[warp][lane] = make_float2(c, s);
     __syncthreads();
-    // warp w joins row w's: a lane a part, then halves
-    const int mine = int(blockIdx.x) * 32 + warp;
-    c = part[lane][warp].x, s = part[lane][warp].y;
+    // a warp joins rows w, w + WARPS, ...: a lane a part, then halves
+    for (int r = warp; r < 32; r += WARPS) {
+        const int mine = int(blockIdx.x) * 32 + r;
+        if (mine >= a.rows) break;
+        const float2 own = lane < WARPS ? part[lane][r] : none;
+        c = own.x, s = own.y;
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-        const float2 v[1] = {make_float2(__shfl_down_sync(kFull, c, d), __shfl_down_sync(kFull, s, d))};
-        join_sums(c, s, v);
+        for (int d = WARPS / 2; d > 0; d >>= 1) {
+            const float2 v[1] = {make_float2(__shfl_down_sync(kFull, c, d), __shfl_down_sync(kFull, s, d))};
+            join_sums(c, s, v);
+        }
+        if (lane > 0) continue;
+        const double lse = (double(c) + double(log2f(s))) * 0.69314718055994530942;
+        const int64_t target = a.wide ? static_cast<const int64_t *>(a.targets)[mine]
+                                      : int64_t(static_cast<const int32_t *>(a.targets)[mine]);
+        a.lse[mine] = float(lse);
+        a.loss[mine] = target >= 0 && target < a.vocab ? float(lse - double(a.at_target[mine])) : 0.0f;
     }
-    if (lane > 0 || mine >= a.rows) return;
-    const double lse = (double(c) + double(log2f(s))) * 0.69314718055994530942;
-    const int64_t target = a.wide ? static_cast<const int64_t *>(a.targets)[mine]
-                                  : int64_t(static_cast<const int32_t *>(a.targets)[mine]);
-    a.lse[mine] = float(lse);
-    a.loss[mine] = target >= 0 && target < a.vocab ? float(lse - double(a.at_target[mine])) : 0.0f;
 }
 
 // ---------------------------------------------------------------------------
@@ -1261,7 +1276,9 @@ extern "C" int dopt_head_loss(const void *x, dopt_dtype dtype, int64_t rows, int
              : launch_op(who, dopt_head_logit_kernel<__half, 0>, grid, dim3(kLogitThreads), logit_smem(0), stream, a);
     if (rc != DOPT_OK) return rc;
     JoinLossArgs j{a.partial, a.at_target, targets, loss, lse, vocab, 2 * a.tiles_n, a.rows, a.wide};
-    return launch_op(who, dopt_head_join_kernel, dim3(unsigned((rows + 31) / 32)), dim3(32 * kJoinWarps), 0, stream, j);
+    const dim3 blocks(unsigned((rows + 31) / 32));
+    return blocks.x >= 152 ? launch_op(who, dopt_head_join_kernel<8>, blocks, dim3(32 * 8), 0, stream, j)
+                           : launch_op(who, dopt_head_join_kernel<32>, blocks, dim3(32 * 32), 0, stream, j);
 }
 
 extern "C" int dopt_head_loss_grad_workspace(int64_t rows, int64_t width, int64_t vocab, dopt_dtype grad_dtype,

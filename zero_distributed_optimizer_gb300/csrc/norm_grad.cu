@@ -1,5 +1,16 @@
 // The gradients of the norms around a block (dopt_norm_grad); dopt.h states the
 // contract.
+//
+// One pass over the rows, which reads h, y and both gradients once and writes
+// d_x and d_y; a thread keeps the sums over its rows that the params' gradients
+// are made of, and a second launch adds the groups' sums.  Four streams in and
+// two out need few instructions a value: sums of a row that do not wait for one
+// another go together, arithmetic is two columns an instruction.  16384 x 2048
+// bf16 with a norm before and after and a gate: 91 us, 4.4 TB/s, instructions in
+// 60 % of the issue slots at two blocks an SM (three spill: 150 us); 259 us
+// with a row's loads waited for, 143 with the next row's in flight, 100 with
+// few shuffles a sum, 94 with two columns an instruction.  Rows of more than
+// 8192 columns spill registers.
 #include "norm.cuh"
 
 namespace {
