@@ -1046,7 +1046,9 @@ int dopt_head_loss_workspace(int64_t rows, int64_t width, int64_t vocab, int32_t
  *                - d_loss[t] * [v == targets[t]]
  *     d_x[t]   = sum over v of d[t][v] * weight[v]
  *     grad[grad_offset + v * width + c] (+)= sum over t of d[t][v] * x[t][c]
- * where a target outside [0, vocab) makes d_loss[t] count as 0.  The vocabulary
+ * where a target outside [0, vocab) makes d_loss[t] count as 0, and a row whose
+ * d_loss and d_loss + d_lse count as 0 adds nothing even where its logits are
+ * not finite (as long as x is).  The vocabulary
  * goes in pieces: the logits of one are computed again and their gradients d
  * kept in the workspace for the two products.  d over the largest d_loss (so
  * that equal weights are ones; with fp16 times 2^13, so that it stays in range)

@@ -237,6 +237,20 @@ def test_every_target_ignored():
     _check_grad(c, lse, torch.float32, d_x, grad, c.d_lse)
 
 
+@pytest.mark.parametrize("grad_type", [torch.bfloat16, torch.float32], ids=str)
+def test_ignored_rows_that_overflow(grad_type):
+    """Rows without a target or a penalty whose logits are infinite or NaN add nothing, whatever their lse."""
+    c = Case(300, 128, 600, torch.bfloat16)
+    _, lse = c.loss()
+    want_x, want_w = _grad(c, lse, grad_type, first=3)
+    dead = [1, 2, 3]  # the ignored ones
+    c.x[dead] = 3e38 * torch.sign(c.x[dead])
+    loss, lse = c.loss()
+    assert not loss[dead].any() and not bool(torch.isfinite(lse[dead]).any())
+    d_x, grad = _grad(c, lse, grad_type, first=3)
+    assert torch.equal(d_x, want_x) and torch.equal(grad, want_w) and not d_x[dead].any()
+
+
 def test_penalty_far_larger_than_the_loss():
     """fp16: what the loss adds to a row's gradient is small beside the penalty, but stays in range."""
     c = Case(150, 136, 400, torch.float16)

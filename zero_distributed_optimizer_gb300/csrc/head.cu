@@ -460,6 +460,10 @@ __global__ void __launch_bounds__(kLogitThreads, 1) __cluster_dims__(2, 1, 1)
                 } else {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) l[j] = by_p * exp2_of((l[j] - lse) * kLog2e);
+                    if (by_p == 0.0f && by_target == 0.0f && ok) {  // nothing, were its logits infinite
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) l[j] = 0.0f;
+                    }
                     if (has_target) {
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
@@ -871,7 +875,7 @@ __device__ __forceinline__ void find_factor(const ReadyArgs &a) {
     if (!(top_p <= 4.0f * top)) top = top_p;
     const float most = a.half ? 8192.0f : 1.0f;
     // (nothing to scale by: zeros, infinities, and what has no normal inverse)
-    const bool fine = top >= 1e-30f && top <= 1e30f;
+    const bool fine = top >= 1e-34f && top <= 1e34f;
     a.factor[0] = fine ? most / top : 1.0f;
     a.factor[1] = fine ? top / most : 1.0f;
 }
