@@ -150,9 +150,29 @@ def _norm_offsets(offsets):
 
 
 def _norm_params(params, row_gate, dtype, shape, index):
-    cols = (shape[1],)
-    at = [None if p is None else _dense(p, name, dtype, cols, index) for name, p in zip(_NORM_PARAMS, params)]
-    return _SixPointers(*at, None if row_gate is None else _dense(row_gate, "row_gate", torch.float32, shape[:1], index))
+    cols, at = shape[1:], []
+    for p in params:
+        if p is None:
+            at.append(None)
+        elif p.dtype is dtype and p.shape == cols and p.get_device() == index and p.is_contiguous():
+            at.append(p.data_ptr())
+        else:
+            _dense(p, _NORM_PARAMS[len(at)], dtype, cols, index)  # raises
+    at.append(None if row_gate is None else _dense(row_gate, "row_gate", torch.float32, shape[:1], index))
+    return _SixPointers(*at)
+
+
+def _matrices(named, dtype, shape, index):
+    """(address, row stride) of each of the matrices, one after another."""
+    cols, found = shape[1], []
+    for name, t in named:
+        if t is None:
+            found += (None, cols)
+        elif t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == index:
+            found += (t.data_ptr(), cols)
+        else:
+            found += _rows(t, name, dtype, shape, index)
+    return found
 
 
 def _matrix(t, name, dtype, shape, index):
@@ -179,8 +199,7 @@ def dopt_norm(kind: str, x, n, weight=None, bias=None, y=None, h=None, post: boo
     dt, shape = x.dtype, x.shape
     _call(index, stream, lib().dopt_norm, ctypes.byref(_norm_cfg(kind, 1 if post else 0, eps, scale)),
           _norm_params((weight, bias, post_weight, post_bias, gate), row_gate, dt, shape, index), _dtype_code(dt, "x"),
-          *shape, *_matrix(x, "x", dt, shape, index), *_matrix(y, "y", dt, shape, index),
-          *_matrix(h, "h", dt, shape, index), *_matrix(n, "n", dt, shape, index))
+          *shape, *_matrices((("x", x), ("y", y), ("h", h), ("n", n)), dt, shape, index))
 
 
 def norm_workspace(rows: int, cols: int, device=None):
@@ -215,9 +234,8 @@ def dopt_norm_grad(kind: str, h, d_n, d_x, weight=None, y=None, d_y=None, d_h=No
     rp = None if d_row_gate is None else _dense(d_row_gate, "d_row_gate", torch.float32, shape[:1], index)
     _call(index, stream, lib().dopt_norm_grad, ctypes.byref(_norm_cfg(kind, 1 if post else 0, eps, scale)),
           _norm_params((weight, None, post_weight, post_bias, gate), row_gate, dt, shape, index), _dtype_code(dt, "h"),
-          *shape, *_matrix(h, "h", dt, shape, index), *_matrix(y, "y", dt, shape, index),
-          *_matrix(d_n, "d_n", dt, shape, index), *_matrix(d_h, "d_h", dt, shape, index),
-          *_matrix(d_x, "d_x", dt, shape, index), *_matrix(d_y, "d_y", dt, shape, index), rp, gp, code, numel, at,
+          *shape, *_matrices((("h", h), ("y", y), ("d_n", d_n), ("d_h", d_h), ("d_x", d_x), ("d_y", d_y)), dt, shape, index),
+          rp, gp, code, numel, at,
           DOPT_NORM_ACCUMULATE if accumulate else 0, wp, wn)
 
 
