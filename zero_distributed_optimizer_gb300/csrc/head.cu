@@ -587,6 +587,16 @@ struct ProductArgs {
     int32_t tiles_m, items, whole, split, chunk;
     int32_t accumulate, out_dtype;
 };
+// What a launch makes: d_x, for which k is contiguous in the logits' gradients;
+// d_w, for which n is; or both, where all their tiles fit the card at once
+// (beside each other they take 33 us where two launches take 42, 1001 x 512 x
+// 5003 bf16; where there are more, the choice at each tile costs more).
+enum Which { kDx = 0, kDw = 1, kBoth = 2 };
+struct Products {
+    ProductArgs p[2];
+    int32_t first, items;       // items of p[0], and of both
+    int32_t joined;             // split tiles of p[0]
+};
 struct Item {
     int m0, n0, from, steps, slot;
 };
@@ -606,6 +616,19 @@ __device__ __forceinline__ Item item_of(const ProductArgs &a, int item) {
     it.from = int(all * part / parts);
     it.steps = int(all * (part + 1) / parts) - it.from;
     return it;
+}
+
+template <Which WHICH>
+__device__ __forceinline__ bool is_dx(const Products &w, int item) {
+    return WHICH == kDx || (WHICH == kBoth && item < w.first);
+}
+template <Which WHICH>
+__device__ __forceinline__ const ProductArgs &product_of(const Products &w, int item) {
+    return WHICH == kBoth && item >= w.first ? w.p[1] : w.p[0];
+}
+template <Which WHICH>
+__device__ __forceinline__ Item item_of(const Products &w, int item) {
+    return item_of(product_of<WHICH>(w, item), WHICH == kBoth && item >= w.first ? item - w.first : item);
 }
 
 // 16 sums of one column, of which `there` are outputs, to the rows from p on;
@@ -668,10 +691,9 @@ __device__ __forceinline__ void store_tile(const ProductArgs &a, int m, int n, f
     }
 }
 
-// B_K: k is contiguous in the logits' gradients (d_x); otherwise n is (d_w).
-template <typename T, bool B_K>
+template <typename T, Which WHICH>
 __global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
-    dopt_head_product_kernel(const __grid_constant__ ProductArgs a) {
+    dopt_head_product_kernel(const __grid_constant__ Products w) {
     extern __shared__ __align__(1024) unsigned char smem[];
     constexpr int kRing = kProductRing, kMmaWarp = kStoreWarps, kLoadWarp = kStoreWarps + 1;
     HeadBarriers &b = *reinterpret_cast<HeadBarriers *>(smem + kRing * kStage);
@@ -683,8 +705,9 @@ __global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
     if (warp == kLoadWarp) {
         int n = 0;
         bool ok = true;
-        for (int item = pair; ok && item < a.items; item += pairs) {
-            const Item it = item_of(a, item);
+        for (int item = pair; ok && item < w.items; item += pairs) {
+            const ProductArgs &a = product_of<WHICH>(w, item);
+            const Item it = item_of<WHICH>(w, item);
             for (int i = it.from; i < it.from + it.steps; ++i, ++n) {
                 const int s = n % kRing;
                 if (n >= kRing) ok = wait_phase<64>(b, b.empty[s], uint32_t(n / kRing - 1) & 1);
@@ -696,7 +719,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
                     if (rank == 0) expect_bytes(full, 2 * kStage);
                     load_box(to, &a.a_map, m, k, bar);
                     load_box(to + kSlab, &a.a_map, m + 64, k, bar);
-                    if (B_K) {
+                    if (is_dx<WHICH>(w, item)) {
                         load_box(to + kOperand, &a.b_map[plane], k, o, bar);
                     } else {
                         load_box(to + kOperand, &a.b_map[plane], o, k, bar);
@@ -709,16 +732,19 @@ __global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
         if (ok) drain(b, kRing, n);
     } else if (warp == kMmaWarp) {
         if (rank == 0) {
-            constexpr uint32_t kIdesc = instruction<T>(true, !B_K);
             const uint32_t base = uniform(tmem);
             const uint64_t a0 = mn_descriptor(smem_of(smem));
-            const uint64_t b0 = B_K ? k_descriptor(smem_of(smem + kOperand)) : mn_descriptor(smem_of(smem + kOperand));
             int n = 0, t = 0;
             uint32_t used = 0, odd = 0;  // bit per buffer: used before, an odd number of times
             bool ok = true;
-            for (int item = pair; ok && item < a.items; item += pairs, ++t) {
+            for (int item = pair; ok && item < w.items; item += pairs, ++t) {
                 if (products_withheld(t)) break;
-                const Item it = item_of(a, item);
+                const ProductArgs &a = product_of<WHICH>(w, item);
+                const Item it = item_of<WHICH>(w, item);
+                const bool b_k = is_dx<WHICH>(w, item);
+                const uint32_t idesc = b_k ? instruction<T>(true, false) : instruction<T>(true, true);
+                const uint64_t b0 = b_k ? k_descriptor(smem_of(smem + kOperand)) : mn_descriptor(smem_of(smem + kOperand));
+                const uint64_t b_step = b_k ? 2 : 128;  // 16 k on
                 int buffer = t & 1, left = 0;  // steps left of the sum
                 uint32_t sums = base;
                 for (int i = 0; i < it.steps && ok; ++i, ++n, --left) {
@@ -740,7 +766,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
                     if (elect_one()) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            product(sums, da + 128 * k, db + (B_K ? 2 : 128) * k, kIdesc, !fresh || k > 0);
+                            product(sums, da + 128 * k, db + b_step * k, idesc, !fresh || k > 0);
                         commit(b.empty[s]);
                         if (left == 1) commit(b.sum_full[buffer]);
                     }
@@ -751,12 +777,13 @@ __global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
     } else {
         const int m_in = int(rank) * (kM / 2) + (warp & 3) * 32 + lane, half = (warp >> 2) * (kN / 2);
         const uint32_t lanes = tmem + (uint32_t((warp & 3) * 32) << 16) + uint32_t(half);
-        const float back = a.back ? *a.back : 1.0f;
         int t = 0;
         uint32_t odd = 0;
         bool ok = true;
-        for (int item = pair; item < a.items; item += pairs, ++t) {
-            const Item it = item_of(a, item);
+        for (int item = pair; item < w.items; item += pairs, ++t) {
+            const ProductArgs &a = product_of<WHICH>(w, item);
+            const Item it = item_of<WHICH>(w, item);
+            const float back = a.back ? *a.back : 1.0f;
             const int buffer = t & 1, m = it.m0 + m_in;
             const uint32_t sums = lanes + uint32_t(buffer * kN);
             for (int i = 0; ok && i < it.steps; i += a.chunk) {
@@ -795,10 +822,12 @@ __global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
 
 // The split tiles' parts, added in order and written.  blockIdx.x: tile,
 // blockIdx.y: 16 of its outputs; a thread: one column.
-__global__ void __launch_bounds__(kM) dopt_head_parts_kernel(const __grid_constant__ ProductArgs a) {
+__global__ void __launch_bounds__(kM) dopt_head_parts_kernel(const __grid_constant__ Products w) {
     let_dependents_start();
     wait_for_grids_before();
-    const Item it = item_of(a, a.whole + int(blockIdx.x) * a.split);
+    const int second = int(blockIdx.x) >= w.joined;
+    const ProductArgs &a = w.p[second];
+    const Item it = item_of(a, a.whole + (int(blockIdx.x) - second * w.joined) * a.split);
     const int o = int(blockIdx.y) * 16;
     if (it.n0 + o >= a.outs) return;
     float f[16] = {};
@@ -920,8 +949,9 @@ cudaError_t allow_all() {
     cudaError_t e = allow_smem(dopt_head_logit_kernel<T, 0>, logit_smem(0));
     if (e == cudaSuccess) e = allow_smem(dopt_head_logit_kernel<T, 1>, logit_smem(1));
     if (e == cudaSuccess) e = allow_smem(dopt_head_logit_kernel<T, 2>, logit_smem(2));
-    if (e == cudaSuccess) e = allow_smem(dopt_head_product_kernel<T, false>, kProductSmem);
-    if (e == cudaSuccess) e = allow_smem(dopt_head_product_kernel<T, true>, kProductSmem);
+    if (e == cudaSuccess) e = allow_smem(dopt_head_product_kernel<T, kDx>, kProductSmem);
+    if (e == cudaSuccess) e = allow_smem(dopt_head_product_kernel<T, kDw>, kProductSmem);
+    if (e == cudaSuccess) e = allow_smem(dopt_head_product_kernel<T, kBoth>, kProductSmem);
     return e;
 }
 
@@ -977,18 +1007,21 @@ int make_map(const char *who, EncodeTiled encode, CUtensorMap *map, dopt_dtype d
 struct Plan {
     int64_t whole, tail;
     int parts;
+    double time;  // of all tiles
 };
 Plan plan_product(int64_t tiles, int64_t steps, int64_t pairs) {
     const int64_t tail = tiles % pairs;
-    Plan best{tiles, 0, 1};
+    const double waves = double(tiles / pairs) * (double(steps) + 4);
+    Plan best{tiles, 0, 1, waves};
     if (tail == 0) return best;
     double least = double(steps) + 4;
+    best.time = waves + least;
     for (int parts = 2; parts <= kMostSplit; ++parts) {
         if (steps / parts < 4 || tail * parts > kMostSlots) break;
         const double t = double((tail * parts + pairs - 1) / pairs) * (double(steps) / parts + 4) + 12 + 0.5 * double(tail * parts);
         if (t < least) {
             least = t;
-            best = Plan{tiles - tail, tail, parts};
+            best = Plan{tiles - tail, tail, parts, waves + t};
         }
     }
     return best;
@@ -1019,6 +1052,10 @@ struct HeadSpace {
 int64_t loss_rest(int64_t rows, int64_t vocab) {
     return up_to(rows * 4, 256) + 2 * ((vocab + kN - 1) / kN) * rows * int64_t(sizeof(float2));
 }
+// Parts of split tiles that a product of `outs` rows has at most.
+int64_t most_slots(int64_t width, int64_t outs) {
+    return std::min<int64_t>(kMostSlots, kMostSplit * ((width + kM - 1) / kM) * ((outs + kN - 1) / kN));
+}
 // The gradients' workspace after the copies: the factor, fp32 sums of d_x
 // where the vocabulary goes in pieces, parts of split tiles, and a piece's
 // gradients of the logits.
@@ -1031,9 +1068,7 @@ struct GradSpace {
         factor = 0;
         sums = 256;
         parts = sums + (piece < vocab ? up_to(rows * width * 4, 256) : 0);
-        const int64_t tiles_m = (width + kM - 1) / kM;
-        const int64_t tiles = std::max(tiles_m * ((rows + kN - 1) / kN), tiles_m * ((piece + kN - 1) / kN));
-        logits = parts + std::min<int64_t>(kMostSlots, kMostSplit * tiles) * kM * kN * 4;
+        logits = parts + (most_slots(width, rows) + most_slots(width, piece)) * kM * kN * 4;
         bytes = logits + planes * up_to(rows * piece_ld * 2, 256);
     }
 };
@@ -1105,18 +1140,68 @@ int fill_tiles(LogitArgs &a, dopt_dtype dtype, int64_t rows, int64_t width, int6
     return items <= INT32_MAX / 2;
 }
 
-template <typename T>
-int run_product(const char *who, bool b_k, ProductArgs &a, int64_t pairs, cudaStream_t stream) {
-    const int64_t tiles = int64_t(a.tiles_m) * ((a.outs + kN - 1) / kN), steps = int64_t(a.steps) * a.planes;
-    const Plan plan = plan_product(tiles, steps, pairs);
+int64_t tiles_of(const ProductArgs &a) { return int64_t(a.tiles_m) * ((a.outs + kN - 1) / kN); }
+void use(ProductArgs &a, const Plan &plan) {
     a.whole = int32_t(plan.whole);
     a.split = plan.parts;
     a.items = int32_t(plan.whole + plan.tail * plan.parts);
-    const dim3 grid(unsigned(2 * std::min<int64_t>(a.items, pairs)));
-    int rc = b_k ? launch_op(who, dopt_head_product_kernel<T, true>, grid, dim3(kProductThreads), kProductSmem, stream, a)
-                 : launch_op(who, dopt_head_product_kernel<T, false>, grid, dim3(kProductThreads), kProductSmem, stream, a);
-    if (rc != DOPT_OK || plan.parts == 1) return rc;
-    return launch_op(who, dopt_head_parts_kernel, dim3(unsigned(plan.tail), kN / 16), dim3(kM), 0, stream, a);
+}
+template <typename T>
+int launch_products(const char *who, Which which, Products &w, int64_t pairs, cudaStream_t stream) {
+    int64_t joined[2] = {};
+    for (int i = 0; i < (which == kBoth ? 2 : 1); ++i)
+        if (w.p[i].split > 1) joined[i] = (w.p[i].items - w.p[i].whole) / w.p[i].split;
+    w.first = w.p[0].items;
+    w.items = w.first + (which == kBoth ? w.p[1].items : 0);
+    w.joined = int32_t(joined[0]);
+    auto kernel = which == kDx ? dopt_head_product_kernel<T, kDx>
+                               : which == kDw ? dopt_head_product_kernel<T, kDw> : dopt_head_product_kernel<T, kBoth>;
+    const int rc = launch_op(who, kernel, dim3(unsigned(2 * std::min<int64_t>(w.items, pairs))), dim3(kProductThreads),
+                             kProductSmem, stream, w);
+    if (rc != DOPT_OK || joined[0] + joined[1] == 0) return rc;
+    return launch_op(who, dopt_head_parts_kernel, dim3(unsigned(joined[0] + joined[1]), kN / 16), dim3(kM), 0, stream, w);
+}
+// d_x and d_w, either or both of them: in one launch where all their tiles fit
+// at once and the estimates, in the plan's units, say so: d_x's tiles, few and
+// long, in as many parts as leave room for d_w's, against two plans of their own
+// and a launch.  (How sums are divided depends on the sizes alone, not on what
+// is wanted or on the grads' type.)
+template <typename T>
+int run_products(const char *who, const ProductArgs &dx, const ProductArgs &dw, bool want_dx, bool want_dw, int64_t pairs,
+                 cudaStream_t stream) {
+    const int64_t tiles_x = tiles_of(dx), tiles_w = tiles_of(dw);
+    Plan plan_x = plan_product(tiles_x, dx.steps, pairs);
+    Plan plan_w = plan_product(tiles_w, int64_t(dw.steps) * dw.planes, pairs);
+    bool together = tiles_x + tiles_w <= pairs;
+    if (together) {
+        const int parts = int(std::max<int64_t>(1, std::min({int64_t(kMostSplit), (pairs - tiles_w) / tiles_x, int64_t(dx.steps) / 4})));
+        const double time = std::max(double(dx.steps) / parts, double(dw.steps)) + 4 +
+                            (parts > 1 ? 12 + 0.5 * double(tiles_x * parts) : 0);
+        together = time < plan_x.time + plan_product(tiles_w, dw.steps, pairs).time + 12;
+        if (together) {
+            plan_x = parts > 1 ? Plan{0, tiles_x, parts, 0} : Plan{tiles_x, 0, 1, 0};
+            plan_w = Plan{tiles_w, 0, 1, 0};
+        }
+    }
+    Products w{};
+    if (together && want_dx && want_dw) {
+        w.p[0] = dx, w.p[1] = dw;
+        use(w.p[0], plan_x);
+        use(w.p[1], plan_w);
+        return launch_products<T>(who, kBoth, w, pairs, stream);
+    }
+    int rc = DOPT_OK;
+    if (want_dx) {
+        w.p[0] = dx;
+        use(w.p[0], plan_x);
+        rc = launch_products<T>(who, kDx, w, pairs, stream);
+    }
+    if (rc == DOPT_OK && want_dw) {
+        w.p[0] = dw;
+        use(w.p[0], plan_w);
+        rc = launch_products<T>(who, kDw, w, pairs, stream);
+    }
+    return rc;
 }
 
 struct GradCall {
@@ -1170,44 +1255,44 @@ int run_grad(const char *who, const GradCall &c, Operands o, const HeadSpace &sp
                        dim3(unsigned(2 * std::min<int64_t>(a.items, pairs))), dim3(kLogitThreads), logit_smem(c.planes),
                        stream, a);
         if (rc != DOPT_OK) return rc;
-        ProductArgs p{};
-        p.partial = reinterpret_cast<float *>(rest + g.parts);
-        p.cols = int32_t(c.width);
-        p.tiles_m = int32_t((c.width + kM - 1) / kM);
+        ProductArgs dx{}, dw{};
+        float *partial = reinterpret_cast<float *>(rest + g.parts);
+        dx.cols = dw.cols = int32_t(c.width);
+        dx.tiles_m = dw.tiles_m = int32_t((c.width + kM - 1) / kM);
+        dx.outs = int32_t(c.rows);
+        dx.steps = int32_t((cols + kK - 1) / kK);
+        dx.planes = 1;
+        dx.chunk = sum_chunk(c.dtype, c.dtype);
+        dx.partial = partial;
+        dw.outs = int32_t(cols);
+        dw.steps = int32_t((c.rows + kK - 1) / kK);
+        dw.planes = c.planes;
+        dw.chunk = sum_chunk(c.dtype, c.grad_dtype);
+        dw.partial = partial + most_slots(c.width, c.rows) * kM * kN;
         if (c.d_x) {
             const bool last = v0 + cols == c.vocab;
-            rc = make_map(who, encode, &p.a_map, c.dtype, w, c.width, cols, o.ld_w, 64, 64);
+            rc = make_map(who, encode, &dx.a_map, c.dtype, w, c.width, cols, o.ld_w, 64, 64);
             if (rc == DOPT_OK)
-                rc = make_map(who, encode, &p.b_map[0], c.dtype, rest + g.logits, cols, c.rows, g.piece_ld, 64, 128);
+                rc = make_map(who, encode, &dx.b_map[0], c.dtype, rest + g.logits, cols, c.rows, g.piece_ld, 64, 128);
             if (rc != DOPT_OK) return rc;
-            p.out = last ? c.d_x : sums;
-            p.ld = last ? c.ld_d_x : c.width;
-            p.add = v0 > 0 ? sums : nullptr;
-            p.back = last ? factor + 1 : nullptr;
-            p.out_dtype = last ? c.dtype : DOPT_FP32;
-            p.outs = int32_t(c.rows);
-            p.steps = int32_t((cols + kK - 1) / kK);
-            p.planes = 1;
-            p.chunk = sum_chunk(c.dtype, c.dtype);
-            if ((rc = run_product<T>(who, true, p, pairs, stream)) != DOPT_OK) return rc;
+            dx.out = last ? c.d_x : sums;
+            dx.ld = last ? c.ld_d_x : c.width;
+            dx.add = v0 > 0 ? sums : nullptr;
+            dx.back = last ? factor + 1 : nullptr;
+            dx.out_dtype = last ? c.dtype : DOPT_FP32;
         }
         if (c.grad) {
-            rc = make_map(who, encode, &p.a_map, c.dtype, o.x, c.width, c.rows, o.ld_x, 64, 64);
+            rc = make_map(who, encode, &dw.a_map, c.dtype, o.x, c.width, c.rows, o.ld_x, 64, 64);
             for (int q = 0; q < c.planes && rc == DOPT_OK; ++q)
-                rc = make_map(who, encode, &p.b_map[q], c.dtype, rest + g.logits + q * plane, cols, c.rows, g.piece_ld, 64, 64);
+                rc = make_map(who, encode, &dw.b_map[q], c.dtype, rest + g.logits + q * plane, cols, c.rows, g.piece_ld, 64, 64);
             if (rc != DOPT_OK) return rc;
-            p.out = c.grad + v0 * c.width * int64_t(elem_bytes(c.grad_dtype));
-            p.ld = c.width;
-            p.add = nullptr;
-            p.back = factor + 1;
-            p.out_dtype = c.grad_dtype;
-            p.outs = int32_t(cols);
-            p.steps = int32_t((c.rows + kK - 1) / kK);
-            p.planes = c.planes;
-            p.chunk = sum_chunk(c.dtype, c.grad_dtype);
-            p.accumulate = c.accumulate;
-            if ((rc = run_product<T>(who, false, p, pairs, stream)) != DOPT_OK) return rc;
+            dw.out = c.grad + v0 * c.width * int64_t(elem_bytes(c.grad_dtype));
+            dw.ld = c.width;
+            dw.back = factor + 1;
+            dw.out_dtype = c.grad_dtype;
+            dw.accumulate = c.accumulate;
         }
+        if ((rc = run_products<T>(who, dx, dw, c.d_x != nullptr, c.grad != nullptr, pairs, stream)) != DOPT_OK) return rc;
     }
     return DOPT_OK;
 }
