@@ -198,10 +198,10 @@ __device__ __forceinline__ char *grad_row(const EmbedGradArgs &a, int64_t row) {
 
 // The tokens sorted by the key of their row (stable).  A block owns `range`
 // rows of the table.  It goes through all ids, so that it knows without any
-// other block how many belong to those before it, lists those that are its own in order and sorts the
-// list: counts of each (warp, row), their prefixes, places.  A lane's rank
-// among its warp's tokens of one row comes from a ballot per bit of the row
-// and is kept with the token for the second pass.  The sort is bound by
+// other block how many belong to those before it, lists those that are its own
+// in order and sorts the list: counts of each (warp, row), their prefixes,
+// places.  A lane's rank among its warp's tokens of one row comes from a ballot
+// per bit of the row and is kept with the token for the second pass.  The sort is bound by
 // latencies, so blocks that write zeros to the first rows of the table run
 // beside it.
 template <typename I>
@@ -486,8 +486,8 @@ __global__ void __launch_bounds__(kEmbedThreads) dopt_embed_grad_kernel(const __
                     for (int q = 0; q < kPer; ++q) g[k * kPer + q] = part[q];
                 }
             }
-            fetch(i + kAhead);
             add(i, g);
+            fetch(i + kAhead);  // into the place that was just read
         }
     } else {
         using V = Values<T, kCols>;
