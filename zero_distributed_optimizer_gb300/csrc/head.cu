@@ -27,8 +27,8 @@ namespace {
 // gradients 2070-2170 and 2390-2450 us (1.83 and 1.56-1.59 PFLOP/s).  The logits'
 // gradients are stored as they are made, 1.6 GB, which keeps the tensor cores at
 // 83 % there; in pieces that stay in L2 d_x's fp32 sums would move more.  Few
-// tokens: 24 x 2048 x 32000, loss 32 us (19 at the copy rate), of which 7 are the
-// two launches and 16 the products of 256 rows in the pairs with two tiles.
+// tokens: 24 x 2048 x 32000, loss 32 us (19 at the copy rate), 20 for the
+// matrix, 7 of two launches, 4 until the first steps are there.
 constexpr int kM = 256, kN = 256, kK = 64;  // of a pair's tile, and of a step
 constexpr int kSlab = 64 * 128;             // 64 rows of 128 bytes
 constexpr int kOperand = 2 * kSlab;         // a CTA's share of one operand in a step
