@@ -1054,7 +1054,8 @@ int dopt_head_loss_workspace(int64_t rows, int64_t width, int64_t vocab, int32_t
  * that equal weights are ones; with fp16 times 2^13, so that it stays in range)
  * is rounded to x's type, about as much as the 16-bit results are; for fp32
  * grads what that rounding leaves is multiplied too, so that d counts with 17
- * bits (bf16) or 23 (fp16): grads are off by 1-3e-6 or 4e-7 of their size.  Sums are
+ * bits (bf16) or 23 (fp16): grads are off by 1-3e-6 or 0.4-1.6e-6 of their
+ * size.  Sums are
  * fp32 (of at most 1024 products, 512 with fp16, on the tensor cores for fp32
  * grads), in an order that depends on the sizes alone, and each result is
  * rounded once (after adding the old grad, with DOPT_HEAD_ACCUMULATE).

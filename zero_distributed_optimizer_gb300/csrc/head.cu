@@ -23,8 +23,8 @@ namespace {
 //
 // Long products are bound by the tensor cores (active 96-98 % of the cycles) and
 // then by the card's power: 16384 tokens x 768 x 50257, bf16, loss 618-647 us in
-// short runs (1.96-2.05 PFLOP/s), 708-725 under the power cap (1.75-1.79);
-// gradients 2070-2170 and 2390-2450 us (1.83 and 1.56-1.59 PFLOP/s).  The logits'
+// short runs (1.96-2.05 PFLOP/s), 706-725 under the power cap (1.75-1.79);
+// gradients 2070-2180 and 2350-2450 us (1.83 and 1.55-1.62 PFLOP/s).  The logits'
 // gradients are stored as they are made, 1.6 GB, which keeps the tensor cores at
 // 83 % there; in pieces that stay in L2 d_x's fp32 sums would move more.  Few
 // tokens: 24 x 2048 x 32000, loss 32 us (19 at the copy rate), 20 for the
