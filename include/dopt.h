@@ -1050,12 +1050,15 @@ int dopt_head_loss_workspace(int64_t rows, int64_t width, int64_t vocab, int32_t
  * d_loss and d_loss + d_lse count as 0 adds nothing even where its logits are
  * not finite (as long as x is).  The vocabulary
  * goes in pieces: the logits of one are computed again and their gradients d
- * kept in the workspace for the two products.  d over the largest d_loss (so
- * that equal weights are ones; with fp16 times 2^13, so that it stays in range)
- * is rounded to x's type, about as much as the 16-bit results are; for fp32
- * grads what that rounding leaves is multiplied too, so that d counts with 17
- * bits (bf16) or 23 (fp16): grads are off by 1-3e-6 or 0.4-1.6e-6 of their
- * size.  Sums are
+ * kept in the workspace for the two products.  d over the largest finite d_loss
+ * (so that equal weights are ones; with fp16 times 2^13, so that it stays in
+ * range) is rounded to x's type, about as much as the 16-bit results are; for
+ * fp32 grads what that rounding leaves is multiplied too, so that d counts with
+ * 17 bits (bf16) or 23 (fp16): grads are off by 1-3e-6 or 0.4-1.6e-6 of their
+ * size.  With fp16 d counts no finer than 2^-38 of the largest d_loss for grad,
+ * and than 2^-34 of the row's own d_loss for d_x: where the rows' weights are
+ * further apart than that needs (16 times), a row's d for d_x is over its own,
+ * which takes a second pass over the vocabulary if grad is wanted too.  Sums are
  * fp32 (of at most 1024 products, 512 with fp16, on the tensor cores for fp32
  * grads), in an order that depends on the sizes alone, and each result is
  * rounded once (after adding the old grad, with DOPT_HEAD_ACCUMULATE).

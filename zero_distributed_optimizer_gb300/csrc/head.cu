@@ -243,12 +243,17 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 // Logits
 // ---------------------------------------------------------------------------
 
+// Types whose range is so short that rows of d_x may need factors of their own.
+template <typename T>
+constexpr bool kHasRows = std::is_same<T, __half>::value;
+
 struct LogitArgs {
     CUtensorMap x_map, w_map;
     CUtensorMap d_map[2];       // gradients: their 16 bits, and what those leave (fp32 grads)
     const void *targets;
     const float *lse, *d_loss, *d_lse;
-    const float *factor;        // gradients: what they are multiplied by
+    const float *factor;        // gradients: what they are multiplied by, what takes it back, and if rows have their own
+    const float *row_back;      // gradients for d_x: what takes each row's own back, or NULL
     float2 *partial;            // loss: [2 * tiles_n][rows] (reference, sum), powers of two
     float *at_target;           // loss: [rows] the target's logit
     int64_t first, vocab;       // this launch's first column of the vocabulary; all of them
@@ -257,6 +262,7 @@ struct LogitArgs {
     int32_t group;              // blocks of tokens that go through the vocabulary together
     int32_t x_ctas, step_bytes; // CTAs of a pair that have tokens; bytes of a pair's step
     int32_t wide;
+    int32_t for_rows;           // 1: nothing is done unless rows have their own factors
 };
 
 struct Tile {
@@ -343,6 +349,10 @@ __global__ void __launch_bounds__(kLogitThreads, 1) __cluster_dims__(2, 1, 1)
     constexpr bool GRAD = PLANES > 0;
     constexpr int kRing = logit_ring(PLANES);
     constexpr int kMmaWarp = kLogitWarps, kLoadWarp = kLogitWarps + 1;
+    if (GRAD && kHasRows<T> && a.for_rows) {
+        wait_for_grids_before();
+        if (a.factor[2] == 0.0f) return;
+    }
     unsigned char *out_buffers = smem + kRing * kStage;
     HeadBarriers &b = *reinterpret_cast<HeadBarriers *>(out_buffers + PLANES * kLogitWarps * kOutBuffer);
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -425,7 +435,8 @@ __global__ void __launch_bounds__(kLogitThreads, 1) __cluster_dims__(2, 1, 1)
                 by_target = whole >= 0 && whole < a.vocab ? a.d_loss[row] : 0.0f;
                 by_p = by_target + (a.d_lse ? a.d_lse[row] : 0.0f);
                 lse = a.lse[row];
-                by_p *= a.factor[0], by_target *= a.factor[0];
+                const float factor = kHasRows<T> && a.row_back && a.factor[2] != 0.0f ? 1.0f / a.row_back[row] : a.factor[0];
+                by_p *= factor, by_target *= factor;
             }
             // the logits of 128 columns: their sums' parts, added as they come
             float all[4][32];
@@ -591,7 +602,8 @@ struct ProductArgs {
     CUtensorMap b_map[2];       // the logits' gradients
     void *out;                  // [outs][cols], row stride ld
     const float *add;           // fp32 [outs][cols] added to the sums, or NULL
-    const float *back;          // factor of the result, or NULL
+    const float *back;          // factor of the result (then: if rows have their own), or NULL
+    const float *row_back;      // d_x: each row's own
     float *partial;             // [slot][n][m] parts of split tiles
     int64_t ld;
     int32_t cols, outs, steps;  // steps of 64 k a plane
@@ -603,12 +615,17 @@ struct ProductArgs {
 // d_w, for which n is; or both, where all their tiles fit the card at once
 // (beside each other they take 33 us where two launches take 42, 1001 x 512 x
 // 5003 bf16; where there are more, the choice at each tile costs more).
-enum Which { kDx = 0, kDw = 1, kBoth = 2 };
+enum Which { kDx = 0, kDw = 1, kBoth = 2, kDxRows = 3 };  // kDxRows: d_x of rows that may have their own factors
 struct Products {
     ProductArgs p[2];
     int32_t first, items;       // items of p[0], and of both
     int32_t joined;             // split tiles of p[0]
+    const float *for_rows;      // not NULL: whether rows have their own factors, and nothing is done
+    int32_t unless;             // where they have none (0) or have some (1)
 };
+__device__ __forceinline__ bool not_for_these(const Products &w) {
+    return w.for_rows && (*w.for_rows != 0.0f) == (w.unless != 0);
+}
 struct Item {
     int m0, n0, from, steps, slot;
 };
@@ -632,7 +649,7 @@ __device__ __forceinline__ Item item_of(const ProductArgs &a, int item) {
 
 template <Which WHICH>
 __device__ __forceinline__ bool is_dx(const Products &w, int item) {
-    return WHICH == kDx || (WHICH == kBoth && item < w.first);
+    return WHICH == kDx || WHICH == kDxRows || (WHICH == kBoth && item < w.first);
 }
 template <Which WHICH>
 __device__ __forceinline__ const ProductArgs &product_of(const Products &w, int item) {
@@ -643,10 +660,24 @@ __device__ __forceinline__ Item item_of(const Products &w, int item) {
     return item_of(product_of<WHICH>(w, item), WHICH == kBoth && item >= w.first ? item - w.first : item);
 }
 
-// 16 sums of one column, of which `there` are outputs, to the rows from p on;
-// `add`: the sums so far.
-template <typename G, bool ALL>
-__device__ __forceinline__ void store_sums(const ProductArgs &a, G *p, const float *add, int there, float back, float (&v)[16]) {
+// The factor of a product's results: one, or each row's own.
+struct Back {
+    float all = 1.0f;
+    const float *rows = nullptr;
+};
+__device__ __forceinline__ Back back_of(const ProductArgs &a, bool rows) {
+    Back back;
+    if (!a.back) return back;
+    if (rows && a.back[1] != 0.0f) back.rows = a.row_back;
+    else back.all = *a.back;
+    return back;
+}
+
+// 16 sums of one column, of which `there` are outputs, to the rows from p on
+// (n: the first one's number); `add`: the sums so far.
+template <typename G, bool ALL, bool ROWS>
+__device__ __forceinline__ void store_sums(const ProductArgs &a, G *p, const float *add, int there, int n, const Back &back,
+                                           float (&v)[16]) {
     if (add) {
         float more[16];
 #pragma unroll
@@ -656,8 +687,14 @@ __device__ __forceinline__ void store_sums(const ProductArgs &a, G *p, const flo
         for (int j = 0; j < 16; ++j)
             if (ALL || j < there) v[j] += more[j];
     }
+    if (ROWS && back.rows) {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) v[j] *= back;
+        for (int j = 0; j < 16; ++j)
+            if (ALL || j < there) v[j] *= back.rows[n + j];
+    } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] *= back.all;
+    }
     if (a.accumulate) {
         G old[16];
 #pragma unroll
@@ -671,18 +708,18 @@ __device__ __forceinline__ void store_sums(const ProductArgs &a, G *p, const flo
     for (int j = 0; j < 16; ++j, p += a.ld)
         if (ALL || j < there) *p = from_f32<G>(v[j]);
 }
-template <typename G>
-__device__ __forceinline__ void store_column(const ProductArgs &a, int m, int n, float back, float (&v)[16]) {
+template <typename G, bool ROWS>
+__device__ __forceinline__ void store_column(const ProductArgs &a, int m, int n, const Back &back, float (&v)[16]) {
     if (m >= a.cols || n >= a.outs) return;
     G *p = static_cast<G *>(a.out) + n * a.ld + m;
     const float *add = a.add ? a.add + int64_t(n) * a.cols + m : nullptr;
-    if (a.outs - n >= 16) store_sums<G, true>(a, p, add, 16, back, v);
-    else store_sums<G, false>(a, p, add, a.outs - n, back, v);
+    if (a.outs - n >= 16) store_sums<G, true, ROWS>(a, p, add, 16, n, back, v);
+    else store_sums<G, false, ROWS>(a, p, add, a.outs - n, n, back, v);
 }
 // A warp's half of a tile's columns, from column n on, at `sums` in tensor
 // memory, 32 at a time; NaN instead where there are none.
-template <typename G>
-__device__ __forceinline__ void store_tile(const ProductArgs &a, int m, int n, float back, uint32_t sums, bool there_are) {
+template <typename G, bool ROWS>
+__device__ __forceinline__ void store_tile(const ProductArgs &a, int m, int n, const Back &back, uint32_t sums, bool there_are) {
     for (int o = 0; o < kN / 2; o += 32) {
         uint32_t r[2][16];
 #pragma unroll
@@ -698,7 +735,7 @@ __device__ __forceinline__ void store_tile(const ProductArgs &a, int m, int n, f
             float v[16];
 #pragma unroll
             for (int q = 0; q < 16; ++q) v[q] = __uint_as_float(r[h][q]);
-            store_column<G>(a, m, n + o + 16 * h, back, v);
+            store_column<G, ROWS>(a, m, n + o + 16 * h, back, v);
         }
     }
 }
@@ -708,6 +745,11 @@ __global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
     dopt_head_product_kernel(const __grid_constant__ Products w) {
     extern __shared__ __align__(1024) unsigned char smem[];
     constexpr int kRing = kProductRing, kMmaWarp = kStoreWarps, kLoadWarp = kStoreWarps + 1;
+    constexpr bool ROWS = WHICH == kDxRows;
+    if (kHasRows<T> && (WHICH == kDx || ROWS) && w.for_rows) {
+        wait_for_grids_before();
+        if (not_for_these(w)) return;
+    }
     HeadBarriers &b = *reinterpret_cast<HeadBarriers *>(smem + kRing * kStage);
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
@@ -795,7 +837,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
         for (int item = pair; item < w.items; item += pairs, ++t) {
             const ProductArgs &a = product_of<WHICH>(w, item);
             const Item it = item_of<WHICH>(w, item);
-            const float back = a.back ? *a.back : 1.0f;
+            const Back back = back_of(a, ROWS);
             const int buffer = t & 1, m = it.m0 + m_in;
             const uint32_t sums = lanes + uint32_t(buffer * kN);
             for (int i = 0; ok && i < it.steps; i += a.chunk) {
@@ -820,11 +862,11 @@ __global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
                     for (int q = 0; q < 16; ++q, p += kM) *p = __uint_as_float(r[q]);
                 }
             } else if (a.out_dtype == DOPT_FP32) {
-                store_tile<float>(a, m, it.n0 + half, back, sums, ok);
+                store_tile<float, ROWS>(a, m, it.n0 + half, back, sums, ok);
             } else if (a.out_dtype == DOPT_BF16) {
-                store_tile<__nv_bfloat16>(a, m, it.n0 + half, back, sums, ok);
+                store_tile<__nv_bfloat16, ROWS>(a, m, it.n0 + half, back, sums, ok);
             } else {
-                store_tile<__half>(a, m, it.n0 + half, back, sums, ok);
+                store_tile<__half, ROWS>(a, m, it.n0 + half, back, sums, ok);
             }
             if (ok) release_sums(b, buffer, lane);
         }
@@ -837,6 +879,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
 __global__ void __launch_bounds__(kM) dopt_head_parts_kernel(const __grid_constant__ Products w) {
     let_dependents_start();
     wait_for_grids_before();
+    if (not_for_these(w)) return;
     const int second = int(blockIdx.x) >= w.joined;
     const ProductArgs &a = w.p[second];
     const Item it = item_of(a, a.whole + (int(blockIdx.x) - second * w.joined) * a.split);
@@ -851,11 +894,11 @@ __global__ void __launch_bounds__(kM) dopt_head_parts_kernel(const __grid_consta
 #pragma unroll
         for (int q = 0; q < 16; ++q) f[q] += v[q];
     }
-    const float back = a.back ? *a.back : 1.0f;
+    const Back back = back_of(a, a.row_back != nullptr);
     const int m = it.m0 + int(threadIdx.x);
-    if (a.out_dtype == DOPT_FP32) store_column<float>(a, m, it.n0 + o, back, f);
-    else if (a.out_dtype == DOPT_BF16) store_column<__nv_bfloat16>(a, m, it.n0 + o, back, f);
-    else store_column<__half>(a, m, it.n0 + o, back, f);
+    if (a.out_dtype == DOPT_FP32) store_column<float, true>(a, m, it.n0 + o, back, f);
+    else if (a.out_dtype == DOPT_BF16) store_column<__nv_bfloat16, true>(a, m, it.n0 + o, back, f);
+    else store_column<__half, true>(a, m, it.n0 + o, back, f);
 }
 
 // What comes before the products, in one launch.  Matrices whose rows are not
@@ -865,7 +908,12 @@ __global__ void __launch_bounds__(kM) dopt_head_parts_kernel(const __grid_consta
 // over the largest d_loss, so that a mean's equal weights become ones and a
 // target's -(1 - p) is rounded by what p is, not by what 1 / rows happens to be
 // (the same way in every row: gradients were up to 2^-9 too large or small
-// throughout), and for fp16 times 2^13, to stay in its normal range.
+// throughout), and for fp16 times 2^13, to stay in its normal range.  A d_loss
+// that is not finite is no measure of the others.
+// fp16 reaches no further than 2^-38 of the largest so.  Rows of d_x have nothing
+// to do with one another: where a row's weight is less than a 16th of the
+// largest, all have a factor of their own for d_x (row_back takes it back, and
+// factor[2] says so); the output matrix's grads are sums over rows of one factor.
 struct ReadyArgs {
     const void *from[2];
     void *to[2];
@@ -876,15 +924,24 @@ struct ReadyArgs {
     const float *d_loss, *d_lse;
     const void *targets;
     float *factor;      // or NULL
+    float *row_back;    // fp16: each row's own, or NULL
     int64_t vocab;
     int32_t wide, half;
     int32_t tokens;
 };
 constexpr int kReadyThreads = 512, kReadyRows = kReadyThreads / 32;
+// The measure of weights of which d_loss's largest is `top`, d_loss + d_lse's `top_p`.
+// (a gradient is then at most 5 times as large; where d_lse is far larger, twice)
+__device__ __forceinline__ float measure(float top, float top_p) { return top_p <= 4.0f * top ? top : top_p; }
+// (nothing to scale by: zeros, infinities, and what has no normal inverse)
+__device__ __forceinline__ bool has_factor(float top) { return top >= 1e-34f && top <= 1e34f; }
+template <bool ROWS>
 __device__ __forceinline__ void find_factor(const ReadyArgs &a) {
-    __shared__ float tops[2][kReadyRows];
+    __shared__ float tops[3][kReadyRows];
     constexpr int kAhead = 8;
+    const float most = a.half ? 8192.0f : 1.0f;
     float top = 0.0f, top_p = 0.0f;  // of d_loss, and of d_loss + d_lse
+    float least = kLargest;          // of the rows' own measures, if they count at all
     for (int r0 = threadIdx.x; r0 < a.tokens; r0 += kAhead * kReadyThreads) {
         int64_t t[kAhead];
         float loss[kAhead], lse[kAhead];
@@ -898,27 +955,35 @@ __device__ __forceinline__ void find_factor(const ReadyArgs &a) {
         }
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
+            const int r = r0 + i * kReadyThreads;
             const float by_target = t[i] >= 0 && t[i] < a.vocab ? loss[i] : 0.0f;
-            top = fmaxf(top, fabsf(by_target));
-            top_p = fmaxf(top_p, fabsf(by_target + lse[i]));
+            const float l = fabsf(by_target), p = fabsf(by_target + lse[i]);
+            if (l <= kLargest) top = fmaxf(top, l);
+            if (p <= kLargest) top_p = fmaxf(top_p, p);
+            if (ROWS && a.row_back) {
+                const float own = measure(l, p);
+                if (own > 0.0f) least = fminf(least, own);
+                if (r < a.tokens) a.row_back[r] = has_factor(own) ? own / most : 1.0f;
+            }
         }
     }
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) {
         top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
         top_p = fmaxf(top_p, __shfl_xor_sync(kFull, top_p, d));
+        if (ROWS) least = fminf(least, __shfl_xor_sync(kFull, least, d));
     }
-    if ((threadIdx.x & 31) == 0) tops[0][threadIdx.x >> 5] = top, tops[1][threadIdx.x >> 5] = top_p;
+    if ((threadIdx.x & 31) == 0)
+        tops[0][threadIdx.x >> 5] = top, tops[1][threadIdx.x >> 5] = top_p, tops[2][threadIdx.x >> 5] = least;
     __syncthreads();
     if (threadIdx.x > 0) return;
-    for (int w = 1; w < kReadyRows; ++w) top = fmaxf(top, tops[0][w]), top_p = fmaxf(top_p, tops[1][w]);
-    // (a gradient is then at most 5 * 2^13; where d_lse is far larger, twice 2^13)
-    if (!(top_p <= 4.0f * top)) top = top_p;
-    const float most = a.half ? 8192.0f : 1.0f;
-    // (nothing to scale by: zeros, infinities, and what has no normal inverse)
-    const bool fine = top >= 1e-34f && top <= 1e34f;
+    for (int w = 1; w < kReadyRows; ++w)
+        top = fmaxf(top, tops[0][w]), top_p = fmaxf(top_p, tops[1][w]), least = fminf(least, tops[2][w]);
+    top = measure(top, top_p);
+    const bool fine = has_factor(top);
     a.factor[0] = fine ? most / top : 1.0f;
     a.factor[1] = fine ? top / most : 1.0f;
+    a.factor[2] = ROWS && a.row_back && top > 16.0f * least ? 1.0f : 0.0f;
 }
 template <typename T>
 __global__ void __launch_bounds__(kReadyThreads) dopt_head_ready_kernel(const __grid_constant__ ReadyArgs a) {
@@ -927,7 +992,7 @@ __global__ void __launch_bounds__(kReadyThreads) dopt_head_ready_kernel(const __
     int64_t block = blockIdx.x;
     if (a.factor) {
         if (block == 0) {
-            find_factor(a);
+            find_factor<kHasRows<T>>(a);
             return;
         }
         --block;
@@ -964,6 +1029,8 @@ cudaError_t allow_all() {
     if (e == cudaSuccess) e = allow_smem(dopt_head_product_kernel<T, kDx>, kProductSmem);
     if (e == cudaSuccess) e = allow_smem(dopt_head_product_kernel<T, kDw>, kProductSmem);
     if (e == cudaSuccess) e = allow_smem(dopt_head_product_kernel<T, kBoth>, kProductSmem);
+    if constexpr (kHasRows<T>)
+        if (e == cudaSuccess) e = allow_smem(dopt_head_product_kernel<T, kDxRows>, kProductSmem);
     return e;
 }
 
@@ -1068,17 +1135,18 @@ int64_t loss_rest(int64_t rows, int64_t vocab) {
 int64_t most_slots(int64_t width, int64_t outs) {
     return std::min<int64_t>(kMostSlots, kMostSplit * ((width + kM - 1) / kM) * ((outs + kN - 1) / kN));
 }
-// The gradients' workspace after the copies: the factor, fp32 sums of d_x
+// The gradients' workspace after the copies: the factor, the rows' own, fp32 sums of d_x
 // where the vocabulary goes in pieces, parts of split tiles, and a piece's
 // gradients of the logits.
 struct GradSpace {
-    int64_t factor, sums, parts, logits, bytes;
+    int64_t factor, row_back, sums, parts, logits, bytes;
     int64_t piece, piece_ld;  // columns of a piece, and of its rows
     GradSpace(int64_t rows, int64_t width, int64_t vocab, int planes, int64_t pieces) {
         piece = std::min(vocab, up_to((vocab + pieces - 1) / pieces, kN));
         piece_ld = up_to(piece, 64);
         factor = 0;
-        sums = 256;
+        row_back = 256;
+        sums = row_back + up_to(rows * 4, 256);
         parts = sums + (piece < vocab ? up_to(rows * width * 4, 256) : 0);
         logits = parts + (most_slots(width, rows) + most_slots(width, piece)) * kM * kN * 4;
         bytes = logits + planes * up_to(rows * piece_ld * 2, 256);
@@ -1168,6 +1236,8 @@ int launch_products(const char *who, Which which, Products &w, int64_t pairs, cu
     w.joined = int32_t(joined[0]);
     auto kernel = which == kDx ? dopt_head_product_kernel<T, kDx>
                                : which == kDw ? dopt_head_product_kernel<T, kDw> : dopt_head_product_kernel<T, kBoth>;
+    if constexpr (kHasRows<T>)
+        if (which == kDxRows) kernel = dopt_head_product_kernel<T, kDxRows>;
     const int rc = launch_op(who, kernel, dim3(unsigned(2 * std::min<int64_t>(w.items, pairs))), dim3(kProductThreads),
                              kProductSmem, stream, w);
     if (rc != DOPT_OK || joined[0] + joined[1] == 0) return rc;
@@ -1177,10 +1247,12 @@ int launch_products(const char *who, Which which, Products &w, int64_t pairs, cu
 // at once and the estimates, in the plan's units, say so: d_x's tiles, few and
 // long, in as many parts as leave room for d_w's, against two plans of their own
 // and a launch.  (How sums are divided depends on the sizes alone, not on what
-// is wanted or on the grads' type.)
+// is wanted or on the grads' type.)  for_rows: d_x is made on its own here if
+// these are the rows' factors and there are some, or if they are not and there
+// are none.
 template <typename T>
-int run_products(const char *who, const ProductArgs &dx, const ProductArgs &dw, bool want_dx, bool want_dw, int64_t pairs,
-                 cudaStream_t stream) {
+int run_products(const char *who, const ProductArgs &dx, const ProductArgs &dw, bool want_dx, bool want_dw,
+                 const float *for_rows, int64_t pairs, cudaStream_t stream) {
     const int64_t tiles_x = tiles_of(dx), tiles_w = tiles_of(dw);
     Plan plan_x = plan_product(tiles_x, dx.steps, pairs);
     Plan plan_w = plan_product(tiles_w, int64_t(dw.steps) * dw.planes, pairs);
@@ -1205,8 +1277,11 @@ int run_products(const char *who, const ProductArgs &dx, const ProductArgs &dw, 
     int rc = DOPT_OK;
     if (want_dx) {
         w.p[0] = dx;
+        w.for_rows = for_rows;
+        w.unless = !dx.row_back;
         use(w.p[0], plan_x);
-        rc = launch_products<T>(who, kDx, w, pairs, stream);
+        rc = launch_products<T>(who, dx.row_back ? kDxRows : kDx, w, pairs, stream);
+        w.for_rows = nullptr;
     }
     if (rc == DOPT_OK && want_dw) {
         w.p[0] = dw;
@@ -1228,23 +1303,21 @@ struct GradCall {
     bool accumulate;
 };
 
+// One pass over the vocabulary, piece by piece.
+struct Pass {
+    bool d_x, grad;       // what it makes
+    int32_t planes;       // of the logits' gradients
+    bool by_row;          // with the rows' own factors, if they have any
+    bool if_rows;         // nothing is done unless they have
+    bool two;             // (one of two such passes)
+};
+
 template <typename T>
-int run_grad(const char *who, const GradCall &c, Operands o, const HeadSpace &space, const GradSpace &g, char *ws,
+int run_pass(const char *who, const GradCall &c, const Pass &pass, const Operands &o, const GradSpace &g, char *rest,
              EncodeTiled encode, int pairs, cudaStream_t stream) {
-    char *rest = ws + space.rest;
     float *factor = reinterpret_cast<float *>(rest + g.factor), *sums = reinterpret_cast<float *>(rest + g.sums);
+    const float *row_back = pass.by_row ? reinterpret_cast<const float *>(rest + g.row_back) : nullptr;
     const int64_t plane = up_to(c.rows * g.piece_ld * 2, 256);
-    ReadyArgs ready{};
-    ready.d_loss = c.d_loss;
-    ready.d_lse = c.d_lse;
-    ready.targets = c.targets;
-    ready.factor = factor;
-    ready.half = c.dtype == DOPT_FP16;
-    ready.vocab = c.vocab;
-    ready.wide = c.target_bytes == 8;
-    ready.tokens = int32_t(c.rows);
-    int rc = make_ready<T>(who, o, space, ws, c.rows, c.width, c.vocab, ready, stream);
-    if (rc != DOPT_OK) return rc;
     for (int64_t v0 = 0; v0 < c.vocab; v0 += g.piece) {
         const int64_t cols = std::min(g.piece, c.vocab - v0);
         const char *w = static_cast<const char *>(o.w) + v0 * o.ld_w * 2;
@@ -1255,16 +1328,18 @@ int run_grad(const char *who, const GradCall &c, Operands o, const HeadSpace &sp
         a.d_loss = c.d_loss;
         a.d_lse = c.d_lse;
         a.factor = factor;
+        a.row_back = row_back;
+        a.for_rows = pass.if_rows;
         a.first = v0;
         a.vocab = c.vocab;
         a.wide = c.target_bytes == 8;
-        rc = make_map(who, encode, &a.x_map, c.dtype, o.x, c.width, c.rows, o.ld_x, 64, x_box_rows(c.rows));
+        int rc = make_map(who, encode, &a.x_map, c.dtype, o.x, c.width, c.rows, o.ld_x, 64, x_box_rows(c.rows));
         if (rc == DOPT_OK) rc = make_map(who, encode, &a.w_map, c.dtype, w, c.width, cols, o.ld_w, 64, 128);
-        for (int p = 0; p < c.planes && rc == DOPT_OK; ++p)
+        for (int p = 0; p < pass.planes && rc == DOPT_OK; ++p)
             rc = make_map(who, encode, &a.d_map[p], c.dtype, rest + g.logits + p * plane, cols, c.rows, g.piece_ld, 64, 32);
         if (rc != DOPT_OK) return rc;
-        rc = launch_op(who, c.planes == 2 ? dopt_head_logit_kernel<T, 2> : dopt_head_logit_kernel<T, 1>,
-                       dim3(unsigned(2 * std::min<int64_t>(a.items, pairs))), dim3(kLogitThreads), logit_smem(c.planes),
+        rc = launch_op(who, pass.planes == 2 ? dopt_head_logit_kernel<T, 2> : dopt_head_logit_kernel<T, 1>,
+                       dim3(unsigned(2 * std::min<int64_t>(a.items, pairs))), dim3(kLogitThreads), logit_smem(pass.planes),
                        stream, a);
         if (rc != DOPT_OK) return rc;
         ProductArgs dx{}, dw{};
@@ -1281,7 +1356,7 @@ int run_grad(const char *who, const GradCall &c, Operands o, const HeadSpace &sp
         dw.planes = c.planes;
         dw.chunk = sum_chunk(c.dtype, c.grad_dtype);
         dw.partial = partial + most_slots(c.width, c.rows) * kM * kN;
-        if (c.d_x) {
+        if (pass.d_x) {
             const bool last = v0 + cols == c.vocab;
             rc = make_map(who, encode, &dx.a_map, c.dtype, w, c.width, cols, o.ld_w, 64, 64);
             if (rc == DOPT_OK)
@@ -1291,11 +1366,12 @@ int run_grad(const char *who, const GradCall &c, Operands o, const HeadSpace &sp
             dx.ld = last ? c.ld_d_x : c.width;
             dx.add = v0 > 0 ? sums : nullptr;
             dx.back = last ? factor + 1 : nullptr;
+            dx.row_back = row_back;
             dx.out_dtype = last ? c.dtype : DOPT_FP32;
         }
-        if (c.grad) {
+        if (pass.grad) {
             rc = make_map(who, encode, &dw.a_map, c.dtype, o.x, c.width, c.rows, o.ld_x, 64, 64);
-            for (int q = 0; q < c.planes && rc == DOPT_OK; ++q)
+            for (int q = 0; q < pass.planes && rc == DOPT_OK; ++q)
                 rc = make_map(who, encode, &dw.b_map[q], c.dtype, rest + g.logits + q * plane, cols, c.rows, g.piece_ld, 64, 64);
             if (rc != DOPT_OK) return rc;
             dw.out = c.grad + v0 * c.width * int64_t(elem_bytes(c.grad_dtype));
@@ -1304,9 +1380,40 @@ int run_grad(const char *who, const GradCall &c, Operands o, const HeadSpace &sp
             dw.out_dtype = c.grad_dtype;
             dw.accumulate = c.accumulate;
         }
-        if ((rc = run_products<T>(who, dx, dw, c.d_x != nullptr, c.grad != nullptr, pairs, stream)) != DOPT_OK) return rc;
+        if ((rc = run_products<T>(who, dx, dw, pass.d_x, pass.grad, pass.two ? factor + 2 : nullptr, pairs, stream)) != DOPT_OK)
+            return rc;
     }
     return DOPT_OK;
+}
+
+// With fp16, d_x alone takes the rows' own factors at once.  Where the matrix's
+// grads are wanted too, whose sums need one factor, a second pass makes d_x from
+// logits' gradients with the rows' own if weights are that far apart (the device
+// knows): the logits' product a third time, 16384 x 768 x 50257 2.6 -> 3.55 ms;
+// else two or three launches that end at once, 1001 x 512 x 5003 35 -> 40 us.
+template <typename T>
+int run_grad(const char *who, const GradCall &c, Operands o, const HeadSpace &space, const GradSpace &g, char *ws,
+             EncodeTiled encode, int pairs, cudaStream_t stream) {
+    char *rest = ws + space.rest;
+    constexpr bool half = kHasRows<T>;
+    const bool by_row = half && c.d_x && !c.grad;
+    ReadyArgs ready{};
+    ready.d_loss = c.d_loss;
+    ready.d_lse = c.d_lse;
+    ready.targets = c.targets;
+    ready.factor = reinterpret_cast<float *>(rest + g.factor);
+    ready.row_back = half && c.d_x ? reinterpret_cast<float *>(rest + g.row_back) : nullptr;
+    ready.half = half;
+    ready.vocab = c.vocab;
+    ready.wide = c.target_bytes == 8;
+    ready.tokens = int32_t(c.rows);
+    int rc = make_ready<T>(who, o, space, ws, c.rows, c.width, c.vocab, ready, stream);
+    const bool two = half && c.d_x && c.grad;
+    if (rc == DOPT_OK)
+        rc = run_pass<T>(who, c, Pass{c.d_x != nullptr, c.grad != nullptr, c.planes, by_row, false, two}, o, g, rest, encode,
+                         pairs, stream);
+    if (rc == DOPT_OK && two) rc = run_pass<T>(who, c, Pass{true, false, 1, true, true, true}, o, g, rest, encode, pairs, stream);
+    return rc;
 }
 
 // The grads of a call without rows.
