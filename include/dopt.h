@@ -968,7 +968,9 @@ int dopt_norm(const dopt_norm_cfg *cfg, const dopt_norm_params *params, dopt_dty
  *     d_row_gate[t] = scale * sum over columns of gate * d_x * u
  * The mean and the mean square of h and y are computed again.  fp32 sums, in
  * an order that depends on the sizes alone; each result is rounded once (after
- * adding the old grad, with DOPT_NORM_ACCUMULATE).
+ * adding the old grad, with DOPT_NORM_ACCUMULATE).  Rows and params that are all
+ * 16-byte aligned, of a multiple of 8 columns, have kernels of their own, here and
+ * in dopt_norm: the same values in other places may be rounded differently.
  *   d_x, d_y      device [rows][cols], written, or NULL; d_x may be d_h with
  *                 its row stride
  *   d_row_gate    device fp32 [rows], written, or NULL

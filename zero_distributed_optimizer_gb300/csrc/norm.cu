@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(NV == 4 ? kMostRow : 256, NV == 1 ? 4 : NV == 
                 for (int q = 0; q < kPairs; ++q) sum = sum + v[i][q];
             float f[1] = {both(sum)};
             row_sums(s, turn, f);
-            const F2 less(-f[0] * per_col);
+            const F2 less(-f[0] / float(a.cols));  // (divided: so many times a rounded 1 / cols leaves constant rows a residue)
 #pragma unroll
             for (int i = 0; i < NV; ++i)
                 if (in[i])

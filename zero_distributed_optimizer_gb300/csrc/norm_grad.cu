@@ -204,7 +204,8 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : kMostRow, NV == 1 ? 2 : 1)
                 for (int q = 0; q < kPairs; ++q) sum[0] = sum[0] + h[i][q], sum[1] = sum[1] + u[i][q];
             float f[2] = {both(sum[0]), both(sum[1])};
             row_sums(s, turn, f);
-            const F2 h_less(-f[0] * per_col), y_less(a.post ? -f[1] * per_col : 0.0f);
+            // (divided: so many times a rounded 1 / cols leaves constant rows a residue)
+            const F2 h_less(-f[0] / float(a.cols)), y_less(a.post ? -f[1] / float(a.cols) : 0.0f);
 #pragma unroll
             for (int i = 0; i < NV; ++i)
                 if (in[i])
