@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+from operator import index as index_of
 
 import torch
 
@@ -132,7 +133,8 @@ _FiveOffsets = ctypes.c_int64 * 5
 
 @functools.lru_cache(maxsize=256)
 def _norm_cfg(kind, post, eps, scale):
-    """The configuration of these values (kept by value: the library only reads it)."""
+    """The configuration of these values (kept by value, of plain numbers: a tensor
+    is the same key whatever it holds; the library only reads it)."""
     code = _KINDS.get(kind)
     if code is None:
         raise _bad(f"unknown norm {kind!r}: one of {', '.join(_KINDS)}")
@@ -197,7 +199,7 @@ def dopt_norm(kind: str, x, n, weight=None, bias=None, y=None, h=None, post: boo
     if x.dim() != 2:
         raise _bad("x must be [rows, cols]")
     dt, shape = x.dtype, x.shape
-    _call(index, stream, lib().dopt_norm, ctypes.byref(_norm_cfg(kind, 1 if post else 0, eps, scale)),
+    _call(index, stream, lib().dopt_norm, ctypes.byref(_norm_cfg(kind, 1 if post else 0, float(eps), float(scale))),
           _norm_params((weight, bias, post_weight, post_bias, gate), row_gate, dt, shape, index), _dtype_code(dt, "x"),
           *shape, *_matrices((("x", x), ("y", y), ("h", h), ("n", n)), dt, shape, index))
 
@@ -228,11 +230,11 @@ def dopt_norm_grad(kind: str, h, d_n, d_x, weight=None, y=None, d_y=None, d_h=No
     if h.dim() != 2:
         raise _bad("h must be [rows, cols]")
     dt, shape = h.dtype, h.shape
-    at = _norm_offsets(tuple(grad_offsets.items()) if grad_offsets else ())
+    at = _norm_offsets(tuple((n, index_of(a)) for n, a in grad_offsets.items()) if grad_offsets else ())
     gp, code, numel = (None, 0, 0) if grad is None else _flat(grad, index)
     wp, wn = _workspace(workspace, index)
     rp = None if d_row_gate is None else _dense(d_row_gate, "d_row_gate", torch.float32, shape[:1], index)
-    _call(index, stream, lib().dopt_norm_grad, ctypes.byref(_norm_cfg(kind, 1 if post else 0, eps, scale)),
+    _call(index, stream, lib().dopt_norm_grad, ctypes.byref(_norm_cfg(kind, 1 if post else 0, float(eps), float(scale))),
           _norm_params((weight, None, post_weight, post_bias, gate), row_gate, dt, shape, index), _dtype_code(dt, "h"),
           *shape, *_matrices((("h", h), ("y", y), ("d_n", d_n), ("d_h", d_h), ("d_x", d_x), ("d_y", d_y)), dt, shape, index),
           rp, gp, code, numel, at,
