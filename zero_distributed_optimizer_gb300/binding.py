@@ -271,13 +271,14 @@ class AdamConfig:
 
     def to_c(self) -> dopt_adam_cfg:
         """The C struct (one per distinct config, kept: the library only reads it)."""
-        return _adam_c(self)
+        return _adam_c(float(self.lr), float(self.beta1), float(self.beta2), float(self.eps),
+                       float(self.weight_decay), float(self.grad_scale))
 
 
 @functools.lru_cache(maxsize=256)
-def _adam_c(adam: AdamConfig) -> dopt_adam_cfg:
-    return dopt_adam_cfg(adam.lr, adam.beta1, adam.beta2, adam.eps, adam.weight_decay,
-                         adam.grad_scale)
+def _adam_c(*numbers) -> dopt_adam_cfg:
+    """(by plain numbers: a tensor is the same key whatever it holds)"""
+    return dopt_adam_cfg(*numbers)
 
 
 def _on(device):

@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+from operator import index as index_of
 from typing import NamedTuple
 
 import torch
@@ -268,7 +269,7 @@ def dopt_ckpt_act_grad(ckpt: Checkpoint, act: str, d_out, d_in, stream=None) -> 
 
 @functools.lru_cache(maxsize=256)
 def _starts(grad_offsets: tuple):
-    """The C array of these offsets (kept by value: the library only reads it)."""
+    """The C array of these offsets, plain numbers (kept by value: the library only reads it)."""
     return (ctypes.c_int64 * max(len(grad_offsets), 1))(*grad_offsets)
 
 
@@ -313,7 +314,7 @@ def dopt_ckpt_wgrad(ckpt: Checkpoint, dy, grad, grad_offsets, offsets=None, row_
         if workspace.get_device() != index or workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
             raise _bad(f"workspace must be a contiguous uint8 tensor on cuda:{index}")
         wp, wn = workspace.data_ptr(), workspace.numel()
-    starts = _starts(tuple(grad_offsets))
+    starts = _starts(tuple(map(index_of, grad_offsets)))
     _call(index, stream, lib().dopt_ckpt_wgrad, cp, _dtype_code(ckpt.dtype, "checkpoint"), ckpt.rows, ckpt.cols,
           rp, dp, _dtype_code(dy.dtype, "dy"), dy_rows, outs, ld, op, n_groups, starts, gp,
           _dtype_code(grad.dtype, "grad"), numel, DOPT_WGRAD_ACCUMULATE if accumulate else 0, wp, wn)
