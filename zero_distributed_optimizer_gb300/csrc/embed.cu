@@ -74,11 +74,12 @@ __global__ void __launch_bounds__(kEmbedThreads) dopt_embed_kernel(const __grid_
 #pragma unroll
     for (int i = 0; i < kTokens; ++i) {
         if (t0 + i >= a.tokens) break;
-        if (a.accumulate && uint64_t(id[i]) >= uint64_t(a.vocab)) continue;  // nothing is added
+        const bool there = uint64_t(id[i]) < uint64_t(a.vocab);
+        if (a.accumulate && !there) continue;  // nothing is added
         V v;
         v.take(ahead[i], a.vec, lane, 32);
         T *row = static_cast<T *>(a.out) + (t0 + i) * a.ld_out;
-        if (a.scale != 1.0f || a.accumulate) {
+        if (there && (a.scale != 1.0f || a.accumulate)) {  // (zeros stay zeros whatever the scale is)
             float f[kCols], old[kCols] = {};
             v.get(f);
             if (a.accumulate) {
@@ -116,11 +117,12 @@ __global__ void __launch_bounds__(kEmbedThreads) dopt_embed_whole_kernel(const _
     }
 #pragma unroll
     for (int i = 0; i < kTokens; ++i) {
-        if (t0 + i >= a.tokens || (a.accumulate && uint64_t(id[i]) >= uint64_t(a.vocab))) continue;
+        const bool there = uint64_t(id[i]) < uint64_t(a.vocab);
+        if (t0 + i >= a.tokens || (a.accumulate && !there)) continue;
         uint4 *row = reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + (t0 + i) * a.ld_out + c);
 #pragma unroll
         for (int k = 0; k < kPieces; ++k) {
-            if (a.scale != 1.0f || a.accumulate) {
+            if (there && (a.scale != 1.0f || a.accumulate)) {
                 float f[kPer], old[kPer] = {};
                 unpack<T, 16>(v[i][k], f);
                 if (a.accumulate) unpack<T, 16>(row[k], old);
