@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import model_reference as R
+import zero_distributed_optimizer_gb300 as dopt
 from test_head_gpu import EPS, F, TINY, Case, _check_grad, _grad
 
 pytestmark = pytest.mark.gpu
@@ -100,3 +101,45 @@ def test_dead_rows_beside_far_weights():
     lse[[1, 2, 3]] = float("nan")  # the ignored ones
     d_x, grad = _grad(c, lse, torch.float32)
     assert torch.equal(d_x, want[0]) and torch.equal(grad, want[1]) and not d_x[[1, 2, 3]].any()
+
+
+@pytest.mark.parametrize("grad_type", [torch.float16, torch.float32], ids=str)
+def test_many_rows_far_apart(grad_type):
+    c = _case(9001, 72, 300, torch.float16)
+    _spread(c, 1e-6)
+    _, lse = c.loss()
+    d_x, grad = _grad(c, lse, grad_type, d_lse=c.d_lse)
+    _check_rows(c, lse, d_x, c.d_lse, torch.ones(c.rows, dtype=torch.bool))
+    _check_grad(c, lse, grad_type, None, grad, c.d_lse)
+
+
+def test_one_graph_for_equal_weights_and_far_ones():
+    """Whether the rows' weights are far apart is found at each replay."""
+    c = _case(300, 136, 2049, torch.float16)
+    _, lse = c.loss()
+    weights = []
+    for low in (1.0, 1e-6, 0.5, 1e-3):
+        _spread(c, low)
+        weights.append((c.d_loss.clone(), c.d_lse.clone()))
+    want = []
+    for c.d_loss, d_lse in weights:
+        want.append(_grad(c, lse, torch.float32, d_lse=d_lse))
+    d_loss, d_lse = (torch.zeros(c.rows, device=DEV) for _ in range(2))
+    d_x, grad = torch.zeros_like(want[0][0]), torch.full_like(want[0][1], 2.0)
+    ws = dopt.head_loss_grad_workspace(c.rows, c.width, c.vocab, torch.float32)
+    ws.fill_(255)
+
+    def run():
+        dopt.dopt_head_loss_grad(c.x, c.w, c.targets, lse, d_loss, d_x, grad, 3, d_lse=d_lse, workspace=ws)
+
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for k in (0, 1, 2, 3, 1, 0):
+        d_loss.copy_(weights[k][0])
+        d_lse.copy_(weights[k][1])
+        d_x.fill_(7.0)
+        graph.replay()
+        assert torch.equal(d_x, want[k][0]) and torch.equal(grad, want[k][1]), k
