@@ -944,7 +944,8 @@ typedef struct {
  * once.  Without y (a model's first norm), h is x and n = norm(x).  Params
  * that are NULL count as ones (bias as zeros).
  *   x, y  device [rows][cols], row strides ld_x, ld_y; y may be NULL
- *   h     device [rows][cols], written, or NULL; may be x with its row stride
+ *   h     device [rows][cols], written, or NULL (as it is without y); may be x
+ *         with its row stride
  *   n     device [rows][cols], written, or NULL
  * rows < 2^31, 1 <= cols <= DOPT_NORM_MAX_COLS.  Errors: DOPT_E_ARG,
  * DOPT_E_ALIGN, DOPT_E_CUDA.
@@ -1012,7 +1013,9 @@ int dopt_norm_workspace(int64_t rows, int64_t cols, int64_t *bytes);
  * and 0 where targets[t] is outside [0, vocab) (an ignored token; its lse is
  * computed all the same).  The logits are fp32 sums of exact products on the
  * tensor cores, and live in tensor memory alone; maxima and sums of
- * exponentials are fp32.
+ * exponentials are fp32.  Logits of any size count as they are: those masked by
+ * values far below the others, down to -inf, add nothing, one of +inf makes lse
+ * infinite, a NaN makes it NaN.
  *   x          device [rows][width], row stride ld_x, bf16 or fp16
  *   weight     device [vocab][width], row stride ld_w, of the same type, e.g. a
  *              param replica of dopt_step

@@ -1,10 +1,12 @@
 // The token embedding (dopt_embed) and its gradient into the flat grad buffer
 // (dopt_embed_grad); dopt.h states the contracts.
 //
-// The embedding is a copy, bound by memory: a warp takes 256 columns of four
-// tokens, so that four rows' loads are in flight together (16384 tokens of 768
-// bf16 columns: 7.5 us, 6.7 TB/s; rows that are not 16-byte aligned go in
-// shifted pieces, rows.cuh).
+// The embedding is a copy: a warp takes 256 columns of four tokens, so that four
+// rows' loads are in flight together.  16384 tokens of 768 bf16 columns whose ids
+// name some 6000 rows, as text's do: 6.8 us, where the 34 MB of those rows and the
+// output take 5.1 at the copy rate; what is left is the latency of ids and then
+// rows, most of which come from L2, and instructions (half of the issue slots).
+// Rows that are not 16-byte aligned go in shifted pieces (rows.cuh).
 //
 // The gradient sorts the tokens by row and sums each row's tokens in that order,
 // so that it does not depend on which block runs when, and every row of the
@@ -778,8 +780,10 @@ extern "C" int dopt_embed_grad(const void *ids, int32_t id_bytes, int64_t tokens
     auto sort = id_bytes == 8 ? dopt_embed_sort_kernel<int64_t> : dopt_embed_sort_kernel<int32_t>;
     // Zeros are written beside the sort (64 KB a block, up to two blocks an SM),
     // which is bound by latencies, and a quarter of them after the sums' blocks,
-    // for the same reason (16384 x 768 into 50257 rows: all beside the sort 28.5
-    // us, three quarters 26.9, half 28.0).
+    // for the same reason.  All beside the sort, three quarters, half, in a loop:
+    // 16384 x 768 into 50257 rows bf16 28.4, 26.1, 27.1 us, fp32 42.2, 39.4, 38.0;
+    // 8192 x 2048 into 32000 bf16 37.3, 38.0, 33.4; 16384 x 4096 into 32000 bf16
+    // 87, 83, 79; 4096 x 1024 into 8192 and smaller ones no difference.
     a.zeroed = a.accumulate ? 0 : tokens > 0 ? vocab - vocab / 4 : vocab;
     const int64_t zero_blocks = std::min<int64_t>(304, (a.zeroed * cols * int64_t(gb) + 65535) / 65536);
     rc = launch_op(who, sort, dim3(unsigned(a.ranges + zero_blocks)), dim3(kSortThreads), smem, stream, a);

@@ -24,12 +24,13 @@ namespace {
 //
 // Long products are bound by the tensor cores (active 96-98 % of the cycles) and
 // then by the card's power: 16384 tokens x 768 x 50257, bf16, loss 618-647 us in
-// short runs (1.96-2.05 PFLOP/s), 706-725 under the power cap (1.75-1.79);
+// short runs (1.96-2.05 PFLOP/s), 706-728 under the power cap (1.74-1.79);
 // gradients 2070-2180 and 2350-2450 us (1.83 and 1.55-1.62 PFLOP/s).  The logits'
 // gradients are stored as they are made, 1.6 GB, which keeps the tensor cores at
 // 83 % there; in pieces that stay in L2 d_x's fp32 sums would move more.  Few
 // tokens: 24 x 2048 x 32000, loss 32 us (19 at the copy rate), 20 for the
-// matrix, 7 of two launches, 4 until the first steps are there.
+// matrix, 7 of two launches, 4 until the first steps are there; its 125 tiles are
+// two waves on 76 pairs, the second of 49.
 constexpr int kM = 256, kN = 256, kK = 64;  // of a pair's tile, and of a step
 constexpr int kSlab = 64 * 128;             // 64 rows of 128 bytes
 constexpr int kOperand = 2 * kSlab;         // a CTA's share of one operand in a step
@@ -613,8 +614,9 @@ struct ProductArgs {
 };
 // What a launch makes: d_x, for which k is contiguous in the logits' gradients;
 // d_w, for which n is; or both, where all their tiles fit the card at once
-// (beside each other they take 33 us where two launches take 42, 1001 x 512 x
-// 5003 bf16; where there are more, the choice at each tile costs more).
+// (all gradients of 1001 x 512 x 5003 bf16 33 us where two launches take 43, of 512
+// x 768 x 4096 28 and 38, of 700 x 1024 x 2048 fp16 30 and 38; where there are more
+// tiles, the choice at each costs more).
 enum Which { kDx = 0, kDw = 1, kBoth = 2, kDxRows = 3 };  // kDxRows: d_x of rows that may have their own factors
 struct Products {
     ProductArgs p[2];
@@ -1082,7 +1084,9 @@ int make_map(const char *who, EncodeTiled encode, CUtensorMap *map, dopt_dtype d
 // How a product's tiles go over the pairs: whole waves tile by tile, the last
 // partial wave's tiles split along k.  Chosen for the least estimated time in
 // steps of 64 k: a tile's stores 4 (they run under the next tile's products),
-// the join's launch 12 and a part's trip through memory 0.5.
+// the join's launch 12 and a part's trip through memory 0.5 (fitted at 1001 x 515 x
+// 5003; gradients without split tiles: 2048 x 768 x 5003 63 us for 56, 512 x 2048
+// x 32000 256 for 162, 24 x 2048 x 32000 226 for 117).
 struct Plan {
     int64_t whole, tail;
     int parts;
@@ -1109,7 +1113,8 @@ Plan plan_product(int64_t tiles, int64_t steps, int64_t pairs) {
 // Steps of one sum: the tensor cores cut off what 24 bits do not hold, always
 // toward zero, so that the error grows with the sum's length.  Logits and fp32
 // results add sums of 1024 k (512 with fp16 factors) up in fp32, rounding to
-// nearest (lse of width 4096 was 1.7e-6 off in one sum, torch's 6.7e-7);
+// nearest (lse of width 2048 and 4096, bf16: 6.3e-7 and 1.29e-6 off in one sum,
+// 3.0e-7 and 2.9e-7 so; an fp32 product's is 3e-8 off);
 // 16-bit results lose less than an eighth of their own rounding in 131072
 // (bf16) or 16384 (fp16).
 int32_t sum_chunk(dopt_dtype factors, dopt_dtype out) {

@@ -6,7 +6,12 @@
 // instructions, of which a row's sums have many: threads hold 16 columns from
 // 1024 columns on (norm.cuh).  16384 x 2048 bf16 with a norm before and after
 // and a gate: 46 us, 5.9 TB/s (146 us with a row's loads waited for, 63 with
-// the next row's in flight, 47 with few shuffles a sum).
+// the next row's in flight, 47 with few shuffles a sum); layer norms, of two more
+// sums a row, 65.  As many bytes in rows of 4096 columns 48 and 68 us; above those
+// a thread holds 32 and spills 48-92 bytes (fp32 up to 424): of 8192 57 and 103,
+// of 16384 65 and 110.  Rows of 2047 columns, whose loads are waited for, 160 and
+// 192 (16-bit ones spill from 4097 columns on, bf16 layer norms a little and fp32
+// ones from 1025).
 #include "norm.cuh"
 
 namespace {

@@ -9,8 +9,12 @@
 // bf16 with a norm before and after and a gate: 91 us, 4.4 TB/s, instructions in
 // 60 % of the issue slots at two blocks an SM (three spill: 150 us); 259 us
 // with a row's loads waited for, 143 with the next row's in flight, 100 with
-// few shuffles a sum, 94 with two columns an instruction.  Rows of more than
-// 8192 columns spill registers.
+// few shuffles a sum, 94 with two columns an instruction; layer norms 138.
+// Rows of more than 2048 columns take two groups of columns a thread, of more than
+// 8192 four, and spill: 460-960 bytes a thread and 1560-2672 (fp32 the most; of
+// up to 2048 columns fp32 layer norms alone, 108).  As many bytes in rows of 4096
+// columns 147 us (layer 173), of 8192 175 (205), of 16384 329 (468).  Rows of 2047
+// columns, whose loads are waited for, 308 (350).
 #include "norm.cuh"
 
 namespace {

@@ -192,7 +192,7 @@ def dopt_norm(kind: str, x, n, weight=None, bias=None, y=None, h=None, post: boo
 
     kind: "rms" or "layer".  x, y, h, n: [rows, cols] with contiguous rows, of
     one type; h or n may be None (not wanted), h may be x.  Without y: n =
-    norm(x).  weight, bias, post_weight, post_bias, gate: [cols] of that type,
+    norm(x), and h is None.  weight, bias, post_weight, post_bias, gate: [cols] of that type,
     row_gate: fp32 [rows]; None counts as ones (biases: zeros).
     """
     index = _cuda_index(x, "x")
@@ -282,7 +282,8 @@ def _head(x, weight, targets):
 
 def dopt_head_loss(x, weight, targets, loss, lse, workspace=None, stream=None) -> None:
     """lse[t] = log(sum over v of exp(x[t] . weight[v])) and loss[t] = lse[t] -
-    x[t] . weight[targets[t]], 0 where the target is outside [0, vocab).
+    x[t] . weight[targets[t]], 0 where the target is outside [0, vocab).  Logits
+    masked by values far below the others, down to -inf, add nothing.
 
     x: [rows, width], weight: [vocab, width], bf16 or fp16 with contiguous rows;
     targets: int32 or int64 [rows]; loss, lse: fp32 [rows].  workspace: from
@@ -303,7 +304,9 @@ def dopt_head_loss_grad(x, weight, targets, lse, d_loss, d_x, grad, grad_offset:
     d_x: [rows, width] of x's type with contiguous rows, or None; grad: a flat
     grad buffer that takes the matrix's gradient at grad_offset, or None.
     accumulate: add to the grads that are there.  workspace: from
-    :func:`head_loss_grad_workspace`.
+    :func:`head_loss_grad_workspace`.  With fp16, where rows' weights (d_loss,
+    d_lse) are more than 16 times apart and grad is wanted too, d_x takes a pass
+    of its own over the vocabulary.
     """
     index, args = _head(x, weight, targets)
     rows, width, f32 = args[2], args[3], torch.float32
