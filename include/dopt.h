@@ -1054,7 +1054,7 @@ int dopt_head_loss_workspace(int64_t rows, int64_t width, int64_t vocab, int32_t
  * where a target outside [0, vocab) makes d_loss[t] count as 0, and a row whose
  * d_loss and d_loss + d_lse count as 0 adds nothing even where its logits are
  * not finite (as long as x is).  An infinite entry of weight makes its column of
- * d_x NaN, as 0 * infinity is; masks that training meets are finite.  The vocabulary
+ * d_x NaN, as 0 * infinity is: mask by finite values for it.  The vocabulary
  * goes in pieces: the logits of one are computed again and their gradients d
  * kept in the workspace for the two products.  d over the largest finite d_loss
  * (so that equal weights are ones; with fp16 times 2^13, so that it stays in
